@@ -25,6 +25,8 @@ FT_PREFILL_DOUBLE_BUFFER = 1
 FT_PREFILL_DEBUG_X = 2
 FT_PREFILL_ON_DEMAND = 4
 FT_BACKEND_OFFLOAD, FT_BACKEND_HYBRID = 0, 1
+FT_KV_NVFP4, FT_KV_FP8 = 0, 1
+KV_FORMATS = {"nvfp4": FT_KV_NVFP4, "fp8": FT_KV_FP8}
 FT_PROF_KINDS = 5
 PROF_NAMES = ("decode", "prefill_gemm1", "prefill_gemm2", "prefill_other", "prefill_copy")
 
@@ -33,9 +35,9 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-c_void_p, c_int32, c_uint32, c_int64, c_size_t, c_double = (
+c_void_p, c_int32, c_uint32, c_int64, c_size_t, c_double, c_float = (
     ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_int64, ctypes.c_size_t,
-    ctypes.c_double)
+    ctypes.c_double, ctypes.c_float)
 
 
 class FtSplit(ctypes.Structure):
@@ -61,6 +63,13 @@ class FtBwProfile(ctypes.Structure):
     _fields_ = [("pcie_gbs", c_double), ("cpu_gbs", c_double), ("pcie_ov_gbs", c_double),
                 ("cpu_ov_gbs", c_double), ("recommend", c_int32), ("f_q16", c_uint32),
                 ("n_records", c_int32)]
+
+
+class FtKvDesc(ctypes.Structure):
+    _fields_ = [("L", c_int32), ("n_pages", c_int32), ("page_size", c_int32), ("n_kv_heads", c_int32),
+                ("head_dim", c_int32), ("n_q_heads", c_int32), ("max_seqs", c_int32),
+                ("format", c_int32), ("k_scale", c_float), ("v_scale", c_float),
+                ("pool", c_void_p), ("workspace", c_void_p)]
 
 
 def _sig(name, res, *args):
@@ -121,6 +130,20 @@ _f = {
     "ft_profile_bandwidth": _sig("ft_profile_bandwidth", c_int32, c_void_p, c_void_p, c_int32,
                                  c_void_p, _P(FtBwProfile)),
     "ft_recommend_backend": _sig("ft_recommend_backend", c_int32, c_double, c_double),
+    "ft_kv_required_sizes": _sig("ft_kv_required_sizes", c_int32, _P(FtKvDesc), _P(c_size_t),
+                                 _P(c_size_t)),
+    "ft_kv_create": _sig("ft_kv_create", c_int32, _P(FtKvDesc), _P(c_void_p)),
+    "ft_kv_destroy": _sig("ft_kv_destroy", None, c_void_p),
+    "ft_kv_append": _sig("ft_kv_append", c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int64,
+                         c_int64, c_void_p, c_int32, c_void_p),
+    "ft_kv_read": _sig("ft_kv_read", c_int32, c_void_p, c_int32, c_void_p, c_int32, c_void_p,
+                       c_void_p, c_void_p),
+    "ft_kv_attention": _sig("ft_kv_attention", c_int32, c_void_p, c_int32, c_void_p, c_int64,
+                            c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32,
+                            c_void_p, c_int32, c_int32, c_float, c_void_p, c_int64, c_void_p,
+                            c_void_p),
+    "ft_kv_status": _sig("ft_kv_status", c_int32, c_void_p, _P(c_int32)),
+    "ft_kv_last_error": _sig("ft_kv_last_error", ctypes.c_char_p, c_void_p),
     "ft_status_string": _sig("ft_status_string", ctypes.c_char_p, c_int32),
     "ft_last_error": _sig("ft_last_error", ctypes.c_char_p, c_void_p),
 }
@@ -360,6 +383,64 @@ def ft_recommend_backend(cpu_gbs, pcie_gbs):
     return _f["ft_recommend_backend"](cpu_gbs, pcie_gbs)
 
 
+def _check_kv(status, handle=None):
+    if status != FT_OK:
+        raise FtError(status, _f["ft_kv_last_error"](handle).decode() if handle else "")
+
+
+def ft_kv_required_sizes(desc: FtKvDesc):
+    """(pool bytes, workspace bytes)"""
+    pb, wb = c_size_t(), c_size_t()
+    _check_kv(_f["ft_kv_required_sizes"](ctypes.byref(desc), ctypes.byref(pb), ctypes.byref(wb)))
+    return pb.value, wb.value
+
+
+def ft_kv_create(desc: FtKvDesc):
+    h = c_void_p()
+    _check_kv(_f["ft_kv_create"](ctypes.byref(desc), ctypes.byref(h)))
+    return h.value
+
+
+def ft_kv_destroy(handle):
+    _f["ft_kv_destroy"](handle)
+
+
+def _stride(t, given, name):
+    """Token stride in elements: the one given, or that of a tensor."""
+    if given is not None:
+        return given
+    if hasattr(t, "stride"):
+        return t.stride(0)
+    raise TypeError(f"{name} is needed with a raw pointer")
+
+
+def ft_kv_append(handle, layer, k, v, slots, n, k_stride=None, v_stride=None, stream=None):
+    _check_kv(_f["ft_kv_append"](handle, layer, _ptr(k), _ptr(v), _stride(k, k_stride, "k_stride"),
+                                 _stride(v, v_stride, "v_stride"), _ptr(slots), n,
+                                 _stream(stream)), handle)
+
+
+def ft_kv_read(handle, layer, slots, n, k_out, v_out, stream=None):
+    _check_kv(_f["ft_kv_read"](handle, layer, _ptr(slots), n, _ptr(k_out), _ptr(v_out),
+                               _stream(stream)), handle)
+
+
+def ft_kv_attention(handle, layer, q, q_start, kv_len, block_table, table_stride, n_seqs, n_tokens,
+                    max_q, o, tree_mask=None, window=0, n_sink=0, sm_scale=1.0, lse=None,
+                    q_stride=None, o_stride=None, stream=None):
+    _check_kv(_f["ft_kv_attention"](handle, layer, _ptr(q), _stride(q, q_stride, "q_stride"),
+                                    _ptr(q_start), _ptr(kv_len), _ptr(block_table), table_stride,
+                                    n_seqs, n_tokens, max_q, _ptr(tree_mask), window, n_sink,
+                                    sm_scale, _ptr(o), _stride(o, o_stride, "o_stride"), _ptr(lse),
+                                    _stream(stream)), handle)
+
+
+def ft_kv_status(handle):
+    s = c_int32()
+    _check_kv(_f["ft_kv_status"](handle, ctypes.byref(s)), handle)
+    return s.value
+
+
 # ----------------------------------------------------------------- memory plumbing
 
 class PinnedBuffer:
@@ -413,6 +494,40 @@ class ExpertCache:
     def close(self):
         if self.handle:
             ft_cache_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KVCache:
+    """Owns the device memory (torch allocations) and the ft_kv handle of a quantised
+    key/value cache; `pool` may be given (a uint8 tensor of ft_kv_required_sizes bytes, its
+    tokens are kept)."""
+
+    def __init__(self, L, n_pages, page_size, n_kv_heads, head_dim, n_q_heads, max_seqs,
+                 fmt="nvfp4", k_scale=1.0, v_scale=1.0, pool=None, device="cuda"):
+        import torch
+        self.handle = None
+        self.desc = FtKvDesc(L, n_pages, page_size, n_kv_heads, head_dim, n_q_heads, max_seqs,
+                             KV_FORMATS[fmt], k_scale, v_scale, None, None)
+        self.pool_bytes, ws_bytes = ft_kv_required_sizes(self.desc)
+        if pool is None:
+            pool = torch.empty(self.pool_bytes, dtype=torch.uint8, device=device)
+        elif pool.numel() * pool.element_size() < self.pool_bytes or not pool.is_contiguous():
+            raise ValueError(f"pool must be contiguous and hold {self.pool_bytes} bytes")
+        self.pool = pool
+        self.workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=pool.device)
+        self.desc.pool = pool.data_ptr()
+        self.desc.workspace = self.workspace.data_ptr()
+        self.handle = ft_kv_create(self.desc)
+
+    def close(self):
+        if self.handle:
+            ft_kv_destroy(self.handle)
             self.handle = None
 
     def __del__(self):

@@ -1,0 +1,109 @@
+// Internal declarations of the quantised key/value cache and its attention.
+#pragma once
+#include "ft_internal.cuh"
+
+namespace ft {
+
+constexpr int kKvTile = 16;            // tokens per tile record
+constexpr int kTreeMax = 64;           // drafted tokens of one sequence (bits of a mask)
+
+// Byte layout of one tile record (16 tokens of one kv head).
+struct KvTile {
+    int code_bytes;      // of K, and again of V
+    int k_scales, v_scales, bytes;
+};
+
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline constexpr KvTile kv_tile(int D, int format) {
+    return format == FT_KV_NVFP4 ? KvTile{kKvTile * D / 2, kKvTile * D, kKvTile * D + D, kKvTile * D + 2 * D}
+                                 : KvTile{kKvTile * D, 2 * kKvTile * D, 2 * kKvTile * D, 2 * kKvTile * D};
+}
+
+// One layer of a cache as the kernels see it.
+struct KvView {
+    uint8_t* pool;       // the layer's pages
+    int n_pages, page_shift, hkv;      // page_size = 1 << page_shift
+    float k_scale, v_scale;
+    int* status;
+};
+
+struct AttnArgs {
+    KvView kv;
+    const __nv_bfloat16* q;
+    size_t q_stride;
+    const int32_t* q_start;
+    const int32_t* kv_len;
+    const int32_t* table;
+    int table_stride, n_seqs, n_tokens, max_q;
+    int hq, G;
+    const unsigned long long* tree;
+    int window, n_sink;
+    float scale;
+    __nv_bfloat16* o;
+    size_t o_stride;
+    float* lse;
+};
+
+cudaError_t launch_kv_append(const KvView& kv, int D, int format, const void* k, const void* v, size_t k_stride,
+                             size_t v_stride, const int32_t* slots, int n, cudaStream_t s);
+cudaError_t launch_kv_read(const KvView& kv, int D, int format, const int32_t* slots, int n, void* k_out, void* v_out,
+                           cudaStream_t s);
+cudaError_t launch_kv_attention(const AttnArgs& a, int D, int format, cudaStream_t s);
+
+#ifdef __CUDACC__
+
+// Byte of the tile where a lane's code byte b stands (16-byte vectors, [vector][lane][16]).
+__device__ __forceinline__ int kv_lane_byte(int lane, int b) { return (b >> 4) * 512 + lane * 16 + (b & 15); }
+
+// First byte of the run of codes of token r's dims d.. (d a multiple of 8) in K or V.
+template <int D, int kFormat>
+__device__ __forceinline__ int kv_k_byte(int r, int d) {
+    const int in = (r >> 3) * (D / 4) + d % (D / 4);
+    return kv_lane_byte(4 * (r & 7) + d / (D / 4), kFormat == FT_KV_NVFP4 ? in / 2 : in);
+}
+template <int D, int kFormat>
+__device__ __forceinline__ int kv_v_byte(int r, int d) {
+    const int in = (2 * (r >> 3) + (r & 1)) * (D / 8) + d % (D / 8);
+    return kv_tile(D, kFormat).code_bytes +
+           kv_lane_byte(4 * (d / (D / 8)) + ((r & 7) >> 1), kFormat == FT_KV_NVFP4 ? in / 2 : in);
+}
+// Scale byte of token r's block b of 16 dims (NVFP4).
+template <int D>
+__device__ __forceinline__ int kv_k_scale_byte(int r, int b) {
+    return kv_tile(D, FT_KV_NVFP4).k_scales + (4 * (r & 7) + b / (D / 64)) * (D / 32) + (r >> 3) * (D / 64) + b % (D / 64);
+}
+template <int D>
+__device__ __forceinline__ int kv_v_scale_byte(int r, int b) {
+    return kv_tile(D, FT_KV_NVFP4).v_scales + (b * 4 + ((r & 7) >> 1)) * 4 + 2 * (r >> 3) + (r & 1);
+}
+
+// Rows and cached length of sequence s, bounded as the interface says.
+struct SeqInfo {
+    int q0, n, len;      // first row, rows, cached tokens
+    bool bad;
+};
+__device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int s) {
+    SeqInfo r;
+    const int a0 = a.q_start[s], a1 = a.q_start[s + 1], len = a.kv_len[s];
+    r.q0 = min(max(a0, 0), a.n_tokens);
+    const int q1 = min(max(a1, r.q0), a.n_tokens);
+    r.n = min(q1 - r.q0, a.max_q);
+    const long long most = (long long)a.table_stride << a.kv.page_shift;
+    r.len = (int)min((long long)max(len, 0), most);
+    r.bad = r.q0 != a0 || q1 != a1 || r.n != q1 - r.q0 || r.len != len;
+    return r;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace ft
+
+struct ft_kv {
+    ft_kv_desc d;
+    ft::KvTile tile;
+    size_t layer_bytes;
+    int page_shift;
+    char err[256];
+};

@@ -393,6 +393,117 @@ ft_status ft_profile_bandwidth(ft_cache* c, ft_host_branch* hb, int32_t n_record
  * twice as fast as the fill path (cpu_gbs > 2 * pcie_gbs), else FT_BACKEND_OFFLOAD. */
 int32_t   ft_recommend_backend(double cpu_gbs, double pcie_gbs);
 
+/* ---- Quantised key/value cache and the attention over it.  The attention layers of the
+ * served models stay on the GPU ([EXPLAINER §8.2]) and their cache shares HBM with the
+ * expert slots ([EXPLAINER §7.2]; [JUHE "显存还要在专家缓存和 KV Cache 之间动态分配"]); holding
+ * keys and values in 4 or 8 bits leaves that HBM to slots.  The pages give no kernel for
+ * this part; the layouts and rules below are this library's.
+ *
+ * A cache is L layers of n_pages pages of page_size tokens.  Token slot s of a layer is
+ * place s % page_size of page s / page_size.  A page holds, for each kv head in order,
+ * page_size / 16 tiles of 16 tokens, each one contiguous record of K codes, V codes and
+ * (NVFP4) K scales and V scales, its bytes in the order in which the attention's matrix
+ * instructions read them.  With D = head_dim and lane = 4 g + t (g 0..7, t 0..3):
+ *   K codes   per lane [v 2][D/4 dims]: token 8 v + g, dims t D/4 and on;
+ *   V codes   per lane [q 4][D/8 dims]: token 8 (q / 2) + 2 t + q % 2, dims g D/8 and on;
+ *             a lane's bytes are stored as 16-byte vectors, [vector][lane][16];
+ *   K scales  [lane][v 2][D/64 blocks of 16 dims];
+ *   V scales  [block of 16 dims][t 4][q 4].
+ * FT_KV_NVFP4: value = e2m1(code) * e4m3(scale) * s, one scale per 16 dims of a token and
+ *   head, two codes per byte, the even dim in the low nibble; 9/16 byte per element.
+ *   scale = E4M3_RNE((amax16 / 6) / s), code = E2M1_RNE_sat(x / (scale * s)); a zero scale
+ *   gives zeros (the record quantiser's fp32 IEEE steps).
+ * FT_KV_FP8: value = e4m3(code) * s, code = E4M3_RNE_sat(x / s); 1 byte per element.
+ * s is k_scale for keys and v_scale for values.  A NaN is stored as 0 and an infinity as
+ * the largest value, so nothing that is stored can turn a masked key into a NaN. */
+#define FT_KV_NVFP4 0
+#define FT_KV_FP8   1
+typedef struct ft_kv ft_kv;
+typedef struct {
+    int32_t L;              /* layers */
+    int32_t n_pages;        /* pages per layer; n_pages * page_size < 2^31 */
+    int32_t page_size;      /* tokens per page: 16, 32, 64, 128 or 256 */
+    int32_t n_kv_heads;     /* 1..1024 */
+    int32_t head_dim;       /* 64, 128 or 256 */
+    int32_t n_q_heads;      /* a multiple of n_kv_heads, at most 1024 */
+    int32_t max_seqs;       /* largest n_seqs passed to ft_kv_attention (1..4096) */
+    int32_t format;         /* FT_KV_NVFP4 or FT_KV_FP8 */
+    float k_scale, v_scale; /* tensor scales, finite and > 0 */
+    void* pool;             /* device, 256-byte aligned, pool_bytes; any contents */
+    void* workspace;        /* device, 256-byte aligned, workspace_bytes; owned by the handle */
+} ft_kv_desc;
+
+/* Bytes of the pool (L layers) and of the workspace (pointers in d are ignored). */
+ft_status ft_kv_required_sizes(const ft_kv_desc* d, size_t* pool_bytes, size_t* workspace_bytes);
+/* Create a cache over caller-owned memory; the pool's contents are kept (they may hold
+ * tokens that another handle of the same description wrote).  Synchronous.  Errors:
+ * FT_ERR_ARG (sizes, NULL, host or misaligned pointers), FT_ERR_CUDA. */
+ft_status ft_kv_create(const ft_kv_desc* d, ft_kv** out);
+void      ft_kv_destroy(ft_kv* kv);
+
+/* Quantise n new tokens of one layer into their slots.
+ *   k, v      device bf16 [n, n_kv_heads, D], 16-byte aligned; token strides k_stride and
+ *             v_stride in elements (multiples of 8, at least n_kv_heads * D)
+ *   slots     device int32 [n]; a token whose slot is -1 is padding and is skipped; another
+ *             slot outside [0, n_pages * page_size) is skipped and sets FT_DEV_BAD_ID;
+ *             the slots of one call differ from each other
+ * Asynchronous on stream, capturable.  n = 0 does nothing.  Errors (nothing launched):
+ * FT_ERR_ARG for layer outside [0, L), n < 0, NULL or misaligned k/v, bad strides. */
+ft_status ft_kv_append(ft_kv* kv, int32_t layer, const void* k, const void* v, int64_t k_stride,
+                       int64_t v_stride, const int32_t* slots, int32_t n, void* stream);
+
+/* Read n tokens of one layer back: the stored values rounded to bf16.
+ *   slots     device int32 [n], repeats allowed; -1 gives zeros, another slot outside the
+ *             cache gives zeros and sets FT_DEV_BAD_ID
+ *   k_out, v_out  device bf16 [n, n_kv_heads, D], 16-byte aligned
+ * Asynchronous on stream, capturable.  Errors: as ft_kv_append's. */
+ft_status ft_kv_read(ft_kv* kv, int32_t layer, const int32_t* slots, int32_t n, void* k_out,
+                     void* v_out, void* stream);
+
+/* Attention of each sequence's new tokens over its cached tokens, the new ones included
+ * (append them first).  Sequence s has the rows i = 0..n-1 at q_start[s] + i of q and o,
+ * n = q_start[s+1] - q_start[s], and kv_len[s] cached tokens; base = kv_len[s] - n.  Query
+ * head h reads kv head h / (n_q_heads / n_kv_heads).  Row i sees the key j, 0 <= j < kv_len, if
+ *   tree_mask NULL:  j <= base + i (causal);
+ *   tree_mask given: j < base, or bit j - base of tree_mask[q_start[s] + i] is set (drafted
+ *                    tokens: a row's ancestors and itself);
+ *   and window > 0:  j < n_sink or pos(i) - pos(j) < window, where pos is the token's index
+ *                    and, for a drafted token under a tree, base + the number of set bits of
+ *                    its mask other than its own.
+ * o = sum_j softmax_j(sm_scale * q.k_j) v_j over the keys seen, lse = log sum_j exp(sm_scale *
+ * q.k_j); a row that sees no key has o = 0 and lse = -inf.  Products are exact, sums and
+ * softmax statistics fp32, the softmax weights rounded to f16; results do not depend on the
+ * run (every sum has a fixed order for given arguments on one GPU).
+ *   q           device bf16 [n_tokens, n_q_heads, D], token stride q_stride (elements)
+ *   q_start     device int32 [n_seqs + 1], ascending, within [0, n_tokens]
+ *   kv_len      device int32 [n_seqs]
+ *   block_table device int32 [n_seqs, table_stride]: page of each page_size tokens in order;
+ *               only the pages that hold keys some row sees are read
+ *   max_q       the most new tokens that any sequence has (at most 64 with tree_mask)
+ *   tree_mask   device uint64 [n_tokens] or NULL
+ *   o           device bf16 [n_tokens, n_q_heads, D], token stride o_stride (elements)
+ *   lse         device fp32 [n_tokens, n_q_heads] or NULL
+ * Rows of q and o are 16-byte aligned.  Rows outside every sequence are left as they are.
+ * Asynchronous on stream, capturable, no allocation; calls of one handle share its
+ * workspace, so they run one after another (one stream, or ordered by events).
+ * What the host cannot see is bounded on the device: q_start outside its range, more than
+ * max_q rows (the rest are left as they are), kv_len outside [0, table_stride * page_size]
+ * and pages outside [0, n_pages) (their keys are not seen) set FT_DEV_BAD_ID.
+ * Errors (nothing launched): FT_ERR_ARG for layer, n_seqs outside [0, max_seqs], n_tokens
+ * < 0, table_stride < 1, max_q < 1 (or > 64 with tree_mask), window < 0, n_sink < 0, a
+ * sm_scale that is not finite, NULL or misaligned pointers, bad strides. */
+ft_status ft_kv_attention(ft_kv* kv, int32_t layer, const void* q, int64_t q_stride,
+                          const int32_t* q_start, const int32_t* kv_len,
+                          const int32_t* block_table, int32_t table_stride, int32_t n_seqs,
+                          int32_t n_tokens, int32_t max_q, const uint64_t* tree_mask,
+                          int32_t window, int32_t n_sink, float sm_scale, void* o,
+                          int64_t o_stride, float* lse, void* stream);
+
+/* Read and clear the handle's device status word (FT_DEV_* bits).  Synchronises. */
+ft_status ft_kv_status(ft_kv* kv, int32_t* device_status);
+/* Message of the last failed call on kv, or "" */
+const char* ft_kv_last_error(const ft_kv* kv);
+
 const char* ft_status_string(ft_status s);
 /* Message of the last failed call on c (static storage), or "" */
 const char* ft_last_error(const ft_cache* c);

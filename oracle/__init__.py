@@ -23,6 +23,7 @@ Modules:
   lru              the global cross-layer LRU slot cache (OrderedDict) and a
                    brute-force history-based twin
   moe              dense fp64 MoE-layer definitions for decode and prefill
+  kv               quantised key/value cache: formats, tile layout, masked attention
   static_placement the static (prefill-time) placement baseline simulator
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test against
