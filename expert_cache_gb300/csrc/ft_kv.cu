@@ -238,8 +238,6 @@ using namespace ft;
 
 namespace {
 
-constexpr size_t kStatusBytes = 256;
-
 ft_status fail(ft_kv* kv, ft_status s, const char* what) {
     if (kv) snprintf(kv->err, sizeof kv->err, "%s", what);
     return s;
@@ -267,7 +265,7 @@ ft_status check_desc(const ft_kv_desc* d) {
     if (d->n_kv_heads < 1 || d->n_kv_heads > 1024) return FT_ERR_ARG;
     if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return FT_ERR_ARG;
     if (d->n_q_heads < 1 || d->n_q_heads > 1024 || d->n_q_heads % d->n_kv_heads) return FT_ERR_ARG;
-    if (d->max_seqs < 1 || d->max_seqs > 4096) return FT_ERR_ARG;
+    if (d->max_seqs < 1 || d->max_seqs > kMaxSeqs) return FT_ERR_ARG;
     if (d->format != FT_KV_NVFP4 && d->format != FT_KV_FP8) return FT_ERR_ARG;
     if (!positive(d->k_scale) || !positive(d->v_scale)) return FT_ERR_ARG;
     return FT_OK;
@@ -300,7 +298,7 @@ ft_status ft_kv_required_sizes(const ft_kv_desc* d, size_t* pool_bytes, size_t* 
     const ft_status s = check_desc(d);
     if (s != FT_OK) return s;
     if (pool_bytes) *pool_bytes = (size_t)d->L * layer_bytes(*d);
-    if (workspace_bytes) *workspace_bytes = kStatusBytes;
+    if (workspace_bytes) *workspace_bytes = kKvStatusBytes + kKvPrefixBytes + kv_parts_bytes(d->head_dim);
     return FT_OK;
 }
 
@@ -319,7 +317,7 @@ ft_status ft_kv_create(const ft_kv_desc* d, ft_kv** out) {
     kv->page_shift = shift_of(d->page_size);
     kv->err[0] = 0;
     cudaError_t e = cudaDeviceSynchronize();
-    if (e == cudaSuccess) e = cudaMemset(d->workspace, 0, kStatusBytes);
+    if (e == cudaSuccess) e = cudaMemset(d->workspace, 0, kKvStatusBytes);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         delete kv;
@@ -399,6 +397,9 @@ ft_status ft_kv_attention(ft_kv* kv, int32_t layer, const void* q, int64_t q_str
     a.o = static_cast<__nv_bfloat16*>(o);
     a.o_stride = (size_t)o_stride;
     a.lse = lse;
+    uint8_t* ws = static_cast<uint8_t*>(d.workspace);
+    a.prefix = reinterpret_cast<long long*>(ws + kKvStatusBytes);
+    a.parts = reinterpret_cast<float*>(ws + kKvStatusBytes + kKvPrefixBytes);
     const cudaError_t e = launch_kv_attention(a, d.head_dim, d.format, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FT_OK : cuda_fail(kv, e, "attention launch");
 }

@@ -44,7 +44,15 @@ struct AttnArgs {
     __nv_bfloat16* o;
     size_t o_stride;
     float* lse;
+    long long* prefix;   // workspace: first tile of each sequence in the line of all tiles, [n_seqs + 1]
+    float* parts;        // workspace: partial sums of the units that a share's end cuts
 };
+
+constexpr int kMaxSeqs = 1024;         // sequences of one attention call
+
+// Bytes of the workspace's regions: status, prefix, parts.
+constexpr size_t kKvStatusBytes = 256, kKvPrefixBytes = (kMaxSeqs + 32) * 8;
+size_t kv_parts_bytes(int D);
 
 cudaError_t launch_kv_append(const KvView& kv, int D, int format, const void* k, const void* v, size_t k_stride,
                              size_t v_stride, const int32_t* slots, int n, cudaStream_t s);
@@ -90,7 +98,7 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int s) {
     r.q0 = min(max(a0, 0), a.n_tokens);
     const int q1 = min(max(a1, r.q0), a.n_tokens);
     r.n = min(q1 - r.q0, a.max_q);
-    const long long most = (long long)a.table_stride << a.kv.page_shift;
+    const long long most = min((long long)a.table_stride << a.kv.page_shift, 0x7FFFFC00LL);   // block ends fit 32 bits
     r.len = (int)min((long long)max(len, 0), most);
     r.bad = r.q0 != a0 || q1 != a1 || r.n != q1 - r.q0 || r.len != len;
     return r;

@@ -1,97 +1,777 @@
 // Attention over the quantised key/value cache.
 //
-// o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i.k_j - m_i), one pass over the keys with
-// the running maximum m_i and sum: a larger maximum m' rescales both by exp(m - m').
-#include "ft_kv.cuh"
-#include "ft_quant.cuh"
+// o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(t_ij - m_i),  t_ij = log2(e) scale q_i.k_j: one pass
+// over the keys with a running reference m_i and sum; partial (m, sum, o) of two key ranges join
+// by rescaling both to the larger m.
+//
+// Few rows share a key (a decode step has G = query heads per kv head of them), so the pass is
+// bound by the bytes of the cache and by unpacking them: 9/16 byte per element is 41 elements
+// per clock and SM at the copy rate.  Layout of the work:
+//   * A warp owns a run of 16-token tiles.  Tiles are contiguous records; the warp streams them
+//     through a ring in shared memory with one bulk copy each, several in flight, and no barrier
+//     but its own.
+//   * Keys stand on the m side of the matrix instruction (m16n8k16, f16 in, fp32 sums):
+//     S^T = K Q^T and O^T = V^T P^T with 8 rows on the n side, so a group of 8 query heads wastes
+//     nothing.  A tile's bytes are stored in the order in which the lanes' fragments need them:
+//     16-byte shared-memory loads, no shuffles; P^T is the transpose (movmatrix) of S^T's
+//     accumulators.
+//   * Codes become f16 by the conversion instructions; code * scale is exact in f16 (2 + 4
+//     significant bits, 2^-10 .. 2688); q is scaled by a power of two per row into f16's range.
+//   * The tiles of all (sequence, row tile, kv head) units are laid end to end and every CTA takes
+//     an equal share, so ragged batches balance; a unit cut by a share's end leaves partial sums
+//     in the workspace, which a second kernel (a programmatic dependent) joins in a fixed order.
+#include <atomic>
+
+#include "ft_kv_attn.cuh"
 
 namespace ft {
 
 namespace {
 
-// Stored value (without the tensor scale) of token r's dim d.
-template <int D, int kFormat, bool kV>
-__device__ __forceinline__ float kv_value(const uint8_t* tile, int r, int d) {
-    const int at = (kV ? kv_v_byte<D, kFormat>(r, d & ~7) : kv_k_byte<D, kFormat>(r, d & ~7)) +
-                   (kFormat == FT_KV_NVFP4 ? (d & 7) >> 1 : d & 7);
-    const uint32_t byte = tile[at];
-    if constexpr (kFormat == FT_KV_FP8) {
-        const float m = e4m3_value((uint8_t)(byte & 127u));
-        return byte & 128u ? -m : m;
-    } else {
-        const uint32_t c = byte >> (4 * (d & 1)) & 15u, m = c & 7u;
-        const float mag = m < 2 ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-        const float sc = e4m3_value(tile[kV ? kv_v_scale_byte<D>(r, d / 16) : kv_k_scale_byte<D>(r, d / 16)]);
-        return (c & 8u ? -mag : mag) * sc;
-    }
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kMinTiles = 2;           // tiles of a warp at least, unless there are fewer
+constexpr int kMaxPerSm = 4, kMaxShares = 640;     // CTAs
+constexpr int kMaxRows = 16;           // rows of a unit
+constexpr long kWaitLimit = 1L << 24;
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
+// Four f16 pairs from 8 E2M1 codes (a 32-bit word); two from 4 E4M3 codes.
+__device__ __forceinline__ void e2m1_unpack(uint32_t w, uint32_t (&o)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(w));
+}
+__device__ __forceinline__ void e4m3_unpack(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Tiles in flight per warp, about 9 to 16 KB.
+constexpr int stages(int D, int format) {
+    const int b = kv_tile(D, format).bytes;
+    return b <= 1152 ? 8 : b <= 2304 ? 4 : b <= 4096 ? 3 : 2;
+}
+
+template <int D, int kFormat, int NT>
+constexpr size_t rows_smem() {
+    const size_t ring = (size_t)kWarps * stages(D, kFormat) * kv_tile(D, kFormat).bytes;
+    const size_t join = (size_t)kWarps * 8 * NT * D * 4;
+    return ring > join ? ring : join;
 }
 
 }  // namespace
 
-// One warp per row and query head; lane l holds the dims l, l + 32, ...
-template <int D, int kFormat>
-__global__ void __launch_bounds__(128) kv_attention_simple_kernel(const AttnArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int s = blockIdx.y;
-    const SeqInfo si = seq_info(a, s);
-    if (si.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.kv.status, FT_DEV_BAD_ID);
-    const int base = si.len - si.n;
-    for (long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5); w < (long long)si.n * a.hq; w += (long long)gridDim.x * 4) {
-        const int i = (int)(w / a.hq), h = (int)(w % a.hq), kvh = h / a.G;
-        const size_t row = (size_t)si.q0 + i;
-        float q[D / 32], acc[D / 32];
+// The sequences' first tiles in the line of all tiles: prefix[0..n_seqs], in shared memory.
+template <int kB>
+__device__ __forceinline__ void tile_prefix(const AttnArgs& a, int R, long long* prefix, long long* scratch) {
+    const int per = (a.n_seqs + blockDim.x - 1) / blockDim.x;
+    const int s0 = min((int)threadIdx.x * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
+    long long sum = 0;
+    for (int s = s0; s < s1; ++s) {
+        const SeqInfo si = seq_info(a, s);
+        if (si.bad && blockIdx.x == 0) atomicOr(a.kv.status, FT_DEV_BAD_ID);
+        long long t = 0;
+        const int rt = (si.n * a.G + R - 1) / R;
+        for (int r = 0; r < rt; ++r) t += row_tile<kB>(a, si, r, R).nt;
+        prefix[s + 1] = t * a.kv.hkv;
+        sum += t * a.kv.hkv;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long incl = sum;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) {
-            q[e] = __bfloat162float(a.q[row * a.q_stride + (size_t)h * D + lane + 32 * e]);
-            acc[e] = 0.f;
-        }
-        const unsigned long long mine = a.tree ? a.tree[row] : 0;
-        const int pos = base + (a.tree ? __popcll(mine & ~(1ull << (i & 63))) : i);
-        float m = -INFINITY, l = 0.f;
-        for (int j = 0; j < si.len; ++j) {
-            const int jj = j - base;
-            if (a.tree ? (jj >= 0 && (jj > 63 || !(mine >> jj & 1))) : jj > i) continue;
-            if (a.window > 0 && j >= a.n_sink) {
-                const int pj = a.tree && jj >= 0 ? base + __popcll(a.tree[si.q0 + jj] & ~(1ull << jj)) : j;
-                if (pos - pj >= a.window) continue;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long at = incl - sum;
+    for (int w = 0; w < warp; ++w) at += scratch[w];
+    if (threadIdx.x == 0) prefix[0] = 0;
+    for (int s = s0; s < s1; ++s) {
+        at += prefix[s + 1];
+        prefix[s + 1] = at;
+    }
+    __syncthreads();
+}
+
+// The shares of the CTAs: cut of c = first tile of CTA c; the shares differ by one tile at most
+// and hold at least one each.
+struct Shares {
+    int nc;
+    long long q, rem;
+    __device__ __forceinline__ Shares(long long total, int grid) {
+        const long long want = (total + kWarps * kMinTiles - 1) / (kWarps * kMinTiles);
+        nc = (int)min((long long)grid, max(want, 1LL));
+        q = total / nc;
+        rem = total % nc;
+    }
+    __device__ __forceinline__ long long cut(int c) const { return q * c + min((long long)c, rem); }
+    __device__ __forceinline__ int holder(long long tile) const {
+        const long long wide = rem * (q + 1);
+        return (int)(tile < wide ? tile / (q + 1) : rem + (tile - wide) / q);
+    }
+};
+
+struct Unit {
+    int s, r, h;
+    long long first;         // its first tile in the line
+    SeqInfo si;
+    RowTile rt;
+};
+
+__device__ __forceinline__ Unit find_unit(const AttnArgs& a, const long long* prefix, long long tile, int R) {
+    Unit u;
+    int lo = 0, hi = a.n_seqs;
+    while (hi - lo > 1) {              // largest s with prefix[s] <= tile
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= tile) lo = mid; else hi = mid;
+    }
+    u.s = lo;
+    u.si = seq_info(a, lo);
+    u.first = prefix[lo];
+    for (u.r = 0;; ++u.r) {
+        u.rt = row_tile<kKvTile>(a, u.si, u.r, R);
+        const long long all = (long long)u.rt.nt * a.kv.hkv;
+        if (tile < u.first + all) break;
+        u.first += all;
+    }
+    u.h = (int)((tile - u.first) / u.rt.nt);
+    u.first += (long long)u.h * u.rt.nt;
+    return u;
+}
+
+// Partial sums of one share of a unit in the workspace: [R] references, [R] sums, [R][D] values.
+template <int D, int R>
+__device__ __forceinline__ float* partial(const AttnArgs& a, int slot) { return a.parts + (size_t)slot * (R * (D + 2)); }
+
+template <int D, int kFormat, int NT>
+__global__ void __launch_bounds__(kThreads) kv_rows_kernel(const AttnArgs a) {
+    constexpr int R = 8 * NT, kStages = stages(D, kFormat);
+    constexpr KvTile kT = kv_tile(D, kFormat);
+    constexpr bool kFour = kFormat == FT_KV_NVFP4;
+    constexpr int kKW = (kFour ? D / 4 : D / 2) / 4;       // 32-bit words of K codes per lane (both tokens)
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long prefix[kMaxSeqs + 1], scratch[kWarps];
+    __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+    __shared__ float join_m[kWarps][R], join_l[kWarps][R];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t bar0 = smem_u32(&bars[warp][0]);
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(bar0 + 8 * s));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    pdl_wait_and_release();
+    tile_prefix<kKvTile>(a, R, prefix, scratch);
+    if (blockIdx.x == 0)
+        for (int s = threadIdx.x; s <= a.n_seqs; s += kThreads) a.prefix[s] = prefix[s];
+    const long long total = prefix[a.n_seqs];
+    if (total == 0) return;
+    const Shares shares(total, gridDim.x);
+    if ((int)blockIdx.x >= shares.nc) return;
+    const long long c0 = shares.cut(blockIdx.x), c1 = shares.cut(blockIdx.x + 1);
+    Unit u = find_unit(a, prefix, c0, R);
+    const bool whole = c1 <= u.first + u.rt.nt;           // the CTA's share lies in one unit
+    const long long w0 = c0 + (c1 - c0) * warp / kWarps, w1 = c0 + (c1 - c0) * (warp + 1) / kWarps;
+    uint8_t* ring = smem + (size_t)warp * kStages * kT.bytes;
+    const uint32_t ring_u32 = smem_u32(ring);
+    uint32_t parity = 0;                                  // bit s: phase of stage s to wait for
+    int next = 0;                                         // stage that the next tile takes
+
+    for (long long pos = w0; pos < w1 || whole;) {
+        if (!whole && pos >= u.first + u.rt.nt) u = find_unit(a, prefix, pos, R);
+        const int v0 = (int)(pos - u.first), v1 = (int)min((long long)u.rt.nt, w1 - u.first);
+        const int base = u.si.len - u.si.n, row0 = u.r * R;
+
+        // ---------------------------------------------------------------- the rows
+        RowRule rule[NT][2];
+        uint32_t qf[NT][D / 16][2];
+        float coef[NT][2], m[NT][2], l[NT][2];
+        int lim_min = 0x7fffffff, low_max = 0;            // keys that every row sees: below lim_min, from low_max
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = row0 + 8 * nt + g, i = row / a.G;
+            const bool on = i < u.si.n;
+            const __nv_bfloat16* src = a.q + (size_t)(u.si.q0 + i) * a.q_stride + (size_t)(u.h * a.G + row % a.G) * D + t * (D / 4);
+            uint32_t raw[D / 8];
+            float amax = 0.f;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {
+                const uint4 x = on ? *reinterpret_cast<const uint4*>(src + 8 * e) : make_uint4(0, 0, 0, 0);
+                raw[4 * e] = x.x; raw[4 * e + 1] = x.y; raw[4 * e + 2] = x.z; raw[4 * e + 3] = x.w;
             }
-            const int page = a.table[(size_t)s * a.table_stride + (j >> a.kv.page_shift)];
-            if (page < 0 || page >= a.kv.n_pages) {
-                if (lane == 0) atomicOr(a.kv.status, FT_DEV_BAD_ID);
-                continue;
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e)
+                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[e] << 16)), fabsf(__uint_as_float(raw[e] & 0xFFFF0000u))));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // the row's largest magnitude goes to [2^13, 2^14): exact in f16 down to 2^-27 of it
+            const int ex = amax > 0.f && amax < INFINITY ? max((int)(__float_as_uint(amax) >> 23) - 140, -126) : 0;
+            const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e)
+                qf[nt][e >> 1][e & 1] = pack_f16(__uint_as_float(raw[e] << 16) * down,
+                                                 __uint_as_float(raw[e] & 0xFFFF0000u) * down);
+            const float c = a.scale * a.kv.k_scale * 1.44269504088896340736f * up;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                coef[nt][b] = __shfl_sync(0xffffffffu, c, 4 * (2 * t + b));
+                const int mine = row0 + 8 * nt + 2 * t + b;
+                rule[nt][b] = row_rule(a, u.si, mine);
+                if (mine / a.G < u.si.n) {
+                    lim_min = min(lim_min, a.tree ? min(rule[nt][b].lim, base - 1) : rule[nt][b].lim);
+                    low_max = max(low_max, rule[nt][b].low);
+                }
+                m[nt][b] = kNoRef;
+                l[nt][b] = 0.f;
             }
-            const int in = j & ((1 << a.kv.page_shift) - 1);
-            const uint8_t* tile = a.kv.pool + ((((size_t)page * a.kv.hkv + kvh) << (a.kv.page_shift - 4)) + (in >> 4)) *
-                                                  kv_tile(D, kFormat).bytes;
-            float z = 0.f;
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) z += q[e] * kv_value<D, kFormat, false>(tile, in & 15, lane + 32 * e);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-            z *= a.kv.k_scale * a.scale;
-            const float mn = fmaxf(m, z), ms = mn == -INFINITY ? 0.f : mn;      // a NaN logit stays a NaN weight
-            const float f = expf(m - ms), p = expf(z - ms);
-            m = mn;
-            l = l * f + p;
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e)
-                acc[e] = acc[e] * f + p * kv_value<D, kFormat, true>(tile, in & 15, lane + 32 * e);
         }
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            a.o[row * a.o_stride + (size_t)h * D + lane + 32 * e] =
-                __float2bfloat16(l > 0.f ? acc[e] / l * a.kv.v_scale : (l == 0.f ? 0.f : l));
-        if (a.lse && lane == 0) a.lse[row * a.hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+        for (int o = 1; o < 4; o <<= 1) {
+            lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
+            low_max = max(low_max, __shfl_xor_sync(0xffffffffu, low_max, o));
+        }
+        float acc[D / 16][NT][4];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
+
+        // ---------------------------------------------------------------- the keys
+        // lane x of the warp holds the page of tile v0 + 32 * (group of 32) + x
+        const int32_t* table = a.table + (size_t)u.s * a.table_stride;
+        const int per = a.kv.page_shift - 4;              // log2 of the tiles of a page
+        int page = -1, group = -1;
+        auto issue = [&](int v) {                         // start the copy of tile v, every lane of the warp
+            const int gr = (v - v0) >> 5;
+            if (gr != group) {
+                group = gr;
+                const int mine = v0 + 32 * gr + lane;
+                page = -1;
+                if (mine < v1) {
+                    page = table[u.rt.block(mine) >> per];
+                    if (page < 0 || page >= a.kv.n_pages) {
+                        atomicOr(a.kv.status, FT_DEV_BAD_ID);
+                        page = -1;
+                    }
+                }
+            }
+            const int pg = __shfl_sync(0xffffffffu, page, (v - v0) & 31);
+            if (lane == 0) {
+                const uint32_t bar = bar0 + 8 * next;
+                if (pg >= 0) {
+                    const int blk = u.rt.block(v);
+                    const uint8_t* src = a.kv.pool + ((((size_t)pg * a.kv.hkv + u.h) << per) + (blk & ((1 << per) - 1))) * kT.bytes;
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(kT.bytes) : "memory");
+                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                                 :: "r"(ring_u32 + next * kT.bytes), "l"(src), "r"(kT.bytes), "r"(bar) : "memory");
+                } else {
+                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+                }
+            }
+            next = next + 1 == kStages ? 0 : next + 1;
+            return pg >= 0;
+        };
+        const int vend = u.rt.empty ? v0 : v1;
+        uint32_t present = 0;                             // bit of a stage: its tile's page is one of the cache's
+        const int stage0 = next;
+        int cur = stage0;
+        for (int v = v0; v < min(vend, v0 + kStages); ++v) {
+            const int st = next;
+            if (issue(v)) present |= 1u << st;
+        }
+        for (int v = v0; v < vend; ++v) {
+            const uint32_t bar = bar0 + 8 * cur;
+            bool ok = false;
+            for (long it = 0; it < kWaitLimit && !ok; ++it) ok = mbar_try(bar, parity >> cur & 1);
+            if (!ok && lane == 0) atomicOr(a.kv.status, FT_DEV_TIMEOUT);
+            parity ^= 1u << cur;
+            const uint8_t* tile = ring + cur * kT.bytes;
+            const int j0 = u.rt.block(v) * kKvTile;
+            const bool have = present >> cur & 1;
+
+            // S^T = K Q^T
+            float sc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
+            {
+                uint32_t kw[kKW];
+#pragma unroll
+                for (int x = 0; x < kKW / 4; ++x) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(tile + x * 512 + lane * 16);
+                    kw[4 * x] = w.x; kw[4 * x + 1] = w.y; kw[4 * x + 2] = w.z; kw[4 * x + 3] = w.w;
+                }
+                if constexpr (kFour) {
+                    uint32_t sw[2] = {0, 0};              // the D/32 scale bytes of the lane: [token 2][D/64]
+                    const uint8_t* sp = tile + kT.k_scales + lane * (D / 32);
+                    if constexpr (D == 64) sw[0] = *reinterpret_cast<const uint16_t*>(sp);
+                    if constexpr (D == 128) sw[0] = *reinterpret_cast<const uint32_t*>(sp);
+                    if constexpr (D == 256) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(sp);
+                        sw[0] = w.x; sw[1] = w.y;
+                    }
+#pragma unroll
+                    for (int b = 0; b < D / 64; ++b) {    // block b of the lane's dims: 4 k-steps
+                        uint32_t s2[2];
+#pragma unroll
+                        for (int v2 = 0; v2 < 2; ++v2) {
+                            const int at = v2 * (D / 64) + b;
+                            const uint32_t byte = sw[at >> 2] >> (8 * (at & 3)) & 255u;
+                            uint32_t hi;
+                            e4m3_unpack(byte | byte << 8, s2[v2], hi);
+                        }
+                        uint32_t f[2][8];
+#pragma unroll
+                        for (int v2 = 0; v2 < 2; ++v2)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                uint32_t o[4];
+                                e2m1_unpack(kw[v2 * (D / 32) + 2 * b + x], o);
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) f[v2][4 * x + y] = hmul2(o[y], s2[v2]);
+                            }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma(sc[nt], f[0][2 * x], f[1][2 * x], f[0][2 * x + 1], f[1][2 * x + 1],
+                                    qf[nt][4 * b + x][0], qf[nt][4 * b + x][1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        uint32_t a0, a1, a2, a3;
+                        e4m3_unpack(kw[x], a0, a2);
+                        e4m3_unpack(kw[D / 16 + x], a1, a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma(sc[nt], a0, a1, a2, a3, qf[nt][x][0], qf[nt][x][1]);
+                    }
+                }
+            }
+
+            // weights.  sc[nt][0..1]: key j0 + g, rows 2t, 2t+1; [2..3]: key j0 + g + 8
+            const bool edge = !have || j0 + 15 > lim_min || (j0 < low_max && j0 + 15 >= a.n_sink);
+            bool over = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[nt][e] *= coef[nt][e & 1];
+            if (edge) {
+#pragma unroll
+                for (int e2 = 0; e2 < 2; ++e2) {
+                    const int j = j0 + g + 8 * e2;
+                    const bool drafted = a.tree && j >= base && j < u.si.len;
+                    const int jp = drafted && a.window > 0 ? drafted_pos(a, u.si, j) : 0x7fffffff;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const bool ok2 = have && (drafted ? sees_drafted(a, rule[nt][b], base, j, jp) : sees(a, rule[nt][b], j));
+                            if (!ok2) sc[nt][2 * e2 + b] = -INFINITY;
+                        }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) over |= sc[nt][e] - m[nt][e & 1] > kHeadroom;
+            if (__any_sync(0xffffffffu, over)) {          // raise the references to the rows' maxima
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        float x = fmaxf(sc[nt][b], sc[nt][2 + b]);
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                        x = fmaxf(x, m[nt][b]);
+                        const float f = ex2(m[nt][b] - x);
+                        m[nt][b] = x;
+                        l[nt][b] *= f;
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            acc[i][nt][b] *= f;
+                            acc[i][nt][2 + b] *= f;
+                        }
+                    }
+            }
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = ex2(sc[nt][e] - m[nt][e & 1] + kHeadroom);
+                    l[nt][e & 1] += p[e];
+                }
+                pf[nt][0] = transpose8x8(pack_f16(p[0], p[1]));
+                pf[nt][1] = transpose8x8(pack_f16(p[2], p[3]));
+            }
+
+            // O^T += V^T P^T.  The lane holds tokens 2t, 2t+1, 2t+8, 2t+9 and dims g D/8 ..
+            // Past the cached tokens (and in a tile that is not there) the bytes may be anything: zeroed.
+            const bool tail = !have || j0 + 16 > u.si.len;
+            if constexpr (kFour) {
+                uint32_t vw[D / 16];                      // [token 4][D/64 words]
+                if constexpr (D == 64) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(tile + kT.code_bytes + lane * 16);
+                    vw[0] = w.x; vw[1] = w.y; vw[2] = w.z; vw[3] = w.w;
+                } else {
+#pragma unroll
+                    for (int x = 0; x < D / 64; ++x) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(tile + kT.code_bytes + x * 512 + lane * 16);
+                        vw[4 * x] = w.x; vw[4 * x + 1] = w.y; vw[4 * x + 2] = w.z; vw[4 * x + 3] = w.w;
+                    }
+                }
+                constexpr int kBlocks = D == 256 ? 2 : 1; // blocks of 16 dims that the lane's dims touch
+                constexpr int kPer = D / 64 / kBlocks;    // words per token and block: 1, 2, 2
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    const int blk = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + b;
+                    uint32_t sw = *reinterpret_cast<const uint32_t*>(tile + kT.v_scales + (blk * 4 + t) * 4);
+                    if (tail) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (!have || j0 + 2 * t + (q & 1) + 8 * (q >> 1) >= u.si.len) sw &= ~(255u << (8 * q));
+                    }
+                    uint32_t s2[4];
+                    {
+                        uint32_t p01, p23;
+                        e4m3_unpack(sw, p01, p23);
+                        s2[0] = __byte_perm(p01, 0, 0x1010); s2[1] = __byte_perm(p01, 0, 0x3232);
+                        s2[2] = __byte_perm(p23, 0, 0x1010); s2[3] = __byte_perm(p23, 0, 0x3232);
+                    }
+#pragma unroll
+                    for (int x = 0; x < kPer; ++x) {
+                        uint32_t f[4][4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            e2m1_unpack(vw[q * (D / 64) + b * kPer + x], f[q]);
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) f[q][y] = hmul2(f[q][y], s2[q]);
+                        }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma(acc[(b * kPer + x) * 4 + y][nt], __byte_perm(f[0][y], f[1][y], 0x5410),
+                                    __byte_perm(f[0][y], f[1][y], 0x7632), __byte_perm(f[2][y], f[3][y], 0x5410),
+                                    __byte_perm(f[2][y], f[3][y], 0x7632), pf[nt][0], pf[nt][1]);
+                    }
+                }
+            } else {
+                uint32_t vw[D / 8];                       // [token 4][D/32 words]
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(tile + kT.code_bytes + x * 512 + lane * 16);
+                    vw[4 * x] = w.x; vw[4 * x + 1] = w.y; vw[4 * x + 2] = w.z; vw[4 * x + 3] = w.w;
+                }
+                if (tail) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (!have || j0 + 2 * t + (q & 1) + 8 * (q >> 1) >= u.si.len) {
+#pragma unroll
+                            for (int x = 0; x < D / 32; ++x) vw[q * (D / 32) + x] = 0;
+                        }
+                }
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x) {
+                    uint32_t f[4][2];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) e4m3_unpack(vw[q * (D / 32) + x], f[q][0], f[q][1]);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma(acc[2 * x + y][nt], __byte_perm(f[0][y], f[1][y], 0x5410), __byte_perm(f[0][y], f[1][y], 0x7632),
+                                __byte_perm(f[2][y], f[3][y], 0x5410), __byte_perm(f[2][y], f[3][y], 0x7632), pf[nt][0], pf[nt][1]);
+                }
+            }
+
+            __syncwarp();                                 // every lane has read the stage: refill it
+            present &= ~(1u << cur);
+            if (v + kStages < vend) {
+                const int st = next;
+                if (issue(v + kStages)) present |= 1u << st;
+            }
+            cur = cur + 1 == kStages ? 0 : cur + 1;
+        }
+        // ---------------------------------------------------------------- the sums of this run
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[nt][b] += __shfl_xor_sync(0xffffffffu, l[nt][b], o);
+
+        if (whole) {                                      // the CTA's warps join in shared memory
+            if (g == 0) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        join_m[warp][8 * nt + 2 * t + b] = m[nt][b];
+                        join_l[warp][8 * nt + 2 * t + b] = l[nt][b];
+                    }
+            }
+            __syncthreads();                              // also: no warp reads its ring any more
+            float* buf = reinterpret_cast<float*>(smem);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int row = 8 * nt + 2 * t + b;
+                    float mm = join_m[0][row];
+#pragma unroll
+                    for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, join_m[w][row]);
+                    const float f = ex2(m[nt][b] - mm);
+                    float* dst = buf + ((size_t)warp * R + row) * D + g * (D / 8);
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][nt][b] * f, acc[i][nt][2 + b] * f);
+                }
+            __syncthreads();
+            const bool done = c0 == u.first && c1 == u.first + u.rt.nt;
+            float* out = partial<D, R>(a, 2 * kWarps * blockIdx.x + (c0 > u.first ? 0 : 1));
+            for (int e = threadIdx.x; e < R * D / 4; e += kThreads) {
+                const int row = e / (D / 4), d = e % (D / 4) * 4;
+                const int i = (row0 + row) / a.G;
+                if (i >= u.si.n) continue;
+                float mm = join_m[0][row], ll = 0.f;
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, join_m[w][row]);
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    ll += join_l[w][row] * ex2(join_m[w][row] - mm);
+                    const float4 y = *reinterpret_cast<const float4*>(buf + ((size_t)w * R + row) * D + d);
+                    x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+                }
+                if (done) {
+                    const int h = u.h * a.G + (row0 + row) % a.G;
+                    store_out<4>(a, (size_t)(u.si.q0 + i), h, D, d, &x.x, mm, ll);
+                } else {
+                    *reinterpret_cast<float4*>(out + 2 * R + row * D + d) = x;
+                    if (d == 0) {
+                        out[row] = mm;
+                        out[R + row] = ll;
+                    }
+                }
+            }
+            return;
+        }
+
+        const bool done = v0 == 0 && v1 == u.rt.nt;
+        float* out = partial<D, R>(a, 2 * (kWarps * blockIdx.x + warp) + (v0 > 0 ? 0 : 1));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int row = 8 * nt + 2 * t + b, i = (row0 + row) / a.G;
+                if (i >= u.si.n) continue;
+                if (done) {
+                    const int h = u.h * a.G + (row0 + row) % a.G;
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x) {
+                        const float v[4] = {acc[2 * x][nt][b], acc[2 * x][nt][2 + b], acc[2 * x + 1][nt][b],
+                                            acc[2 * x + 1][nt][2 + b]};
+                        store_out<4>(a, (size_t)(u.si.q0 + i), h, D, g * (D / 8) + 4 * x, v, m[nt][b], l[nt][b]);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < D / 32; ++x)
+                        *reinterpret_cast<float4*>(out + 2 * R + row * D + g * (D / 8) + 4 * x) =
+                            make_float4(acc[2 * x][nt][b], acc[2 * x][nt][2 + b], acc[2 * x + 1][nt][b], acc[2 * x + 1][nt][2 + b]);
+                    if (g == 0) {
+                        out[row] = m[nt][b];
+                        out[R + row] = l[nt][b];
+                    }
+                }
+            }
+        pos = u.first + v1;
     }
 }
 
+// The shares of the units that a share's end cut, joined: kPer warps per row.  Partials are
+// taken in the order of the key ranges (by warp, then over the warps), so results do not depend
+// on timing.
+template <int D, int R, int kPer>
+__global__ void __launch_bounds__(kPer == 1 ? 256 : 32 * kPer) kv_join_kernel(const AttnArgs a, int row_tiles, int grid) {
+    constexpr int kRows = kPer == 1 ? 8 : 1;              // rows of a CTA
+    constexpr int E = D / 32;                             // values of a lane: dims lane * E ..
+    __shared__ float sm[kPer], sl[kPer];
+    __shared__ float sv[kPer == 1 ? 1 : kPer * D];
+    pdl_wait_and_release();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int unit = blockIdx.x / (R / kRows), row = blockIdx.x % (R / kRows) * kRows + (kPer == 1 ? warp : 0);
+    const int h = unit % a.kv.hkv, r = unit / a.kv.hkv % row_tiles, s = unit / a.kv.hkv / row_tiles;
+    const SeqInfo si = seq_info(a, s);
+    const int grow = r * R + row, i = grow / a.G;
+    if (i >= si.n) return;                                // the whole CTA, or its warps on their own
+    const Shares shares(a.prefix[a.n_seqs], grid);
+    long long u0 = a.prefix[s];
+    RowTile rt = row_tile<kKvTile>(a, si, 0, R);
+    for (int x = 0; x < r; ++x) {
+        u0 += (long long)rt.nt * a.kv.hkv;
+        rt = row_tile<kKvTile>(a, si, x + 1, R);
+    }
+    u0 += (long long)h * rt.nt;
+    const long long u1 = u0 + rt.nt;
+    const int ca = shares.holder(u0), cb = shares.holder(u1 - 1);
+    float m = kNoRef, l = 0.f, v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = 0.f;
+    auto take = [&](int slot) {
+        const float* p = partial<D, R>(a, slot);
+        const float pm = p[row], pl = p[R + row];
+        const float mm = fmaxf(m, pm), f = ex2(m - mm), pf = ex2(pm - mm);
+        m = mm;
+        l = l * f + pl * pf;
+        const float* src = p + 2 * R + row * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(src + e);
+            v[e] = v[e] * f + x.x * pf;
+            v[e + 1] = v[e + 1] * f + x.y * pf;
+        }
+    };
+    // a CTA at an end of the unit: one partial if its share lies in the unit, else its warps';
+    // false if the first kernel has written the unit
+    auto end = [&](int c) {
+        const long long c0 = shares.cut(c), c1 = shares.cut(c + 1);
+        if (c0 >= u0 && c1 <= u1) {
+            if (c0 == u0 && c1 == u1) return false;
+            if (warp == 0 || kPer == 1) take(2 * kWarps * c + (c0 > u0 ? 0 : 1));
+            return true;
+        }
+        for (int w = 0; w < kWarps; ++w) {
+            const long long w0 = max(c0 + (c1 - c0) * w / kWarps, u0), w1 = min(c0 + (c1 - c0) * (w + 1) / kWarps, u1);
+            if (w0 >= w1) continue;
+            if (w0 == u0 && w1 == u1) return false;
+            if (warp == w || kPer == 1) take(2 * (kWarps * c + w) + (w0 > u0 ? 0 : 1));
+        }
+        return true;
+    };
+    if (!end(ca)) return;
+#pragma unroll 4
+    for (int c = ca + 1 + (kPer == 1 ? 0 : warp); c < cb; c += kPer) take(2 * kWarps * c);
+    if (cb > ca) end(cb);
+    if constexpr (kPer > 1) {
+        if (lane == 0) {
+            sm[warp] = m;
+            sl[warp] = l;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) sv[warp * D + lane * E + e] = v[e];
+        __syncthreads();
+        if (threadIdx.x >= D / 4) return;
+        const int d = threadIdx.x * 4;
+        float mm = sm[0], ll = 0.f;
+        for (int w = 1; w < kPer; ++w) mm = fmaxf(mm, sm[w]);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < kPer; ++w) {
+            const float f = ex2(sm[w] - mm);
+            const float4 y = *reinterpret_cast<const float4*>(sv + w * D + d);
+            ll += sl[w] * f;
+            x.x += y.x * f; x.y += y.y * f; x.z += y.z * f; x.w += y.w * f;
+        }
+        store_out<4>(a, (size_t)(si.q0 + i), h * a.G + grow % a.G, D, d, &x.x, mm, ll);
+    } else {
+        #pragma unroll
+        for (int e = 0; e < E; e += E < 4 ? 2 : 4)
+            store_out<E < 4 ? 2 : 4>(a, (size_t)(si.q0 + i), h * a.G + grow % a.G, D, lane * E + e, v + e, m, l);
+    }
+}
+
+namespace {
+
+// CTAs of the rows kernel (looked up once per device): every one resident at once.
+template <int D, int kFormat, int NT>
+int rows_grid() {
+    static std::atomic<int> grids[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return 0;
+    }
+    int v = grids[dev].load(std::memory_order_relaxed);
+    if (!v) {
+        auto kern = kv_rows_kernel<D, kFormat, NT>;
+        constexpr size_t smem = rows_smem<D, kFormat, NT>();
+        int n = 0;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        v = min(sm_count() * min(n, kMaxPerSm), kMaxShares);
+        grids[dev].store(v, std::memory_order_relaxed);
+    }
+    return v;
+}
+
+template <int D, int kFormat, int NT>
+cudaError_t run_rows(const AttnArgs& a, cudaStream_t s) {
+    constexpr int R = 8 * NT;
+    const int grid = rows_grid<D, kFormat, NT>();
+    if (grid < 1) return cudaErrorInvalidConfiguration;
+    cudaError_t e = launch_pdl(kv_rows_kernel<D, kFormat, NT>, dim3(grid), dim3(kThreads), rows_smem<D, kFormat, NT>(), s, a);
+    if (e != cudaSuccess) return e;
+    const int row_tiles = (int)(((long long)a.max_q * a.G + R - 1) / R);
+    const long long rows = (long long)a.n_seqs * a.kv.hkv * row_tiles * R;
+    if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
+    // a few rows are joined by many warps each: their partials are many
+    if (rows <= 4 * 152) return launch_pdl(kv_join_kernel<D, R, 32>, dim3((unsigned)rows), dim3(1024), 0, s, a, row_tiles, grid);
+    if (rows <= 16 * 152) return launch_pdl(kv_join_kernel<D, R, 8>, dim3((unsigned)rows), dim3(256), 0, s, a, row_tiles, grid);
+    return launch_pdl(kv_join_kernel<D, R, 1>, dim3((unsigned)(rows / 8)), dim3(256), 0, s, a, row_tiles, grid);
+}
+
+template <int D, int kFormat>
+cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+    return (long long)a.max_q * a.G <= 8 ? run_rows<D, kFormat, 1>(a, s) : run_rows<D, kFormat, 2>(a, s);
+}
+
+}  // namespace
+
+size_t kv_parts_bytes(int D) { return (size_t)2 * kWarps * kMaxShares * kMaxRows * (D + 2) * sizeof(float); }
+
 cudaError_t launch_kv_attention(const AttnArgs& a, int D, int format, cudaStream_t s) {
-    const dim3 grid(256, a.n_seqs);
-#define FT_RUN(d, f) if (D == d && format == f) kv_attention_simple_kernel<d, f><<<grid, 128, 0, s>>>(a);
-    FT_RUN(64, FT_KV_NVFP4) FT_RUN(128, FT_KV_NVFP4) FT_RUN(256, FT_KV_NVFP4)
-    FT_RUN(64, FT_KV_FP8) FT_RUN(128, FT_KV_FP8) FT_RUN(256, FT_KV_FP8)
-#undef FT_RUN
-    return cudaGetLastError();
+    if (format == FT_KV_NVFP4)
+        return D == 64 ? run<64, FT_KV_NVFP4>(a, s) : D == 128 ? run<128, FT_KV_NVFP4>(a, s) : run<256, FT_KV_NVFP4>(a, s);
+    return D == 64 ? run<64, FT_KV_FP8>(a, s) : D == 128 ? run<128, FT_KV_FP8>(a, s) : run<256, FT_KV_FP8>(a, s);
 }
 
 }  // namespace ft

@@ -426,14 +426,16 @@ typedef struct {
     int32_t n_kv_heads;     /* 1..1024 */
     int32_t head_dim;       /* 64, 128 or 256 */
     int32_t n_q_heads;      /* a multiple of n_kv_heads, at most 1024 */
-    int32_t max_seqs;       /* largest n_seqs passed to ft_kv_attention (1..4096) */
+    int32_t max_seqs;       /* largest n_seqs passed to ft_kv_attention (1..1024) */
     int32_t format;         /* FT_KV_NVFP4 or FT_KV_FP8 */
     float k_scale, v_scale; /* tensor scales, finite and > 0 */
     void* pool;             /* device, 256-byte aligned, pool_bytes; any contents */
     void* workspace;        /* device, 256-byte aligned, workspace_bytes; owned by the handle */
 } ft_kv_desc;
 
-/* Bytes of the pool (L layers) and of the workspace (pointers in d are ignored). */
+/* Bytes of the pool (L layers) and of the workspace (pointers in d are ignored).  The
+ * workspace (one for all layers, 22 to 85 MB by head_dim) holds the partial sums of
+ * sequences whose keys several SMs share. */
 ft_status ft_kv_required_sizes(const ft_kv_desc* d, size_t* pool_bytes, size_t* workspace_bytes);
 /* Create a cache over caller-owned memory; the pool's contents are kept (they may hold
  * tokens that another handle of the same description wrote).  Synchronous.  Errors:
