@@ -170,10 +170,21 @@ def _ptr(t):
     raise TypeError(f"cannot take the address of {type(t)}")
 
 
+_raw_stream = None
+
+
 def _stream(s):
+    """cudaStream_t of a stream; None: torch's current one (asked for without building a
+    Stream object, which costs 3 us a call)."""
+    global _raw_stream
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            import torch
+            raw, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+            torch.cuda.init()
+            device = getattr(torch._C, "_cuda_getDevice", device)
+            _raw_stream = lambda: raw(device())  # noqa: E731
+        return _raw_stream()
     return s if isinstance(s, int) else s.cuda_stream
 
 

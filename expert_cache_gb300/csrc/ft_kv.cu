@@ -298,7 +298,7 @@ ft_status ft_kv_required_sizes(const ft_kv_desc* d, size_t* pool_bytes, size_t* 
     const ft_status s = check_desc(d);
     if (s != FT_OK) return s;
     if (pool_bytes) *pool_bytes = (size_t)d->L * layer_bytes(*d);
-    if (workspace_bytes) *workspace_bytes = kKvStatusBytes + kKvPrefixBytes + kv_parts_bytes(d->head_dim);
+    if (workspace_bytes) *workspace_bytes = kKvHeadBytes + kv_task_bytes() + kv_parts_bytes(d->head_dim);
     return FT_OK;
 }
 
@@ -317,7 +317,7 @@ ft_status ft_kv_create(const ft_kv_desc* d, ft_kv** out) {
     kv->page_shift = shift_of(d->page_size);
     kv->err[0] = 0;
     cudaError_t e = cudaDeviceSynchronize();
-    if (e == cudaSuccess) e = cudaMemset(d->workspace, 0, kKvStatusBytes);
+    if (e == cudaSuccess) e = cudaMemset(d->workspace, 0, kKvHeadBytes);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) {
         delete kv;
@@ -398,8 +398,8 @@ ft_status ft_kv_attention(ft_kv* kv, int32_t layer, const void* q, int64_t q_str
     a.o_stride = (size_t)o_stride;
     a.lse = lse;
     uint8_t* ws = static_cast<uint8_t*>(d.workspace);
-    a.prefix = reinterpret_cast<long long*>(ws + kKvStatusBytes);
-    a.parts = reinterpret_cast<float*>(ws + kKvStatusBytes + kKvPrefixBytes);
+    a.tasks = reinterpret_cast<JoinTask*>(ws + kKvHeadBytes);
+    a.parts = reinterpret_cast<float*>(ws + kKvHeadBytes + kv_task_bytes());
     const cudaError_t e = launch_kv_attention(a, d.head_dim, d.format, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? FT_OK : cuda_fail(kv, e, "attention launch");
 }

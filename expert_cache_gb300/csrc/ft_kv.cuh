@@ -29,6 +29,8 @@ struct KvView {
     int* status;
 };
 
+struct JoinTask;
+
 struct AttnArgs {
     KvView kv;
     const __nv_bfloat16* q;
@@ -44,14 +46,15 @@ struct AttnArgs {
     __nv_bfloat16* o;
     size_t o_stride;
     float* lse;
-    long long* prefix;   // workspace: first tile of each sequence in the line of all tiles, [n_seqs + 1]
+    JoinTask* tasks;      // workspace: what the joining kernel has to do
     float* parts;        // workspace: partial sums of the units that a share's end cuts
 };
 
 constexpr int kMaxSeqs = 1024;         // sequences of one attention call
 
-// Bytes of the workspace's regions: status, prefix, parts.
-constexpr size_t kKvStatusBytes = 256, kKvPrefixBytes = (kMaxSeqs + 32) * 8;
+// The workspace: a status word, the joining kernel's tasks, partial sums.
+constexpr size_t kKvHeadBytes = 256;
+size_t kv_task_bytes();
 size_t kv_parts_bytes(int D);
 
 cudaError_t launch_kv_append(const KvView& kv, int D, int format, const void* k, const void* v, size_t k_stride,

@@ -17,9 +17,11 @@
 //     accumulators.
 //   * Codes become f16 by the conversion instructions; code * scale is exact in f16 (2 + 4
 //     significant bits, 2^-10 .. 2688); q is scaled by a power of two per row into f16's range.
-//   * The tiles of all (sequence, row tile, kv head) units are laid end to end and every CTA takes
-//     an equal share, so ragged batches balance; a unit cut by a share's end leaves partial sums
-//     in the workspace, which a second kernel (a programmatic dependent) joins in a fixed order.
+//   * The (sequence, row tile, kv head) units are laid end to end, each as long as its tiles plus
+//     a constant for its own start and end, and every CTA takes an equal share of the line, so
+//     ragged batches balance.  A unit cut by a share's end leaves partial sums in the workspace;
+//     a second kernel, a programmatic dependent with the same grid, joins them in a fixed order:
+//     each of its CTAs a slice of the unit that the CTA's share began inside.
 #include <atomic>
 
 #include "ft_kv_attn.cuh"
@@ -30,6 +32,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kMinTiles = 2;           // tiles of a warp at least, unless there are fewer
+constexpr int kUnitCost = 8;           // a unit's start and end, in tiles
 constexpr int kMaxPerSm = 4, kMaxShares = 640;     // CTAs
 constexpr int kMaxRows = 16;           // rows of a unit
 constexpr long kWaitLimit = 1L << 24;
@@ -87,9 +90,12 @@ constexpr size_t rows_smem() {
     return ring > join ? ring : join;
 }
 
+// CTAs per SM that the register allocation aims at.
+constexpr int rows_ctas(int D, int NT) { return D == 256 ? (NT == 1 ? 3 : 2) : D == 128 ? (NT == 1 ? 4 : 3) : NT == 1 ? 4 : 3; }
+
 }  // namespace
 
-// The sequences' first tiles in the line of all tiles: prefix[0..n_seqs], in shared memory.
+// The sequences' first places in the line of all units: prefix[0..n_seqs], in shared memory.
 template <int kB>
 __device__ __forceinline__ void tile_prefix(const AttnArgs& a, int R, long long* prefix, long long* scratch) {
     const int per = (a.n_seqs + blockDim.x - 1) / blockDim.x;
@@ -100,7 +106,7 @@ __device__ __forceinline__ void tile_prefix(const AttnArgs& a, int R, long long*
         if (si.bad && blockIdx.x == 0) atomicOr(a.kv.status, FT_DEV_BAD_ID);
         long long t = 0;
         const int rt = (si.n * a.G + R - 1) / R;
-        for (int r = 0; r < rt; ++r) t += row_tile<kB>(a, si, r, R).nt;
+        for (int r = 0; r < rt; ++r) t += kUnitCost + row_tile<kB>(a, si, r, R).nt;
         prefix[s + 1] = t * a.kv.hkv;
         sum += t * a.kv.hkv;
     }
@@ -123,58 +129,150 @@ __device__ __forceinline__ void tile_prefix(const AttnArgs& a, int R, long long*
     __syncthreads();
 }
 
-// The shares of the CTAs: cut of c = first tile of CTA c; the shares differ by one tile at most
-// and hold at least one each.
+// The shares of the CTAs: cut(c) = first place of CTA c; they differ by one at most.
 struct Shares {
     int nc;
     long long q, rem;
+    __device__ __forceinline__ Shares(int nc_, long long q_, long long rem_) : nc(nc_), q(q_), rem(rem_) {}
     __device__ __forceinline__ Shares(long long total, int grid) {
         const long long want = (total + kWarps * kMinTiles - 1) / (kWarps * kMinTiles);
         nc = (int)min((long long)grid, max(want, 1LL));
         q = total / nc;
-        rem = total % nc;
+        rem = total - q * nc;
     }
     __device__ __forceinline__ long long cut(int c) const { return q * c + min((long long)c, rem); }
-    __device__ __forceinline__ int holder(long long tile) const {
+    __device__ __forceinline__ int holder(long long place) const {
         const long long wide = rem * (q + 1);
-        return (int)(tile < wide ? tile / (q + 1) : rem + (tile - wide) / q);
+        return (int)(place < wide ? place / (q + 1) : rem + (place - wide) / q);
     }
 };
 
 struct Unit {
     int s, r, h;
-    long long first;         // its first tile in the line
+    long long first, end;    // its places in the line
     SeqInfo si;
     RowTile rt;
+    __device__ __forceinline__ int tile_at(long long place) const;
 };
 
-__device__ __forceinline__ Unit find_unit(const AttnArgs& a, const long long* prefix, long long tile, int R) {
+// Tile of a unit that stands at a place (0 before its first tile, nt from its end on).
+__device__ __forceinline__ int tile_at(long long first, int nt, long long place) {
+    return (int)min(max(place - first - kUnitCost, 0LL), (long long)nt);
+}
+__device__ __forceinline__ int Unit::tile_at(long long place) const { return ft::tile_at(first, rt.nt, place); }
+
+__device__ __forceinline__ Unit find_unit(const AttnArgs& a, const long long* prefix, long long place, int R) {
     Unit u;
     int lo = 0, hi = a.n_seqs;
-    while (hi - lo > 1) {              // largest s with prefix[s] <= tile
+    while (hi - lo > 1) {              // largest s with prefix[s] <= place
         const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= tile) lo = mid; else hi = mid;
+        if (prefix[mid] <= place) lo = mid; else hi = mid;
     }
     u.s = lo;
     u.si = seq_info(a, lo);
     u.first = prefix[lo];
+    long long len;
     for (u.r = 0;; ++u.r) {
         u.rt = row_tile<kKvTile>(a, u.si, u.r, R);
-        const long long all = (long long)u.rt.nt * a.kv.hkv;
-        if (tile < u.first + all) break;
-        u.first += all;
+        len = kUnitCost + u.rt.nt;
+        if (place < u.first + len * a.kv.hkv) break;
+        u.first += len * a.kv.hkv;
     }
-    u.h = (int)((tile - u.first) / u.rt.nt);
-    u.first += (long long)u.h * u.rt.nt;
+    u.h = (int)((place - u.first) / len);
+    u.first += u.h * len;
+    u.end = u.first + len;
     return u;
+}
+
+// The pieces of a unit: one per CTA whose share lies in the unit, one per warp elsewhere.
+struct Piece {
+    int v0, v1, slot;        // tiles [v0, v1), where its partial sums stand
+};
+__device__ __forceinline__ Piece piece_of(const Shares& sh, long long first, int nt, int c, int w) {
+    const long long c0 = sh.cut(c), c1 = sh.cut(c + 1);
+    Piece p{0, 0, 0};
+    if (c0 >= first && c1 <= first + kUnitCost + nt) {
+        if (w == 0) {
+            p.v0 = tile_at(first, nt, c0);
+            p.v1 = tile_at(first, nt, c1);
+        }
+    } else {
+        p.v0 = tile_at(first, nt, c0 + (c1 - c0) * w / kWarps);
+        p.v1 = tile_at(first, nt, c0 + (c1 - c0) * (w + 1) / kWarps);
+    }
+    // a share holds at most one unit's later piece and one unit's first
+    p.slot = 2 * (kWarps * c + w) + (p.v0 > 0 ? 0 : 1);
+    return p;
 }
 
 // Partial sums of one share of a unit in the workspace: [R] references, [R] sums, [R][D] values.
 template <int D, int R>
 __device__ __forceinline__ float* partial(const AttnArgs& a, int slot) { return a.parts + (size_t)slot * (R * (D + 2)); }
 
+// What the second kernel needs to know of a unit that is cut (a: its first and last CTA).
+struct __align__(16) JoinTask {
+    long long q, rem, first;
+    int nc, nt, q0, n, r, h, ca, cb, on;
+};
+
+// Slice `part` of `parts` of unit u's output from its pieces, by n_threads threads (a multiple of
+// 32, whole warps, `sync` between them).  A team of lanes takes four values of a row: lane k of it
+// the pieces k, k + team, ..., then a butterfly, so the order of the sums is fixed.  Teams are as
+// large as the slice leaves threads for.  slots: shared, 2 kWarps + CTAs of the unit.
+template <int D, int R, typename Sync>
+__device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u, int part, int parts, int thread,
+                                           int n_threads, int* slots, Sync sync) {
+    const Shares sh(u.nc, u.q, u.rem);
+    const int ca = u.ca, cb = u.cb;
+    // pieces: the warps of the first CTA, one each of the CTAs between, the warps of the last
+    const int n = cb == ca ? kWarps : 2 * kWarps + cb - ca - 1;
+    for (int k = thread; k < n; k += n_threads) {
+        const int mid = k - kWarps, c = mid < 0 ? ca : min(ca + 1 + mid, cb);
+        const Piece p = piece_of(sh, u.first, u.nt, c, mid < 0 ? k : max(mid - (cb - ca - 1), 0));
+        slots[k] = p.v0 == p.v1 ? -1 : p.v1 - p.v0 == u.nt ? -2 : p.slot;
+    }
+    sync();
+    for (int w = 0; w < kWarps; ++w)
+        if (slots[w] == -2 || slots[n - 1 - w] == -2) return;                // not cut: written already
+    const int rows = min(R, u.n * a.G - u.r * R), groups = rows * (D / 4);
+    const int ga = (int)((long long)groups * part / parts), gb = (int)((long long)groups * (part + 1) / parts);
+    int team = 1;
+    while (team < 32 && team < n && (gb - ga) * team < n_threads) team *= 2;
+    for (int g0 = ga; g0 < gb; g0 += n_threads / team) {
+        const int e = min(g0 + thread / team, gb - 1);
+        const int row = e / (D / 4), d = e % (D / 4) * 4;
+        float m = kNoRef, l = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = thread & (team - 1); k < n; k += team) {
+            const int slot = slots[k];
+            if (slot < 0) continue;
+            const float* src = partial<D, R>(a, slot);
+            const float pm = __ldcg(src + row), pl = __ldcg(src + R + row);
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(src + 2 * R + row * D + d));
+            const float mm = fmaxf(m, pm), f = ex2(m - mm), pf = ex2(pm - mm);
+            m = mm;
+            l = l * f + pl * pf;
+            x.x = x.x * f + y.x * pf; x.y = x.y * f + y.y * pf; x.z = x.z * f + y.z * pf; x.w = x.w * f + y.w * pf;
+        }
+        for (int o = 1; o < team; o <<= 1) {
+            const float om = __shfl_xor_sync(0xffffffffu, m, o), mm = fmaxf(m, om), f = ex2(m - mm), of = ex2(om - mm);
+            const float ol = __shfl_xor_sync(0xffffffffu, l, o);
+            const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o),
+                                         __shfl_xor_sync(0xffffffffu, x.z, o), __shfl_xor_sync(0xffffffffu, x.w, o));
+            m = mm;
+            l = l * f + ol * of;
+            x.x = x.x * f + y.x * of; x.y = x.y * f + y.y * of; x.z = x.z * f + y.z * of; x.w = x.w * f + y.w * of;
+        }
+        if (g0 + thread / team < gb && (thread & (team - 1)) == 0) {
+            const int grow = u.r * R + row;
+            store_out<4>(a, (size_t)(u.q0 + grow / a.G), u.h * a.G + grow % a.G, D, d, &x.x, m, l);
+        }
+    }
+}
+
 template <int D, int kFormat, int NT>
-__global__ void __launch_bounds__(kThreads) kv_rows_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(const AttnArgs a) {
     constexpr int R = 8 * NT, kStages = stages(D, kFormat);
     constexpr KvTile kT = kv_tile(D, kFormat);
     constexpr bool kFour = kFormat == FT_KV_NVFP4;
@@ -193,25 +291,99 @@ __global__ void __launch_bounds__(kThreads) kv_rows_kernel(const AttnArgs a) {
     __syncwarp();
     pdl_wait_and_release();
     tile_prefix<kKvTile>(a, R, prefix, scratch);
-    if (blockIdx.x == 0)
-        for (int s = threadIdx.x; s <= a.n_seqs; s += kThreads) a.prefix[s] = prefix[s];
     const long long total = prefix[a.n_seqs];
-    if (total == 0) return;
     const Shares shares(total, gridDim.x);
-    if ((int)blockIdx.x >= shares.nc) return;
-    const long long c0 = shares.cut(blockIdx.x), c1 = shares.cut(blockIdx.x + 1);
+    const int cta = blockIdx.x;
+    JoinTask* task = a.tasks + kWarps * cta + warp;
+    if (total == 0 || cta >= shares.nc) {
+        if (lane == 0) task->on = 0;
+        return;
+    }
+    const long long c0 = shares.cut(cta), c1 = shares.cut(cta + 1);
     Unit u = find_unit(a, prefix, c0, R);
-    const bool whole = c1 <= u.first + u.rt.nt;           // the CTA's share lies in one unit
+    const bool whole = c1 <= u.end;                       // the CTA's share lies in one unit: its warps split the tiles
     const long long w0 = c0 + (c1 - c0) * warp / kWarps, w1 = c0 + (c1 - c0) * (warp + 1) / kWarps;
     uint8_t* ring = smem + (size_t)warp * kStages * kT.bytes;
     const uint32_t ring_u32 = smem_u32(ring);
     uint32_t parity = 0;                                  // bit s: phase of stage s to wait for
     int next = 0;                                         // stage that the next tile takes
 
-    for (long long pos = w0; pos < w1 || whole;) {
-        if (!whole && pos >= u.first + u.rt.nt) u = find_unit(a, prefix, pos, R);
-        const int v0 = (int)(pos - u.first), v1 = (int)min((long long)u.rt.nt, w1 - u.first);
+    // The cut at the start of the CTA's share goes through unit v, or the cut at the start of the
+    // warp's is the first through a unit that begins and ends in the CTA's.
+    auto note_task = [&](const Unit& v) {
+        if (lane != 0) return;
+        JoinTask j;
+        j.on = warp == 0 ? v.first < c0 : !whole && v.first < w0 && v.first >= c0 + (c1 - c0) * (warp - 1) / kWarps && v.end <= c1;
+        if (j.on) {
+            j.q = shares.q; j.rem = shares.rem; j.nc = shares.nc;
+            j.first = v.first; j.nt = v.rt.nt;
+            j.q0 = v.si.q0; j.n = v.si.n; j.r = v.r; j.h = v.h;
+            j.ca = warp == 0 ? shares.holder(v.first) : cta;
+            j.cb = warp == 0 ? shares.holder(v.end - 1) : cta;
+            *task = j;
+        } else {
+            task->on = 0;
+        }
+    };
+
+    for (long long pos = w0; pos < w1 || whole; pos = u.end) {
+        if (!whole && (pos >= u.end || pos < u.first)) u = find_unit(a, prefix, pos, R);
+        int v0 = u.tile_at(whole ? c0 : pos), v1 = u.tile_at(whole ? c1 : w1);
+        const int cv0 = v0, cv1 = v1;
+        if (whole) {
+            v0 = cv0 + (cv1 - cv0) * warp / kWarps;
+            v1 = cv0 + (cv1 - cv0) * (warp + 1) / kWarps;
+        }
+        if (cv0 == cv1) {                                 // none of the unit's tiles
+            if (pos == w0) note_task(u);
+            if (whole) break;
+            continue;
+        }
         const int base = u.si.len - u.si.n, row0 = u.r * R;
+
+        // ---------------------------------------------------------------- the first copies
+        // lane x of the warp holds the page of tile v0 + 32 * (group of 32) + x
+        const int32_t* table = a.table + (size_t)u.s * a.table_stride;
+        const int per = a.kv.page_shift - 4;              // log2 of the tiles of a page
+        int page = -1, group = -1;
+        auto issue = [&](int v) {                         // start the copy of tile v, every lane of the warp
+            const int gr = (v - v0) >> 5;
+            if (gr != group) {
+                group = gr;
+                const int mine = v0 + 32 * gr + lane;
+                page = -1;
+                if (mine < v1) {
+                    page = table[u.rt.block(mine) >> per];
+                    if (page < 0 || page >= a.kv.n_pages) {
+                        atomicOr(a.kv.status, FT_DEV_BAD_ID);
+                        page = -1;
+                    }
+                }
+            }
+            const int pg = __shfl_sync(0xffffffffu, page, (v - v0) & 31);
+            if (lane == 0) {
+                const uint32_t bar = bar0 + 8 * next;
+                if (pg >= 0) {
+                    const int blk = u.rt.block(v);
+                    const uint8_t* src = a.kv.pool + ((((size_t)pg * a.kv.hkv + u.h) << per) + (blk & ((1 << per) - 1))) * kT.bytes;
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(kT.bytes) : "memory");
+                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                                 :: "r"(ring_u32 + next * kT.bytes), "l"(src), "r"(kT.bytes), "r"(bar) : "memory");
+                } else {
+                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
+                }
+            }
+            next = next + 1 == kStages ? 0 : next + 1;
+            return pg >= 0;
+        };
+        const int vend = u.rt.empty ? v0 : v1;
+        uint32_t present = 0;                             // bit of a stage: its tile's page is one of the cache's
+        int cur = next;
+        for (int v = v0; v < min(vend, v0 + kStages); ++v) {
+            const int st = next;
+            if (issue(v)) present |= 1u << st;
+        }
+        if (pos == w0) note_task(u);
 
         // ---------------------------------------------------------------- the rows
         RowRule rule[NT][2];
@@ -270,48 +442,6 @@ __global__ void __launch_bounds__(kThreads) kv_rows_kernel(const AttnArgs a) {
                 for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
 
         // ---------------------------------------------------------------- the keys
-        // lane x of the warp holds the page of tile v0 + 32 * (group of 32) + x
-        const int32_t* table = a.table + (size_t)u.s * a.table_stride;
-        const int per = a.kv.page_shift - 4;              // log2 of the tiles of a page
-        int page = -1, group = -1;
-        auto issue = [&](int v) {                         // start the copy of tile v, every lane of the warp
-            const int gr = (v - v0) >> 5;
-            if (gr != group) {
-                group = gr;
-                const int mine = v0 + 32 * gr + lane;
-                page = -1;
-                if (mine < v1) {
-                    page = table[u.rt.block(mine) >> per];
-                    if (page < 0 || page >= a.kv.n_pages) {
-                        atomicOr(a.kv.status, FT_DEV_BAD_ID);
-                        page = -1;
-                    }
-                }
-            }
-            const int pg = __shfl_sync(0xffffffffu, page, (v - v0) & 31);
-            if (lane == 0) {
-                const uint32_t bar = bar0 + 8 * next;
-                if (pg >= 0) {
-                    const int blk = u.rt.block(v);
-                    const uint8_t* src = a.kv.pool + ((((size_t)pg * a.kv.hkv + u.h) << per) + (blk & ((1 << per) - 1))) * kT.bytes;
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(kT.bytes) : "memory");
-                    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                                 :: "r"(ring_u32 + next * kT.bytes), "l"(src), "r"(kT.bytes), "r"(bar) : "memory");
-                } else {
-                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
-                }
-            }
-            next = next + 1 == kStages ? 0 : next + 1;
-            return pg >= 0;
-        };
-        const int vend = u.rt.empty ? v0 : v1;
-        uint32_t present = 0;                             // bit of a stage: its tile's page is one of the cache's
-        const int stage0 = next;
-        int cur = stage0;
-        for (int v = v0; v < min(vend, v0 + kStages); ++v) {
-            const int st = next;
-            if (issue(v)) present |= 1u << st;
-        }
         for (int v = v0; v < vend; ++v) {
             const uint32_t bar = bar0 + 8 * cur;
             bool ok = false;
@@ -564,8 +694,8 @@ __global__ void __launch_bounds__(kThreads) kv_rows_kernel(const AttnArgs a) {
                         *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][nt][b] * f, acc[i][nt][2 + b] * f);
                 }
             __syncthreads();
-            const bool done = c0 == u.first && c1 == u.first + u.rt.nt;
-            float* out = partial<D, R>(a, 2 * kWarps * blockIdx.x + (c0 > u.first ? 0 : 1));
+            const bool done = cv0 == 0 && cv1 == u.rt.nt;
+            float* out = partial<D, R>(a, 2 * kWarps * cta + (cv0 > 0 ? 0 : 1));
             for (int e = threadIdx.x; e < R * D / 4; e += kThreads) {
                 const int row = e / (D / 4), d = e % (D / 4) * 4;
                 const int i = (row0 + row) / a.G;
@@ -591,11 +721,11 @@ __global__ void __launch_bounds__(kThreads) kv_rows_kernel(const AttnArgs a) {
                     }
                 }
             }
-            return;
+            break;
         }
 
         const bool done = v0 == 0 && v1 == u.rt.nt;
-        float* out = partial<D, R>(a, 2 * (kWarps * blockIdx.x + warp) + (v0 > 0 ? 0 : 1));
+        float* out = partial<D, R>(a, 2 * (kWarps * cta + warp) + (v0 > 0 ? 0 : 1));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -621,99 +751,22 @@ __global__ void __launch_bounds__(kThreads) kv_rows_kernel(const AttnArgs a) {
                     }
                 }
             }
-        pos = u.first + v1;
     }
+
 }
 
-// The shares of the units that a share's end cut, joined: kPer warps per row.  Partials are
-// taken in the order of the key ranges (by warp, then over the warps), so results do not depend
-// on timing.
-template <int D, int R, int kPer>
-__global__ void __launch_bounds__(kPer == 1 ? 256 : 32 * kPer) kv_join_kernel(const AttnArgs a, int row_tiles, int grid) {
-    constexpr int kRows = kPer == 1 ? 8 : 1;              // rows of a CTA
-    constexpr int E = D / 32;                             // values of a lane: dims lane * E ..
-    __shared__ float sm[kPer], sl[kPer];
-    __shared__ float sv[kPer == 1 ? 1 : kPer * D];
+// The second kernel: CTA c joins a slice of the unit that holds the first place of its share and
+// began before it (the CTAs behind the one that the unit began in take a slice each), and each warp
+// the unit that began and ends in the CTA's share and that the warp's place is the first cut in.
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads) kv_join_kernel(const AttnArgs a) {
+    __shared__ int slots[2 * kWarps + kMaxShares], warp_slots[kWarps][kWarps];
     pdl_wait_and_release();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int unit = blockIdx.x / (R / kRows), row = blockIdx.x % (R / kRows) * kRows + (kPer == 1 ? warp : 0);
-    const int h = unit % a.kv.hkv, r = unit / a.kv.hkv % row_tiles, s = unit / a.kv.hkv / row_tiles;
-    const SeqInfo si = seq_info(a, s);
-    const int grow = r * R + row, i = grow / a.G;
-    if (i >= si.n) return;                                // the whole CTA, or its warps on their own
-    const Shares shares(a.prefix[a.n_seqs], grid);
-    long long u0 = a.prefix[s];
-    RowTile rt = row_tile<kKvTile>(a, si, 0, R);
-    for (int x = 0; x < r; ++x) {
-        u0 += (long long)rt.nt * a.kv.hkv;
-        rt = row_tile<kKvTile>(a, si, x + 1, R);
-    }
-    u0 += (long long)h * rt.nt;
-    const long long u1 = u0 + rt.nt;
-    const int ca = shares.holder(u0), cb = shares.holder(u1 - 1);
-    float m = kNoRef, l = 0.f, v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = 0.f;
-    auto take = [&](int slot) {
-        const float* p = partial<D, R>(a, slot);
-        const float pm = p[row], pl = p[R + row];
-        const float mm = fmaxf(m, pm), f = ex2(m - mm), pf = ex2(pm - mm);
-        m = mm;
-        l = l * f + pl * pf;
-        const float* src = p + 2 * R + row * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const float2 x = *reinterpret_cast<const float2*>(src + e);
-            v[e] = v[e] * f + x.x * pf;
-            v[e + 1] = v[e + 1] * f + x.y * pf;
-        }
-    };
-    // a CTA at an end of the unit: one partial if its share lies in the unit, else its warps';
-    // false if the first kernel has written the unit
-    auto end = [&](int c) {
-        const long long c0 = shares.cut(c), c1 = shares.cut(c + 1);
-        if (c0 >= u0 && c1 <= u1) {
-            if (c0 == u0 && c1 == u1) return false;
-            if (warp == 0 || kPer == 1) take(2 * kWarps * c + (c0 > u0 ? 0 : 1));
-            return true;
-        }
-        for (int w = 0; w < kWarps; ++w) {
-            const long long w0 = max(c0 + (c1 - c0) * w / kWarps, u0), w1 = min(c0 + (c1 - c0) * (w + 1) / kWarps, u1);
-            if (w0 >= w1) continue;
-            if (w0 == u0 && w1 == u1) return false;
-            if (warp == w || kPer == 1) take(2 * (kWarps * c + w) + (w0 > u0 ? 0 : 1));
-        }
-        return true;
-    };
-    if (!end(ca)) return;
-#pragma unroll 4
-    for (int c = ca + 1 + (kPer == 1 ? 0 : warp); c < cb; c += kPer) take(2 * kWarps * c);
-    if (cb > ca) end(cb);
-    if constexpr (kPer > 1) {
-        if (lane == 0) {
-            sm[warp] = m;
-            sl[warp] = l;
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) sv[warp * D + lane * E + e] = v[e];
-        __syncthreads();
-        if (threadIdx.x >= D / 4) return;
-        const int d = threadIdx.x * 4;
-        float mm = sm[0], ll = 0.f;
-        for (int w = 1; w < kPer; ++w) mm = fmaxf(mm, sm[w]);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < kPer; ++w) {
-            const float f = ex2(sm[w] - mm);
-            const float4 y = *reinterpret_cast<const float4*>(sv + w * D + d);
-            ll += sl[w] * f;
-            x.x += y.x * f; x.y += y.y * f; x.z += y.z * f; x.w += y.w * f;
-        }
-        store_out<4>(a, (size_t)(si.q0 + i), h * a.G + grow % a.G, D, d, &x.x, mm, ll);
-    } else {
-        #pragma unroll
-        for (int e = 0; e < E; e += E < 4 ? 2 : 4)
-            store_out<E < 4 ? 2 : 4>(a, (size_t)(si.q0 + i), h * a.G + grow % a.G, D, lane * E + e, v + e, m, l);
-    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const JoinTask all = a.tasks[kWarps * blockIdx.x], mine = a.tasks[kWarps * blockIdx.x + warp];
+    if (all.on)
+        join_slice<D, R>(a, all, blockIdx.x - all.ca - 1, all.cb - all.ca, threadIdx.x, kThreads, slots, [] { __syncthreads(); });
+    if (warp > 0 && mine.on) join_slice<D, R>(a, mine, 0, 1, lane, 32, warp_slots[warp], [] { __syncwarp(); });
 }
 
 namespace {
@@ -745,18 +798,11 @@ int rows_grid() {
 
 template <int D, int kFormat, int NT>
 cudaError_t run_rows(const AttnArgs& a, cudaStream_t s) {
-    constexpr int R = 8 * NT;
     const int grid = rows_grid<D, kFormat, NT>();
     if (grid < 1) return cudaErrorInvalidConfiguration;
-    cudaError_t e = launch_pdl(kv_rows_kernel<D, kFormat, NT>, dim3(grid), dim3(kThreads), rows_smem<D, kFormat, NT>(), s, a);
+    const cudaError_t e = launch_pdl(kv_rows_kernel<D, kFormat, NT>, dim3(grid), dim3(kThreads), rows_smem<D, kFormat, NT>(), s, a);
     if (e != cudaSuccess) return e;
-    const int row_tiles = (int)(((long long)a.max_q * a.G + R - 1) / R);
-    const long long rows = (long long)a.n_seqs * a.kv.hkv * row_tiles * R;
-    if (rows > 0x7fffffffLL) return cudaErrorInvalidValue;
-    // a few rows are joined by many warps each: their partials are many
-    if (rows <= 4 * 152) return launch_pdl(kv_join_kernel<D, R, 32>, dim3((unsigned)rows), dim3(1024), 0, s, a, row_tiles, grid);
-    if (rows <= 16 * 152) return launch_pdl(kv_join_kernel<D, R, 8>, dim3((unsigned)rows), dim3(256), 0, s, a, row_tiles, grid);
-    return launch_pdl(kv_join_kernel<D, R, 1>, dim3((unsigned)(rows / 8)), dim3(256), 0, s, a, row_tiles, grid);
+    return launch_pdl(kv_join_kernel<D, 8 * NT>, dim3(grid), dim3(kThreads), 0, s, a);
 }
 
 template <int D, int kFormat>
@@ -766,6 +812,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+size_t kv_task_bytes() { return sizeof(JoinTask) * kWarps * kMaxShares; }
 size_t kv_parts_bytes(int D) { return (size_t)2 * kWarps * kMaxShares * kMaxRows * (D + 2) * sizeof(float); }
 
 cudaError_t launch_kv_attention(const AttnArgs& a, int D, int format, cudaStream_t s) {
