@@ -1,5 +1,6 @@
 // The quantised key/value cache: host side of the C ABI, the writing kernel (bf16 -> codes
 // and scales in their tiles) and the reading one (codes -> bf16).
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <new>
@@ -203,10 +204,24 @@ unsigned grid_of(long long threads) {
     return (unsigned)(need < most ? need : most);
 }
 
+// Once per kernel and device.
+template <auto kKernel>
+cudaError_t prepare() {
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices || done[dev].load(std::memory_order_relaxed)) return e;
+    e = all_shared(kKernel);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
 template <int D, int kFormat>
 struct Append {
     static cudaError_t run(const KvView& kv, const void* k, const void* v, size_t ks, size_t vs, const int32_t* slots,
                            int n, cudaStream_t s) {
+        const cudaError_t e = prepare<kv_append_kernel<D, kFormat>>();
+        if (e != cudaSuccess) return e;
         return launch_pdl(kv_append_kernel<D, kFormat>, dim3(grid_of(2LL * n * kv.hkv * (D / 16))), dim3(256), 0, s, kv,
                           static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), ks, vs, slots, n);
     }
@@ -215,6 +230,8 @@ struct Append {
 template <int D, int kFormat>
 struct Read {
     static cudaError_t run(const KvView& kv, const int32_t* slots, int n, void* k, void* v, cudaStream_t s) {
+        const cudaError_t e = prepare<kv_read_kernel<D, kFormat>>();
+        if (e != cudaSuccess) return e;
         return launch_pdl(kv_read_kernel<D, kFormat>, dim3(grid_of(2LL * n * kv.hkv * (D / 16))), dim3(256), 0, s, kv,
                           slots, n, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v));
     }

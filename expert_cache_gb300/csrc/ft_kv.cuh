@@ -65,6 +65,15 @@ cudaError_t launch_kv_attention(const AttnArgs& a, int D, int format, cudaStream
 
 #ifdef __CUDACC__
 
+// Every kernel of the cache asks for the SM's largest shared memory: a kernel that follows as a
+// programmatic dependent starts beside this one's last CTAs, on SMs still split as this one asked,
+// and with less shared memory only a part of the attention's CTAs would fit (measured: a third of
+// the grid started when the rest had finished, 84 us against 64 us for a batch of 32).
+template <typename F>
+inline cudaError_t all_shared(F* kern) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+}
+
 // Byte of the tile where a lane's code byte b stands (16-byte vectors, [vector][lane][16]).
 __device__ __forceinline__ int kv_lane_byte(int lane, int b) { return (b >> 4) * 512 + lane * 16 + (b & 15); }
 

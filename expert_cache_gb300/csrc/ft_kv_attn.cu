@@ -91,7 +91,7 @@ constexpr size_t rows_smem() {
 }
 
 // CTAs per SM that the register allocation aims at.
-constexpr int rows_ctas(int D, int NT) { return D == 256 ? (NT == 1 ? 3 : 2) : D == 128 ? (NT == 1 ? 4 : 3) : NT == 1 ? 4 : 3; }
+constexpr int rows_ctas(int D, int NT) { return D == 256 ? 2 : D == 128 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : 3; }
 
 }  // namespace
 
@@ -205,7 +205,7 @@ __device__ __forceinline__ Piece piece_of(const Shares& sh, long long first, int
     return p;
 }
 
-// Partial sums of one share of a unit in the workspace: [R] references, [R] sums, [R][D] values.
+// Partial sums of one piece of a unit in the workspace: [R] (reference, sum of weights), [R][D] values.
 template <int D, int R>
 __device__ __forceinline__ float* partial(const AttnArgs& a, int slot) { return a.parts + (size_t)slot * (R * (D + 2)); }
 
@@ -234,7 +234,10 @@ __device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u,
     sync();
     for (int w = 0; w < kWarps; ++w)
         if (slots[w] == -2 || slots[n - 1 - w] == -2) return;                // not cut: written already
+    // a slice is at least 128 contiguous bytes of every piece
     const int rows = min(R, u.n * a.G - u.r * R), groups = rows * (D / 4);
+    parts = min(parts, groups / 8);
+    if (part >= parts) return;
     const int ga = (int)((long long)groups * part / parts), gb = (int)((long long)groups * (part + 1) / parts);
     int team = 1;
     while (team < 32 && team < n && (gb - ga) * team < n_threads) team *= 2;
@@ -243,17 +246,37 @@ __device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u,
         const int row = e / (D / 4), d = e % (D / 4) * 4;
         float m = kNoRef, l = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = thread & (team - 1); k < n; k += team) {
-            const int slot = slots[k];
-            if (slot < 0) continue;
-            const float* src = partial<D, R>(a, slot);
-            const float pm = __ldcg(src + row), pl = __ldcg(src + R + row);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(src + 2 * R + row * D + d));
-            const float mm = fmaxf(m, pm), f = ex2(m - mm), pf = ex2(pm - mm);
+        constexpr int kBatch = 8;                         // pieces in flight
+        for (int k0 = thread & (team - 1); k0 < n; k0 += team * kBatch) {
+            float pm[kBatch], pl[kBatch];
+            float4 y[kBatch];
+            float mm = m;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int k = k0 + b * team, slot = k < n ? slots[k] : -1;
+                pm[b] = kNoRef;
+                pl[b] = 0.f;
+                y[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (slot >= 0) {
+                    const float* src = partial<D, R>(a, slot);
+                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(src) + row);
+                    pm[b] = ml.x;
+                    pl[b] = ml.y;
+                    y[b] = __ldcg(reinterpret_cast<const float4*>(src + 2 * R + row * D + d));
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) mm = fmaxf(mm, pm[b]);
+            float f = ex2(m - mm);
             m = mm;
-            l = l * f + pl * pf;
-            x.x = x.x * f + y.x * pf; x.y = x.y * f + y.y * pf; x.z = x.z * f + y.z * pf; x.w = x.w * f + y.w * pf;
+            l *= f;
+            x.x *= f; x.y *= f; x.z *= f; x.w *= f;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                f = ex2(pm[b] - mm);
+                l += pl[b] * f;
+                x.x += y[b].x * f; x.y += y[b].y * f; x.z += y[b].z * f; x.w += y[b].w * f;
+            }
         }
         for (int o = 1; o < team; o <<= 1) {
             const float om = __shfl_xor_sync(0xffffffffu, m, o), mm = fmaxf(m, om), f = ex2(m - mm), of = ex2(om - mm);
@@ -383,8 +406,6 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
             const int st = next;
             if (issue(v)) present |= 1u << st;
         }
-        if (pos == w0) note_task(u);
-
         // ---------------------------------------------------------------- the rows
         RowRule rule[NT][2];
         uint32_t qf[NT][D / 16][2];
@@ -440,6 +461,8 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
+
+        if (pos == w0) note_task(u);                      // while the first tiles are under way
 
         // ---------------------------------------------------------------- the keys
         for (int v = v0; v < vend; ++v) {
@@ -715,10 +738,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                     store_out<4>(a, (size_t)(u.si.q0 + i), h, D, d, &x.x, mm, ll);
                 } else {
                     *reinterpret_cast<float4*>(out + 2 * R + row * D + d) = x;
-                    if (d == 0) {
-                        out[row] = mm;
-                        out[R + row] = ll;
-                    }
+                    if (d == 0) reinterpret_cast<float2*>(out)[row] = make_float2(mm, ll);
                 }
             }
             break;
@@ -745,10 +765,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                     for (int x = 0; x < D / 32; ++x)
                         *reinterpret_cast<float4*>(out + 2 * R + row * D + g * (D / 8) + 4 * x) =
                             make_float4(acc[2 * x][nt][b], acc[2 * x][nt][2 + b], acc[2 * x + 1][nt][b], acc[2 * x + 1][nt][2 + b]);
-                    if (g == 0) {
-                        out[row] = m[nt][b];
-                        out[R + row] = l[nt][b];
-                    }
+                    if (g == 0) reinterpret_cast<float2*>(out)[row] = make_float2(m[nt][b], l[nt][b]);
                 }
             }
     }
@@ -786,6 +803,7 @@ int rows_grid() {
         constexpr size_t smem = rows_smem<D, kFormat, NT>();
         int n = 0;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+            all_shared(kern) != cudaSuccess || all_shared(kv_join_kernel<D, 8 * NT>) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem) != cudaSuccess) {
             cudaGetLastError();
             return 0;
