@@ -62,6 +62,7 @@ cudaError_t launch_kv_append(const KvView& kv, int D, int format, const void* k,
 cudaError_t launch_kv_read(const KvView& kv, int D, int format, const int32_t* slots, int n, void* k_out, void* v_out,
                            cudaStream_t s);
 cudaError_t launch_kv_attention(const AttnArgs& a, int D, int format, cudaStream_t s);
+cudaError_t launch_kv_tiles(const AttnArgs& a, int D, int format, cudaStream_t s);    // many rows per key
 
 #ifdef __CUDACC__
 

@@ -31,10 +31,10 @@ namespace ft {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kMinTiles = 2;           // tiles of a warp at least, unless there are fewer
-constexpr int kUnitCost = 8;           // a unit's start and end, in tiles
-constexpr int kMaxPerSm = 4, kMaxShares = 640;     // CTAs
-constexpr int kMaxRows = 16;           // rows of a unit
+constexpr int kMaxPerSm = 4;           // CTAs
+// at least 2 places of the line per warp; a unit's start and end cost about 8 tiles
+template <int NT>
+using RowsLine = Line<kKvTile, 8 * NT, kWarps, 2 * kWarps, 8>;
 constexpr long kWaitLimit = 1L << 24;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -95,207 +95,9 @@ constexpr int rows_ctas(int D, int NT) { return D == 256 ? 2 : D == 128 ? (NT ==
 
 }  // namespace
 
-// The sequences' first places in the line of all units: prefix[0..n_seqs], in shared memory.
-template <int kB>
-__device__ __forceinline__ void tile_prefix(const AttnArgs& a, int R, long long* prefix, long long* scratch) {
-    const int per = (a.n_seqs + blockDim.x - 1) / blockDim.x;
-    const int s0 = min((int)threadIdx.x * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
-    long long sum = 0;
-    for (int s = s0; s < s1; ++s) {
-        const SeqInfo si = seq_info(a, s);
-        if (si.bad && blockIdx.x == 0) atomicOr(a.kv.status, FT_DEV_BAD_ID);
-        long long t = 0;
-        const int rt = (si.n * a.G + R - 1) / R;
-        for (int r = 0; r < rt; ++r) t += kUnitCost + row_tile<kB>(a, si, r, R).nt;
-        prefix[s + 1] = t * a.kv.hkv;
-        sum += t * a.kv.hkv;
-    }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
-    }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    long long at = incl - sum;
-    for (int w = 0; w < warp; ++w) at += scratch[w];
-    if (threadIdx.x == 0) prefix[0] = 0;
-    for (int s = s0; s < s1; ++s) {
-        at += prefix[s + 1];
-        prefix[s + 1] = at;
-    }
-    __syncthreads();
-}
-
-// The shares of the CTAs: cut(c) = first place of CTA c; they differ by one at most.
-struct Shares {
-    int nc;
-    long long q, rem;
-    __device__ __forceinline__ Shares(int nc_, long long q_, long long rem_) : nc(nc_), q(q_), rem(rem_) {}
-    __device__ __forceinline__ Shares(long long total, int grid) {
-        const long long want = (total + kWarps * kMinTiles - 1) / (kWarps * kMinTiles);
-        nc = (int)min((long long)grid, max(want, 1LL));
-        q = total / nc;
-        rem = total - q * nc;
-    }
-    __device__ __forceinline__ long long cut(int c) const { return q * c + min((long long)c, rem); }
-    __device__ __forceinline__ int holder(long long place) const {
-        const long long wide = rem * (q + 1);
-        return (int)(place < wide ? place / (q + 1) : rem + (place - wide) / q);
-    }
-};
-
-struct Unit {
-    int s, r, h;
-    long long first, end;    // its places in the line
-    SeqInfo si;
-    RowTile rt;
-    __device__ __forceinline__ int tile_at(long long place) const;
-};
-
-// Tile of a unit that stands at a place (0 before its first tile, nt from its end on).
-__device__ __forceinline__ int tile_at(long long first, int nt, long long place) {
-    return (int)min(max(place - first - kUnitCost, 0LL), (long long)nt);
-}
-__device__ __forceinline__ int Unit::tile_at(long long place) const { return ft::tile_at(first, rt.nt, place); }
-
-__device__ __forceinline__ Unit find_unit(const AttnArgs& a, const long long* prefix, long long place, int R) {
-    Unit u;
-    int lo = 0, hi = a.n_seqs;
-    while (hi - lo > 1) {              // largest s with prefix[s] <= place
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= place) lo = mid; else hi = mid;
-    }
-    u.s = lo;
-    u.si = seq_info(a, lo);
-    u.first = prefix[lo];
-    long long len;
-    for (u.r = 0;; ++u.r) {
-        u.rt = row_tile<kKvTile>(a, u.si, u.r, R);
-        len = kUnitCost + u.rt.nt;
-        if (place < u.first + len * a.kv.hkv) break;
-        u.first += len * a.kv.hkv;
-    }
-    u.h = (int)((place - u.first) / len);
-    u.first += u.h * len;
-    u.end = u.first + len;
-    return u;
-}
-
-// The pieces of a unit: one per CTA whose share lies in the unit, one per warp elsewhere.
-struct Piece {
-    int v0, v1, slot;        // tiles [v0, v1), where its partial sums stand
-};
-__device__ __forceinline__ Piece piece_of(const Shares& sh, long long first, int nt, int c, int w) {
-    const long long c0 = sh.cut(c), c1 = sh.cut(c + 1);
-    Piece p{0, 0, 0};
-    if (c0 >= first && c1 <= first + kUnitCost + nt) {
-        if (w == 0) {
-            p.v0 = tile_at(first, nt, c0);
-            p.v1 = tile_at(first, nt, c1);
-        }
-    } else {
-        p.v0 = tile_at(first, nt, c0 + (c1 - c0) * w / kWarps);
-        p.v1 = tile_at(first, nt, c0 + (c1 - c0) * (w + 1) / kWarps);
-    }
-    // a share holds at most one unit's later piece and one unit's first
-    p.slot = 2 * (kWarps * c + w) + (p.v0 > 0 ? 0 : 1);
-    return p;
-}
-
-// Partial sums of one piece of a unit in the workspace: [R] (reference, sum of weights), [R][D] values.
-template <int D, int R>
-__device__ __forceinline__ float* partial(const AttnArgs& a, int slot) { return a.parts + (size_t)slot * (R * (D + 2)); }
-
-// What the second kernel needs to know of a unit that is cut (a: its first and last CTA).
-struct __align__(16) JoinTask {
-    long long q, rem, first;
-    int nc, nt, q0, n, r, h, ca, cb, on;
-};
-
-// Slice `part` of `parts` of unit u's output from its pieces, by n_threads threads (a multiple of
-// 32, whole warps, `sync` between them).  A team of lanes takes four values of a row: lane k of it
-// the pieces k, k + team, ..., then a butterfly, so the order of the sums is fixed.  Teams are as
-// large as the slice leaves threads for.  slots: shared, 2 kWarps + CTAs of the unit.
-template <int D, int R, typename Sync>
-__device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u, int part, int parts, int thread,
-                                           int n_threads, int* slots, Sync sync) {
-    const Shares sh(u.nc, u.q, u.rem);
-    const int ca = u.ca, cb = u.cb;
-    // pieces: the warps of the first CTA, one each of the CTAs between, the warps of the last
-    const int n = cb == ca ? kWarps : 2 * kWarps + cb - ca - 1;
-    for (int k = thread; k < n; k += n_threads) {
-        const int mid = k - kWarps, c = mid < 0 ? ca : min(ca + 1 + mid, cb);
-        const Piece p = piece_of(sh, u.first, u.nt, c, mid < 0 ? k : max(mid - (cb - ca - 1), 0));
-        slots[k] = p.v0 == p.v1 ? -1 : p.v1 - p.v0 == u.nt ? -2 : p.slot;
-    }
-    sync();
-    for (int w = 0; w < kWarps; ++w)
-        if (slots[w] == -2 || slots[n - 1 - w] == -2) return;                // not cut: written already
-    // a slice is at least 128 contiguous bytes of every piece
-    const int rows = min(R, u.n * a.G - u.r * R), groups = rows * (D / 4);
-    parts = min(parts, groups / 8);
-    if (part >= parts) return;
-    const int ga = (int)((long long)groups * part / parts), gb = (int)((long long)groups * (part + 1) / parts);
-    int team = 1;
-    while (team < 32 && team < n && (gb - ga) * team < n_threads) team *= 2;
-    for (int g0 = ga; g0 < gb; g0 += n_threads / team) {
-        const int e = min(g0 + thread / team, gb - 1);
-        const int row = e / (D / 4), d = e % (D / 4) * 4;
-        float m = kNoRef, l = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kBatch = 8;                         // pieces in flight
-        for (int k0 = thread & (team - 1); k0 < n; k0 += team * kBatch) {
-            float pm[kBatch], pl[kBatch];
-            float4 y[kBatch];
-            float mm = m;
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                const int k = k0 + b * team, slot = k < n ? slots[k] : -1;
-                pm[b] = kNoRef;
-                pl[b] = 0.f;
-                y[b] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (slot >= 0) {
-                    const float* src = partial<D, R>(a, slot);
-                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(src) + row);
-                    pm[b] = ml.x;
-                    pl[b] = ml.y;
-                    y[b] = __ldcg(reinterpret_cast<const float4*>(src + 2 * R + row * D + d));
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) mm = fmaxf(mm, pm[b]);
-            float f = ex2(m - mm);
-            m = mm;
-            l *= f;
-            x.x *= f; x.y *= f; x.z *= f; x.w *= f;
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                f = ex2(pm[b] - mm);
-                l += pl[b] * f;
-                x.x += y[b].x * f; x.y += y[b].y * f; x.z += y[b].z * f; x.w += y[b].w * f;
-            }
-        }
-        for (int o = 1; o < team; o <<= 1) {
-            const float om = __shfl_xor_sync(0xffffffffu, m, o), mm = fmaxf(m, om), f = ex2(m - mm), of = ex2(om - mm);
-            const float ol = __shfl_xor_sync(0xffffffffu, l, o);
-            const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o),
-                                         __shfl_xor_sync(0xffffffffu, x.z, o), __shfl_xor_sync(0xffffffffu, x.w, o));
-            m = mm;
-            l = l * f + ol * of;
-            x.x = x.x * f + y.x * of; x.y = x.y * f + y.y * of; x.z = x.z * f + y.z * of; x.w = x.w * f + y.w * of;
-        }
-        if (g0 + thread / team < gb && (thread & (team - 1)) == 0) {
-            const int grow = u.r * R + row;
-            store_out<4>(a, (size_t)(u.q0 + grow / a.G), u.h * a.G + grow % a.G, D, d, &x.x, m, l);
-        }
-    }
-}
-
 template <int D, int kFormat, int NT>
 __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(const AttnArgs a) {
+    using L = RowsLine<NT>;
     constexpr int R = 8 * NT, kStages = stages(D, kFormat);
     constexpr KvTile kT = kv_tile(D, kFormat);
     constexpr bool kFour = kFormat == FT_KV_NVFP4;
@@ -313,9 +115,9 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
     }
     __syncwarp();
     pdl_wait_and_release();
-    tile_prefix<kKvTile>(a, R, prefix, scratch);
+    line_prefix<L>(a, prefix, scratch);
     const long long total = prefix[a.n_seqs];
-    const Shares shares(total, gridDim.x);
+    const Shares shares(total, gridDim.x, L::kMin);
     const int cta = blockIdx.x;
     JoinTask* task = a.tasks + kWarps * cta + warp;
     if (total == 0 || cta >= shares.nc) {
@@ -323,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
         return;
     }
     const long long c0 = shares.cut(cta), c1 = shares.cut(cta + 1);
-    Unit u = find_unit(a, prefix, c0, R);
+    Unit u = find_unit<L>(a, prefix, c0);
     const bool whole = c1 <= u.end;                       // the CTA's share lies in one unit: its warps split the tiles
     const long long w0 = c0 + (c1 - c0) * warp / kWarps, w1 = c0 + (c1 - c0) * (warp + 1) / kWarps;
     uint8_t* ring = smem + (size_t)warp * kStages * kT.bytes;
@@ -335,23 +137,15 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
     // warp's is the first through a unit that begins and ends in the CTA's.
     auto note_task = [&](const Unit& v) {
         if (lane != 0) return;
-        JoinTask j;
-        j.on = warp == 0 ? v.first < c0 : !whole && v.first < w0 && v.first >= c0 + (c1 - c0) * (warp - 1) / kWarps && v.end <= c1;
-        if (j.on) {
-            j.q = shares.q; j.rem = shares.rem; j.nc = shares.nc;
-            j.first = v.first; j.nt = v.rt.nt;
-            j.q0 = v.si.q0; j.n = v.si.n; j.r = v.r; j.h = v.h;
-            j.ca = warp == 0 ? shares.holder(v.first) : cta;
-            j.cb = warp == 0 ? shares.holder(v.end - 1) : cta;
-            *task = j;
-        } else {
+        if (warp == 0 ? v.first < c0 : !whole && v.first < w0 && v.first >= c0 + (c1 - c0) * (warp - 1) / kWarps && v.end <= c1)
+            *task = join_task(shares, v, warp == 0 ? shares.holder(v.first) : cta, warp == 0 ? shares.holder(v.end - 1) : cta);
+        else
             task->on = 0;
-        }
     };
 
     for (long long pos = w0; pos < w1 || whole; pos = u.end) {
-        if (!whole && (pos >= u.end || pos < u.first)) u = find_unit(a, prefix, pos, R);
-        int v0 = u.tile_at(whole ? c0 : pos), v1 = u.tile_at(whole ? c1 : w1);
+        if (!whole && (pos >= u.end || pos < u.first)) u = find_unit<L>(a, prefix, pos);
+        int v0 = block_at<L>(u.first, u.rt.nt, whole ? c0 : pos), v1 = block_at<L>(u.first, u.rt.nt, whole ? c1 : w1);
         const int cv0 = v0, cv1 = v1;
         if (whole) {
             v0 = cv0 + (cv1 - cv0) * warp / kWarps;
@@ -428,14 +222,12 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                 amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[e] << 16)), fabsf(__uint_as_float(raw[e] & 0xFFFF0000u))));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // the row's largest magnitude goes to [2^13, 2^14): exact in f16 down to 2^-27 of it
-            const int ex = amax > 0.f && amax < INFINITY ? max((int)(__float_as_uint(amax) >> 23) - 140, -126) : 0;
-            const float down = __uint_as_float((uint32_t)(127 - ex) << 23), up = __uint_as_float((uint32_t)(127 + ex) << 23);
+            const RowScale rs = row_scale(amax);
 #pragma unroll
             for (int e = 0; e < D / 8; ++e)
-                qf[nt][e >> 1][e & 1] = pack_f16(__uint_as_float(raw[e] << 16) * down,
-                                                 __uint_as_float(raw[e] & 0xFFFF0000u) * down);
-            const float c = a.scale * a.kv.k_scale * 1.44269504088896340736f * up;
+                qf[nt][e >> 1][e & 1] = pack_f16(__uint_as_float(raw[e] << 16) * rs.down,
+                                                 __uint_as_float(raw[e] & 0xFFFF0000u) * rs.down);
+            const float c = a.scale * a.kv.k_scale * 1.44269504088896340736f * rs.up;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 coef[nt][b] = __shfl_sync(0xffffffffu, c, 4 * (2 * t + b));
@@ -542,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[nt][e] *= coef[nt][e & 1];
+                for (int e = 0; e < 4; ++e) sc[nt][e] = __fmul_rn(sc[nt][e], coef[nt][e & 1]);   // not fused: t - m stays exact near m
             if (edge) {
 #pragma unroll
                 for (int e2 = 0; e2 < 2; ++e2) {
@@ -772,20 +564,6 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
 
 }
 
-// The second kernel: CTA c joins a slice of the unit that holds the first place of its share and
-// began before it (the CTAs behind the one that the unit began in take a slice each), and each warp
-// the unit that began and ends in the CTA's share and that the warp's place is the first cut in.
-template <int D, int R>
-__global__ void __launch_bounds__(kThreads) kv_join_kernel(const AttnArgs a) {
-    __shared__ int slots[2 * kWarps + kMaxShares], warp_slots[kWarps][kWarps];
-    pdl_wait_and_release();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const JoinTask all = a.tasks[kWarps * blockIdx.x], mine = a.tasks[kWarps * blockIdx.x + warp];
-    if (all.on)
-        join_slice<D, R>(a, all, blockIdx.x - all.ca - 1, all.cb - all.ca, threadIdx.x, kThreads, slots, [] { __syncthreads(); });
-    if (warp > 0 && mine.on) join_slice<D, R>(a, mine, 0, 1, lane, 32, warp_slots[warp], [] { __syncwarp(); });
-}
-
 namespace {
 
 // CTAs of the rows kernel (looked up once per device): every one resident at once.
@@ -803,7 +581,7 @@ int rows_grid() {
         constexpr size_t smem = rows_smem<D, kFormat, NT>();
         int n = 0;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-            all_shared(kern) != cudaSuccess || all_shared(kv_join_kernel<D, 8 * NT>) != cudaSuccess ||
+            all_shared(kern) != cudaSuccess || all_shared(kv_join_kernel<RowsLine<NT>, D>) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem) != cudaSuccess) {
             cudaGetLastError();
             return 0;
@@ -820,18 +598,20 @@ cudaError_t run_rows(const AttnArgs& a, cudaStream_t s) {
     if (grid < 1) return cudaErrorInvalidConfiguration;
     const cudaError_t e = launch_pdl(kv_rows_kernel<D, kFormat, NT>, dim3(grid), dim3(kThreads), rows_smem<D, kFormat, NT>(), s, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv_join_kernel<D, 8 * NT>, dim3(grid), dim3(kThreads), 0, s, a);
+    return launch_pdl(kv_join_kernel<RowsLine<NT>, D>, dim3(grid), dim3(kJoinThreads), 0, s, a);
 }
 
 template <int D, int kFormat>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
-    return (long long)a.max_q * a.G <= 8 ? run_rows<D, kFormat, 1>(a, s) : run_rows<D, kFormat, 2>(a, s);
+    const long long rows = (long long)a.max_q * a.G;
+    if (rows > 16) return launch_kv_tiles(a, D, kFormat, s);
+    return rows <= 8 ? run_rows<D, kFormat, 1>(a, s) : run_rows<D, kFormat, 2>(a, s);
 }
 
 }  // namespace
 
 size_t kv_task_bytes() { return sizeof(JoinTask) * kWarps * kMaxShares; }
-size_t kv_parts_bytes(int D) { return (size_t)2 * kWarps * kMaxShares * kMaxRows * (D + 2) * sizeof(float); }
+size_t kv_parts_bytes(int D) { return (size_t)2 * kWarps * kMaxShares * 16 * (D + 2) * sizeof(float); }
 
 cudaError_t launch_kv_attention(const AttnArgs& a, int D, int format, cudaStream_t s) {
     if (format == FT_KV_NVFP4)

@@ -85,7 +85,17 @@ __device__ __forceinline__ bool sees_drafted(const AttnArgs& a, const RowRule& r
     return (r.mask >> (j - base) & 1) && (pos >= r.low || j < a.n_sink);
 }
 
-// N (2 or 4) output values, dims d.., of one row and query head from their weighted sums x, the
+// Powers of two that take a row's largest magnitude to [2^13, 2^14) and back: exact in f16 down to
+// 2^-27 of the largest.  A row of zeros, or with an infinity, stays as it is.
+struct RowScale {
+    float down, up;
+};
+__device__ __forceinline__ RowScale row_scale(float amax) {
+    const int ex = amax > 0.f && amax < INFINITY ? max((int)(__float_as_uint(amax) >> 23) - 140, -126) : 0;
+    return {__uint_as_float((uint32_t)(127 - ex) << 23), __uint_as_float((uint32_t)(127 + ex) << 23)};
+}
+
+// N (4 or 8) output values, dims d.., of one row and query head from their weighted sums x, the
 // reference m and the sum of weights l; a row without keys (l = 0) gives 0 and -inf.
 template <int N>
 __device__ __forceinline__ void store_out(const AttnArgs& a, size_t token, int h, int D, int d, const float* x, float m, float l) {
@@ -97,10 +107,292 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, size_t token, int h
         w[e] = *reinterpret_cast<const uint32_t*>(&p);
     }
     __nv_bfloat16* dst = a.o + token * a.o_stride + (size_t)h * D + d;
-    if constexpr (N == 2) *reinterpret_cast<uint32_t*>(dst) = w[0];
-    else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    if constexpr (N == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     if (d == 0 && a.lse)
         a.lse[token * a.hq + h] = l == 0.f ? -INFINITY : (m - kHeadroom + log2f(l)) * 0.693147180559945309417f;
+}
+
+// ---------------------------------------------------------------------------- the line of units
+// A unit is a row tile of a sequence and a kv head; its work comes in blocks of kB keys.  Units are
+// laid end to end, a unit being kCost + nt places long (its own start and end cost about as much as
+// kCost blocks), and every CTA takes an equal share of the places.  Within a CTA the kW workers
+// split the share: its tiles of the unit where the whole share lies in one unit (the workers then
+// join in the CTA), its places otherwise.
+template <int kB_, int kR_, int kW_, int kMin_, int kCost_>
+struct Line {
+    static constexpr int kB = kB_, kR = kR_, kW = kW_, kMin = kMin_, kCost = kCost_;
+};
+
+constexpr int kMaxShares = 640;        // CTAs of a launch
+constexpr int kJoinThreads = 128;
+
+// The sequences' first places: prefix[0..n_seqs], in shared memory.  Called by the whole CTA.
+template <typename L>
+__device__ __forceinline__ void line_prefix(const AttnArgs& a, long long* prefix, long long* scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if ((long long)a.max_q * a.G > 8 * L::kR) {           // many row tiles: a warp per sequence
+        for (int s = warp; s < a.n_seqs; s += blockDim.x >> 5) {
+            const SeqInfo si = seq_info(a, s);
+            if (lane == 0 && si.bad && blockIdx.x == 0) atomicOr(a.kv.status, FT_DEV_BAD_ID);
+            const int rt = (int)(((long long)si.n * a.G + L::kR - 1) / L::kR);
+            long long t = 0;
+            for (int r = lane; r < rt; r += 32) t += L::kCost + row_tile<L::kB>(a, si, r, L::kR).nt;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+            if (lane == 0) prefix[s + 1] = t * a.kv.hkv;
+        }
+    } else {
+        for (int s = threadIdx.x; s < a.n_seqs; s += blockDim.x) {
+            const SeqInfo si = seq_info(a, s);
+            if (si.bad && blockIdx.x == 0) atomicOr(a.kv.status, FT_DEV_BAD_ID);
+            const int rt = (si.n * a.G + L::kR - 1) / L::kR;
+            long long t = 0;
+            for (int r = 0; r < rt; ++r) t += L::kCost + row_tile<L::kB>(a, si, r, L::kR).nt;
+            prefix[s + 1] = t * a.kv.hkv;
+        }
+    }
+    __syncthreads();
+    const int per = (a.n_seqs + blockDim.x - 1) / blockDim.x;
+    const int s0 = min((int)threadIdx.x * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
+    long long sum = 0;
+    for (int s = s0; s < s1; ++s) sum += prefix[s + 1];
+    long long incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += t;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long at = incl - sum;
+    for (int w = 0; w < warp; ++w) at += scratch[w];
+    if (threadIdx.x == 0) prefix[0] = 0;
+    for (int s = s0; s < s1; ++s) {
+        at += prefix[s + 1];
+        prefix[s + 1] = at;
+    }
+    __syncthreads();
+}
+
+// The shares of the CTAs: cut(c) = first place of CTA c; they differ by one at most.
+struct Shares {
+    int nc;
+    long long q, rem;
+    __device__ __forceinline__ Shares(int nc_, long long q_, long long rem_) : nc(nc_), q(q_), rem(rem_) {}
+    __device__ __forceinline__ Shares(long long total, int grid, int least) {
+        nc = (int)min((long long)grid, max((total + least - 1) / least, 1LL));
+        q = total / nc;
+        rem = total - q * nc;
+    }
+    __device__ __forceinline__ long long cut(int c) const { return q * c + min((long long)c, rem); }
+    __device__ __forceinline__ int holder(long long place) const {
+        const long long wide = rem * (q + 1);
+        return (int)(place < wide ? place / (q + 1) : rem + (place - wide) / q);
+    }
+};
+
+// Block of a unit that stands at a place (0 before its first block, nt from its end on).
+template <typename L>
+__device__ __forceinline__ int block_at(long long first, int nt, long long place) {
+    return (int)min(max(place - first - L::kCost, 0LL), (long long)nt);
+}
+
+struct Unit {
+    int s, r, h;
+    long long first, end;    // its places in the line
+    SeqInfo si;
+    RowTile rt;
+};
+
+// The unit that holds a place.  Called by whole warps.
+template <typename L>
+__device__ __forceinline__ Unit find_unit(const AttnArgs& a, const long long* prefix, long long place) {
+    Unit u;
+    int lo = 0, hi = a.n_seqs;
+    while (hi - lo > 1) {              // largest s with prefix[s] <= place
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= place) lo = mid; else hi = mid;
+    }
+    u.s = lo;
+    u.si = seq_info(a, lo);
+    u.first = prefix[lo];
+    u.r = 0;
+    if (u.si.n * (long long)a.G > 4 * L::kR) {            // many row tiles: 32 at a time, one per lane
+        const int lane = threadIdx.x & 31;
+        for (;; u.r += 32) {
+            const int r = u.r + lane;
+            const bool on = (long long)r * L::kR < (long long)u.si.n * a.G;
+            const long long mine = on ? (long long)(L::kCost + row_tile<L::kB>(a, u.si, r, L::kR).nt) * a.kv.hkv : 0;
+            long long incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += t;
+            }
+            const unsigned past = __ballot_sync(0xffffffffu, u.first + incl > place);
+            const int pick = past ? __ffs(past) - 1 : 31;
+            const long long before = __shfl_sync(0xffffffffu, past ? incl - mine : incl, pick);
+            if (!past && (long long)(u.r + 32) * L::kR >= (long long)u.si.n * a.G) break;   // lengths changed under the call
+            u.first += before;
+            if (past) {
+                u.r += pick;
+                break;
+            }
+        }
+        u.rt = row_tile<L::kB>(a, u.si, u.r, L::kR);
+    } else {
+        for (;; ++u.r) {
+            u.rt = row_tile<L::kB>(a, u.si, u.r, L::kR);
+            const long long all = (long long)(L::kCost + u.rt.nt) * a.kv.hkv;
+            if (place < u.first + all || (u.r + 1) * L::kR >= u.si.n * a.G) break;
+            u.first += all;
+        }
+    }
+    const long long len = L::kCost + u.rt.nt;
+    u.h = (int)min((place - u.first) / len, (long long)a.kv.hkv - 1);
+    u.first += u.h * len;
+    u.end = u.first + len;
+    return u;
+}
+
+// The pieces of a unit: one per CTA whose share lies in the unit, one per worker elsewhere.
+struct Piece {
+    int v0, v1, slot;        // blocks [v0, v1), where its partial sums stand
+};
+template <typename L>
+__device__ __forceinline__ Piece piece_of(const Shares& sh, long long first, int nt, int c, int w) {
+    const long long c0 = sh.cut(c), c1 = sh.cut(c + 1);
+    Piece p{0, 0, 0};
+    if (c0 >= first && c1 <= first + L::kCost + nt) {
+        if (w == 0) {
+            p.v0 = block_at<L>(first, nt, c0);
+            p.v1 = block_at<L>(first, nt, c1);
+        }
+    } else {
+        p.v0 = block_at<L>(first, nt, c0 + (c1 - c0) * w / L::kW);
+        p.v1 = block_at<L>(first, nt, c0 + (c1 - c0) * (w + 1) / L::kW);
+    }
+    // a share holds at most one unit's later piece and one unit's first
+    p.slot = 2 * (L::kW * c + w) + (p.v0 > 0 ? 0 : 1);
+    return p;
+}
+
+// Partial sums of one piece of a unit in the workspace: [R] (reference, sum of weights), [R][D] values.
+template <int D, int R>
+__device__ __forceinline__ float* partial(const AttnArgs& a, int slot) { return a.parts + (size_t)slot * (R * (D + 2)); }
+
+// What the second kernel needs to know of a unit that is cut (ca, cb: its first and last CTA).
+struct __align__(16) JoinTask {
+    long long q, rem, first;
+    int nc, nt, q0, n, r, h, ca, cb, on;
+};
+
+__device__ __forceinline__ JoinTask join_task(const Shares& sh, const Unit& u, int ca, int cb) {
+    JoinTask j;
+    j.q = sh.q; j.rem = sh.rem; j.nc = sh.nc;
+    j.first = u.first; j.nt = u.rt.nt;
+    j.q0 = u.si.q0; j.n = u.si.n; j.r = u.r; j.h = u.h;
+    j.ca = ca; j.cb = cb; j.on = 1;
+    return j;
+}
+
+// Slice `part` of `parts` of unit u's output from its pieces, by n_threads threads (a multiple of
+// 32, whole warps, `sync` between them).  A team of lanes takes four values of a row: lane k of it
+// the pieces k, k + team, ..., then a butterfly, so the order of the sums is fixed.  Teams are as
+// large as the slice leaves threads for.  slots: shared, 2 kW + CTAs of the unit.
+template <typename L, int D, typename Sync>
+__device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u, int part, int parts, int thread,
+                                           int n_threads, int* slots, Sync sync) {
+    constexpr int R = L::kR;
+    const Shares sh(u.nc, u.q, u.rem);
+    const int ca = u.ca, cb = u.cb;
+    // pieces: the workers of the first CTA, one each of the CTAs between, the workers of the last
+    const int n = cb == ca ? L::kW : 2 * L::kW + cb - ca - 1;
+    for (int k = thread; k < n; k += n_threads) {
+        const int mid = k - L::kW, c = mid < 0 ? ca : min(ca + 1 + mid, cb);
+        const Piece p = piece_of<L>(sh, u.first, u.nt, c, mid < 0 ? k : max(mid - (cb - ca - 1), 0));
+        slots[k] = p.v0 == p.v1 ? -1 : p.v1 - p.v0 == u.nt ? -2 : p.slot;
+    }
+    sync();
+    for (int w = 0; w < L::kW; ++w)
+        if (slots[w] == -2 || slots[n - 1 - w] == -2) return;                // not cut: written already
+    // a slice is at least 128 contiguous bytes of every piece
+    const int rows = min(R, u.n * a.G - u.r * R), groups = rows * (D / 4);
+    parts = min(parts, groups / 8);
+    if (part >= parts) return;
+    const int ga = (int)((long long)groups * part / parts), gb = (int)((long long)groups * (part + 1) / parts);
+    int team = 1;
+    while (team < 32 && team < n && (gb - ga) * team < n_threads) team *= 2;
+    for (int g0 = ga; g0 < gb; g0 += n_threads / team) {
+        const int e = min(g0 + thread / team, gb - 1);
+        const int row = e / (D / 4), d = e % (D / 4) * 4;
+        float m = kNoRef, l = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kBatch = 8;                         // pieces in flight
+        for (int k0 = thread & (team - 1); k0 < n; k0 += team * kBatch) {
+            float pm[kBatch], pl[kBatch];
+            float4 y[kBatch];
+            float mm = m;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int k = k0 + b * team, slot = k < n ? slots[k] : -1;
+                pm[b] = kNoRef;
+                pl[b] = 0.f;
+                y[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (slot >= 0) {
+                    const float* src = partial<D, R>(a, slot);
+                    const float2 ml = __ldcg(reinterpret_cast<const float2*>(src) + row);
+                    pm[b] = ml.x;
+                    pl[b] = ml.y;
+                    y[b] = __ldcg(reinterpret_cast<const float4*>(src + 2 * R + row * D + d));
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) mm = fmaxf(mm, pm[b]);
+            float f = ex2(m - mm);
+            m = mm;
+            l *= f;
+            x.x *= f; x.y *= f; x.z *= f; x.w *= f;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                f = ex2(pm[b] - mm);
+                l += pl[b] * f;
+                x.x += y[b].x * f; x.y += y[b].y * f; x.z += y[b].z * f; x.w += y[b].w * f;
+            }
+        }
+        for (int o = 1; o < team; o <<= 1) {
+            const float om = __shfl_xor_sync(0xffffffffu, m, o), mm = fmaxf(m, om), f = ex2(m - mm), of = ex2(om - mm);
+            const float ol = __shfl_xor_sync(0xffffffffu, l, o);
+            const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o),
+                                         __shfl_xor_sync(0xffffffffu, x.z, o), __shfl_xor_sync(0xffffffffu, x.w, o));
+            m = mm;
+            l = l * f + ol * of;
+            x.x = x.x * f + y.x * of; x.y = x.y * f + y.y * of; x.z = x.z * f + y.z * of; x.w = x.w * f + y.w * of;
+        }
+        if (g0 + thread / team < gb && (thread & (team - 1)) == 0) {
+            const int grow = u.r * R + row;
+            store_out<4>(a, (size_t)(u.q0 + grow / a.G), u.h * a.G + grow % a.G, D, d, &x.x, m, l);
+        }
+    }
+}
+
+// The second kernel: CTA c joins a slice of the unit that holds the first place of its share and
+// began before it (the CTAs behind the one that the unit began in take a slice each), and each warp
+// the unit that began and ends in the CTA's share and that its worker's place is the first cut in.
+template <typename L, int D>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttnArgs a) {
+    __shared__ int slots[2 * L::kW + kMaxShares], warp_slots[L::kW][L::kW];
+    pdl_wait_and_release();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const JoinTask all = a.tasks[L::kW * blockIdx.x];
+    JoinTask mine;
+    mine.on = 0;
+    if (warp > 0 && warp < L::kW) mine = a.tasks[L::kW * blockIdx.x + warp];
+    if (all.on)
+        join_slice<L, D>(a, all, blockIdx.x - all.ca - 1, all.cb - all.ca, threadIdx.x, kJoinThreads, slots,
+                         [] { __syncthreads(); });
+    if (mine.on) join_slice<L, D>(a, mine, 0, 1, lane, 32, warp_slots[warp], [] { __syncwarp(); });
 }
 
 }  // namespace ft

@@ -1,0 +1,794 @@
+// Attention over the quantised cache for many rows per key: trees of drafted tokens and chunks of
+// prompts (max_q query tokens times the query heads of a group above 16 rows).
+//
+// The same one-pass softmax as the rows kernel, on the 5th-generation tensor cores.  A unit is 128
+// rows (token-major: row = token * G + head of the group) of a sequence and kv head; its keys come
+// in blocks of 128.  Per block S = Q K^T (128 x 128 x D, both operands in shared memory, fp32 in
+// tensor memory), P = 2^(t - m) as f16 back into tensor memory in the place of S, O += P V (128 x D
+// x 128, P from tensor memory, V from shared memory with the head dim contiguous).  One CTA per SM:
+//   warps 0-3   softmax: one row per thread, so maxima and sums need no exchange; O is rescaled in
+//               tensor memory only when a row's maximum has grown past the headroom
+//   warps 4-7   K: codes -> f16 in the 128-byte swizzled layout; at a unit's start also Q
+//   warps 8-11  V: the same
+//   warp 12     issues the matrix instructions: S of block j + 1 before O of block j, so the tensor
+//               cores work while the softmax warps do (13-15 only complete its warpgroup)
+// The block starts with 128 registers a thread; the last warpgroup gives up 88 of them and the K and
+// V warpgroups take 40 each (128 + 168 + 168 + 40 <= 4 * 128), which hold a block's codes.
+// Unpacking a block costs as many issue slots as its softmax, so it has as many warps again; the
+// codes of the next block are loaded into registers before the wait for its buffer.  Within a
+// lane's 16-byte vectors the order of the shared-memory stores is permuted so that the 8 lanes of a
+// store phase hit the 8 banks groups of a swizzle row.
+// Units are laid on the line of shares like the rows kernel's (a unit's start and end cost about
+// three blocks), so causal and ragged chunks balance; cut units are joined by the second kernel.
+// Every wait is bounded: on expiry the CTA sets FT_DEV_TIMEOUT, leaves its loops and frees its
+// tensor memory.
+#include <atomic>
+
+#include "ft_kv_attn.cuh"
+
+namespace ft {
+
+namespace {
+
+constexpr int kKeys = 128, kRows = 128;
+constexpr int kThreads = 16 * 32;
+constexpr long kWaitLimit = 1L << 22;
+using TilesLine = Line<kKeys, kRows, 1, 4, 3>;
+
+// Buffers of K and of V: two blocks where they fit beside Q.
+constexpr int bufs(int D) { return D == 256 ? 1 : 2; }
+constexpr int region(int D) { return kKeys * D * 2; }                    // bytes of a block of K or V, and of Q
+constexpr size_t tiles_smem(int D) { return (size_t)region(D) * (1 + 2 * bufs(D)) + 1024; }
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint32_t b, int n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(b), "r"(n));
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(b) : "memory");
+}
+// Bounded wait of a whole warp for the phase of the given parity; false (for every lane) once the
+// limit is hit or a role gave up.
+__device__ __forceinline__ bool mbar_wait(uint32_t b, uint32_t parity, volatile int* abort_flag) {
+    bool done = false;
+    for (long it = 0; it < kWaitLimit && !done; ++it) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(b), "r"(parity) : "memory");
+        done = ok != 0;
+        if (!done && (it & 255) == 255 && *abort_flag) break;
+    }
+    done = __all_sync(0xffffffffu, done);
+    if (!done) *abort_flag = 1;
+    return done;
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+// 128-byte swizzled operand, 64 f16 per row of the swizzle, 8-row groups 1024 bytes apart.  K-major
+// (Q, K: rows are the m or n index): the k index runs along the row, the next 64 of it are a region
+// of 128 rows further.  MN-major (V: rows are the k index): the n index runs along the row, the next
+// 64 of it 16 KB further (the leading offset).
+__device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lead) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+constexpr uint32_t idesc(int n, bool b_mn) {       // f16 x f16 -> f32, M = 128
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+}
+
+#define FT_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+#define FT_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : FT_R8(r, 0), FT_R8(r, 8), FT_R8(r, 16), FT_R8(r, 24) : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+                 :: FT_I8(r, 0), FT_I8(r, 8), FT_I8(r, 16), FT_I8(r, 24), "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+                 :: FT_I8(r, 0), FT_I8(r, 8), "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Four f16 pairs of 8 E2M1 codes times a scale pair; of 8 E4M3 codes (two words).
+__device__ __forceinline__ uint4 unpack_e2m1(uint32_t w, uint32_t s2) {
+    uint4 o;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 x0, x1, x2, x3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 x0, b0;\n\tcvt.rn.f16x2.e2m1x2 x1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 x2, b2;\n\tcvt.rn.f16x2.e2m1x2 x3, b3;\n\t"
+        "mul.rn.f16x2 %0, x0, %5;\n\tmul.rn.f16x2 %1, x1, %5;\n\tmul.rn.f16x2 %2, x2, %5;\n\tmul.rn.f16x2 %3, x3, %5;\n\t}"
+        : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w) : "r"(w), "r"(s2));
+    return o;
+}
+__device__ __forceinline__ uint4 unpack_e4m3(uint32_t w0, uint32_t w1) {
+    uint4 o;
+    asm("{\n\t.reg .b16 a, b, c, d;\n\tmov.b32 {a, b}, %4;\n\tmov.b32 {c, d}, %5;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %2, c;\n\tcvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
+        : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w) : "r"(w0), "r"(w1));
+    return o;
+}
+// The byte of w at a lane's place as a pair of equal f16.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
+    uint32_t o;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(o) : "r"(byte * 0x101u));
+    return o;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// Two fp32 at a time.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+    f32x2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 unpair(f32x2 a) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+    return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// 16-byte chunk c (8 dims) of row r of a [128 rows][D] operand.
+__device__ __forceinline__ void store_chunk(uint8_t* base, int r, int c, uint4 v) {
+    *reinterpret_cast<uint4*>(base + (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+}
+
+// A lane's raw bytes of a tile's K or V.
+template <int D, int kFormat>
+struct Raw {
+    static constexpr int kVecs = kFormat == FT_KV_NVFP4 ? D / 64 : D / 32;
+    uint4 v[kVecs];
+    uint2 s;                 // K: the lane's D/32 scales; V: the word of each of its blocks (NVFP4)
+};
+
+// K.  The lane (g, t) holds dims t D/4 .. of tokens g and 8 + g: chunks t D/32 + z, z < D/32.  The
+// lanes t of a store phase differ in chunk z ^ perm(t).
+template <int D, int kFormat>
+__device__ __forceinline__ void load_k(Raw<D, kFormat>& r, const uint8_t* tile, int lane) {
+    constexpr KvTile T = kv_tile(D, kFormat);
+    const int t = lane & 3;
+    // which vector of its token a lane loads k-th
+    const int swap = kFormat == FT_KV_NVFP4 ? (D == 256 ? t >> 1 : 0) : D == 128 ? t >> 1 : D == 256 ? t : 0;
+#pragma unroll
+    for (int x = 0; x < r.kVecs; ++x)
+        r.v[x] = __ldg(reinterpret_cast<const uint4*>(tile + (x ^ swap) * 512 + lane * 16));
+    if constexpr (kFormat == FT_KV_NVFP4) {
+        const uint8_t* sp = tile + T.k_scales + lane * (D / 32);
+        if constexpr (D == 64) r.s.x = __ldg(reinterpret_cast<const uint16_t*>(sp));
+        if constexpr (D == 128) r.s.x = __ldg(reinterpret_cast<const uint32_t*>(sp));
+        if constexpr (D == 256) r.s = __ldg(reinterpret_cast<const uint2*>(sp));
+    }
+}
+template <int D, int kFormat>
+__device__ __forceinline__ void write_k(uint8_t* base, const Raw<D, kFormat>& r, int row0, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    if constexpr (kFormat == FT_KV_NVFP4) {
+        if constexpr (D == 64) {
+            const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const uint32_t s2 = scale_pair(r.s.x >> (8 * v) & 255u);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) store_chunk(base, row0 + 8 * v + g, t * 2 + i, unpack_e2m1(w[2 * v + i], s2));
+            }
+        } else {
+            // words of a vector swapped in pairs for half of the lanes
+            const bool pairs = D == 128 ? t >> 1 : t & 1;
+#pragma unroll
+            for (int x = 0; x < r.kVecs; ++x) {
+                const int v = D == 128 ? x : x >> 1;
+                const int half = D == 128 ? 0 : (x & 1) ^ (t >> 1);       // which 32 dims of the lane's
+                const uint32_t a0 = pairs ? r.v[x].z : r.v[x].x, a1 = pairs ? r.v[x].w : r.v[x].y;
+                const uint32_t b0 = pairs ? r.v[x].x : r.v[x].z, b1 = pairs ? r.v[x].y : r.v[x].w;
+                const uint32_t sw = D == 128 ? r.s.x >> (16 * v) : (v ? r.s.y : r.s.x) >> (16 * half);
+                const int p = pairs ? 1 : 0;
+                const uint32_t sa = scale_pair(sw >> (8 * p) & 255u), sb = scale_pair(sw >> (8 * (p ^ 1)) & 255u);
+                const int c = t * (D / 32) + half * 4, row = row0 + 8 * v + g;
+                store_chunk(base, row, c + 2 * p, unpack_e2m1(a0, sa));
+                store_chunk(base, row, c + 2 * p + 1, unpack_e2m1(a1, sa));
+                store_chunk(base, row, c + 2 * (p ^ 1), unpack_e2m1(b0, sb));
+                store_chunk(base, row, c + 2 * (p ^ 1) + 1, unpack_e2m1(b1, sb));
+            }
+        }
+    } else {
+        const int swap = D == 128 ? t >> 1 : D == 256 ? t : 0;
+        constexpr int kPer = D / 64;                                      // vectors of a token
+#pragma unroll
+        for (int x = 0; x < r.kVecs; ++x) {
+            const int y = x ^ swap, row = row0 + 8 * (x / kPer) + g, c = t * (D / 32) + (y % kPer) * 2;
+            store_chunk(base, row, c, unpack_e4m3(r.v[x].x, r.v[x].y));
+            store_chunk(base, row, c + 1, unpack_e4m3(r.v[x].z, r.v[x].w));
+        }
+    }
+}
+
+// V.  The lane holds dims g D/8 .. of tokens 2t, 2t + 1, 2t + 8, 2t + 9: chunks g D/64 + z.  Odd g take
+// neighbouring chunks in the other order.
+template <int D, int kFormat>
+__device__ __forceinline__ void load_v(Raw<D, kFormat>& r, const uint8_t* tile, int lane) {
+    constexpr KvTile T = kv_tile(D, kFormat);
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int x = 0; x < r.kVecs; ++x) r.v[x] = __ldg(reinterpret_cast<const uint4*>(tile + T.code_bytes + x * 512 + lane * 16));
+    if constexpr (kFormat == FT_KV_NVFP4) {
+        const int blk = D == 64 ? g >> 1 : D == 128 ? g : 2 * g;
+        r.s.x = __ldg(reinterpret_cast<const uint32_t*>(tile + T.v_scales + (blk * 4 + t) * 4));
+        if constexpr (D == 256) r.s.y = __ldg(reinterpret_cast<const uint32_t*>(tile + T.v_scales + ((blk + 1) * 4 + t) * 4));
+    }
+}
+template <int D, int kFormat>
+__device__ __forceinline__ void write_v(uint8_t* base, const Raw<D, kFormat>& r, int row0, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    const bool odd = g & 1;
+    auto row_of = [&](int q) { return row0 + 2 * t + (q & 1) + 8 * (q >> 1); };
+    if constexpr (kFormat == FT_KV_NVFP4) {
+        if constexpr (D == 64) {
+            const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) store_chunk(base, row_of(q), g, unpack_e2m1(w[q], scale_pair(r.s.x >> (8 * q) & 255u)));
+        } else if constexpr (D == 128) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t w[4] = {odd ? r.v[x].y : r.v[x].x, odd ? r.v[x].x : r.v[x].y, odd ? r.v[x].w : r.v[x].z,
+                                       odd ? r.v[x].z : r.v[x].w};
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int q = 2 * x + y;
+                    const uint32_t s2 = scale_pair(r.s.x >> (8 * q) & 255u);
+                    store_chunk(base, row_of(q), 2 * g + (odd ? 1 : 0), unpack_e2m1(w[2 * y], s2));
+                    store_chunk(base, row_of(q), 2 * g + (odd ? 0 : 1), unpack_e2m1(w[2 * y + 1], s2));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t w[4] = {odd ? r.v[q].y : r.v[q].x, odd ? r.v[q].x : r.v[q].y, odd ? r.v[q].w : r.v[q].z,
+                                       odd ? r.v[q].z : r.v[q].w};
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const uint32_t s2 = scale_pair((b ? r.s.y : r.s.x) >> (8 * q) & 255u);
+                    store_chunk(base, row_of(q), 4 * g + 2 * b + (odd ? 1 : 0), unpack_e2m1(w[2 * b], s2));
+                    store_chunk(base, row_of(q), 4 * g + 2 * b + (odd ? 0 : 1), unpack_e2m1(w[2 * b + 1], s2));
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int x = 0; x < r.kVecs; ++x) {
+            const uint4 v = r.v[x];
+            if constexpr (D == 64) {
+                store_chunk(base, row_of(2 * x), g, unpack_e4m3(v.x, v.y));
+                store_chunk(base, row_of(2 * x + 1), g, unpack_e4m3(v.z, v.w));
+            } else {
+                constexpr int kPer = D / 128;                             // vectors of a token
+                const int c = g * (D / 64) + x % kPer * 2, row = row_of(x / kPer);
+                store_chunk(base, row, c + (odd ? 1 : 0), unpack_e4m3(odd ? v.z : v.x, odd ? v.w : v.y));
+                store_chunk(base, row, c + (odd ? 0 : 1), unpack_e4m3(odd ? v.x : v.z, odd ? v.y : v.w));
+            }
+        }
+    }
+}
+template <int D, int kFormat>
+__device__ __forceinline__ void clear(Raw<D, kFormat>& r) {
+#pragma unroll
+    for (int x = 0; x < r.kVecs; ++x) r.v[x] = make_uint4(0, 0, 0, 0);
+    r.s = make_uint2(0, 0);
+}
+
+// What a CTA does of one unit: its blocks [v0, v1).
+struct Run {
+    Unit u;
+    int v0, v1;
+};
+
+}  // namespace
+
+template <int D, int kFormat>
+__global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a) {
+    using L = TilesLine;
+    constexpr int kBufs = bufs(D), kRegion = region(D);
+    constexpr KvTile kT = kv_tile(D, kFormat);
+    constexpr uint32_t kColO = 256;                       // S and P: columns 0..127 and 128..255
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t* sq = smem;
+    uint8_t* sk = smem + kRegion;
+    uint8_t* sv = sk + kBufs * kRegion;
+    __shared__ long long prefix[kMaxSeqs + 1], scratch[kThreads / 32];
+    __shared__ __align__(8) uint64_t bars[4 * 2 + 2 + 2 + 2];
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int abort_flag;
+    // Written by the K warps, read by the softmax warps up to two blocks (or three short units) later:
+    // four slots each, the block's or the unit's number modulo 4.
+    __shared__ float coef[4][kRows];                      // t = s * coef
+    __shared__ unsigned present[4][4];                    // by K warp: which of its two tiles are there
+    __shared__ int drafted[4][kTreeMax];                  // places of the drafted tokens
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t b0 = smem_u32(&bars[0]);
+    // K full/empty, V full/empty by buffer; S full, P full by parity; O done
+    auto k_full = [&](int b) { return b0 + 8 * b; };
+    auto k_empty = [&](int b) { return b0 + 16 + 8 * b; };
+    auto v_full = [&](int b) { return b0 + 32 + 8 * b; };
+    auto v_empty = [&](int b) { return b0 + 48 + 8 * b; };
+    auto s_full = [&](int b) { return b0 + 64 + 8 * b; };
+    auto p_full = [&](int b) { return b0 + 80 + 8 * b; };
+    const uint32_t o_done = b0 + 96, drain = b0 + 104;
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(k_full(b), 4);
+            mbar_init(k_empty(b), 1);
+            mbar_init(v_full(b), 4);
+            mbar_init(v_empty(b), 1);
+            mbar_init(s_full(b), 1);
+            mbar_init(p_full(b), 4);
+        }
+        mbar_init(o_done, 1);
+        mbar_init(drain, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(&tmem_base)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    pdl_wait_and_release();
+    line_prefix<L>(a, prefix, scratch);                   // ends with a CTA barrier
+    tc_after();
+    const uint32_t tmem = tmem_base;
+
+    const long long total = prefix[a.n_seqs];
+    const Shares shares(total, gridDim.x, L::kMin);
+    const int cta = blockIdx.x;
+    const bool work = total > 0 && cta < shares.nc;
+    const long long c0 = work ? shares.cut(cta) : 0, c1 = work ? shares.cut(cta + 1) : 0;
+
+    // The runs of the CTA in order; every role walks them by itself.
+    long long pos = c0;
+    auto next_run = [&](Run& r) {
+        while (pos < c1) {
+            r.u = find_unit<L>(a, prefix, pos);
+            r.v0 = block_at<L>(r.u.first, r.u.rt.nt, pos);
+            r.v1 = block_at<L>(r.u.first, r.u.rt.nt, c1);
+            pos = r.u.end;
+            if (r.v0 < r.v1) return true;
+        }
+        return false;
+    };
+
+    Run run;
+    bool ok = true;
+    if (warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    else if (warp >= 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    if (warp < 4) {
+        // ------------------------------------------------------------------------ softmax
+        const int row = 32 * warp + lane;                 // of the unit's 128
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16);
+        unsigned it = 0;
+        for (int un = 0; ok && next_run(run); ++un) {
+            const SeqInfo& si = run.u.si;
+            const int base = si.len - si.n, grow = run.u.r * kRows + row;
+            const RowRule rule = row_rule(a, si, grow);
+            // keys below all_lim and from all_low on are seen by every row of the unit
+            const RowRule first_rule = row_rule(a, si, run.u.r * kRows);
+            const int all_lim = a.tree ? base - 1 : first_rule.lim;
+            const int all_low = a.window > 0 ? (int)max((long long)(a.tree ? base + si.n : base + run.u.rt.i1) - a.window + 1, 0LL) : 0;
+            // the reference is kept in units of s, so that s - m is exact near it however large t is
+            float m = kNoRef, c = 0.f;
+            f32x2 l2 = pair(0.f, 0.f);                    // two halves of the sum of weights
+            for (int v = run.v0; v < run.v1; ++v, ++it) {
+                const int b = it & 1;
+                if (!mbar_wait(s_full(b), it >> 1 & 1, &abort_flag)) { ok = false; break; }
+                tc_after();
+                if (v == run.v0) c = coef[un & 3][row];
+                const uint32_t s_addr = lane_addr + 128 * b;
+                const int j0 = run.u.rt.block(v) * kKeys;
+                unsigned there = 0;                       // the block's tiles
+#pragma unroll
+                for (int w = 0; w < 4; ++w) there |= present[it & 3][w] << (2 * w);
+                const bool edge = there != 255u || j0 + kKeys - 1 > all_lim || (j0 < all_low && j0 + kKeys > a.n_sink) || run.u.rt.empty;
+                // which of the 32 keys from j on the row sees
+                auto mask_of = [&](int ch) {
+                    const int j = j0 + 32 * ch;
+                    auto below = [&](int x) {             // bits of keys < x
+                        const int n = x - j;
+                        return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1;
+                    };
+                    const int lim1 = rule.lim + 1;
+                    unsigned ok_bits = below(lim1) & (~below(rule.low) | below(a.n_sink));
+                    if (a.tree && j + 31 >= base && rule.lim >= 0) {
+                        const unsigned old = below(base);
+                        const int sh = j - base;          // drafted token of bit 0
+                        unsigned d = sh >= 64 ? 0u : sh >= 0 ? (unsigned)(rule.mask >> sh) : sh > -32 ? (unsigned)(rule.mask << -sh) : 0u;
+                        d &= below(lim1) & ~old;
+                        if (a.window > 0) {
+                            unsigned far = 0;
+                            for (unsigned x = d; x; x &= x - 1) {
+                                const int e = __ffs(x) - 1;
+                                if (drafted[un & 3][sh + e] < rule.low && j + e >= a.n_sink) far |= 1u << e;
+                            }
+                            d &= ~far;
+                        }
+                        ok_bits = (ok_bits & old) | d;
+                    }
+                    const unsigned t2 = there >> (2 * ch);
+                    return ok_bits & ((t2 & 1 ? 0xFFFFu : 0u) | (t2 & 2 ? 0xFFFF0000u : 0u));
+                };
+                // the row's largest s
+                float top = kNoRef;
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t s[32];
+                    tmem_ld32(s_addr + 32 * ch, s);
+                    const unsigned seen = edge ? mask_of(ch) : 0xFFFFFFFFu;
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float x = __uint_as_float(s[e]), y = __uint_as_float(s[e + 1]);
+                        top = fmaxf(top, fmaxf(seen >> e & 1 ? x : kNoRef, seen >> (e + 1) & 1 ? y : kNoRef));
+                    }
+                }
+                // O of the block before is complete (waited for at every block, so that no phase is missed)
+                if (it > 0 && !mbar_wait(o_done, (it - 1) & 1, &abort_flag)) { ok = false; break; }
+                const bool raise = top > m && (m == kNoRef || (top - m) * c > kHeadroom);
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float mm = fmaxf(m, top), f = m == kNoRef ? 0.f : ex2((m - mm) * c);
+                    m = mm;
+                    l2 = mul2(l2, pair(f, f));
+                    if (v > run.v0) {
+                        tc_after();
+#pragma unroll 1
+                        for (int x = 0; x < D; x += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(lane_addr + kColO + x, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(lane_addr + kColO + x, o);
+                        }
+                    }
+                }
+                const f32x2 m2 = pair(-m, -m), c2 = pair(c, c), head2 = pair(kHeadroom, kHeadroom);
+                // P over S: 32 columns of S become 16 of f16 pairs, over columns that have been read
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t s[32], p[16];
+                    tmem_ld32(s_addr + 32 * ch, s);
+                    const unsigned seen = edge ? mask_of(ch) : 0xFFFFFFFFu;
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 x = unpair(fma2(add2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), m2), c2, head2));
+                        x.x = seen >> e & 1 ? ex2(x.x) : 0.f;
+                        x.y = seen >> (e + 1) & 1 ? ex2(x.y) : 0.f;
+                        l2 = add2(l2, pair(x.x, x.y));
+                        p[e >> 1] = pack_f16(x.x, x.y);
+                    }
+                    tmem_st16(s_addr + 16 * ch, p);
+                }
+                tmem_wait_st();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(b));
+            }
+            if (!ok) break;
+            // the unit's sums
+            if (!mbar_wait(o_done, (it - 1) & 1, &abort_flag)) { ok = false; break; }
+            tc_after();
+            const float l = unpair(l2).x + unpair(l2).y;
+            if (m != kNoRef) m *= c;
+            const int i = grow / a.G;
+            const bool on = i < si.n, done = run.v0 == 0 && run.v1 == run.u.rt.nt;
+            float* out = partial<D, kRows>(a, 2 * cta + (run.v0 > 0 ? 0 : 1));
+            if (on && !done) reinterpret_cast<float2*>(out)[row] = make_float2(m, l);
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+                uint32_t o[32];
+                __syncwarp();
+                tmem_ld32(lane_addr + kColO + x, o);
+                tmem_wait_ld();
+                if (on) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        float y[8];
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(o[e + z]);
+                        if (done) {
+                            store_out<8>(a, (size_t)(si.q0 + i), run.u.h * a.G + grow % a.G, D, x + e, y, m, l);
+                        } else {
+                            float4* dst = reinterpret_cast<float4*>(out + 2 * kRows + row * D + x + e);
+                            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            tc_before();                                  // the next unit's first P follows these reads
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------------------ K (and Q), V
+        const bool is_k = warp < 8;
+        const int w = warp & 3;                           // tiles 2w, 2w + 1 of a block
+        const int per = a.kv.page_shift - 4;
+        unsigned it = 0;
+        for (int un = 0; ok && next_run(run); ++un) {
+            const SeqInfo& si = run.u.si;
+            const int base = si.len - si.n;
+            const int32_t* table = a.table + (size_t)run.u.s * a.table_stride;
+            // keys that some row sees: below hi, from lo on or among the first tokens
+            const int hi = run.u.rt.empty ? 0 : a.tree ? si.len : min(si.len, base + run.u.rt.i1 + 1);
+            const int lo = a.window > 0 ? (int)max((long long)base + (a.tree ? 0 : run.u.rt.i0) - a.window + 1, 0LL) : 0;
+            // pages of this warp's tiles: lane x holds that of tile (x & 1) of block v0 + 16 * group + (x >> 1)
+            int group = -1, page = -1;
+            Raw<D, kFormat> raw[2];
+            unsigned there = 0;
+            auto load = [&](int v) {
+                const int gr = (v - run.v0) >> 4;
+                if (gr != group) {
+                    group = gr;
+                    page = -1;
+                    const int mine = run.v0 + 16 * gr + (lane >> 1);
+                    if (mine < run.v1) {
+                        const int tile = run.u.rt.block(mine) * (kKeys / 16) + 2 * w + (lane & 1), key = tile * 16;
+                        if (key < hi && (key + 15 >= lo || key < a.n_sink)) {
+                            page = table[tile >> per];
+                            if (page < 0 || page >= a.kv.n_pages) {
+                                atomicOr(a.kv.status, FT_DEV_BAD_ID);
+                                page = -1;
+                            }
+                        }
+                    }
+                }
+                there = 0;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int pg = __shfl_sync(0xffffffffu, page, ((v - run.v0) & 15) * 2 + x);
+                    if (pg >= 0) {
+                        there |= 1u << x;
+                        const int tile = run.u.rt.block(v) * (kKeys / 16) + 2 * w + x;
+                        const uint8_t* src = a.kv.pool + ((((size_t)pg * a.kv.hkv + run.u.h) << per) + (tile & ((1 << per) - 1))) * kT.bytes;
+                        if (is_k) load_k<D, kFormat>(raw[x], src, lane);
+                        else load_v<D, kFormat>(raw[x], src, lane);
+                    } else {
+                        clear(raw[x]);
+                    }
+                }
+            };
+            load(run.v0);
+            if (is_k) {
+                // Q of the unit: every product of the unit before is through with it
+                if (it > 0 && !mbar_wait(k_empty((it - 1) % kBufs), ((it - 1) / kBufs) & 1, &abort_flag)) { ok = false; break; }
+                if (a.tree && w == 0)
+                    for (int j = lane; j < si.n; j += 32)
+                        drafted[un & 3][j] = base + __popcll(a.tree[si.q0 + j] & ~(1ull << j));
+                // 8 lanes per row, D/8 dims each
+#pragma unroll 1
+                for (int x = 0; x < 8; ++x) {
+                    const int row = 32 * w + 4 * x + (lane >> 3), part = lane & 7, grow = run.u.r * kRows + row, i = grow / a.G;
+                    const bool on = i < si.n;
+                    const __nv_bfloat16* src = a.q + (size_t)(si.q0 + i) * a.q_stride + (size_t)(run.u.h * a.G + grow % a.G) * D + part * 8;
+                    uint4 q[D / 64];
+                    float amax = 0.f;
+#pragma unroll
+                    for (int e = 0; e < D / 64; ++e) {
+                        q[e] = on ? *reinterpret_cast<const uint4*>(src + 64 * e) : make_uint4(0, 0, 0, 0);
+                        const uint32_t wd[4] = {q[e].x, q[e].y, q[e].z, q[e].w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(wd[y] << 16)), fabsf(__uint_as_float(wd[y] & 0xFFFF0000u))));
+                    }
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    const RowScale rs = row_scale(amax);
+                    // the coefficient is not negative: q carries the scale's sign
+                    const float down = a.scale < 0.f ? -rs.down : rs.down;
+                    if (part == 0) coef[un & 3][row] = fabsf(a.scale) * a.kv.k_scale * 1.44269504088896340736f * rs.up;
+#pragma unroll
+                    for (int e = 0; e < D / 64; ++e) {
+                        const uint32_t wd[4] = {q[e].x, q[e].y, q[e].z, q[e].w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            o[y] = pack_f16(__uint_as_float(wd[y] << 16) * down, __uint_as_float(wd[y] & 0xFFFF0000u) * down);
+                        store_chunk(sq, row, e * 8 + part, make_uint4(o[0], o[1], o[2], o[3]));
+                    }
+                }
+            }
+            for (int v = run.v0; v < run.v1; ++v, ++it) {
+                const int b = it % kBufs;
+                const uint32_t ph = (it / kBufs) & 1;
+                if (!mbar_wait(is_k ? k_empty(b) : v_empty(b), ph ^ 1, &abort_flag)) { ok = false; break; }
+                uint8_t* dst = (is_k ? sk : sv) + b * kRegion;
+                const int j0 = run.u.rt.block(v) * kKeys;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int row0 = 32 * w + 16 * x;
+                    if (is_k) {
+                        write_k<D, kFormat>(dst, raw[x], row0, lane);
+                    } else {
+                        if (there >> x & 1 && j0 + row0 + 16 > si.len) {
+                            // past the cached tokens the bytes may be anything: zero the lane's tokens there
+                            const int t = lane & 3;
+                            if constexpr (kFormat == FT_KV_NVFP4) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (j0 + row0 + 2 * t + (q & 1) + 8 * (q >> 1) >= si.len) {
+                                        raw[x].s.x &= ~(255u << (8 * q));
+                                        raw[x].s.y &= ~(255u << (8 * q));
+                                    }
+                            } else {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (j0 + row0 + 2 * t + (q & 1) + 8 * (q >> 1) >= si.len) {
+                                        if constexpr (D == 64) {
+                                            if (q & 1) raw[x].v[q >> 1].z = raw[x].v[q >> 1].w = 0;
+                                            else raw[x].v[q >> 1].x = raw[x].v[q >> 1].y = 0;
+                                        } else {
+#pragma unroll
+                                            for (int y = 0; y < D / 128; ++y) raw[x].v[q * (D / 128) + y] = make_uint4(0, 0, 0, 0);
+                                        }
+                                    }
+                            }
+                        }
+                        write_v<D, kFormat>(dst, raw[x], row0, lane);
+                    }
+                }
+                if (is_k && lane == 0) present[it & 3][w] = there;
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(is_k ? k_full(b) : v_full(b));
+                if (v + 1 < run.v1) load(v + 1);
+            }
+        }
+        if (is_k && w == 0) {                             // the unit that the cut at the CTA's first place goes through
+            if (work) run.u = find_unit<L>(a, prefix, c0);
+            if (lane == 0) {
+                if (work && run.u.first < c0)
+                    a.tasks[cta] = join_task(shares, run.u, shares.holder(run.u.first), shares.holder(run.u.end - 1));
+                else
+                    a.tasks[cta].on = 0;
+            }
+        }
+    } else if (warp == 12) {
+        // ------------------------------------------------------------------------ matrix instructions
+        unsigned it = 0;
+        const uint32_t q_addr = smem_u32(sq), k_addr = smem_u32(sk), v_addr = smem_u32(sv);
+        auto products_s = [&](unsigned n) {               // S of block n
+            const int b = n % kBufs;
+            if (!mbar_wait(k_full(b), (n / kBufs) & 1, &abort_flag)) return false;
+            tc_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint32_t at = (x >> 2) * (kKeys * 128) + (x & 3) * 32;
+                    mma_ss(tmem + 128 * (n & 1), desc(q_addr + at, 16), desc(k_addr + b * kRegion + at, 16), idesc(kKeys, false), x > 0);
+                }
+                tc_commit(k_empty(b));
+                tc_commit(s_full(n & 1));
+            }
+            __syncwarp();
+            return true;
+        };
+        auto products_o = [&](unsigned n, bool first) {   // O of block n
+            const int b = n % kBufs;
+            if (!mbar_wait(v_full(b), (n / kBufs) & 1, &abort_flag)) return false;
+            if (!mbar_wait(p_full(n & 1), n >> 1 & 1, &abort_flag)) return false;
+            tc_after();
+            if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < kKeys / 16; ++x)
+                    mma_ts(tmem + kColO, tmem + 128 * (n & 1) + 8 * x, desc(v_addr + b * kRegion + x * 2048, kKeys * 128),
+                           idesc(D, true), !first || x > 0);
+                tc_commit(v_empty(b));
+                tc_commit(o_done);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool pending = false, pending_first = false;      // O of block it - 1 is still to be issued
+        while (ok && next_run(run)) {
+            for (int v = run.v0; v < run.v1 && ok; ++v, ++it) {
+                ok = products_s(it);
+                if (ok && pending) ok = products_o(it - 1, pending_first);
+                pending = true;
+                pending_first = v == run.v0;
+            }
+        }
+        if (ok && pending) ok = products_o(it - 1, pending_first);
+        if (!ok) {                                        // what was issued still reads shared memory
+            if (lane == 0) tc_commit(drain);
+            mbar_wait(drain, 0, &abort_flag);
+        }
+    }
+    if (!ok && lane == 0) atomicOr(a.kv.status, FT_DEV_TIMEOUT);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+}
+
+namespace {
+
+// CTAs: one per SM (0 when the kernel cannot be set up; looked up once per device).
+template <int D, int kFormat>
+int tiles_grid() {
+    static std::atomic<int> grids[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return 0;
+    }
+    int v = grids[dev].load(std::memory_order_relaxed);
+    if (!v) {
+        auto kern = kv_tiles_kernel<D, kFormat>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tiles_smem(D)) != cudaSuccess ||
+            all_shared(kern) != cudaSuccess || all_shared(kv_join_kernel<TilesLine, D>) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        v = min(sm_count(), kMaxShares / 2);
+        grids[dev].store(v, std::memory_order_relaxed);
+    }
+    return v;
+}
+
+template <int D, int kFormat>
+cudaError_t run_tiles(const AttnArgs& a, cudaStream_t s) {
+    const int grid = tiles_grid<D, kFormat>();
+    if (grid < 1) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = launch_pdl(kv_tiles_kernel<D, kFormat>, dim3(grid), dim3(kThreads), tiles_smem(D), s, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kv_join_kernel<TilesLine, D>, dim3(grid), dim3(kJoinThreads), 0, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_tiles(const AttnArgs& a, int D, int format, cudaStream_t s) {
+    if (format == FT_KV_NVFP4)
+        return D == 64 ? run_tiles<64, FT_KV_NVFP4>(a, s) : D == 128 ? run_tiles<128, FT_KV_NVFP4>(a, s) : run_tiles<256, FT_KV_NVFP4>(a, s);
+    return D == 64 ? run_tiles<64, FT_KV_FP8>(a, s) : D == 128 ? run_tiles<128, FT_KV_FP8>(a, s) : run_tiles<256, FT_KV_FP8>(a, s);
+}
+
+}  // namespace ft
