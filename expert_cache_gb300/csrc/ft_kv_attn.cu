@@ -34,7 +34,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kMaxPerSm = 4;           // CTAs
 // at least 2 places of the line per warp; a unit's start and end cost about 8 tiles
 template <int NT>
-using RowsLine = Line<kKvTile, 8 * NT, kWarps, 2 * kWarps, 8>;
+using RowsLine = Line<kKvTile, 8 * NT, kWarps, 2 * kWarps, 8, 1>;
 constexpr long kWaitLimit = 1L << 24;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }

@@ -119,9 +119,10 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, size_t token, int h
 // kCost blocks), and every CTA takes an equal share of the places.  Within a CTA the kW workers
 // split the share: its tiles of the unit where the whole share lies in one unit (the workers then
 // join in the CTA), its places otherwise.
-template <int kB_, int kR_, int kW_, int kMin_, int kCost_>
+// kSplit: CTAs of the joining kernel per share.
+template <int kB_, int kR_, int kW_, int kMin_, int kCost_, int kSplit_>
 struct Line {
-    static constexpr int kB = kB_, kR = kR_, kW = kW_, kMin = kMin_, kCost = kCost_;
+    static constexpr int kB = kB_, kR = kR_, kW = kW_, kMin = kMin_, kCost = kCost_, kSplit = kSplit_;
 };
 
 constexpr int kMaxShares = 640;        // CTAs of a launch
@@ -385,13 +386,14 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttnArgs a)
     __shared__ int slots[2 * L::kW + kMaxShares], warp_slots[L::kW][L::kW];
     pdl_wait_and_release();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const JoinTask all = a.tasks[L::kW * blockIdx.x];
+    const int cta = blockIdx.x / L::kSplit, sub = blockIdx.x % L::kSplit;
+    const JoinTask all = a.tasks[L::kW * cta];
     JoinTask mine;
     mine.on = 0;
-    if (warp > 0 && warp < L::kW) mine = a.tasks[L::kW * blockIdx.x + warp];
+    if (warp > 0 && warp < L::kW && sub == 0) mine = a.tasks[L::kW * cta + warp];
     if (all.on)
-        join_slice<L, D>(a, all, blockIdx.x - all.ca - 1, all.cb - all.ca, threadIdx.x, kJoinThreads, slots,
-                         [] { __syncthreads(); });
+        join_slice<L, D>(a, all, (cta - all.ca - 1) * L::kSplit + sub, (all.cb - all.ca) * L::kSplit, threadIdx.x,
+                         kJoinThreads, slots, [] { __syncthreads(); });
     if (mine.on) join_slice<L, D>(a, mine, 0, 1, lane, 32, warp_slots[warp], [] { __syncwarp(); });
 }
 

@@ -6,14 +6,15 @@
 // in blocks of 128.  Per block S = Q K^T (128 x 128 x D, both operands in shared memory, fp32 in
 // tensor memory), P = 2^(t - m) as f16 back into tensor memory in the place of S, O += P V (128 x D
 // x 128, P from tensor memory, V from shared memory with the head dim contiguous).  One CTA per SM:
-//   warps 0-3   softmax: one row per thread, so maxima and sums need no exchange; O is rescaled in
-//               tensor memory only when a row's maximum has grown past the headroom
-//   warps 4-7   K: codes -> f16 in the 128-byte swizzled layout; at a unit's start also Q
-//   warps 8-11  V: the same
-//   warp 12     issues the matrix instructions: S of block j + 1 before O of block j, so the tensor
-//               cores work while the softmax warps do (13-15 only complete its warpgroup)
-// The block starts with 128 registers a thread; the last warpgroup gives up 88 of them and the K and
-// V warpgroups take 40 each (128 + 168 + 168 + 40 <= 4 * 128), which hold a block's codes.
+//   warps 0-7   softmax: two threads per row, 64 keys each, which exchange their maxima through
+//               shared memory; O is rescaled in tensor memory only when a row's maximum has grown
+//               past the headroom
+//   warps 8-11  K: codes -> f16 in the 128-byte swizzled layout; at a unit's start also Q
+//   warps 12-15 V: the same
+//   warp 16     issues the matrix instructions: S of block j + 1 before O of block j, so the tensor
+//               cores work while the softmax warps do (17-19 only complete its warpgroup)
+// The block starts with 96 registers a thread; the last warpgroup gives up 56 of them, the softmax
+// warpgroups take 16 each and K's and V's 8 (2 * 112 + 2 * 104 + 40 <= 5 * 96).
 // Unpacking a block costs as many issue slots as its softmax, so it has as many warps again; the
 // codes of the next block are loaded into registers before the wait for its buffer.  Within a
 // lane's 16-byte vectors the order of the shared-memory stores is permuted so that the 8 lanes of a
@@ -31,9 +32,11 @@ namespace ft {
 namespace {
 
 constexpr int kKeys = 128, kRows = 128;
-constexpr int kThreads = 16 * 32;
+constexpr int kThreads = 20 * 32;
+constexpr int kWarpK = 8, kWarpV = 12, kWarpMma = 16;      // first warps of the roles after the softmax's
 constexpr long kWaitLimit = 1L << 22;
-using TilesLine = Line<kKeys, kRows, 1, 4, 3>;
+constexpr float kLeast = 1.2e-38f;
+using TilesLine = Line<kKeys, kRows, 1, 4, 3, 16>;
 
 // Buffers of K and of V: two blocks where they fit beside Q.
 constexpr int bufs(int D) { return D == 256 ? 1 : 2; }
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     uint8_t* sk = smem + kRegion;
     uint8_t* sv = sk + kBufs * kRegion;
     __shared__ long long prefix[kMaxSeqs + 1], scratch[kThreads / 32];
-    __shared__ __align__(8) uint64_t bars[4 * 2 + 2 + 2 + 2];
+    __shared__ __align__(8) uint64_t bars[4 * 2 + 2 + 2 + 2 + 8];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int abort_flag;
     // Written by the K warps, read by the softmax warps up to two blocks (or three short units) later:
@@ -343,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     __shared__ float coef[4][kRows];                      // t = s * coef
     __shared__ unsigned present[4][4];                    // by K warp: which of its two tiles are there
     __shared__ int drafted[4][kTreeMax];                  // places of the drafted tokens
+    __shared__ float tops[2][2][kRows];                   // by parity and half: what the halves of a row exchange
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t b0 = smem_u32(&bars[0]);
@@ -354,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     auto s_full = [&](int b) { return b0 + 64 + 8 * b; };
     auto p_full = [&](int b) { return b0 + 80 + 8 * b; };
     const uint32_t o_done = b0 + 96, drain = b0 + 104;
+    auto x_full = [&](int pair, int p) { return b0 + 112 + 16 * pair + 8 * p; };    // the halves of 32 rows
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(k_full(b), 4);
@@ -361,14 +366,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             mbar_init(v_full(b), 4);
             mbar_init(v_empty(b), 1);
             mbar_init(s_full(b), 1);
-            mbar_init(p_full(b), 4);
+            mbar_init(p_full(b), 8);
         }
         mbar_init(o_done, 1);
         mbar_init(drain, 1);
+        for (int x = 0; x < 8; ++x) mbar_init(x_full(x >> 1, x & 1), 2);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 12) {
+    if (warp == kWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" :: "r"(smem_u32(&tmem_base)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -399,13 +405,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
 
     Run run;
     bool ok = true;
-    if (warp >= 12) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    else if (warp >= 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-    if (warp < 4) {
+    if (warp >= kWarpMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    else if (warp >= kWarpK) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    if (warp < kWarpK) {
         // ------------------------------------------------------------------------ softmax
-        const int row = 32 * warp + lane;                 // of the unit's 128
-        const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16);
-        unsigned it = 0;
+        const int row = 32 * (warp & 3) + lane;           // of the unit's 128
+        const int half = warp >> 2;                       // keys 64 half .. of a block, dims D/2 half .. of O
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        unsigned it = 0, xn = 0;
+        // y of the row's other half for x of this one
+        auto exchange = [&](float x, float& y) {
+            const int p = xn & 1;
+            tops[p][half][row] = x;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x_full(warp & 3, p));
+            if (!mbar_wait(x_full(warp & 3, p), xn >> 1 & 1, &abort_flag)) return false;
+            ++xn;
+            y = tops[p][half ^ 1][row];
+            return true;
+        };
         for (int un = 0; ok && next_run(run); ++un) {
             const SeqInfo& si = run.u.si;
             const int base = si.len - si.n, grow = run.u.r * kRows + row;
@@ -455,20 +474,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     const unsigned t2 = there >> (2 * ch);
                     return ok_bits & ((t2 & 1 ? 0xFFFFu : 0u) | (t2 & 2 ? 0xFFFF0000u : 0u));
                 };
+                uint32_t s[2][32];
+                tmem_ld32(s_addr + 64 * half, s[0]);
+                tmem_ld32(s_addr + 64 * half + 32, s[1]);
+                unsigned seen[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+                if (edge) {
+                    seen[0] = mask_of(2 * half);
+                    seen[1] = mask_of(2 * half + 1);
+                }
+                tmem_wait_ld();
                 // the row's largest s
                 float top = kNoRef;
-#pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t s[32];
-                    tmem_ld32(s_addr + 32 * ch, s);
-                    const unsigned seen = edge ? mask_of(ch) : 0xFFFFFFFFu;
-                    tmem_wait_ld();
+                if (!edge) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float x = __uint_as_float(s[e]), y = __uint_as_float(s[e + 1]);
-                        top = fmaxf(top, fmaxf(seen >> e & 1 ? x : kNoRef, seen >> (e + 1) & 1 ? y : kNoRef));
+                    for (int e = 0; e < 64; ++e) top = fmaxf(top, __uint_as_float(s[e >> 5][e & 31]));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) {
+                        // a key that is not seen gets -inf, whatever its bytes gave (weight 0: c is not negative)
+                        if (!(seen[e >> 5] >> (e & 31) & 1)) s[e >> 5][e & 31] = 0xFF800000u;
+                        top = fmaxf(top, __uint_as_float(s[e >> 5][e & 31]));
                     }
                 }
+                float other;                              // exchanged: also, all of the rows' S is read, P may go over it
+                if (!exchange(top, other)) { ok = false; break; }
+                top = fmaxf(top, other);
                 // O of the block before is complete (waited for at every block, so that no phase is missed)
                 if (it > 0 && !mbar_wait(o_done, (it - 1) & 1, &abort_flag)) { ok = false; break; }
                 const bool raise = top > m && (m == kNoRef || (top - m) * c > kHeadroom);
@@ -479,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     if (v > run.v0) {
                         tc_after();
 #pragma unroll 1
-                        for (int x = 0; x < D; x += 32) {
+                        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 32) {
                             uint32_t o[32];
                             tmem_ld32(lane_addr + kColO + x, o);
                             tmem_wait_ld();
@@ -489,23 +519,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                         }
                     }
                 }
-                const f32x2 m2 = pair(-m, -m), c2 = pair(c, c), head2 = pair(kHeadroom, kHeadroom);
-                // P over S: 32 columns of S become 16 of f16 pairs, over columns that have been read
-#pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t s[32], p[16];
-                    tmem_ld32(s_addr + 32 * ch, s);
-                    const unsigned seen = edge ? mask_of(ch) : 0xFFFFFFFFu;
-                    tmem_wait_ld();
+                // a row that has seen nothing keeps finite differences: its s are -inf
+                const float ref = m == kNoRef ? 0.f : m;
+                const f32x2 m2 = pair(-ref, -ref), c2 = pair(c, c), head2 = pair(kHeadroom, kHeadroom);
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float2 x = unpair(fma2(add2(pair(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), m2), c2, head2));
-                        x.x = seen >> e & 1 ? ex2(x.x) : 0.f;
-                        x.y = seen >> (e + 1) & 1 ? ex2(x.y) : 0.f;
+                        float2 x = unpair(fma2(add2(pair(__uint_as_float(s[ch][e]), __uint_as_float(s[ch][e + 1])), m2), c2, head2));
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
                         l2 = add2(l2, pair(x.x, x.y));
                         p[e >> 1] = pack_f16(x.x, x.y);
                     }
-                    tmem_st16(s_addr + 16 * ch, p);
+                    tmem_st16(s_addr + 32 * half + 16 * ch, p);
                 }
                 tmem_wait_st();
                 tc_before();
@@ -516,14 +544,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             // the unit's sums
             if (!mbar_wait(o_done, (it - 1) & 1, &abort_flag)) { ok = false; break; }
             tc_after();
-            const float l = unpair(l2).x + unpair(l2).y;
+            float l = unpair(l2).x + unpair(l2).y, other;
+            if (!exchange(l, other)) { ok = false; break; }
+            l += other;
             if (m != kNoRef) m *= c;
             const int i = grow / a.G;
             const bool on = i < si.n, done = run.v0 == 0 && run.v1 == run.u.rt.nt;
             float* out = partial<D, kRows>(a, 2 * cta + (run.v0 > 0 ? 0 : 1));
-            if (on && !done) reinterpret_cast<float2*>(out)[row] = make_float2(m, l);
+            if (on && !done && half == 0) reinterpret_cast<float2*>(out)[row] = make_float2(m, l);
 #pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
+            for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 32) {
                 uint32_t o[32];
                 __syncwarp();
                 tmem_ld32(lane_addr + kColO + x, o);
@@ -547,9 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             __syncwarp();
             tc_before();                                  // the next unit's first P follows these reads
         }
-    } else if (warp < 12) {
+    } else if (warp < kWarpMma) {
         // ------------------------------------------------------------------------ K (and Q), V
-        const bool is_k = warp < 8;
+        const bool is_k = warp < kWarpV;
         const int w = warp & 3;                           // tiles 2w, 2w + 1 of a block
         const int per = a.kv.page_shift - 4;
         unsigned it = 0;
@@ -622,9 +652,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
 #pragma unroll
                     for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                     const RowScale rs = row_scale(amax);
-                    // the coefficient is not negative: q carries the scale's sign
+                    // the coefficient is positive (q carries the scale's sign): times -inf it stays -inf
                     const float down = a.scale < 0.f ? -rs.down : rs.down;
-                    if (part == 0) coef[un & 3][row] = fabsf(a.scale) * a.kv.k_scale * 1.44269504088896340736f * rs.up;
+                    if (part == 0) coef[un & 3][row] = fmaxf(fabsf(a.scale) * a.kv.k_scale * 1.44269504088896340736f * rs.up, kLeast);
 #pragma unroll
                     for (int e = 0; e < D / 64; ++e) {
                         const uint32_t wd[4] = {q[e].x, q[e].y, q[e].z, q[e].w};
@@ -691,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     a.tasks[cta].on = 0;
             }
         }
-    } else if (warp == 12) {
+    } else if (warp == kWarpMma) {
         // ------------------------------------------------------------------------ matrix instructions
         unsigned it = 0;
         const uint32_t q_addr = smem_u32(sq), k_addr = smem_u32(sk), v_addr = smem_u32(sv);
@@ -746,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+    if (warp == kWarpMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
 }
 
 namespace {
@@ -780,7 +810,7 @@ cudaError_t run_tiles(const AttnArgs& a, cudaStream_t s) {
     if (grid < 1) return cudaErrorInvalidConfiguration;
     const cudaError_t e = launch_pdl(kv_tiles_kernel<D, kFormat>, dim3(grid), dim3(kThreads), tiles_smem(D), s, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv_join_kernel<TilesLine, D>, dim3(grid), dim3(kJoinThreads), 0, s, a);
+    return launch_pdl(kv_join_kernel<TilesLine, D>, dim3(grid * TilesLine::kSplit), dim3(kJoinThreads), 0, s, a);
 }
 
 }  // namespace
