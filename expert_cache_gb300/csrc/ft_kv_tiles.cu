@@ -36,6 +36,7 @@ constexpr int kThreads = 20 * 32;
 constexpr int kWarpK = 8, kWarpV = 12, kWarpMma = 16;      // first warps of the roles after the softmax's
 constexpr long kWaitLimit = 1L << 22;
 constexpr float kLeast = 1.2e-38f;
+constexpr unsigned kFirst = 0, kNext = 1, kEnd = 2;
 using TilesLine = Line<kKeys, kRows, 1, 4, 3, 16>;
 
 // Buffers of K and of V: two blocks where they fit beside Q.
@@ -64,6 +65,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t b, uint32_t parity, volatile 
     done = __all_sync(0xffffffffu, done);
     if (!done) *abort_flag = 1;
     return done;
+}
+// One lane of a whole warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -341,10 +348,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     __shared__ __align__(8) uint64_t bars[4 * 2 + 2 + 2 + 2 + 8];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int abort_flag;
-    // Written by the K warps, read by the softmax warps up to two blocks (or three short units) later:
+    // Written by the K warps, read by the softmax and issuing warps up to two blocks (or three short units) later:
     // four slots each, the block's or the unit's number modulo 4.
     __shared__ float coef[4][kRows];                      // t = s * coef
     __shared__ unsigned present[4][4];                    // by K warp: which of its two tiles are there
+    __shared__ unsigned what[4];                          // the block: first of a unit's, a later one, or none left
     __shared__ int drafted[4][kTreeMax];                  // places of the drafted tokens
     __shared__ float tops[2][2][kRows];                   // by parity and half: what the halves of a row exchange
 
@@ -705,12 +713,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                         write_v<D, kFormat>(dst, raw[x], row0, lane);
                     }
                 }
-                if (is_k && lane == 0) present[it & 3][w] = there;
+                if (is_k && lane == 0) {
+                    present[it & 3][w] = there;
+                    if (w == 0) what[it & 3] = v == run.v0 ? kFirst : kNext;
+                }
                 fence_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(is_k ? k_full(b) : v_full(b));
                 if (v + 1 < run.v1) load(v + 1);
             }
+        }
+        if (ok && is_k) {                                 // no more blocks
+            ok = mbar_wait(k_empty(it % kBufs), ((it / kBufs) & 1) ^ 1, &abort_flag);
+            if (w == 0 && lane == 0) what[it & 3] = kEnd;
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(k_full(it % kBufs));
         }
         if (is_k && w == 0) {                             // the unit that the cut at the CTA's first place goes through
             if (work) run.u = find_unit<L>(a, prefix, c0);
@@ -723,52 +740,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
         }
     } else if (warp == kWarpMma) {
         // ------------------------------------------------------------------------ matrix instructions
-        unsigned it = 0;
-        const uint32_t q_addr = smem_u32(sq), k_addr = smem_u32(sk), v_addr = smem_u32(sv);
-        auto products_s = [&](unsigned n) {               // S of block n
-            const int b = n % kBufs;
-            if (!mbar_wait(k_full(b), (n / kBufs) & 1, &abort_flag)) return false;
+        // descriptors of the regions' first bytes; an offset adds to the address field (16-byte units)
+        const uint64_t q_desc = desc(smem_u32(sq), 16), k_desc = desc(smem_u32(sk), 16), v_desc = desc(smem_u32(sv), kKeys * 128);
+        const bool lead = elect();
+        for (unsigned it = 0, before = kEnd;; ++it) {
+            const int b = it % kBufs;
+            ok = mbar_wait(k_full(b), (it / kBufs) & 1, &abort_flag);
+            if (!ok) break;
             tc_after();
-            if (lane == 0) {
+            const unsigned now = what[it & 3];
+            if (now != kEnd) {                            // S of this block
+                if (lead) {
+                    const uint64_t kd = k_desc + b * (kRegion >> 4);
+                    const uint32_t d = tmem + 128 * (it & 1);
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    const uint32_t at = (x >> 2) * (kKeys * 128) + (x & 3) * 32;
-                    mma_ss(tmem + 128 * (n & 1), desc(q_addr + at, 16), desc(k_addr + b * kRegion + at, 16), idesc(kKeys, false), x > 0);
+                    for (int x = 0; x < D / 16; ++x) {
+                        const uint64_t at = ((x >> 2) * (kKeys * 128) + (x & 3) * 32) >> 4;
+                        mma_ss(d, q_desc + at, kd + at, idesc(kKeys, false), x > 0);
+                    }
+                    tc_commit(k_empty(b));
+                    tc_commit(s_full(it & 1));
                 }
-                tc_commit(k_empty(b));
-                tc_commit(s_full(n & 1));
+                __syncwarp();
             }
-            __syncwarp();
-            return true;
-        };
-        auto products_o = [&](unsigned n, bool first) {   // O of block n
-            const int b = n % kBufs;
-            if (!mbar_wait(v_full(b), (n / kBufs) & 1, &abort_flag)) return false;
-            if (!mbar_wait(p_full(n & 1), n >> 1 & 1, &abort_flag)) return false;
-            tc_after();
-            if (lane == 0) {
+            if (before != kEnd) {                         // O of the one before
+                const unsigned n = it - 1;
+                const int c = n % kBufs;
+                ok = mbar_wait(v_full(c), (n / kBufs) & 1, &abort_flag) && mbar_wait(p_full(n & 1), n >> 1 & 1, &abort_flag);
+                if (!ok) break;
+                tc_after();
+                if (lead) {
+                    const uint64_t vd = v_desc + c * (kRegion >> 4);
+                    const uint32_t pa = tmem + 128 * (n & 1);
 #pragma unroll
-                for (int x = 0; x < kKeys / 16; ++x)
-                    mma_ts(tmem + kColO, tmem + 128 * (n & 1) + 8 * x, desc(v_addr + b * kRegion + x * 2048, kKeys * 128),
-                           idesc(D, true), !first || x > 0);
-                tc_commit(v_empty(b));
-                tc_commit(o_done);
+                    for (int x = 0; x < kKeys / 16; ++x)
+                        mma_ts(tmem + kColO, pa + 8 * x, vd + x * (2048 >> 4), idesc(D, true), x > 0 || before != kFirst);
+                    tc_commit(v_empty(c));
+                    tc_commit(o_done);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            return true;
-        };
-        bool pending = false, pending_first = false;      // O of block it - 1 is still to be issued
-        while (ok && next_run(run)) {
-            for (int v = run.v0; v < run.v1 && ok; ++v, ++it) {
-                ok = products_s(it);
-                if (ok && pending) ok = products_o(it - 1, pending_first);
-                pending = true;
-                pending_first = v == run.v0;
-            }
+            if (now == kEnd) break;
+            before = now;
         }
-        if (ok && pending) ok = products_o(it - 1, pending_first);
         if (!ok) {                                        // what was issued still reads shared memory
-            if (lane == 0) tc_commit(drain);
+            if (lead) tc_commit(drain);
             mbar_wait(drain, 0, &abort_flag);
         }
     }
