@@ -6,9 +6,10 @@
 // in blocks of 128.  Per block S = Q K^T (128 x 128 x D, both operands in shared memory, fp32 in
 // tensor memory), P = 2^(t - m) as f16 back into tensor memory in the place of S, O += P V (128 x D
 // x 128, P from tensor memory, V from shared memory with the head dim contiguous).  One CTA per SM:
-//   warps 0-7   softmax: two threads per row, 64 keys each, which exchange their maxima through
-//               shared memory; O is rescaled in tensor memory only when a row's maximum has grown
-//               past the headroom
+//   warps 0-7   softmax: one row per thread, the two warpgroups taking turns with the blocks, so
+//               that two blocks are under way; a block's reference follows from the one before
+//               (handed over in shared memory) and O is rescaled in tensor memory only when a row's
+//               maximum has grown past the headroom
 //   warps 8-11  K: codes -> f16 in the 128-byte swizzled layout; at a unit's start also Q
 //   warps 12-15 V: the same
 //   warp 16     issues the matrix instructions: S of block j + 1 before O of block j, so the tensor
@@ -34,7 +35,7 @@ namespace {
 constexpr int kKeys = 128, kRows = 128;
 constexpr int kThreads = 20 * 32;
 constexpr int kWarpK = 8, kWarpV = 12, kWarpMma = 16;      // first warps of the roles after the softmax's
-constexpr long kWaitLimit = 1L << 22;
+constexpr int kWaitLimit = 1 << 20;
 constexpr float kLeast = 1.2e-38f;
 constexpr unsigned kFirst = 0, kNext = 1, kEnd = 2;
 using TilesLine = Line<kKeys, kRows, 1, 4, 3, 16>;
@@ -55,12 +56,12 @@ __device__ __forceinline__ void mbar_arrive(uint32_t b) {
 // limit is hit or a role gave up.
 __device__ __forceinline__ bool mbar_wait(uint32_t b, uint32_t parity, volatile int* abort_flag) {
     bool done = false;
-    for (long it = 0; it < kWaitLimit && !done; ++it) {
-        uint32_t ok;
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+    for (int it = 0; it < kWaitLimit && !done; ++it) {
+        uint32_t ok;                                       // suspends for up to 2 us
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
                      "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(b), "r"(parity) : "memory");
         done = ok != 0;
-        if (!done && (it & 255) == 255 && *abort_flag) break;
+        if (!done && *abort_flag) break;
     }
     done = __all_sync(0xffffffffu, done);
     if (!done) *abort_flag = 1;
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     uint8_t* sk = smem + kRegion;
     uint8_t* sv = sk + kBufs * kRegion;
     __shared__ long long prefix[kMaxSeqs + 1], scratch[kThreads / 32];
-    __shared__ __align__(8) uint64_t bars[4 * 2 + 2 + 2 + 2 + 8];
+    __shared__ __align__(8) uint64_t bars[28];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int abort_flag;
     // Written by the K warps, read by the softmax and issuing warps up to two blocks (or three short units) later:
@@ -354,19 +355,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     __shared__ unsigned present[4][4];                    // by K warp: which of its two tiles are there
     __shared__ unsigned what[4];                          // the block: first of a unit's, a later one, or none left
     __shared__ int drafted[4][kTreeMax];                  // places of the drafted tokens
-    __shared__ float tops[2][2][kRows];                   // by parity and half: what the halves of a row exchange
+    __shared__ float refs[2][kRows];                      // by block parity: the rows' references
+    __shared__ float halves[2][2][kRows];                 // by unit parity and warpgroup: the rows' sums
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t b0 = smem_u32(&bars[0]);
-    // K full/empty, V full/empty by buffer; S full, P full by parity; O done
+    // K full/empty, V full/empty by buffer; S full, P full, O done by the block's parity; the softmax
+    // warps' references and sums; O read at a unit's end
     auto k_full = [&](int b) { return b0 + 8 * b; };
     auto k_empty = [&](int b) { return b0 + 16 + 8 * b; };
     auto v_full = [&](int b) { return b0 + 32 + 8 * b; };
     auto v_empty = [&](int b) { return b0 + 48 + 8 * b; };
     auto s_full = [&](int b) { return b0 + 64 + 8 * b; };
     auto p_full = [&](int b) { return b0 + 80 + 8 * b; };
-    const uint32_t o_done = b0 + 96, drain = b0 + 104;
-    auto x_full = [&](int pair, int p) { return b0 + 112 + 16 * pair + 8 * p; };    // the halves of 32 rows
+    auto o_done = [&](int b) { return b0 + 96 + 8 * b; };
+    auto m_full = [&](int quad, int b) { return b0 + 112 + 16 * quad + 8 * b; };    // by 32 rows
+    auto l_full = [&](int quad) { return b0 + 176 + 8 * quad; };
+    const uint32_t o_free = b0 + 208, drain = b0 + 216;
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(k_full(b), 4);
@@ -374,11 +379,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             mbar_init(v_full(b), 4);
             mbar_init(v_empty(b), 1);
             mbar_init(s_full(b), 1);
-            mbar_init(p_full(b), 8);
+            mbar_init(p_full(b), 4);
+            mbar_init(o_done(b), 1);
+            for (int q = 0; q < 4; ++q) mbar_init(m_full(q, b), 1);
         }
-        mbar_init(o_done, 1);
+        for (int q = 0; q < 4; ++q) mbar_init(l_full(q), 2);
+        mbar_init(o_free, 8);
         mbar_init(drain, 1);
-        for (int x = 0; x < 8; ++x) mbar_init(x_full(x >> 1, x & 1), 2);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -418,21 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
     if (warp < kWarpK) {
         // ------------------------------------------------------------------------ softmax
-        const int row = 32 * (warp & 3) + lane;           // of the unit's 128
-        const int half = warp >> 2;                       // keys 64 half .. of a block, dims D/2 half .. of O
-        const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        unsigned it = 0, xn = 0;
-        // y of the row's other half for x of this one
-        auto exchange = [&](float x, float& y) {
-            const int p = xn & 1;
-            tops[p][half][row] = x;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(x_full(warp & 3, p));
-            if (!mbar_wait(x_full(warp & 3, p), xn >> 1 & 1, &abort_flag)) return false;
-            ++xn;
-            y = tops[p][half ^ 1][row];
-            return true;
-        };
+        const int quad = warp & 3, wg = warp >> 2;        // the warpgroup takes the blocks of its parity
+        const int row = 32 * quad + lane;                 // of the unit's 128
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * quad) << 16);
+        unsigned it = 0;
         for (int un = 0; ok && next_run(run); ++un) {
             const SeqInfo& si = run.u.si;
             const int base = si.len - si.n, grow = run.u.r * kRows + row;
@@ -443,19 +439,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             const int all_low = a.window > 0 ? (int)max((long long)(a.tree ? base + si.n : base + run.u.rt.i1) - a.window + 1, 0LL) : 0;
             // the reference is kept in units of s, so that s - m is exact near it however large t is
             float m = kNoRef, c = 0.f;
-            f32x2 l2 = pair(0.f, 0.f);                    // two halves of the sum of weights
+            f32x2 l2 = pair(0.f, 0.f);                    // the sum of this warpgroup's weights, in two halves
+            const unsigned it0 = it;
+            // the reference that the block before was weighed with
+            auto take_ref = [&](unsigned n) {
+                if (!mbar_wait(m_full(quad, n & 1), n >> 1 & 1, &abort_flag)) return false;
+                const float now = refs[n & 1][row];
+                if (now != m) {
+                    const float f = m == kNoRef ? 0.f : ex2((m - now) * c);
+                    l2 = mul2(l2, pair(f, f));
+                    m = now;
+                }
+                return true;
+            };
             for (int v = run.v0; v < run.v1; ++v, ++it) {
                 const int b = it & 1;
+                if (b != wg) continue;
                 if (!mbar_wait(s_full(b), it >> 1 & 1, &abort_flag)) { ok = false; break; }
                 tc_after();
-                if (v == run.v0) c = coef[un & 3][row];
+                c = coef[un & 3][row];
                 const uint32_t s_addr = lane_addr + 128 * b;
                 const int j0 = run.u.rt.block(v) * kKeys;
                 unsigned there = 0;                       // the block's tiles
 #pragma unroll
                 for (int w = 0; w < 4; ++w) there |= present[it & 3][w] << (2 * w);
                 const bool edge = there != 255u || j0 + kKeys - 1 > all_lim || (j0 < all_low && j0 + kKeys > a.n_sink) || run.u.rt.empty;
-                // which of the 32 keys from j on the row sees
+                // which of 32 keys the row sees
                 auto mask_of = [&](int ch) {
                     const int j = j0 + 32 * ch;
                     auto below = [&](int x) {             // bits of keys < x
@@ -482,66 +491,85 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     const unsigned t2 = there >> (2 * ch);
                     return ok_bits & ((t2 & 1 ? 0xFFFFu : 0u) | (t2 & 2 ? 0xFFFF0000u : 0u));
                 };
-                uint32_t s[2][32];
-                tmem_ld32(s_addr + 64 * half, s[0]);
-                tmem_ld32(s_addr + 64 * half + 32, s[1]);
-                unsigned seen[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-                if (edge) {
-                    seen[0] = mask_of(2 * half);
-                    seen[1] = mask_of(2 * half + 1);
-                }
-                tmem_wait_ld();
-                // the row's largest s
+                // the row's largest s.  Keys that are not seen get -inf, whatever their bytes gave (weight
+                // 0: c is positive), in tensor memory too.
                 float top = kNoRef;
                 if (!edge) {
+                    uint32_t s[2][32];
+                    tmem_ld32(s_addr, s[0]);
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) top = fmaxf(top, __uint_as_float(s[e >> 5][e & 31]));
-                } else {
+                    for (int ch = 0; ch < 4; ++ch) {
+                        tmem_wait_ld();
+                        if (ch < 3) tmem_ld32(s_addr + 32 * (ch + 1), s[(ch + 1) & 1]);
+                        float x = kNoRef, y = kNoRef;
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) {
-                        // a key that is not seen gets -inf, whatever its bytes gave (weight 0: c is not negative)
-                        if (!(seen[e >> 5] >> (e & 31) & 1)) s[e >> 5][e & 31] = 0xFF800000u;
-                        top = fmaxf(top, __uint_as_float(s[e >> 5][e & 31]));
-                    }
-                }
-                float other;                              // exchanged: also, all of the rows' S is read, P may go over it
-                if (!exchange(top, other)) { ok = false; break; }
-                top = fmaxf(top, other);
-                // O of the block before is complete (waited for at every block, so that no phase is missed)
-                if (it > 0 && !mbar_wait(o_done, (it - 1) & 1, &abort_flag)) { ok = false; break; }
-                const bool raise = top > m && (m == kNoRef || (top - m) * c > kHeadroom);
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float mm = fmaxf(m, top), f = m == kNoRef ? 0.f : ex2((m - mm) * c);
-                    m = mm;
-                    l2 = mul2(l2, pair(f, f));
-                    if (v > run.v0) {
-                        tc_after();
-#pragma unroll 1
-                        for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(lane_addr + kColO + x, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st32(lane_addr + kColO + x, o);
+                        for (int e = 0; e < 32; e += 4) {
+                            x = fmaxf(x, fmaxf(__uint_as_float(s[ch & 1][e]), __uint_as_float(s[ch & 1][e + 1])));
+                            y = fmaxf(y, fmaxf(__uint_as_float(s[ch & 1][e + 2]), __uint_as_float(s[ch & 1][e + 3])));
                         }
+                        top = fmaxf(top, fmaxf(x, y));
+                    }
+                } else {
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t s[32];
+                        const unsigned seen = mask_of(ch);
+                        __syncwarp();
+                        tmem_ld32(s_addr + 32 * ch, s);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            if (!(seen >> e & 1)) s[e] = 0xFF800000u;
+                            top = fmaxf(top, __uint_as_float(s[e]));
+                        }
+                        tmem_st32(s_addr + 32 * ch, s);
+                    }
+                    tmem_wait_st();
+                }
+                if (it > it0 && !take_ref(it - 1)) { ok = false; break; }
+                const bool raise = top > m && (m == kNoRef || (top - m) * c > kHeadroom);
+                float f = 1.f;
+                if (raise) {
+                    f = m == kNoRef ? 0.f : ex2((m - top) * c);
+                    m = top;
+                    l2 = mul2(l2, pair(f, f));
+                }
+                refs[b][row] = m;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(m_full(quad, b));
+                if (__any_sync(0xffffffffu, raise) && it > it0) {
+                    if (!mbar_wait(o_done(b ^ 1), (it - 1) >> 1 & 1, &abort_flag)) { ok = false; break; }
+                    tc_after();
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(lane_addr + kColO + x, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(lane_addr + kColO + x, o);
                     }
                 }
                 // a row that has seen nothing keeps finite differences: its s are -inf
                 const float ref = m == kNoRef ? 0.f : m;
                 const f32x2 m2 = pair(-ref, -ref), c2 = pair(c, c), head2 = pair(kHeadroom, kHeadroom);
+                // P over S: 32 columns of S become 16 of f16 pairs, over columns that have been read
+                uint32_t s[2][32];
+                tmem_ld32(s_addr, s[0]);
 #pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
+                for (int ch = 0; ch < 4; ++ch) {
+                    tmem_wait_ld();
+                    if (ch < 3) tmem_ld32(s_addr + 32 * (ch + 1), s[(ch + 1) & 1]);
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float2 x = unpair(fma2(add2(pair(__uint_as_float(s[ch][e]), __uint_as_float(s[ch][e + 1])), m2), c2, head2));
+                        float2 x = unpair(fma2(add2(pair(__uint_as_float(s[ch & 1][e]), __uint_as_float(s[ch & 1][e + 1])), m2), c2, head2));
                         x.x = ex2(x.x);
                         x.y = ex2(x.y);
                         l2 = add2(l2, pair(x.x, x.y));
                         p[e >> 1] = pack_f16(x.x, x.y);
                     }
-                    tmem_st16(s_addr + 32 * half + 16 * ch, p);
+                    tmem_st16(s_addr + 16 * ch, p);
                 }
                 tmem_wait_st();
                 tc_before();
@@ -549,19 +577,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                 if (lane == 0) mbar_arrive(p_full(b));
             }
             if (!ok) break;
-            // the unit's sums
-            if (!mbar_wait(o_done, (it - 1) & 1, &abort_flag)) { ok = false; break; }
-            tc_after();
-            float l = unpair(l2).x + unpair(l2).y, other;
-            if (!exchange(l, other)) { ok = false; break; }
-            l += other;
+            // the unit's sums: the last block's reference, both warpgroups' weights
+            c = coef[un & 3][row];
+            if (((it - 1) & 1) != wg && !take_ref(it - 1)) { ok = false; break; }
+            halves[un & 1][wg][row] = unpair(l2).x + unpair(l2).y;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(l_full(quad));
+            if (!mbar_wait(l_full(quad), un & 1, &abort_flag)) { ok = false; break; }
+            const float l = halves[un & 1][0][row] + halves[un & 1][1][row];
             if (m != kNoRef) m *= c;
+            if (!mbar_wait(o_done((it - 1) & 1), (it - 1) >> 1 & 1, &abort_flag)) { ok = false; break; }
+            tc_after();
             const int i = grow / a.G;
             const bool on = i < si.n, done = run.v0 == 0 && run.v1 == run.u.rt.nt;
             float* out = partial<D, kRows>(a, 2 * cta + (run.v0 > 0 ? 0 : 1));
-            if (on && !done && half == 0) reinterpret_cast<float2*>(out)[row] = make_float2(m, l);
+            if (on && !done && wg == 0) reinterpret_cast<float2*>(out)[row] = make_float2(m, l);
 #pragma unroll 1
-            for (int x = half * (D / 2); x < (half + 1) * (D / 2); x += 32) {
+            for (int x = wg * (D / 2); x < (wg + 1) * (D / 2); x += 32) {
                 uint32_t o[32];
                 __syncwarp();
                 tmem_ld32(lane_addr + kColO + x, o);
@@ -582,8 +614,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     }
                 }
             }
+            // O is free for the next unit once both warpgroups have read their halves
+            tc_before();
             __syncwarp();
-            tc_before();                                  // the next unit's first P follows these reads
+            if (lane == 0) mbar_arrive(o_free);
         }
     } else if (warp < kWarpMma) {
         // ------------------------------------------------------------------------ K (and Q), V
@@ -743,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
         // descriptors of the regions' first bytes; an offset adds to the address field (16-byte units)
         const uint64_t q_desc = desc(smem_u32(sq), 16), k_desc = desc(smem_u32(sk), 16), v_desc = desc(smem_u32(sv), kKeys * 128);
         const bool lead = elect();
+        unsigned units = 0;
         for (unsigned it = 0, before = kEnd;; ++it) {
             const int b = it % kBufs;
             ok = mbar_wait(k_full(b), (it / kBufs) & 1, &abort_flag);
@@ -767,6 +802,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                 const unsigned n = it - 1;
                 const int c = n % kBufs;
                 ok = mbar_wait(v_full(c), (n / kBufs) & 1, &abort_flag) && mbar_wait(p_full(n & 1), n >> 1 & 1, &abort_flag);
+                if (ok && before == kFirst && units++ > 0)    // the unit before has been read out of O
+                    ok = mbar_wait(o_free, units & 1, &abort_flag);
                 if (!ok) break;
                 tc_after();
                 if (lead) {
@@ -776,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     for (int x = 0; x < kKeys / 16; ++x)
                         mma_ts(tmem + kColO, pa + 8 * x, vd + x * (2048 >> 4), idesc(D, true), x > 0 || before != kFirst);
                     tc_commit(v_empty(c));
-                    tc_commit(o_done);
+                    tc_commit(o_done(n & 1));
                 }
                 __syncwarp();
             }
