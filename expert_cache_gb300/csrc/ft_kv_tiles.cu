@@ -179,9 +179,13 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
     return d;
 }
 
-// 16-byte chunk c (8 dims) of row r of a [128 rows][D] operand.
-__device__ __forceinline__ void store_chunk(uint8_t* base, int r, int c, uint4 v) {
-    *reinterpret_cast<uint4*>(base + (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+__device__ __forceinline__ void st_shared(uint32_t at, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// Byte of 16-byte chunk c (8 dims) of row r of a [128 rows][D] operand.  Chunks that differ in the low
+// three bits of c differ in the same bits of (byte >> 4): at(r, c ^ z) = at(r, c) ^ (z << 4) for z < 8.
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // A lane's raw bytes of a tile's K or V.
@@ -211,8 +215,10 @@ __device__ __forceinline__ void load_k(Raw<D, kFormat>& r, const uint8_t* tile, 
     }
 }
 template <int D, int kFormat>
-__device__ __forceinline__ void write_k(uint8_t* base, const Raw<D, kFormat>& r, int row0, int lane) {
+__device__ __forceinline__ void write_k(uint32_t base, const Raw<D, kFormat>& r, int row0, int lane) {
     const int g = lane >> 2, t = lane & 3;
+    // the lane's first chunk of row 8 v + g: rows 8 apart are 1024 bytes apart
+    const uint32_t at = base + chunk_at(row0 + g, t * (D / 32));
     if constexpr (kFormat == FT_KV_NVFP4) {
         if constexpr (D == 64) {
             const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
@@ -220,25 +226,25 @@ __device__ __forceinline__ void write_k(uint8_t* base, const Raw<D, kFormat>& r,
             for (int v = 0; v < 2; ++v) {
                 const uint32_t s2 = scale_pair(r.s.x >> (8 * v) & 255u);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) store_chunk(base, row0 + 8 * v + g, t * 2 + i, unpack_e2m1(w[2 * v + i], s2));
+                for (int i = 0; i < 2; ++i) st_shared((at ^ (i << 4)) + 1024 * v, unpack_e2m1(w[2 * v + i], s2));
             }
         } else {
             // words of a vector swapped in pairs for half of the lanes
             const bool pairs = D == 128 ? t >> 1 : t & 1;
+            const uint32_t p = pairs ? 1 : 0;
 #pragma unroll
             for (int x = 0; x < r.kVecs; ++x) {
                 const int v = D == 128 ? x : x >> 1;
-                const int half = D == 128 ? 0 : (x & 1) ^ (t >> 1);       // which 32 dims of the lane's
+                const uint32_t half = D == 128 ? 0 : (x & 1) ^ (t >> 1);  // which 32 dims of the lane's
                 const uint32_t a0 = pairs ? r.v[x].z : r.v[x].x, a1 = pairs ? r.v[x].w : r.v[x].y;
                 const uint32_t b0 = pairs ? r.v[x].x : r.v[x].z, b1 = pairs ? r.v[x].y : r.v[x].w;
-                const uint32_t sw = D == 128 ? r.s.x >> (16 * v) : (v ? r.s.y : r.s.x) >> (16 * half);
-                const int p = pairs ? 1 : 0;
+                const uint32_t sw = (D == 128 ? r.s.x >> (16 * v) : (v ? r.s.y : r.s.x) >> (16 * half)) & 0xFFFFu;
                 const uint32_t sa = scale_pair(sw >> (8 * p) & 255u), sb = scale_pair(sw >> (8 * (p ^ 1)) & 255u);
-                const int c = t * (D / 32) + half * 4, row = row0 + 8 * v + g;
-                store_chunk(base, row, c + 2 * p, unpack_e2m1(a0, sa));
-                store_chunk(base, row, c + 2 * p + 1, unpack_e2m1(a1, sa));
-                store_chunk(base, row, c + 2 * (p ^ 1), unpack_e2m1(b0, sb));
-                store_chunk(base, row, c + 2 * (p ^ 1) + 1, unpack_e2m1(b1, sb));
+                const uint32_t c = at ^ (half << 6) ^ (p << 5);
+                st_shared(c + 1024 * v, unpack_e2m1(a0, sa));
+                st_shared((c ^ 16) + 1024 * v, unpack_e2m1(a1, sa));
+                st_shared((c ^ 32) + 1024 * v, unpack_e2m1(b0, sb));
+                st_shared((c ^ 48) + 1024 * v, unpack_e2m1(b1, sb));
             }
         }
     } else {
@@ -246,9 +252,9 @@ __device__ __forceinline__ void write_k(uint8_t* base, const Raw<D, kFormat>& r,
         constexpr int kPer = D / 64;                                      // vectors of a token
 #pragma unroll
         for (int x = 0; x < r.kVecs; ++x) {
-            const int y = x ^ swap, row = row0 + 8 * (x / kPer) + g, c = t * (D / 32) + (y % kPer) * 2;
-            store_chunk(base, row, c, unpack_e4m3(r.v[x].x, r.v[x].y));
-            store_chunk(base, row, c + 1, unpack_e4m3(r.v[x].z, r.v[x].w));
+            const uint32_t c = at ^ ((((x ^ swap) % kPer) * 2) << 4);
+            st_shared(c + 1024 * (x / kPer), unpack_e4m3(r.v[x].x, r.v[x].y));
+            st_shared((c ^ 16) + 1024 * (x / kPer), unpack_e4m3(r.v[x].z, r.v[x].w));
         }
     }
 }
@@ -268,15 +274,17 @@ __device__ __forceinline__ void load_v(Raw<D, kFormat>& r, const uint8_t* tile, 
     }
 }
 template <int D, int kFormat>
-__device__ __forceinline__ void write_v(uint8_t* base, const Raw<D, kFormat>& r, int row0, int lane) {
+__device__ __forceinline__ void write_v(uint32_t base, const Raw<D, kFormat>& r, int row0, int lane) {
     const int g = lane >> 2, t = lane & 3;
     const bool odd = g & 1;
-    auto row_of = [&](int q) { return row0 + 2 * t + (q & 1) + 8 * (q >> 1); };
+    // the lane's first chunk (odd lanes: second) of tokens 2t and 2t + 1; 8 tokens are 1024 bytes
+    const uint32_t flip = odd && D > 64 ? 16 : 0;
+    const uint32_t at[2] = {base + (chunk_at(row0 + 2 * t, g * (D / 64)) ^ flip), base + (chunk_at(row0 + 2 * t + 1, g * (D / 64)) ^ flip)};
     if constexpr (kFormat == FT_KV_NVFP4) {
         if constexpr (D == 64) {
             const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) store_chunk(base, row_of(q), g, unpack_e2m1(w[q], scale_pair(r.s.x >> (8 * q) & 255u)));
+            for (int q = 0; q < 4; ++q) st_shared(at[q & 1] + 1024 * (q >> 1), unpack_e2m1(w[q], scale_pair(r.s.x >> (8 * q) & 255u)));
         } else if constexpr (D == 128) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -284,10 +292,9 @@ __device__ __forceinline__ void write_v(uint8_t* base, const Raw<D, kFormat>& r,
                                        odd ? r.v[x].z : r.v[x].w};
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const int q = 2 * x + y;
-                    const uint32_t s2 = scale_pair(r.s.x >> (8 * q) & 255u);
-                    store_chunk(base, row_of(q), 2 * g + (odd ? 1 : 0), unpack_e2m1(w[2 * y], s2));
-                    store_chunk(base, row_of(q), 2 * g + (odd ? 0 : 1), unpack_e2m1(w[2 * y + 1], s2));
+                    const uint32_t s2 = scale_pair(r.s.x >> (8 * (2 * x + y)) & 255u);
+                    st_shared(at[y] + 1024 * x, unpack_e2m1(w[2 * y], s2));
+                    st_shared((at[y] ^ 16) + 1024 * x, unpack_e2m1(w[2 * y + 1], s2));
                 }
             }
         } else {
@@ -298,8 +305,8 @@ __device__ __forceinline__ void write_v(uint8_t* base, const Raw<D, kFormat>& r,
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const uint32_t s2 = scale_pair((b ? r.s.y : r.s.x) >> (8 * q) & 255u);
-                    store_chunk(base, row_of(q), 4 * g + 2 * b + (odd ? 1 : 0), unpack_e2m1(w[2 * b], s2));
-                    store_chunk(base, row_of(q), 4 * g + 2 * b + (odd ? 0 : 1), unpack_e2m1(w[2 * b + 1], s2));
+                    st_shared((at[q & 1] ^ (b << 5)) + 1024 * (q >> 1), unpack_e2m1(w[2 * b], s2));
+                    st_shared((at[q & 1] ^ (b << 5) ^ 16) + 1024 * (q >> 1), unpack_e2m1(w[2 * b + 1], s2));
                 }
             }
         }
@@ -308,13 +315,14 @@ __device__ __forceinline__ void write_v(uint8_t* base, const Raw<D, kFormat>& r,
         for (int x = 0; x < r.kVecs; ++x) {
             const uint4 v = r.v[x];
             if constexpr (D == 64) {
-                store_chunk(base, row_of(2 * x), g, unpack_e4m3(v.x, v.y));
-                store_chunk(base, row_of(2 * x + 1), g, unpack_e4m3(v.z, v.w));
+                st_shared(at[0] + 1024 * x, unpack_e4m3(v.x, v.y));
+                st_shared(at[1] + 1024 * x, unpack_e4m3(v.z, v.w));
             } else {
                 constexpr int kPer = D / 128;                             // vectors of a token
-                const int c = g * (D / 64) + x % kPer * 2, row = row_of(x / kPer);
-                store_chunk(base, row, c + (odd ? 1 : 0), unpack_e4m3(odd ? v.z : v.x, odd ? v.w : v.y));
-                store_chunk(base, row, c + (odd ? 0 : 1), unpack_e4m3(odd ? v.x : v.z, odd ? v.y : v.w));
+                const int q = x / kPer;
+                const uint32_t c = (at[q & 1] ^ ((x % kPer) << 5)) + 1024 * (q >> 1);
+                st_shared(c, unpack_e4m3(odd ? v.z : v.x, odd ? v.w : v.y));
+                st_shared((at[q & 1] ^ ((x % kPer) << 5) ^ 16) + 1024 * (q >> 1), unpack_e4m3(odd ? v.x : v.z, odd ? v.y : v.w));
             }
         }
     }
@@ -325,6 +333,28 @@ __device__ __forceinline__ void clear(Raw<D, kFormat>& r) {
     for (int x = 0; x < r.kVecs; ++x) r.v[x] = make_uint4(0, 0, 0, 0);
     r.s = make_uint2(0, 0);
 }
+
+// Zeroes the V of the lane's tokens from n on (n below 16).
+template <int D, int kFormat>
+__device__ __forceinline__ void zero_past(Raw<D, kFormat>& r, int n, int t) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (2 * t + (q & 1) + 8 * (q >> 1) >= n) {
+            if constexpr (kFormat == FT_KV_NVFP4) {
+                r.s.x &= ~(255u << (8 * q));
+                r.s.y &= ~(255u << (8 * q));
+            } else if constexpr (D == 64) {
+                if (q & 1) r.v[q >> 1].z = r.v[q >> 1].w = 0;
+                else r.v[q >> 1].x = r.v[q >> 1].y = 0;
+            } else {
+#pragma unroll
+                for (int y = 0; y < D / 128; ++y) r.v[q * (D / 128) + y] = make_uint4(0, 0, 0, 0);
+            }
+        }
+}
+
+// Tiles whose codes a K or V warp loads ahead into registers.
+constexpr int ahead(int D, int format) { return D == 256 && format == FT_KV_FP8 ? 1 : 2; }
 
 // What a CTA does of one unit: its blocks [v0, v1).
 struct Run {
@@ -337,14 +367,11 @@ struct Run {
 template <int D, int kFormat>
 __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a) {
     using L = TilesLine;
-    constexpr int kBufs = bufs(D), kRegion = region(D);
+    constexpr int kBufs = bufs(D), kRegion = region(D), kAhead = ahead(D, kFormat);
     constexpr KvTile kT = kv_tile(D, kFormat);
     constexpr uint32_t kColO = 256;                       // S and P: columns 0..127 and 128..255
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    uint8_t* sq = smem;
-    uint8_t* sk = smem + kRegion;
-    uint8_t* sv = sk + kBufs * kRegion;
+    const uint32_t sq = (smem_u32(smem_raw) + 1023) & ~1023u, sk = sq + kRegion, sv = sk + kBufs * kRegion;
     __shared__ long long prefix[kMaxSeqs + 1], scratch[kThreads / 32];
     __shared__ __align__(8) uint64_t bars[28];
     __shared__ uint32_t tmem_base;
@@ -360,14 +387,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t b0 = smem_u32(&bars[0]);
-    // K full/empty, V full/empty by buffer; S full, P full, O done by the block's parity; the softmax
+    // K full/empty, V empty by buffer; S full, V and P full, O done by the block's parity; the softmax
     // warps' references and sums; O read at a unit's end
     auto k_full = [&](int b) { return b0 + 8 * b; };
     auto k_empty = [&](int b) { return b0 + 16 + 8 * b; };
-    auto v_full = [&](int b) { return b0 + 32 + 8 * b; };
     auto v_empty = [&](int b) { return b0 + 48 + 8 * b; };
     auto s_full = [&](int b) { return b0 + 64 + 8 * b; };
-    auto p_full = [&](int b) { return b0 + 80 + 8 * b; };
+    auto vp_full = [&](int b) { return b0 + 80 + 8 * b; };
     auto o_done = [&](int b) { return b0 + 96 + 8 * b; };
     auto m_full = [&](int quad, int b) { return b0 + 112 + 16 * quad + 8 * b; };    // by 32 rows
     auto l_full = [&](int quad) { return b0 + 176 + 8 * quad; };
@@ -376,10 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
         for (int b = 0; b < 2; ++b) {
             mbar_init(k_full(b), 4);
             mbar_init(k_empty(b), 1);
-            mbar_init(v_full(b), 4);
             mbar_init(v_empty(b), 1);
             mbar_init(s_full(b), 1);
-            mbar_init(p_full(b), 4);
+            mbar_init(vp_full(b), 8);
             mbar_init(o_done(b), 1);
             for (int q = 0; q < 4; ++q) mbar_init(m_full(q, b), 1);
         }
@@ -574,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                 tmem_wait_st();
                 tc_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(b));
+                if (lane == 0) mbar_arrive(vp_full(b));
             }
             if (!ok) break;
             // the unit's sums: the last block's reference, both warpgroups' weights
@@ -632,18 +657,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             // keys that some row sees: below hi, from lo on or among the first tokens
             const int hi = run.u.rt.empty ? 0 : a.tree ? si.len : min(si.len, base + run.u.rt.i1 + 1);
             const int lo = a.window > 0 ? (int)max((long long)base + (a.tree ? 0 : run.u.rt.i0) - a.window + 1, 0LL) : 0;
-            // pages of this warp's tiles: lane x holds that of tile (x & 1) of block v0 + 16 * group + (x >> 1)
+            // The warp's tiles of the run in order: tile n is 2w + (n & 1) of block v0 + (n >> 1).  Lane x
+            // holds the page of tile 32 * group + x.
+            const int tiles = 2 * (run.v1 - run.v0);
             int group = -1, page = -1;
-            Raw<D, kFormat> raw[2];
-            unsigned there = 0;
-            auto load = [&](int v) {
-                const int gr = (v - run.v0) >> 4;
-                if (gr != group) {
-                    group = gr;
+            Raw<D, kFormat> raw[kAhead];
+            unsigned have = 0;                            // bit n % 32: tile n is one of the cache's and some row sees a key of it
+            auto load = [&](int n, Raw<D, kFormat>& r) {
+                if (n >= tiles) return;
+                if (n >> 5 != group) {
+                    group = n >> 5;
                     page = -1;
-                    const int mine = run.v0 + 16 * gr + (lane >> 1);
-                    if (mine < run.v1) {
-                        const int tile = run.u.rt.block(mine) * (kKeys / 16) + 2 * w + (lane & 1), key = tile * 16;
+                    const int mine = (n & ~31) + lane;
+                    if (mine < tiles) {
+                        const int tile = run.u.rt.block(run.v0 + (mine >> 1)) * (kKeys / 16) + 2 * w + (mine & 1), key = tile * 16;
                         if (key < hi && (key + 15 >= lo || key < a.n_sink)) {
                             page = table[tile >> per];
                             if (page < 0 || page >= a.kv.n_pages) {
@@ -653,22 +680,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                         }
                     }
                 }
-                there = 0;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int pg = __shfl_sync(0xffffffffu, page, ((v - run.v0) & 15) * 2 + x);
-                    if (pg >= 0) {
-                        there |= 1u << x;
-                        const int tile = run.u.rt.block(v) * (kKeys / 16) + 2 * w + x;
-                        const uint8_t* src = a.kv.pool + ((((size_t)pg * a.kv.hkv + run.u.h) << per) + (tile & ((1 << per) - 1))) * kT.bytes;
-                        if (is_k) load_k<D, kFormat>(raw[x], src, lane);
-                        else load_v<D, kFormat>(raw[x], src, lane);
-                    } else {
-                        clear(raw[x]);
-                    }
+                const int pg = __shfl_sync(0xffffffffu, page, n & 31);
+                have &= ~(1u << (n & 31));
+                if (pg >= 0) {
+                    have |= 1u << (n & 31);
+                    const int tile = run.u.rt.block(run.v0 + (n >> 1)) * (kKeys / 16) + 2 * w + (n & 1);
+                    const uint8_t* src = a.kv.pool + ((((size_t)pg * a.kv.hkv + run.u.h) << per) + (tile & ((1 << per) - 1))) * kT.bytes;
+                    if (is_k) load_k<D, kFormat>(r, src, lane);
+                    else load_v<D, kFormat>(r, src, lane);
+                } else {
+                    clear(r);
                 }
             };
-            load(run.v0);
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) load(x, raw[x]);
             if (is_k) {
                 // Q of the unit: every product of the unit before is through with it
                 if (it > 0 && !mbar_wait(k_empty((it - 1) % kBufs), ((it - 1) / kBufs) & 1, &abort_flag)) { ok = false; break; }
@@ -704,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             o[y] = pack_f16(__uint_as_float(wd[y] << 16) * down, __uint_as_float(wd[y] & 0xFFFF0000u) * down);
-                        store_chunk(sq, row, e * 8 + part, make_uint4(o[0], o[1], o[2], o[3]));
+                        st_shared(sq + chunk_at(row, e * 8 + part), make_uint4(o[0], o[1], o[2], o[3]));
                     }
                 }
             }
@@ -712,49 +737,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                 const int b = it % kBufs;
                 const uint32_t ph = (it / kBufs) & 1;
                 if (!mbar_wait(is_k ? k_empty(b) : v_empty(b), ph ^ 1, &abort_flag)) { ok = false; break; }
-                uint8_t* dst = (is_k ? sk : sv) + b * kRegion;
+                const uint32_t dst = (is_k ? sk : sv) + b * kRegion;
+                const int n0 = 2 * (v - run.v0);
                 const int j0 = run.u.rt.block(v) * kKeys;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int row0 = 32 * w + 16 * x;
+                    Raw<D, kFormat>& r = raw[x % kAhead];
                     if (is_k) {
-                        write_k<D, kFormat>(dst, raw[x], row0, lane);
+                        write_k<D, kFormat>(dst, r, row0, lane);
                     } else {
-                        if (there >> x & 1 && j0 + row0 + 16 > si.len) {
-                            // past the cached tokens the bytes may be anything: zero the lane's tokens there
-                            const int t = lane & 3;
-                            if constexpr (kFormat == FT_KV_NVFP4) {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    if (j0 + row0 + 2 * t + (q & 1) + 8 * (q >> 1) >= si.len) {
-                                        raw[x].s.x &= ~(255u << (8 * q));
-                                        raw[x].s.y &= ~(255u << (8 * q));
-                                    }
-                            } else {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    if (j0 + row0 + 2 * t + (q & 1) + 8 * (q >> 1) >= si.len) {
-                                        if constexpr (D == 64) {
-                                            if (q & 1) raw[x].v[q >> 1].z = raw[x].v[q >> 1].w = 0;
-                                            else raw[x].v[q >> 1].x = raw[x].v[q >> 1].y = 0;
-                                        } else {
-#pragma unroll
-                                            for (int y = 0; y < D / 128; ++y) raw[x].v[q * (D / 128) + y] = make_uint4(0, 0, 0, 0);
-                                        }
-                                    }
-                            }
-                        }
-                        write_v<D, kFormat>(dst, raw[x], row0, lane);
+                        // past the cached tokens the bytes may be anything: zero the lane's tokens there
+                        if (j0 + row0 + 16 > si.len) zero_past<D, kFormat>(r, si.len - j0 - row0, lane & 3);
+                        write_v<D, kFormat>(dst, r, row0, lane);
                     }
+                    load(n0 + x + kAhead, r);
                 }
                 if (is_k && lane == 0) {
-                    present[it & 3][w] = there;
+                    present[it & 3][w] = have >> (n0 & 31) & 3u;
                     if (w == 0) what[it & 3] = v == run.v0 ? kFirst : kNext;
                 }
                 fence_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(is_k ? k_full(b) : v_full(b));
-                if (v + 1 < run.v1) load(v + 1);
+                if (lane == 0) mbar_arrive(is_k ? k_full(b) : vp_full(it & 1));
             }
         }
         if (ok && is_k) {                                 // no more blocks
@@ -775,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     } else if (warp == kWarpMma) {
         // ------------------------------------------------------------------------ matrix instructions
         // descriptors of the regions' first bytes; an offset adds to the address field (16-byte units)
-        const uint64_t q_desc = desc(smem_u32(sq), 16), k_desc = desc(smem_u32(sk), 16), v_desc = desc(smem_u32(sv), kKeys * 128);
+        const uint64_t q_desc = desc(sq, 16), k_desc = desc(sk, 16), v_desc = desc(sv, kKeys * 128);
         const bool lead = elect();
         unsigned units = 0;
         for (unsigned it = 0, before = kEnd;; ++it) {
@@ -801,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             if (before != kEnd) {                         // O of the one before
                 const unsigned n = it - 1;
                 const int c = n % kBufs;
-                ok = mbar_wait(v_full(c), (n / kBufs) & 1, &abort_flag) && mbar_wait(p_full(n & 1), n >> 1 & 1, &abort_flag);
+                ok = mbar_wait(vp_full(n & 1), n >> 1 & 1, &abort_flag);
                 if (ok && before == kFirst && units++ > 0)    // the unit before has been read out of O
                     ok = mbar_wait(o_free, units & 1, &abort_flag);
                 if (!ok) break;
