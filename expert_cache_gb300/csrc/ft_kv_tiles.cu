@@ -10,16 +10,18 @@
 //               that two blocks are under way; a block's reference follows from the one before
 //               (handed over in shared memory) and O is rescaled in tensor memory only when a row's
 //               maximum has grown past the headroom
-//   warps 8-11  K: codes -> f16 in the 128-byte swizzled layout; at a unit's start also Q
-//   warps 12-15 V: the same
-//   warp 16     issues the matrix instructions: S of block j + 1 before O of block j, so the tensor
-//               cores work while the softmax warps do (17-19 only complete its warpgroup)
-// The block starts with 96 registers a thread; the last warpgroup gives up 56 of them, the softmax
-// warpgroups take 16 each and K's and V's 8 (2 * 112 + 2 * 104 + 40 <= 5 * 96).
-// Unpacking a block costs as many issue slots as its softmax, so it has as many warps again; the
-// codes of the next block are loaded into registers before the wait for its buffer.  Within a
-// lane's 16-byte vectors the order of the shared-memory stores is permuted so that the 8 lanes of a
-// store phase hit the 8 banks groups of a swizzle row.
+//   warps 8-15  K: codes -> f16 in the 128-byte swizzled layout, a tile of 16 tokens per warp; at a
+//               unit's start also half of Q
+//   warps 16-23 V: the same, and the other half of Q
+//   warp 24     issues the matrix instructions: S of block j + 1 before O of block j, so the tensor
+//               cores work while the softmax warps do (25-27 only complete its warpgroup)
+// The block starts with 72 registers a thread; the last warpgroup gives up 32 of them and K's and V's
+// 8, the softmax warpgroups take 32 each (8 * 104 + 16 * 64 + 4 * 40 <= 28 * 72 per lane).
+// Unpacking a block costs more issue slots than its softmax and more latency (codes, conversion,
+// store, fence), so it has twice the warps; the codes of a warp's next tile are loaded into
+// registers as soon as it has stored the one before.  Within a lane's 16-byte vectors the order of
+// the shared-memory stores is permuted so that the 8 lanes of a store phase hit the 8 bank groups of
+// a swizzle row.
 // Units are laid on the line of shares like the rows kernel's (a unit's start and end cost about
 // three blocks), so causal and ragged chunks balance; cut units are joined by the second kernel.
 // Every wait is bounded: on expiry the CTA sets FT_DEV_TIMEOUT, leaves its loops and frees its
@@ -33,8 +35,9 @@ namespace ft {
 namespace {
 
 constexpr int kKeys = 128, kRows = 128;
-constexpr int kThreads = 20 * 32;
-constexpr int kWarpK = 8, kWarpV = 12, kWarpMma = 16;      // first warps of the roles after the softmax's
+constexpr int kWarpK = 8, kWarpV = 16, kWarpMma = 24;      // first warps of the roles after the softmax's
+constexpr int kThreads = (kWarpMma + 4) * 32;
+constexpr int kTiles = kKeys / kKvTile;                    // of a block: one per K warp and one per V warp
 constexpr int kWaitLimit = 1 << 20;
 constexpr float kLeast = 1.2e-38f;
 constexpr unsigned kFirst = 0, kNext = 1, kEnd = 2;
@@ -353,9 +356,6 @@ __device__ __forceinline__ void zero_past(Raw<D, kFormat>& r, int n, int t) {
         }
 }
 
-// Tiles whose codes a K or V warp loads ahead into registers.
-constexpr int ahead(int D, int format) { return D == 256 && format == FT_KV_FP8 ? 1 : 2; }
-
 // What a CTA does of one unit: its blocks [v0, v1).
 struct Run {
     Unit u;
@@ -367,7 +367,7 @@ struct Run {
 template <int D, int kFormat>
 __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a) {
     using L = TilesLine;
-    constexpr int kBufs = bufs(D), kRegion = region(D), kAhead = ahead(D, kFormat);
+    constexpr int kBufs = bufs(D), kRegion = region(D);
     constexpr KvTile kT = kv_tile(D, kFormat);
     constexpr uint32_t kColO = 256;                       // S and P: columns 0..127 and 128..255
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     // Written by the K warps, read by the softmax and issuing warps up to two blocks (or three short units) later:
     // four slots each, the block's or the unit's number modulo 4.
     __shared__ float coef[4][kRows];                      // t = s * coef
-    __shared__ unsigned present[4][4];                    // by K warp: which of its two tiles are there
+    __shared__ unsigned char present[4][kTiles];          // the tile is one of the cache's and some row sees a key of it
     __shared__ unsigned what[4];                          // the block: first of a unit's, a later one, or none left
     __shared__ int drafted[4][kTreeMax];                  // places of the drafted tokens
     __shared__ float refs[2][kRows];                      // by block parity: the rows' references
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t b0 = smem_u32(&bars[0]);
-    // K full/empty, V empty by buffer; S full, V and P full, O done by the block's parity; the softmax
+    // K full/empty, V empty by buffer; Q full; S full, V and P full, O done by the block's parity; the softmax
     // warps' references and sums; O read at a unit's end
     auto k_full = [&](int b) { return b0 + 8 * b; };
     auto k_empty = [&](int b) { return b0 + 16 + 8 * b; };
@@ -397,19 +397,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     auto o_done = [&](int b) { return b0 + 96 + 8 * b; };
     auto m_full = [&](int quad, int b) { return b0 + 112 + 16 * quad + 8 * b; };    // by 32 rows
     auto l_full = [&](int quad) { return b0 + 176 + 8 * quad; };
-    const uint32_t o_free = b0 + 208, drain = b0 + 216;
+    const uint32_t o_free = b0 + 208, drain = b0 + 216, q_full = b0 + 32;
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
-            mbar_init(k_full(b), 4);
+            mbar_init(k_full(b), kTiles);
             mbar_init(k_empty(b), 1);
             mbar_init(v_empty(b), 1);
             mbar_init(s_full(b), 1);
-            mbar_init(vp_full(b), 8);
+            mbar_init(vp_full(b), 4 + kTiles);
             mbar_init(o_done(b), 1);
             for (int q = 0; q < 4; ++q) mbar_init(m_full(q, b), 1);
         }
         for (int q = 0; q < 4; ++q) mbar_init(l_full(q), 2);
         mbar_init(o_free, 8);
+        mbar_init(q_full, 2 * kTiles);
         mbar_init(drain, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -434,10 +435,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     long long pos = c0;
     auto next_run = [&](Run& r) {
         while (pos < c1) {
-            r.u = find_unit<L>(a, prefix, pos);
-            r.v0 = block_at<L>(r.u.first, r.u.rt.nt, pos);
-            r.v1 = block_at<L>(r.u.first, r.u.rt.nt, c1);
-            pos = r.u.end;
+            Unit& u = r.u;
+            if (pos > c0 && u.h + 1 < a.kv.hkv) {         // the same rows, the next head
+                ++u.h;
+                u.end += u.end - u.first;
+                u.first = pos;
+            } else {
+                u = find_unit<L>(a, prefix, pos);
+            }
+            r.v0 = block_at<L>(u.first, u.rt.nt, pos);
+            r.v1 = block_at<L>(u.first, u.rt.nt, c1);
+            pos = u.end;
             if (r.v0 < r.v1) return true;
         }
         return false;
@@ -446,8 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     Run run;
     bool ok = true;
     if (warp >= kWarpMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    else if (warp >= kWarpK) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    else if (warp >= kWarpK) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     if (warp < kWarpK) {
         // ------------------------------------------------------------------------ softmax
         const int quad = warp & 3, wg = warp >> 2;        // the warpgroup takes the blocks of its parity
@@ -487,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                 const int j0 = run.u.rt.block(v) * kKeys;
                 unsigned there = 0;                       // the block's tiles
 #pragma unroll
-                for (int w = 0; w < 4; ++w) there |= present[it & 3][w] << (2 * w);
+                for (int w = 0; w < kTiles; ++w) there |= (unsigned)present[it & 3][w] << w;
                 const bool edge = there != 255u || j0 + kKeys - 1 > all_lim || (j0 < all_low && j0 + kKeys > a.n_sink) || run.u.rt.empty;
                 // which of 32 keys the row sees
                 auto mask_of = [&](int ch) {
@@ -647,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     } else if (warp < kWarpMma) {
         // ------------------------------------------------------------------------ K (and Q), V
         const bool is_k = warp < kWarpV;
-        const int w = warp & 3;                           // tiles 2w, 2w + 1 of a block
+        const int w = (warp - kWarpK) & (kTiles - 1);     // the warp's tile of a block
         const int per = a.kv.page_shift - 4;
         unsigned it = 0;
         for (int un = 0; ok && next_run(run); ++un) {
@@ -657,20 +665,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             // keys that some row sees: below hi, from lo on or among the first tokens
             const int hi = run.u.rt.empty ? 0 : a.tree ? si.len : min(si.len, base + run.u.rt.i1 + 1);
             const int lo = a.window > 0 ? (int)max((long long)base + (a.tree ? 0 : run.u.rt.i0) - a.window + 1, 0LL) : 0;
-            // The warp's tiles of the run in order: tile n is 2w + (n & 1) of block v0 + (n >> 1).  Lane x
-            // holds the page of tile 32 * group + x.
-            const int tiles = 2 * (run.v1 - run.v0);
-            int group = -1, page = -1;
-            Raw<D, kFormat> raw[kAhead];
-            unsigned have = 0;                            // bit n % 32: tile n is one of the cache's and some row sees a key of it
-            auto load = [&](int n, Raw<D, kFormat>& r) {
-                if (n >= tiles) return;
+            int group = -1, page = -1;                    // lane x holds the page of the tile of block v0 + 32 * group + x
+            Raw<D, kFormat> raw;
+            bool have = false;                            // the tile is one of the cache's and some row sees a key of it
+            auto load = [&](int v) {
+                const int n = v - run.v0;
                 if (n >> 5 != group) {
                     group = n >> 5;
                     page = -1;
-                    const int mine = (n & ~31) + lane;
-                    if (mine < tiles) {
-                        const int tile = run.u.rt.block(run.v0 + (mine >> 1)) * (kKeys / 16) + 2 * w + (mine & 1), key = tile * 16;
+                    const int mine = (v - (n & 31)) + lane;
+                    if (mine < run.v1) {
+                        const int tile = run.u.rt.block(mine) * kTiles + w, key = tile * 16;
                         if (key < hi && (key + 15 >= lo || key < a.n_sink)) {
                             page = table[tile >> per];
                             if (page < 0 || page >= a.kv.n_pages) {
@@ -681,37 +686,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     }
                 }
                 const int pg = __shfl_sync(0xffffffffu, page, n & 31);
-                have &= ~(1u << (n & 31));
-                if (pg >= 0) {
-                    have |= 1u << (n & 31);
-                    const int tile = run.u.rt.block(run.v0 + (n >> 1)) * (kKeys / 16) + 2 * w + (n & 1);
+                have = pg >= 0;
+                if (have) {
+                    const int tile = run.u.rt.block(v) * kTiles + w;
                     const uint8_t* src = a.kv.pool + ((((size_t)pg * a.kv.hkv + run.u.h) << per) + (tile & ((1 << per) - 1))) * kT.bytes;
-                    if (is_k) load_k<D, kFormat>(r, src, lane);
-                    else load_v<D, kFormat>(r, src, lane);
+                    if (is_k) load_k<D, kFormat>(raw, src, lane);
+                    else load_v<D, kFormat>(raw, src, lane);
                 } else {
-                    clear(r);
+                    clear(raw);
                 }
             };
+            load(run.v0);
+            // Q of the unit, once every product of the unit before is through with it: 8 rows per warp, 8
+            // lanes per row, two rows under way
+            if (it > 0 && !mbar_wait(s_full((it - 1) & 1), (it - 1) >> 1 & 1, &abort_flag)) { ok = false; break; }
+            if (a.tree && warp == kWarpK)
+                for (int j = lane; j < si.n; j += 32)
+                    drafted[un & 3][j] = base + __popcll(a.tree[si.q0 + j] & ~(1ull << j));
+            {
+                const int row = 8 * (warp - kWarpK) + (lane >> 3), part = lane & 7;
+                uint4 q[2][D / 64];
 #pragma unroll
-            for (int x = 0; x < kAhead; ++x) load(x, raw[x]);
-            if (is_k) {
-                // Q of the unit: every product of the unit before is through with it
-                if (it > 0 && !mbar_wait(k_empty((it - 1) % kBufs), ((it - 1) / kBufs) & 1, &abort_flag)) { ok = false; break; }
-                if (a.tree && w == 0)
-                    for (int j = lane; j < si.n; j += 32)
-                        drafted[un & 3][j] = base + __popcll(a.tree[si.q0 + j] & ~(1ull << j));
-                // 8 lanes per row, D/8 dims each
-#pragma unroll 1
-                for (int x = 0; x < 8; ++x) {
-                    const int row = 32 * w + 4 * x + (lane >> 3), part = lane & 7, grow = run.u.r * kRows + row, i = grow / a.G;
-                    const bool on = i < si.n;
-                    const __nv_bfloat16* src = a.q + (size_t)(si.q0 + i) * a.q_stride + (size_t)(run.u.h * a.G + grow % a.G) * D + part * 8;
-                    uint4 q[D / 64];
+                for (int x = 0; x < 2; ++x) {
+                    const int grow = run.u.r * kRows + row + 4 * x, i = grow / a.G;
+                    const __nv_bfloat16* src = a.q + (size_t)(si.q0 + i) * a.q_stride + (size_t)(run.u.h * a.G + grow - i * a.G) * D + part * 8;
+#pragma unroll
+                    for (int e = 0; e < D / 64; ++e)
+                        q[x][e] = i < si.n ? *reinterpret_cast<const uint4*>(src + 64 * e) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
                     float amax = 0.f;
 #pragma unroll
                     for (int e = 0; e < D / 64; ++e) {
-                        q[e] = on ? *reinterpret_cast<const uint4*>(src + 64 * e) : make_uint4(0, 0, 0, 0);
-                        const uint32_t wd[4] = {q[e].x, q[e].y, q[e].z, q[e].w};
+                        const uint32_t wd[4] = {q[x][e].x, q[x][e].y, q[x][e].z, q[x][e].w};
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(wd[y] << 16)), fabsf(__uint_as_float(wd[y] & 0xFFFF0000u))));
@@ -721,45 +729,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     const RowScale rs = row_scale(amax);
                     // the coefficient is positive (q carries the scale's sign): times -inf it stays -inf
                     const float down = a.scale < 0.f ? -rs.down : rs.down;
-                    if (part == 0) coef[un & 3][row] = fmaxf(fabsf(a.scale) * a.kv.k_scale * 1.44269504088896340736f * rs.up, kLeast);
+                    if (part == 0) coef[un & 3][row + 4 * x] = fmaxf(fabsf(a.scale) * a.kv.k_scale * 1.44269504088896340736f * rs.up, kLeast);
 #pragma unroll
                     for (int e = 0; e < D / 64; ++e) {
-                        const uint32_t wd[4] = {q[e].x, q[e].y, q[e].z, q[e].w};
+                        const uint32_t wd[4] = {q[x][e].x, q[x][e].y, q[x][e].z, q[x][e].w};
                         uint32_t o[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             o[y] = pack_f16(__uint_as_float(wd[y] << 16) * down, __uint_as_float(wd[y] & 0xFFFF0000u) * down);
-                        st_shared(sq + chunk_at(row, e * 8 + part), make_uint4(o[0], o[1], o[2], o[3]));
+                        st_shared(sq + chunk_at(row + 4 * x, e * 8 + part), make_uint4(o[0], o[1], o[2], o[3]));
                     }
                 }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
             }
             for (int v = run.v0; v < run.v1; ++v, ++it) {
                 const int b = it % kBufs;
-                const uint32_t ph = (it / kBufs) & 1;
-                if (!mbar_wait(is_k ? k_empty(b) : v_empty(b), ph ^ 1, &abort_flag)) { ok = false; break; }
+                if (!mbar_wait(is_k ? k_empty(b) : v_empty(b), ((it / kBufs) & 1) ^ 1, &abort_flag)) { ok = false; break; }
                 const uint32_t dst = (is_k ? sk : sv) + b * kRegion;
-                const int n0 = 2 * (v - run.v0);
-                const int j0 = run.u.rt.block(v) * kKeys;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int row0 = 32 * w + 16 * x;
-                    Raw<D, kFormat>& r = raw[x % kAhead];
-                    if (is_k) {
-                        write_k<D, kFormat>(dst, r, row0, lane);
-                    } else {
-                        // past the cached tokens the bytes may be anything: zero the lane's tokens there
-                        if (j0 + row0 + 16 > si.len) zero_past<D, kFormat>(r, si.len - j0 - row0, lane & 3);
-                        write_v<D, kFormat>(dst, r, row0, lane);
+                if (is_k) {
+                    write_k<D, kFormat>(dst, raw, 16 * w, lane);
+                    if (lane == 0) {
+                        present[it & 3][w] = have;
+                        if (w == 0) what[it & 3] = v == run.v0 ? kFirst : kNext;
                     }
-                    load(n0 + x + kAhead, r);
-                }
-                if (is_k && lane == 0) {
-                    present[it & 3][w] = have >> (n0 & 31) & 3u;
-                    if (w == 0) what[it & 3] = v == run.v0 ? kFirst : kNext;
+                } else {
+                    // past the cached tokens the bytes may be anything: zero the lane's tokens there
+                    const int left = si.len - run.u.rt.block(v) * kKeys - 16 * w;
+                    if (left < 16) zero_past<D, kFormat>(raw, left, lane & 3);
+                    write_v<D, kFormat>(dst, raw, 16 * w, lane);
                 }
                 fence_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(is_k ? k_full(b) : vp_full(it & 1));
+                if (v + 1 < run.v1) load(v + 1);
             }
         }
         if (ok && is_k) {                                 // no more blocks
@@ -768,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             __syncwarp();
             if (ok && lane == 0) mbar_arrive(k_full(it % kBufs));
         }
-        if (is_k && w == 0) {                             // the unit that the cut at the CTA's first place goes through
+        if (warp == kWarpK) {                             // the unit that the cut at the CTA's first place goes through
             if (work) run.u = find_unit<L>(a, prefix, c0);
             if (lane == 0) {
                 if (work && run.u.first < c0)
@@ -782,13 +786,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
         // descriptors of the regions' first bytes; an offset adds to the address field (16-byte units)
         const uint64_t q_desc = desc(sq, 16), k_desc = desc(sk, 16), v_desc = desc(sv, kKeys * 128);
         const bool lead = elect();
-        unsigned units = 0;
+        unsigned units = 0, units_q = 0;
         for (unsigned it = 0, before = kEnd;; ++it) {
             const int b = it % kBufs;
             ok = mbar_wait(k_full(b), (it / kBufs) & 1, &abort_flag);
             if (!ok) break;
             tc_after();
             const unsigned now = what[it & 3];
+            if (now == kFirst) {                          // of a unit: its Q
+                ok = mbar_wait(q_full, units_q++ & 1, &abort_flag);
+                if (!ok) break;
+                tc_after();
+            }
             if (now != kEnd) {                            // S of this block
                 if (lead) {
                     const uint64_t kd = k_desc + b * (kRegion >> 4);
