@@ -1,5 +1,19 @@
-// The quantised key/value cache: host side of the C ABI, the writing kernel (bf16 -> codes
-// and scales in their tiles) and the reading one (codes -> bf16).
+// The quantised key/value cache: host side of the C ABI, the writing kernels (bf16 -> codes
+// and scales in their tiles) and the reading ones (codes -> bf16).
+//
+// Both directions are bound by the bytes of the bf16 side (4 of 5.1 bytes per element of NVFP4).
+// A call of few tokens takes one thread per 16 dims of a row: latency is all there is.  A call of
+// many takes a warp per 16 tokens and head: where the tokens are a whole tile in order, a lane has
+// exactly the tokens and dims whose codes it stores as 16-byte vectors, so that both the rows and
+// the tile move in full sectors (one 8-byte store per block cost 20 us for 8192 tokens of 8 heads
+// of 128 where the bytes take 6.3); the other tokens go row by row.
+//
+// Quotients are the definition's x / (scale * s), rounded to nearest, in three operations: with
+// r = RN(1/d) and q0 = RN(x r), q0 + RN(x - q0 d) r rounds to RN(x/d) (Markstein's correction, 1990;
+// compared with the division for every bf16 significand over every fp32 one: no difference), as long
+// as nothing over- or underflows; a block where something could, with a NaN, an infinity or
+// a saturated scale, takes the division itself.  The conversion instructions round to nearest even
+// and saturate like the definition; only a zero's sign is dropped afterwards.
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -68,70 +82,363 @@ __device__ __forceinline__ uint8_t* kv_tile_ptr(const KvView& kv, int slot, int 
     return kv.pool + (((size_t)page * kv.hkv + head) * per + (in >> 4)) * tile_bytes;
 }
 
-// Quantise block b (16 dims) of one token's K or V row into its tile.
-template <int D, int kFormat, bool kV>
-__device__ __forceinline__ void append_block(uint8_t* tile, int r, int b, const __nv_bfloat16* src, float st) {
-    const uint4 x0 = *reinterpret_cast<const uint4*>(src), x1 = *reinterpret_cast<const uint4*>(src + 8);
-    const uint32_t xw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-    float x[16];
+// max |x| of a block of 16 bf16 (8 words); NaN if there is one.
+__device__ __forceinline__ float block_amax(const uint32_t (&xw)[8]) {
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&xw[0]));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        x[2 * j] = __uint_as_float(xw[j] << 16);
-        x[2 * j + 1] = __uint_as_float(xw[j] & 0xFFFF0000u);
-    }
-    uint32_t w[4] = {0, 0, 0, 0};
+    for (int j = 1; j < 8; ++j) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&xw[j])));
+    const __nv_bfloat16 h = __hmax_nan(__low2bfloat16(m), __high2bfloat16(m));
+    return __bfloat162float(h);
+}
+__device__ __forceinline__ float bf16_at(const uint32_t (&xw)[8], int j) {
+    return __uint_as_float(j & 1 ? xw[j >> 1] & 0xFFFF0000u : xw[j >> 1] << 16);
+}
+
+// RN(x / d) with r = RN(1/d), in the range where the remainder is exact.
+__device__ __forceinline__ float quotient(float x, float d, float r) {
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
+}
+// Magnitudes for which quotients of the block are in that range.
+__device__ __forceinline__ bool tame(float amax, float d) {
+    return amax < 1e30f && d > 1e-25f && d < 1e25f && amax < 1e4f * d;
+}
+
+// 16 codes of a block (xw: 8 words of bf16) with divisor d, and for NVFP4 its scale byte.
+// FP8: 16 bytes; NVFP4: 8 bytes.
+template <int kFormat>
+__device__ __forceinline__ uint32_t quantise(const uint32_t (&xw)[8], float st, float inv_st, uint32_t* w) {
+    const float amax = block_amax(xw);
     if constexpr (kFormat == FT_KV_FP8) {
+        if (tame(amax, st)) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) w[j >> 2] |= e4m3_encode_signed(__fdiv_rn(x[j], st)) << (8 * (j & 3));
+            for (int j = 0; j < 4; ++j) {
+                const float q[4] = {quotient(bf16_at(xw, 4 * j), st, inv_st), quotient(bf16_at(xw, 4 * j + 1), st, inv_st),
+                                    quotient(bf16_at(xw, 4 * j + 2), st, inv_st), quotient(bf16_at(xw, 4 * j + 3), st, inv_st)};
+                uint32_t c;
+                asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+                    "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+                    : "=r"(c) : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]));
+                const uint32_t mag = c & 0x7F7F7F7Fu;                 // a sign only where the magnitude is not zero
+                w[j] = mag | (c & (mag + 0x7F7F7F7Fu) & 0x80808080u);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = 0;
+#pragma unroll 1
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t word = xw[0 + (j >> 1)];
+                const float x = __uint_as_float(j & 1 ? word & 0xFFFF0000u : word << 16);
+                w[j >> 2] |= e4m3_encode_signed(__fdiv_rn(x, st)) << (8 * (j & 3));
+            }
+        }
+        return 0;
     } else {
-        float amax = 0.f;
+        const bool number = amax == amax;
+        float m = amax;
+        if (!number) {                                                // the largest of the others
+            m = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(x[j]));       // fmaxf drops a NaN
-        const uint8_t sc = e4m3_encode_rne(__fdiv_rn(__fdiv_rn(amax, 6.0f), st));
-        const float denom = __fmul_rn(e4m3_value(sc), st);
-        if (denom != 0.f) {
+            for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(bf16_at(xw, j)));
+        }
+        const uint8_t sc = e4m3_encode_rne(__fdiv_rn(__fdiv_rn(m, 6.0f), st));
+        const float d = __fmul_rn(e4m3_value(sc), st);
+        w[0] = w[1] = 0;
+        if (d == 0.f) return 0;
+        if (number && sc < 0x7E && tame(amax, d)) {
+            const float r = __frcp_rn(d);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float q[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q[e] = quotient(bf16_at(xw, 8 * j + e), d, r);
+                uint32_t c;
+                asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tcvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+                    "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+                    "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\tmov.b32 %0, {b0, b1, b2, b3};\n\t}"
+                    : "=r"(c) : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+                const uint32_t mag = c & 0x77777777u;
+                w[j] = mag | (c & (mag + 0x77777777u) & 0x88888888u);
+            }
+        } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                w[j >> 3] |= (uint32_t)e2m1_encode_rne(__fdiv_rn(x[j], denom)) << (4 * (j & 7));
+                w[j >> 3] |= (uint32_t)e2m1_encode_rne(__fdiv_rn(bf16_at(xw, j), d)) << (4 * (j & 7));
         }
-        tile[kV ? kv_v_scale_byte<D>(r, b) : kv_k_scale_byte<D>(r, b)] = denom != 0.f ? sc : 0;
+        return sc;
     }
+}
+
+__device__ __forceinline__ void load_block(uint32_t (&xw)[8], const __nv_bfloat16* src) {
+    const uint4 x0 = *reinterpret_cast<const uint4*>(src), x1 = *reinterpret_cast<const uint4*>(src + 8);
+    xw[0] = x0.x; xw[1] = x0.y; xw[2] = x0.z; xw[3] = x0.w;
+    xw[4] = x1.x; xw[5] = x1.y; xw[6] = x1.z; xw[7] = x1.w;
+}
+
+// Quantise block b (16 dims) of one token's K or V row into its tile.
+template <int D, int kFormat, bool kV>
+__device__ __forceinline__ void append_block(uint8_t* tile, int r, int b, const __nv_bfloat16* src, float st, float inv_st) {
+    uint32_t xw[8], w[4];
+    load_block(xw, src);
+    const uint32_t sc = quantise<kFormat>(xw, st, inv_st, w);
+    if constexpr (kFormat == FT_KV_NVFP4) tile[kV ? kv_v_scale_byte<D>(r, b) : kv_k_scale_byte<D>(r, b)] = (uint8_t)sc;
     store_codes<D, kFormat, kV>(tile, r, 16 * b, w);
+}
+
+// bf16 pairs of 8 (NVFP4: one word) or 4 (FP8: one word) codes; sc: the block's scale as two f16.
+__device__ __forceinline__ uint32_t to_bf16(uint32_t f16x2, float st) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f16x2));
+    const __nv_bfloat162 p = __floats2bfloat162_rn(__fmul_rn(f.x, st), __fmul_rn(f.y, st));
+    return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ void dequant_e2m1(uint32_t w, uint32_t sc2, float st, uint32_t* out) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t.reg .b32 x0, x1, x2, x3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 x0, b0;\n\tcvt.rn.f16x2.e2m1x2 x1, b1;\n\tcvt.rn.f16x2.e2m1x2 x2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 x3, b3;\n\tmul.rn.f16x2 %0, x0, %5;\n\tmul.rn.f16x2 %1, x1, %5;\n\t"
+        "mul.rn.f16x2 %2, x2, %5;\n\tmul.rn.f16x2 %3, x3, %5;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w), "r"(sc2));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[j] = to_bf16(h[j], st);          // code * scale is exact in f16
+}
+__device__ __forceinline__ void dequant_e4m3(uint32_t w, float st, uint32_t* out) {
+    uint32_t h[2];
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]) : "r"(w));
+    out[0] = to_bf16(h[0], st);
+    out[1] = to_bf16(h[1], st);
+}
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
+    uint32_t o;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(o) : "r"(byte * 0x101u));
+    return o;
 }
 
 template <int D, int kFormat, bool kV>
 __device__ __forceinline__ void read_block(const uint8_t* tile, int r, int b, __nv_bfloat16* dst, float st) {
-    uint32_t w[4];
+    uint32_t w[4], out[8];
     load_codes<D, kFormat, kV>(w, tile, r, 16 * b);
-    float sc = 1.f;
-    if constexpr (kFormat == FT_KV_NVFP4)
-        sc = e4m3_value(tile[kV ? kv_v_scale_byte<D>(r, b) : kv_k_scale_byte<D>(r, b)]);
-    uint32_t out[8];
+    if constexpr (kFormat == FT_KV_NVFP4) {
+        const uint32_t sc2 = scale_pair(tile[kV ? kv_v_scale_byte<D>(r, b) : kv_k_scale_byte<D>(r, b)]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float f[2];
+        for (int j = 0; j < 2; ++j) dequant_e2m1(w[j], sc2, st, out + 4 * j);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = 2 * j + e;
-            if constexpr (kFormat == FT_KV_NVFP4) {
-                const uint32_t c = w[i >> 3] >> (4 * (i & 7)) & 15u;
-                const uint32_t m = c & 7u;
-                const float mag = m < 2 ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-                f[e] = __fmul_rn(__fmul_rn(c & 8u ? -mag : mag, sc), st);
-            } else {
-                const uint32_t c = w[i >> 2] >> (8 * (i & 3)) & 255u;
-                const float mag = e4m3_value((uint8_t)(c & 127u));
-                f[e] = __fmul_rn(c & 128u ? -mag : mag, st);
-            }
-        }
-        const __nv_bfloat162 p = __floats2bfloat162_rn(f[0], f[1]);
-        out[j] = *reinterpret_cast<const uint32_t*>(&p);
+        for (int j = 0; j < 4; ++j) dequant_e4m3(w[j], st, out + 2 * j);
     }
     reinterpret_cast<uint4*>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
+// ---------------------------------------------------------------------------- whole tiles
+
+// A warp's window of 16 tokens of a call and what they are.
+struct Window {
+    int head;            // token (from the window's first) that starts a whole tile, or -1: it runs past the window
+    unsigned rest;       // tokens of the window that belong to no whole tile: bits
+    int slot;            // of token `lane` (0..31 from the window's first), -1 past the end
+};
+// Tokens first.. of the call; the lanes hold the slots of 32 tokens from the window's first on and of the 16
+// before it.
+__device__ __forceinline__ Window window_of(const KvView& kv, const int32_t* slots, int n, int first, int lane) {
+    const int most = kv.n_pages << kv.page_shift;
+    auto slot_of = [&](int i) {
+        const int s = i >= 0 && i < n ? slots[i] : -1;
+        return s >= 0 && s < most ? s : -1;
+    };
+    Window w;
+    w.slot = slot_of(first + lane);
+    const int before = slot_of(first - 16 + lane);           // lanes 0..15: the 16 tokens before the window
+    // bit i: tokens i and i + 1 of the 32 (of the 16 before and the 16 of the window) stand in order
+    const int next = __shfl_down_sync(0xffffffffu, w.slot, 1), next_before = __shfl_down_sync(0xffffffffu, before, 1);
+    const unsigned run = __ballot_sync(0xffffffffu, w.slot >= 0 && next == w.slot + 1);
+    const unsigned run_before = __ballot_sync(0xffffffffu, before >= 0 && next_before == before + 1);
+    const unsigned lead = __ballot_sync(0xffffffffu, w.slot >= 0 && (w.slot & 15) == 0);
+    const unsigned lead_before = __ballot_sync(0xffffffffu, before >= 0 && (before & 15) == 0);
+    auto head = [](unsigned runs, unsigned leads) {          // the token i < 16 that starts 16 in order at a tile's start
+        int h = -1;
+        for (unsigned x = leads & 0xFFFFu; x; x &= x - 1) {
+            const int i = __ffs(x) - 1;
+            if ((runs >> i & 0x7FFFu) == 0x7FFFu) h = i;
+        }
+        return h;
+    };
+    w.head = head(run, lead);
+    const int prev = head(run_before, lead_before);          // a tile that began before reaches tokens 0 .. prev - 1
+    w.rest = 0xFFFFu;
+    if (prev >= 0) w.rest &= ~((1u << prev) - 1);
+    if (w.head >= 0) w.rest &= (1u << w.head) - 1;
+    const int left = n - first;
+    if (left < 16) w.rest &= (1u << left) - 1;
+    return w;
+}
+
+// A whole tile of one head: the lane (g, t) quantises the blocks whose codes it stores.
+template <int D, int kFormat, bool kV>
+__device__ __forceinline__ void append_tile(uint8_t* tile, const __nv_bfloat16* src, size_t stride, float st, float inv_st, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    constexpr bool kFour = kFormat == FT_KV_NVFP4;
+    if constexpr (!kV) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int b = 0; b < D / 64; ++b) {
+                uint32_t xw[8], w[4];
+                load_block(xw, src + (size_t)(8 * v + g) * stride + t * (D / 4) + 16 * b);
+                const uint32_t sc = quantise<kFormat>(xw, st, inv_st, w);
+                store_run<kFour ? 8 : 16>(tile + kv_lane_byte(lane, (v * (D / 4) + 16 * b) / (kFour ? 2 : 1)), w);
+                if constexpr (kFour) tile[kv_tile(D, kFormat).k_scales + lane * (D / 32) + v * (D / 64) + b] = (uint8_t)sc;
+            }
+    } else if constexpr (D == 64) {
+        // a block of 16 dims belongs to two lanes: each takes it for two of the four tokens
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int q = 2 * x + (g & 1), r = 2 * t + (q & 1) + 8 * (q >> 1), b = g >> 1;
+            uint32_t xw[8], w[4];
+            load_block(xw, src + (size_t)r * stride + 16 * b);
+            const uint32_t sc = quantise<kFormat>(xw, st, inv_st, w);
+            store_codes<D, kFormat, true>(tile, r, 16 * b, w);
+            if constexpr (kFour) tile[kv_v_scale_byte<D>(r, b)] = (uint8_t)sc;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int b = 0; b < D / 128; ++b) {
+                const int r = 2 * t + (q & 1) + 8 * (q >> 1), blk = g * (D / 128) + b;
+                uint32_t xw[8], w[4];
+                load_block(xw, src + (size_t)r * stride + 16 * blk);
+                const uint32_t sc = quantise<kFormat>(xw, st, inv_st, w);
+                store_run<kFour ? 8 : 16>(tile + kv_tile(D, kFormat).code_bytes + kv_lane_byte(lane, (q * (D / 8) + 16 * b) / (kFour ? 2 : 1)), w);
+                if constexpr (kFour) tile[kv_v_scale_byte<D>(r, blk)] = (uint8_t)sc;
+            }
+    }
+}
+
 }  // namespace
+
+// A warp per 16 tokens of the call and head, K then V.
+template <int D, int kFormat>
+__global__ void __launch_bounds__(256) kv_append_tiles_kernel(const KvView kv, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                                                              size_t k_stride, size_t v_stride, const int32_t* slots, int n) {
+    pdl_wait_and_release();
+    const int lane = threadIdx.x & 31;
+    const float inv_k = __frcp_rn(kv.k_scale), inv_v = __frcp_rn(kv.v_scale);
+    const long long items = (long long)((n + 15) / 16) * kv.hkv * 2;
+    for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += (long long)gridDim.x * 8) {
+        const int first = (int)(it / (2 * kv.hkv)) * 16, rest = (int)(it % (2 * kv.hkv));
+        const bool is_v = rest >= kv.hkv;
+        const int head = is_v ? rest - kv.hkv : rest;
+        const Window w = window_of(kv, slots, n, first, lane);
+        const __nv_bfloat16* src = (is_v ? v : k) + (size_t)head * D;
+        const size_t stride = is_v ? v_stride : k_stride;
+        if (w.head >= 0) {
+            const int slot = __shfl_sync(0xffffffffu, w.slot, w.head);
+            uint8_t* tile = kv_tile_ptr(kv, slot, head, kv_tile(D, kFormat).bytes);
+            const __nv_bfloat16* from = src + (size_t)(first + w.head) * stride;
+            if (is_v) append_tile<D, kFormat, true>(tile, from, stride, kv.v_scale, inv_v, lane);
+            else append_tile<D, kFormat, false>(tile, from, stride, kv.k_scale, inv_k, lane);
+        }
+        for (unsigned x = w.rest; x;) {                      // 32 / (D/16) tokens at a time
+            constexpr int kAt = 512 / D;
+            int tok = -1;
+#pragma unroll
+            for (int y = 0; y < kAt; ++y) {
+                const int bit = __ffs(x) - 1;
+                if (lane / (D / 16) == y && x) tok = bit;
+                x &= x - 1;
+            }
+            const int slot = __shfl_sync(0xffffffffu, w.slot, max(tok, 0));
+            if (tok >= 0) {
+                if (slot >= 0) {
+                    uint8_t* tile = kv_tile_ptr(kv, slot, head, kv_tile(D, kFormat).bytes);
+                    const int b = lane % (D / 16);
+                    const __nv_bfloat16* from = src + (size_t)(first + tok) * stride + 16 * b;
+                    if (is_v) append_block<D, kFormat, true>(tile, slot & 15, b, from, kv.v_scale, inv_v);
+                    else append_block<D, kFormat, false>(tile, slot & 15, b, from, kv.k_scale, inv_k);
+                } else if (rest == 0 && lane % (D / 16) == 0 && slots[first + tok] != -1) {
+                    atomicOr(kv.status, FT_DEV_BAD_ID);
+                }
+            }
+        }
+    }
+}
+
+namespace {
+
+// A whole tile of one head back: the lane's 16-byte vectors to rows.
+template <int D, int kFormat, bool kV>
+__device__ __forceinline__ void read_tile(const uint8_t* tile, __nv_bfloat16* dst, size_t stride, float st, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    constexpr bool kFour = kFormat == FT_KV_NVFP4;
+    constexpr int kVecs = kFour ? D / 64 : D / 32, kDims = kFour ? 32 : 16;      // vectors of a lane, codes of one
+    constexpr int kRow = kV ? D / 8 : D / 4;                                     // dims of a token that the lane has
+#pragma unroll
+    for (int x = 0; x < kVecs; ++x) {
+        const uint4 c = *reinterpret_cast<const uint4*>(tile + (kV ? kv_tile(D, kFormat).code_bytes : 0) + x * 512 + lane * 16);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int y = 0; y < kDims; y += 8) {                                     // 8 codes: 16 bytes of a row
+            const int at = x * kDims + y, q = at / kRow, d = (kV ? g : t) * kRow + at % kRow;
+            const int r = kV ? 2 * t + (q & 1) + 8 * (q >> 1) : 8 * q + g;
+            uint32_t out[4];
+            if constexpr (kFour) {
+                dequant_e2m1(w[y / 8], scale_pair(tile[kV ? kv_v_scale_byte<D>(r, d / 16) : kv_k_scale_byte<D>(r, d / 16)]), st, out);
+            } else {
+                dequant_e4m3(w[y / 4], st, out);
+                dequant_e4m3(w[y / 4 + 1], st, out + 2);
+            }
+            *reinterpret_cast<uint4*>(dst + (size_t)r * stride + d) = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+    }
+}
+
+}  // namespace
+
+template <int D, int kFormat>
+__global__ void __launch_bounds__(256) kv_read_tiles_kernel(const KvView kv, const int32_t* slots, int n, __nv_bfloat16* k,
+                                                            __nv_bfloat16* v) {
+    pdl_wait_and_release();
+    const int lane = threadIdx.x & 31;
+    const size_t stride = (size_t)kv.hkv * D;
+    const long long items = (long long)((n + 15) / 16) * kv.hkv * 2;
+    for (long long it = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); it < items; it += (long long)gridDim.x * 8) {
+        const int first = (int)(it / (2 * kv.hkv)) * 16, rest = (int)(it % (2 * kv.hkv));
+        const bool is_v = rest >= kv.hkv;
+        const int head = is_v ? rest - kv.hkv : rest;
+        const Window w = window_of(kv, slots, n, first, lane);
+        __nv_bfloat16* dst = (is_v ? v : k) + (size_t)head * D;
+        if (w.head >= 0) {
+            const int slot = __shfl_sync(0xffffffffu, w.slot, w.head);
+            const uint8_t* tile = kv_tile_ptr(kv, slot, head, kv_tile(D, kFormat).bytes);
+            __nv_bfloat16* to = dst + (size_t)(first + w.head) * stride;
+            if (is_v) read_tile<D, kFormat, true>(tile, to, stride, kv.v_scale, lane);
+            else read_tile<D, kFormat, false>(tile, to, stride, kv.k_scale, lane);
+        }
+        for (unsigned x = w.rest; x;) {
+            constexpr int kAt = 512 / D;
+            int tok = -1;
+#pragma unroll
+            for (int y = 0; y < kAt; ++y) {
+                const int bit = __ffs(x) - 1;
+                if (lane / (D / 16) == y && x) tok = bit;
+                x &= x - 1;
+            }
+            const int slot = __shfl_sync(0xffffffffu, w.slot, max(tok, 0)), b = lane % (D / 16);
+            if (tok < 0) continue;
+            __nv_bfloat16* to = dst + (size_t)(first + tok) * stride + 16 * b;
+            if (slot < 0) {
+                if (rest == 0 && b == 0 && slots[first + tok] != -1) atomicOr(kv.status, FT_DEV_BAD_ID);
+                reinterpret_cast<uint4*>(to)[0] = make_uint4(0, 0, 0, 0);
+                reinterpret_cast<uint4*>(to)[1] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            const uint8_t* tile = kv_tile_ptr(kv, slot, head, kv_tile(D, kFormat).bytes);
+            if (is_v) read_block<D, kFormat, true>(tile, slot & 15, b, to, kv.v_scale);
+            else read_block<D, kFormat, false>(tile, slot & 15, b, to, kv.k_scale);
+        }
+    }
+}
 
 // One thread per 16 dims of a token's key or value row; the threads of a token run over K's
 // heads and blocks, then V's, so a warp reads whole rows.
@@ -140,6 +447,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvView kv, const _
                                                         size_t k_stride, size_t v_stride, const int32_t* slots, int n) {
     pdl_wait_and_release();
     const int per = kv.hkv * (D / 16);
+    const float inv_k = __frcp_rn(kv.k_scale), inv_v = __frcp_rn(kv.v_scale);
     const long long total = 2LL * n * per;
     for (long long g = (long long)blockIdx.x * blockDim.x + threadIdx.x; g < total; g += (long long)gridDim.x * blockDim.x) {
         const int tok = (int)(g / (2 * per)), rest = (int)(g % (2 * per));
@@ -153,8 +461,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvView kv, const _
         const int head = hb / (D / 16), b = hb % (D / 16);
         uint8_t* tile = kv_tile_ptr(kv, slot, head, kv_tile(D, kFormat).bytes);
         const int r = slot & 15;
-        if (is_v) append_block<D, kFormat, true>(tile, r, b, v + (size_t)tok * v_stride + hb * 16, kv.v_scale);
-        else append_block<D, kFormat, false>(tile, r, b, k + (size_t)tok * k_stride + hb * 16, kv.k_scale);
+        if (is_v) append_block<D, kFormat, true>(tile, r, b, v + (size_t)tok * v_stride + hb * 16, kv.v_scale, inv_v);
+        else append_block<D, kFormat, false>(tile, r, b, k + (size_t)tok * k_stride + hb * 16, kv.k_scale, inv_k);
     }
 }
 
@@ -204,6 +512,9 @@ unsigned grid_of(long long threads) {
     return (unsigned)(need < most ? need : most);
 }
 
+// Rows (tokens times kv heads) from which a call goes by tiles.
+constexpr long long kManyRows = 4096;
+
 // Once per kernel and device.
 template <auto kKernel>
 cudaError_t prepare() {
@@ -220,6 +531,12 @@ template <int D, int kFormat>
 struct Append {
     static cudaError_t run(const KvView& kv, const void* k, const void* v, size_t ks, size_t vs, const int32_t* slots,
                            int n, cudaStream_t s) {
+        if ((long long)n * kv.hkv >= kManyRows) {
+            const cudaError_t e = prepare<kv_append_tiles_kernel<D, kFormat>>();
+            if (e != cudaSuccess) return e;
+            return launch_pdl(kv_append_tiles_kernel<D, kFormat>, dim3(grid_of(((n + 15LL) / 16) * kv.hkv * 64)), dim3(256), 0, s, kv,
+                              static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v), ks, vs, slots, n);
+        }
         const cudaError_t e = prepare<kv_append_kernel<D, kFormat>>();
         if (e != cudaSuccess) return e;
         return launch_pdl(kv_append_kernel<D, kFormat>, dim3(grid_of(2LL * n * kv.hkv * (D / 16))), dim3(256), 0, s, kv,
@@ -230,6 +547,12 @@ struct Append {
 template <int D, int kFormat>
 struct Read {
     static cudaError_t run(const KvView& kv, const int32_t* slots, int n, void* k, void* v, cudaStream_t s) {
+        if ((long long)n * kv.hkv >= kManyRows) {
+            const cudaError_t e = prepare<kv_read_tiles_kernel<D, kFormat>>();
+            if (e != cudaSuccess) return e;
+            return launch_pdl(kv_read_tiles_kernel<D, kFormat>, dim3(grid_of(((n + 15LL) / 16) * kv.hkv * 64)), dim3(256), 0, s, kv,
+                              slots, n, static_cast<__nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(v));
+        }
         const cudaError_t e = prepare<kv_read_kernel<D, kFormat>>();
         if (e != cudaSuccess) return e;
         return launch_pdl(kv_read_kernel<D, kFormat>, dim3(grid_of(2LL * n * kv.hkv * (D / 16))), dim3(256), 0, s, kv,

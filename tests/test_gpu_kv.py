@@ -416,3 +416,68 @@ def test_refusals(ft):
         ft.ft_kv_create(d)
     assert ei.value.status == ft.FT_ERR_ARG
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "fp8"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_whole_tiles_and_loose_tokens(ft, fmt, D):
+    """Many tokens in one call: tiles in order, tiles cut by padding or by a jump, tokens in
+    reverse, a start inside a tile, an odd end; bit-exact like the calls of few tokens."""
+    rng = np.random.default_rng(D)
+    hkv, page, n_pages, st = 8, 32, 40, (0.37, 1.9)
+    runs = [np.arange(5, 5 + 70), np.arange(200, 264), np.array([-1]), np.arange(320, 352)[::-1], np.arange(400, 416),
+            np.array([640]), np.arange(417, 431), np.arange(801, 801 + 300)]
+    slots = np.concatenate(runs).astype(np.int32)
+    assert len(set(slots)) == slots.size
+    slots[100] = -1
+    while slots.size * hkv < 5000:                           # enough rows for the calls by tiles
+        slots = np.concatenate([slots, np.arange(1104, 1104 + 160, dtype=np.int32)])
+    n = slots.size
+    assert len(set(slots[slots >= 0])) == (slots >= 0).sum()
+    x = rng.standard_normal((2, n, hkv, D)).astype(np.float32) * np.exp(rng.standard_normal((2, n, hkv, 1)))
+    x[0, ::7, 0, :4] = [np.nan, np.inf, -np.inf, -0.0]
+    x[1, ::5, 1, 16:20] = [3e38, -1e-38, 1e-30, np.nan]
+    x = torch.from_numpy(x).to(torch.bfloat16)
+    dev = x.cuda()
+    sd = torch.from_numpy(slots).cuda()
+    a, b = (ft.KVCache(1, n_pages, page, hkv, D, hkv, 1, fmt, *st) for _ in range(2))
+    a.pool.fill_(0x5A)
+    b.pool.fill_(0x5A)
+    ft.ft_kv_append(a.handle, 0, dev[0], dev[1], sd, n)
+    for i in range(0, n, 300):                               # the same tokens in calls of few
+        m = min(300, n - i)
+        ft.ft_kv_append(b.handle, 0, dev[0, i:i + m], dev[1, i:i + m], sd[i:i + m], m)
+    torch.cuda.synchronize()
+    assert torch.equal(a.pool, b.pool)
+    ko, vo = (torch.full((n, hkv, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ft.ft_kv_read(a.handle, 0, sd, n, ko, vo)
+    torch.cuda.synchronize()
+    for got, which in ((ko, 0), (vo, 1)):
+        val = K.values(*K.quantise(x[which].float().numpy(), fmt, st[which]), fmt, st[which])
+        val[slots < 0] = 0
+        assert torch.equal(got.cpu(), torch.from_numpy(val.astype(np.float32)).to(torch.bfloat16))
+    assert ft.ft_kv_status(a.handle) == 0
+    sd[3], sd[50] = -7, n_pages * page
+    ft.ft_kv_append(a.handle, 0, dev[0], dev[1], sd, n)
+    assert ft.ft_kv_status(a.handle) == ft.FT_DEV_BAD_ID
+    ft.ft_kv_read(a.handle, 0, sd, n, ko, vo)
+    assert ft.ft_kv_status(a.handle) == ft.FT_DEV_BAD_ID
+    assert not ko[3].any() and not vo[50].any()
+
+
+@pytest.mark.parametrize("n", [1, 5, 40])
+def test_negative_and_zero_scale(ft, n):
+    for scale in (-0.2, 0.0):
+        c = Case(ft, "nvfp4", 128, 1, 4, 16, [150, 60], [n, n], seed=12)
+        c.scale = scale
+        o, z = c.run()
+        torch.cuda.synchronize()
+        q = c.q.double().numpy()
+        for s, length in enumerate(c.lens):
+            at = c.start_np[s]
+            for h in range(4):
+                ro, rl, av, mag = K.attention(q[at:at + n, h], c.kval[s][:, 0], c.vval[s][:, 0], K.seen(n, length), scale)
+                e = (abs(scale) * (c.D + 16) * 2.0 ** -23 * mag)[:, None]
+                got = o[at:at + n, h].double().cpu().numpy()
+                assert np.all(np.abs(got - ro) <= 2.0 ** -8 * np.abs(ro) + (2 * e + 2.0 ** -10) * av + length * 2.0 ** -24 * np.abs(c.vval[s]).max())
+                assert np.allclose(z[at:at + n, h].double().cpu().numpy(), rl, rtol=1e-6, atol=1e-5)
