@@ -104,6 +104,21 @@ __device__ __forceinline__ bool tame(float amax, float d) {
     return amax < 1e30f && d > 1e-25f && d < 1e25f && amax < 1e4f * d;
 }
 
+// The codes of a block by the division itself (out of line: rare, and ten copies of it would not fit
+// the instruction cache).
+template <int kFormat>
+__device__ __noinline__ uint4 codes_by_division(uint4 x0, uint4 x1, float d) {
+    const uint32_t xw[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const float q = __fdiv_rn(bf16_at(xw, j), d);
+        if constexpr (kFormat == FT_KV_FP8) w[j >> 2] |= e4m3_encode_signed(q) << (8 * (j & 3));
+        else w[j >> 3] |= (uint32_t)e2m1_encode_rne(q) << (4 * (j & 7));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // 16 codes of a block (xw: 8 words of bf16) with divisor d, and for NVFP4 its scale byte.
 // FP8: 16 bytes; NVFP4: 8 bytes.
 template <int kFormat>
@@ -123,14 +138,8 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&xw)[8], float st, 
                 w[j] = mag | (c & (mag + 0x7F7F7F7Fu) & 0x80808080u);
             }
         } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = 0;
-#pragma unroll 1
-            for (int j = 0; j < 16; ++j) {
-                const uint32_t word = xw[0 + (j >> 1)];
-                const float x = __uint_as_float(j & 1 ? word & 0xFFFF0000u : word << 16);
-                w[j >> 2] |= e4m3_encode_signed(__fdiv_rn(x, st)) << (8 * (j & 3));
-            }
+            const uint4 c = codes_by_division<kFormat>(make_uint4(xw[0], xw[1], xw[2], xw[3]), make_uint4(xw[4], xw[5], xw[6], xw[7]), st);
+            w[0] = c.x; w[1] = c.y; w[2] = c.z; w[3] = c.w;
         }
         return 0;
     } else {
@@ -141,8 +150,11 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&xw)[8], float st, 
 #pragma unroll
             for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(bf16_at(xw, j)));
         }
-        const uint8_t sc = e4m3_encode_rne(__fdiv_rn(__fdiv_rn(m, 6.0f), st));
-        const float d = __fmul_rn(e4m3_value(sc), st);
+        const float sixth = m > 1e-30f && m < 1e30f ? quotient(m, 6.0f, 1.0f / 6.0f) : __fdiv_rn(m, 6.0f);
+        uint32_t sc, sc2;
+        asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %3;\n\tcvt.rn.f16x2.e4m3x2 %1, x;\n\t"
+            "cvt.u32.u16 %0, x;\n\t}" : "=r"(sc), "=r"(sc2) : "f"(0.f), "f"(__fdiv_rn(sixth, st)));
+        const float d = __fmul_rn(__low2float(*reinterpret_cast<const __half2*>(&sc2)), st);
         w[0] = w[1] = 0;
         if (d == 0.f) return 0;
         if (number && sc < 0x7E && tame(amax, d)) {
@@ -161,9 +173,8 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&xw)[8], float st, 
                 w[j] = mag | (c & (mag + 0x77777777u) & 0x88888888u);
             }
         } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                w[j >> 3] |= (uint32_t)e2m1_encode_rne(__fdiv_rn(bf16_at(xw, j), d)) << (4 * (j & 7));
+            const uint4 c = codes_by_division<kFormat>(make_uint4(xw[0], xw[1], xw[2], xw[3]), make_uint4(xw[4], xw[5], xw[6], xw[7]), d);
+            w[0] = c.x; w[1] = c.y;
         }
         return sc;
     }
@@ -273,45 +284,54 @@ __device__ __forceinline__ Window window_of(const KvView& kv, const int32_t* slo
     return w;
 }
 
+// The next 512 / D tokens of a set, one per group of D / 16 lanes (-1: none), taken out of it.
+template <int D>
+__device__ __forceinline__ int pick(unsigned& x, int lane) {
+    int tok = -1;
+#pragma unroll
+    for (int y = 0; y < 512 / D; ++y) {
+        if (lane / (D / 16) == y && x) tok = __ffs(x) - 1;
+        x &= x - 1;
+    }
+    return tok;
+}
+
 // A whole tile of one head: the lane (g, t) quantises the blocks whose codes it stores.
 template <int D, int kFormat, bool kV>
 __device__ __forceinline__ void append_tile(uint8_t* tile, const __nv_bfloat16* src, size_t stride, float st, float inv_st, int lane) {
     const int g = lane >> 2, t = lane & 3;
     constexpr bool kFour = kFormat == FT_KV_NVFP4;
-    if constexpr (!kV) {
+    // the lane's blocks: K [token v][b < D/64]; V [token q][b < D/128], at D = 64 (a block of two lanes) two
+    // of the four tokens each.  Four at a time, every load of them first.
+    constexpr int kBlocks = !kV ? 2 * (D / 64) : D == 64 ? 2 : 4 * (D / 128), kAt = kBlocks < 4 ? kBlocks : 4;
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
-#pragma unroll
-            for (int b = 0; b < D / 64; ++b) {
-                uint32_t xw[8], w[4];
-                load_block(xw, src + (size_t)(8 * v + g) * stride + t * (D / 4) + 16 * b);
-                const uint32_t sc = quantise<kFormat>(xw, st, inv_st, w);
-                store_run<kFour ? 8 : 16>(tile + kv_lane_byte(lane, (v * (D / 4) + 16 * b) / (kFour ? 2 : 1)), w);
-                if constexpr (kFour) tile[kv_tile(D, kFormat).k_scales + lane * (D / 32) + v * (D / 64) + b] = (uint8_t)sc;
+    for (int x0 = 0; x0 < kBlocks; x0 += kAt) {
+        uint32_t xw[kAt][8];
+        auto place = [&](int x, int& r, int& blk) {
+            if (!kV) {
+                r = 8 * (x / (D / 64)) + g;
+                blk = t * (D / 64) + x % (D / 64);
+            } else {
+                const int q = D == 64 ? 2 * x + (g & 1) : x / (D / 128 > 0 ? D / 128 : 1);
+                r = 2 * t + (q & 1) + 8 * (q >> 1);
+                blk = D == 64 ? g >> 1 : g * (D / 128) + x % (D / 128 > 0 ? D / 128 : 1);
             }
-    } else if constexpr (D == 64) {
-        // a block of 16 dims belongs to two lanes: each takes it for two of the four tokens
+        };
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int q = 2 * x + (g & 1), r = 2 * t + (q & 1) + 8 * (q >> 1), b = g >> 1;
-            uint32_t xw[8], w[4];
-            load_block(xw, src + (size_t)r * stride + 16 * b);
-            const uint32_t sc = quantise<kFormat>(xw, st, inv_st, w);
-            store_codes<D, kFormat, true>(tile, r, 16 * b, w);
-            if constexpr (kFour) tile[kv_v_scale_byte<D>(r, b)] = (uint8_t)sc;
+        for (int x = 0; x < kAt; ++x) {
+            int r, blk;
+            place(x0 + x, r, blk);
+            load_block(xw[x], src + (size_t)r * stride + 16 * blk);
         }
-    } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int b = 0; b < D / 128; ++b) {
-                const int r = 2 * t + (q & 1) + 8 * (q >> 1), blk = g * (D / 128) + b;
-                uint32_t xw[8], w[4];
-                load_block(xw, src + (size_t)r * stride + 16 * blk);
-                const uint32_t sc = quantise<kFormat>(xw, st, inv_st, w);
-                store_run<kFour ? 8 : 16>(tile + kv_tile(D, kFormat).code_bytes + kv_lane_byte(lane, (q * (D / 8) + 16 * b) / (kFour ? 2 : 1)), w);
-                if constexpr (kFour) tile[kv_v_scale_byte<D>(r, blk)] = (uint8_t)sc;
-            }
+        for (int x = 0; x < kAt; ++x) {
+            int r, blk;
+            place(x0 + x, r, blk);
+            uint32_t w[4];
+            const uint32_t sc = quantise<kFormat>(xw[x], st, inv_st, w);
+            store_codes<D, kFormat, kV>(tile, r, 16 * blk, w);
+            if constexpr (kFour) tile[kV ? kv_v_scale_byte<D>(r, blk) : kv_k_scale_byte<D>(r, blk)] = (uint8_t)sc;
+        }
     }
 }
 
@@ -319,7 +339,7 @@ __device__ __forceinline__ void append_tile(uint8_t* tile, const __nv_bfloat16* 
 
 // A warp per 16 tokens of the call and head, K then V.
 template <int D, int kFormat>
-__global__ void __launch_bounds__(256) kv_append_tiles_kernel(const KvView kv, const __nv_bfloat16* k, const __nv_bfloat16* v,
+__global__ void __launch_bounds__(256, 4) kv_append_tiles_kernel(const KvView kv, const __nv_bfloat16* k, const __nv_bfloat16* v,
                                                               size_t k_stride, size_t v_stride, const int32_t* slots, int n) {
     pdl_wait_and_release();
     const int lane = threadIdx.x & 31;
@@ -339,26 +359,31 @@ __global__ void __launch_bounds__(256) kv_append_tiles_kernel(const KvView kv, c
             if (is_v) append_tile<D, kFormat, true>(tile, from, stride, kv.v_scale, inv_v, lane);
             else append_tile<D, kFormat, false>(tile, from, stride, kv.k_scale, inv_k, lane);
         }
-        for (unsigned x = w.rest; x;) {                      // 32 / (D/16) tokens at a time
-            constexpr int kAt = 512 / D;
-            int tok = -1;
+        for (unsigned x = w.rest; x;) {                      // kAt tokens at a time, kBatch times under way
+            constexpr int kAt = 512 / D, kBatch = 2;
+            int tok[kBatch], slot[kBatch];
+            uint32_t xw[kBatch][8];
+            const int b = lane % (D / 16);
 #pragma unroll
-            for (int y = 0; y < kAt; ++y) {
-                const int bit = __ffs(x) - 1;
-                if (lane / (D / 16) == y && x) tok = bit;
-                x &= x - 1;
+            for (int z = 0; z < kBatch; ++z) {
+                tok[z] = pick<D>(x, lane);
+                slot[z] = __shfl_sync(0xffffffffu, w.slot, max(tok[z], 0));
+                if (tok[z] >= 0 && slot[z] >= 0) load_block(xw[z], src + (size_t)(first + tok[z]) * stride + 16 * b);
             }
-            const int slot = __shfl_sync(0xffffffffu, w.slot, max(tok, 0));
-            if (tok >= 0) {
-                if (slot >= 0) {
-                    uint8_t* tile = kv_tile_ptr(kv, slot, head, kv_tile(D, kFormat).bytes);
-                    const int b = lane % (D / 16);
-                    const __nv_bfloat16* from = src + (size_t)(first + tok) * stride + 16 * b;
-                    if (is_v) append_block<D, kFormat, true>(tile, slot & 15, b, from, kv.v_scale, inv_v);
-                    else append_block<D, kFormat, false>(tile, slot & 15, b, from, kv.k_scale, inv_k);
-                } else if (rest == 0 && lane % (D / 16) == 0 && slots[first + tok] != -1) {
-                    atomicOr(kv.status, FT_DEV_BAD_ID);
+#pragma unroll
+            for (int z = 0; z < kBatch; ++z) {
+                if (tok[z] < 0) continue;
+                if (slot[z] < 0) {
+                    if (rest == 0 && b == 0 && slots[first + tok[z]] != -1) atomicOr(kv.status, FT_DEV_BAD_ID);
+                    continue;
                 }
+                uint8_t* tile = kv_tile_ptr(kv, slot[z], head, kv_tile(D, kFormat).bytes);
+                const int r = slot[z] & 15;
+                uint32_t c[4];
+                const uint32_t sc = quantise<kFormat>(xw[z], is_v ? kv.v_scale : kv.k_scale, is_v ? inv_v : inv_k, c);
+                if constexpr (kFormat == FT_KV_NVFP4) tile[is_v ? kv_v_scale_byte<D>(r, b) : kv_k_scale_byte<D>(r, b)] = (uint8_t)sc;
+                if (is_v) store_codes<D, kFormat, true>(tile, r, 16 * b, c);
+                else store_codes<D, kFormat, false>(tile, r, 16 * b, c);
             }
         }
     }
@@ -373,17 +398,35 @@ __device__ __forceinline__ void read_tile(const uint8_t* tile, __nv_bfloat16* ds
     constexpr bool kFour = kFormat == FT_KV_NVFP4;
     constexpr int kVecs = kFour ? D / 64 : D / 32, kDims = kFour ? 32 : 16;      // vectors of a lane, codes of one
     constexpr int kRow = kV ? D / 8 : D / 4;                                     // dims of a token that the lane has
+    uint4 c[kVecs];
+    uint32_t sc[kVecs][kFour ? 4 : 1];
+    auto place = [&](int x, int y, int& r, int& d) {                             // of code y of vector x
+        const int at = x * kDims + y, q = at / kRow;
+        d = (kV ? g : t) * kRow + at % kRow;
+        r = kV ? 2 * t + (q & 1) + 8 * (q >> 1) : 8 * q + g;
+    };
+#pragma unroll
+    for (int x = 0; x < kVecs; ++x) {                                            // every load first
+        c[x] = *reinterpret_cast<const uint4*>(tile + (kV ? kv_tile(D, kFormat).code_bytes : 0) + x * 512 + lane * 16);
+        if constexpr (kFour) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) {
+                int r, d;
+                place(x, y, r, d);
+                sc[x][y / 8] = tile[kV ? kv_v_scale_byte<D>(r, d / 16) : kv_k_scale_byte<D>(r, d / 16)];
+            }
+        }
+    }
 #pragma unroll
     for (int x = 0; x < kVecs; ++x) {
-        const uint4 c = *reinterpret_cast<const uint4*>(tile + (kV ? kv_tile(D, kFormat).code_bytes : 0) + x * 512 + lane * 16);
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        const uint32_t w[4] = {c[x].x, c[x].y, c[x].z, c[x].w};
 #pragma unroll
         for (int y = 0; y < kDims; y += 8) {                                     // 8 codes: 16 bytes of a row
-            const int at = x * kDims + y, q = at / kRow, d = (kV ? g : t) * kRow + at % kRow;
-            const int r = kV ? 2 * t + (q & 1) + 8 * (q >> 1) : 8 * q + g;
+            int r, d;
+            place(x, y, r, d);
             uint32_t out[4];
             if constexpr (kFour) {
-                dequant_e2m1(w[y / 8], scale_pair(tile[kV ? kv_v_scale_byte<D>(r, d / 16) : kv_k_scale_byte<D>(r, d / 16)]), st, out);
+                dequant_e2m1(w[y / 8], scale_pair(sc[x][y / 8]), st, out);
             } else {
                 dequant_e4m3(w[y / 4], st, out);
                 dequant_e4m3(w[y / 4 + 1], st, out + 2);
@@ -396,7 +439,7 @@ __device__ __forceinline__ void read_tile(const uint8_t* tile, __nv_bfloat16* ds
 }  // namespace
 
 template <int D, int kFormat>
-__global__ void __launch_bounds__(256) kv_read_tiles_kernel(const KvView kv, const int32_t* slots, int n, __nv_bfloat16* k,
+__global__ void __launch_bounds__(256, 4) kv_read_tiles_kernel(const KvView kv, const int32_t* slots, int n, __nv_bfloat16* k,
                                                             __nv_bfloat16* v) {
     pdl_wait_and_release();
     const int lane = threadIdx.x & 31;
@@ -416,14 +459,7 @@ __global__ void __launch_bounds__(256) kv_read_tiles_kernel(const KvView kv, con
             else read_tile<D, kFormat, false>(tile, to, stride, kv.k_scale, lane);
         }
         for (unsigned x = w.rest; x;) {
-            constexpr int kAt = 512 / D;
-            int tok = -1;
-#pragma unroll
-            for (int y = 0; y < kAt; ++y) {
-                const int bit = __ffs(x) - 1;
-                if (lane / (D / 16) == y && x) tok = bit;
-                x &= x - 1;
-            }
+            const int tok = pick<D>(x, lane);
             const int slot = __shfl_sync(0xffffffffu, w.slot, max(tok, 0)), b = lane % (D / 16);
             if (tok < 0) continue;
             __nv_bfloat16* to = dst + (size_t)(first + tok) * stride + 16 * b;
