@@ -32,6 +32,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kMaxPerSm = 4;           // CTAs
+constexpr int kDirectTiles = 24;       // tiles of a warp at most for one cluster per unit
 // at least 2 places of the line per warp; a unit's start and end cost about 8 tiles
 template <int NT>
 using RowsLine = Line<kKvTile, 8 * NT, kWarps, 2 * kWarps, 8, 1>;
@@ -93,9 +94,49 @@ constexpr size_t rows_smem() {
 // CTAs per SM that the register allocation aims at.
 constexpr int rows_ctas(int D, int NT) { return D == 256 ? 2 : D == 128 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : 3; }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+    uint32_t d;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(p)), "r"(rank));
+    return d;
+}
+
+// A unit's sums from the CTAs of its cluster (each has its own in x [R][D] and ml): a slice of the
+// values per CTA, the CTAs' sums in the order of their ranks.
+template <int D, int R>
+__device__ __forceinline__ void join_cluster(const AttnArgs& a, const Unit& u, const float* x, const float2* ml) {
+    cluster_sync();
+    const int rank = blockIdx.x % a.split;
+    const int groups = min(R, u.si.n * a.G - u.r * R) * (D / 4);
+    for (int e = groups * rank / a.split + threadIdx.x; e < groups * (rank + 1) / a.split; e += kThreads) {
+        const int row = e / (D / 4), d = e % (D / 4) * 4;
+        float m = kNoRef, l = 0.f;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int c = 0; c < a.split; ++c) {
+            float2 p;
+            float4 y;
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(p.x), "=f"(p.y) : "r"(cluster_addr(ml + row, c)));
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w) : "r"(cluster_addr(x + row * D + d, c)));
+            const float mm = fmaxf(m, p.x), f = ex2(m - mm), g = ex2(p.x - mm);
+            m = mm;
+            l = l * f + p.y * g;
+            sum.x = sum.x * f + y.x * g; sum.y = sum.y * f + y.y * g; sum.z = sum.z * f + y.z * g; sum.w = sum.w * f + y.w * g;
+        }
+        const int grow = u.r * R + row;
+        store_out<4>(a, (size_t)(u.si.q0 + grow / a.G), u.h * a.G + grow % a.G, D, d, &sum.x, m, l);
+    }
+    cluster_sync();                                       // the others may still read this CTA's sums
+}
+
 }  // namespace
 
-template <int D, int kFormat, int NT>
+// kDirect: short sequences.  A cluster of a.split CTAs (1 to 16) takes one unit, its CTAs join through
+// distributed shared memory, and there is no line of shares, no workspace and no second kernel.
+template <int D, int kFormat, int NT, bool kDirect>
 __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(const AttnArgs a) {
     using L = RowsLine<NT>;
     constexpr int R = 8 * NT, kStages = stages(D, kFormat);
@@ -103,9 +144,10 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
     constexpr bool kFour = kFormat == FT_KV_NVFP4;
     constexpr int kKW = (kFour ? D / 4 : D / 2) / 4;       // 32-bit words of K codes per lane (both tokens)
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long prefix[kMaxSeqs + 1], scratch[kWarps];
+    __shared__ long long prefix[kDirect ? 1 : kMaxSeqs + 1], scratch[kWarps];
     __shared__ __align__(8) uint64_t bars[kWarps][kStages];
     __shared__ float join_m[kWarps][R], join_l[kWarps][R];
+    __shared__ float2 cluster_ml[R];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t bar0 = smem_u32(&bars[warp][0]);
@@ -115,19 +157,38 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
     }
     __syncwarp();
     pdl_wait_and_release();
-    line_prefix<L>(a, prefix, scratch);
-    const long long total = prefix[a.n_seqs];
-    const Shares shares(total, gridDim.x, L::kMin);
+    Unit u;
+    long long c0 = 0, c1 = 0, w0 = 0, w1 = 0;             // the CTA's and the warp's places in the line
+    bool whole = true;                                    // the CTA's share lies in one unit: its warps split the tiles
     const int cta = blockIdx.x;
     JoinTask* task = a.tasks + kWarps * cta + warp;
-    if (total == 0 || cta >= shares.nc) {
-        if (lane == 0) task->on = 0;
-        return;
+    Shares shares(1, 1LL, 0LL);
+    if constexpr (kDirect) {
+        const int id = cta / a.split;
+        u.h = id % a.kv.hkv;
+        u.r = id / a.kv.hkv % a.row_tiles;
+        u.s = id / a.kv.hkv / a.row_tiles;
+        u.si = seq_info(a, u.s);
+        if (u.si.bad && threadIdx.x == 0) atomicOr(a.kv.status, FT_DEV_BAD_ID);
+        if (u.r * R >= u.si.n * a.G) return;              // the whole cluster
+        u.rt = row_tile<L::kB>(a, u.si, u.r, R);
+        u.first = 0;
+        u.end = 1;
+    } else {
+        line_prefix<L>(a, prefix, scratch);
+        const long long total = prefix[a.n_seqs];
+        shares = Shares(total, gridDim.x, L::kMin);
+        if (total == 0 || cta >= shares.nc) {
+            if (lane == 0) task->on = 0;
+            return;
+        }
+        c0 = shares.cut(cta);
+        c1 = shares.cut(cta + 1);
+        u = find_unit<L>(a, prefix, c0);
+        whole = c1 <= u.end;
+        w0 = c0 + (c1 - c0) * warp / kWarps;
+        w1 = c0 + (c1 - c0) * (warp + 1) / kWarps;
     }
-    const long long c0 = shares.cut(cta), c1 = shares.cut(cta + 1);
-    Unit u = find_unit<L>(a, prefix, c0);
-    const bool whole = c1 <= u.end;                       // the CTA's share lies in one unit: its warps split the tiles
-    const long long w0 = c0 + (c1 - c0) * warp / kWarps, w1 = c0 + (c1 - c0) * (warp + 1) / kWarps;
     uint8_t* ring = smem + (size_t)warp * kStages * kT.bytes;
     const uint32_t ring_u32 = smem_u32(ring);
     uint32_t parity = 0;                                  // bit s: phase of stage s to wait for
@@ -146,19 +207,32 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
     for (long long pos = w0; pos < w1 || whole; pos = u.end) {
         if (!whole && (pos >= u.end || pos < u.first)) u = find_unit<L>(a, prefix, pos);
         int v0 = block_at<L>(u.first, u.rt.nt, whole ? c0 : pos), v1 = block_at<L>(u.first, u.rt.nt, whole ? c1 : w1);
+        if constexpr (kDirect) {
+            v0 = (int)((long long)u.rt.nt * (cta % a.split) / a.split);
+            v1 = (int)((long long)u.rt.nt * (cta % a.split + 1) / a.split);
+        }
         const int cv0 = v0, cv1 = v1;
         if (whole) {
             v0 = cv0 + (cv1 - cv0) * warp / kWarps;
             v1 = cv0 + (cv1 - cv0) * (warp + 1) / kWarps;
         }
-        if (cv0 == cv1) {                                 // none of the unit's tiles
+        if (!kDirect && cv0 == cv1) {                     // none of the unit's tiles
             if (pos == w0) note_task(u);
             if (whole) break;
             continue;
         }
         const int base = u.si.len - u.si.n, row0 = u.r * R;
 
-        // ---------------------------------------------------------------- the first copies
+        // ---------------------------------------------------------------- the rows' loads, the first copies
+        uint4 raw[NT][D / 32];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = row0 + 8 * nt + g, i = row / a.G;
+            const __nv_bfloat16* src = a.q + (size_t)(u.si.q0 + i) * a.q_stride + (size_t)(u.h * a.G + row - i * a.G) * D + t * (D / 4);
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e)
+                raw[nt][e] = i < u.si.n ? *reinterpret_cast<const uint4*>(src + 8 * e) : make_uint4(0, 0, 0, 0);
+        }
         // lane x of the warp holds the page of tile v0 + 32 * (group of 32) + x
         const int32_t* table = a.table + (size_t)u.s * a.table_stride;
         const int per = a.kv.page_shift - 4;              // log2 of the tiles of a page
@@ -207,26 +281,25 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
         int lim_min = 0x7fffffff, low_max = 0;            // keys that every row sees: below lim_min, from low_max
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = row0 + 8 * nt + g, i = row / a.G;
-            const bool on = i < u.si.n;
-            const __nv_bfloat16* src = a.q + (size_t)(u.si.q0 + i) * a.q_stride + (size_t)(u.h * a.G + row % a.G) * D + t * (D / 4);
-            uint32_t raw[D / 8];
             float amax = 0.f;
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
-                const uint4 x = on ? *reinterpret_cast<const uint4*>(src + 8 * e) : make_uint4(0, 0, 0, 0);
-                raw[4 * e] = x.x; raw[4 * e + 1] = x.y; raw[4 * e + 2] = x.z; raw[4 * e + 3] = x.w;
-            }
+                const uint32_t wd[4] = {raw[nt][e].x, raw[nt][e].y, raw[nt][e].z, raw[nt][e].w};
 #pragma unroll
-            for (int e = 0; e < D / 8; ++e)
-                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(raw[e] << 16)), fabsf(__uint_as_float(raw[e] & 0xFFFF0000u))));
+                for (int y = 0; y < 4; ++y)
+                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(wd[y] << 16)), fabsf(__uint_as_float(wd[y] & 0xFFFF0000u))));
+            }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             const RowScale rs = row_scale(amax);
 #pragma unroll
-            for (int e = 0; e < D / 8; ++e)
-                qf[nt][e >> 1][e & 1] = pack_f16(__uint_as_float(raw[e] << 16) * rs.down,
-                                                 __uint_as_float(raw[e] & 0xFFFF0000u) * rs.down);
+            for (int e = 0; e < D / 32; ++e) {
+                const uint32_t wd[4] = {raw[nt][e].x, raw[nt][e].y, raw[nt][e].z, raw[nt][e].w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    qf[nt][2 * e + (y >> 1)][y & 1] = pack_f16(__uint_as_float(wd[y] << 16) * rs.down,
+                                                               __uint_as_float(wd[y] & 0xFFFF0000u) * rs.down);
+            }
             const float c = a.scale * a.kv.k_scale * 1.44269504088896340736f * rs.up;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -254,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
 
-        if (pos == w0) note_task(u);                      // while the first tiles are under way
+        if (!kDirect && pos == w0) note_task(u);          // while the first tiles are under way
 
         // ---------------------------------------------------------------- the keys
         for (int v = v0; v < vend; ++v) {
@@ -509,8 +582,8 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                         *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][nt][b] * f, acc[i][nt][2 + b] * f);
                 }
             __syncthreads();
-            const bool done = cv0 == 0 && cv1 == u.rt.nt;
-            float* out = partial<D, R>(a, 2 * kWarps * cta + (cv0 > 0 ? 0 : 1));
+            const bool done = kDirect ? a.split == 1 : cv0 == 0 && cv1 == u.rt.nt;
+            float* out = kDirect ? nullptr : partial<D, R>(a, 2 * kWarps * cta + (cv0 > 0 ? 0 : 1));
             for (int e = threadIdx.x; e < R * D / 4; e += kThreads) {
                 const int row = e / (D / 4), d = e % (D / 4) * 4;
                 const int i = (row0 + row) / a.G;
@@ -528,11 +601,15 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                 if (done) {
                     const int h = u.h * a.G + (row0 + row) % a.G;
                     store_out<4>(a, (size_t)(u.si.q0 + i), h, D, d, &x.x, mm, ll);
+                } else if (kDirect) {                     // for the cluster: in the place of warp 0's
+                    *reinterpret_cast<float4*>(buf + (size_t)row * D + d) = x;
+                    if (d == 0) cluster_ml[row] = make_float2(mm, ll);
                 } else {
                     *reinterpret_cast<float4*>(out + 2 * R + row * D + d) = x;
                     if (d == 0) reinterpret_cast<float2*>(out)[row] = make_float2(mm, ll);
                 }
             }
+            if (kDirect && a.split > 1) join_cluster<D, R>(a, u, buf, cluster_ml);
             break;
         }
 
@@ -566,7 +643,8 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
 
 namespace {
 
-// CTAs of the rows kernel (looked up once per device): every one resident at once.
+// CTAs of the rows kernel that are resident at once (0 when it cannot be set up; looked up once per
+// device).
 template <int D, int kFormat, int NT>
 int rows_grid() {
     static std::atomic<int> grids[kMaxDevices];
@@ -577,11 +655,15 @@ int rows_grid() {
     }
     int v = grids[dev].load(std::memory_order_relaxed);
     if (!v) {
-        auto kern = kv_rows_kernel<D, kFormat, NT>;
+        auto kern = kv_rows_kernel<D, kFormat, NT, false>;
+        auto direct = kv_rows_kernel<D, kFormat, NT, true>;
         constexpr size_t smem = rows_smem<D, kFormat, NT>();
         int n = 0;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-            all_shared(kern) != cudaSuccess || all_shared(kv_join_kernel<RowsLine<NT>, D>) != cudaSuccess ||
+            cudaFuncSetAttribute(direct, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+            cudaFuncSetAttribute(direct, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+            all_shared(kern) != cudaSuccess || all_shared(direct) != cudaSuccess ||
+            all_shared(kv_join_kernel<RowsLine<NT>, D>) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem) != cudaSuccess) {
             cudaGetLastError();
             return 0;
@@ -593,10 +675,36 @@ int rows_grid() {
 }
 
 template <int D, int kFormat, int NT>
-cudaError_t run_rows(const AttnArgs& a, cudaStream_t s) {
+cudaError_t run_rows(AttnArgs a, cudaStream_t s) {
     const int grid = rows_grid<D, kFormat, NT>();
     if (grid < 1) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_pdl(kv_rows_kernel<D, kFormat, NT>, dim3(grid), dim3(kThreads), rows_smem<D, kFormat, NT>(), s, a);
+    // The host knows how long a sequence can be at most.  Direct where that leaves a warp few tiles
+    // with all of a unit's CTAs in one cluster and all clusters (nearly) at once: it saves the scan of
+    // the lengths, the partial sums and the second kernel (one token over 4096 of 2 heads of 256: 14.1
+    // us by shares), but a unit's length is not evened out over the SMs.
+    a.row_tiles = (int)(((long long)a.max_q * a.G + 8 * NT - 1) / (8 * NT));
+    const long long units = (long long)a.n_seqs * a.kv.hkv * a.row_tiles;
+    long long tiles = ((long long)a.table_stride << a.kv.page_shift) / kKvTile;
+    if (a.window > 0) tiles = min(tiles, ((long long)a.window + a.max_q + a.n_sink) / kKvTile + 4);
+    a.split = 1;
+    while (a.split < 16 && units * a.split * 2 <= grid && tiles > kWarps * a.split) a.split *= 2;
+    if (tiles <= kDirectTiles * kWarps * a.split && units * a.split <= 2LL * grid) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(units * a.split));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = rows_smem<D, kFormat, NT>();
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = a.split;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = a.split > 1 ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, kv_rows_kernel<D, kFormat, NT, true>, a);
+    }
+    const cudaError_t e = launch_pdl(kv_rows_kernel<D, kFormat, NT, false>, dim3(grid), dim3(kThreads), rows_smem<D, kFormat, NT>(), s, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(kv_join_kernel<RowsLine<NT>, D>, dim3(grid), dim3(kJoinThreads), 0, s, a);
 }
@@ -604,7 +712,7 @@ cudaError_t run_rows(const AttnArgs& a, cudaStream_t s) {
 template <int D, int kFormat>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     const long long rows = (long long)a.max_q * a.G;
-    if (rows > 16) return launch_kv_tiles(a, D, kFormat, s);
+    if (rows > 32) return launch_kv_tiles(a, D, kFormat, s);
     return rows <= 8 ? run_rows<D, kFormat, 1>(a, s) : run_rows<D, kFormat, 2>(a, s);
 }
 

@@ -181,7 +181,7 @@ struct Shares {
     int nc;
     long long q, rem;
     __device__ __forceinline__ Shares(int nc_, long long q_, long long rem_) : nc(nc_), q(q_), rem(rem_) {}
-    __device__ __forceinline__ Shares(long long total, int grid, int least) {
+    __device__ __forceinline__ Shares(long long total, unsigned grid, int least) {
         nc = (int)min((long long)grid, max((total + least - 1) / least, 1LL));
         q = total / nc;
         rem = total - q * nc;

@@ -32,14 +32,14 @@ class Case:
     oracle's values of every token."""
 
     def __init__(self, ft, fmt="nvfp4", D=128, hkv=2, G=4, page=16, lens=(40,), nq=(1,), seed=0, L=2, layer=1,
-                 k_scale=0.5, v_scale=0.25, masks=None, kmul=1.0):
+                 k_scale=0.5, v_scale=0.25, masks=None, kmul=1.0, spare=1):
         rng = np.random.default_rng(seed)
         self.ft, self.fmt, self.D, self.hkv, self.G, self.layer = ft, fmt, D, hkv, G, layer
         self.lens, self.nq, self.masks, self.page = list(lens), list(nq), masks, page
         per = [-(-n // page) for n in lens]
         n_pages = sum(per) + 3
         order = rng.permutation(n_pages)
-        stride = max(per + [1]) + 1
+        stride = max(per + [1]) + spare                      # spare columns: the longest sequence the host can expect
         table = np.full((len(lens), stride), -1, np.int32)              # never read past the keys
         self.kv = ft.KVCache(L, n_pages, page, hkv, D, hkv * G, max(len(lens), 1), fmt, k_scale, v_scale,
                              pool=torch.full((ft.ft_kv_required_sizes(ft.FtKvDesc(
@@ -481,3 +481,19 @@ def test_negative_and_zero_scale(ft, n):
                 got = o[at:at + n, h].double().cpu().numpy()
                 assert np.all(np.abs(got - ro) <= 2.0 ** -8 * np.abs(ro) + (2 * e + 2.0 ** -10) * av + length * 2.0 ** -24 * np.abs(c.vval[s]).max())
                 assert np.allclose(z[at:at + n, h].double().cpu().numpy(), rl, rtol=1e-6, atol=1e-5)
+
+
+@pytest.mark.parametrize("fmt,D,G,page", [("nvfp4", 128, 4, 16), ("fp8", 64, 1, 64), ("nvfp4", 256, 8, 32), ("fp8", 256, 3, 16),
+                                          ("fp8", 128, 16, 16), ("nvfp4", 64, 16, 128)])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (33, 5)])
+def test_long_tables(ft, fmt, D, G, page, window, n_sink):
+    """Tables wide enough for sequences far longer than the present ones: the same answers."""
+    rng = np.random.default_rng(21)
+    lens = [1, 700, 15, 0, 64, 129, 300, 17, 16, 40] + [int(x) for x in rng.integers(1, 60, 30)]
+    nq = [1, 1, 1, 2, 1, 2, 1, 1, 0, 1] + [1] * 30
+    kw = dict(seed=D, spare=(1 << 17) // page)
+    Case(ft, fmt, D, 2, G, page, lens, nq, **kw).both(window=window, n_sink=n_sink)
+    if G <= 8:
+        masks = [tree(rng, n) for n in (4, 3, 1)]
+        Case(ft, fmt, D, 1, G, page, [4, 260, 90], [4, 3, 1], masks=masks, **kw).both(window=window, n_sink=n_sink)
+    Case(ft, fmt, D, 1, G, page, [5000], [1], **kw).both(window=window, n_sink=n_sink)
