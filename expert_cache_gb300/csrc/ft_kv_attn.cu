@@ -84,15 +84,32 @@ constexpr int stages(int D, int format) {
     return b <= 1152 ? 8 : b <= 2304 ? 4 : b <= 4096 ? 3 : 2;
 }
 
+// Floats of a row where the warps of a CTA join: [D/16][g 8][2] (dims g D/8 + 2 i), padded so that the
+// 32 lanes of a store (8 g, 4 rows) spread over the banks.
+constexpr int join_row(int D) { return D + 8; }
+template <int D>
+__device__ __forceinline__ int join_at(int row, int i, int g) { return row * join_row(D) + i * 16 + g * 2; }
+// The e-th four values of a row block: row, first dim, place of the first two (the others: 16 floats on).
+template <int D>
+__device__ __forceinline__ void join_group(int e, int& row, int& d, int& at) {
+    row = e / (D / 4);
+    const int q = e % (D / 4), g = q & 7, i = (q >> 3) * 2;
+    d = g * (D / 8) + 2 * i;
+    at = join_at<D>(row, i, g);
+}
+
+// Heads of 256: q's fragments (32 registers a row tile) stay in shared memory, so that three CTAs fit.
+constexpr bool q_in_smem(int D) { return D == 256; }
+
 template <int D, int kFormat, int NT>
 constexpr size_t rows_smem() {
     const size_t ring = (size_t)kWarps * stages(D, kFormat) * kv_tile(D, kFormat).bytes;
-    const size_t join = (size_t)kWarps * 8 * NT * D * 4;
-    return ring > join ? ring : join;
+    const size_t join = (size_t)kWarps * 8 * NT * join_row(D) * 4;
+    return (ring > join ? ring : join) + (q_in_smem(D) ? (size_t)kWarps * NT * D * 16 : 0);
 }
 
 // CTAs per SM that the register allocation aims at.
-constexpr int rows_ctas(int D, int NT) { return D == 256 ? 2 : D == 128 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : 3; }
+constexpr int rows_ctas(int D, int NT) { return D == 256 ? (NT == 1 ? 3 : 2) : D == 128 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : 3; }
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -103,31 +120,47 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
     return d;
 }
 
-// A unit's sums from the CTAs of its cluster (each has its own in x [R][D] and ml): a slice of the
-// values per CTA, the CTAs' sums in the order of their ranks.
+// A unit's sums from the CTAs of its cluster (each has its own in x and ml): a slice of the
+// values per CTA.  A team of lanes takes four values: lane k of it the ranks k, k + team, ..., then a
+// butterfly, so the order of the sums is fixed.
 template <int D, int R>
 __device__ __forceinline__ void join_cluster(const AttnArgs& a, const Unit& u, const float* x, const float2* ml) {
     cluster_sync();
     const int rank = blockIdx.x % a.split;
     const int groups = min(R, u.si.n * a.G - u.r * R) * (D / 4);
-    for (int e = groups * rank / a.split + threadIdx.x; e < groups * (rank + 1) / a.split; e += kThreads) {
-        const int row = e / (D / 4), d = e % (D / 4) * 4;
+    const int ga = groups * rank / a.split, gb = groups * (rank + 1) / a.split;
+    int team = 1;
+    while (team < a.split && team * 2 * (gb - ga) <= kThreads) team *= 2;
+    for (int g0 = ga; g0 < gb; g0 += kThreads / team) {
+        int row, d, at;
+        join_group<D>(min(g0 + (int)threadIdx.x / team, gb - 1), row, d, at);
         float m = kNoRef, l = 0.f;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int c = 0; c < a.split; ++c) {
+        for (int c = threadIdx.x & (team - 1); c < a.split; c += team) {
             float2 p;
             float4 y;
             asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(p.x), "=f"(p.y) : "r"(cluster_addr(ml + row, c)));
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w) : "r"(cluster_addr(x + row * D + d, c)));
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(y.x), "=f"(y.y) : "r"(cluster_addr(x + at, c)));
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(y.z), "=f"(y.w) : "r"(cluster_addr(x + at + 16, c)));
             const float mm = fmaxf(m, p.x), f = ex2(m - mm), g = ex2(p.x - mm);
             m = mm;
             l = l * f + p.y * g;
             sum.x = sum.x * f + y.x * g; sum.y = sum.y * f + y.y * g; sum.z = sum.z * f + y.z * g; sum.w = sum.w * f + y.w * g;
         }
-        const int grow = u.r * R + row;
-        store_out<4>(a, (size_t)(u.si.q0 + grow / a.G), u.h * a.G + grow % a.G, D, d, &sum.x, m, l);
+        for (int o = 1; o < team; o <<= 1) {
+            const float om = __shfl_xor_sync(0xffffffffu, m, o), mm = fmaxf(m, om), f = ex2(m - mm), of = ex2(om - mm);
+            const float ol = __shfl_xor_sync(0xffffffffu, l, o);
+            const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, sum.x, o), __shfl_xor_sync(0xffffffffu, sum.y, o),
+                                         __shfl_xor_sync(0xffffffffu, sum.z, o), __shfl_xor_sync(0xffffffffu, sum.w, o));
+            m = mm;
+            l = l * f + ol * of;
+            sum.x = sum.x * f + y.x * of; sum.y = sum.y * f + y.y * of; sum.z = sum.z * f + y.z * of; sum.w = sum.w * f + y.w * of;
+        }
+        if (g0 + (int)threadIdx.x / team < gb && (threadIdx.x & (team - 1)) == 0) {
+            const int grow = u.r * R + row;
+            store_out<4>(a, (size_t)(u.si.q0 + grow / a.G), u.h * a.G + grow % a.G, D, d, &sum.x, m, l);
+        }
     }
     cluster_sync();                                       // the others may still read this CTA's sums
 }
@@ -147,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
     __shared__ long long prefix[kDirect ? 1 : kMaxSeqs + 1], scratch[kWarps];
     __shared__ __align__(8) uint64_t bars[kWarps][kStages];
     __shared__ float join_m[kWarps][R], join_l[kWarps][R];
-    __shared__ float2 cluster_ml[R];
+    __shared__ float2 row_ml[R];                          // the CTA's references and sums
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t bar0 = smem_u32(&bars[warp][0]);
@@ -191,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
     }
     uint8_t* ring = smem + (size_t)warp * kStages * kT.bytes;
     const uint32_t ring_u32 = smem_u32(ring);
+    uint2* q_frag = reinterpret_cast<uint2*>(smem + rows_smem<D, kFormat, NT>()) - (kWarps - warp) * NT * (D / 16) * 32;   // heads of 256
     uint32_t parity = 0;                                  // bit s: phase of stage s to wait for
     int next = 0;                                         // stage that the next tile takes
 
@@ -276,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
         }
         // ---------------------------------------------------------------- the rows
         RowRule rule[NT][2];
-        uint32_t qf[NT][D / 16][2];
+        uint32_t qf[NT][q_in_smem(D) ? 1 : D / 16][2];
         float coef[NT][2], m[NT][2], l[NT][2];
         int lim_min = 0x7fffffff, low_max = 0;            // keys that every row sees: below lim_min, from low_max
 #pragma unroll
@@ -295,10 +329,17 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
                 const uint32_t wd[4] = {raw[nt][e].x, raw[nt][e].y, raw[nt][e].z, raw[nt][e].w};
+                uint32_t o[4];
 #pragma unroll
                 for (int y = 0; y < 4; ++y)
-                    qf[nt][2 * e + (y >> 1)][y & 1] = pack_f16(__uint_as_float(wd[y] << 16) * rs.down,
-                                                               __uint_as_float(wd[y] & 0xFFFF0000u) * rs.down);
+                    o[y] = pack_f16(__uint_as_float(wd[y] << 16) * rs.down, __uint_as_float(wd[y] & 0xFFFF0000u) * rs.down);
+                if constexpr (q_in_smem(D)) {
+                    q_frag[(nt * (D / 16) + 2 * e) * 32 + lane] = make_uint2(o[0], o[1]);
+                    q_frag[(nt * (D / 16) + 2 * e + 1) * 32 + lane] = make_uint2(o[2], o[3]);
+                } else {
+                    qf[nt][2 * e][0] = o[0]; qf[nt][2 * e][1] = o[1];
+                    qf[nt][2 * e + 1][0] = o[2]; qf[nt][2 * e + 1][1] = o[3];
+                }
             }
             const float c = a.scale * a.kv.k_scale * 1.44269504088896340736f * rs.up;
 #pragma unroll
@@ -328,6 +369,11 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                 for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
 
         if (!kDirect && pos == w0) note_task(u);          // while the first tiles are under way
+
+        auto q_of = [&](int nt, int x) {                  // the lane's fragment of k-step x
+            if constexpr (q_in_smem(D)) return q_frag[(nt * (D / 16) + x) * 32 + lane];
+            else return make_uint2(qf[nt][x][0], qf[nt][x][1]);
+        };
 
         // ---------------------------------------------------------------- the keys
         for (int v = v0; v < vend; ++v) {
@@ -386,8 +432,10 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                         for (int x = 0; x < 4; ++x)
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma(sc[nt], f[0][2 * x], f[1][2 * x], f[0][2 * x + 1], f[1][2 * x + 1],
-                                    qf[nt][4 * b + x][0], qf[nt][4 * b + x][1]);
+                            {
+                                const uint2 q = q_of(nt, 4 * b + x);
+                                mma(sc[nt], f[0][2 * x], f[1][2 * x], f[0][2 * x + 1], f[1][2 * x + 1], q.x, q.y);
+                            }
                     }
                 } else {
 #pragma unroll
@@ -396,7 +444,10 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                         e4m3_unpack(kw[x], a0, a2);
                         e4m3_unpack(kw[D / 16 + x], a1, a3);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma(sc[nt], a0, a1, a2, a3, qf[nt][x][0], qf[nt][x][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint2 q = q_of(nt, x);
+                            mma(sc[nt], a0, a1, a2, a3, q.x, q.y);
+                        }
                     }
                 }
             }
@@ -576,40 +627,48 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
 #pragma unroll
                     for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, join_m[w][row]);
                     const float f = ex2(m[nt][b] - mm);
-                    float* dst = buf + ((size_t)warp * R + row) * D + g * (D / 8);
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i)
-                        *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(acc[i][nt][b] * f, acc[i][nt][2 + b] * f);
+                        *reinterpret_cast<float2*>(buf + warp * R * join_row(D) + join_at<D>(row, i, g)) =
+                            make_float2(acc[i][nt][b] * f, acc[i][nt][2 + b] * f);
                 }
-            __syncthreads();
-            const bool done = kDirect ? a.split == 1 : cv0 == 0 && cv1 == u.rt.nt;
-            float* out = kDirect ? nullptr : partial<D, R>(a, 2 * kWarps * cta + (cv0 > 0 ? 0 : 1));
-            for (int e = threadIdx.x; e < R * D / 4; e += kThreads) {
-                const int row = e / (D / 4), d = e % (D / 4) * 4;
-                const int i = (row0 + row) / a.G;
-                if (i >= u.si.n) continue;
+            if (threadIdx.x < R) {
+                const int row = threadIdx.x;
                 float mm = join_m[0][row], ll = 0.f;
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, join_m[w][row]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) ll += join_l[w][row] * ex2(join_m[w][row] - mm);
+                row_ml[row] = make_float2(mm, ll);
+            }
+            __syncthreads();
+            const bool done = kDirect ? a.split == 1 : cv0 == 0 && cv1 == u.rt.nt;
+            float* out = kDirect ? nullptr : partial<D, R>(a, 2 * kWarps * cta + (cv0 > 0 ? 0 : 1));
+            const int groups = min(R, u.si.n * a.G - row0) * (D / 4);
+#pragma unroll 4
+            for (int e = threadIdx.x; e < groups; e += kThreads) {
+                int row, d, at;
+                join_group<D>(e, row, d, at);
+                const float2 ml = row_ml[row];
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    ll += join_l[w][row] * ex2(join_m[w][row] - mm);
-                    const float4 y = *reinterpret_cast<const float4*>(buf + ((size_t)w * R + row) * D + d);
-                    x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+                    const float2 y = *reinterpret_cast<const float2*>(buf + w * R * join_row(D) + at);
+                    const float2 z = *reinterpret_cast<const float2*>(buf + w * R * join_row(D) + at + 16);
+                    x.x += y.x; x.y += y.y; x.z += z.x; x.w += z.y;
                 }
                 if (done) {
-                    const int h = u.h * a.G + (row0 + row) % a.G;
-                    store_out<4>(a, (size_t)(u.si.q0 + i), h, D, d, &x.x, mm, ll);
+                    const int i = (row0 + row) / a.G;
+                    store_out<4>(a, (size_t)(u.si.q0 + i), u.h * a.G + row0 + row - i * a.G, D, d, &x.x, ml.x, ml.y);
                 } else if (kDirect) {                     // for the cluster: in the place of warp 0's
-                    *reinterpret_cast<float4*>(buf + (size_t)row * D + d) = x;
-                    if (d == 0) cluster_ml[row] = make_float2(mm, ll);
+                    *reinterpret_cast<float2*>(buf + at) = make_float2(x.x, x.y);
+                    *reinterpret_cast<float2*>(buf + at + 16) = make_float2(x.z, x.w);
                 } else {
                     *reinterpret_cast<float4*>(out + 2 * R + row * D + d) = x;
-                    if (d == 0) reinterpret_cast<float2*>(out)[row] = make_float2(mm, ll);
+                    if (d == 0) reinterpret_cast<float2*>(out)[row] = ml;
                 }
             }
-            if (kDirect && a.split > 1) join_cluster<D, R>(a, u, buf, cluster_ml);
+            if (kDirect && a.split > 1) join_cluster<D, R>(a, u, buf, row_ml);
             break;
         }
 
