@@ -299,12 +299,18 @@ __device__ __forceinline__ JoinTask join_task(const Shares& sh, const Unit& u, i
 }
 
 // Slice `part` of `parts` of unit u's output from its pieces, by n_threads threads (a multiple of
-// 32, whole warps, `sync` between them).  A team of lanes takes four values of a row: lane k of it
-// the pieces k, k + team, ..., then a butterfly, so the order of the sums is fixed.  Teams are as
-// large as the slice leaves threads for.  slots: shared, 2 kW + CTAs of the unit.
+// 32, whole warps, `sync` between them).  A team of threads takes four values of a row: thread k of it
+// the pieces k, k + team, ..., then one of them their sums in order, so the order is fixed.  Teams
+// are as large as the slice leaves threads for; neighbouring threads have neighbouring values of the
+// same piece, so that partial sums are read in whole sectors.  slots: shared, 2 kW + CTAs of the
+// unit; sums: shared, one per thread.
+struct TeamSum {
+    float m, l;
+    float4 x;
+};
 template <typename L, int D, typename Sync>
 __device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u, int part, int parts, int thread,
-                                           int n_threads, int* slots, Sync sync) {
+                                           int n_threads, int* slots, TeamSum* sums, Sync sync) {
     constexpr int R = L::kR;
     const Shares sh(u.nc, u.q, u.rem);
     const int ca = u.ca, cb = u.cb;
@@ -325,13 +331,14 @@ __device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u,
     const int ga = (int)((long long)groups * part / parts), gb = (int)((long long)groups * (part + 1) / parts);
     int team = 1;
     while (team < 32 && team < n && (gb - ga) * team < n_threads) team *= 2;
-    for (int g0 = ga; g0 < gb; g0 += n_threads / team) {
-        const int e = min(g0 + thread / team, gb - 1);
+    const int wide = n_threads / team, mine = thread % wide, first = thread / wide;
+    for (int g0 = ga; g0 < gb; g0 += wide) {
+        const int e = min(g0 + mine, gb - 1);
         const int row = e / (D / 4), d = e % (D / 4) * 4;
         float m = kNoRef, l = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         constexpr int kBatch = 8;                         // pieces in flight
-        for (int k0 = thread & (team - 1); k0 < n; k0 += team * kBatch) {
+        for (int k0 = first; k0 < n; k0 += team * kBatch) {
             float pm[kBatch], pl[kBatch];
             float4 y[kBatch];
             float mm = m;
@@ -362,16 +369,21 @@ __device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u,
                 x.x += y[b].x * f; x.y += y[b].y * f; x.z += y[b].z * f; x.w += y[b].w * f;
             }
         }
-        for (int o = 1; o < team; o <<= 1) {
-            const float om = __shfl_xor_sync(0xffffffffu, m, o), mm = fmaxf(m, om), f = ex2(m - mm), of = ex2(om - mm);
-            const float ol = __shfl_xor_sync(0xffffffffu, l, o);
-            const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o),
-                                         __shfl_xor_sync(0xffffffffu, x.z, o), __shfl_xor_sync(0xffffffffu, x.w, o));
-            m = mm;
-            l = l * f + ol * of;
-            x.x = x.x * f + y.x * of; x.y = x.y * f + y.y * of; x.z = x.z * f + y.z * of; x.w = x.w * f + y.w * of;
+        if (team > 1) {
+            sums[thread] = {m, l, x};
+            sync();
+            if (first == 0) {
+                for (int k = 1; k < team; ++k) {
+                    const TeamSum o = sums[k * wide + mine];
+                    const float mm = fmaxf(m, o.m), f = ex2(m - mm), of = ex2(o.m - mm);
+                    m = mm;
+                    l = l * f + o.l * of;
+                    x.x = x.x * f + o.x.x * of; x.y = x.y * f + o.x.y * of; x.z = x.z * f + o.x.z * of; x.w = x.w * f + o.x.w * of;
+                }
+            }
+            sync();
         }
-        if (g0 + thread / team < gb && (thread & (team - 1)) == 0) {
+        if (g0 + mine < gb && first == 0) {
             const int grow = u.r * R + row;
             store_out<4>(a, (size_t)(u.q0 + grow / a.G), u.h * a.G + grow % a.G, D, d, &x.x, m, l);
         }
@@ -384,6 +396,7 @@ __device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u,
 template <typename L, int D>
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttnArgs a) {
     __shared__ int slots[2 * L::kW + kMaxShares], warp_slots[L::kW][L::kW];
+    __shared__ TeamSum sums[kJoinThreads];
     pdl_wait_and_release();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = blockIdx.x / L::kSplit, sub = blockIdx.x % L::kSplit;
@@ -393,8 +406,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttnArgs a)
     if (warp > 0 && warp < L::kW && sub == 0) mine = a.tasks[L::kW * cta + warp];
     if (all.on)
         join_slice<L, D>(a, all, (cta - all.ca - 1) * L::kSplit + sub, (all.cb - all.ca) * L::kSplit, threadIdx.x,
-                         kJoinThreads, slots, [] { __syncthreads(); });
-    if (mine.on) join_slice<L, D>(a, mine, 0, 1, lane, 32, warp_slots[warp], [] { __syncwarp(); });
+                         kJoinThreads, slots, sums, [] { __syncthreads(); });
+    if (mine.on) {
+        __syncwarp();
+        join_slice<L, D>(a, mine, 0, 1, lane, 32, warp_slots[warp], sums + 32 * warp, [] { __syncwarp(); });
+    }
 }
 
 }  // namespace ft
