@@ -35,7 +35,7 @@ constexpr int kMaxPerSm = 4;           // CTAs
 constexpr int kDirectTiles = 24;       // tiles of a warp at most for one cluster per unit
 // at least 2 places of the line per warp; a unit's start and end cost about 8 tiles
 template <int NT>
-using RowsLine = Line<kKvTile, 8 * NT, kWarps, 2 * kWarps, 8, 1>;
+using RowsLine = Line<kKvTile, 8 * NT, kWarps, 2 * kWarps, 8, 2>;
 constexpr long kWaitLimit = 1L << 24;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -765,7 +765,7 @@ cudaError_t run_rows(AttnArgs a, cudaStream_t s) {
     }
     const cudaError_t e = launch_pdl(kv_rows_kernel<D, kFormat, NT, false>, dim3(grid), dim3(kThreads), rows_smem<D, kFormat, NT>(), s, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv_join_kernel<RowsLine<NT>, D>, dim3(grid), dim3(kJoinThreads), 0, s, a);
+    return launch_pdl(kv_join_kernel<RowsLine<NT>, D>, dim3(grid * RowsLine<NT>::kSplit), dim3(kJoinThreads), 0, s, a);
 }
 
 template <int D, int kFormat>

@@ -400,13 +400,14 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttnArgs a)
     pdl_wait_and_release();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cta = blockIdx.x / L::kSplit, sub = blockIdx.x % L::kSplit;
+    constexpr int kParts = L::kW == 1 ? L::kSplit : L::kSplit - 1;       // the last CTA of a share has its warps' units
     const JoinTask all = a.tasks[L::kW * cta];
     JoinTask mine;
     mine.on = 0;
-    if (warp > 0 && warp < L::kW && sub == 0) mine = a.tasks[L::kW * cta + warp];
-    if (all.on)
-        join_slice<L, D>(a, all, (cta - all.ca - 1) * L::kSplit + sub, (all.cb - all.ca) * L::kSplit, threadIdx.x,
-                         kJoinThreads, slots, sums, [] { __syncthreads(); });
+    if (warp > 0 && warp < L::kW && sub == L::kSplit - 1) mine = a.tasks[L::kW * cta + warp];
+    if (all.on && (L::kW == 1 || sub < L::kSplit - 1))
+        join_slice<L, D>(a, all, (cta - all.ca - 1) * kParts + sub, (all.cb - all.ca) * kParts, threadIdx.x, kJoinThreads,
+                         slots, sums, [] { __syncthreads(); });
     if (mine.on) {
         __syncwarp();
         join_slice<L, D>(a, mine, 0, 1, lane, 32, warp_slots[warp], sums + 32 * warp, [] { __syncwarp(); });
