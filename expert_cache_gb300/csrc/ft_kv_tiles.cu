@@ -40,13 +40,14 @@ constexpr int kThreads = (kWarpMma + 4) * 32;
 constexpr int kTiles = kKeys / kKvTile;                    // of a block: one per K warp and one per V warp
 constexpr int kWaitLimit = 1 << 20;
 constexpr float kLeast = 1.2e-38f;
-constexpr unsigned kFirst = 0, kNext = 1, kEnd = 2;
-using TilesLine = Line<kKeys, kRows, 1, 4, 3, 16>;
+constexpr unsigned kFirst = 0, kNext = 1, kEnd = 2, kTwo = 4;   // a block's marks; kTwo: the unit has a second tile of rows
+template <bool kPair>
+using TilesLine = Line<kKeys, kPair ? 2 * kRows : kRows, 1, 4, 3, 16>;
 
 // Buffers of K and of V: two blocks where they fit beside Q.
 constexpr int bufs(int D) { return D == 256 ? 1 : 2; }
 constexpr int region(int D) { return kKeys * D * 2; }                    // bytes of a block of K or V, and of Q
-constexpr size_t tiles_smem(int D) { return (size_t)region(D) * (1 + 2 * bufs(D)) + 1024; }
+constexpr size_t tiles_smem(int D, bool pair) { return (size_t)region(D) * ((pair ? 2 : 1) + 2 * bufs(D)) + 1024; }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void mbar_init(uint32_t b, int n) {
@@ -364,21 +365,25 @@ struct Run {
 
 }  // namespace
 
-template <int D, int kFormat>
+// kPair: units of 256 rows, a tile of 128 per softmax warpgroup.  Both share each block of K and V, and
+// neither waits for the other: S and O of a tile have their own tensor memory (2 * 128 + 2 * D columns,
+// so D up to 128).  Otherwise units of 128 rows, the warpgroups taking turns with the blocks.
+template <int D, int kFormat, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a) {
-    using L = TilesLine;
+    using L = TilesLine<kPair>;
+    constexpr int kUnit = L::kR;
     constexpr int kBufs = bufs(D), kRegion = region(D);
     constexpr KvTile kT = kv_tile(D, kFormat);
     constexpr uint32_t kColO = 256;                       // S and P: columns 0..127 and 128..255
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t sq = (smem_u32(smem_raw) + 1023) & ~1023u, sk = sq + kRegion, sv = sk + kBufs * kRegion;
+    const uint32_t sq = (smem_u32(smem_raw) + 1023) & ~1023u, sk = sq + (kPair ? 2 : 1) * kRegion, sv = sk + kBufs * kRegion;
     __shared__ long long prefix[kMaxSeqs + 1], scratch[kThreads / 32];
-    __shared__ __align__(8) uint64_t bars[28];
+    __shared__ __align__(8) uint64_t bars[30];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int abort_flag;
     // Written by the K warps, read by the softmax and issuing warps up to two blocks (or three short units) later:
     // four slots each, the block's or the unit's number modulo 4.
-    __shared__ float coef[4][kRows];                      // t = s * coef
+    __shared__ float coef[4][kUnit];                      // t = s * coef
     __shared__ unsigned char present[4][kTiles];          // the tile is one of the cache's and some row sees a key of it
     __shared__ unsigned what[4];                          // the block: first of a unit's, a later one, or none left
     __shared__ int drafted[4][kTreeMax];                  // places of the drafted tokens
@@ -398,13 +403,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     auto m_full = [&](int quad, int b) { return b0 + 112 + 16 * quad + 8 * b; };    // by 32 rows
     auto l_full = [&](int quad) { return b0 + 176 + 8 * quad; };
     const uint32_t o_free = b0 + 208, drain = b0 + 216, q_full = b0 + 32;
+    auto v_full = [&](int b) { return b0 + 224 + 8 * b; };    // pairs: V by buffer, P (in vp_full), S and O by tile
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(k_full(b), kTiles);
             mbar_init(k_empty(b), 1);
             mbar_init(v_empty(b), 1);
             mbar_init(s_full(b), 1);
-            mbar_init(vp_full(b), 4 + kTiles);
+            mbar_init(vp_full(b), kPair ? 4 : 4 + kTiles);
+            mbar_init(v_full(b), kTiles);
             mbar_init(o_done(b), 1);
             for (int q = 0; q < 4; ++q) mbar_init(m_full(q, b), 1);
         }
@@ -458,18 +465,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     if (warp < kWarpK) {
         // ------------------------------------------------------------------------ softmax
-        const int quad = warp & 3, wg = warp >> 2;        // the warpgroup takes the blocks of its parity
-        const int row = 32 * quad + lane;                 // of the unit's 128
+        const int quad = warp & 3, wg = warp >> 2;        // the warpgroup's tile, or the parity of its blocks
+        const int row0 = kPair ? kRows * wg : 0;          // its first row of the unit
+        const int row = row0 + 32 * quad + lane;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * quad) << 16);
-        unsigned it = 0;
+        const uint32_t o_addr = lane_addr + kColO + (kPair ? D * wg : 0);
+        unsigned it = 0, cnt = 0;                         // blocks of the CTA; of the warpgroup
         for (int un = 0; ok && next_run(run); ++un) {
             const SeqInfo& si = run.u.si;
-            const int base = si.len - si.n, grow = run.u.r * kRows + row;
+            const int base = si.len - si.n, grow = run.u.r * kUnit + row;
+            if (kPair && (long long)run.u.r * kUnit + row0 >= (long long)si.n * a.G) {    // no rows
+                it += run.v1 - run.v0;
+                continue;
+            }
             const RowRule rule = row_rule(a, si, grow);
-            // keys below all_lim and from all_low on are seen by every row of the unit
-            const RowRule first_rule = row_rule(a, si, run.u.r * kRows);
+            // keys below all_lim and from all_low on are seen by every row of the tile
+            const RowRule first_rule = row_rule(a, si, run.u.r * kUnit + row0);
             const int all_lim = a.tree ? base - 1 : first_rule.lim;
-            const int all_low = a.window > 0 ? (int)max((long long)(a.tree ? base + si.n : base + run.u.rt.i1) - a.window + 1, 0LL) : 0;
+            const int last = kPair ? min(si.n - 1, (run.u.r * kUnit + row0 + kRows - 1) / a.G) : run.u.rt.i1;
+            const int all_low = a.window > 0 ? (int)max((long long)(a.tree ? base + si.n : base + last) - a.window + 1, 0LL) : 0;
             // the reference is kept in units of s, so that s - m is exact near it however large t is
             float m = kNoRef, c = 0.f;
             f32x2 l2 = pair(0.f, 0.f);                    // the sum of this warpgroup's weights, in two halves
@@ -486,9 +500,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                 return true;
             };
             for (int v = run.v0; v < run.v1; ++v, ++it) {
-                const int b = it & 1;
+                const int b = kPair ? wg : it & 1;        // S's place
                 if (b != wg) continue;
-                if (!mbar_wait(s_full(b), it >> 1 & 1, &abort_flag)) { ok = false; break; }
+                if (!mbar_wait(s_full(b), kPair ? cnt & 1 : it >> 1 & 1, &abort_flag)) { ok = false; break; }
+                ++cnt;
                 tc_after();
                 c = coef[un & 3][row];
                 const uint32_t s_addr = lane_addr + 128 * b;
@@ -559,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     }
                     tmem_wait_st();
                 }
-                if (it > it0 && !take_ref(it - 1)) { ok = false; break; }
+                if (!kPair && it > it0 && !take_ref(it - 1)) { ok = false; break; }
                 const bool raise = top > m && (m == kNoRef || (top - m) * c > kHeadroom);
                 float f = 1.f;
                 if (raise) {
@@ -567,20 +582,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     m = top;
                     l2 = mul2(l2, pair(f, f));
                 }
-                refs[b][row] = m;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(m_full(quad, b));
+                if constexpr (!kPair) {
+                    refs[b][row] = m;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(m_full(quad, b));
+                }
                 if (__any_sync(0xffffffffu, raise) && it > it0) {
-                    if (!mbar_wait(o_done(b ^ 1), (it - 1) >> 1 & 1, &abort_flag)) { ok = false; break; }
+                    // O of the block before: complete with this block's S where one tile has both
+                    if (!kPair && !mbar_wait(o_done(b ^ 1), (it - 1) >> 1 & 1, &abort_flag)) { ok = false; break; }
                     tc_after();
 #pragma unroll 1
                     for (int x = 0; x < D; x += 32) {
                         uint32_t o[32];
-                        tmem_ld32(lane_addr + kColO + x, o);
+                        tmem_ld32(o_addr + x, o);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(lane_addr + kColO + x, o);
+                        tmem_st32(o_addr + x, o);
                     }
                 }
                 // a row that has seen nothing keeps finite differences: its s are -inf
@@ -610,26 +628,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                 if (lane == 0) mbar_arrive(vp_full(b));
             }
             if (!ok) break;
-            // the unit's sums: the last block's reference, both warpgroups' weights
+            // the unit's sums: for turns, the last block's reference and both warpgroups' weights
             c = coef[un & 3][row];
-            if (((it - 1) & 1) != wg && !take_ref(it - 1)) { ok = false; break; }
-            halves[un & 1][wg][row] = unpair(l2).x + unpair(l2).y;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(l_full(quad));
-            if (!mbar_wait(l_full(quad), un & 1, &abort_flag)) { ok = false; break; }
-            const float l = halves[un & 1][0][row] + halves[un & 1][1][row];
+            float l = unpair(l2).x + unpair(l2).y;
+            if constexpr (kPair) {
+                if (!mbar_wait(o_done(wg), (cnt - 1) & 1, &abort_flag)) { ok = false; break; }
+            } else {
+                if (((it - 1) & 1) != wg && !take_ref(it - 1)) { ok = false; break; }
+                halves[un & 1][wg][row] = unpair(l2).x + unpair(l2).y;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(l_full(quad));
+                if (!mbar_wait(l_full(quad), un & 1, &abort_flag)) { ok = false; break; }
+                l = halves[un & 1][0][row] + halves[un & 1][1][row];
+                if (!mbar_wait(o_done((it - 1) & 1), (it - 1) >> 1 & 1, &abort_flag)) { ok = false; break; }
+            }
             if (m != kNoRef) m *= c;
-            if (!mbar_wait(o_done((it - 1) & 1), (it - 1) >> 1 & 1, &abort_flag)) { ok = false; break; }
             tc_after();
             const int i = grow / a.G;
             const bool on = i < si.n, done = run.v0 == 0 && run.v1 == run.u.rt.nt;
-            float* out = partial<D, kRows>(a, 2 * cta + (run.v0 > 0 ? 0 : 1));
-            if (on && !done && wg == 0) reinterpret_cast<float2*>(out)[row] = make_float2(m, l);
+            float* out = partial<D, kUnit>(a, 2 * cta + (run.v0 > 0 ? 0 : 1));
+            if (on && !done && (kPair || wg == 0)) reinterpret_cast<float2*>(out)[row] = make_float2(m, l);
 #pragma unroll 1
-            for (int x = wg * (D / 2); x < (wg + 1) * (D / 2); x += 32) {
+            for (int x = kPair ? 0 : wg * (D / 2); x < (kPair ? D : (wg + 1) * (D / 2)); x += 32) {
                 uint32_t o[32];
                 __syncwarp();
-                tmem_ld32(lane_addr + kColO + x, o);
+                tmem_ld32(o_addr + x, o);
                 tmem_wait_ld();
                 if (on) {
 #pragma unroll
@@ -640,17 +663,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                         if (done) {
                             store_out<8>(a, (size_t)(si.q0 + i), run.u.h * a.G + grow % a.G, D, x + e, y, m, l);
                         } else {
-                            float4* dst = reinterpret_cast<float4*>(out + 2 * kRows + row * D + x + e);
+                            float4* dst = reinterpret_cast<float4*>(out + 2 * kUnit + row * D + x + e);
                             dst[0] = make_float4(y[0], y[1], y[2], y[3]);
                             dst[1] = make_float4(y[4], y[5], y[6], y[7]);
                         }
                     }
                 }
             }
-            // O is free for the next unit once both warpgroups have read their halves
+            // with turns, O is free for the next unit once both warpgroups have read their halves
             tc_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(o_free);
+            if (!kPair && lane == 0) mbar_arrive(o_free);
         }
     } else if (warp < kWarpMma) {
         // ------------------------------------------------------------------------ K (and Q), V
@@ -699,16 +722,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             load(run.v0);
             // Q of the unit, once every product of the unit before is through with it: 8 rows per warp, 8
             // lanes per row, two rows under way
-            if (it > 0 && !mbar_wait(s_full((it - 1) & 1), (it - 1) >> 1 & 1, &abort_flag)) { ok = false; break; }
+            if (it > 0 && !mbar_wait(k_empty((it - 1) % kBufs), ((it - 1) / kBufs) & 1, &abort_flag)) { ok = false; break; }
             if (a.tree && warp == kWarpK)
                 for (int j = lane; j < si.n; j += 32)
                     drafted[un & 3][j] = base + __popcll(a.tree[si.q0 + j] & ~(1ull << j));
-            {
+            const int row_tiles = kPair && (long long)run.u.r * kUnit + kRows < (long long)si.n * a.G ? 2 : 1;
+#pragma unroll 1
+            for (int rt = 0; rt < row_tiles; ++rt) {
                 const int row = 8 * (warp - kWarpK) + (lane >> 3), part = lane & 7;
                 uint4 q[2][D / 64];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int grow = run.u.r * kRows + row + 4 * x, i = grow / a.G;
+                    const int grow = run.u.r * kUnit + kRows * rt + row + 4 * x, i = grow / a.G;
                     const __nv_bfloat16* src = a.q + (size_t)(si.q0 + i) * a.q_stride + (size_t)(run.u.h * a.G + grow - i * a.G) * D + part * 8;
 #pragma unroll
                     for (int e = 0; e < D / 64; ++e)
@@ -729,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     const RowScale rs = row_scale(amax);
                     // the coefficient is positive (q carries the scale's sign): times -inf it stays -inf
                     const float down = a.scale < 0.f ? -rs.down : rs.down;
-                    if (part == 0) coef[un & 3][row + 4 * x] = fmaxf(fabsf(a.scale) * a.kv.k_scale * 1.44269504088896340736f * rs.up, kLeast);
+                    if (part == 0) coef[un & 3][kRows * rt + row + 4 * x] = fmaxf(fabsf(a.scale) * a.kv.k_scale * 1.44269504088896340736f * rs.up, kLeast);
 #pragma unroll
                     for (int e = 0; e < D / 64; ++e) {
                         const uint32_t wd[4] = {q[x][e].x, q[x][e].y, q[x][e].z, q[x][e].w};
@@ -737,13 +762,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             o[y] = pack_f16(__uint_as_float(wd[y] << 16) * down, __uint_as_float(wd[y] & 0xFFFF0000u) * down);
-                        st_shared(sq + chunk_at(row + 4 * x, e * 8 + part), make_uint4(o[0], o[1], o[2], o[3]));
+                        st_shared(sq + rt * kRegion + chunk_at(row + 4 * x, e * 8 + part), make_uint4(o[0], o[1], o[2], o[3]));
                     }
                 }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
             }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
             for (int v = run.v0; v < run.v1; ++v, ++it) {
                 const int b = it % kBufs;
                 if (!mbar_wait(is_k ? k_empty(b) : v_empty(b), ((it / kBufs) & 1) ^ 1, &abort_flag)) { ok = false; break; }
@@ -752,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     write_k<D, kFormat>(dst, raw, 16 * w, lane);
                     if (lane == 0) {
                         present[it & 3][w] = have;
-                        if (w == 0) what[it & 3] = v == run.v0 ? kFirst : kNext;
+                        if (w == 0) what[it & 3] = (v == run.v0 ? kFirst : kNext) | (row_tiles > 1 ? kTwo : 0);
                     }
                 } else {
                     // past the cached tokens the bytes may be anything: zero the lane's tokens there
@@ -762,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                 }
                 fence_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(is_k ? k_full(b) : vp_full(it & 1));
+                if (lane == 0) mbar_arrive(is_k ? k_full(b) : kPair ? v_full(b) : vp_full(it & 1));
                 if (v + 1 < run.v1) load(v + 1);
             }
         }
@@ -786,50 +811,84 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
         // descriptors of the regions' first bytes; an offset adds to the address field (16-byte units)
         const uint64_t q_desc = desc(sq, 16), k_desc = desc(sk, 16), v_desc = desc(sv, kKeys * 128);
         const bool lead = elect();
-        unsigned units = 0, units_q = 0;
+        unsigned units = 0, units_q = 0, tile_blocks[2] = {0, 0};
+        // S of a tile of the block in buffer b; O of a tile of the block in buffer c, P at p
+        auto products_s = [&](int tile, int b, uint32_t d) {
+            if (lead) {
+                const uint64_t qd = q_desc + tile * (kRegion >> 4), kd = k_desc + b * (kRegion >> 4);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    const uint64_t at = ((x >> 2) * (kKeys * 128) + (x & 3) * 32) >> 4;
+                    mma_ss(d, qd + at, kd + at, idesc(kKeys, false), x > 0);
+                }
+            }
+            __syncwarp();
+        };
+        auto products_o = [&](int tile, int c, uint32_t p, bool first) {
+            if (lead) {
+                const uint64_t vd = v_desc + c * (kRegion >> 4);
+#pragma unroll
+                for (int x = 0; x < kKeys / 16; ++x)
+                    mma_ts(tmem + kColO + D * tile, p + 8 * x, vd + x * (2048 >> 4), idesc(D, true), x > 0 || !first);
+            }
+            __syncwarp();
+        };
+        auto commit = [&](uint32_t bar) {
+            if (lead) tc_commit(bar);
+            __syncwarp();
+        };
         for (unsigned it = 0, before = kEnd;; ++it) {
-            const int b = it % kBufs;
+            const int b = it % kBufs, c = (it - 1) % kBufs;
             ok = mbar_wait(k_full(b), (it / kBufs) & 1, &abort_flag);
             if (!ok) break;
             tc_after();
             const unsigned now = what[it & 3];
-            if (now == kFirst) {                          // of a unit: its Q
+            if ((now & ~kTwo) == kFirst) {                // of a unit: its Q
                 ok = mbar_wait(q_full, units_q++ & 1, &abort_flag);
                 if (!ok) break;
                 tc_after();
             }
-            if (now != kEnd) {                            // S of this block
-                if (lead) {
-                    const uint64_t kd = k_desc + b * (kRegion >> 4);
-                    const uint32_t d = tmem + 128 * (it & 1);
+            const bool first = (before & ~kTwo) == kFirst;
+            if constexpr (kPair) {
+                // tile by tile: O of the block before, then S of this one over its P
+                if (before != kEnd) ok = mbar_wait(v_full(c), ((it - 1) / kBufs) & 1, &abort_flag);
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        const uint64_t at = ((x >> 2) * (kKeys * 128) + (x & 3) * 32) >> 4;
-                        mma_ss(d, q_desc + at, kd + at, idesc(kKeys, false), x > 0);
+                for (int tile = 0; tile < 2; ++tile) {
+                    if (ok && before != kEnd && (tile == 0 || before & kTwo)) {
+                        ok = mbar_wait(vp_full(tile), (tile_blocks[tile] - 1) & 1, &abort_flag);
+                        if (ok) {
+                            tc_after();
+                            products_o(tile, c, tmem + 128 * tile, first);
+                            commit(o_done(tile));
+                        }
                     }
-                    tc_commit(k_empty(b));
-                    tc_commit(s_full(it & 1));
+                    if (ok && now != kEnd && (tile == 0 || now & kTwo)) {
+                        products_s(tile, b, tmem + 128 * tile);
+                        commit(s_full(tile));
+                        ++tile_blocks[tile];
+                    }
                 }
-                __syncwarp();
-            }
-            if (before != kEnd) {                         // O of the one before
-                const unsigned n = it - 1;
-                const int c = n % kBufs;
-                ok = mbar_wait(vp_full(n & 1), n >> 1 & 1, &abort_flag);
-                if (ok && before == kFirst && units++ > 0)    // the unit before has been read out of O
-                    ok = mbar_wait(o_free, units & 1, &abort_flag);
                 if (!ok) break;
-                tc_after();
-                if (lead) {
-                    const uint64_t vd = v_desc + c * (kRegion >> 4);
-                    const uint32_t pa = tmem + 128 * (n & 1);
-#pragma unroll
-                    for (int x = 0; x < kKeys / 16; ++x)
-                        mma_ts(tmem + kColO, pa + 8 * x, vd + x * (2048 >> 4), idesc(D, true), x > 0 || before != kFirst);
-                    tc_commit(v_empty(c));
-                    tc_commit(o_done(n & 1));
+                if (now != kEnd) commit(k_empty(b));
+                if (before != kEnd) commit(v_empty(c));
+            } else {
+                // S of this block, then O of the one before
+                if (now != kEnd) {
+                    products_s(0, b, tmem + 128 * (it & 1));
+                    commit(k_empty(b));
+                    commit(s_full(it & 1));
                 }
-                __syncwarp();
+                if (before != kEnd) {
+                    const unsigned n = it - 1;
+                    ok = mbar_wait(vp_full(n & 1), n >> 1 & 1, &abort_flag);
+                    if (ok && first && units++ > 0)       // the unit before has been read out of O
+                        ok = mbar_wait(o_free, units & 1, &abort_flag);
+                    if (!ok) break;
+                    tc_after();
+                    products_o(0, c, tmem + 128 * (n & 1), first);
+                    commit(v_empty(c));
+                    commit(o_done(n & 1));
+                }
             }
             if (now == kEnd) break;
             before = now;
@@ -849,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
 namespace {
 
 // CTAs: one per SM (0 when the kernel cannot be set up; looked up once per device).
-template <int D, int kFormat>
+template <int D, int kFormat, bool kPair>
 int tiles_grid() {
     static std::atomic<int> grids[kMaxDevices];
     int dev = 0;
@@ -859,33 +918,40 @@ int tiles_grid() {
     }
     int v = grids[dev].load(std::memory_order_relaxed);
     if (!v) {
-        auto kern = kv_tiles_kernel<D, kFormat>;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tiles_smem(D)) != cudaSuccess ||
-            all_shared(kern) != cudaSuccess || all_shared(kv_join_kernel<TilesLine, D>) != cudaSuccess) {
+        auto kern = kv_tiles_kernel<D, kFormat, kPair>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tiles_smem(D, kPair)) != cudaSuccess ||
+            all_shared(kern) != cudaSuccess || all_shared(kv_join_kernel<TilesLine<kPair>, D>) != cudaSuccess) {
             cudaGetLastError();
             return 0;
         }
-        v = min(sm_count(), kMaxShares / 2);
+        v = min(sm_count(), kMaxShares / 4);          // two pieces of up to 256 rows each fit the workspace
         grids[dev].store(v, std::memory_order_relaxed);
     }
     return v;
 }
 
-template <int D, int kFormat>
+template <int D, int kFormat, bool kPair>
 cudaError_t run_tiles(const AttnArgs& a, cudaStream_t s) {
-    const int grid = tiles_grid<D, kFormat>();
+    const int grid = tiles_grid<D, kFormat, kPair>();
     if (grid < 1) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_pdl(kv_tiles_kernel<D, kFormat>, dim3(grid), dim3(kThreads), tiles_smem(D), s, a);
+    const cudaError_t e = launch_pdl(kv_tiles_kernel<D, kFormat, kPair>, dim3(grid), dim3(kThreads), tiles_smem(D, kPair), s, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv_join_kernel<TilesLine, D>, dim3(grid * TilesLine::kSplit), dim3(kJoinThreads), 0, s, a);
+    return launch_pdl(kv_join_kernel<TilesLine<kPair>, D>, dim3(grid * TilesLine<kPair>::kSplit), dim3(kJoinThreads), 0, s, a);
+}
+
+template <int D, int kFormat>
+cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+    if constexpr (D <= 128)
+        if ((long long)a.max_q * a.G > kRows) return run_tiles<D, kFormat, true>(a, s);
+    return run_tiles<D, kFormat, false>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_tiles(const AttnArgs& a, int D, int format, cudaStream_t s) {
     if (format == FT_KV_NVFP4)
-        return D == 64 ? run_tiles<64, FT_KV_NVFP4>(a, s) : D == 128 ? run_tiles<128, FT_KV_NVFP4>(a, s) : run_tiles<256, FT_KV_NVFP4>(a, s);
-    return D == 64 ? run_tiles<64, FT_KV_FP8>(a, s) : D == 128 ? run_tiles<128, FT_KV_FP8>(a, s) : run_tiles<256, FT_KV_FP8>(a, s);
+        return D == 64 ? run<64, FT_KV_NVFP4>(a, s) : D == 128 ? run<128, FT_KV_NVFP4>(a, s) : run<256, FT_KV_NVFP4>(a, s);
+    return D == 64 ? run<64, FT_KV_FP8>(a, s) : D == 128 ? run<128, FT_KV_FP8>(a, s) : run<256, FT_KV_FP8>(a, s);
 }
 
 }  // namespace ft
