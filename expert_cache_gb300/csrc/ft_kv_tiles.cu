@@ -10,18 +10,17 @@
 //               that two blocks are under way; a block's reference follows from the one before
 //               (handed over in shared memory) and O is rescaled in tensor memory only when a row's
 //               maximum has grown past the headroom
-//   warps 8-15  K: codes -> f16 in the 128-byte swizzled layout, a tile of 16 tokens per warp; at a
-//               unit's start also half of Q
-//   warps 16-23 V: the same, and the other half of Q
-//   warp 24     issues the matrix instructions: S of block j + 1 before O of block j, so the tensor
-//               cores work while the softmax warps do (25-27 only complete its warpgroup)
-// The block starts with 72 registers a thread; the last warpgroup gives up 32 of them and K's and V's
-// 8, the softmax warpgroups take 32 each (8 * 104 + 16 * 64 + 4 * 40 <= 28 * 72 per lane).
-// Unpacking a block costs more issue slots than its softmax and more latency (codes, conversion,
-// store, fence), so it has twice the warps; the codes of a warp's next tile are loaded into
-// registers as soon as it has stored the one before.  Within a lane's 16-byte vectors the order of
-// the shared-memory stores is permuted so that the 8 lanes of a store phase hit the 8 bank groups of
-// a swizzle row.
+//   then        K: codes -> f16 in the 128-byte swizzled layout, and at a unit's start a share of Q;
+//               V: the same; with pairs four warps each (two tiles of 16 tokens per warp and block),
+//               else eight
+//   then        one warp issues the matrix instructions: with turns S of block j + 1 before O of block
+//               j, with pairs O of a tile's block and S of its next one, tile after tile (three warps
+//               more only complete the warpgroup)
+// Registers move between the roles at the start (the sums stand at setmaxnreg).  Unpacking a block
+// costs more issue slots than its softmax and more latency (codes, conversion, store, fence); the
+// codes of a warp's next block are loaded into registers as soon as it has stored the one before.
+// Within a lane's 16-byte vectors the order of the shared-memory stores is permuted so that the 8
+// lanes of a store phase hit the 8 bank groups of a swizzle row.
 // Units are laid on the line of shares like the rows kernel's (a unit's start and end cost about
 // three blocks), so causal and ragged chunks balance; cut units are joined by the second kernel.
 // Every wait is bounded: on expiry the CTA sets FT_DEV_TIMEOUT, leaves its loops and frees its
@@ -35,12 +34,18 @@ namespace ft {
 namespace {
 
 constexpr int kKeys = 128, kRows = 128;
-constexpr int kWarpK = 8, kWarpV = 16, kWarpMma = 24;      // first warps of the roles after the softmax's
-constexpr int kThreads = (kWarpMma + 4) * 32;
-constexpr int kTiles = kKeys / kKvTile;                    // of a block: one per K warp and one per V warp
+constexpr int kTiles = kKeys / kKvTile;                    // tiles of a block
+// Warps of K (and again of V), their tiles of a block, first warps of the roles after the softmax's.
+template <bool kPair>
+struct Roles {
+    static constexpr int kWide = kPair ? 4 : 8, kEach = kTiles / kWide;
+    static constexpr int kK = 8, kV = kK + kWide, kMma = kV + kWide, kThreads = (kMma + 4) * 32;
+};
 constexpr int kWaitLimit = 1 << 20;
 constexpr float kLeast = 1.2e-38f;
-constexpr unsigned kFirst = 0, kNext = 1, kEnd = 2, kTwo = 4;   // a block's marks; kTwo: the unit has a second tile of rows
+// A block's marks: the first or a later one of its unit, or none left; the unit has a second tile of
+// rows; the last of the unit's.
+constexpr unsigned kFirst = 0, kNext = 1, kEnd = 2, kKind = 3, kTwo = 4, kLast = 8;
 template <bool kPair>
 using TilesLine = Line<kKeys, kPair ? 2 * kRows : kRows, 1, 4, 3, 16>;
 
@@ -357,6 +362,12 @@ __device__ __forceinline__ void zero_past(Raw<D, kFormat>& r, int n, int t) {
         }
 }
 
+// What the softmax warps need to know of a unit.
+struct UnitInfo {
+    int q0, n, len, r, h, i1, slot;      // slot of its partial sums, -1 when the CTA has the whole unit
+    bool empty;
+};
+
 // What a CTA does of one unit: its blocks [v0, v1).
 struct Run {
     Unit u;
@@ -369,9 +380,11 @@ struct Run {
 // neither waits for the other: S and O of a tile have their own tensor memory (2 * 128 + 2 * D columns,
 // so D up to 128).  Otherwise units of 128 rows, the warpgroups taking turns with the blocks.
 template <int D, int kFormat, bool kPair>
-__global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(Roles<kPair>::kThreads, 1) kv_tiles_kernel(const AttnArgs a) {
     using L = TilesLine<kPair>;
-    constexpr int kUnit = L::kR;
+    using Role = Roles<kPair>;
+    constexpr int kUnit = L::kR, kWarpK = Role::kK, kWarpV = Role::kV, kWarpMma = Role::kMma, kThreads = Role::kThreads;
+    constexpr int kEach = Role::kEach;
     constexpr int kBufs = bufs(D), kRegion = region(D);
     constexpr KvTile kT = kv_tile(D, kFormat);
     constexpr uint32_t kColO = 256;                       // S and P: columns 0..127 and 128..255
@@ -381,11 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     __shared__ __align__(8) uint64_t bars[30];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int abort_flag;
-    // Written by the K warps, read by the softmax and issuing warps up to two blocks (or three short units) later:
-    // four slots each, the block's or the unit's number modulo 4.
+    // Written by the K warps, read by the softmax and issuing warps: by the block's number modulo 8 (a
+    // softmax warpgroup may be two blocks behind the products, which are up to two blocks behind K),
+    // and by the unit's number modulo 4.
     __shared__ float coef[4][kUnit];                      // t = s * coef
-    __shared__ unsigned char present[4][kTiles];          // the tile is one of the cache's and some row sees a key of it
-    __shared__ unsigned what[4];                          // the block: first of a unit's, a later one, or none left
+    __shared__ unsigned char present[8][kTiles];          // by K warp: bit x, its x-th tile is one of the cache's and some row sees a key of it
+    __shared__ unsigned what[8];                          // the block's marks
+    __shared__ int key0[8];                               // its first key
+    __shared__ UnitInfo units[4];
     __shared__ int drafted[4][kTreeMax];                  // places of the drafted tokens
     __shared__ float refs[2][kRows];                      // by block parity: the rows' references
     __shared__ float halves[2][2][kRows];                 // by unit parity and warpgroup: the rows' sums
@@ -406,18 +422,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     auto v_full = [&](int b) { return b0 + 224 + 8 * b; };    // pairs: V by buffer, P (in vp_full), S and O by tile
     if (threadIdx.x == 0) {
         for (int b = 0; b < 2; ++b) {
-            mbar_init(k_full(b), kTiles);
+            mbar_init(k_full(b), Role::kWide);
             mbar_init(k_empty(b), 1);
             mbar_init(v_empty(b), 1);
             mbar_init(s_full(b), 1);
-            mbar_init(vp_full(b), kPair ? 4 : 4 + kTiles);
-            mbar_init(v_full(b), kTiles);
+            mbar_init(vp_full(b), kPair ? 4 : 4 + Role::kWide);
+            mbar_init(v_full(b), Role::kWide);
             mbar_init(o_done(b), 1);
             for (int q = 0; q < 4; ++q) mbar_init(m_full(q, b), 1);
         }
         for (int q = 0; q < 4; ++q) mbar_init(l_full(q), 2);
         mbar_init(o_free, 8);
-        mbar_init(q_full, 2 * kTiles);
+        mbar_init(q_full, 2 * Role::kWide);
         mbar_init(drain, 1);
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -460,9 +476,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
 
     Run run;
     bool ok = true;
-    if (warp >= kWarpMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    else if (warp >= kWarpK) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    if constexpr (kPair) {                                // of 20 * 96: 8 * 128 + 8 * 88 + 4 * 40
+        if (warp >= kWarpMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        else if (warp >= kWarpK) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    } else {                                              // of 28 * 72: 8 * 104 + 16 * 64 + 4 * 40
+        if (warp >= kWarpMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        else if (warp >= kWarpK) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    }
     if (warp < kWarpK) {
         // ------------------------------------------------------------------------ softmax
         const int quad = warp & 3, wg = warp >> 2;        // the warpgroup's tile, or the parity of its blocks
@@ -470,48 +492,59 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
         const int row = row0 + 32 * quad + lane;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * quad) << 16);
         const uint32_t o_addr = lane_addr + kColO + (kPair ? D * wg : 0);
-        unsigned it = 0, cnt = 0;                         // blocks of the CTA; of the warpgroup
-        for (int un = 0; ok && next_run(run); ++un) {
-            const SeqInfo& si = run.u.si;
-            const int base = si.len - si.n, grow = run.u.r * kUnit + row;
-            if (kPair && (long long)run.u.r * kUnit + row0 >= (long long)si.n * a.G) {    // no rows
-                it += run.v1 - run.v0;
+        unsigned o_blocks = 0;                            // units that the warpgroup has read out of O
+        SeqInfo si;
+        UnitInfo u;
+        RowRule rule;
+        int grow = 0, base = 0, all_lim = 0, all_low = 0;
+        // the reference is kept in units of s, so that s - m is exact near it however large t is
+        float m = kNoRef, c = 0.f;
+        f32x2 l2 = 0;                                     // the sum of this warpgroup's weights, in two halves
+        // the reference that the block before was weighed with
+        auto take_ref = [&](unsigned n) {
+            if (!mbar_wait(m_full(quad, n & 1), n >> 1 & 1, &abort_flag)) return false;
+            const float now = refs[n & 1][row];
+            if (now != m) {
+                const float f = m == kNoRef ? 0.f : ex2((m - now) * c);
+                l2 = mul2(l2, pair(f, f));
+                m = now;
+            }
+            return true;
+        };
+        unsigned un = 0;
+        for (unsigned it = 0;; ++it) {                    // every block, the other warpgroup's too
+            const int b = kPair ? wg : it & 1;            // S's place
+            if (!mbar_wait(s_full(b), kPair ? it & 1 : it >> 1 & 1, &abort_flag)) { ok = false; break; }
+            tc_after();
+            const unsigned marks = what[it & 7];
+            if ((marks & kKind) == kEnd) break;
+            if ((marks & kKind) == kFirst) {
+                u = units[un & 3];
+                si = SeqInfo{u.q0, u.n, u.len, false};
+                base = si.len - si.n;
+                grow = u.r * kUnit + row;
+                rule = row_rule(a, si, grow);
+                // keys below all_lim and from all_low on are seen by every row of the tile
+                all_lim = a.tree ? base - 1 : row_rule(a, si, u.r * kUnit + row0).lim;
+                const int last = kPair ? min(si.n - 1, (u.r * kUnit + row0 + kRows - 1) / a.G) : u.i1;
+                all_low = a.window > 0 ? (int)max((long long)(a.tree ? base + si.n : base + last) - a.window + 1, 0LL) : 0;
+                m = kNoRef;
+                c = coef[un & 3][row];
+                l2 = pair(0.f, 0.f);
+            }
+            if (kPair && wg == 1 && !(marks & kTwo)) {    // no rows: told, so that it keeps step
+                if (lane == 0) mbar_arrive(vp_full(1));
+                if (marks & kLast) ++un;
                 continue;
             }
-            const RowRule rule = row_rule(a, si, grow);
-            // keys below all_lim and from all_low on are seen by every row of the tile
-            const RowRule first_rule = row_rule(a, si, run.u.r * kUnit + row0);
-            const int all_lim = a.tree ? base - 1 : first_rule.lim;
-            const int last = kPair ? min(si.n - 1, (run.u.r * kUnit + row0 + kRows - 1) / a.G) : run.u.rt.i1;
-            const int all_low = a.window > 0 ? (int)max((long long)(a.tree ? base + si.n : base + last) - a.window + 1, 0LL) : 0;
-            // the reference is kept in units of s, so that s - m is exact near it however large t is
-            float m = kNoRef, c = 0.f;
-            f32x2 l2 = pair(0.f, 0.f);                    // the sum of this warpgroup's weights, in two halves
-            const unsigned it0 = it;
-            // the reference that the block before was weighed with
-            auto take_ref = [&](unsigned n) {
-                if (!mbar_wait(m_full(quad, n & 1), n >> 1 & 1, &abort_flag)) return false;
-                const float now = refs[n & 1][row];
-                if (now != m) {
-                    const float f = m == kNoRef ? 0.f : ex2((m - now) * c);
-                    l2 = mul2(l2, pair(f, f));
-                    m = now;
-                }
-                return true;
-            };
-            for (int v = run.v0; v < run.v1; ++v, ++it) {
-                const int b = kPair ? wg : it & 1;        // S's place
-                if (b != wg) continue;
-                if (!mbar_wait(s_full(b), kPair ? cnt & 1 : it >> 1 & 1, &abort_flag)) { ok = false; break; }
-                ++cnt;
-                tc_after();
-                c = coef[un & 3][row];
+            const bool opens = (marks & kKind) == kFirst;
+            if (kPair || b == wg) {
                 const uint32_t s_addr = lane_addr + 128 * b;
-                const int j0 = run.u.rt.block(v) * kKeys;
+                const int j0 = key0[it & 7];
                 unsigned there = 0;                       // the block's tiles
 #pragma unroll
-                for (int w = 0; w < kTiles; ++w) there |= (unsigned)present[it & 3][w] << w;
-                const bool edge = there != 255u || j0 + kKeys - 1 > all_lim || (j0 < all_low && j0 + kKeys > a.n_sink) || run.u.rt.empty;
+                for (int w = 0; w < Role::kWide; ++w) there |= (unsigned)present[it & 7][w] << (w * kEach);
+                const bool edge = there != 255u || j0 + kKeys - 1 > all_lim || (j0 < all_low && j0 + kKeys > a.n_sink) || u.empty;
                 // which of 32 keys the row sees
                 auto mask_of = [&](int ch) {
                     const int j = j0 + 32 * ch;
@@ -574,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     }
                     tmem_wait_st();
                 }
-                if (!kPair && it > it0 && !take_ref(it - 1)) { ok = false; break; }
+                if (!kPair && !opens && !take_ref(it - 1)) { ok = false; break; }
                 const bool raise = top > m && (m == kNoRef || (top - m) * c > kHeadroom);
                 float f = 1.f;
                 if (raise) {
@@ -587,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(m_full(quad, b));
                 }
-                if (__any_sync(0xffffffffu, raise) && it > it0) {
+                if (__any_sync(0xffffffffu, raise) && !opens) {
                     // O of the block before: complete with this block's S where one tile has both
                     if (!kPair && !mbar_wait(o_done(b ^ 1), (it - 1) >> 1 & 1, &abort_flag)) { ok = false; break; }
                     tc_after();
@@ -627,26 +660,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(vp_full(b));
             }
-            if (!ok) break;
+            if (!(marks & kLast)) continue;
             // the unit's sums: for turns, the last block's reference and both warpgroups' weights
-            c = coef[un & 3][row];
             float l = unpair(l2).x + unpair(l2).y;
             if constexpr (kPair) {
-                if (!mbar_wait(o_done(wg), (cnt - 1) & 1, &abort_flag)) { ok = false; break; }
+                if (!mbar_wait(o_done(wg), o_blocks++ & 1, &abort_flag)) { ok = false; break; }
             } else {
-                if (((it - 1) & 1) != wg && !take_ref(it - 1)) { ok = false; break; }
+                if (b != wg && !take_ref(it)) { ok = false; break; }
                 halves[un & 1][wg][row] = unpair(l2).x + unpair(l2).y;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(l_full(quad));
                 if (!mbar_wait(l_full(quad), un & 1, &abort_flag)) { ok = false; break; }
                 l = halves[un & 1][0][row] + halves[un & 1][1][row];
-                if (!mbar_wait(o_done((it - 1) & 1), (it - 1) >> 1 & 1, &abort_flag)) { ok = false; break; }
+                if (!mbar_wait(o_done(it & 1), it >> 1 & 1, &abort_flag)) { ok = false; break; }
             }
+            ++un;
             if (m != kNoRef) m *= c;
             tc_after();
             const int i = grow / a.G;
-            const bool on = i < si.n, done = run.v0 == 0 && run.v1 == run.u.rt.nt;
-            float* out = partial<D, kUnit>(a, 2 * cta + (run.v0 > 0 ? 0 : 1));
+            const bool on = i < si.n, done = u.slot < 0;
+            float* out = partial<D, kUnit>(a, max(u.slot, 0));
             if (on && !done && (kPair || wg == 0)) reinterpret_cast<float2*>(out)[row] = make_float2(m, l);
 #pragma unroll 1
             for (int x = kPair ? 0 : wg * (D / 2); x < (kPair ? D : (wg + 1) * (D / 2)); x += 32) {
@@ -661,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
 #pragma unroll
                         for (int z = 0; z < 8; ++z) y[z] = __uint_as_float(o[e + z]);
                         if (done) {
-                            store_out<8>(a, (size_t)(si.q0 + i), run.u.h * a.G + grow % a.G, D, x + e, y, m, l);
+                            store_out<8>(a, (size_t)(si.q0 + i), u.h * a.G + grow - i * a.G, D, x + e, y, m, l);
                         } else {
                             float4* dst = reinterpret_cast<float4*>(out + 2 * kUnit + row * D + x + e);
                             dst[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -678,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
     } else if (warp < kWarpMma) {
         // ------------------------------------------------------------------------ K (and Q), V
         const bool is_k = warp < kWarpV;
-        const int w = (warp - kWarpK) & (kTiles - 1);     // the warp's tile of a block
+        const int w = (warp - kWarpK) & (Role::kWide - 1);       // the warp's tiles of a block: w kEach ..
         const int per = a.kv.page_shift - 4;
         unsigned it = 0;
         for (int un = 0; ok && next_run(run); ++un) {
@@ -688,17 +721,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             // keys that some row sees: below hi, from lo on or among the first tokens
             const int hi = run.u.rt.empty ? 0 : a.tree ? si.len : min(si.len, base + run.u.rt.i1 + 1);
             const int lo = a.window > 0 ? (int)max((long long)base + (a.tree ? 0 : run.u.rt.i0) - a.window + 1, 0LL) : 0;
-            int group = -1, page = -1;                    // lane x holds the page of the tile of block v0 + 32 * group + x
-            Raw<D, kFormat> raw;
-            bool have = false;                            // the tile is one of the cache's and some row sees a key of it
+            int group = -1, page = -1;                    // lane x: the page of its (x % kEach)-th tile of block v0 + 32 / kEach * group + x / kEach
+            Raw<D, kFormat> raw[kEach];
+            unsigned have = 0;                            // bit x: the tile is one of the cache's and some row sees a key of it
             auto load = [&](int v) {
-                const int n = v - run.v0;
+                const int n = (v - run.v0) * kEach;
                 if (n >> 5 != group) {
                     group = n >> 5;
                     page = -1;
-                    const int mine = (v - (n & 31)) + lane;
+                    const int mine = run.v0 + ((n & ~31) + lane) / kEach;
                     if (mine < run.v1) {
-                        const int tile = run.u.rt.block(mine) * kTiles + w, key = tile * 16;
+                        const int tile = run.u.rt.block(mine) * kTiles + w * kEach + lane % kEach, key = tile * 16;
                         if (key < hi && (key + 15 >= lo || key < a.n_sink)) {
                             page = table[tile >> per];
                             if (page < 0 || page >= a.kv.n_pages) {
@@ -708,28 +741,37 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                         }
                     }
                 }
-                const int pg = __shfl_sync(0xffffffffu, page, n & 31);
-                have = pg >= 0;
-                if (have) {
-                    const int tile = run.u.rt.block(v) * kTiles + w;
-                    const uint8_t* src = a.kv.pool + ((((size_t)pg * a.kv.hkv + run.u.h) << per) + (tile & ((1 << per) - 1))) * kT.bytes;
-                    if (is_k) load_k<D, kFormat>(raw, src, lane);
-                    else load_v<D, kFormat>(raw, src, lane);
-                } else {
-                    clear(raw);
+                have = 0;
+#pragma unroll
+                for (int x = 0; x < kEach; ++x) {
+                    const int pg = __shfl_sync(0xffffffffu, page, (n + x) & 31);
+                    if (pg >= 0) {
+                        have |= 1u << x;
+                        const int tile = run.u.rt.block(v) * kTiles + w * kEach + x;
+                        const uint8_t* src = a.kv.pool + ((((size_t)pg * a.kv.hkv + run.u.h) << per) + (tile & ((1 << per) - 1))) * kT.bytes;
+                        if (is_k) load_k<D, kFormat>(raw[x], src, lane);
+                        else load_v<D, kFormat>(raw[x], src, lane);
+                    } else {
+                        clear(raw[x]);
+                    }
                 }
             };
             load(run.v0);
-            // Q of the unit, once every product of the unit before is through with it: 8 rows per warp, 8
-            // lanes per row, two rows under way
+            // Q of the unit, once every product of the unit before is through with it: 8 lanes per row, two
+            // rows of a lane under way
             if (it > 0 && !mbar_wait(k_empty((it - 1) % kBufs), ((it - 1) / kBufs) & 1, &abort_flag)) { ok = false; break; }
+            if (warp == kWarpK && lane == 0) {
+                const bool all = run.v0 == 0 && run.v1 == run.u.rt.nt;
+                units[un & 3] = UnitInfo{si.q0, si.n, si.len, run.u.r, run.u.h, run.u.rt.i1, all ? -1 : 2 * cta + (run.v0 > 0 ? 0 : 1), run.u.rt.empty};
+            }
             if (a.tree && warp == kWarpK)
                 for (int j = lane; j < si.n; j += 32)
                     drafted[un & 3][j] = base + __popcll(a.tree[si.q0 + j] & ~(1ull << j));
             const int row_tiles = kPair && (long long)run.u.r * kUnit + kRows < (long long)si.n * a.G ? 2 : 1;
+            constexpr int kTimes = kTiles / Role::kWide;  // 8 rows at a time
 #pragma unroll 1
-            for (int rt = 0; rt < row_tiles; ++rt) {
-                const int row = 8 * (warp - kWarpK) + (lane >> 3), part = lane & 7;
+            for (int y = 0; y < row_tiles * kTimes; ++y) {
+                const int rt = y / kTimes, row = 8 * ((warp - kWarpK) * kTimes + y % kTimes) + (lane >> 3), part = lane & 7;
                 uint4 q[2][D / 64];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -773,17 +815,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                 const int b = it % kBufs;
                 if (!mbar_wait(is_k ? k_empty(b) : v_empty(b), ((it / kBufs) & 1) ^ 1, &abort_flag)) { ok = false; break; }
                 const uint32_t dst = (is_k ? sk : sv) + b * kRegion;
-                if (is_k) {
-                    write_k<D, kFormat>(dst, raw, 16 * w, lane);
-                    if (lane == 0) {
-                        present[it & 3][w] = have;
-                        if (w == 0) what[it & 3] = (v == run.v0 ? kFirst : kNext) | (row_tiles > 1 ? kTwo : 0);
+#pragma unroll
+                for (int x = 0; x < kEach; ++x) {
+                    const int row = 16 * (w * kEach + x);
+                    if (is_k) {
+                        write_k<D, kFormat>(dst, raw[x], row, lane);
+                    } else {
+                        // past the cached tokens the bytes may be anything: zero the lane's tokens there
+                        const int left = si.len - run.u.rt.block(v) * kKeys - row;
+                        if (left < 16) zero_past<D, kFormat>(raw[x], left, lane & 3);
+                        write_v<D, kFormat>(dst, raw[x], row, lane);
                     }
-                } else {
-                    // past the cached tokens the bytes may be anything: zero the lane's tokens there
-                    const int left = si.len - run.u.rt.block(v) * kKeys - 16 * w;
-                    if (left < 16) zero_past<D, kFormat>(raw, left, lane & 3);
-                    write_v<D, kFormat>(dst, raw, 16 * w, lane);
+                }
+                if (is_k && lane == 0) {
+                    present[it & 7][w] = have;
+                    if (w == 0) {
+                        what[it & 7] = (v == run.v0 ? kFirst : kNext) | (row_tiles > 1 ? kTwo : 0) | (v + 1 == run.v1 ? kLast : 0);
+                        key0[it & 7] = run.u.rt.block(v) * kKeys;
+                    }
                 }
                 fence_async();
                 __syncwarp();
@@ -793,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
         }
         if (ok && is_k) {                                 // no more blocks
             ok = mbar_wait(k_empty(it % kBufs), ((it / kBufs) & 1) ^ 1, &abort_flag);
-            if (w == 0 && lane == 0) what[it & 3] = kEnd;
+            if (w == 0 && lane == 0) what[it & 7] = what[(it + 1) & 7] = kEnd;       // the other warpgroup's turn too
             __syncwarp();
             if (ok && lane == 0) mbar_arrive(k_full(it % kBufs));
         }
@@ -811,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
         // descriptors of the regions' first bytes; an offset adds to the address field (16-byte units)
         const uint64_t q_desc = desc(sq, 16), k_desc = desc(sk, 16), v_desc = desc(sv, kKeys * 128);
         const bool lead = elect();
-        unsigned units = 0, units_q = 0, tile_blocks[2] = {0, 0};
+        unsigned units_o = 0, units_q = 0;
         // S of a tile of the block in buffer b; O of a tile of the block in buffer c, P at p
         auto products_s = [&](int tile, int b, uint32_t d) {
             if (lead) {
@@ -842,47 +891,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
             ok = mbar_wait(k_full(b), (it / kBufs) & 1, &abort_flag);
             if (!ok) break;
             tc_after();
-            const unsigned now = what[it & 3];
-            if ((now & ~kTwo) == kFirst) {                // of a unit: its Q
+            const unsigned now = what[it & 7];
+            const bool more = (now & kKind) != kEnd, owed = before != kEnd;
+            if ((now & kKind) == kFirst) {                // of a unit: its Q
                 ok = mbar_wait(q_full, units_q++ & 1, &abort_flag);
                 if (!ok) break;
                 tc_after();
             }
-            const bool first = (before & ~kTwo) == kFirst;
+            const bool first = (before & kKind) == kFirst;
             if constexpr (kPair) {
                 // tile by tile: O of the block before, then S of this one over its P
-                if (before != kEnd) ok = mbar_wait(v_full(c), ((it - 1) / kBufs) & 1, &abort_flag);
+                if (owed) ok = mbar_wait(v_full(c), ((it - 1) / kBufs) & 1, &abort_flag);
 #pragma unroll
                 for (int tile = 0; tile < 2; ++tile) {
-                    if (ok && before != kEnd && (tile == 0 || before & kTwo)) {
-                        ok = mbar_wait(vp_full(tile), (tile_blocks[tile] - 1) & 1, &abort_flag);
-                        if (ok) {
+                    if (ok && owed) {
+                        ok = mbar_wait(vp_full(tile), (it - 1) & 1, &abort_flag);
+                        if (ok && (tile == 0 || before & kTwo)) {
                             tc_after();
                             products_o(tile, c, tmem + 128 * tile, first);
-                            commit(o_done(tile));
+                            if (before & kLast) commit(o_done(tile));
                         }
                     }
-                    if (ok && now != kEnd && (tile == 0 || now & kTwo)) {
-                        products_s(tile, b, tmem + 128 * tile);
-                        commit(s_full(tile));
-                        ++tile_blocks[tile];
-                    }
+                    if (ok && more && (tile == 0 || now & kTwo)) products_s(tile, b, tmem + 128 * tile);
+                    if (ok) commit(s_full(tile));         // a tile without rows and the end are told too
                 }
                 if (!ok) break;
-                if (now != kEnd) commit(k_empty(b));
-                if (before != kEnd) commit(v_empty(c));
+                if (more) commit(k_empty(b));
+                if (owed) commit(v_empty(c));
             } else {
                 // S of this block, then O of the one before
-                if (now != kEnd) {
+                if (more) {
                     products_s(0, b, tmem + 128 * (it & 1));
                     commit(k_empty(b));
                     commit(s_full(it & 1));
                 }
-                if (before != kEnd) {
+                if (owed) {
                     const unsigned n = it - 1;
                     ok = mbar_wait(vp_full(n & 1), n >> 1 & 1, &abort_flag);
-                    if (ok && first && units++ > 0)       // the unit before has been read out of O
-                        ok = mbar_wait(o_free, units & 1, &abort_flag);
+                    if (ok && first && units_o++ > 0)     // the unit before has been read out of O
+                        ok = mbar_wait(o_free, units_o & 1, &abort_flag);
                     if (!ok) break;
                     tc_after();
                     products_o(0, c, tmem + 128 * (n & 1), first);
@@ -890,7 +937,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(const AttnArgs a)
                     commit(o_done(n & 1));
                 }
             }
-            if (now == kEnd) break;
+            if (!more) {
+                if (!kPair) {                             // the end, for both turns
+                    commit(s_full(it & 1));
+                    commit(s_full((it + 1) & 1));
+                }
+                break;
+            }
             before = now;
         }
         if (!ok) {                                        // what was issued still reads shared memory
@@ -934,7 +987,7 @@ template <int D, int kFormat, bool kPair>
 cudaError_t run_tiles(const AttnArgs& a, cudaStream_t s) {
     const int grid = tiles_grid<D, kFormat, kPair>();
     if (grid < 1) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_pdl(kv_tiles_kernel<D, kFormat, kPair>, dim3(grid), dim3(kThreads), tiles_smem(D, kPair), s, a);
+    const cudaError_t e = launch_pdl(kv_tiles_kernel<D, kFormat, kPair>, dim3(grid), dim3(Roles<kPair>::kThreads), tiles_smem(D, kPair), s, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(kv_join_kernel<TilesLine<kPair>, D>, dim3(grid * TilesLine<kPair>::kSplit), dim3(kJoinThreads), 0, s, a);
 }
