@@ -35,7 +35,7 @@ constexpr int kMaxPerSm = 4;           // CTAs
 constexpr int kDirectTiles = 24;       // tiles of a warp at most for one cluster per unit
 // at least 2 places of the line per warp; a unit's start and end cost about 8 tiles
 template <int NT>
-using RowsLine = Line<kKvTile, 8 * NT, kWarps, 2 * kWarps, 8, 2>;
+using RowsLine = Line<kKvTile, 8 * NT, kWarps, 2 * kWarps, 8, 2, false>;
 constexpr long kWaitLimit = 1L << 24;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }

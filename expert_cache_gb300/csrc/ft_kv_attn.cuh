@@ -119,10 +119,12 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, size_t token, int h
 // kCost blocks), and every CTA takes an equal share of the places.  Within a CTA the kW workers
 // split the share: its tiles of the unit where the whole share lies in one unit (the workers then
 // join in the CTA), its places otherwise.
-// kSplit: CTAs of the joining kernel per share.
-template <int kB_, int kR_, int kW_, int kMin_, int kCost_, int kSplit_>
+// kSplit: CTAs of the joining kernel per share.  kByRow: a thread of the first kernel has a whole row, so
+// partial sums stand as [D/4][R] groups of four values and neighbouring rows are written together.
+template <int kB_, int kR_, int kW_, int kMin_, int kCost_, int kSplit_, bool kByRow_>
 struct Line {
     static constexpr int kB = kB_, kR = kR_, kW = kW_, kMin = kMin_, kCost = kCost_, kSplit = kSplit_;
+    static constexpr bool kByRow = kByRow_;
 };
 
 constexpr int kMaxShares = 640;        // CTAs of a launch
@@ -279,7 +281,11 @@ __device__ __forceinline__ Piece piece_of(const Shares& sh, long long first, int
     return p;
 }
 
-// Partial sums of one piece of a unit in the workspace: [R] (reference, sum of weights), [R][D] values.
+// Where the four values d.. of a row stand among a piece's.
+template <typename L, int D>
+__device__ __forceinline__ int piece_at(int row, int d) { return L::kByRow ? d / 4 * L::kR + row : row * (D / 4) + d / 4; }
+
+// Partial sums of one piece of a unit in the workspace: [R] (reference, sum of weights), R D values.
 template <int D, int R>
 __device__ __forceinline__ float* partial(const AttnArgs& a, int slot) { return a.parts + (size_t)slot * (R * (D + 2)); }
 
@@ -334,7 +340,7 @@ __device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u,
     const int wide = n_threads / team, mine = thread % wide, first = thread / wide;
     for (int g0 = ga; g0 < gb; g0 += wide) {
         const int e = min(g0 + mine, gb - 1);
-        const int row = e / (D / 4), d = e % (D / 4) * 4;
+        const int row = L::kByRow ? e % rows : e / (D / 4), d = (L::kByRow ? e / rows : e % (D / 4)) * 4;
         float m = kNoRef, l = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         constexpr int kBatch = 8;                         // pieces in flight
@@ -353,7 +359,7 @@ __device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u,
                     const float2 ml = __ldcg(reinterpret_cast<const float2*>(src) + row);
                     pm[b] = ml.x;
                     pl[b] = ml.y;
-                    y[b] = __ldcg(reinterpret_cast<const float4*>(src + 2 * R + row * D + d));
+                    y[b] = __ldcg(reinterpret_cast<const float4*>(src + 2 * R) + piece_at<L, D>(row, d));
                 }
             }
 #pragma unroll

@@ -47,7 +47,7 @@ constexpr float kLeast = 1.2e-38f;
 // rows; the last of the unit's.
 constexpr unsigned kFirst = 0, kNext = 1, kEnd = 2, kKind = 3, kTwo = 4, kLast = 8;
 template <bool kPair>
-using TilesLine = Line<kKeys, kPair ? 2 * kRows : kRows, 1, 4, 3, 16>;
+using TilesLine = Line<kKeys, kPair ? 2 * kRows : kRows, 1, 4, 3, 8, true>;
 
 // Buffers of K and of V: two blocks where they fit beside Q.
 constexpr int bufs(int D) { return D == 256 ? 1 : 2; }
@@ -696,9 +696,9 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1) kv_tiles_kernel(con
                         if (done) {
                             store_out<8>(a, (size_t)(si.q0 + i), u.h * a.G + grow - i * a.G, D, x + e, y, m, l);
                         } else {
-                            float4* dst = reinterpret_cast<float4*>(out + 2 * kUnit + row * D + x + e);
+                            float4* dst = reinterpret_cast<float4*>(out + 2 * kUnit) + piece_at<L, D>(row, x + e);
                             dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                            dst[kUnit] = make_float4(y[4], y[5], y[6], y[7]);
                         }
                     }
                 }
