@@ -3,7 +3,7 @@
 //
 // The same one-pass softmax as the rows kernel, on the 5th-generation tensor cores.  A unit is 128
 // rows (token-major: row = token * G + head of the group) of a sequence and kv head; its keys come
-// in blocks of 128.  Per block S = Q K^T (128 x 128 x D, both operands in shared memory, fp32 in
+// in blocks of 128 (64 with heads of 256).  Per block S = Q K^T (128 x 128 x D, both operands in shared memory, fp32 in
 // tensor memory), P = 2^(t - m) as f16 back into tensor memory in the place of S, O += P V (128 x D
 // x 128, P from tensor memory, V from shared memory with the head dim contiguous).  One CTA per SM:
 //   warps 0-7   softmax: one row per thread, the two warpgroups taking turns with the blocks, so
@@ -33,12 +33,15 @@ namespace ft {
 
 namespace {
 
-constexpr int kKeys = 128, kRows = 128;
-constexpr int kTiles = kKeys / kKvTile;                    // tiles of a block
+constexpr int kRows = 128;
+// Keys of a block: with heads of 256 half as many, so that two blocks of K and of V fit beside Q (one
+// block of 128 each left the tensor cores waiting for every K: 10,000 clocks a block).
+constexpr int keys(int D) { return D == 256 ? 64 : 128; }
 // Warps of K (and again of V), their tiles of a block, first warps of the roles after the softmax's.
-template <bool kPair>
+template <int D, bool kPair>
 struct Roles {
-    static constexpr int kWide = kPair ? 4 : 8, kEach = kTiles / kWide;
+    static constexpr int kTiles = keys(D) / kKvTile;
+    static constexpr int kWide = kPair || D == 256 ? 4 : 8, kEach = kTiles / kWide;
     static constexpr int kK = 8, kV = kK + kWide, kMma = kV + kWide, kThreads = (kMma + 4) * 32;
 };
 constexpr int kWaitLimit = 1 << 20;
@@ -46,13 +49,14 @@ constexpr float kLeast = 1.2e-38f;
 // A block's marks: the first or a later one of its unit, or none left; the unit has a second tile of
 // rows; the last of the unit's.
 constexpr unsigned kFirst = 0, kNext = 1, kEnd = 2, kKind = 3, kTwo = 4, kLast = 8;
-template <bool kPair>
-using TilesLine = Line<kKeys, kPair ? 2 * kRows : kRows, 1, 4, 3, 8, true>;
+// a unit's start and end cost about 400 keys
+template <int D, bool kPair>
+using TilesLine = Line<keys(D), kPair ? 2 * kRows : kRows, 1, 4, D == 256 ? 6 : 3, 8, true>;
 
-// Buffers of K and of V: two blocks where they fit beside Q.
-constexpr int bufs(int D) { return D == 256 ? 1 : 2; }
-constexpr int region(int D) { return kKeys * D * 2; }                    // bytes of a block of K or V, and of Q
-constexpr size_t tiles_smem(int D, bool pair) { return (size_t)region(D) * ((pair ? 2 : 1) + 2 * bufs(D)) + 1024; }
+constexpr int kBufs = 2;                                                 // blocks of K and of V in shared memory
+constexpr int region(int D) { return keys(D) * D * 2; }                  // bytes of one
+constexpr int q_region(int D) { return kRows * D * 2; }                  // of a tile of rows of Q
+constexpr size_t tiles_smem(int D, bool pair) { return (size_t)(pair ? 2 : 1) * q_region(D) + 2 * kBufs * region(D) + 1024; }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void mbar_init(uint32_t b, int n) {
@@ -191,10 +195,11 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
 __device__ __forceinline__ void st_shared(uint32_t at, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-// Byte of 16-byte chunk c (8 dims) of row r of a [128 rows][D] operand.  Chunks that differ in the low
+// Byte of 16-byte chunk c (8 dims) of row r of a [kTall rows][D] operand.  Chunks that differ in the low
 // three bits of c differ in the same bits of (byte >> 4): at(r, c ^ z) = at(r, c) ^ (z << 4) for z < 8.
+template <int kTall>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-    return (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    return (c >> 3) * (kTall * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // A lane's raw bytes of a tile's K or V.
@@ -227,7 +232,7 @@ template <int D, int kFormat>
 __device__ __forceinline__ void write_k(uint32_t base, const Raw<D, kFormat>& r, int row0, int lane) {
     const int g = lane >> 2, t = lane & 3;
     // the lane's first chunk of row 8 v + g: rows 8 apart are 1024 bytes apart
-    const uint32_t at = base + chunk_at(row0 + g, t * (D / 32));
+    const uint32_t at = base + chunk_at<keys(D)>(row0 + g, t * (D / 32));
     if constexpr (kFormat == FT_KV_NVFP4) {
         if constexpr (D == 64) {
             const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
@@ -288,7 +293,8 @@ __device__ __forceinline__ void write_v(uint32_t base, const Raw<D, kFormat>& r,
     const bool odd = g & 1;
     // the lane's first chunk (odd lanes: second) of tokens 2t and 2t + 1; 8 tokens are 1024 bytes
     const uint32_t flip = odd && D > 64 ? 16 : 0;
-    const uint32_t at[2] = {base + (chunk_at(row0 + 2 * t, g * (D / 64)) ^ flip), base + (chunk_at(row0 + 2 * t + 1, g * (D / 64)) ^ flip)};
+    const uint32_t at[2] = {base + (chunk_at<keys(D)>(row0 + 2 * t, g * (D / 64)) ^ flip),
+                            base + (chunk_at<keys(D)>(row0 + 2 * t + 1, g * (D / 64)) ^ flip)};
     if constexpr (kFormat == FT_KV_NVFP4) {
         if constexpr (D == 64) {
             const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
@@ -380,16 +386,17 @@ struct Run {
 // neither waits for the other: S and O of a tile have their own tensor memory (2 * 128 + 2 * D columns,
 // so D up to 128).  Otherwise units of 128 rows, the warpgroups taking turns with the blocks.
 template <int D, int kFormat, bool kPair>
-__global__ void __launch_bounds__(Roles<kPair>::kThreads, 1) kv_tiles_kernel(const AttnArgs a) {
-    using L = TilesLine<kPair>;
-    using Role = Roles<kPair>;
+__global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(const AttnArgs a) {
+    using L = TilesLine<D, kPair>;
+    using Role = Roles<D, kPair>;
+    constexpr int kKeys = keys(D), kTiles = Role::kTiles;
     constexpr int kUnit = L::kR, kWarpK = Role::kK, kWarpV = Role::kV, kWarpMma = Role::kMma, kThreads = Role::kThreads;
     constexpr int kEach = Role::kEach;
-    constexpr int kBufs = bufs(D), kRegion = region(D);
+    constexpr int kRegion = region(D), kRegionQ = q_region(D);
     constexpr KvTile kT = kv_tile(D, kFormat);
     constexpr uint32_t kColO = 256;                       // S and P: columns 0..127 and 128..255
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    const uint32_t sq = (smem_u32(smem_raw) + 1023) & ~1023u, sk = sq + (kPair ? 2 : 1) * kRegion, sv = sk + kBufs * kRegion;
+    const uint32_t sq = (smem_u32(smem_raw) + 1023) & ~1023u, sk = sq + (kPair ? 2 : 1) * kRegionQ, sv = sk + kBufs * kRegion;
     __shared__ long long prefix[kMaxSeqs + 1], scratch[kThreads / 32];
     __shared__ __align__(8) uint64_t bars[30];
     __shared__ uint32_t tmem_base;
@@ -476,7 +483,7 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1) kv_tiles_kernel(con
 
     Run run;
     bool ok = true;
-    if constexpr (kPair) {                                // of 20 * 96: 8 * 128 + 8 * 88 + 4 * 40
+    if constexpr (Role::kWide == 4) {                     // of 20 * 96: 8 * 128 + 8 * 88 + 4 * 40
         if (warp >= kWarpMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         else if (warp >= kWarpK) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1) kv_tiles_kernel(con
                 unsigned there = 0;                       // the block's tiles
 #pragma unroll
                 for (int w = 0; w < Role::kWide; ++w) there |= (unsigned)present[it & 7][w] << (w * kEach);
-                const bool edge = there != 255u || j0 + kKeys - 1 > all_lim || (j0 < all_low && j0 + kKeys > a.n_sink) || u.empty;
+                const bool edge = there != (1u << kTiles) - 1 || j0 + kKeys - 1 > all_lim || (j0 < all_low && j0 + kKeys > a.n_sink) || u.empty;
                 // which of 32 keys the row sees
                 auto mask_of = [&](int ch) {
                     const int j = j0 + 32 * ch;
@@ -579,9 +586,9 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1) kv_tiles_kernel(con
                     uint32_t s[2][32];
                     tmem_ld32(s_addr, s[0]);
 #pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
+                    for (int ch = 0; ch < kKeys / 32; ++ch) {
                         tmem_wait_ld();
-                        if (ch < 3) tmem_ld32(s_addr + 32 * (ch + 1), s[(ch + 1) & 1]);
+                        if (ch + 1 < kKeys / 32) tmem_ld32(s_addr + 32 * (ch + 1), s[(ch + 1) & 1]);
                         float x = kNoRef, y = kNoRef;
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
@@ -592,7 +599,7 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1) kv_tiles_kernel(con
                     }
                 } else {
 #pragma unroll 1
-                    for (int ch = 0; ch < 4; ++ch) {
+                    for (int ch = 0; ch < kKeys / 32; ++ch) {
                         uint32_t s[32];
                         const unsigned seen = mask_of(ch);
                         __syncwarp();
@@ -641,9 +648,9 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1) kv_tiles_kernel(con
                 uint32_t s[2][32];
                 tmem_ld32(s_addr, s[0]);
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
+                for (int ch = 0; ch < kKeys / 32; ++ch) {
                     tmem_wait_ld();
-                    if (ch < 3) tmem_ld32(s_addr + 32 * (ch + 1), s[(ch + 1) & 1]);
+                    if (ch + 1 < kKeys / 32) tmem_ld32(s_addr + 32 * (ch + 1), s[(ch + 1) & 1]);
                     uint32_t p[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
@@ -768,7 +775,7 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1) kv_tiles_kernel(con
                 for (int j = lane; j < si.n; j += 32)
                     drafted[un & 3][j] = base + __popcll(a.tree[si.q0 + j] & ~(1ull << j));
             const int row_tiles = kPair && (long long)run.u.r * kUnit + kRows < (long long)si.n * a.G ? 2 : 1;
-            constexpr int kTimes = kTiles / Role::kWide;  // 8 rows at a time
+            constexpr int kTimes = kRows / 8 / (2 * Role::kWide);     // 8 rows at a time
 #pragma unroll 1
             for (int y = 0; y < row_tiles * kTimes; ++y) {
                 const int rt = y / kTimes, row = 8 * ((warp - kWarpK) * kTimes + y % kTimes) + (lane >> 3), part = lane & 7;
@@ -804,7 +811,7 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1) kv_tiles_kernel(con
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             o[y] = pack_f16(__uint_as_float(wd[y] << 16) * down, __uint_as_float(wd[y] & 0xFFFF0000u) * down);
-                        st_shared(sq + rt * kRegion + chunk_at(row + 4 * x, e * 8 + part), make_uint4(o[0], o[1], o[2], o[3]));
+                        st_shared(sq + rt * kRegionQ + chunk_at<kRows>(row + 4 * x, e * 8 + part), make_uint4(o[0], o[1], o[2], o[3]));
                     }
                 }
             }
@@ -864,11 +871,11 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1) kv_tiles_kernel(con
         // S of a tile of the block in buffer b; O of a tile of the block in buffer c, P at p
         auto products_s = [&](int tile, int b, uint32_t d) {
             if (lead) {
-                const uint64_t qd = q_desc + tile * (kRegion >> 4), kd = k_desc + b * (kRegion >> 4);
+                const uint64_t qd = q_desc + tile * (kRegionQ >> 4), kd = k_desc + b * (kRegion >> 4);
 #pragma unroll
                 for (int x = 0; x < D / 16; ++x) {
-                    const uint64_t at = ((x >> 2) * (kKeys * 128) + (x & 3) * 32) >> 4;
-                    mma_ss(d, qd + at, kd + at, idesc(kKeys, false), x > 0);
+                    const uint64_t in = ((x & 3) * 32) >> 4;
+                    mma_ss(d, qd + (x >> 2) * (kRows * 128 >> 4) + in, kd + (x >> 2) * (kKeys * 128 >> 4) + in, idesc(kKeys, false), x > 0);
                 }
             }
             __syncwarp();
@@ -973,7 +980,7 @@ int tiles_grid() {
     if (!v) {
         auto kern = kv_tiles_kernel<D, kFormat, kPair>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tiles_smem(D, kPair)) != cudaSuccess ||
-            all_shared(kern) != cudaSuccess || all_shared(kv_join_kernel<TilesLine<kPair>, D>) != cudaSuccess) {
+            all_shared(kern) != cudaSuccess || all_shared(kv_join_kernel<TilesLine<D, kPair>, D>) != cudaSuccess) {
             cudaGetLastError();
             return 0;
         }
@@ -987,9 +994,9 @@ template <int D, int kFormat, bool kPair>
 cudaError_t run_tiles(const AttnArgs& a, cudaStream_t s) {
     const int grid = tiles_grid<D, kFormat, kPair>();
     if (grid < 1) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_pdl(kv_tiles_kernel<D, kFormat, kPair>, dim3(grid), dim3(Roles<kPair>::kThreads), tiles_smem(D, kPair), s, a);
+    const cudaError_t e = launch_pdl(kv_tiles_kernel<D, kFormat, kPair>, dim3(grid), dim3(Roles<D, kPair>::kThreads), tiles_smem(D, kPair), s, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv_join_kernel<TilesLine<kPair>, D>, dim3(grid * TilesLine<kPair>::kSplit), dim3(kJoinThreads), 0, s, a);
+    return launch_pdl(kv_join_kernel<TilesLine<D, kPair>, D>, dim3(grid * TilesLine<D, kPair>::kSplit), dim3(kJoinThreads), 0, s, a);
 }
 
 template <int D, int kFormat>
