@@ -766,6 +766,9 @@ ft_status ft_kv_attention(ft_kv* kv, int32_t layer, const void* q, int64_t q_str
     a.max_q = max_q;
     a.hq = d.n_q_heads;
     a.G = d.n_q_heads / d.n_kv_heads;
+    a.g_shift = 0;
+    while ((1 << a.g_shift) < a.G) ++a.g_shift;
+    a.g_mul = (unsigned)((((uint64_t)1 << 32) * (uint64_t)((1 << a.g_shift) - a.G)) / (uint64_t)a.G + 1);
     a.tree = reinterpret_cast<const unsigned long long*>(tree_mask);
     a.window = window;
     a.n_sink = n_sink;

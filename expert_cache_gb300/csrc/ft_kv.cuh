@@ -40,6 +40,8 @@ struct AttnArgs {
     const int32_t* table;
     int table_stride, n_seqs, n_tokens, max_q;
     int hq, G;
+    unsigned g_mul;      // division by G: div_g
+    int g_shift;
     const unsigned long long* tree;
     int window, n_sink;
     float scale;
@@ -99,6 +101,12 @@ __device__ __forceinline__ int kv_k_scale_byte(int r, int b) {
 template <int D>
 __device__ __forceinline__ int kv_v_scale_byte(int r, int b) {
     return kv_tile(D, FT_KV_NVFP4).v_scales + (b * 4 + ((r & 7) >> 1)) * 4 + 2 * (r >> 3) + (r & 1);
+}
+
+// x / G for 0 <= x < 2^31 (division by an invariant integer through a multiplication, Granlund and
+// Montgomery 1994): shift = ceil(log2 G), mul = floor(2^32 (2^shift - G) / G) + 1.
+__device__ __forceinline__ int div_g(const AttnArgs& a, int x) {
+    return (int)((__umulhi(a.g_mul, (unsigned)x) + (unsigned)x) >> a.g_shift);
 }
 
 // Rows and cached length of sequence s, bounded as the interface says.

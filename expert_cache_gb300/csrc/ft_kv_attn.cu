@@ -159,7 +159,7 @@ __device__ __forceinline__ void join_cluster(const AttnArgs& a, const Unit& u, c
         }
         if (g0 + (int)threadIdx.x / team < gb && (threadIdx.x & (team - 1)) == 0) {
             const int grow = u.r * R + row;
-            store_out<4>(a, (size_t)(u.si.q0 + grow / a.G), u.h * a.G + grow % a.G, D, d, &sum.x, m, l);
+            store_out<4>(a, (size_t)(u.si.q0 + div_g(a, grow)), u.h * a.G + grow - div_g(a, grow) * a.G, D, d, &sum.x, m, l);
         }
     }
     cluster_sync();                                       // the others may still read this CTA's sums
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
         uint4 raw[NT][D / 32];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = row0 + 8 * nt + g, i = row / a.G;
+            const int row = row0 + 8 * nt + g, i = div_g(a, row);
             const __nv_bfloat16* src = a.q + (size_t)(u.si.q0 + i) * a.q_stride + (size_t)(u.h * a.G + row - i * a.G) * D + t * (D / 4);
 #pragma unroll
             for (int e = 0; e < D / 32; ++e)
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                 coef[nt][b] = __shfl_sync(0xffffffffu, c, 4 * (2 * t + b));
                 const int mine = row0 + 8 * nt + 2 * t + b;
                 rule[nt][b] = row_rule(a, u.si, mine);
-                if (mine / a.G < u.si.n) {
+                if (div_g(a, mine) < u.si.n) {
                     lim_min = min(lim_min, a.tree ? min(rule[nt][b].lim, base - 1) : rule[nt][b].lim);
                     low_max = max(low_max, rule[nt][b].low);
                 }
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                     x.x += y.x; x.y += y.y; x.z += z.x; x.w += z.y;
                 }
                 if (done) {
-                    const int i = (row0 + row) / a.G;
+                    const int i = div_g(a, row0 + row);
                     store_out<4>(a, (size_t)(u.si.q0 + i), u.h * a.G + row0 + row - i * a.G, D, d, &x.x, ml.x, ml.y);
                 } else if (kDirect) {                     // for the cluster: in the place of warp 0's
                     *reinterpret_cast<float2*>(buf + at) = make_float2(x.x, x.y);
@@ -678,10 +678,10 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int row = 8 * nt + 2 * t + b, i = (row0 + row) / a.G;
+                const int row = 8 * nt + 2 * t + b, i = div_g(a, row0 + row);
                 if (i >= u.si.n) continue;
                 if (done) {
-                    const int h = u.h * a.G + (row0 + row) % a.G;
+                    const int h = u.h * a.G + row0 + row - i * a.G;
 #pragma unroll
                     for (int x = 0; x < D / 32; ++x) {
                         const float v[4] = {acc[2 * x][nt][b], acc[2 * x][nt][2 + b], acc[2 * x + 1][nt][b],

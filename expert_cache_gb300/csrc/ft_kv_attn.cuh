@@ -31,8 +31,8 @@ struct RowTile {
 template <int kB>
 __device__ __forceinline__ RowTile row_tile(const AttnArgs& a, const SeqInfo& s, int r, int R) {
     RowTile t;
-    t.i0 = r * R / a.G;
-    t.i1 = min(s.n - 1, (r * R + R - 1) / a.G);
+    t.i0 = div_g(a, r * R);
+    t.i1 = min(s.n - 1, div_g(a, r * R + R - 1));
     const int base = s.len - s.n;
     const int hi = a.tree ? s.len : min(s.len, base + t.i1 + 1);
     // a drafted token stands at base or after it
@@ -58,7 +58,7 @@ struct RowRule {
 };
 __device__ __forceinline__ RowRule row_rule(const AttnArgs& a, const SeqInfo& s, int row) {
     RowRule r{-1, 0, 0};
-    const int i = row / a.G;
+    const int i = div_g(a, row);
     if (i >= s.n) return r;            // padding
     const int base = s.len - s.n;
     int pos = base + i;
@@ -391,7 +391,7 @@ __device__ __forceinline__ void join_slice(const AttnArgs& a, const JoinTask& u,
         }
         if (g0 + mine < gb && first == 0) {
             const int grow = u.r * R + row;
-            store_out<4>(a, (size_t)(u.q0 + grow / a.G), u.h * a.G + grow % a.G, D, d, &x.x, m, l);
+            store_out<4>(a, (size_t)(u.q0 + div_g(a, grow)), u.h * a.G + grow - div_g(a, grow) * a.G, D, d, &x.x, m, l);
         }
     }
 }

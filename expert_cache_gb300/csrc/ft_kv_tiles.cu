@@ -483,7 +483,11 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
 
     Run run;
     bool ok = true;
-    if constexpr (Role::kWide == 4) {                     // of 20 * 96: 8 * 128 + 8 * 88 + 4 * 40
+    if constexpr (D == 256) {                             // of 20 * 96: 8 * 112 + 8 * 104 + 4 * 40
+        if (warp >= kWarpMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        else if (warp >= kWarpK) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    } else if constexpr (Role::kWide == 4) {              // of 20 * 96: 8 * 128 + 8 * 88 + 4 * 40
         if (warp >= kWarpMma) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
         else if (warp >= kWarpK) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
@@ -533,7 +537,7 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
                 rule = row_rule(a, si, grow);
                 // keys below all_lim and from all_low on are seen by every row of the tile
                 all_lim = a.tree ? base - 1 : row_rule(a, si, u.r * kUnit + row0).lim;
-                const int last = kPair ? min(si.n - 1, (u.r * kUnit + row0 + kRows - 1) / a.G) : u.i1;
+                const int last = kPair ? min(si.n - 1, div_g(a, u.r * kUnit + row0 + kRows - 1)) : u.i1;
                 all_low = a.window > 0 ? (int)max((long long)(a.tree ? base + si.n : base + last) - a.window + 1, 0LL) : 0;
                 m = kNoRef;
                 c = coef[un & 3][row];
@@ -684,7 +688,7 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             ++un;
             if (m != kNoRef) m *= c;
             tc_after();
-            const int i = grow / a.G;
+            const int i = div_g(a, grow);
             const bool on = i < si.n, done = u.slot < 0;
             float* out = partial<D, kUnit>(a, max(u.slot, 0));
             if (on && !done && (kPair || wg == 0)) reinterpret_cast<float2*>(out)[row] = make_float2(m, l);
@@ -763,9 +767,8 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
                     }
                 }
             };
-            load(run.v0);
-            // Q of the unit, once every product of the unit before is through with it: 8 lanes per row, two
-            // rows of a lane under way
+            // Q of the unit, once every product of the unit before is through with it: 8 lanes per row, a
+            // tile's rows of a lane under way together
             if (it > 0 && !mbar_wait(k_empty((it - 1) % kBufs), ((it - 1) / kBufs) & 1, &abort_flag)) { ok = false; break; }
             if (warp == kWarpK && lane == 0) {
                 const bool all = run.v0 == 0 && run.v1 == run.u.rt.nt;
@@ -775,21 +778,21 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
                 for (int j = lane; j < si.n; j += 32)
                     drafted[un & 3][j] = base + __popcll(a.tree[si.q0 + j] & ~(1ull << j));
             const int row_tiles = kPair && (long long)run.u.r * kUnit + kRows < (long long)si.n * a.G ? 2 : 1;
-            constexpr int kTimes = kRows / 8 / (2 * Role::kWide);     // 8 rows at a time
+            constexpr int kLane = kRows / (8 * Role::kWide);      // rows of a lane
 #pragma unroll 1
-            for (int y = 0; y < row_tiles * kTimes; ++y) {
-                const int rt = y / kTimes, row = 8 * ((warp - kWarpK) * kTimes + y % kTimes) + (lane >> 3), part = lane & 7;
-                uint4 q[2][D / 64];
+            for (int rt = 0; rt < row_tiles; ++rt) {
+                const int row = 4 * kLane * (warp - kWarpK) + (lane >> 3), part = lane & 7;
+                uint4 q[kLane][D / 64];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int grow = run.u.r * kUnit + kRows * rt + row + 4 * x, i = grow / a.G;
+                for (int x = 0; x < kLane; ++x) {
+                    const int grow = run.u.r * kUnit + kRows * rt + row + 4 * x, i = div_g(a, grow);
                     const __nv_bfloat16* src = a.q + (size_t)(si.q0 + i) * a.q_stride + (size_t)(run.u.h * a.G + grow - i * a.G) * D + part * 8;
 #pragma unroll
                     for (int e = 0; e < D / 64; ++e)
                         q[x][e] = i < si.n ? *reinterpret_cast<const uint4*>(src + 64 * e) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
+                for (int x = 0; x < kLane; ++x) {
                     float amax = 0.f;
 #pragma unroll
                     for (int e = 0; e < D / 64; ++e) {
@@ -818,6 +821,7 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
+            load(run.v0);
             for (int v = run.v0; v < run.v1; ++v, ++it) {
                 const int b = it % kBufs;
                 if (!mbar_wait(is_k ? k_empty(b) : v_empty(b), ((it / kBufs) & 1) ^ 1, &abort_flag)) { ok = false; break; }
@@ -893,8 +897,32 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             if (lead) tc_commit(bar);
             __syncwarp();
         };
+        // O of block n, the last of its unit, without waiting for the next unit's K
+        auto finish = [&](unsigned n, unsigned marks) {
+            const int c = n % kBufs;
+            if (kPair && !mbar_wait(v_full(c), (n / kBufs) & 1, &abort_flag)) return false;
+#pragma unroll
+            for (int tile = 0; tile < (kPair ? 2 : 1); ++tile) {
+                const int at = kPair ? tile : n & 1;
+                if (!mbar_wait(vp_full(at), (kPair ? n : n >> 1) & 1, &abort_flag)) return false;
+                const bool first = (marks & kKind) == kFirst;
+                if (!kPair && first && units_o++ > 0 && !mbar_wait(o_free, units_o & 1, &abort_flag)) return false;
+                if (tile == 0 || marks & kTwo) {
+                    tc_after();
+                    products_o(tile, c, tmem + 128 * at, first);
+                    commit(o_done(at));
+                }
+            }
+            commit(v_empty(c));
+            return true;
+        };
         for (unsigned it = 0, before = kEnd;; ++it) {
             const int b = it % kBufs, c = (it - 1) % kBufs;
+            if (before != kEnd && before & kLast) {
+                ok = finish(it - 1, before);
+                if (!ok) break;
+                before = kEnd;
+            }
             ok = mbar_wait(k_full(b), (it / kBufs) & 1, &abort_flag);
             if (!ok) break;
             tc_after();
@@ -916,7 +944,6 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
                         if (ok && (tile == 0 || before & kTwo)) {
                             tc_after();
                             products_o(tile, c, tmem + 128 * tile, first);
-                            if (before & kLast) commit(o_done(tile));
                         }
                     }
                     if (ok && more && (tile == 0 || now & kTwo)) products_s(tile, b, tmem + 128 * tile);
