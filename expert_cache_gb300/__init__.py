@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -138,10 +139,7 @@ _f = {
                          c_int64, c_void_p, c_int32, c_void_p),
     "ft_kv_read": _sig("ft_kv_read", c_int32, c_void_p, c_int32, c_void_p, c_int32, c_void_p,
                        c_void_p, c_void_p),
-    "ft_kv_attention": _sig("ft_kv_attention", c_int32, c_void_p, c_int32, c_void_p, c_int64,
-                            c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32,
-                            c_void_p, c_int32, c_int32, c_float, c_void_p, c_int64, c_void_p,
-                            c_void_p),
+    "ft_kv_attention": _sig("ft_kv_attention", c_int32, c_void_p, c_void_p, c_void_p),
     "ft_kv_status": _sig("ft_kv_status", c_int32, c_void_p, _P(c_int32)),
     "ft_kv_last_error": _sig("ft_kv_last_error", ctypes.c_char_p, c_void_p),
     "ft_status_string": _sig("ft_status_string", ctypes.c_char_p, c_int32),
@@ -159,12 +157,12 @@ class FtError(RuntimeError):
 
 def _ptr(t):
     """Raw address of a tensor / ndarray / int / None."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    if hasattr(t, "data_ptr"):
+    try:
         return t.data_ptr()
+    except AttributeError:
+        pass
+    if t is None or isinstance(t, int):
+        return t
     if isinstance(t, np.ndarray):
         return t.ctypes.data
     raise TypeError(f"cannot take the address of {type(t)}")
@@ -420,9 +418,10 @@ def _stride(t, given, name):
     """Token stride in elements: the one given, or that of a tensor."""
     if given is not None:
         return given
-    if hasattr(t, "stride"):
+    try:
         return t.stride(0)
-    raise TypeError(f"{name} is needed with a raw pointer")
+    except AttributeError:
+        raise TypeError(f"{name} is needed with a raw pointer") from None
 
 
 def ft_kv_append(handle, layer, k, v, slots, n, k_stride=None, v_stride=None, stream=None):
@@ -436,14 +435,21 @@ def ft_kv_read(handle, layer, slots, n, k_out, v_out, stream=None):
                                _stream(stream)), handle)
 
 
+# ft_kv_attn, packed at once (one conversion per field would cost more than the launch)
+_KV_ATTN = struct.Struct("@3P2q4P7if")
+_kv_attention = _f["ft_kv_attention"]
+
+
 def ft_kv_attention(handle, layer, q, q_start, kv_len, block_table, table_stride, n_seqs, n_tokens,
                     max_q, o, tree_mask=None, window=0, n_sink=0, sm_scale=1.0, lse=None,
                     q_stride=None, o_stride=None, stream=None):
-    _check_kv(_f["ft_kv_attention"](handle, layer, _ptr(q), _stride(q, q_stride, "q_stride"),
-                                    _ptr(q_start), _ptr(kv_len), _ptr(block_table), table_stride,
-                                    n_seqs, n_tokens, max_q, _ptr(tree_mask), window, n_sink,
-                                    sm_scale, _ptr(o), _stride(o, o_stride, "o_stride"), _ptr(lse),
-                                    _stream(stream)), handle)
+    status = _kv_attention(handle, _KV_ATTN.pack(
+        _ptr(q) or 0, _ptr(o) or 0, _ptr(lse) or 0, _stride(q, q_stride, "q_stride"),
+        _stride(o, o_stride, "o_stride"), _ptr(q_start) or 0, _ptr(kv_len) or 0,
+        _ptr(block_table) or 0, _ptr(tree_mask) or 0, layer, table_stride, n_seqs, n_tokens, max_q,
+        window, n_sink, sm_scale), _stream(stream))
+    if status:
+        _check_kv(status, handle)
 
 
 def ft_kv_status(handle):

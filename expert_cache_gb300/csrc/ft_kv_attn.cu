@@ -32,11 +32,10 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kMaxPerSm = 4;           // CTAs
-constexpr int kDirectTiles = 24;       // tiles of a warp at most for one cluster per unit
 // at least 2 places of the line per warp; a unit's start and end cost about 8 tiles
 template <int NT>
 using RowsLine = Line<kKvTile, 8 * NT, kWarps, 2 * kWarps, 8, 2, false>;
-constexpr long kWaitLimit = 1L << 24;
+constexpr int kWaitLimit = 1 << 24;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -109,7 +108,7 @@ constexpr size_t rows_smem() {
 }
 
 // CTAs per SM that the register allocation aims at.
-constexpr int rows_ctas(int D, int NT) { return D == 256 ? (NT == 1 ? 3 : 2) : D == 128 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : 3; }
+constexpr int rows_ctas(int D, int NT) { return D == 256 ? 2 : D == 128 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : 3; }
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -376,11 +375,18 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
         };
 
         // ---------------------------------------------------------------- the keys
+        bool gave_up = false;
         for (int v = v0; v < vend; ++v) {
             const uint32_t bar = bar0 + 8 * cur;
             bool ok = false;
-            for (long it = 0; it < kWaitLimit && !ok; ++it) ok = mbar_try(bar, parity >> cur & 1);
-            if (!ok && lane == 0) atomicOr(a.kv.status, FT_DEV_TIMEOUT);
+            for (int it = 0; it < kWaitLimit && !ok; ++it) ok = mbar_try(bar, parity >> cur & 1);
+            if (!__all_sync(0xffffffffu, ok)) {           // give up, once the copies in flight have had their time
+                for (int x = 0; x < kStages && x < vend - v; ++x, cur = cur + 1 == kStages ? 0 : cur + 1)
+                    for (int it = 0; it < kWaitLimit && !mbar_try(bar0 + 8 * cur, parity >> cur & 1); ++it) {}
+                if (lane == 0) atomicOr(a.kv.status, FT_DEV_TIMEOUT);
+                gave_up = true;
+                break;
+            }
             parity ^= 1u << cur;
             const uint8_t* tile = ring + cur * kT.bytes;
             const int j0 = u.rt.block(v) * kKvTile;
@@ -696,83 +702,131 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                     if (g == 0) reinterpret_cast<float2*>(out)[row] = make_float2(m[nt][b], l[nt][b]);
                 }
             }
+        if (gave_up) break;
     }
-
 }
 
 namespace {
 
-// CTAs of the rows kernel that are resident at once (0 when it cannot be set up; looked up once per
-// device).
+void direct_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], unsigned grid, int split, size_t smem, cudaStream_t s) {
+    cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1] = {};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+}
+
+// What of the rows kernel is resident at once, in CTAs: by shares, and direct by the log2 of a cluster's
+// CTAs (clusters lie within a part of the GPU, so the largest leave SMs out).  Looked up once per device.
+struct RowsRoom {
+    int grid, room[5];
+};
 template <int D, int kFormat, int NT>
-int rows_grid() {
-    static std::atomic<int> grids[kMaxDevices];
+cudaError_t rows_room(RowsRoom& r) {
+    static std::atomic<int> known[kMaxDevices][6];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-        cudaGetLastError();
-        return 0;
-    }
-    int v = grids[dev].load(std::memory_order_relaxed);
-    if (!v) {
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!known[dev][0].load(std::memory_order_acquire)) {
         auto kern = kv_rows_kernel<D, kFormat, NT, false>;
         auto direct = kv_rows_kernel<D, kFormat, NT, true>;
         constexpr size_t smem = rows_smem<D, kFormat, NT>();
         int n = 0;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-            cudaFuncSetAttribute(direct, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-            cudaFuncSetAttribute(direct, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-            all_shared(kern) != cudaSuccess || all_shared(direct) != cudaSuccess ||
-            all_shared(kv_join_kernel<RowsLine<NT>, D>) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem) != cudaSuccess) {
-            cudaGetLastError();
-            return 0;
+        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(direct, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(direct, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess ||
+            (e = all_shared(kern)) != cudaSuccess || (e = all_shared(direct)) != cudaSuccess ||
+            (e = all_shared(kv_join_kernel<RowsLine<NT>, D>)) != cudaSuccess ||
+            (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem)) != cudaSuccess)
+            return e;
+        const int grid = min(sm_count() * min(n, kMaxPerSm), kMaxShares);
+        if (grid < 1) return cudaErrorInvalidConfiguration;
+        known[dev][1].store(grid, std::memory_order_relaxed);
+        for (int x = 1; x < 5; ++x) {
+            cudaLaunchConfig_t cfg;
+            cudaLaunchAttribute attr[2];
+            direct_config(cfg, attr, grid >> x << x, 1 << x, smem, nullptr);
+            cfg.attrs = attr + 1;
+            cfg.numAttrs = 1;
+            if ((e = cudaOccupancyMaxActiveClusters(&n, direct, &cfg)) != cudaSuccess) return e;
+            known[dev][1 + x].store(min(n << x, grid), std::memory_order_relaxed);
         }
-        v = min(sm_count() * min(n, kMaxPerSm), kMaxShares);
-        grids[dev].store(v, std::memory_order_relaxed);
+        known[dev][0].store(1, std::memory_order_release);
     }
-    return v;
+    r.grid = known[dev][1].load(std::memory_order_relaxed);
+    for (int x = 0; x < 5; ++x) r.room[x] = known[dev][1 + x].load(std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+// 16-token tiles of a unit at most, as far as the host knows.
+long long most_tiles(const AttnArgs& a) {
+    const long long tiles = ((long long)a.table_stride << a.kv.page_shift) / kKvTile;
+    return a.window > 0 ? min(tiles, ((long long)a.window + a.max_q + a.n_sink) / kKvTile + 4) : tiles;
+}
+
+// Direct: a.split CTAs per unit.  It saves the scan of the lengths, the partial sums and the second kernel,
+// but a unit's tiles are not evened out over the SMs.  So it goes up to 24 tiles a warp where there are two
+// CTAs per SM (32 sequences of 1024 with 8 heads of 256: 23 us, 36 us by shares; of 300 to 1850, 29 tiles, with
+// heads of 128: 26 and 24 us), fewer where SMs stay idle, down to 12 (one sequence with 2 heads of 128: 4096
+// tokens, 4 tiles, 7.6 us and 10.0 us; 16384, 16 tiles, 15.0 and 13.2 us).
+bool plan_direct(AttnArgs& a, const RowsRoom& room, int rows) {
+    a.row_tiles = (int)(((long long)a.max_q * a.G + rows - 1) / rows);
+    const long long units = (long long)a.n_seqs * a.kv.hkv * a.row_tiles, tiles = most_tiles(a);
+    int x = 0;
+    while (x < 4 && units << (x + 1) <= room.room[x + 1] && tiles > kWarps << x) ++x;
+    a.split = 1 << x;
+    const long long ctas = units << x;
+    return ctas <= 2LL * room.grid && tiles <= max(12LL, min(24LL, 12 * ctas / sm_count())) * kWarps << x;
 }
 
 template <int D, int kFormat, int NT>
-cudaError_t run_rows(AttnArgs a, cudaStream_t s) {
-    const int grid = rows_grid<D, kFormat, NT>();
-    if (grid < 1) return cudaErrorInvalidConfiguration;
-    // The host knows how long a sequence can be at most.  Direct where that leaves a warp few tiles
-    // with all of a unit's CTAs in one cluster and all clusters (nearly) at once: it saves the scan of
-    // the lengths, the partial sums and the second kernel (one token over 4096 of 2 heads of 256: 14.1
-    // us by shares), but a unit's length is not evened out over the SMs.
-    a.row_tiles = (int)(((long long)a.max_q * a.G + 8 * NT - 1) / (8 * NT));
-    const long long units = (long long)a.n_seqs * a.kv.hkv * a.row_tiles;
-    long long tiles = ((long long)a.table_stride << a.kv.page_shift) / kKvTile;
-    if (a.window > 0) tiles = min(tiles, ((long long)a.window + a.max_q + a.n_sink) / kKvTile + 4);
-    a.split = 1;
-    while (a.split < 16 && units * a.split * 2 <= grid && tiles > kWarps * a.split) a.split *= 2;
-    if (tiles <= kDirectTiles * kWarps * a.split && units * a.split <= 2LL * grid) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(units * a.split));
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = rows_smem<D, kFormat, NT>();
-        cfg.stream = s;
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = a.split;
-        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = a.split > 1 ? 2 : 1;
-        return cudaLaunchKernelEx(&cfg, kv_rows_kernel<D, kFormat, NT, true>, a);
-    }
-    const cudaError_t e = launch_pdl(kv_rows_kernel<D, kFormat, NT, false>, dim3(grid), dim3(kThreads), rows_smem<D, kFormat, NT>(), s, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kv_join_kernel<RowsLine<NT>, D>, dim3(grid * RowsLine<NT>::kSplit), dim3(kJoinThreads), 0, s, a);
+cudaError_t launch_direct(const AttnArgs& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    direct_config(cfg, attr, (unsigned)(a.n_seqs * a.kv.hkv * a.row_tiles * a.split), a.split, rows_smem<D, kFormat, NT>(), s);
+    return cudaLaunchKernelEx(&cfg, kv_rows_kernel<D, kFormat, NT, true>, a);
 }
 
+template <int D, int kFormat, int NT>
+cudaError_t run_rows(AttnArgs a, const RowsRoom& room, cudaStream_t s) {
+    if (plan_direct(a, room, 8 * NT)) return launch_direct<D, kFormat, NT>(a, s);
+    const cudaError_t e = launch_pdl(kv_rows_kernel<D, kFormat, NT, false>, dim3(room.grid), dim3(kThreads), rows_smem<D, kFormat, NT>(), s, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kv_join_kernel<RowsLine<NT>, D>, dim3(room.grid * RowsLine<NT>::kSplit), dim3(kJoinThreads), 0, s, a);
+}
+
+// Up to 32 rows of a sequence and kv head go by the rows kernel, row tiles of 8 or of 16 (8 rows over 4096
+// tokens of 2 heads of 128: 7.5 us, 8.3 us in a tile of 16).  It unpacks a key once per 16 rows, the tiles
+// kernel once per 128 or 256, which takes longer to start (16 sequences of 8192 with 2 heads of 128, 32 rows: 37
+// us, 39 us by tiles; 48 rows: 51 and 39 us).  More rows go by it too while all the call's work is small:
+// (16-row tile, key tile) products times (D + 128) up to 3 * 2^20, which take 15 to 21 us of the 20 to 27 us of
+// the tiles kernel's shortest calls (512 rows over 1024 of 2 heads of 128: 10.5 and 30 us; 256 rows over
+// 16384: 37 and 27 us).
 template <int D, int kFormat>
-cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+cudaError_t run(AttnArgs a, cudaStream_t s) {
     const long long rows = (long long)a.max_q * a.G;
-    if (rows > 32) return launch_kv_tiles(a, D, kFormat, s);
-    return rows <= 8 ? run_rows<D, kFormat, 1>(a, s) : run_rows<D, kFormat, 2>(a, s);
+    RowsRoom room;
+    cudaError_t e;
+    if (rows <= 8) {
+        if ((e = rows_room<D, kFormat, 1>(room)) != cudaSuccess) return e;
+        return run_rows<D, kFormat, 1>(a, room, s);
+    }
+    const long long row_tiles = (rows + 15) / 16, most = (3LL << 20) / (D + 128);
+    const bool small = row_tiles <= most && row_tiles * a.n_seqs * a.kv.hkv <= most / most_tiles(a);
+    if (rows > 32 && !small) return launch_kv_tiles(a, D, kFormat, s);
+    if ((e = rows_room<D, kFormat, 2>(room)) != cudaSuccess) return e;
+    if (rows <= 32) return run_rows<D, kFormat, 2>(a, room, s);
+    return plan_direct(a, room, 16) ? launch_direct<D, kFormat, 2>(a, s) : launch_kv_tiles(a, D, kFormat, s);
 }
 
 }  // namespace

@@ -473,18 +473,11 @@ ft_status ft_kv_read(ft_kv* kv, int32_t layer, const int32_t* slots, int32_t n, 
  *                    and, for a drafted token under a tree, base + the number of set bits of
  *                    its mask other than its own.
  * o = sum_j softmax_j(sm_scale * q.k_j) v_j over the keys seen, lse = log sum_j exp(sm_scale *
- * q.k_j); a row that sees no key has o = 0 and lse = -inf.  Products are exact, sums and
- * softmax statistics fp32, the softmax weights rounded to f16; results do not depend on the
- * run (every sum has a fixed order for given arguments on one GPU).
- *   q           device bf16 [n_tokens, n_q_heads, D], token stride q_stride (elements)
- *   q_start     device int32 [n_seqs + 1], ascending, within [0, n_tokens]
- *   kv_len      device int32 [n_seqs]
- *   block_table device int32 [n_seqs, table_stride]: page of each page_size tokens in order;
- *               only the pages that hold keys some row sees are read
- *   max_q       the most new tokens that any sequence has (at most 64 with tree_mask)
- *   tree_mask   device uint64 [n_tokens] or NULL
- *   o           device bf16 [n_tokens, n_q_heads, D], token stride o_stride (elements)
- *   lse         device fp32 [n_tokens, n_q_heads] or NULL
+ * q.k_j); a row that sees no key has o = 0 and lse = -inf.  Stored values enter the products
+ * exactly, q exactly down to 2^-27 of its row's largest magnitude (rounded below); sums and
+ * softmax statistics are fp32, the softmax weights rounded to f16.  Results do not depend on
+ * the run: every sum has a fixed order for given arguments on one GPU.
+ * The call's arguments are the fields of ft_kv_attn, read before it returns.
  * Rows of q and o are 16-byte aligned.  Rows outside every sequence are left as they are.
  * Asynchronous on stream, capturable, no allocation; calls of one handle share its
  * workspace, so they run one after another (one stream, or ordered by events).
@@ -492,14 +485,32 @@ ft_status ft_kv_read(ft_kv* kv, int32_t layer, const int32_t* slots, int32_t n, 
  * max_q rows (the rest are left as they are), kv_len outside [0, table_stride * page_size]
  * and pages outside [0, n_pages) (their keys are not seen) set FT_DEV_BAD_ID.
  * Errors (nothing launched): FT_ERR_ARG for layer, n_seqs outside [0, max_seqs], n_tokens
- * < 0, table_stride < 1, max_q < 1 (or > 64 with tree_mask), window < 0, n_sink < 0, a
- * sm_scale that is not finite, NULL or misaligned pointers, bad strides. */
-ft_status ft_kv_attention(ft_kv* kv, int32_t layer, const void* q, int64_t q_stride,
-                          const int32_t* q_start, const int32_t* kv_len,
-                          const int32_t* block_table, int32_t table_stride, int32_t n_seqs,
-                          int32_t n_tokens, int32_t max_q, const uint64_t* tree_mask,
-                          int32_t window, int32_t n_sink, float sm_scale, void* o,
-                          int64_t o_stride, float* lse, void* stream);
+ * < 0, table_stride < 1, max_q < 1 (or > 64 with tree_mask, or more than 2^30 rows with a
+ * group's query heads), window < 0, n_sink < 0, a sm_scale that is not finite, NULL or
+ * misaligned pointers, bad strides. */
+typedef struct {
+    const void* q;          /* device bf16 [n_tokens, n_q_heads, D] */
+    void* o;                /* device bf16 [n_tokens, n_q_heads, D] */
+    float* lse;             /* device fp32 [n_tokens, n_q_heads] or NULL */
+    int64_t q_stride;       /* token strides of q and o in elements: multiples of 8, at least */
+    int64_t o_stride;       /*   n_q_heads * D */
+    const int32_t* q_start; /* device [n_seqs + 1], ascending, within [0, n_tokens] */
+    const int32_t* kv_len;  /* device [n_seqs] */
+    const int32_t* block_table; /* device [n_seqs, table_stride]: page of each page_size tokens in
+                               order; only the pages that hold keys some row sees are read */
+    const uint64_t* tree_mask;  /* device [n_tokens] or NULL */
+    int32_t layer;
+    int32_t table_stride;   /* also bounds the sequences' lengths: how the work is divided follows
+                               from it, so a table no wider than the lengths need is faster */
+    int32_t n_seqs;
+    int32_t n_tokens;
+    int32_t max_q;          /* the most new tokens that any sequence has (at most 64 with
+                               tree_mask); max_q * n_q_heads / n_kv_heads at most 2^30 */
+    int32_t window;         /* 0: none */
+    int32_t n_sink;
+    float sm_scale;
+} ft_kv_attn;
+ft_status ft_kv_attention(ft_kv* kv, const ft_kv_attn* call, void* stream);
 
 /* Read and clear the handle's device status word (FT_DEV_* bits).  Synchronises. */
 ft_status ft_kv_status(ft_kv* kv, int32_t* device_status);

@@ -27,6 +27,13 @@ def bf16(rng, *shape, scale=1.0):
     return torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(torch.bfloat16)
 
 
+@pytest.fixture(autouse=True, params=[0, 980], ids=["alone", "crowd"])
+def crowd(request):
+    """Empty sequences behind every call's own: with many of them the host has to expect much work, so the same
+    small cases go by the kernels of large calls."""
+    Case.crowd = request.param
+
+
 class Case:
     """A cache filled through ft_kv_append (the rest of the pool holds 0xFF bytes) and the
     oracle's values of every token."""
@@ -41,7 +48,7 @@ class Case:
         order = rng.permutation(n_pages)
         stride = max(per + [1]) + spare                      # spare columns: the longest sequence the host can expect
         table = np.full((len(lens), stride), -1, np.int32)              # never read past the keys
-        self.kv = ft.KVCache(L, n_pages, page, hkv, D, hkv * G, max(len(lens), 1), fmt, k_scale, v_scale,
+        self.kv = ft.KVCache(L, n_pages, page, hkv, D, hkv * G, max(len(lens), 1) + self.crowd, fmt, k_scale, v_scale,
                              pool=torch.full((ft.ft_kv_required_sizes(ft.FtKvDesc(
                                  L, n_pages, page, hkv, D, hkv * G, len(lens), ft.KV_FORMATS[fmt], k_scale, v_scale,
                                  None, None))[0],), 255, dtype=torch.uint8, device="cuda"))
@@ -61,10 +68,10 @@ class Case:
             ft.ft_kv_append(self.kv.handle, layer, torch.cat(ks).cuda(), torch.cat(vs).cuda(),
                             torch.from_numpy(slots).cuda(), slots.size)
         self.table_np, self.slots = table, slots
-        self.table = torch.from_numpy(table).cuda()
+        self.table = torch.from_numpy(np.concatenate([table, np.full((self.crowd, stride), -1, np.int32)])).cuda()[:len(lens)]
         self.start_np = np.concatenate([[0], np.cumsum(nq)]).astype(np.int32)
-        self.start = torch.from_numpy(self.start_np).cuda()
-        self.len_dev = torch.tensor(self.lens, dtype=torch.int32, device="cuda")
+        self.start = torch.from_numpy(np.concatenate([self.start_np, np.repeat(self.start_np[-1:], self.crowd)])).cuda()
+        self.len_dev = torch.tensor(self.lens + [0] * self.crowd, dtype=torch.int32, device="cuda")[:len(lens)]
         self.T = int(self.start_np[-1])
         self.q = bf16(rng, self.T, hkv * G, D)
         self.scale = 1.0 / np.sqrt(D)
@@ -78,7 +85,7 @@ class Case:
         o = torch.full((self.T, self.hkv * self.G, self.D), float("nan"), dtype=torch.bfloat16, device="cuda") if o is None else o
         z = torch.full((self.T, self.hkv * self.G), float("nan"), device="cuda") if lse else None
         self.ft.ft_kv_attention(self.kv.handle, self.layer, q, self.start, self.len_dev, self.table, self.table.stride(0),
-                                len(self.lens), self.T, max_q or max(self.nq), o, tree_mask=self.tree, window=window,
+                                len(self.lens) + self.crowd, self.T, max_q or max(self.nq), o, tree_mask=self.tree, window=window,
                                 n_sink=n_sink, sm_scale=self.scale, lse=z, stream=stream)
         return o, z
 
@@ -389,8 +396,8 @@ def test_refusals(ft):
     good = dict(layer=0, q=q, q_start=c.start, kv_len=c.len_dev, block_table=c.table, table_stride=c.table.stride(0),
                 n_seqs=1, n_tokens=1, max_q=1, o=o)
     ft.ft_kv_attention(h, **good)
-    bad = [dict(layer=-1), dict(layer=2), dict(n_seqs=-1), dict(n_seqs=2), dict(n_tokens=-1), dict(table_stride=0),
-           dict(max_q=0), dict(max_q=65, tree_mask=c.start), dict(window=-1), dict(n_sink=-1), dict(sm_scale=float("nan")),
+    bad = [dict(layer=-1), dict(layer=2), dict(n_seqs=-1), dict(n_seqs=c.crowd + 2), dict(n_tokens=-1), dict(table_stride=0),
+           dict(max_q=0), dict(max_q=65, tree_mask=c.start), dict(max_q=(1 << 29) + 1), dict(window=-1), dict(n_sink=-1), dict(sm_scale=float("nan")),
            dict(sm_scale=float("inf")), dict(q=None, q_stride=128), dict(o=None, o_stride=128), dict(kv_len=None),
            dict(block_table=None), dict(q_start=None), dict(q_stride=120), dict(q_stride=132), dict(o_stride=64),
            dict(q=q.data_ptr() + 2, q_stride=128), dict(o=o.data_ptr() + 8, o_stride=128)]

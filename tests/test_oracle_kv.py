@@ -1,6 +1,8 @@
 """Pins for oracle.kv: the cache's formats, its tile layout, who sees whom, attention.
 Also the host-side refusals of the cache's C ABI (nothing here reaches a CUDA call)."""
 import ctypes
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -127,3 +129,23 @@ def test_create_and_calls_without_memory(ft):
             call()
         assert ei.value.status == ft.FT_ERR_ARG
     assert ctypes.sizeof(ft.FtKvDesc) == 56
+
+
+def test_binding_matches_the_header(ft, tmp_path):
+    """The layout that the binding packs is the C compiler's."""
+    fields = ["q", "o", "lse", "q_stride", "o_stride", "q_start", "kv_len", "block_table", "tree_mask", "layer",
+              "table_stride", "n_seqs", "n_tokens", "max_q", "window", "n_sink", "sm_scale"]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "ft.h"\nint main(void) {\n'
+                   '    printf("%zu %zu", sizeof(ft_kv_desc), sizeof(ft_kv_attn));\n' +
+                   "".join(f'    printf(" %zu", offsetof(ft_kv_attn, {f}));\n' for f in fields) + "    return 0;\n}\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run(["gcc", "-I", os.path.join(root, "include"), str(src), "-o", str(tmp_path / "layout")], check=True)
+    got = [int(x) for x in subprocess.run([str(tmp_path / "layout")], check=True, capture_output=True, text=True).stdout.split()]
+    at, want = 0, []
+    for size in [8] * 9 + [4] * 8:
+        want.append(at)
+        at += size
+    assert got == [ctypes.sizeof(ft.FtKvDesc), ft._KV_ATTN.size] + want
+    one = ft._KV_ATTN.unpack(ft._KV_ATTN.pack(*range(1, 17), 0.5))
+    assert one == (*range(1, 17), 0.5)
