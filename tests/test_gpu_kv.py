@@ -504,3 +504,26 @@ def test_long_tables(ft, fmt, D, G, page, window, n_sink):
         masks = [tree(rng, n) for n in (4, 3, 1)]
         Case(ft, fmt, D, 1, G, page, [4, 260, 90], [4, 3, 1], masks=masks, **kw).both(window=window, n_sink=n_sink)
     Case(ft, fmt, D, 1, G, page, [5000], [1], **kw).both(window=window, n_sink=n_sink)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "fp8"])
+def test_layers_together(ft, fmt):
+    """The example: a decoder over both caches, by single tokens and by chunks and trees.  The two ways differ by
+    attention's roundings (2^-8) and the order of the experts' sums; a rounding that flips in a stored key or
+    an expert's input moves it by a step of its format (up to 2^-3 of an element), one in a few dozen."""
+    import importlib.util
+    import os
+    spec = importlib.util.spec_from_file_location("tree_decode", os.path.join(os.path.dirname(os.path.dirname(
+        os.path.abspath(__file__))), "examples", "tree_decode.py"))
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    rng = np.random.default_rng(1)
+    prompt = rng.integers(0, ex.VOCAB, 45).tolist()
+    a, la = ex.plain(prompt, 60, fmt=fmt)
+    b, lb, steps = ex.by_trees(prompt, 60, a, rng, fmt=fmt)
+    same = next((i for i in range(60) if a[i] != b[i]), 60)
+    gap = la.topk(2).values
+    assert same == 60 or (gap[same, 0] - gap[same, 1]) < 2.0 ** -4 * la[same].abs().max(), "a token that is no tie"
+    # a right guess gives depth + 1 = 7 tokens a step, a wrong one still one
+    assert same >= 10 and steps <= -(-same // 7) + 60 - same + 1
+    assert ((la - lb)[:same].norm() / la[:same].norm()).item() < 2.0 ** -4
