@@ -8,7 +8,9 @@ namespace ft {
 // Softmax in base 2: a weight is exp2(t - m + kHeadroom) with t = s * scale * log2(e) and a
 // reference m that is raised (and everything rescaled) only when some t exceeds it by more than
 // kHeadroom.  Weights are then at most 2^(2 kHeadroom) = 2^14 and a weight 2^-20 times the
-// reference's is still a normal f16.
+// reference's is still a normal f16.  They are rounded to f16 because the products with V take f16: 2^-11 of a
+// weight at most, below the output's own bf16 rounding (2^-9); their sum is taken before that rounding, in
+// fp32.
 constexpr float kHeadroom = 7.f;
 constexpr float kNoRef = -1.7e38f;     // reference of a row that has seen no key: any finite t exceeds it
 
