@@ -48,7 +48,7 @@ struct AttnArgs {
     __nv_bfloat16* o;
     size_t o_stride;
     float* lse;
-    int split, row_tiles;        // rows kernel, direct: CTAs of a unit (a cluster), row tiles of a sequence at most
+    int split, row_tiles;        // direct: CTAs of a unit (a cluster), row tiles of a sequence at most
     JoinTask* tasks;      // workspace: what the joining kernel has to do
     float* parts;        // workspace: partial sums of the units that a share's end cuts
 };

@@ -45,8 +45,6 @@ template <int NT>
 using RowsLine = Line<kKvTile, 8 * NT, kWarps, 2 * kWarps, 8, 2, false>;
 constexpr int kWaitLimit = 1 << 24;
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
@@ -118,15 +116,6 @@ constexpr size_t rows_smem() {
 // CTAs per SM that the register allocation aims at.  Heads of 256 leave three of them too few registers: 16
 // sequences of 8192 with 2 heads, 4-bit, 31.6 us with three and 24.8 with two.
 constexpr int rows_ctas(int D, int NT) { return D == 256 ? 2 : D == 128 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : 3; }
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
-    uint32_t d;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(p)), "r"(rank));
-    return d;
-}
 
 // A unit's sums from the CTAs of its cluster (each has its own in x and ml): a slice of the
 // values per CTA.  A team of lanes takes four values: lane k of it the ranks k, k + team, ..., then a
@@ -717,70 +706,11 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
 
 namespace {
 
-void direct_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], unsigned grid, int split, size_t smem, cudaStream_t s) {
-    cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    attr[0] = {};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1] = {};
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = split;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 2 : 1;
-}
-
-// What of the rows kernel is resident at once, in CTAs: by shares, and direct by the log2 of a cluster's
-// CTAs (clusters lie within a part of the GPU, so the largest leave SMs out).  Looked up once per device.
-struct RowsRoom {
-    int grid, room[5];
-};
 template <int D, int kFormat, int NT>
-cudaError_t rows_room(RowsRoom& r) {
-    static std::atomic<int> known[kMaxDevices][6];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (!known[dev][0].load(std::memory_order_acquire)) {
-        auto kern = kv_rows_kernel<D, kFormat, NT, false>;
-        auto direct = kv_rows_kernel<D, kFormat, NT, true>;
-        constexpr size_t smem = rows_smem<D, kFormat, NT>();
-        int n = 0;
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(direct, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
-            (e = cudaFuncSetAttribute(direct, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess ||
-            (e = all_shared(kern)) != cudaSuccess || (e = all_shared(direct)) != cudaSuccess ||
-            (e = all_shared(kv_join_kernel<RowsLine<NT>, D>)) != cudaSuccess ||
-            (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem)) != cudaSuccess)
-            return e;
-        const int grid = min(sm_count() * min(n, kMaxPerSm), kMaxShares);
-        if (grid < 1) return cudaErrorInvalidConfiguration;
-        known[dev][1].store(grid, std::memory_order_relaxed);
-        for (int x = 1; x < 5; ++x) {
-            cudaLaunchConfig_t cfg;
-            cudaLaunchAttribute attr[2];
-            direct_config(cfg, attr, grid >> x << x, 1 << x, smem, nullptr);
-            cfg.attrs = attr + 1;
-            cfg.numAttrs = 1;
-            if ((e = cudaOccupancyMaxActiveClusters(&n, direct, &cfg)) != cudaSuccess) return e;
-            known[dev][1 + x].store(min(n << x, grid), std::memory_order_relaxed);
-        }
-        known[dev][0].store(1, std::memory_order_release);
-    }
-    r.grid = known[dev][1].load(std::memory_order_relaxed);
-    for (int x = 0; x < 5; ++x) r.room[x] = known[dev][1 + x].load(std::memory_order_relaxed);
-    return cudaSuccess;
-}
-
-// 16-token tiles of a unit at most, as far as the host knows.
-long long most_tiles(const AttnArgs& a) {
-    const long long tiles = ((long long)a.table_stride << a.kv.page_shift) / kKvTile;
-    return a.window > 0 ? min(tiles, ((long long)a.window + a.max_q + a.n_sink) / kKvTile + 4) : tiles;
+cudaError_t rows_room(Room& r) {
+    static RoomStore store;
+    return store.get(r, kv_rows_kernel<D, kFormat, NT, false>, kv_rows_kernel<D, kFormat, NT, true>, kv_join_kernel<RowsLine<NT>, D>,
+                     kThreads, rows_smem<D, kFormat, NT>(), kMaxPerSm, kMaxShares);
 }
 
 // Direct: a.split CTAs per unit.  It saves the scan of the lengths, the partial sums and the second kernel,
@@ -788,9 +718,9 @@ long long most_tiles(const AttnArgs& a) {
 // CTAs per SM (32 sequences of 1024 with 8 heads of 256: 23 us, 36 us by shares; of 300 to 1850, 29 tiles, with
 // heads of 128: 26 and 24 us), fewer where SMs stay idle, down to 12 (one sequence with 2 heads of 128: 4096
 // tokens, 4 tiles, 7.6 us and 10.0 us; 16384, 16 tiles, 15.0 and 13.2 us).
-bool plan_direct(AttnArgs& a, const RowsRoom& room, int rows) {
+bool plan_direct(AttnArgs& a, const Room& room, int rows) {
     a.row_tiles = (int)(((long long)a.max_q * a.G + rows - 1) / rows);
-    const long long units = (long long)a.n_seqs * a.kv.hkv * a.row_tiles, tiles = most_tiles(a);
+    const long long units = (long long)a.n_seqs * a.kv.hkv * a.row_tiles, tiles = most_blocks(a, kKvTile);
     int x = 0;
     while (x < 4 && units << (x + 1) <= room.room[x + 1] && tiles > kWarps << x) ++x;
     a.split = 1 << x;
@@ -800,14 +730,12 @@ bool plan_direct(AttnArgs& a, const RowsRoom& room, int rows) {
 
 template <int D, int kFormat, int NT>
 cudaError_t launch_direct(const AttnArgs& a, cudaStream_t s) {
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr[2];
-    direct_config(cfg, attr, (unsigned)(a.n_seqs * a.kv.hkv * a.row_tiles * a.split), a.split, rows_smem<D, kFormat, NT>(), s);
-    return cudaLaunchKernelEx(&cfg, kv_rows_kernel<D, kFormat, NT, true>, a);
+    DirectLaunch l(a, kThreads, rows_smem<D, kFormat, NT>(), s);
+    return cudaLaunchKernelEx(&l.cfg, kv_rows_kernel<D, kFormat, NT, true>, a);
 }
 
 template <int D, int kFormat, int NT>
-cudaError_t run_rows(AttnArgs a, const RowsRoom& room, cudaStream_t s) {
+cudaError_t run_rows(AttnArgs a, const Room& room, cudaStream_t s) {
     if (plan_direct(a, room, 8 * NT)) return launch_direct<D, kFormat, NT>(a, s);
     const cudaError_t e = launch_pdl(kv_rows_kernel<D, kFormat, NT, false>, dim3(room.grid), dim3(kThreads), rows_smem<D, kFormat, NT>(), s, a);
     if (e != cudaSuccess) return e;
@@ -824,14 +752,14 @@ cudaError_t run_rows(AttnArgs a, const RowsRoom& room, cudaStream_t s) {
 template <int D, int kFormat>
 cudaError_t run(AttnArgs a, cudaStream_t s) {
     const long long rows = (long long)a.max_q * a.G;
-    RowsRoom room;
+    Room room;
     cudaError_t e;
     if (rows <= 8) {
         if ((e = rows_room<D, kFormat, 1>(room)) != cudaSuccess) return e;
         return run_rows<D, kFormat, 1>(a, room, s);
     }
     const long long row_tiles = (rows + 15) / 16, most = (3LL << 20) / (D + 128);
-    const bool small = row_tiles <= most && row_tiles * a.n_seqs * a.kv.hkv <= most / most_tiles(a);
+    const bool small = row_tiles <= most && row_tiles * a.n_seqs * a.kv.hkv <= most / most_blocks(a, kKvTile);
     if (rows > 32 && !small) return launch_kv_tiles(a, D, kFormat, s);
     if ((e = rows_room<D, kFormat, 2>(room)) != cudaSuccess) return e;
     if (rows <= 32) return run_rows<D, kFormat, 2>(a, room, s);

@@ -1,9 +1,23 @@
 // What the attention kernels share: which keys a row tile needs, the rule of who sees whom,
 // and the numbers of the running softmax.
 #pragma once
+#include <atomic>
+
 #include "ft_kv.cuh"
 
 namespace ft {
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+    uint32_t d;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(p)), "r"(rank));
+    return d;
+}
+
 
 // Softmax in base 2: a weight is exp2(t - m + kHeadroom) with t = s * scale * log2(e) and a
 // reference m that is raised (and everything rescaled) only when some t exceeds it by more than
@@ -421,5 +435,78 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const AttnArgs a)
         join_slice<L, D>(a, mine, 0, 1, lane, 32, warp_slots[warp], sums + 32 * warp, [] { __syncwarp(); });
     }
 }
+
+// ---------------------------------------------------------------------------- launches
+
+// Blocks of `keys` keys that a unit has at most, as far as the host knows.
+inline long long most_blocks(const AttnArgs& a, int keys) {
+    const long long len = (long long)a.table_stride << a.kv.page_shift, n = (len + keys - 1) / keys;
+    return a.window > 0 ? min(n, ((long long)a.window + a.max_q + a.n_sink) / keys + 4) : n;
+}
+
+// The launch of a direct kernel: a cluster of a.split CTAs per unit.
+struct DirectLaunch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2] = {};
+    DirectLaunch(unsigned grid, int split, int threads, size_t smem, cudaStream_t s) {
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = split;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = split > 1 ? 2 : 1;
+    }
+    DirectLaunch(const AttnArgs& a, int threads, size_t smem, cudaStream_t s)
+        : DirectLaunch((unsigned)(a.n_seqs * a.kv.hkv * a.row_tiles * a.split), a.split, threads, smem, s) {}
+    DirectLaunch(const DirectLaunch&) = delete;
+};
+
+// CTAs that are resident at once: by shares, and direct by the log2 of a cluster's CTAs (clusters lie within a
+// part of the GPU, so the largest leave SMs out).
+struct Room {
+    int grid, room[5];
+};
+// Looked up, with the kernels' attributes set, once per device.  direct may be NULL.
+struct RoomStore {
+    std::atomic<int> known[kMaxDevices][6];
+    using Kernel = void (*)(AttnArgs);
+    cudaError_t get(Room& r, Kernel shares, Kernel direct, Kernel join, int threads, size_t smem, int per_sm, int most) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+        std::atomic<int>(&at)[6] = known[dev];
+        if (!at[0].load(std::memory_order_acquire)) {
+            int n = 0;
+            if ((e = cudaFuncSetAttribute(shares, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
+                (e = all_shared(shares)) != cudaSuccess || (e = all_shared(join)) != cudaSuccess ||
+                (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, shares, threads, smem)) != cudaSuccess)
+                return e;
+            const int grid = min(sm_count() * min(n, per_sm), most);
+            if (grid < 1) return cudaErrorInvalidConfiguration;
+            at[1].store(grid, std::memory_order_relaxed);
+            if (direct && ((e = cudaFuncSetAttribute(direct, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
+                           (e = cudaFuncSetAttribute(direct, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess ||
+                           (e = all_shared(direct)) != cudaSuccess))
+                return e;
+            for (int x = 1; direct && x < 5; ++x) {
+                DirectLaunch l((unsigned)(grid >> x << x), 1 << x, threads, smem, nullptr);
+                l.cfg.attrs = l.attr + 1;
+                l.cfg.numAttrs = 1;
+                if ((e = cudaOccupancyMaxActiveClusters(&n, direct, &l.cfg)) != cudaSuccess) return e;
+                at[1 + x].store(min(n << x, grid), std::memory_order_relaxed);
+            }
+            at[0].store(1, std::memory_order_release);
+        }
+        r.grid = at[1].load(std::memory_order_relaxed);
+        for (int x = 0; x < 5; ++x) r.room[x] = at[1 + x].load(std::memory_order_relaxed);
+        return cudaSuccess;
+    }
+};
 
 }  // namespace ft

@@ -56,16 +56,16 @@ constexpr float kLeast = 1.2e-38f;
 // A block's marks: the first or a later one of its unit, or none left; the unit has a second tile of
 // rows; the last of the unit's.
 constexpr unsigned kFirst = 0, kNext = 1, kEnd = 2, kKind = 3, kTwo = 4, kLast = 8;
-// a unit's start and end cost about 400 keys
+// at least 2 places of the line per CTA (4: 22.2 us instead of 19.7 for 512 rows over 4096 of 2 heads of 128); a unit's
+// start and end cost about 400 keys (a cost of 2 blocks: 74 us instead of 64 for 16 ragged trees)
 template <int D, bool kPair>
-using TilesLine = Line<keys(D), kPair ? 2 * kRows : kRows, 1, 4, D == 256 ? 6 : 3, 8, true>;
+using TilesLine = Line<keys(D), kPair ? 2 * kRows : kRows, 1, 2, D == 256 ? 6 : 3, 8, true>;
 
 constexpr int kBufs = 2;                                                 // blocks of K and of V in shared memory
 constexpr int region(int D) { return keys(D) * D * 2; }                  // bytes of one
 constexpr int q_region(int D) { return kRows * D * 2; }                  // of a tile of rows of Q
 constexpr size_t tiles_smem(int D, bool pair) { return (size_t)(pair ? 2 : 1) * q_region(D) + 2 * kBufs * region(D) + 1024; }
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void mbar_init(uint32_t b, int n) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(b), "r"(n));
 }
@@ -393,7 +393,9 @@ struct Run {
 // neither waits for the other: S and O of a tile have their own tensor memory (2 * 128 + 2 * D columns,
 // so D up to 128; a chunk of 2048 tokens: 267 us, 328 us by turns).  Otherwise units of 128 rows, the
 // warpgroups taking turns with the blocks.
-template <int D, int kFormat, bool kPair>
+// kDirect: few blocks per CTA.  A cluster of a.split CTAs takes one unit, its blocks in equal runs, and joins through
+// distributed shared memory: no line of shares, no workspace, no second kernel.
+template <int D, int kFormat, bool kPair, bool kDirect>
 __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(const AttnArgs a) {
     using L = TilesLine<D, kPair>;
     using Role = Roles<D, kPair>;
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
     constexpr uint32_t kColO = 256;                       // S and P: columns 0..127 and 128..255
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t sq = (smem_u32(smem_raw) + 1023) & ~1023u, sk = sq + (kPair ? 2 : 1) * kRegionQ, sv = sk + kBufs * kRegion;
-    __shared__ long long prefix[kMaxSeqs + 1], scratch[kThreads / 32];
+    __shared__ long long prefix[kDirect ? 1 : kMaxSeqs + 1], scratch[kThreads / 32];
     __shared__ __align__(8) uint64_t bars[30];
     __shared__ uint32_t tmem_base;
     __shared__ volatile int abort_flag;
@@ -417,6 +419,7 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
     __shared__ unsigned what[8];                          // the block's marks
     __shared__ int key0[8];                               // its first key
     __shared__ UnitInfo units[4];
+    __shared__ Unit own;                                  // direct: the cluster's unit
     __shared__ int drafted[4][kTreeMax];                  // places of the drafted tokens
     __shared__ float refs[2][kRows];                      // by block parity: the rows' references
     __shared__ float halves[2][2][kRows];                 // by unit parity and warpgroup: the rows' sums
@@ -459,35 +462,68 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
     }
     tc_before();
     pdl_wait_and_release();
-    line_prefix<L>(a, prefix, scratch);                   // ends with a CTA barrier
+    Shares shares(1, 1LL, 0LL);
+    long long c0 = 0, c1 = 0;
+    bool work;
+    const int cta = blockIdx.x;
+    if constexpr (kDirect) {
+        if (threadIdx.x == 0) {
+            const int id = cta / a.split;
+            Unit u;
+            u.h = id % a.kv.hkv;
+            u.r = id / a.kv.hkv % a.row_tiles;
+            u.s = id / a.kv.hkv / a.row_tiles;
+            u.si = seq_info(a, u.s);
+            if (u.si.bad) atomicOr(a.kv.status, FT_DEV_BAD_ID);
+            u.rt = row_tile<kKeys>(a, u.si, u.r, kUnit);
+            u.first = u.end = 0;
+            own = u;
+        }
+        __syncthreads();
+        work = (long long)own.r * kUnit < (long long)own.si.n * a.G;     // the whole cluster's, or none
+    } else {
+        line_prefix<L>(a, prefix, scratch);               // ends with a CTA barrier
+        const long long total = prefix[a.n_seqs];
+        shares = Shares(total, gridDim.x, L::kMin);
+        work = total > 0 && cta < shares.nc;
+        if (work) {
+            c0 = shares.cut(cta);
+            c1 = shares.cut(cta + 1);
+        }
+    }
     tc_after();
     const uint32_t tmem = tmem_base;
 
-    const long long total = prefix[a.n_seqs];
-    const Shares shares(total, gridDim.x, L::kMin);
-    const int cta = blockIdx.x;
-    const bool work = total > 0 && cta < shares.nc;
-    const long long c0 = work ? shares.cut(cta) : 0, c1 = work ? shares.cut(cta + 1) : 0;
-
     // The runs of the CTA in order; every role walks them by itself.
     long long pos = c0;
+    auto cut_of = [&](int rank) { return (int)((long long)own.rt.nt * rank / a.split); };    // direct: a CTA's first block
     auto next_run = [&](Run& r) {
-        while (pos < c1) {
-            Unit& u = r.u;
-            if (pos > c0 && u.h + 1 < a.kv.hkv) {         // the same rows, the next head
-                ++u.h;
-                u.end += u.end - u.first;
-                u.first = pos;
-            } else {
-                u = find_unit<L>(a, prefix, pos);
+        if constexpr (kDirect) {
+            if (!work || pos++ > 0) return false;
+            r.u = own;
+            r.v0 = cut_of(cta % a.split);
+            r.v1 = cut_of(cta % a.split + 1);
+            return r.v0 < r.v1;
+        } else {
+            while (pos < c1) {
+                Unit& u = r.u;
+                if (pos > c0 && u.h + 1 < a.kv.hkv) {     // the same rows, the next head
+                    ++u.h;
+                    u.end += u.end - u.first;
+                    u.first = pos;
+                } else {
+                    u = find_unit<L>(a, prefix, pos);
+                }
+                r.v0 = block_at<L>(u.first, u.rt.nt, pos);
+                r.v1 = block_at<L>(u.first, u.rt.nt, c1);
+                pos = u.end;
+                if (r.v0 < r.v1) return true;
             }
-            r.v0 = block_at<L>(u.first, u.rt.nt, pos);
-            r.v1 = block_at<L>(u.first, u.rt.nt, c1);
-            pos = u.end;
-            if (r.v0 < r.v1) return true;
+            return false;
         }
-        return false;
     };
+    // direct: the CTA's sums for the others, in the place of Q and the blocks (laid out like a piece in the workspace)
+    float* const sums = reinterpret_cast<float*>(smem_raw + (sq - smem_u32(smem_raw)));
 
     Run run;
     bool ok = true;
@@ -684,6 +720,8 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             float l = unpair(l2).x + unpair(l2).y;
             if constexpr (kPair) {
                 if (!mbar_wait(o_done(wg), o_blocks++ & 1, &abort_flag)) { ok = false; break; }
+                // the sums take the place of what the other tile's products read
+                if (kDirect && marks & kTwo && !mbar_wait(o_done(1 - wg), 0, &abort_flag)) { ok = false; break; }
             } else {
                 if (b != wg && !take_ref(it)) { ok = false; break; }
                 halves[un & 1][wg][row] = unpair(l2).x + unpair(l2).y;
@@ -698,7 +736,7 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             tc_after();
             const int i = div_g(a, grow);
             const bool on = i < si.n, done = u.slot < 0;
-            float* out = partial<D, kUnit>(a, max(u.slot, 0));
+            float* out = kDirect ? sums : partial<D, kUnit>(a, max(u.slot, 0));
             if (on && !done && (kPair || wg == 0)) reinterpret_cast<float2*>(out)[row] = make_float2(m, l);
 #pragma unroll 1
             for (int x = kPair ? 0 : wg * (D / 2); x < (kPair ? D : (wg + 1) * (D / 2)); x += 32) {
@@ -726,6 +764,46 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             tc_before();
             __syncwarp();
             if (!kPair && lane == 0) mbar_arrive(o_free);
+        }
+        if (kDirect && a.split > 1) {                     // a slice of the unit's values per CTA, the ranks in order
+            cluster_sync();
+            const int rank = cta % a.split, rows = work ? min(kUnit, own.si.n * a.G - own.r * kUnit) : 0, groups = rows * (D / 4);
+            const int ga = (int)((long long)groups * rank / a.split), gb = (int)((long long)groups * (rank + 1) / a.split);
+            for (int e = ga + threadIdx.x; e < gb; e += 8 * 32) {
+                const int r = e % rows, d = e / rows * 4;
+                float m1 = kNoRef, l1 = 0.f;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                constexpr int kBatch = 8;                 // ranks in flight
+                for (int k0 = 0; k0 < a.split; k0 += kBatch) {
+                    float2 ml[kBatch];
+                    float4 y[kBatch];
+                    float mm = m1;
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        ml[k] = make_float2(kNoRef, 0.f);
+                        y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (k0 + k < a.split && cut_of(k0 + k) < cut_of(k0 + k + 1)) {
+                            const uint32_t src = cluster_addr(sums, k0 + k);
+                            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(ml[k].x), "=f"(ml[k].y) : "r"(src + 8 * r));
+                            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(y[k].x), "=f"(y[k].y), "=f"(y[k].z), "=f"(y[k].w)
+                                         : "r"(src + 8 * kUnit + 16 * piece_at<L, D>(r, d)));
+                        }
+                        mm = fmaxf(mm, ml[k].x);
+                    }
+                    float f = ex2(m1 - mm);
+                    m1 = mm;
+                    l1 *= f;
+                    x.x *= f; x.y *= f; x.z *= f; x.w *= f;
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        f = ex2(ml[k].x - mm);
+                        l1 += ml[k].y * f;
+                        x.x += y[k].x * f; x.y += y[k].y * f; x.z += y[k].z * f; x.w += y[k].w * f;
+                    }
+                }
+                const int gr = own.r * kUnit + r, i = div_g(a, gr);
+                store_out<4>(a, (size_t)(own.si.q0 + i), own.h * a.G + gr - i * a.G, D, d, &x.x, m1, l1);
+            }
         }
     } else if (warp < kWarpMma) {
         // ------------------------------------------------------------------------ K (and Q), V
@@ -779,8 +857,8 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             // tile's rows of a lane under way together
             if (it > 0 && !mbar_wait(k_empty((it - 1) % kBufs), ((it - 1) / kBufs) & 1, &abort_flag)) { ok = false; break; }
             if (warp == kWarpK && lane == 0) {
-                const bool all = run.v0 == 0 && run.v1 == run.u.rt.nt;
-                units[un & 3] = UnitInfo{si.q0, si.n, si.len, run.u.r, run.u.h, run.u.rt.i1, all ? -1 : 2 * cta + (run.v0 > 0 ? 0 : 1), run.u.rt.empty};
+                const bool all = kDirect ? a.split == 1 : run.v0 == 0 && run.v1 == run.u.rt.nt;
+                units[un & 3] = UnitInfo{si.q0, si.n, si.len, run.u.r, run.u.h, run.u.rt.i1, all ? -1 : kDirect ? 0 : 2 * cta + (run.v0 > 0 ? 0 : 1), run.u.rt.empty};
             }
             if (a.tree && warp == kWarpK)
                 for (int j = lane; j < si.n; j += 32)
@@ -865,7 +943,7 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             __syncwarp();
             if (ok && lane == 0) mbar_arrive(k_full(it % kBufs));
         }
-        if (warp == kWarpK) {                             // the unit that the cut at the CTA's first place goes through
+        if (!kDirect && warp == kWarpK) {                 // the unit that the cut at the CTA's first place goes through
             if (work) run.u = find_unit<L>(a, prefix, c0);
             if (lane == 0) {
                 if (work && run.u.first < c0)
@@ -994,6 +1072,10 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
         }
     }
     if (!ok && lane == 0) atomicOr(a.kv.status, FT_DEV_TIMEOUT);
+    if (kDirect && a.split > 1) {
+        if (warp >= kWarpK) cluster_sync();
+        cluster_sync();                                   // the others may still read this CTA's sums
+    }
     tc_before();
     __syncthreads();
     tc_after();
@@ -1002,36 +1084,49 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
 
 namespace {
 
-// CTAs: one per SM (0 when the kernel cannot be set up; looked up once per device).
 template <int D, int kFormat, bool kPair>
-int tiles_grid() {
-    static std::atomic<int> grids[kMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-        cudaGetLastError();
-        return 0;
-    }
-    int v = grids[dev].load(std::memory_order_relaxed);
-    if (!v) {
-        auto kern = kv_tiles_kernel<D, kFormat, kPair>;
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tiles_smem(D, kPair)) != cudaSuccess ||
-            all_shared(kern) != cudaSuccess || all_shared(kv_join_kernel<TilesLine<D, kPair>, D>) != cudaSuccess) {
-            cudaGetLastError();
-            return 0;
-        }
-        v = min(sm_count(), kMaxShares / 4);          // two pieces of up to 256 rows each fit the workspace
-        grids[dev].store(v, std::memory_order_relaxed);
-    }
-    return v;
+cudaError_t tiles_room(Room& r) {
+    static RoomStore store;
+    void (*direct)(AttnArgs) = nullptr;
+    if constexpr (D <= 128) direct = kv_tiles_kernel<D, kFormat, kPair, true>;
+    return store.get(r, kv_tiles_kernel<D, kFormat, kPair, false>, direct, kv_join_kernel<TilesLine<D, kPair>, D>,
+                     Roles<D, kPair>::kThreads, tiles_smem(D, kPair), 1, kMaxShares / 4);   // two pieces of up to 256 rows each fit the workspace
+}
+
+// Direct: a.split CTAs per unit.  A CTA's start and end then come once, and there is no second kernel, but SMs
+// stay idle.  So it goes where a CTA gets at most three blocks more than an even share (320 rows over 4096 of 2
+// heads of 128, 4 blocks and 1: 17.7 us, 19.7 by shares; 256 rows over 16384 of one head, 8 and 1: 26 and 18 us), and
+// with a CTA per unit up to 8 blocks (3 prompts of 400 over 1000, 4 heads of 128, 4 query heads each: 28 us, 44
+// us by shares, whose CTAs have two or three units to start and end).  Not with heads of 256: a block takes
+// them longer (320 rows over 4096: 26 us, 23 by shares).
+template <int D, bool kPair>
+bool plan_direct(AttnArgs& a, const Room& room) {
+    constexpr int kUnit = TilesLine<D, kPair>::kR;
+    const long long rows = (long long)a.max_q * a.G, row_tiles = (rows + kUnit - 1) / kUnit;
+    if (row_tiles > room.grid) return false;
+    const long long units = row_tiles * a.n_seqs * a.kv.hkv, blocks = most_blocks(a, keys(D));
+    if (units > room.grid) return false;
+    int x = 0;
+    while (x < 4 && units << (x + 1) <= room.room[x + 1] && blocks > 1LL << x) ++x;
+    a.row_tiles = (int)row_tiles;
+    a.split = 1 << x;
+    const long long each = (blocks + a.split - 1) / a.split;
+    return each <= 8 && (x == 0 || each <= units * blocks / room.grid + 3);
 }
 
 template <int D, int kFormat, bool kPair>
-cudaError_t run_tiles(const AttnArgs& a, cudaStream_t s) {
-    const int grid = tiles_grid<D, kFormat, kPair>();
-    if (grid < 1) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = launch_pdl(kv_tiles_kernel<D, kFormat, kPair>, dim3(grid), dim3(Roles<D, kPair>::kThreads), tiles_smem(D, kPair), s, a);
+cudaError_t run_tiles(AttnArgs a, cudaStream_t s) {
+    Room room;
+    cudaError_t e = tiles_room<D, kFormat, kPair>(room);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv_join_kernel<TilesLine<D, kPair>, D>, dim3(grid * TilesLine<D, kPair>::kSplit), dim3(kJoinThreads), 0, s, a);
+    if constexpr (D <= 128)
+        if (plan_direct<D, kPair>(a, room)) {
+            DirectLaunch l(a, Roles<D, kPair>::kThreads, tiles_smem(D, kPair), s);
+            return cudaLaunchKernelEx(&l.cfg, kv_tiles_kernel<D, kFormat, kPair, true>, a);
+        }
+    e = launch_pdl(kv_tiles_kernel<D, kFormat, kPair, false>, dim3(room.grid), dim3(Roles<D, kPair>::kThreads), tiles_smem(D, kPair), s, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kv_join_kernel<TilesLine<D, kPair>, D>, dim3(room.grid * TilesLine<D, kPair>::kSplit), dim3(kJoinThreads), 0, s, a);
 }
 
 template <int D, int kFormat>
@@ -1041,9 +1136,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
         // heads of 128: 26.6 us, 22.5 us without) but share a block's unpacking (over 16384: 34 and 38 us; 1024
         // rows over 16384: 49 and 60 us).
         const long long rows = (long long)a.max_q * a.G;
-        long long blocks = ((long long)a.table_stride << a.kv.page_shift) / 128 + 1;
-        if (a.window > 0) blocks = min(blocks, ((long long)a.window + a.max_q + a.n_sink) / 128 + 3);
-        if (rows > kRows && (rows + kRows - 1) / kRows * blocks >= 5LL * sm_count() / a.kv.hkv / a.n_seqs + 1)
+        if (rows > kRows && (rows + kRows - 1) / kRows * most_blocks(a, 128) >= 5LL * sm_count() / a.kv.hkv / a.n_seqs + 1)
             return run_tiles<D, kFormat, true>(a, s);
     }
     return run_tiles<D, kFormat, false>(a, s);

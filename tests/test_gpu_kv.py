@@ -506,6 +506,22 @@ def test_long_tables(ft, fmt, D, G, page, window, n_sink):
     Case(ft, fmt, D, 1, G, page, [5000], [1], **kw).both(window=window, n_sink=n_sink)
 
 
+@pytest.mark.parametrize("fmt,D", [("nvfp4", 64), ("fp8", 64), ("nvfp4", 128), ("fp8", 128), ("nvfp4", 256)])
+@pytest.mark.parametrize("hkv,seqs,tokens", [(4, 1, 2100), (2, 6, 2100), (4, 12, 1000)])
+@pytest.mark.parametrize("kind,window,n_sink", [("causal", 0, 0), ("tree", 0, 0), ("tree", 900, 3)])
+def test_units_of_many_rows_over_short_tables(ft, fmt, D, hkv, seqs, tokens, kind, window, n_sink):
+    """Up to 512 rows a unit over tables of 1000 and 2100 tokens: a unit's blocks divided among a few CTAs or in one,
+    some of them without a block, sequences much shorter than the table, of no rows and of no tokens."""
+    rng = np.random.default_rng(D + seqs)
+    lens = [tokens - 40, 64, 0, 129, 700, 3, 64, 65, 500, 1, 0, 260][:seqs]
+    nq = [64, 5, 2, 64, 33, 3, 64, 17, 0, 1, 0, 50][:seqs]
+    masks = [tree(rng, n) for n in nq] if kind == "tree" else None
+    c = Case(ft, fmt, D, hkv, 8, 16, lens, nq, seed=hkv, masks=masks, spare=2)
+    o, z = c.run(window=window, n_sink=n_sink)
+    c.check(o, z, window=window, n_sink=n_sink, rows=[0, 1, 2, 4, 15, 16, 31, 32, 40, 49, 62, 63])
+    assert torch.isfinite(o.float()).all() and ft.ft_kv_status(c.kv.handle) == 0
+
+
 @pytest.mark.parametrize("fmt", ["nvfp4", "fp8"])
 def test_layers_together(ft, fmt):
     """The example: a decoder over both caches, by single tokens and by chunks and trees.  The two ways differ by
