@@ -43,13 +43,22 @@ constexpr int kMaxPerSm = 4;           // CTAs
 // weight: 116 us, with it 66 us)
 template <int NT>
 using RowsLine = Line<kKvTile, 8 * NT, kWarps, 2 * kWarps, 8, 2, false>;
-constexpr int kWaitLimit = 1 << 24;
 
+// Waits give up after about two seconds.
+constexpr long long kWaitClocks = 1LL << 32;
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+    if (mbar_try(bar, parity)) return true;
+    const long long from = clock64();
+    do {
+        if (mbar_try(bar, parity)) return true;
+    } while (clock64() - from < kWaitClocks);
+    return false;
 }
 
 // Four f16 pairs from 8 E2M1 codes (a 32-bit word); two from 4 E4M3 codes.
@@ -376,11 +385,9 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
         bool gave_up = false;
         for (int v = v0; v < vend; ++v) {
             const uint32_t bar = bar0 + 8 * cur;
-            bool ok = false;
-            for (int it = 0; it < kWaitLimit && !ok; ++it) ok = mbar_try(bar, parity >> cur & 1);
-            if (!__all_sync(0xffffffffu, ok)) {           // give up, once the copies in flight have had their time
+            if (!__all_sync(0xffffffffu, mbar_wait(bar, parity >> cur & 1))) {    // give up, once the copies in flight have had their time
                 for (int x = 0; x < kStages && x < vend - v; ++x, cur = cur + 1 == kStages ? 0 : cur + 1)
-                    for (int it = 0; it < kWaitLimit && !mbar_try(bar0 + 8 * cur, parity >> cur & 1); ++it) {}
+                    mbar_wait(bar0 + 8 * cur, parity >> cur & 1);
                 if (lane == 0) atomicOr(a.kv.status, FT_DEV_TIMEOUT);
                 gave_up = true;
                 break;

@@ -27,9 +27,9 @@
 // tensor memory.
 //
 // 2048 tokens x 32 heads of 128 over 8192 keys of 8 heads, causal, 4-bit: 243 us, 990 TFLOP/s, half of what a
-// large library product reaches; the tensor pipe is busy 45 % of the time.  A block's chain S - softmax - P - O
-// sets the pace: 4650 clocks for 256 rows x 128 keys, of which the products take 2070 and the softmax
-// warps' instructions about 3000 of each scheduler's slots.  A short call is bound by its way through the
+// large library product reaches; the tensor pipe is busy 45 % of the time.  A block's softmax
+// sets the pace (two passes over tensor memory, one row per thread): 4650 clocks for 256 rows x 128 keys, of which
+// the products take 2070; with blocks in halves, S one half ahead of the softmax, it took 281 us.  A short call is bound by its way through the
 // roles: 9 us from the launch to the first unit's last block, of which Q takes 3.5, and 5 to 8 us for the second
 // kernel.
 #include <atomic>
