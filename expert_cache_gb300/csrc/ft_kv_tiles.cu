@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             mbar_init(k_empty(b), 1);
             mbar_init(v_empty(b), 1);
             mbar_init(s_full(b), 1);
-            mbar_init(vp_full(b), kPair ? 4 : 4 + Role::kWide);
+            mbar_init(vp_full(b), kPair ? 4 : 8 + Role::kWide);
             mbar_init(v_full(b), Role::kWide);
             mbar_init(o_done(b), 1);
             for (int q = 0; q < 4; ++q) mbar_init(m_full(q, b), 1);
@@ -573,6 +573,12 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             tc_after();
             const unsigned marks = what[it & 7];
             if ((marks & kKind) == kEnd) break;
+            // The warpgroup whose turn it is not has seen the block too: S's barrier, of which a wait sees only the
+            // phase's parity, is not used again before (it would be after this block's O).
+            if (!kPair && b != wg) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(vp_full(b));
+            }
             if ((marks & kKind) == kFirst) {
                 u = units[un & 3];
                 si = SeqInfo{u.q0, u.n, u.len, false};
