@@ -23,8 +23,8 @@
 // bank groups of a swizzle row.
 // Units are laid on the line of shares like the rows kernel's (a unit's start and end cost about
 // three blocks), so causal and ragged chunks balance; cut units are joined by the second kernel.
-// Every wait is bounded: on expiry the CTA sets FT_DEV_TIMEOUT, leaves its loops and frees its
-// tensor memory.
+// Every wait is bounded: on expiry the CTA sets FT_DEV_TIMEOUT, leaves its loops, waits for the products under way and
+// frees its tensor memory.
 //
 // 2048 tokens x 32 heads of 128 over 8192 keys of 8 heads, causal, 4-bit: 243 us, 990 TFLOP/s, half of what a
 // large library product reaches; the tensor pipe is busy 45 % of the time.  A block's softmax
@@ -86,6 +86,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t b, uint32_t parity, volatile 
     done = __all_sync(0xffffffffu, done);
     if (!done) *abort_flag = 1;
     return done;
+}
+// The same for the last wait, which a role that gave up does not cut short: about two seconds by the clock.
+constexpr long long kDrainClocks = 1LL << 32;
+__device__ __forceinline__ bool mbar_drained(uint32_t b) {
+    const long long from = clock64();
+    uint32_t ok;
+    do {
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0, 2000;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(b) : "memory");
+    } while (!ok && clock64() - from < kDrainClocks);
+    return __all_sync(0xffffffffu, ok != 0);
 }
 // One lane of a whole warp.
 __device__ __forceinline__ bool elect() {
@@ -1072,10 +1083,10 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             }
             before = now;
         }
-        if (!ok) {                                        // what was issued still reads shared memory
-            if (lead) tc_commit(drain);
-            mbar_wait(drain, 0, &abort_flag);
-        }
+        // what was issued reads shared memory and writes tensor memory: before the CTA's end, whether a role gave up or not
+        if (lead) tc_commit(drain);
+        __syncwarp();
+        if (!mbar_drained(drain)) ok = false;
     }
     if (!ok && lane == 0) atomicOr(a.kv.status, FT_DEV_TIMEOUT);
     if (kDirect && a.split > 1) {

@@ -72,9 +72,11 @@ def roles(units, both_see=True):
     return [issue] + softmax, counts
 
 
-def explore(programs, counts):
-    """Every reachable end: 'done', or 'stuck' where a role waits for ever."""
-    names = sorted({op[1] for p in programs for op in p if len(op) > 1})
+def explore(programs, counts, expire=False, drain=None):
+    """Every reachable end: 'done', 'stuck' (a role waits for ever) and, where waits may expire (which sets the abort
+    flag and sends the role to its end), 'early' if tensor memory is freed while a product is under way.  drain: what the
+    issuing role's last wait does once the flag is set: 'leaves' or 'waits'."""
+    names = sorted({op[1] for p in programs for op in p if len(op) > 1}) + ["drain"]
     at = {b: i for i, b in enumerate(names)}
     need = [counts.get(b, 1) for b in names]
 
@@ -85,26 +87,52 @@ def explore(programs, counts):
         bars[at[b]] = (phases + 1, 0) if have == need[at[b]] else (phases, have)
         return tuple(bars)
 
-    start = (tuple(0 for _ in programs), (), tuple((0, 0) for _ in names))
+    # a role's place: index of its next op; len + 1: at its end (after the issuing role's drain)
+    start = (tuple(0 for _ in programs), (), tuple((0, 0) for _ in names), False)
     seen, todo, ends = {start}, [start], set()
     while todo:
-        pcs, pipe, bars = todo.pop()
+        pcs, pipe, bars, flag = todo.pop()
         out = []
-        if pipe:                                  # the tensor pipe: products ("") and commits in order
-            out.append((pcs, pipe[1:], arrive(bars, pipe[0]) if pipe[0] else bars))
+        if pipe:                                  # the tensor pipe: products and commits in order
+            out.append((pcs, pipe[1:], arrive(bars, pipe[0]) if pipe[0] else bars, flag))
         for r, prog in enumerate(programs):
-            if pcs[r] == len(prog):
+            pc = pcs[r]
+
+            def to(x, pipe=pipe, bars=bars, flag=flag):
+                out.append((pcs[:r] + (x,) + pcs[r + 1:], pipe, bars, flag))
+
+            if pc > len(prog):
                 continue
-            op, to = prog[pcs[r]], pcs[:r] + (pcs[r] + 1,) + pcs[r + 1:]
+            if pc == len(prog):
+                if r or drain is None:
+                    to(pc + 1)
+                elif bars[at["drain"]][0] or (drain == "leaves" and flag):
+                    to(pc + 1)
+                continue
+
+            def end():                            # the issuing role's drain is committed as it gets there
+                return pipe + ("drain",) if r == 0 and drain is not None else pipe
+
+            op = prog[pc]
+            over = pc + 1 == len(prog)
             if op[0] in ("wait", "maybe"):
-                if op[0] == "maybe" or (bars[at[op[1]]][0] & 1) != op[2]:
-                    out.append((to, pipe, bars))
+                if (bars[at[op[1]]][0] & 1) != op[2] or op[0] == "maybe":
+                    to(pc + 1, pipe=end() if over else pipe)
+                if expire and op[0] == "wait" and (bars[at[op[1]]][0] & 1) == op[2]:
+                    to(len(prog), pipe=end(), flag=True)
             elif op[0] == "arrive":
-                out.append((to, pipe, arrive(bars, op[1])))
+                to(pc + 1, bars=arrive(bars, op[1]))
             else:
-                out.append((to, pipe + ("" if op[0] == "product" else op[1],), bars))
-        if not out:
-            ends.add("done" if all(pc == len(p) for pc, p in zip(pcs, programs)) else "stuck")
+                x = "" if op[0] == "product" else op[1]
+                more = pipe + (x,)
+                to(pc + 1, pipe=more + ("drain",) if over and r == 0 and drain is not None else more)
+        if all(pc == len(p) + 1 for pc, p in zip(pcs, programs)):
+            if drain is not None and "" in pipe:
+                ends.add("early")
+            elif not pipe:
+                ends.add("done")
+        elif not out:
+            ends.add("stuck")
         for s in out:
             if s not in seen:
                 seen.add(s)
@@ -124,3 +152,12 @@ def test_a_block_that_one_warpgroup_has_not_seen_is_what_would_get_stuck():
     """Were the products to wait for the block's own warpgroup alone, a late warp of the other one could find S's barrier
     two phases on, which by its parity looks like none."""
     assert "stuck" in explore(*roles([4], both_see=False))
+
+
+def test_tensor_memory_outlives_the_products():
+    """A role gives up at any wait: the issuing role's last wait is for its own products, whether or not the flag is
+    set.  (Left at the flag, memory is freed under them: the check tells the two apart.)"""
+    programs, counts = roles([2, 1])
+    assert "early" in explore(programs, counts, expire=True, drain="leaves")
+    for units in UNITS:
+        assert explore(*roles(units), expire=True, drain="waits") == {"done"}
