@@ -111,18 +111,22 @@ __device__ __forceinline__ int div_g(const AttnArgs& a, int x) {
 
 // Rows and cached length of sequence s, bounded as the interface says.
 struct SeqInfo {
-    int q0, n, len;      // first row, rows, cached tokens
+    int q0, n, len;      // first row, rows that are computed, cached tokens that the table has pages for
+    int base;            // kv_len - (q_start[s + 1] - q_start[s]): the first new token's place, whatever n and len were cut to
     bool bad;
 };
 __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int s) {
     SeqInfo r;
     const int a0 = a.q_start[s], a1 = a.q_start[s + 1], len = a.kv_len[s];
-    r.q0 = min(max(a0, 0), a.n_tokens);
-    const int q1 = min(max(a1, r.q0), a.n_tokens);
-    r.n = min(q1 - r.q0, a.max_q);
-    const long long most = min((long long)a.table_stride << a.kv.page_shift, 0x7FFFFC00LL);   // block ends fit 32 bits
+    const bool in = a0 >= 0 && a0 <= a.n_tokens && a1 >= a0;                                  // otherwise no rows
+    r.q0 = in ? a0 : 0;
+    const int all = in ? a1 - a0 : 0;
+    r.n = min(min(all, a.n_tokens - r.q0), a.max_q);
+    constexpr int kMost = 0x7FFFFC00;                                                         // block ends fit 32 bits
+    const long long most = min((long long)a.table_stride << a.kv.page_shift, (long long)kMost);
     r.len = (int)min((long long)max(len, 0), most);
-    r.bad = r.q0 != a0 || q1 != a1 || r.n != q1 - r.q0 || r.len != len;
+    r.base = min(max(len, 0), kMost) - all;
+    r.bad = !in || r.n != all || r.len != len;
     return r;
 }
 

@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
             if (whole) break;
             continue;
         }
-        const int base = u.si.len - u.si.n, row0 = u.r * R;
+        const int base = u.si.base, row0 = u.r * R;
 
         // ---------------------------------------------------------------- the rows' loads, the first copies
         uint4 raw[NT][D / 32];

@@ -49,12 +49,12 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs& a, const SeqInfo& s,
     RowTile t;
     t.i0 = div_g(a, r * R);
     t.i1 = min(s.n - 1, div_g(a, r * R + R - 1));
-    const int base = s.len - s.n;
+    const int base = s.base;
     const int hi = a.tree ? s.len : min(s.len, base + t.i1 + 1);
     // a drafted token stands at base or after it
     const long long low = a.window > 0 ? (long long)base + (a.tree ? 0 : t.i0) - a.window + 1 : 0;
     const int lo = (int)max(low, 0LL);
-    t.empty = hi <= 0;
+    t.empty = hi <= 0 || (lo >= hi && a.n_sink == 0);     // nothing cached, or the window stands past the table
     t.a_end = 0;
     t.b0 = 0;
     t.nt = 1;
@@ -76,7 +76,7 @@ __device__ __forceinline__ RowRule row_rule(const AttnArgs& a, const SeqInfo& s,
     RowRule r{-1, 0, 0};
     const int i = div_g(a, row);
     if (i >= s.n) return r;            // padding
-    const int base = s.len - s.n;
+    const int base = s.base;
     int pos = base + i;
     r.lim = min(pos, s.len - 1);
     if (a.tree) {
@@ -91,14 +91,14 @@ __device__ __forceinline__ RowRule row_rule(const AttnArgs& a, const SeqInfo& s,
 __device__ __forceinline__ bool sees(const AttnArgs& a, const RowRule& r, int j) {
     return j <= r.lim && (j >= r.low || j < a.n_sink);
 }
-// Place of a drafted key under a tree.
+// Place of the drafted key j >= base under a tree (no mask has the 64th or a later one; of one past the rows no mask is known).
 __device__ __forceinline__ int drafted_pos(const AttnArgs& a, const SeqInfo& s, int j) {
-    const int jj = j - (s.len - s.n);
-    return s.len - s.n + __popcll(a.tree[s.q0 + jj] & ~(1ull << jj));
+    const int jj = j - s.base;
+    return s.base + (jj < min(kTreeMax, a.n_tokens - s.q0) ? __popcll(a.tree[s.q0 + jj] & ~(1ull << jj)) : 0);
 }
 // The rule for a drafted key j >= base, base <= j < len, that stands at place pos.
 __device__ __forceinline__ bool sees_drafted(const AttnArgs& a, const RowRule& r, int base, int j, int pos) {
-    return (r.mask >> (j - base) & 1) && (pos >= r.low || j < a.n_sink);
+    return j - base < kTreeMax && (r.mask >> (j - base) & 1) && (pos >= r.low || j < a.n_sink);
 }
 
 // Powers of two that take a row's largest magnitude to [2^13, 2^14) and back: exact in f16 down to

@@ -388,7 +388,7 @@ __device__ __forceinline__ void zero_past(Raw<D, kFormat>& r, int n, int t) {
 
 // What the softmax warps need to know of a unit.
 struct UnitInfo {
-    int q0, n, len, r, h, i1, slot;      // slot of its partial sums, -1 when the CTA has the whole unit
+    int q0, n, len, base, r, h, i1, slot;    // slot of its partial sums, -1 when the CTA has the whole unit
     bool empty;
 };
 
@@ -592,12 +592,12 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             }
             if ((marks & kKind) == kFirst) {
                 u = units[un & 3];
-                si = SeqInfo{u.q0, u.n, u.len, false};
-                base = si.len - si.n;
+                si = SeqInfo{u.q0, u.n, u.len, u.base, false};
+                base = si.base;
                 grow = u.r * kUnit + row;
                 rule = row_rule(a, si, grow);
                 // keys below all_lim and from all_low on are seen by every row of the tile
-                all_lim = a.tree ? base - 1 : row_rule(a, si, u.r * kUnit + row0).lim;
+                all_lim = a.tree ? min(base, si.len) - 1 : row_rule(a, si, u.r * kUnit + row0).lim;
                 const int last = kPair ? min(si.n - 1, div_g(a, u.r * kUnit + row0 + kRows - 1)) : u.i1;
                 all_low = a.window > 0 ? (int)max((long long)(a.tree ? base + si.n : base + last) - a.window + 1, 0LL) : 0;
                 m = kNoRef;
@@ -830,7 +830,7 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
         unsigned it = 0;
         for (int un = 0; ok && next_run(run); ++un) {
             const SeqInfo& si = run.u.si;
-            const int base = si.len - si.n;
+            const int base = si.base;
             const int32_t* table = a.table + (size_t)run.u.s * a.table_stride;
             // keys that some row sees: below hi, from lo on or among the first tokens
             const int hi = run.u.rt.empty ? 0 : a.tree ? si.len : min(si.len, base + run.u.rt.i1 + 1);
@@ -875,11 +875,11 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
             if (it > 0 && !mbar_wait(k_empty((it - 1) % kBufs), ((it - 1) / kBufs) & 1, &abort_flag)) { ok = false; break; }
             if (warp == kWarpK && lane == 0) {
                 const bool all = kDirect ? a.split == 1 : run.v0 == 0 && run.v1 == run.u.rt.nt;
-                units[un & 3] = UnitInfo{si.q0, si.n, si.len, run.u.r, run.u.h, run.u.rt.i1, all ? -1 : kDirect ? 0 : 2 * cta + (run.v0 > 0 ? 0 : 1), run.u.rt.empty};
+                units[un & 3] = UnitInfo{si.q0, si.n, si.len, si.base, run.u.r, run.u.h, run.u.rt.i1, all ? -1 : kDirect ? 0 : 2 * cta + (run.v0 > 0 ? 0 : 1), run.u.rt.empty};
             }
             if (a.tree && warp == kWarpK)
-                for (int j = lane; j < si.n; j += 32)
-                    drafted[un & 3][j] = base + __popcll(a.tree[si.q0 + j] & ~(1ull << j));
+                for (int j = lane; j < min(si.len - base, kTreeMax); j += 32)
+                    drafted[un & 3][j] = drafted_pos(a, si, base + j);
             const int row_tiles = kPair && (long long)run.u.r * kUnit + kRows < (long long)si.n * a.G ? 2 : 1;
             constexpr int kLane = kRows / (8 * Role::kWide);      // rows of a lane
 #pragma unroll 1

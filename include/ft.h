@@ -481,9 +481,11 @@ ft_status ft_kv_read(ft_kv* kv, int32_t layer, const int32_t* slots, int32_t n, 
  * Rows of q and o are 16-byte aligned.  Rows outside every sequence are left as they are.
  * Asynchronous on stream, capturable, no allocation; calls of one handle share its
  * workspace, so they run one after another (one stream, or ordered by events).
- * What the host cannot see is bounded on the device: q_start outside its range, more than
- * max_q rows (the rest are left as they are), kv_len outside [0, table_stride * page_size]
- * and pages outside [0, n_pages) (their keys are not seen) set FT_DEV_BAD_ID.
+ * What the host cannot see is bounded on the device and sets FT_DEV_BAD_ID.  More than max_q
+ * rows, or rows past n_tokens: the rest are left as they are.  A q_start[s] outside [0, n_tokens]
+ * or above q_start[s+1]: the sequence has no rows.  kv_len outside [0, table_stride * page_size]
+ * and pages outside [0, n_pages): the keys that have no page are not seen.  The rows that are
+ * computed see what the rule above says of the n and kv_len given.
  * Errors (nothing launched): FT_ERR_ARG for layer, n_seqs outside [0, max_seqs], n_tokens
  * < 0, table_stride < 1, max_q < 1 (or > 64 with tree_mask, or more than 2^30 rows with a
  * group's query heads), window < 0, n_sink < 0, a sm_scale that is not finite, NULL or

@@ -1,0 +1,67 @@
+"""Who sees whom at the edges: rows and lengths past what the call says.  Against oracle.kv, with test_gpu_kv's derived bounds."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv as K
+from test_gpu_kv import Case, crowd, ft, tree  # noqa: F401  (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [("nvfp4", 64, 4), ("fp8", 64, 5), ("nvfp4", 128, 4), ("fp8", 128, 8), ("nvfp4", 256, 8), ("fp8", 256, 3)]
+
+
+def check_rows(c, o, s, rows, vis):
+    """Rows of sequence s against the oracle; vis [rows, keys] may end before or after the cached tokens."""
+    n = min(vis.shape[1], c.lens[s])
+    at = int(c.start_np[s]) + rows
+    q = c.q.double().numpy()[at]
+    for h in range(c.hkv * c.G):
+        k, v = c.kval[s][:n, h // c.G], c.vval[s][:n, h // c.G]
+        ro, _, av, mag = K.attention(q[:, h], k, v, vis[:, :n], c.scale)
+        e = (c.scale * (c.D + 16) * 2.0 ** -23 * mag)[:, None]
+        got = o[at, h].double().cpu().numpy()
+        assert np.all(np.abs(got - ro) <= 2.0 ** -8 * np.abs(ro) + (2 * e + 2.0 ** -10) * av + n * 2.0 ** -24 * np.abs(v).max())
+
+
+# ------------------------------------------------------------------------------ rows and lengths past the call's
+
+@pytest.mark.parametrize("fmt,D,G", SHAPES)
+@pytest.mark.parametrize("kind,window,n_sink", [("causal", 0, 0), ("causal", 40, 3), ("tree", 0, 0), ("tree", 90, 2)])
+def test_the_rows_up_to_max_q_see_what_they_should(ft, fmt, D, G, kind, window, n_sink):
+    rng = np.random.default_rng(D)
+    for nq, most in (([9, 3], 5), ([50, 64], 33), ([100, 7], 64)):
+        masks = None
+        if kind == "tree":                                   # rows past the 64th are never computed
+            masks = [tree(rng, min(n, 64)) + [0] * max(n - 64, 0) for n in nq]
+        c = Case(ft, fmt, D, 2, G, 32, [170, 90], nq, seed=G, masks=masks)
+        o, z = c.run(window=window, n_sink=n_sink, max_q=most)
+        c.check(o, z, window=window, n_sink=n_sink, rows=range(most))
+        assert ft.ft_kv_status(c.kv.handle) == ft.FT_DEV_BAD_ID
+        for s, n in enumerate(nq):
+            rest = slice(c.start_np[s] + most, c.start_np[s] + max(n, most))
+            assert torch.isnan(o[rest].float()).all() and torch.isnan(z[rest]).all()
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_a_length_past_the_table_keeps_the_rows_places(ft, nq):
+    c = Case(ft, "fp8", 128, 1, 4, 16, [96, 64], [nq, nq], seed=1, spare=0)
+    c.len_dev[0] = 96 + 37                                   # 37 keys have no page
+    for window, n_sink in ((0, 0), (60, 0), (10, 0), (10, 3), (10, 20)):
+        o, _ = c.run(window=window, n_sink=n_sink)
+        assert ft.ft_kv_status(c.kv.handle) == ft.FT_DEV_BAD_ID
+        check_rows(c, o, 0, np.arange(nq), K.seen(nq, 96 + 37, window, n_sink))
+
+
+def test_a_sequence_that_ends_past_the_rows(ft):
+    """q_start[s + 1] above n_tokens: the rows that there are have their places; a start outside: no rows."""
+    c = Case(ft, "nvfp4", 64, 1, 4, 16, [100, 80], [3, 20], seed=2)
+    c.start[2] = 3 + 30                                      # 30 new tokens, 20 of them in the tensors
+    o, z = c.run(max_q=30)
+    assert ft.ft_kv_status(c.kv.handle) == ft.FT_DEV_BAD_ID
+    check_rows(c, o, 1, np.arange(20), K.seen(30, 80)[:20])
+    c.start[2] = 23
+    c.start[0] = -5
+    o, z = c.run()
+    assert ft.ft_kv_status(c.kv.handle) == ft.FT_DEV_BAD_ID
+    assert torch.isnan(o[:3].float()).all() and torch.isfinite(o[3:].float()).all()
