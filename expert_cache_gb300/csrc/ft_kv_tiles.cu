@@ -596,10 +596,11 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
                 base = si.base;
                 grow = u.r * kUnit + row;
                 rule = row_rule(a, si, grow);
-                // keys below all_lim and from all_low on are seen by every row of the tile
+                // keys below all_lim and from all_low on are seen by every row of the tile (under a tree a row may stand
+                // as far past base as its mask has other bits, whichever they are)
                 all_lim = a.tree ? min(base, si.len) - 1 : row_rule(a, si, u.r * kUnit + row0).lim;
                 const int last = kPair ? min(si.n - 1, div_g(a, u.r * kUnit + row0 + kRows - 1)) : u.i1;
-                all_low = a.window > 0 ? (int)max((long long)(a.tree ? base + si.n : base + last) - a.window + 1, 0LL) : 0;
+                all_low = a.window > 0 ? (int)max((long long)base + (a.tree ? kTreeMax - 1 : last) - a.window + 1, 0LL) : 0;
                 m = kNoRef;
                 c = coef[un & 3][row];
                 l2 = pair(0.f, 0.f);

@@ -1,4 +1,5 @@
-"""Who sees whom at the edges: rows and lengths past what the call says.  Against oracle.kv, with test_gpu_kv's derived bounds."""
+"""Who sees whom at the edges: rows and lengths past what the call says, masks with bits past the drafted tokens.
+Against oracle.kv, with test_gpu_kv's derived bounds."""
 import numpy as np
 import pytest
 import torch
@@ -65,3 +66,21 @@ def test_a_sequence_that_ends_past_the_rows(ft):
     o, z = c.run()
     assert ft.ft_kv_status(c.kv.handle) == ft.FT_DEV_BAD_ID
     assert torch.isnan(o[:3].float()).all() and torch.isfinite(o[3:].float()).all()
+
+
+# ------------------------------------------------------------------------------ bits past the drafted tokens
+
+@pytest.mark.parametrize("fmt,D,G", SHAPES)
+@pytest.mark.parametrize("n,length,window", [(40, 1524, 512), (12, 700, 300), (64, 1000, 256)])
+def test_stray_bits_move_the_window_of_their_row_alone(ft, fmt, D, G, n, length, window):
+    """A row stands at base + the number of its mask's other bits, whichever they are."""
+    rng = np.random.default_rng(n)
+    masks = tree(rng, n)
+    for i in (0, 5, n - 1):
+        masks[i] |= ((1 << 64) - 1) ^ ((1 << n) - 1)
+    masks[7] = (1 << 64) - 1
+    c = Case(ft, fmt, D, 1, G, 64, [length, 50], [n, 3], seed=n, masks=[masks, tree(rng, 3)])
+    for n_sink in (0, 5):
+        o, z = c.run(window=window, n_sink=n_sink)
+        c.check(o, z, window=window, n_sink=n_sink, rows=[0, 1, 2, 5, 6, 7, 8, n - 2, n - 1])
+    assert ft.ft_kv_status(c.kv.handle) == 0
