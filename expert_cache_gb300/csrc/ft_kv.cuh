@@ -103,6 +103,12 @@ __device__ __forceinline__ int kv_v_scale_byte(int r, int b) {
     return kv_tile(D, FT_KV_NVFP4).v_scales + (b * 4 + ((r & 7) >> 1)) * 4 + 2 * (r >> 3) + (r & 1);
 }
 
+// Four E4M3 bytes with the NaNs among them as zeros.
+__device__ __forceinline__ uint32_t e4m3_numbers(uint32_t w) {
+    const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    return w & ~((nan << 1) - (nan >> 7));
+}
+
 // x / G for 0 <= x < 2^31 (division by an invariant integer through a multiplication, Granlund and
 // Montgomery 1994): shift = ceil(log2 G), mul = floor(2^32 (2^shift - G) / G) + 1.
 __device__ __forceinline__ int div_g(const AttnArgs& a, int x) {

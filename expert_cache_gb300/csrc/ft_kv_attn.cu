@@ -522,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
             }
 
             // O^T += V^T P^T.  The lane holds tokens 2t, 2t+1, 2t+8, 2t+9 and dims g D/8 ..
-            // Past the cached tokens (and in a tile that is not there) the bytes may be anything: zeroed.
-            const bool tail = !have || j0 + 16 > u.si.len;
+            // A key that a row does not see has weight 0, but its slot may never have been written (or its tile be a
+            // stale one), and a NaN among its bytes times 0 would be a NaN: there they count as 0.
             if constexpr (kFour) {
                 uint32_t vw[D / 16];                      // [token 4][D/64 words]
                 if constexpr (D == 64) {
@@ -542,11 +542,7 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                 for (int b = 0; b < kBlocks; ++b) {
                     const int blk = D == 64 ? g >> 1 : D == 128 ? g : 2 * g + b;
                     uint32_t sw = *reinterpret_cast<const uint32_t*>(tile + kT.v_scales + (blk * 4 + t) * 4);
-                    if (tail) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (!have || j0 + 2 * t + (q & 1) + 8 * (q >> 1) >= u.si.len) sw &= ~(255u << (8 * q));
-                    }
+                    if (edge) sw = e4m3_numbers(sw);
                     uint32_t s2[4];
                     {
                         uint32_t p01, p23;
@@ -579,13 +575,9 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                     const uint4 w = *reinterpret_cast<const uint4*>(tile + kT.code_bytes + x * 512 + lane * 16);
                     vw[4 * x] = w.x; vw[4 * x + 1] = w.y; vw[4 * x + 2] = w.z; vw[4 * x + 3] = w.w;
                 }
-                if (tail) {
+                if (edge) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        if (!have || j0 + 2 * t + (q & 1) + 8 * (q >> 1) >= u.si.len) {
-#pragma unroll
-                            for (int x = 0; x < D / 32; ++x) vw[q * (D / 32) + x] = 0;
-                        }
+                    for (int x = 0; x < D / 8; ++x) vw[x] = e4m3_numbers(vw[x]);
                 }
 #pragma unroll
                 for (int x = 0; x < D / 32; ++x) {

@@ -1,5 +1,5 @@
-"""Who sees whom at the edges: rows and lengths past what the call says, masks with bits past the drafted tokens.
-Against oracle.kv, with test_gpu_kv's derived bounds."""
+"""Who sees whom at the edges: keys that no row sees and what their slots hold, masks with bits past the drafted
+tokens, rows and lengths past what the call says.  Against oracle.kv, with test_gpu_kv's derived bounds."""
 import numpy as np
 import pytest
 import torch
@@ -10,6 +10,19 @@ from test_gpu_kv import Case, crowd, ft, tree  # noqa: F401  (fixtures)
 pytestmark = pytest.mark.gpu
 
 SHAPES = [("nvfp4", 64, 4), ("fp8", 64, 5), ("nvfp4", 128, 4), ("fp8", 128, 8), ("nvfp4", 256, 8), ("fp8", 256, 3)]
+
+
+def forget(c, s, js):
+    """The bytes of sequence s's tokens js back to 0xFF, as if they had never been written."""
+    pool = c.kv.pool.view(c.kv.desc.L, -1)[c.layer].view(-1, c.hkv, c.page // 16, K.tile_bytes(c.D, c.fmt))
+    d = np.arange(c.D)
+    for j in js:
+        at = pool[int(c.table_np[s, j // c.page]), :, j % c.page // 16]
+        for value in (False, True):
+            where = np.unique(K.code_place(j % 16, d, c.D, c.fmt, value)[0])
+            if c.fmt == "nvfp4":
+                where = np.concatenate([where, [K.scale_place(j % 16, b, c.D, value) for b in range(c.D // 16)]])
+            at[:, torch.from_numpy(where).cuda()] = 255
 
 
 def check_rows(c, o, s, rows, vis):
@@ -84,3 +97,55 @@ def test_stray_bits_move_the_window_of_their_row_alone(ft, fmt, D, G, n, length,
         o, z = c.run(window=window, n_sink=n_sink)
         c.check(o, z, window=window, n_sink=n_sink, rows=[0, 1, 2, 5, 6, 7, 8, n - 2, n - 1])
     assert ft.ft_kv_status(c.kv.handle) == 0
+
+
+# ------------------------------------------------------------------------------ keys that no row sees
+
+@pytest.mark.parametrize("fmt,D,G", SHAPES)
+@pytest.mark.parametrize("n", [1, 6, 40])
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (50, 0), (50, 3), (130, 20)])
+def test_keys_that_the_window_has_left_may_never_have_been_written(ft, fmt, D, G, n, window, n_sink):
+    """A sequence whose cache was filled from its last tokens (and the first ones that stay): bytes of 0xFF before."""
+    lens = [300, n + 11, 190]
+    c = Case(ft, fmt, D, 2, G, 32, lens, [n] * 3, seed=n)
+    for s, length in enumerate(lens):
+        forget(c, s, np.flatnonzero(~K.seen(n, length, window, n_sink).any(0)))
+    c.both(window=window, n_sink=n_sink)
+
+
+@pytest.mark.parametrize("fmt,D,G", SHAPES)
+@pytest.mark.parametrize("pad,window,n_sink", [("nothing", 0, 0), ("itself", 0, 0), ("nothing", 60, 2), ("itself", 2, 0)])
+def test_trees_padded_to_a_fixed_size(ft, fmt, D, G, pad, window, n_sink):
+    """Padding tokens have no slot, so their keys were never written; no other row has them in its mask.  A padding row
+    that has itself there gets what its bytes give, and nobody else does."""
+    rng = np.random.default_rng(3)
+    real, nq, lens, masks = [5, 1, 40, 17], [8, 8, 64, 17], [40, 8, 164, 64], []
+    for n, r in zip(nq, real):
+        masks.append(tree(rng, r) + [1 << j if pad == "itself" else 0 for j in range(r, n)])
+    c = Case(ft, fmt, D, 2, G, 16, lens, nq, seed=4, masks=masks)
+    for s, (n, r, length) in enumerate(zip(nq, real, lens)):
+        forget(c, s, range(length - n + r, length))
+        if window:
+            forget(c, s, np.flatnonzero(~K.seen(n, length, window, n_sink, masks[s]).any(0)))
+    o, z = c.run(window=window, n_sink=n_sink)
+    c.check(o, z, window=window, n_sink=n_sink, rows=None if pad == "nothing" else [0])
+    if pad == "itself":
+        keep = np.concatenate([np.arange(n) < r for n, r in zip(nq, real)])
+        assert torch.isfinite(o.float()[torch.from_numpy(keep).cuda()]).all()
+        for s, r in enumerate(real):
+            check_rows(c, o, s, np.arange(r), K.seen(nq[s], lens[s], window, n_sink, masks[s])[:r])
+
+
+@pytest.mark.parametrize("fmt,D,G", SHAPES)
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (30, 2)])
+def test_prompts_padded_to_a_fixed_size(ft, fmt, D, G, window, n_sink):
+    """Causal rows behind the prompt's end have no slot: they see keys that were never written, the prompt's rows do
+    not, though they share blocks and products."""
+    real, nq, lens = [5, 1, 40, 90], [8, 8, 64, 96], [40, 8, 164, 96]
+    c = Case(ft, fmt, D, 2, G, 16, lens, nq, seed=4)
+    for s, (n, r, length) in enumerate(zip(nq, real, lens)):
+        forget(c, s, range(length - n + r, length))
+    o, _ = c.run(window=window, n_sink=n_sink)
+    torch.cuda.synchronize()
+    for s, r in enumerate(real):
+        check_rows(c, o, s, np.arange(r), K.seen(nq[s], lens[s], window, n_sink)[:r])
