@@ -286,7 +286,9 @@ __global__ void __launch_bounds__(kThreads, rows_ctas(D, NT)) kv_rows_kernel(con
                 if (mine < v1) {
                     page = table[u.rt.block(mine) >> per];
                     if (page < 0 || page >= a.kv.n_pages) {
-                        atomicOr(a.kv.status, FT_DEV_BAD_ID);
+                        if (!a.tree || tree_sees_tile(a.tree + u.si.q0, u.rt.i0, u.rt.i1 + 1 - u.rt.i0, a.n_tokens - u.si.q0, base, u.si.len,
+                                                      u.rt.block(mine) * kKvTile, a.window, a.n_sink))
+                            atomicOr(a.kv.status, FT_DEV_BAD_ID);
                         page = -1;
                     }
                 }

@@ -101,6 +101,23 @@ __device__ __forceinline__ bool sees_drafted(const AttnArgs& a, const RowRule& r
     return j - base < kTreeMax && (r.mask >> (j - base) & 1) && (pos >= r.low || j < a.n_sink);
 }
 
+// Under a tree: whether one of the rows whose masks are m[0..n) (the sequence's tokens from i0 on) sees one of the keys j0 to
+// j0 + 15 below len.  Asked only where the table has no page for them, so that one which no row needs is no error; out of line,
+// since its instructions among the kernels' cost more (windowed chunk 123 us instead of 116) than it ever takes.
+static __device__ __noinline__ bool tree_sees_tile(const unsigned long long* m, int i0, int n, int left, int base, int len, int j0, int window,
+                                                   int n_sink) {
+    const int old = min(min(j0 + kKvTile, base), len) - 1;                     // the last key of the context among them
+    const int d0 = max(j0, base) - base, d1 = min(min(j0 + kKvTile, len) - base, kTreeMax);
+    auto place = [&](unsigned long long mask, int i) { return __popcll(mask & ~(1ull << i)); };
+    for (int i = i0; i < i0 + n; ++i) {
+        const long long low = window > 0 ? (long long)base + place(m[i], i) - window + 1 : 0;
+        if (old >= j0 && (old >= low || j0 < n_sink)) return true;
+        for (int d = d0; d < d1; ++d)
+            if ((m[i] >> d & 1) && (base + (d < left ? place(m[d], d) : 0) >= low || base + d < n_sink)) return true;
+    }
+    return false;
+}
+
 // Powers of two that take a row's largest magnitude to [2^13, 2^14) and back: exact in f16 down to
 // 2^-27 of the largest.  A row of zeros, or with an infinity, stays as it is.
 struct RowScale {

@@ -850,7 +850,9 @@ __global__ void __launch_bounds__(Roles<D, kPair>::kThreads, 1) kv_tiles_kernel(
                         if (key < hi && (key + 15 >= lo || key < a.n_sink)) {
                             page = table[tile >> per];
                             if (page < 0 || page >= a.kv.n_pages) {
-                                atomicOr(a.kv.status, FT_DEV_BAD_ID);
+                                if (!a.tree || tree_sees_tile(a.tree + si.q0, run.u.rt.i0, run.u.rt.i1 + 1 - run.u.rt.i0, a.n_tokens - si.q0, base, si.len,
+                                                              key, a.window, a.n_sink))
+                                    atomicOr(a.kv.status, FT_DEV_BAD_ID);
                                 page = -1;
                             }
                         }

@@ -1,4 +1,4 @@
-"""Who sees whom at the edges: keys that no row sees and what their slots hold, masks with bits past the drafted
+"""Who sees whom at the edges: keys that no row sees, what their slots hold and where they have no page, masks with bits past the drafted
 tokens, rows and lengths past what the call says.  Against oracle.kv, with test_gpu_kv's derived bounds."""
 import numpy as np
 import pytest
@@ -149,3 +149,35 @@ def test_prompts_padded_to_a_fixed_size(ft, fmt, D, G, window, n_sink):
     torch.cuda.synchronize()
     for s, r in enumerate(real):
         check_rows(c, o, s, np.arange(r), K.seen(nq[s], lens[s], window, n_sink)[:r])
+
+
+@pytest.mark.parametrize("fmt,D,G", SHAPES)
+@pytest.mark.parametrize("kind", ["step", "chunk", "tree", "padded"])
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (40, 0), (40, 20), (3, 17)])
+def test_pages_that_no_row_needs_may_be_missing(ft, fmt, D, G, kind, window, n_sink):
+    """Table entries of -1 where no row sees a key of the page: behind the window, and where only padding of a tree
+    stands.  No status, and the same results."""
+    rng = np.random.default_rng(5)
+    lens = [300, 77, 190]
+    nq = [1, 1, 1] if kind == "step" else [40, 9, 33]
+    masks = None
+    if kind in ("tree", "padded"):
+        masks = [tree(rng, n) for n in nq]
+        if kind == "padded":
+            masks = [[m if j < n // 4 else 0 for j, m in enumerate(ms)] for n, ms in zip(nq, masks)]
+    c = Case(ft, fmt, D, 2, G, 16, lens, nq, seed=6, masks=masks)
+    gone = 0
+    for s, (n, length) in enumerate(zip(nq, lens)):
+        seen = K.seen(n, length, window, n_sink, None if masks is None else masks[s]).any(0)
+        for p in range(-(-length // c.page)):
+            if not seen[p * c.page:(p + 1) * c.page].any():
+                c.table[s, p] = -1
+                gone += 1
+    assert gone or not window and kind != "padded"
+    c.both(window=window, n_sink=n_sink)
+    assert ft.ft_kv_status(c.kv.handle) == 0
+    if masks is not None:                                    # a page that some row does need
+        s = 0
+        c.table[s, int(np.flatnonzero(K.seen(nq[s], lens[s], window, n_sink, masks[s]).any(0))[-1]) // c.page] = 10 ** 6
+        c.run(window=window, n_sink=n_sink)
+        assert ft.ft_kv_status(c.kv.handle) == ft.FT_DEV_BAD_ID
