@@ -220,7 +220,8 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return (c >> 3) * (kTall * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
-// A lane's raw bytes of a tile's K or V.
+// A lane's raw bytes of a tile's K or V.  Loaded by plain loads: the read-only path is for memory that nobody writes while the
+// kernel runs, and as a programmatic dependent this one starts while the kernel before may still be writing the cache.
 template <int D, int kFormat>
 struct Raw {
     static constexpr int kVecs = kFormat == FT_KV_NVFP4 ? D / 64 : D / 32;
@@ -238,12 +239,12 @@ __device__ __forceinline__ void load_k(Raw<D, kFormat>& r, const uint8_t* tile, 
     const int swap = kFormat == FT_KV_NVFP4 ? (D == 256 ? t >> 1 : 0) : D == 128 ? t >> 1 : D == 256 ? t : 0;
 #pragma unroll
     for (int x = 0; x < r.kVecs; ++x)
-        r.v[x] = __ldg(reinterpret_cast<const uint4*>(tile + (x ^ swap) * 512 + lane * 16));
+        r.v[x] = *reinterpret_cast<const uint4*>(tile + (x ^ swap) * 512 + lane * 16);
     if constexpr (kFormat == FT_KV_NVFP4) {
         const uint8_t* sp = tile + T.k_scales + lane * (D / 32);
-        if constexpr (D == 64) r.s.x = __ldg(reinterpret_cast<const uint16_t*>(sp));
-        if constexpr (D == 128) r.s.x = __ldg(reinterpret_cast<const uint32_t*>(sp));
-        if constexpr (D == 256) r.s = __ldg(reinterpret_cast<const uint2*>(sp));
+        if constexpr (D == 64) r.s.x = *reinterpret_cast<const uint16_t*>(sp);
+        if constexpr (D == 128) r.s.x = *reinterpret_cast<const uint32_t*>(sp);
+        if constexpr (D == 256) r.s = *reinterpret_cast<const uint2*>(sp);
     }
 }
 template <int D, int kFormat>
@@ -298,11 +299,11 @@ __device__ __forceinline__ void load_v(Raw<D, kFormat>& r, const uint8_t* tile, 
     constexpr KvTile T = kv_tile(D, kFormat);
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int x = 0; x < r.kVecs; ++x) r.v[x] = __ldg(reinterpret_cast<const uint4*>(tile + T.code_bytes + x * 512 + lane * 16));
+    for (int x = 0; x < r.kVecs; ++x) r.v[x] = *reinterpret_cast<const uint4*>(tile + T.code_bytes + x * 512 + lane * 16);
     if constexpr (kFormat == FT_KV_NVFP4) {
         const int blk = D == 64 ? g >> 1 : D == 128 ? g : 2 * g;
-        r.s.x = __ldg(reinterpret_cast<const uint32_t*>(tile + T.v_scales + (blk * 4 + t) * 4));
-        if constexpr (D == 256) r.s.y = __ldg(reinterpret_cast<const uint32_t*>(tile + T.v_scales + ((blk + 1) * 4 + t) * 4));
+        r.s.x = *reinterpret_cast<const uint32_t*>(tile + T.v_scales + (blk * 4 + t) * 4);
+        if constexpr (D == 256) r.s.y = *reinterpret_cast<const uint32_t*>(tile + T.v_scales + ((blk + 1) * 4 + t) * 4);
     }
 }
 template <int D, int kFormat>
