@@ -14,6 +14,7 @@
 // and saturate like the definition; only a zero's sign is dropped afterwards.
 #include <atomic>
 #include <cmath>
+#include <cstdint>
 #include <cstdio>
 #include <new>
 
@@ -419,6 +420,10 @@ int shift_of(int page_size) {
     return -1;
 }
 
+size_t layer_bytes(const ft_kv_desc& d) {
+    return (size_t)d.n_pages * d.n_kv_heads * (d.page_size / kKvTile) * kv_tile(d.head_dim, d.format).bytes;
+}
+
 ft_status check_desc(const ft_kv_desc* d) {
     if (!d) return FT_ERR_ARG;
     if (d->L < 1 || d->n_pages < 1 || shift_of(d->page_size) < 0) return FT_ERR_ARG;
@@ -429,11 +434,8 @@ ft_status check_desc(const ft_kv_desc* d) {
     if (d->max_seqs < 1 || d->max_seqs > kMaxSeqs) return FT_ERR_ARG;
     if (d->format != FT_KV_NVFP4 && d->format != FT_KV_FP8) return FT_ERR_ARG;
     if (!positive(d->k_scale) || !positive(d->v_scale)) return FT_ERR_ARG;
+    if ((size_t)d->L > (SIZE_MAX >> 1) / layer_bytes(*d)) return FT_ERR_ARG;     // the pool's bytes
     return FT_OK;
-}
-
-size_t layer_bytes(const ft_kv_desc& d) {
-    return (size_t)d.n_pages * d.n_kv_heads * (d.page_size / kKvTile) * kv_tile(d.head_dim, d.format).bytes;
 }
 
 bool on_device(const void* p) {

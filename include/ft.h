@@ -420,7 +420,7 @@ int32_t   ft_recommend_backend(double cpu_gbs, double pcie_gbs);
 #define FT_KV_FP8   1
 typedef struct ft_kv ft_kv;
 typedef struct {
-    int32_t L;              /* layers */
+    int32_t L;              /* layers (all of them within 2^63 bytes) */
     int32_t n_pages;        /* pages per layer; n_pages * page_size < 2^31 */
     int32_t page_size;      /* tokens per page: 16, 32, 64, 128 or 256 */
     int32_t n_kv_heads;     /* 1..1024 */

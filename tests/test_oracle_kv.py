@@ -149,3 +149,16 @@ def test_binding_matches_the_header(ft, tmp_path):
     assert got == [ctypes.sizeof(ft.FtKvDesc), ft._KV_ATTN.size] + want
     one = ft._KV_ATTN.unpack(ft._KV_ATTN.pack(*range(1, 17), 0.5))
     assert one == (*range(1, 17), 0.5)
+
+
+def test_pools_past_the_address_space_are_refused(ft):
+    """Layers whose bytes together pass 2^64 would come out as a small pool."""
+    wide = dict(n_pages=(1 << 27) - 1, n_kv_heads=1024, n_q_heads=1024, head_dim=256, format=ft.FT_KV_FP8)
+    pool, _ = ft.ft_kv_required_sizes(_desc(ft, **wide, L=1 << 12))
+    assert pool == (1 << 12) * ((1 << 27) - 1) * 1024 * K.tile_bytes(256, "fp8")
+    for L in (1 << 13, 1 << 14, (1 << 14) + 1, (1 << 31) - 1):
+        if L * ((1 << 27) - 1) * 1024 * K.tile_bytes(256, "fp8") < 1 << 63:
+            continue
+        with pytest.raises(ft.FtError) as ei:
+            ft.ft_kv_required_sizes(_desc(ft, **wide, L=L))
+        assert ei.value.status == ft.FT_ERR_ARG
