@@ -180,9 +180,9 @@ def _stream(s):
             import torch
             raw, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
             torch.cuda.init()
-            device = getattr(torch._C, "_cuda_getDevice", device)
-            _raw_stream = lambda: raw(device())  # noqa: E731
-        return _raw_stream()
+            _raw_stream = raw, getattr(torch._C, "_cuda_getDevice", device)
+        raw, device = _raw_stream
+        return raw(device())
     return s if isinstance(s, int) else s.cuda_stream
 
 
@@ -405,6 +405,8 @@ def ft_kv_required_sizes(desc: FtKvDesc):
 
 
 def ft_kv_create(desc: FtKvDesc):
+    if _bf16 is None:
+        _load_types()
     h = c_void_p()
     _check_kv(_f["ft_kv_create"](ctypes.byref(desc), ctypes.byref(h)))
     return h.value
@@ -414,40 +416,129 @@ def ft_kv_destroy(handle):
     _f["ft_kv_destroy"](handle)
 
 
-def _stride(t, given, name):
-    """Token stride in elements: the one given, or that of a tensor."""
-    if given is not None:
-        return given
+_bf16 = _i32 = _f32 = _i64 = _u64 = None                    # torch's types, known from the first handle on
+
+
+def _load_types():
+    global _bf16, _i32, _f32, _i64, _u64
     try:
-        return t.stride(0)
+        import torch
+    except ImportError:                                     # raw addresses only
+        return
+    _bf16, _i32, _f32, _i64, _u64 = torch.bfloat16, torch.int32, torch.float32, torch.int64, torch.uint64
+
+
+def _refuse(t, what, needs):
+    raise FtError(FT_ERR_ARG, f"{what}: {t.dtype}, sizes {tuple(t.shape)}, strides {t.stride()}; needs {needs}")
+
+
+def _address(t, dtype, what, dense=True):
+    """Address of an array.  A raw one stands for itself; a tensor has to be of the type, and dense."""
+    try:
+        p = t.data_ptr()
     except AttributeError:
-        raise TypeError(f"{name} is needed with a raw pointer") from None
+        return _ptr(t) or 0
+    if t.dtype is not dtype or (dense and not t.is_contiguous()):
+        _refuse(t, what, f"dense {dtype}" if dense else dtype)
+    return p
+
+
+def _inner_dense(t, s):
+    at = 1
+    for n, x in zip(t.shape[:0:-1], s[:0:-1]):
+        if x != at and n != 1:
+            return False
+        at *= n
+    return True
+
+
+def _token_stride(t, what):
+    """Token stride in elements of a tensor whose tokens are dense.  That of a single token means nothing: its
+    elements, rounded to what the calls ask for."""
+    try:
+        s = t.stride()
+    except AttributeError:
+        raise TypeError(f"{what}: a raw address needs its token stride") from None
+    if not ((len(s) == 2 and s[1] == 1) or t.is_contiguous() or _inner_dense(t, s)):
+        _refuse(t, what, "dense rows, or a token stride")
+    return s[0] if t.shape[0] != 1 else t.numel() + 7 & ~7
+
+
+# The calls below look at the tensors' types and strides themselves where that takes one test per tensor (a call's host
+# time is a step's), and leave raw addresses and refusals to _address.  A token stride that is given says how the
+# tensor's memory is meant; one that is not is the tensor's.
+_kv_append, _kv_read, _kv_attention = _f["ft_kv_append"], _f["ft_kv_read"], _f["ft_kv_attention"]
 
 
 def ft_kv_append(handle, layer, k, v, slots, n, k_stride=None, v_stride=None, stream=None):
-    _check_kv(_f["ft_kv_append"](handle, layer, _ptr(k), _ptr(v), _stride(k, k_stride, "k_stride"),
-                                 _stride(v, v_stride, "v_stride"), _ptr(slots), n,
-                                 _stream(stream)), handle)
+    try:
+        pk, pv, ps = k.data_ptr(), v.data_ptr(), slots.data_ptr()
+        plain = k.dtype is _bf16 and v.dtype is _bf16 and slots.dtype is _i32 and slots.is_contiguous()
+    except AttributeError:
+        plain = False
+    if not plain:
+        pk, pv = _address(k, _bf16, "append: k", False), _address(v, _bf16, "append: v", False)
+        ps = _address(slots, _i32, "append: slots")
+    if k_stride is None:
+        k_stride = _token_stride(k, "append: k")
+    if v_stride is None:
+        v_stride = _token_stride(v, "append: v")
+    status = _kv_append(handle, layer, pk, pv, k_stride, v_stride, ps, n, _stream(stream))
+    if status:
+        _check_kv(status, handle)
 
 
 def ft_kv_read(handle, layer, slots, n, k_out, v_out, stream=None):
-    _check_kv(_f["ft_kv_read"](handle, layer, _ptr(slots), n, _ptr(k_out), _ptr(v_out),
-                               _stream(stream)), handle)
+    try:
+        ps, pk, pv = slots.data_ptr(), k_out.data_ptr(), v_out.data_ptr()
+        plain = (slots.dtype is _i32 and k_out.dtype is _bf16 and v_out.dtype is _bf16 and slots.is_contiguous()
+                 and k_out.is_contiguous() and v_out.is_contiguous())
+    except AttributeError:
+        plain = False
+    if not plain:
+        ps = _address(slots, _i32, "read: slots")
+        pk, pv = _address(k_out, _bf16, "read: k_out"), _address(v_out, _bf16, "read: v_out")
+    status = _kv_read(handle, layer, ps, n, pk, pv, _stream(stream))
+    if status:
+        _check_kv(status, handle)
 
 
 # ft_kv_attn, packed at once (one conversion per field would cost more than the launch)
 _KV_ATTN = struct.Struct("@3P2q4P7if")
-_kv_attention = _f["ft_kv_attention"]
 
 
 def ft_kv_attention(handle, layer, q, q_start, kv_len, block_table, table_stride, n_seqs, n_tokens,
                     max_q, o, tree_mask=None, window=0, n_sink=0, sm_scale=1.0, lse=None,
                     q_stride=None, o_stride=None, stream=None):
-    status = _kv_attention(handle, _KV_ATTN.pack(
-        _ptr(q) or 0, _ptr(o) or 0, _ptr(lse) or 0, _stride(q, q_stride, "q_stride"),
-        _stride(o, o_stride, "o_stride"), _ptr(q_start) or 0, _ptr(kv_len) or 0,
-        _ptr(block_table) or 0, _ptr(tree_mask) or 0, layer, table_stride, n_seqs, n_tokens, max_q,
-        window, n_sink, sm_scale), _stream(stream))
+    try:
+        pq, po, pt = q.data_ptr(), o.data_ptr(), block_table.data_ptr()
+        ps, pl = q_start.data_ptr(), kv_len.data_ptr()
+        plain = (q.dtype is _bf16 and o.dtype is _bf16 and block_table.dtype is _i32 and q_start.dtype is _i32
+                 and kv_len.dtype is _i32 and block_table.is_contiguous() and q_start.is_contiguous()
+                 and kv_len.is_contiguous())
+        pe = pm = 0
+        if lse is not None:
+            pe = lse.data_ptr()
+            plain = plain and lse.dtype is _f32 and lse.is_contiguous()
+        if tree_mask is not None:
+            pm = tree_mask.data_ptr()
+            plain = plain and tree_mask.dtype is _i64 and tree_mask.is_contiguous()
+    except AttributeError:
+        plain = False
+    if not plain:
+        pq, po = _address(q, _bf16, "attention: q", False), _address(o, _bf16, "attention: o", False)
+        pt = _address(block_table, _i32, "attention: block_table", False)        # its rows may be parts of longer ones
+        if pt and not isinstance(block_table, int) and not (block_table.is_contiguous() or block_table.stride(-1) == 1):
+            _refuse(block_table, "attention: block_table", "dense rows")
+        ps, pl = _address(q_start, _i32, "attention: q_start"), _address(kv_len, _i32, "attention: kv_len")
+        pe = _address(lse, _f32, "attention: lse")
+        pm = _address(tree_mask, _u64 if getattr(tree_mask, "dtype", None) is _u64 else _i64, "attention: tree_mask")
+    if q_stride is None:
+        q_stride = _token_stride(q, "attention: q")
+    if o_stride is None:
+        o_stride = _token_stride(o, "attention: o")
+    status = _kv_attention(handle, _KV_ATTN.pack(pq, po, pe, q_stride, o_stride, ps, pl, pt, pm, layer, table_stride,
+                                                 n_seqs, n_tokens, max_q, window, n_sink, sm_scale), _stream(stream))
     if status:
         _check_kv(status, handle)
 
