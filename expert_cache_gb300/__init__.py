@@ -141,6 +141,7 @@ _f = {
                        c_void_p, c_void_p),
     "ft_kv_attention": _sig("ft_kv_attention", c_int32, c_void_p, c_void_p, c_void_p),
     "ft_kv_status": _sig("ft_kv_status", c_int32, c_void_p, _P(c_int32)),
+    "ft_kv_check_bounded_waits": _sig("ft_kv_check_bounded_waits", c_int32, _P(c_uint32)),
     "ft_kv_last_error": _sig("ft_kv_last_error", ctypes.c_char_p, c_void_p),
     "ft_status_string": _sig("ft_status_string", ctypes.c_char_p, c_int32),
     "ft_last_error": _sig("ft_last_error", ctypes.c_char_p, c_void_p),
@@ -547,6 +548,12 @@ def ft_kv_status(handle):
     s = c_int32()
     _check_kv(_f["ft_kv_status"](handle, ctypes.byref(s)), handle)
     return s.value
+
+
+def ft_kv_check_bounded_waits():
+    bits = c_uint32()
+    _check_kv(_f["ft_kv_check_bounded_waits"](ctypes.byref(bits)))
+    return bits.value
 
 
 # ----------------------------------------------------------------- memory plumbing

@@ -475,7 +475,6 @@ ft_status ft_kv_create(const ft_kv_desc* d, ft_kv** out) {
     ft_kv* kv = new (std::nothrow) ft_kv();
     if (!kv) return FT_ERR_ARG;
     kv->d = *d;
-    kv->tile = kv_tile(d->head_dim, d->format);
     kv->layer_bytes = layer_bytes(*d);
     kv->page_shift = shift_of(d->page_size);
     kv->err[0] = 0;
@@ -577,6 +576,19 @@ ft_status ft_kv_status(ft_kv* kv, int32_t* device_status) {
     if (e == cudaSuccess) e = cudaMemcpy(device_status, kv->d.workspace, 4, cudaMemcpyDeviceToHost);
     if (e == cudaSuccess) e = cudaMemset(kv->d.workspace, 0, 4);
     return e == cudaSuccess ? FT_OK : cuda_fail(kv, e, "status");
+}
+
+ft_status ft_kv_check_bounded_waits(uint32_t* expired) {
+    if (!expired) return FT_ERR_ARG;
+    unsigned* bits = nullptr;
+    cudaError_t e = cudaMalloc(&bits, sizeof(unsigned));
+    if (e != cudaSuccess) return FT_ERR_CUDA;
+    e = cudaMemset(bits, 0, sizeof(unsigned));
+    if (e == cudaSuccess) e = check_rows_waits(bits);
+    if (e == cudaSuccess) e = check_tiles_waits(bits);
+    if (e == cudaSuccess) e = cudaMemcpy(expired, bits, sizeof(unsigned), cudaMemcpyDeviceToHost);
+    cudaFree(bits);
+    return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }
 
 const char* ft_kv_last_error(const ft_kv* kv) { return kv ? kv->err : ""; }

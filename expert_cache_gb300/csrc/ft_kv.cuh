@@ -66,6 +66,9 @@ cudaError_t launch_kv_read(const KvView& kv, int D, int format, const int32_t* s
                            cudaStream_t s);
 cudaError_t launch_kv_attention(const AttnArgs& a, int D, int format, cudaStream_t s);
 cudaError_t launch_kv_tiles(const AttnArgs& a, int D, int format, cudaStream_t s);    // many rows per key
+// The bounded waits of the two kernels against barriers that nobody arrives on; set bits of *expired (device).
+cudaError_t check_rows_waits(unsigned* expired);      // 1: a tile's copy
+cudaError_t check_tiles_waits(unsigned* expired);     // 2: a role's wait, 4: one after it gave up, 8: the last wait
 
 #ifdef __CUDACC__
 
@@ -142,7 +145,6 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& a, int s) {
 
 struct ft_kv {
     ft_kv_desc d;
-    ft::KvTile tile;
     size_t layer_bytes;
     int page_shift;
     char err[256];

@@ -767,7 +767,24 @@ cudaError_t run(AttnArgs a, cudaStream_t s) {
     return plan_direct(a, room, 16) ? launch_direct<D, kFormat, 2>(a, s) : launch_kv_tiles(a, D, kFormat, s);
 }
 
+__global__ void rows_wait_check_kernel(unsigned* expired) {
+    __shared__ __align__(8) uint64_t bar;
+    const uint32_t b = smem_u32(&bar);
+    if (threadIdx.x == 0) {
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(b));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    const bool done = __all_sync(0xffffffffu, mbar_wait(b, 0));
+    if (threadIdx.x == 0 && !done) atomicOr(expired, 1u);
+}
+
 }  // namespace
+
+cudaError_t check_rows_waits(unsigned* expired) {
+    rows_wait_check_kernel<<<1, 32>>>(expired);
+    return cudaGetLastError();
+}
 
 size_t kv_task_bytes() { return sizeof(JoinTask) * kWarps * kMaxShares; }
 size_t kv_parts_bytes(int D) { return (size_t)2 * kWarps * kMaxShares * 16 * (D + 2) * sizeof(float); }

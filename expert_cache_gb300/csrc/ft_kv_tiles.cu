@@ -1165,7 +1165,31 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     return run_tiles<D, kFormat, false>(a, s);
 }
 
+__global__ void tiles_wait_check_kernel(unsigned* expired) {
+    __shared__ __align__(8) uint64_t bar;
+    __shared__ volatile int abort_flag;
+    const uint32_t b = smem_u32(&bar);
+    if (threadIdx.x == 0) {
+        mbar_init(b, 1);
+        abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    unsigned bits = 0;
+    if (!mbar_wait(b, 0, &abort_flag) && abort_flag) bits |= 2u;
+    const long long from = clock64();
+    if (!mbar_wait(b, 0, &abort_flag) && clock64() - from < kDrainClocks / 64) bits |= 4u;     // leaves at the flag
+    const long long drain = clock64();
+    if (!mbar_drained(b) && clock64() - drain >= kDrainClocks) bits |= 8u;                     // does not
+    if (threadIdx.x == 0) atomicOr(expired, bits);
+}
+
 }  // namespace
+
+cudaError_t check_tiles_waits(unsigned* expired) {
+    tiles_wait_check_kernel<<<1, 32>>>(expired);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_kv_tiles(const AttnArgs& a, int D, int format, cudaStream_t s) {
     if (format == FT_KV_NVFP4)

@@ -519,6 +519,13 @@ ft_status ft_kv_attention(ft_kv* kv, const ft_kv_attn* call, void* stream);
 
 /* Read and clear the handle's device status word (FT_DEV_* bits).  Synchronises. */
 ft_status ft_kv_status(ft_kv* kv, int32_t* device_status);
+/* Diagnostic of the attention's failure path, like ft_check_bounded_waits: a warp runs each kind
+ * of wait of its kernels on a barrier that nobody arrives on.  *expired gets bit 0 when the wait for a
+ * tile's copy gave up, bit 1 a role's wait (which tells the other roles), bit 2 when a wait of
+ * another role then left at once, bit 3 when the wait for the products under way did not leave
+ * but gave up after its own bound: 0xF from a healthy build.  About 6 s; synchronises; needs no
+ * cache.  Errors: FT_ERR_ARG for a NULL expired, FT_ERR_CUDA. */
+ft_status ft_kv_check_bounded_waits(uint32_t* expired);
 /* Message of the last failed call on kv, or "" */
 const char* ft_kv_last_error(const ft_kv* kv);
 
