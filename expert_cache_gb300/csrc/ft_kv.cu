@@ -1,10 +1,10 @@
 // The quantised key/value cache: host side of the C ABI, the writing kernels (bf16 -> codes
 // and scales in their tiles) and the reading ones (codes -> bf16).
 //
-// Both directions are bound by the bytes of the bf16 side (4 of 5.1 bytes per element of NVFP4), and a
-// call of few tokens by its launch.  A thread has 16 dims of a token, K's and V's.  To write 8192 tokens of 8
-// heads of 128 in NVFP4 and read them back (86 MB) takes 18.2 us, 4.7 TB/s; the instructions of the
-// quotients are most of what is left.
+// A thread has 16 dims of a token, K's and V's.  A call of few tokens is bound by its launch.  To write 8192 tokens of 8
+// heads of 128 in NVFP4 and read them back (86 MB) takes 21.8 us where every pass has other tensors, 3.9 TB/s: 12.6
+// us to write and 10.1 to read, of which the bytes need 6.3 each.  Writing takes 263 instructions per 16 values (quotients, packing, place)
+// and issues 65 % of the time; reading 165, 53 %, and waits for the codes behind the slots.
 //
 // Quotients are the definition's x / (scale * s), rounded to nearest, in three operations: with
 // r = RN(1/d) and q0 = RN(x r), q0 + RN(x - q0 d) r rounds to RN(x/d) (Markstein's correction, 1990;
@@ -219,11 +219,6 @@ __device__ __forceinline__ void dequant_e4m3(uint32_t w, float st, uint32_t* out
     out[0] = to_bf16(h[0], st);
     out[1] = to_bf16(h[1], st);
 }
-__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
-    uint32_t o;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(o) : "r"(byte * 0x101u));
-    return o;
-}
 
 template <int D, int kFormat, bool kV>
 __device__ __forceinline__ void read_block(const uint8_t* tile, int r, int b, __nv_bfloat16* dst, float st) {
@@ -243,8 +238,8 @@ __device__ __forceinline__ void read_block(const uint8_t* tile, int r, int b, __
 
 // What a warp takes, a block of 16 dims of a token per lane: 8 tokens, in the call's order, by 4 blocks (64 dims)
 // of a head.  Of tokens that are neighbours in a tile the codes are then stored in full sectors, and rows read
-// 128 bytes at a time (8192 tokens of 8 heads of 128 written and read: 18.2 us; 4 tokens by 8 blocks 19 us; tokens by whole
-// rows, which store V in pieces of 8 bytes, 20.6 us).
+// 128 bytes at a time (8192 tokens of 8 heads of 128 written and read, the same tensors again and again, which L2 holds in
+// part: 18.2 us; 4 tokens by 8 blocks 19 us; tokens by whole rows, which store V in pieces of 8 bytes, 20.6 us).
 constexpr int kPatchBlocks = 4, kPatchTokens = 32 / kPatchBlocks;
 
 struct Place {
@@ -335,7 +330,7 @@ cudaError_t by_shape(int D, int format, A&&... a) {
 }
 
 // A warp per patch, at most 2^20 CTAs (32-bit indexes).  A thread has both K's block and V's, so that it finds its
-// place once (two threads: 21.8 us instead of 18.2 for 8192 tokens of 8 heads of 128), but one of them where
+// place once (two threads: 21.8 us instead of 18.2 for 8192 tokens of 8 heads of 128, the same tensors again), but one of them where
 // that leaves fewer than four warps per SM (16 tokens: 3.7 us instead of 4.3).
 struct PlaceGrid {
     unsigned ctas;

@@ -106,6 +106,19 @@ __device__ __forceinline__ int kv_v_scale_byte(int r, int b) {
     return kv_tile(D, FT_KV_NVFP4).v_scales + (b * 4 + ((r & 7) >> 1)) * 4 + 2 * (r >> 3) + (r & 1);
 }
 
+// An E4M3 byte as a pair of equal f16.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
+    uint32_t o;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(o) : "r"(byte * 0x101u));
+    return o;
+}
+// Two f16 of two fp32.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
 // Four E4M3 bytes with the NaNs among them as zeros.
 __device__ __forceinline__ uint32_t e4m3_numbers(uint32_t w) {
     const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;

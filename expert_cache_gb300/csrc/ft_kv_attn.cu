@@ -24,10 +24,10 @@
 //     unit that a share began inside.
 //   * Short sequences go without the line: a cluster of CTAs per unit (plan_direct).
 //
-// 32 sequences of up to 32768 tokens, 8 heads of 128 in 8 bits (292 MB): 57 us, 5.1 TB/s; the kernel reads at 84 % of
+// 32 sequences of up to 32768 tokens, 8 heads of 128 in 8 bits (292 MB): 58 us, 5.0 TB/s; the kernel reads at 84 % of
 // the copy rate while all its warps run, the rest is the start, the ragged end and the second kernel (about 10
-// us).  One sequence of 262145, 2 heads of 256 in 4 bits (151 MB): 44 us, 3.4 TB/s, bound by the 630
-// instructions of a tile (8192 codes; 1.9 issued per clock and SM by 8 warps, all that 228 registers leave
+// us).  One sequence of 262145, 2 heads of 256 in 4 bits (151 MB): 43 us, 3.5 TB/s, bound by the 633
+// instructions of a tile (8192 codes; 2.0 issued per clock and SM by 8 warps, all that 238 registers leave
 // room for).  One of 4096: 10 us, the latency of a launch, a tile's chain and the cluster's join.
 #include <atomic>
 
@@ -75,11 +75,6 @@ __device__ __forceinline__ void e4m3_unpack(uint32_t w, uint32_t& lo, uint32_t& 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {

@@ -26,10 +26,11 @@
 // Every wait is bounded: on expiry the CTA sets FT_DEV_TIMEOUT, leaves its loops, waits for the products under way and
 // frees its tensor memory.
 //
-// 2048 tokens x 32 heads of 128 over 8192 keys of 8 heads, causal, 4-bit: 243 us, 990 TFLOP/s, half of what a
+// 2048 tokens x 32 heads of 128 over 8192 keys of 8 heads, causal, 4-bit: 247 us, 975 TFLOP/s, half of what a
 // large library product reaches; the tensor pipe is busy 45 % of the time.  A block's softmax
 // sets the pace (two passes over tensor memory, one row per thread): 4650 clocks for 256 rows x 128 keys, of which
-// the products take 2070; with blocks in halves, S one half ahead of the softmax, it took 281 us.  A short call is bound by its way through the
+// the products take 2070; with blocks in halves, S one half ahead of the softmax, it took 281 us where this
+// took 243.  A short call is bound by its way through the
 // roles: 9 us from the launch to the first unit's last block, of which Q takes 3.5, and 5 to 8 us for the second
 // kernel.
 #include <atomic>
@@ -169,17 +170,6 @@ __device__ __forceinline__ uint4 unpack_e4m3(uint32_t w0, uint32_t w1) {
         "cvt.rn.f16x2.e4m3x2 %2, c;\n\tcvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
         : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w) : "r"(w0), "r"(w1));
     return o;
-}
-// The byte of w at a lane's place as a pair of equal f16.
-__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
-    uint32_t o;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(o) : "r"(byte * 0x101u));
-    return o;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
 }
 
 // Two fp32 at a time.

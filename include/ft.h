@@ -479,7 +479,7 @@ ft_status ft_kv_read(ft_kv* kv, int32_t layer, const int32_t* slots, int32_t n, 
  * the run: every sum has a fixed order for given arguments on one GPU.
  * Slots of keys that no row sees need not have been written (padding of a tree, tokens that a
  * window has left): whatever they hold, no row's result depends on it.  A row that sees a key
- * which was never written gets what the bytes give; the other rows do not.
+ * which was never written gets what the bytes give; rows that do not see it stay as they are.
  * The call's arguments are the fields of ft_kv_attn, read before it returns.
  * Rows of q and o are 16-byte aligned.  Rows outside every sequence are left as they are.
  * Asynchronous on stream, capturable, no allocation; calls of one handle share its
