@@ -84,7 +84,8 @@ __device__ __forceinline__ RowRule row_rule(const AttnArgs& a, const SeqInfo& s,
         pos = base + __popcll(r.mask & ~(1ull << i));
         r.lim = s.len - 1;
     }
-    if (a.window > 0) r.low = (int)max((long long)pos - a.window + 1, 0LL);
+    // keys stand at 0 or after it, drafted ones from base on, which is below 0 where fewer tokens are cached than new
+    if (a.window > 0) r.low = (int)max((long long)pos - a.window + 1, (long long)min(base, 0));
     return r;
 }
 // The rule for a key below base or without a tree.

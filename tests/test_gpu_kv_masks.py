@@ -99,6 +99,22 @@ def test_stray_bits_move_the_window_of_their_row_alone(ft, fmt, D, G, n, length,
     assert ft.ft_kv_status(c.kv.handle) == 0
 
 
+@pytest.mark.parametrize("fmt,D,G", SHAPES)
+@pytest.mark.parametrize("window", [1, 3, 20, 64, 100])
+def test_trees_of_more_tokens_than_are_cached(ft, fmt, D, G, window):
+    """The first drafted tokens then stand before the sequence's start, at places below 0, as do some of the keys."""
+    rng = np.random.default_rng(window)
+    lens, nq = [4, 20, 63, 1], [46, 24, 64, 2]
+    masks = [tree(rng, n) for n in nq]
+    for ms in masks:
+        for i in range(0, len(ms), 3):                       # any bits
+            ms[i] |= int(rng.integers(0, 1 << 62)) << 2
+    c = Case(ft, fmt, D, 2, G, 16, lens, nq, seed=window, masks=masks)
+    for n_sink in (0, 2):
+        c.both(window=window, n_sink=n_sink)
+    assert ft.ft_kv_status(c.kv.handle) == 0
+
+
 # ------------------------------------------------------------------------------ keys that no row sees
 
 @pytest.mark.parametrize("fmt,D,G", SHAPES)
