@@ -18,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libft.so")
 
 FT_OK, FT_ERR_ARG, FT_ERR_CUDA, FT_ERR_CAPACITY, FT_ERR_STATE, FT_ERR_TIMEOUT, FT_ERR_UNPINNED = range(7)
-FT_DEV_BAD_ID, FT_DEV_TIMEOUT, FT_DEV_SCALE_RANGE = 0x1, 0x2, 0x4
+FT_DEV_BAD_ID, FT_DEV_TIMEOUT, FT_DEV_SCALE_RANGE, FT_DEV_NO_PAGES = 0x1, 0x2, 0x4, 0x8
 FT_FORMAT_NVFP4, FT_FORMAT_MXFP4 = 0, 1
 FORMATS = {"nvfp4": FT_FORMAT_NVFP4, "mxfp4": FT_FORMAT_MXFP4}
 FT_SPLIT_FULL_OFFLOAD, FT_SPLIT_QSTAR = 0, 1
@@ -28,6 +28,9 @@ FT_PREFILL_ON_DEMAND = 4
 FT_BACKEND_OFFLOAD, FT_BACKEND_HYBRID = 0, 1
 FT_KV_NVFP4, FT_KV_FP8 = 0, 1
 KV_FORMATS = {"nvfp4": FT_KV_NVFP4, "fp8": FT_KV_FP8}
+FT_DTYPE_BF16, FT_DTYPE_F32 = 0, 1
+FT_ROUTE_SOFTMAX, FT_ROUTE_SIGMOID = 0, 1
+ROUTE_SCORES = {"softmax": FT_ROUTE_SOFTMAX, "sigmoid": FT_ROUTE_SIGMOID}
 FT_PROF_KINDS = 5
 PROF_NAMES = ("decode", "prefill_gemm1", "prefill_gemm2", "prefill_other", "prefill_copy")
 
@@ -140,6 +143,11 @@ _f = {
     "ft_kv_read": _sig("ft_kv_read", c_int32, c_void_p, c_int32, c_void_p, c_int32, c_void_p,
                        c_void_p, c_void_p),
     "ft_kv_attention": _sig("ft_kv_attention", c_int32, c_void_p, c_void_p, c_void_p),
+    "ft_kv_plan": _sig("ft_kv_plan", c_int32, c_void_p, c_void_p, c_void_p),
+    "ft_rope_table": _sig("ft_rope_table", c_int32, c_void_p, c_int32, c_int32, c_double, c_void_p, c_void_p),
+    "ft_kv_append_rotated": _sig("ft_kv_append_rotated", c_int32, c_void_p, c_void_p, c_void_p),
+    "ft_moe_route": _sig("ft_moe_route", c_int32, c_void_p, c_void_p),
+    "ft_logprobs": _sig("ft_logprobs", c_int32, c_void_p, c_void_p),
     "ft_kv_status": _sig("ft_kv_status", c_int32, c_void_p, _P(c_int32)),
     "ft_kv_check_bounded_waits": _sig("ft_kv_check_bounded_waits", c_int32, _P(c_uint32)),
     "ft_kv_last_error": _sig("ft_kv_last_error", ctypes.c_char_p, c_void_p),
@@ -417,16 +425,16 @@ def ft_kv_destroy(handle):
     _f["ft_kv_destroy"](handle)
 
 
-_bf16 = _i32 = _f32 = _i64 = _u64 = None                    # torch's types, known from the first handle on
+_bf16 = _i32 = _f32 = _f64 = _i64 = _u64 = None             # torch's types, known from the first handle on
 
 
 def _load_types():
-    global _bf16, _i32, _f32, _i64, _u64
+    global _bf16, _i32, _f32, _f64, _i64, _u64
     try:
         import torch
     except ImportError:                                     # raw addresses only
         return
-    _bf16, _i32, _f32, _i64, _u64 = torch.bfloat16, torch.int32, torch.float32, torch.int64, torch.uint64
+    _bf16, _i32, _f32, _f64, _i64, _u64 = torch.bfloat16, torch.int32, torch.float32, torch.float64, torch.int64, torch.uint64
 
 
 def _refuse(t, what, needs):
@@ -542,6 +550,140 @@ def ft_kv_attention(handle, layer, q, q_start, kv_len, block_table, table_stride
                                                  n_seqs, n_tokens, max_q, window, n_sink, sm_scale), _stream(stream))
     if status:
         _check_kv(status, handle)
+
+# ft_kv_step, ft_kv_qkv, ft_route and ft_logprob, packed at once
+_KV_STEP = struct.Struct("@14P3i4x")
+_KV_QKV = struct.Struct("@5P5q5P5if")
+_ROUTE = struct.Struct("@4Pq9if")
+_LOGPROB = struct.Struct("@6Pq4if4x")
+_kv_plan, _kv_append_rotated, _moe_route, _logprobs = (
+    _f["ft_kv_plan"], _f["ft_kv_append_rotated"], _f["ft_moe_route"], _f["ft_logprobs"])
+
+
+def ft_kv_plan(handle, n_new, len, held, block_table, table_stride, free_pages, n_free, n_seqs, n_tokens, q_start, kv_len, slots,
+               len_out, held_out, n_free_out, positions=None, tree_mask=None, stream=None):
+    ints = (n_new, len, held, n_free, free_pages, q_start, kv_len, slots, len_out, held_out, n_free_out)
+    try:
+        p = [t.data_ptr() for t in ints]
+        plain = True
+        for t in ints:
+            if t.dtype is not _i32 or not t.is_contiguous():
+                plain = False
+        pt, pp, pm = block_table.data_ptr(), 0, 0
+        plain = plain and block_table.dtype is _i32 and block_table.is_contiguous()
+        if positions is not None:
+            pp = positions.data_ptr()
+            plain = plain and positions.dtype is _i32 and positions.is_contiguous()
+        if tree_mask is not None:
+            pm = tree_mask.data_ptr()
+            plain = plain and tree_mask.dtype is _i64 and tree_mask.is_contiguous()
+    except AttributeError:
+        plain = False
+    if not plain:
+        names = ("n_new", "len", "held", "n_free", "free_pages", "q_start", "kv_len", "slots", "len_out", "held_out", "n_free_out")
+        p = [_address(t, _i32, f"plan: {name}") for t, name in zip(ints, names)]
+        pt = _address(block_table, _i32, "plan: block_table", False)             # its rows may be parts of longer ones
+        if pt and not isinstance(block_table, int) and not (block_table.is_contiguous() or block_table.stride(-1) == 1):
+            _refuse(block_table, "plan: block_table", "dense rows")
+        pp = _address(positions, _i32, "plan: positions")
+        pm = _address(tree_mask, _u64 if getattr(tree_mask, "dtype", None) is _u64 else _i64, "plan: tree_mask")
+    status = _kv_plan(handle, _KV_STEP.pack(p[0], p[1], p[2], p[3], pt, p[4], pm, p[5], p[6], p[7], pp, p[8], p[9], p[10],
+                                            n_seqs, table_stride, n_tokens), _stream(stream))
+    if status:
+        _check_kv(status, handle)
+
+
+def ft_rope_table(inv_freq, rope_dim, n_positions, table, mscale=1.0, stream=None):
+    if _bf16 is None:
+        _load_types()
+    pi, pt = _address(inv_freq, _f64, "rope_table: inv_freq"), _address(table, _f32, "rope_table: table")
+    _check(_f["ft_rope_table"](pi, rope_dim, n_positions, mscale, pt, _stream(stream)))
+
+
+def ft_kv_append_rotated(handle, layer, q, k, v, slots, n, q_out, positions, rope, rope_dim, n_positions, k_out=None, q_norm=None,
+                         k_norm=None, eps=1e-6, interleaved=False, q_stride=None, k_stride=None, v_stride=None, q_out_stride=None,
+                         k_out_stride=None, stream=None):
+    pko = pqn = pkn = pr = pp = 0
+    try:
+        pq, pk, pv, po, ps = q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), slots.data_ptr()
+        plain = (q.dtype is _bf16 and k.dtype is _bf16 and v.dtype is _bf16 and q_out.dtype is _bf16 and slots.dtype is _i32
+                 and slots.is_contiguous())
+        if rope is not None:
+            pr, pp = rope.data_ptr(), positions.data_ptr()
+            plain = plain and rope.dtype is _f32 and positions.dtype is _i32 and rope.is_contiguous() and positions.is_contiguous()
+        if k_out is not None:
+            pko = k_out.data_ptr()
+            plain = plain and k_out.dtype is _bf16
+        if q_norm is not None:
+            pqn = q_norm.data_ptr()
+            plain = plain and q_norm.dtype is _f32 and q_norm.is_contiguous()
+        if k_norm is not None:
+            pkn = k_norm.data_ptr()
+            plain = plain and k_norm.dtype is _f32 and k_norm.is_contiguous()
+    except AttributeError:
+        plain = False
+    if not plain:
+        pq, pk, pv, po, pko = (_address(t, _bf16, f"append_rotated: {name}", False)
+                               for t, name in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out"), (k_out, "k_out")))
+        ps, pp = _address(slots, _i32, "append_rotated: slots"), _address(positions, _i32, "append_rotated: positions")
+        pr, pqn, pkn = (_address(t, _f32, f"append_rotated: {name}") for t, name in ((rope, "rope"), (q_norm, "q_norm"), (k_norm, "k_norm")))
+    if q_stride is None:
+        q_stride = _token_stride(q, "append_rotated: q")
+    if k_stride is None:
+        k_stride = _token_stride(k, "append_rotated: k")
+    if v_stride is None:
+        v_stride = _token_stride(v, "append_rotated: v")
+    if q_out_stride is None:
+        q_out_stride = _token_stride(q_out, "append_rotated: q_out")
+    if k_out_stride is None:
+        k_out_stride = _token_stride(k_out, "append_rotated: k_out") if pko else 0
+    status = _kv_append_rotated(handle, _KV_QKV.pack(pq, pk, pv, po, pko, q_stride, k_stride, v_stride, q_out_stride, k_out_stride,
+                                                     pqn, pkn, pr, pp, ps, layer, n, rope_dim, n_positions, interleaved, eps), _stream(stream))
+    if status:
+        _check_kv(status, handle)
+
+
+def _logits(t, width, what, stride, dtype):
+    """(address, type, row stride) of rows of logits."""
+    if _bf16 is None:
+        _load_types()
+    try:
+        p, d = t.data_ptr(), t.dtype
+    except AttributeError:
+        if stride is None:
+            raise TypeError(f"{what}: a raw address needs its row stride") from None
+        return _ptr(t) or 0, FT_DTYPE_F32 if dtype == "fp32" else FT_DTYPE_BF16, stride
+    if d is not _bf16 and d is not _f32:
+        _refuse(t, what, "torch.bfloat16 or torch.float32")
+    if stride is None:
+        s = t.stride()
+        if t.dim() != 2 or (s[1] != 1 and t.shape[1] != 1):
+            _refuse(t, what, "dense rows, or a row stride")
+        stride = s[0] if t.shape[0] != 1 else width
+    return p, FT_DTYPE_BF16 if d is _bf16 else FT_DTYPE_F32, stride
+
+
+def ft_moe_route(logits, T, E, k, topk_ids, topk_w, score="softmax", bias=None, n_group=1, topk_group=1, group_best=1, renormalise=True,
+                 scale=1.0, stride=None, dtype="bf16", stream=None):
+    """dtype ("bf16" or "fp32") names the type of logits that are given as a raw address."""
+    pl, dt, stride = _logits(logits, E, "route: logits", stride, dtype)
+    pi, pw, pb = _address(topk_ids, _i32, "route: topk_ids"), _address(topk_w, _f32, "route: topk_w"), _address(bias, _f32, "route: bias")
+    status = _moe_route(_ROUTE.pack(pl, pb, pi, pw, stride, T, E, k, dt, ROUTE_SCORES[score], n_group, topk_group, group_best,
+                                    bool(renormalise), scale), _stream(stream))
+    if status:
+        _check(status)
+
+
+def ft_logprobs(logits, n, V, tokens=None, logp=None, entropy=None, top_ids=None, top_logp=None, k=0, scale=1.0, stride=None, dtype="bf16",
+                stream=None):
+    """dtype ("bf16" or "fp32") names the type of logits that are given as a raw address."""
+    pl, dt, stride = _logits(logits, V, "logprobs: logits", stride, dtype)
+    pt, pi = _address(tokens, _i32, "logprobs: tokens"), _address(top_ids, _i32, "logprobs: top_ids")
+    pp, pe, px = (_address(t, _f32, what) for t, what in (
+        (logp, "logprobs: logp"), (entropy, "logprobs: entropy"), (top_logp, "logprobs: top_logp")))
+    status = _logprobs(_LOGPROB.pack(pl, pt, pp, pe, pi, px, stride, n, V, k, dt, scale), _stream(stream))
+    if status:
+        _check(status)
 
 
 def ft_kv_status(handle):

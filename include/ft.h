@@ -57,6 +57,11 @@ typedef int32_t ft_status;
 #define FT_DEV_TIMEOUT   0x2 /* a bounded device wait ran out */
 #define FT_DEV_SCALE_RANGE 0x4 /* prefill of MXFP4 experts: a block scale outside
                                   2^-9..2^8 has no exact UE4M3 twin (clamped) */
+#define FT_DEV_NO_PAGES  0x8 /* a sequence needed more pages than were free (ft_kv_plan) */
+
+/* Types of logits. */
+#define FT_DTYPE_BF16 0
+#define FT_DTYPE_F32  1
 
 /* Expert record formats ([EXPLAINER §9.2]: NVFP4 on the NVFP4 machines; DeepSeek-V4-
  * Flash's routed experts are natively MXFP4 and are consumed bit-exactly).
@@ -517,6 +522,92 @@ typedef struct {
 } ft_kv_attn;
 ft_status ft_kv_attention(ft_kv* kv, const ft_kv_attn* call, void* stream);
 
+/* ---- What a step of a server does around the calls above: its rows, slots and pages from the sequences' lengths
+ * (ft_kv_plan), queries and keys normalised and turned by their position on their way into the cache
+ * (ft_kv_append_rotated), the experts of each token (ft_moe_route) and what the logits say about its answer
+ * (ft_logprobs).  The pages describe none of these; the rules below are this library's.  All are asynchronous on
+ * their stream, capturable, allocate nothing and need nothing from the host between steps. */
+
+/* One step's rows, slots and positions, with the pages of each sequence.  Sequence s has len[s] cached tokens that
+ * stay (a caller that rejects drafted tokens lowers it), holds the pages block_table[s, 0 .. held[s]) and gets n_new[s]
+ * tokens; a negative n_new[s] ends it (len and rows count as 0).  With after = len + n_new it holds
+ * want = ceil(after / page_size) pages afterwards:
+ *   - surplus pages (j >= want) of all sequences are pushed on the stack of free pages, in ascending (s, j);
+ *   - then missing ones are popped from it, in ascending (s, j), and entered in the table.
+ * A sequence is refused if pages run out (if it takes any, and those that the sequences up to it take are more than are
+ * free; FT_DEV_NO_PAGES), or if its description does not hold (FT_DEV_BAD_ID): held outside [0, table_stride] or
+ * above n_pages; for one that goes on also len < 0, held less than its len needs, rows past n_tokens, more than
+ * table_stride pages or 2^31 - 1 tokens, and, with tree_mask, more than 64 new tokens.  A refused sequence keeps its len
+ * and its pages; its rows stay in q_start, get the slot -1 (which ft_kv_append skips) and kv_len 0 (under which
+ * ft_kv_attention gives o = 0), and the sequences that it leaves room for are served.
+ *   q_start   [n_seqs + 1]  first row of each sequence, at most n_tokens
+ *   kv_len    [n_seqs]      the length that attention is to use (after, or 0 for a refused sequence)
+ *   slots, positions [n_tokens]  of each row; a drafted row's position is len + the number of set bits of its mask other than
+ *                           its own, another's its index; rows that no served sequence has: -1 and 0
+ *   len_out, held_out [n_seqs], n_free_out [1]  the state after the call; may be len, held and n_free themselves.  No
+ *                           other two arrays may overlap.
+ * Entries of the table past held_out and of the stack from n_free_out on are left as they were (surplus pages' entries keep
+ * their old value).  A page outside [0, n_pages) in the table or on the stack gives its tokens the slot -1 and sets
+ * FT_DEV_BAD_ID, as does n_free outside [0, n_pages] (it is cut to that) or pages pushed past n_pages (dropped).
+ * Errors (nothing launched): FT_ERR_ARG for n_seqs outside [0, max_seqs], n_tokens < 0, table_stride < 1, NULL pointers
+ * (arrays of no elements may be NULL). */
+typedef struct {
+    const int32_t* n_new;       /* device [n_seqs] */
+    const int32_t* len;         /* device [n_seqs] */
+    const int32_t* held;        /* device [n_seqs] */
+    const int32_t* n_free;      /* device [1] */
+    int32_t* block_table;       /* device [n_seqs, table_stride], read and written */
+    int32_t* free_pages;        /* device [n_pages], read and written: the stack, its top at n_free - 1 */
+    const uint64_t* tree_mask;  /* device [n_tokens] or NULL, as ft_kv_attention's */
+    int32_t* q_start;           /* device [n_seqs + 1] */
+    int32_t* kv_len;            /* device [n_seqs] */
+    int32_t* slots;             /* device [n_tokens] */
+    int32_t* positions;         /* device [n_tokens] or NULL */
+    int32_t* len_out;           /* device [n_seqs] */
+    int32_t* held_out;          /* device [n_seqs] */
+    int32_t* n_free_out;        /* device [1] */
+    int32_t n_seqs, table_stride, n_tokens;
+} ft_kv_step;
+ft_status ft_kv_plan(ft_kv* kv, const ft_kv_step* call, void* stream);
+
+/* Angles of the positions 0 .. n_positions - 1: row p of table (device fp32 [n_positions, rope_dim]) holds
+ * mscale * cos(p * inv_freq[i]) for i < rope_dim / 2, then mscale * sin of the same; angles and functions in 64 bits,
+ * rounded once.  inv_freq: device fp64 [rope_dim / 2].  Done once per model.  Errors: FT_ERR_ARG for n_positions < 1,
+ * rope_dim odd or outside [2, 256], NULL, a mscale that is not finite; FT_ERR_CUDA. */
+ft_status ft_rope_table(const double* inv_freq, int32_t rope_dim, int32_t n_positions, double mscale, float* table, void* stream);
+
+/* ft_kv_append of n new tokens whose queries and keys still have to be normalised and turned: per head x of q and k
+ *   y = x * (mean(x^2) + eps)^-1/2 * norm            (norm NULL: y = x)
+ *   the pairs (a, b) of y become (a c - b s, b c + a s) with c and s of the token's row of the table; pair i is
+ *   (y[i], y[i + rope_dim / 2]), or (y[2 i], y[2 i + 1]) if interleaved; dims from rope_dim on stay.
+ * q_out gets q's result rounded to bf16.  k's result is rounded to fp32, then to bf16, and stored as ft_kv_append stores that (k_out
+ * gets it too); v is stored as it is.  q's values are in fp32; k's are good to some 2^-40 of the larger of their pair
+ * before they are rounded, so what is stored is what the formula gives in 64 bits.  Where a head's squares pass fp32's range
+ * its finite dims come out as 0.
+ * Tokens whose slot is -1 are padding: nothing of them is read or written.  Another slot outside the cache, or a position
+ * outside [0, n_positions), sets FT_DEV_BAD_ID and is treated the same way.  Slots differ from each other.
+ * q_out may be q, k_out may be k (of the same stride); no other arrays overlap.
+ * Errors (nothing launched): FT_ERR_ARG for layer outside [0, L), n < 0, NULL or misaligned q, k, v, q_out (16 bytes; k_out
+ * too), norms or table (16 bytes), strides that are no multiples of 8 or less than a token, rope_dim no multiple of 32 or outside
+ * [0, head_dim], n_positions < 1 with rope_dim > 0, eps not finite or <= 0 with a norm. */
+typedef struct {
+    const void* q;            /* device bf16 [n, n_q_heads, D] */
+    const void* k;            /* device bf16 [n, n_kv_heads, D] */
+    const void* v;            /* device bf16 [n, n_kv_heads, D] */
+    void* q_out;              /* device bf16 [n, n_q_heads, D] */
+    void* k_out;              /* device bf16 [n, n_kv_heads, D] or NULL */
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;   /* token strides in elements */
+    const float* q_norm;      /* device fp32 [D] or NULL */
+    const float* k_norm;      /* device fp32 [D] or NULL */
+    const float* rope;        /* device fp32 [n_positions, rope_dim] (ft_rope_table); NULL if rope_dim is 0 */
+    const int32_t* positions; /* device [n]; NULL if rope_dim is 0 */
+    const int32_t* slots;     /* device [n] */
+    int32_t layer, n, rope_dim, n_positions;
+    int32_t interleaved;      /* 0 or 1 */
+    float eps;
+} ft_kv_qkv;
+ft_status ft_kv_append_rotated(ft_kv* kv, const ft_kv_qkv* call, void* stream);
+
 /* Read and clear the handle's device status word (FT_DEV_* bits).  Synchronises. */
 ft_status ft_kv_status(ft_kv* kv, int32_t* device_status);
 /* Diagnostic of the attention's failure path, like ft_check_bounded_waits: a warp runs each kind
@@ -528,6 +619,59 @@ ft_status ft_kv_status(ft_kv* kv, int32_t* device_status);
 ft_status ft_kv_check_bounded_waits(uint32_t* expired);
 /* Message of the last failed call on kv, or "" */
 const char* ft_kv_last_error(const ft_kv* kv);
+
+/* Experts of each token from the router's logits, as ft_moe_decode and ft_moe_prefill_layer take them.  Per row x of E logits:
+ *   score = softmax(x) or sigmoid(x);  choice = score + bias (bias NULL: score);
+ *   n_group > 1: the experts stand in n_group groups of E / n_group; a group is worth the sum of its group_best (1 or 2) largest
+ *     choices (of those there are); only experts of the topk_group worthiest groups stay;
+ *   topk_ids: the k experts of the largest choice, in descending order, the lower index first among equals;
+ *   topk_w: their scores, divided by their sum if renormalise, times scale.
+ * Choices are compared as the formula gives them in 64 bits (as logits where that order is theirs: no bias, and no sums of a
+ * group), so the ids do not depend on how a kernel rounds; weights are fp32.  A logit of NaN or -inf takes its expert out, and so does a choice that
+ * is NaN or -inf (a bias); +inf counts as the largest fp32 value.  Where fewer than k experts are left, the rest of the ids are -1 (a masked route) and their
+ * weights 0.  Renormalised weights are computed against the largest selected score and do not underflow together.
+ * Errors (nothing launched): FT_ERR_ARG for T < 0, E outside [1, 4096], k outside [1, min(E, 32)], a stride below E, an unknown dtype or
+ * score, n_group that does not divide E or is above 32, topk_group outside [1, n_group], group_best other than 1 or 2, a scale
+ * that is not finite, NULL or misaligned (to an element) pointers. */
+#define FT_ROUTE_SOFTMAX 0
+#define FT_ROUTE_SIGMOID 1
+typedef struct {
+    const void* logits;     /* device [T, E], dtype */
+    const float* bias;      /* device [E] or NULL */
+    int32_t* topk_ids;      /* device [T, k] */
+    float* topk_w;          /* device [T, k] */
+    int64_t stride;         /* of the logits' rows, in elements */
+    int32_t T, E, k;
+    int32_t dtype;          /* FT_DTYPE_BF16 or FT_DTYPE_F32 */
+    int32_t score;          /* FT_ROUTE_SOFTMAX or FT_ROUTE_SIGMOID */
+    int32_t n_group, topk_group, group_best;   /* 1, 1, 1: no groups */
+    int32_t renormalise;    /* 0 or 1 */
+    float scale;
+} ft_route;
+ft_status ft_moe_route(const ft_route* call, void* stream);
+
+/* Log probabilities of n rows x of V logits, y = scale * x (scale: 1 / temperature), lse = log sum_i exp(y_i):
+ *   logp      y[token] - lse;  -inf for a token outside [0, V)
+ *   entropy   -sum_i p_i log p_i, p = exp(y - lse)
+ *   top_ids   the k largest logits' indices in descending order, the lower index first among equals; top_logp their y - lse
+ * A logit of NaN counts as -inf (probability 0, never among top_ids, which end in -1 with -inf where fewer than k are left); +inf counts
+ * as the largest fp32 value.  A row of no finite or +inf logit has logp -inf and entropy 0.  Sums are fp32; results do not depend on the run.
+ * Errors (nothing launched): FT_ERR_ARG for n < 0, V outside [1, 2^30], k outside [0, min(V, 32)], a stride below V, an unknown dtype,
+ * a scale that is not finite and > 0, logp without tokens, top_ids or top_logp NULL with k > 0, NULL or misaligned (to an
+ * element) pointers. */
+typedef struct {
+    const void* logits;     /* device [n, V], dtype */
+    const int32_t* tokens;  /* device [n], or NULL with logp NULL */
+    float* logp;            /* device [n] or NULL */
+    float* entropy;         /* device [n] or NULL */
+    int32_t* top_ids;       /* device [n, k] */
+    float* top_logp;        /* device [n, k] */
+    int64_t stride;         /* of the logits' rows, in elements */
+    int32_t n, V, k;
+    int32_t dtype;          /* FT_DTYPE_BF16 or FT_DTYPE_F32 */
+    float scale;
+} ft_logprob;
+ft_status ft_logprobs(const ft_logprob* call, void* stream);
 
 const char* ft_status_string(ft_status s);
 /* Message of the last failed call on c (static storage), or "" */

@@ -24,6 +24,7 @@ Modules:
                    brute-force history-based twin
   moe              dense fp64 MoE-layer definitions for decode and prefill
   kv               quantised key/value cache: formats, tile layout, masked attention
+  step             a step's rows and pages, head norms and rotation, router, log probabilities
   static_placement the static (prefill-time) placement baseline simulator
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test against

@@ -1,0 +1,204 @@
+"""ft_logprobs against oracle.step: indices equal, values within their roundings.
+
+With d = x - max and y = scale d: d and y are rounded once each (2^-24 |y| each, 2^-23 more for the exponential's base), the
+exponential to 2 units in the last place (2^-22), and of the sum S every term passes at most n = V / 256 + 64 additions: relative
+error of S at most s = 2^-24 (n + 4 max_i |y_i| e^y_i + 4) <= 2^-24 (n + 6).  So
+  |d logp| <= 2^-22 |y| + s + 2^-23 |log S| + 2^-149
+  |d entropy| <= s (1 + |log S|) + 2 s sum e^y |y| / S + 2^-22 sum e^y y^2 / S + 2^-22."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import step as S
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ft():
+    import __graft_entry__ as entry
+    entry.build()
+    import expert_cache_gb300
+    return expert_cache_gb300
+
+
+def run(ft, x, tokens, k, scale=1.0, stream=None, out=None, **kw):
+    n, V = x.shape
+    logp, h, ids, top = out or (torch.full((n,), float("nan"), device="cuda"), torch.full((n,), float("nan"), device="cuda"),
+                                torch.full((n, k), -9, dtype=torch.int32, device="cuda"), torch.full((n, k), float("nan"), device="cuda"))
+    ft.ft_logprobs(x, n, V, tokens, logp, h, ids, top, k, scale=scale, stream=stream, **kw)
+    return logp, h, ids, top
+
+
+def check(x, tokens, got, k, scale=1.0, rows=None):
+    torch.cuda.synchronize()
+    logp, h, ids, top = (None if t is None else t.double().cpu().numpy() for t in got)
+    tokens = tokens.cpu().numpy()
+    V = x.shape[1]
+    s = 2.0 ** -24 * (V / 256 + 70)
+    for r in range(len(x)) if rows is None else rows:
+        row = x[r].double().cpu().numpy()
+        lp, e, want, wtop = S.logprobs(row, int(tokens[r]), k, scale)
+        z = S._logits(row)
+        if np.isneginf(z.max()):
+            log_s = far = dot = sq = 0.0
+        else:
+            y = (z - z.max()) * float(np.float32(scale))
+            p = np.exp(y)
+            log_s = np.log(p.sum())
+            some = p > 0
+            dot, sq = (p[some] * -y[some]).sum() / p.sum(), (p[some] * y[some] ** 2).sum() / p.sum()
+            far = 0.0
+
+        def close(a, b):
+            if b < -S.F32_MAX * (1 + 2.0 ** -25):                  # past fp32's range such a value rounds to -inf (IEEE 754, 7.4)
+                return np.isneginf(a)
+            far = abs(b + log_s)
+            return abs(a - b) <= 2.0 ** -22 * far + s + 2.0 ** -23 * abs(log_s) + 2.0 ** -149
+        if logp is not None:
+            assert close(logp[r], lp), (r, logp[r], lp)
+        if h is not None:
+            assert abs(h[r] - e) <= s * (1 + abs(log_s)) + 2 * s * dot + 2.0 ** -22 * sq + 2.0 ** -22, (r, h[r], e)
+        if k:
+            assert ids[r].tolist() == want.tolist(), (r, ids[r], want)
+            assert all(close(a, b) for a, b in zip(top[r], wtop)), (r, top[r], wtop)
+
+
+def logits(seed, n, V, dtype=torch.float32, spread=3.0, pad=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(n, V + pad, generator=g, device="cuda") * spread).to(dtype)[:, :V]
+
+
+def tokens_of(seed, n, V):
+    return torch.from_numpy(np.random.default_rng(seed).integers(0, V, n).astype(np.int32)).cuda()
+
+
+@pytest.mark.parametrize("n,V", [(1, 1), (3, 2), (2, 7), (5, 31), (4, 64), (3, 257), (9, 1000), (2, 4095), (3, 8200), (2, 30011), (1, 65536), (3, 100003), (1, 131072),
+                                 (2, 200000), (1, 262147), (700, 500), (160, 5000), (330, 33000)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("k", [0, 1, 5, 20, 32])
+def test_sizes(ft, n, V, dtype, k):
+    k = min(k, V)
+    x, t = logits(n + V, n, V, dtype, pad=k % 3), tokens_of(V, n, V)
+    scale = [1.0, 0.7, 1.3][k % 3]
+    rows = None if n < 10 else [0, 1, n // 2, n - 1]
+    check(x, t, run(ft, x, t, k, scale), k, scale, rows)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_wherever_they_stand(ft, dtype):
+    """Rows that start at every alignment; what lies around them is not read, outputs behind the call's stay."""
+    for V in (5, 100, 1003, 20001, 70007):
+        for at in range(0, 9, 1 if V < 2000 else 3):
+            flat = torch.full((4 * (V + 1) + 32,), float("inf"), dtype=dtype, device="cuda")
+            x = flat[at:at + 3 * (V + 1)].view(3, V + 1)[:, :V]
+            x.copy_(logits(V + at, 3, V, dtype))
+            t = tokens_of(at, 3, V)
+            out = (torch.full((5,), 7.0, device="cuda"), torch.full((5,), 7.0, device="cuda"), torch.full((5, 4), -9, dtype=torch.int32, device="cuda"),
+                   torch.full((5, 4), 7.0, device="cuda"))
+            run(ft, x, t, 4, out=out)
+            check(x, t, [o[:3] for o in out], 4)
+            assert all((o[3:] == (-9 if o.dtype == torch.int32 else 7)).all() for o in out)
+
+
+@pytest.mark.parametrize("V", [40, 3000, 50000, 140000])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_orders_that_are_hard(ft, V, dtype):
+    """Ties, rising and falling rows, one value everywhere, the largest last: whatever is looked at first."""
+    n = 10
+    x = logits(V, n, V, dtype)
+    i = torch.arange(V, device="cuda", dtype=torch.float32)
+    x[0] = 1.5
+    x[1] = (i / V * 40).to(dtype)
+    x[2] = (-i / V * 40).to(dtype)
+    x[3] = (i % 7).to(dtype)
+    x[4] = torch.where(i < V - 40, 0.0, 5.0).to(dtype)
+    x[5] = torch.where(i % 13 == 3, 9.0, -9.0).to(dtype)
+    x[6] = torch.where(i == V - 1, 100.0, 0.0).to(dtype)
+    x[7] = (torch.round(x[7].float()) * 2).to(dtype)
+    x[8] = torch.where(i < V // 2, -30.0, 0.0).to(dtype)
+    x[9] = 0.0
+    x[9, 1::2] = -0.0                                              # equal
+    t = tokens_of(1, n, V)
+    for k in (1, 7, 32):
+        check(x, t, run(ft, x, t, k), k)
+
+
+@pytest.mark.parametrize("V", [33, 5000, 131072])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_what_is_masked(ft, V, dtype):
+    inf, nan, low = float("inf"), float("nan"), torch.finfo(dtype).min
+    x = logits(V, 14, V, dtype)
+    x[0] = -inf
+    x[1] = nan
+    x[2, 1:] = -inf
+    x[3, :-1] = nan
+    x[4, V // 2] = inf
+    x[5, 3], x[5, V - 2] = inf, inf
+    x[6] = low
+    x[7, 5:] = low
+    x[8] = inf
+    x[9, 20:] = -inf
+    x[10, ::2] = nan
+    x[11, :-3] = -inf
+    x[12] = -5000.0
+    x[12, 7] = -4999.0
+    x[13] = torch.finfo(dtype).max
+    x[13, 9] = inf
+    t = tokens_of(0, 14, V)
+    t[2], t[3], t[4], t[7] = 0, V - 1, V // 2, 5
+    for k, scale in ((4, 1.0), (25, 0.3), (1, 4.0)):
+        got = run(ft, x, t, k, scale)
+        assert not any(torch.isnan(g).any() for g in got)
+        check(x, t, got, k, scale)
+
+
+def test_temperatures_and_tokens(ft):
+    x = logits(3, 6, 40000)
+    t = tokens_of(0, 6, 40000)
+    t[1], t[2], t[3] = -1, 40000, -(1 << 31)                      # no tokens of the row
+    for scale in (1e-6, 1e-3, 0.05, 1.0, 20.0, 1e4, 1e30):
+        check(x, t, run(ft, x, t, 6, scale), 6, scale)
+    got = run(ft, x, t, 0)
+    assert torch.isneginf(got[0][1:4]).all() and torch.isfinite(got[0][[0, 4, 5]]).all()
+    # only what is asked for
+    full = run(ft, x, t, 5)
+    for keep in ((0,), (1,), (2, 3), (0, 1)):
+        out = [torch.full_like(f, -3) for f in full]
+        ft.ft_logprobs(x, 6, 40000, tokens=t if 0 in keep else None, logp=out[0] if 0 in keep else None, entropy=out[1] if 1 in keep else None,
+                       top_ids=out[2] if 2 in keep else None, top_logp=out[3] if 3 in keep else None, k=5 if 2 in keep else 0)
+        for i, (a, b) in enumerate(zip(out, full)):
+            assert torch.equal(a, b if i in keep else torch.full_like(b, -3))
+
+
+def test_far_rows_streams_and_graphs(ft):
+    """Rows whose offsets pass 2^32 bytes; the same bits on another stream and again; a captured call on new logits."""
+    n, V = 9000, 262144
+    x = torch.empty(n, V, dtype=torch.bfloat16, device="cuda")
+    x[::997] = logits(0, len(range(0, n, 997)), V, torch.bfloat16)
+    x[-1] = logits(1, 1, V, torch.bfloat16)[0]
+    t = tokens_of(2, n, V)
+    got = run(ft, x[997::997], t[997::997].contiguous(), 5)        # a row stride of 2^28 elements
+    check(x[997::997], t[997::997], got, 5, rows=[0, 8])
+    rest = run(ft, x[8192:], t[8192:], 5)
+    check(x[8192:], t[8192:], rest, 5, rows=[n - 1 - 8192, 997 * 9 - 8192])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    again = run(ft, x[997::997], t[997::997].contiguous(), 5, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    y, out = x[:3].clone(), [torch.empty_like(g[:3]) for g in got]
+    g = torch.cuda.CUDAGraph()
+    u = t[:3].clone()
+    with torch.cuda.graph(g):
+        run(ft, y, u, 5, out=out)
+    y.copy_(logits(9, 3, V, torch.bfloat16))
+    g.replay()
+    check(y, u, out, 5)
+
+
+def test_results_do_not_depend_on_the_run_or_the_other_rows(ft):
+    x, t = logits(4, 40, 60000, torch.bfloat16), tokens_of(4, 40, 60000)
+    a = run(ft, x, t, 9)
+    for _ in range(3):
+        assert all(torch.equal(p, q) for p, q in zip(a, run(ft, x, t, 9)))
