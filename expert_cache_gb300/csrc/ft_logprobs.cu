@@ -9,6 +9,7 @@
 // put on a list in shared memory (some dozens of 100,000), and the list is ranked at the end.  Where more reach it than
 // the list holds, its own k-th largest is the next bound and the part is read again; where that does not help (equal
 // logits by the thousand), k searches find them.  Which ones these are does not depend on any order: value, then index.
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 
@@ -18,50 +19,114 @@ namespace ft {
 
 namespace {
 
-constexpr int kLogThreads = 512, kLogWarps = kLogThreads / 32;
-constexpr int kSample = 4;             // vectors of a thread's sample
+constexpr int kLogThreads = 512, kLogWarps = kLogThreads / 32, kLogPerSm = 2;
+constexpr int kStreams = 4;            // vectors of a thread in a round, of kStreams stretches of its CTA's part
+constexpr int kRounds = 3;             // rounds under way
+constexpr int kSlot = kLogThreads * 16, kRing = kRounds * kStreams * kSlot;
 constexpr int kListed = 1024;          // entries of a CTA's list
 constexpr int kMaxCtas = 8;            // of a row
 constexpr float kNone = -INFINITY;
 
-struct Best {
+struct alignas(8) Best {
     float x;
     int i;
 };
 __device__ __forceinline__ bool better(Best a, Best b) { return a.x > b.x || (a.x == b.x && a.i < b.i); }
 
-// 16 bytes of logits.
+// Pairs of fp32 (one instruction for both).
+typedef unsigned long long Pair;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ float2 halves(Pair p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// 16 bytes of logits.  Max: the largest so far, NaN aside, in the form that costs least; Floor: where logits are cut off.
 template <typename L>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int kN = 8;
-    uint4 w;
-    __device__ __forceinline__ void none() { w = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void first(const __nv_bfloat16* p) { w.x = (w.x & 0xFFFF0000u) | *reinterpret_cast<const uint16_t*>(p); }
-    __device__ __forceinline__ void get(float (&x)[8]) const {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    typedef __nv_bfloat162 Max;
+    uint32_t w[4];
+    __device__ __forceinline__ void none() {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[2 * j] = __uint_as_float(u[j] << 16), x[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+        for (int j = 0; j < 4; ++j) w[j] = 0xFF80FF80u;
     }
-    // the largest, NaN aside
-    __device__ __forceinline__ float max() const {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(u);
-        const float2 f = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+    }
+    __device__ __forceinline__ void from_shared(uint32_t a) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+    }
+    __device__ __forceinline__ void to_shared(uint32_t a) const {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]));
+    }
+    __device__ __forceinline__ void first(const __nv_bfloat16* p) { w[0] = (w[0] & 0xFFFF0000u) | *reinterpret_cast<const uint16_t*>(p); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[2 * j] = __uint_as_float(w[j] << 16), x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+    __device__ __forceinline__ __nv_bfloat162 at(int j) const { return *reinterpret_cast<const __nv_bfloat162*>(&w[j]); }
+    __device__ __forceinline__ Max max() const { return __hmax2(__hmax2(at(0), at(1)), __hmax2(at(2), at(3))); }
+    static __device__ __forceinline__ Max larger(Max a, Max b) { return __hmax2(a, b); }
+    static __device__ __forceinline__ float value(Max m) {
+        const float2 f = __bfloat1622float2(m);
         return fmaxf(f.x, f.y);
+    }
+    // x rounded down, twice
+    static __device__ __forceinline__ Max limit(float x) { return __bfloat162bfloat162(__float2bfloat16_rd(x)); }
+    static __device__ __forceinline__ bool reaches(Max m, Max limit) { return !__hblt2(m, limit); }
+    __device__ __forceinline__ Pair get(int j, Max floor) const {
+        const __nv_bfloat162 h = __hmax2(at(j), floor);
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+        return pair(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
     }
 };
 template <>
 struct Vec<float> {
     static constexpr int kN = 4;
-    float4 w;
-    __device__ __forceinline__ void none() { w = make_float4(kNone, kNone, kNone, kNone); }
-    __device__ __forceinline__ void load(const float* p) { w = __ldg(reinterpret_cast<const float4*>(p)); }
-    __device__ __forceinline__ void first(const float* p) { w.x = *p; }
-    __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w; }
-    __device__ __forceinline__ float max() const { return fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)); }
+    typedef float Max;
+    float w[4];
+    __device__ __forceinline__ void none() {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = kNone;
+    }
+    __device__ __forceinline__ void load(const float* p) {
+        asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]) : "l"(p));
+    }
+    __device__ __forceinline__ void from_shared(uint32_t a) {
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]) : "r"(a));
+    }
+    __device__ __forceinline__ void to_shared(uint32_t a) const {
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" :: "r"(a), "f"(w[0]), "f"(w[1]), "f"(w[2]), "f"(w[3]));
+    }
+    __device__ __forceinline__ void first(const float* p) { w[0] = *p; }
+    __device__ __forceinline__ void get(float (&x)[4]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = w[j];
+    }
+    __device__ __forceinline__ Max max() const { return fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])); }
+    static __device__ __forceinline__ Max larger(Max a, Max b) { return fmaxf(a, b); }
+    static __device__ __forceinline__ float value(Max m) { return m; }
+    static __device__ __forceinline__ Max limit(float x) { return x; }
+    static __device__ __forceinline__ bool reaches(Max m, Max limit) { return !(m < limit); }
+    __device__ __forceinline__ Pair get(int j, Max floor) const { return pair(fmaxf(w[2 * j], floor), fmaxf(w[2 * j + 1], floor)); }
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -77,71 +142,96 @@ __device__ __forceinline__ unsigned ordered(float x) {
 __device__ __forceinline__ float unordered(unsigned u) { return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
 
 struct LogShared {
-    Best list[kListed];
-    Best top[kMaxCtas * kMaxK];        // the row's CTAs' k best, this one's at its rank in the first
-    float few[kLogWarps * 4];          // the sample's largest
+    alignas(16) Best list[kListed];
+    alignas(16) Best top[kMaxK];                  // this CTA's k best
+    alignas(16) Best tops[kMaxCtas * kMaxK];      // the row's CTAs' (in its first one)
+    alignas(16) float few[kLogWarps * 4];         // the sample's largest
     float red[3][kLogWarps];
-    float sum[3];                      // this CTA's largest, S and D
+    float sums[kMaxCtas][4];                      // the row's CTAs' largest, S and D (in its first one)
     Best one;
     int count;
     float bound, ref;
 };
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// A word of the same place in another CTA's shared memory.
-__device__ __forceinline__ uint32_t remote_word(const void* p, int rank) {
-    uint32_t a = (uint32_t)__cvta_generic_to_shared(p), v;
-    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.b32 %0, [r];\n\t}"
-                 : "=r"(v) : "r"(a), "r"(rank) : "memory");
-    return v;
+// A word to the same place in the shared memory of the cluster's first CTA.
+__device__ __forceinline__ void store_first(const void* p, uint32_t v) {
+    const uint32_t a = (uint32_t)__cvta_generic_to_shared(p);
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\tst.shared::cluster.b32 [r], %1;\n\t}" :: "r"(a), "r"(v) : "memory");
 }
 
-// A thread's sums against its ref (in units of log 2).
+// A thread's sums against its ref, in units of log 2: with y = c x - rc, rc = RN(c ref), S = sum 2^y and D = sum 2^y y.  (What
+// rc's rounding moves them by is taken back at the end.)  Logits below floor, whose 2^y is 0, are raised to it, so that y is a
+// number; those from limit on go out of line, as do all where c ref or the floor would be too large (plain).
+template <typename L>
 struct Sums {
-    float ref, far, top, s, d;         // far: where a logit needs another ref; top: the largest seen
-    __device__ __forceinline__ void start(float at, float c) {
-        ref = at;
-        far = at == kNone ? kNone : at + 100.f / c;
-        s = d = 0.f;
-    }
-    template <int N>
-    __device__ __forceinline__ void add(const float (&x)[N], float c) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float y = fmaxf((x[j] - ref) * c, -200.f), e = exp2_fast(y);       // -200: what adds nothing; NaN too
-            s += e;
-            d = fmaf(e, y, d);
-        }
-    }
-    // The sums against another ref.
-    __device__ __forceinline__ void move(float to, float c) {
-        if (s > 0.f) {
-            const float y = fmaxf((ref - to) * c, -1e30f), f = exp2_fast(y);
-            d = f > 0.f ? f * fmaf(y, s, d) : 0.f;
-            s *= f;
-        }
+    typedef typename Vec<L>::Max Max;
+    float ref, far, rc;                // far: a logit above it needs another ref
+    bool plain;
+    Max top, floor, limit;             // top: the largest seen
+    Pair s, d;
+
+    __device__ __forceinline__ void against(float to, float bound, float c) {
         ref = to;
+        far = to == kNone ? kNone : to + 100.f / c;
+        plain = !(fabsf(to) * c < 0x1p60f && to - 200.f / c > -1e38f);
+        rc = plain ? 0.f : to * c;
+        floor = Vec<L>::limit(to - 200.f / c);
+        limit = Vec<L>::limit(plain ? kNone : fminf(bound, far));
+    }
+    __device__ __forceinline__ void add(const Vec<L>& v, float c) {
+        const Pair c2 = pair(c, c), r2 = pair(-rc, -rc);
+#pragma unroll
+        for (int j = 0; j < Vec<L>::kN / 2; ++j) {
+            const Pair y = fma2(v.get(j, floor), c2, r2);
+            const float2 f = halves(y);
+            const Pair e = pair(exp2_fast(f.x), exp2_fast(f.y));
+            s = add2(s, e);
+            d = fma2(e, y, d);
+        }
+    }
+    // Both sums against `to` exactly.
+    __device__ __forceinline__ float2 moved(float to, float c) const {
+        const float2 a = halves(s), b = halves(d);
+        const float sum = a.x + a.y, dot = b.x + b.y;
+        if (!(sum > 0.f)) return make_float2(0.f, 0.f);
+        const float off = plain ? 0.f : fmaf(ref, c, -rc);                       // y is too large by this much
+        const float y = fmaxf((ref - to) * c, -1e30f) - off, f = exp2_fast(y);
+        return make_float2(f * sum, f > 0.f ? f * fmaf(y, sum, dot) : 0.f);
     }
 };
 
-// A vector with a logit far above a thread's ref (out of line, by value: rare, and the sums stay in registers).
+// A vector with a logit far above a thread's ref, or of a thread whose ref is too large (out of line, by value: rare, and
+// the sums stay in registers).
 template <typename L>
-__device__ __noinline__ Sums add_far(Sums a, Vec<L> v, float most, float c) {
-    const float to = fminf(most, FLT_MAX);
-    if (to > a.ref) {
-        a.move(to, c);
-        a.far = to + 100.f / c;
+__device__ __noinline__ Sums<L> add_far(Sums<L> a, Vec<L> v, float bound, float c) {
+    float most = Vec<L>::value(v.max());
+    most = most == most ? fminf(most, FLT_MAX) : kNone;
+    if (most > a.far) {
+        const float2 m = a.moved(most, c);
+        a.against(most, bound, c);
+        const float off = a.plain ? 0.f : fmaf(a.ref, c, -a.rc), f = exp2_fast(off);
+        a.s = pair(f * m.x, 0.f);
+        a.d = pair(f * fmaf(off, m.x, m.y), 0.f);
+    }
+    if (!a.plain) {
+        a.add(v, c);
+        return a;
     }
     float x[Vec<L>::kN];
     v.get(x);
+    float2 s = halves(a.s), d = halves(a.d);
 #pragma unroll
-    for (int j = 0; j < Vec<L>::kN; ++j) x[j] = x[j] == x[j] ? fminf(x[j], FLT_MAX) : kNone;
-    a.add(x, c);
+    for (int j = 0; j < Vec<L>::kN; ++j) {
+        const float y = fmaxf((fminf(x[j], FLT_MAX) - a.ref) * c, -200.f), e = exp2_fast(x[j] == x[j] ? y : -200.f);
+        s.x += e;
+        d.x = fmaf(e, y, d.x);
+    }
+    a.s = pair(s.x, s.y);
+    a.d = pair(d.x, d.y);
     return a;
 }
 
+// Puts what reaches the bound on the list.
 template <typename L>
 __device__ __forceinline__ void put_on_list(LogShared& sm, const Vec<L>& v, int index, float bound) {
     float x[Vec<L>::kN];
@@ -155,52 +245,105 @@ __device__ __forceinline__ void put_on_list(LogShared& sm, const Vec<L>& v, int 
     }
 }
 
-template <typename L, bool kTop>
-__device__ __forceinline__ void take(LogShared& sm, Sums& a, const Vec<L>& v, int index, float bound, float c) {
-    const float most = v.max();
-    a.top = fmaxf(a.top, most);
-    if (most > a.far) {
-        a = add_far(a, v, most, c);
-    } else {
-        float x[Vec<L>::kN];
-        v.get(x);
-        a.add(x, c);
+template <typename L, bool kTop, typename I>
+__device__ __forceinline__ void take(LogShared& sm, Sums<L>& a, const Vec<L>& v, I index, float bound, float c) {
+    const typename Vec<L>::Max most = v.max();
+    a.top = Vec<L>::larger(a.top, most);
+    if (Vec<L>::reaches(most, a.limit)) {
+        if (kTop) put_on_list(sm, v, index(), bound);
+        if (a.plain || Vec<L>::value(most) > a.far) {
+            a = add_far(a, v, bound, c);
+            return;
+        }
     }
-    if (kTop && most >= bound) put_on_list(sm, v, index, bound);
+    a.add(v, c);
 }
 
-// A CTA's part of a row: vectors lo .. hi, and for the first one the elements before and behind the row's vectors.
+// A CTA's part of a row: the row's vectors from lo on, `steps` for every thread and one more for the first `more`; for the
+// row's first CTA also the elements before and behind its vectors.
 template <typename L>
 struct Part {
     const L* row;
-    int head, lo, hi, steps, V, rest;  // rest: elements outside the vectors (rank 0)
+    int head, lo, steps, more, V, rest;
     __device__ __forceinline__ Part(const L* r, int V_, int rank, int ctas) : row(r), V(V_) {
         constexpr int kN = Vec<L>::kN;
         head = min((int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(L), V);
         const int n = (V - head) / kN;
         lo = (int)((long long)n * rank / ctas);
-        hi = (int)((long long)n * (rank + 1) / ctas);
-        steps = (hi - lo + kLogThreads - 1) / kLogThreads;
+        const int own = (int)((long long)n * (rank + 1) / ctas) - lo;
+        steps = own / kLogThreads;
+        more = own % kLogThreads;
         rest = rank == 0 ? V - n * kN : 0;
     }
-    __device__ __forceinline__ int index(int vec) const { return head + vec * Vec<L>::kN; }
-    // The it-th vector of this thread; false (and no logits) past the end.
-    __device__ __forceinline__ bool load(Vec<L>& v, int it, int& at) const {
-        const int vec = lo + it * kLogThreads + (int)threadIdx.x;
-        at = index(vec);
-        if (vec < hi) {
-            v.load(row + at);
-            return true;
-        }
+    __device__ __forceinline__ int index(int it) const { return head + (lo + it * kLogThreads + (int)threadIdx.x) * Vec<L>::kN; }
+    __device__ __forceinline__ void load(Vec<L>& v, int it) const { v.load(row + index(it)); }
+    // Those that not every thread has (no logits for the others).
+    __device__ __forceinline__ void load_more(Vec<L>& v) const {
         v.none();
-        return false;
+        if ((int)threadIdx.x < more) load(v, steps);
     }
-    __device__ __forceinline__ bool load_rest(Vec<L>& v, int& at) const {
+    __device__ __forceinline__ int rest_index() const { return (int)threadIdx.x < head ? threadIdx.x : V - rest + threadIdx.x; }
+    __device__ __forceinline__ void load_rest(Vec<L>& v) const {
         v.none();
-        if ((int)threadIdx.x >= rest) return false;
-        at = (int)threadIdx.x < head ? threadIdx.x : V - rest + threadIdx.x;
-        v.first(row + at);
-        return true;
+        if ((int)threadIdx.x < rest) v.first(row + rest_index());
+    }
+    // f(vector, index of its first logit) for everything.
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+        Vec<L> v;
+        for (int it = 0; it < steps; ++it) {
+            load(v, it);
+            f(v, index(it));
+        }
+        load_more(v);
+        f(v, index(steps));
+        load_rest(v);
+        f(v, rest_index());
+    }
+};
+
+// A thread's vectors on their way through its own slots of shared memory, kRounds rounds of kStreams.  Round i < full has
+// the i-th vector of each of kStreams stretches of the part, so the first round is a sample of all of it; one more
+// round has what is left.  Nobody else reads a thread's slots, so its own wait for its copies is all there is to wait for.
+template <typename L>
+struct Ring {
+    const Part<L>& p;
+    uint32_t slots;
+    int full, rounds;
+    __device__ __forceinline__ Ring(const Part<L>& part, const void* smem) : p(part) {
+        slots = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+        full = p.steps / kStreams;
+        rounds = full + (p.steps % kStreams || p.more ? 1 : 0);
+    }
+    __device__ __forceinline__ int step(int round, int j) const { return round < full ? j * full + round : kStreams * full + j; }
+    __device__ __forceinline__ void issue(int round, uint32_t at) const {
+        if (round < full) {
+            const L* from = p.row + p.index(round);
+            const size_t stretch = (size_t)full * kLogThreads * Vec<L>::kN;
+#pragma unroll
+            for (int j = 0; j < kStreams; ++j)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slots + at + j * kSlot), "l"(from + j * stretch) : "memory");
+        } else if (round < rounds) {
+#pragma unroll
+            for (int j = 0; j < kStreams; ++j) {
+                const int it = kStreams * full + j;
+                if (it < p.steps || (it == p.steps && (int)threadIdx.x < p.more)) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slots + at + j * kSlot), "l"(p.row + p.index(it)) : "memory");
+                } else {
+                    Vec<L> v;
+                    v.none();
+                    v.to_shared(slots + at + j * kSlot);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Round i's copies are there once only those of the kRounds - 1 issued behind it are not.
+    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" :: "n"(kRounds - 1) : "memory"); }
+    __device__ __forceinline__ Vec<L> get(uint32_t at, int j) const {
+        Vec<L> v;
+        v.from_shared(slots + at + j * kSlot);
+        return v;
     }
 };
 
@@ -208,12 +351,7 @@ struct Part {
 template <typename L>
 __device__ void collect(LogShared& sm, const Part<L>& p) {
     const float bound = sm.bound;
-    Vec<L> v;
-    int at;
-    for (int it = -1; it < p.steps; ++it) {
-        if (!(it < 0 ? p.load_rest(v, at) : p.load(v, it, at))) continue;
-        put_on_list(sm, v, at, bound);
-    }
+    p.each([&](const Vec<L>& v, int index) { put_on_list(sm, v, index, bound); });
 }
 
 // The k best of the list's n entries, in order, to out (entries without one: -inf).
@@ -223,7 +361,13 @@ __device__ __forceinline__ void rank_list(const Best* list, int n, int k, Best* 
     for (int e = threadIdx.x; e < n; e += kLogThreads) {
         const Best mine = list[e];
         int before = 0;
-        for (int i = 0; i < n; ++i) before += better(list[i], mine) || (list[i].x == mine.x && list[i].i == mine.i && i < e);   // several may be none
+#pragma unroll 4
+        for (int i = 0; i < n; i += 2) {                           // pairs of entries; several may be none
+            const float4 q = *reinterpret_cast<const float4*>(list + i);
+            const Best a{q.x, __float_as_int(q.y)}, b{q.z, __float_as_int(q.w)};
+            before += better(a, mine) || (a.x == mine.x && a.i == mine.i && i < e);
+            before += i + 1 < n && (better(b, mine) || (b.x == mine.x && b.i == mine.i && i + 1 < e));
+        }
         if (before < k) out[before] = mine;
     }
 }
@@ -234,18 +378,15 @@ __device__ void search(LogShared& sm, const Part<L>& p, int k, Best* out) {
     Best last{INFINITY, -1};
     for (int j = 0; j < k; ++j) {
         Best b{kNone, 0x7FFFFFFF};
-        Vec<L> v;
-        int at;
-        for (int it = -1; it < p.steps; ++it) {
-            if (!(it < 0 ? p.load_rest(v, at) : p.load(v, it, at))) continue;
+        p.each([&](const Vec<L>& v, int index) {
             float x[Vec<L>::kN];
             v.get(x);
 #pragma unroll
             for (int i = 0; i < Vec<L>::kN; ++i) {
-                const Best e{fminf(x[i], FLT_MAX), at + i};
+                const Best e{fminf(x[i], FLT_MAX), index + i};
                 if (x[i] > kNone && better(last, e) && better(e, b)) b = e;
             }
-        }
+        });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const Best e{__shfl_xor_sync(0xffffffffu, b.x, o), __shfl_xor_sync(0xffffffffu, b.i, o)};
@@ -266,9 +407,10 @@ __device__ void search(LogShared& sm, const Part<L>& p, int k, Best* out) {
 }
 
 template <typename L, bool kTop>
-__global__ void __launch_bounds__(kLogThreads, 2) logprobs_kernel(const ft_logprob c, int ctas) {
+__global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const ft_logprob c, int ctas) {
     __shared__ LogShared sm;
     pdl_wait_and_release();
+    if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");      // waited for before the first remote store
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long r = blockIdx.x / ctas;
     const int rank = blockIdx.x % ctas;
@@ -276,13 +418,12 @@ __global__ void __launch_bounds__(kLogThreads, 2) logprobs_kernel(const ft_logpr
     const Part<L> p(row, c.V, rank, ctas);
     const float c2 = fminf(c.scale * 1.4426950408889634f, FLT_MAX);
 
-    // the sample
-    Vec<L> v[kSample], extra;
-    int at[kSample], extra_at = 0;
-    const int stride = max(p.steps / kSample, 1);
+    extern __shared__ __align__(16) uint8_t log_ring[];
+    const Ring<L> ring(p, log_ring);
 #pragma unroll
-    for (int i = 0; i < kSample; ++i) p.load(v[i], i * stride, at[i]);
-    const bool has_extra = p.load_rest(extra, extra_at);
+    for (int i = 0; i < kRounds; ++i) ring.issue(i, i * kStreams * kSlot);
+    Vec<L> rest;
+    p.load_rest(rest);
     float asked = kNone;                                         // the given token's logit
     if (rank == 0 && threadIdx.x == 0 && c.logp) {
         const int t = c.tokens[r];
@@ -291,9 +432,14 @@ __global__ void __launch_bounds__(kLogThreads, 2) logprobs_kernel(const ft_logpr
             asked = asked == asked ? fminf(asked, FLT_MAX) : kNone;
         }
     }
-    float most = v[0].max();
+    // the sample
+    ring.wait();
+    typename Vec<L>::Max largest = Vec<L>::limit(kNone);
+    if (ring.rounds) {
 #pragma unroll
-    for (int i = 1; i < kSample; ++i) most = fmaxf(most, v[i].max());
+        for (int j = 0; j < kStreams; ++j) largest = Vec<L>::larger(largest, ring.get(0, j).max());
+    }
+    float most = Vec<L>::value(largest);
     most = most == most ? fminf(most, FLT_MAX) : kNone;
     // the warp's four largest
     unsigned key = ordered(most);
@@ -309,10 +455,12 @@ __global__ void __launch_bounds__(kLogThreads, 2) logprobs_kernel(const ft_logpr
         if (threadIdx.x < kLogWarps * 4) {
             const float mine = sm.few[threadIdx.x];
             int before = 0;
-#pragma unroll 16
-            for (int i = 0; i < kLogWarps * 4; ++i) {
-                const float x = sm.few[i];
-                before += x > mine || (x == mine && i < (int)threadIdx.x);
+#pragma unroll
+            for (int i = 0; i < kLogWarps * 4; i += 4) {
+                const float4 x = *reinterpret_cast<const float4*>(sm.few + i);
+                const int t = threadIdx.x;
+                before += (x.x > mine || (x.x == mine && i < t)) + (x.y > mine || (x.y == mine && i + 1 < t)) +
+                          (x.z > mine || (x.z == mine && i + 2 < t)) + (x.w > mine || (x.w == mine && i + 3 < t));
             }
             if (before == c.k - 1) sm.bound = mine;
             if (before == 0) sm.ref = mine;
@@ -324,51 +472,47 @@ __global__ void __launch_bounds__(kLogThreads, 2) logprobs_kernel(const ft_logpr
     }
     __syncthreads();
 
-    const float bound = kTop ? sm.bound : 0.f;
-    Sums a;
-    a.start(sm.ref, c2);
-    a.top = kNone;
+    const float bound = kTop ? sm.bound : INFINITY;
+    Sums<L> a;
+    a.s = a.d = 0;
+    a.top = Vec<L>::limit(kNone);
+    a.against(sm.ref, bound, c2);
+    if (p.rest) take<L, kTop>(sm, a, rest, [&] { return p.rest_index(); }, bound, c2);
+    uint32_t slot = 0;
+    for (int i = 0; i < ring.rounds; ++i) {
+        ring.wait();
 #pragma unroll
-    for (int i = 0; i < kSample; ++i)
-        if (i < p.steps) take<L, kTop>(sm, a, v[i], at[i], bound, c2);
-    if (has_extra) take<L, kTop>(sm, a, extra, extra_at, bound, c2);
-    // the rest of the part
-    for (int i = 0; i < kSample; ++i) {
-        const int end = i == kSample - 1 ? p.steps : min((i + 1) * stride, p.steps);
-        for (int it = i * stride + 1; it < end; it += kSample) {
-#pragma unroll
-            for (int j = 0; j < kSample; ++j) {
-                if (it + j < end) p.load(v[j], it + j, at[j]);
-                else v[j].none();
-            }
-#pragma unroll
-            for (int j = 0; j < kSample; ++j)
-                if (it + j < end) take<L, kTop>(sm, a, v[j], at[j], bound, c2);
-        }
+        for (int j = 0; j < kStreams; ++j) take<L, kTop>(sm, a, ring.get(slot, j), [&] { return p.index(ring.step(i, j)); }, bound, c2);
+        ring.issue(i + kRounds, slot);
+        slot = slot == kRing - kStreams * kSlot ? 0 : slot + kStreams * kSlot;
     }
-    a.top = a.top == a.top ? fminf(a.top, FLT_MAX) : kNone;
+    float m = Vec<L>::value(a.top);
+    m = m == m ? fminf(m, FLT_MAX) : kNone;
 
     // the CTA's sums against its largest
-    float m = unordered(__reduce_max_sync(0xffffffffu, ordered(a.top)));
+    m = unordered(__reduce_max_sync(0xffffffffu, ordered(m)));
     if (lane == 0) sm.red[0][warp] = m;
     __syncthreads();
     m = sm.red[0][0];
 #pragma unroll
     for (int w = 1; w < kLogWarps; ++w) m = fmaxf(m, sm.red[0][w]);
-    a.move(m, c2);
+    float2 sums = a.moved(m, c2);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
-        a.d += __shfl_xor_sync(0xffffffffu, a.d, o);
+        sums.x += __shfl_xor_sync(0xffffffffu, sums.x, o);
+        sums.y += __shfl_xor_sync(0xffffffffu, sums.y, o);
     }
-    if (lane == 0) sm.red[1][warp] = a.s, sm.red[2][warp] = a.d;
+    if (lane == 0) sm.red[1][warp] = sums.x, sm.red[2][warp] = sums.y;
     __syncthreads();
-    if (threadIdx.x < 3) {
-        float x = sm.red[threadIdx.x][0];
-        for (int w = 1; w < kLogWarps; ++w) x = threadIdx.x ? x + sm.red[threadIdx.x][w] : fmaxf(x, sm.red[0][w]);
-        sm.sum[threadIdx.x] = x;
+    if (warp == 0) {
+        float x = lane < kLogWarps ? sm.red[1][lane] : 0.f, y = lane < kLogWarps ? sm.red[2][lane] : 0.f;
+#pragma unroll
+        for (int o = kLogWarps / 2; o > 0; o >>= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, o);
+            y += __shfl_xor_sync(0xffffffffu, y, o);
+        }
+        sums = make_float2(x, y);
     }
-
     if (kTop) {
         int n = sm.count;
         while (n > kListed) {
@@ -388,49 +532,49 @@ __global__ void __launch_bounds__(kLogThreads, 2) logprobs_kernel(const ft_logpr
         else rank_list(sm.list, n, c.k, sm.top);
     }
 
+    __syncthreads();
     if (ctas > 1) {
-        cluster_sync();
-        if (rank == 0) {
-            // the other CTAs' best behind this one's, and all of them on the list
-            for (int e = threadIdx.x; kTop && e < ctas * c.k; e += kLogThreads) {
-                const int from = e / c.k;
-                const Best* b = &sm.top[e % c.k];
-                sm.list[e] = Best{__uint_as_float(remote_word(&b->x, from)), (int)remote_word(&b->i, from)};
-            }
-            if (threadIdx.x == 0) {
-                Sums all;
-                all.s = all.d = 0.f;
-                float to = sm.sum[0];
-                for (int q = 1; q < ctas; ++q) to = fmaxf(to, __uint_as_float(remote_word(&sm.sum[0], q)));
-                for (int q = 0; q < ctas; ++q) {
-                    Sums one;
-                    one.ref = __uint_as_float(remote_word(&sm.sum[0], q));
-                    one.s = __uint_as_float(remote_word(&sm.sum[1], q));
-                    one.d = __uint_as_float(remote_word(&sm.sum[2], q));
-                    one.move(to, c2);
-                    all.s += one.s;
-                    all.d += one.d;
-                }
-                sm.red[0][0] = to;
-                sm.red[1][0] = all.s;
-                sm.red[2][0] = all.d;
-            }
+        // what each CTA found, to the first one
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        if (kTop && (int)threadIdx.x < c.k) {
+            const Best b = sm.top[threadIdx.x];
+            store_first(&sm.tops[rank * c.k + threadIdx.x].x, __float_as_uint(b.x));
+            store_first(&sm.tops[rank * c.k + threadIdx.x].i, (uint32_t)b.i);
         }
-        cluster_sync();
+        if (threadIdx.x == 0) {
+            store_first(&sm.sums[rank][0], __float_as_uint(m));
+            store_first(&sm.sums[rank][1], __float_as_uint(sums.x));
+            store_first(&sm.sums[rank][2], __float_as_uint(sums.y));
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (rank) return;
         if (kTop) {
-            rank_list(sm.list, ctas * c.k, c.k, sm.top);
+            rank_list(sm.tops, ctas * c.k, c.k, sm.top);
+            __syncthreads();
         }
-    } else if (threadIdx.x == 0) {
-        for (int i = 0; i < 3; ++i) sm.red[i][0] = sm.sum[i];
+        if (warp == 0) {
+            const float own = lane < ctas ? sm.sums[lane][0] : kNone;
+            sums = lane < ctas ? make_float2(sm.sums[lane][1], sm.sums[lane][2]) : make_float2(0.f, 0.f);
+            m = unordered(__reduce_max_sync(0xffffffffu, ordered(own)));
+            if (sums.x > 0.f) {
+                const float y = fmaxf((own - m) * c2, -1e30f), f = exp2_fast(y);
+                sums = make_float2(f * sums.x, f > 0.f ? f * fmaf(y, sums.x, sums.y) : 0.f);
+            }
+#pragma unroll
+            for (int o = kMaxCtas / 2; o > 0; o >>= 1) {
+                sums.x += __shfl_xor_sync(0xffffffffu, sums.x, o);
+                sums.y += __shfl_xor_sync(0xffffffffu, sums.y, o);
+            }
+        }
     }
-    __syncthreads();
-    m = sm.red[0][0];
+    if (warp) return;                                            // k is at most a warp's threads
+    sums.x = __shfl_sync(0xffffffffu, sums.x, 0);
     const bool none = m == kNone;
-    const float log_sum = none ? 0.f : logf(sm.red[1][0]);
+    const float log_sum = none ? 0.f : logf(sums.x);
     if (threadIdx.x == 0) {
         if (c.logp) c.logp[r] = asked == kNone ? kNone : (asked - m) * c.scale - log_sum;
-        if (c.entropy) c.entropy[r] = none ? 0.f : fmaxf(log_sum - sm.red[2][0] / sm.red[1][0] * 0.6931471805599453f, 0.f);
+        if (c.entropy) c.entropy[r] = none ? 0.f : fmaxf(log_sum - sums.y / sums.x * 0.6931471805599453f, 0.f);
     }
     if (kTop && (int)threadIdx.x < c.k) {
         const Best b = sm.top[threadIdx.x];
@@ -443,9 +587,19 @@ bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 template <typename L, bool kTop>
 cudaError_t launch(const ft_logprob& c, int ctas, cudaStream_t s) {
+    static std::atomic<bool> done[kMaxDevices];                  // the kernel's attribute is set on this device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices || !done[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(logprobs_kernel<L, kTop>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)c.n * ctas);
     cfg.blockDim = dim3(kLogThreads);
+    cfg.dynamicSmemBytes = kRing;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -474,10 +628,10 @@ extern "C" ft_status ft_logprobs(const ft_logprob* call, void* stream) {
         return FT_ERR_ARG;
     if (!aligned(c.tokens, 4) || !aligned(c.logp, 4) || !aligned(c.entropy, 4) || !aligned(c.top_ids, 4) || !aligned(c.top_logp, 4)) return FT_ERR_ARG;
     NvtxRange r("ft_logprobs");
-    // CTAs of a row: as many as there is room for at two per SM, each with a vector or more per thread
+    // CTAs of a row: as many as there is room for, each with a vector or more per thread
     int ctas = 1;
     const long long vectors = (long long)c.V / (c.dtype == FT_DTYPE_BF16 ? 8 : 4);
-    while (ctas < kMaxCtas && 2LL * ctas * c.n <= 2LL * sm_count() && vectors > (long long)ctas * kLogThreads) ctas *= 2;
+    while (ctas < kMaxCtas && 2LL * ctas * c.n <= (long long)kLogPerSm * sm_count() && vectors > (long long)ctas * kLogThreads) ctas *= 2;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = c.dtype == FT_DTYPE_BF16 ? (c.k ? launch<__nv_bfloat16, true>(c, ctas, s) : launch<__nv_bfloat16, false>(c, ctas, s))
                                                    : (c.k ? launch<float, true>(c, ctas, s) : launch<float, false>(c, ctas, s));

@@ -147,7 +147,7 @@ def test_what_is_masked(ft, V, dtype):
     x[13, 9] = inf
     t = tokens_of(0, 14, V)
     t[2], t[3], t[4], t[7] = 0, V - 1, V // 2, 5
-    for k, scale in ((4, 1.0), (25, 0.3), (1, 4.0)):
+    for k, scale in ((4, 1.0), (25, 0.3), (1, 4.0), (0, 1.0), (3, 1e-37), (3, 1e-42), (0, 1e-37), (2, 1e30), (2, 3e38)):
         got = run(ft, x, t, k, scale)
         assert not any(torch.isnan(g).any() for g in got)
         check(x, t, got, k, scale)
