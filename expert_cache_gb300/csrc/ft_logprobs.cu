@@ -4,8 +4,7 @@
 // give log sum = log S and entropy = log S - D / S.  A thread's ref is a maximum of a sample of the row, so that no
 // sum has to be rescaled unless a logit lies e^69 above it; the row's own maximum is taken at the end.
 //
-// The k largest come out of the same pass.  From the sample (4 vectors of every thread, spread over the CTA's part
-// of the row and kept in registers) the k-th largest of some 64 logits is a lower bound of the row's k-th; only what reaches it is
+// The k largest come out of the same pass.  From the sample (the first 4 vectors of every thread) the k-th largest of some 64 logits is a lower bound of the row's k-th; only what reaches it is
 // put on a list in shared memory (some dozens of 100,000), and the list is ranked at the end.  Where more reach it than
 // the list holds, its own k-th largest is the next bound and the part is read again; where that does not help (equal
 // logits by the thousand), k searches find them.  Which ones these are does not depend on any order: value, then index.
@@ -20,9 +19,9 @@ namespace ft {
 namespace {
 
 constexpr int kLogThreads = 512, kLogWarps = kLogThreads / 32, kLogPerSm = 2;
-constexpr int kStreams = 4;            // vectors of a thread in a round, of kStreams stretches of its CTA's part
-constexpr int kRounds = 3;             // rounds under way
-constexpr int kSlot = kLogThreads * 16, kRing = kRounds * kStreams * kSlot;
+constexpr int kVectors = 4;            // vectors of a thread in a round
+constexpr int kRounds = 2;             // rounds under way
+constexpr int kSlot = kLogThreads * 16, kRing = kRounds * kVectors * kSlot;
 constexpr int kListed = 1024;          // entries of a CTA's list
 constexpr int kMaxCtas = 8;            // of a row
 constexpr float kNone = -INFINITY;
@@ -167,7 +166,8 @@ struct Sums {
     typedef typename Vec<L>::Max Max;
     float ref, far, rc;                // far: a logit above it needs another ref
     bool plain;
-    Max top, floor, limit;             // top: the largest seen
+    Max floor, limit;
+    float top;                         // the largest seen: the sample's, or one that reached the limit
     Pair s, d;
 
     __device__ __forceinline__ void against(float to, float bound, float c) {
@@ -247,11 +247,12 @@ __device__ __forceinline__ void put_on_list(LogShared& sm, const Vec<L>& v, int 
 
 template <typename L, bool kTop, typename I>
 __device__ __forceinline__ void take(LogShared& sm, Sums<L>& a, const Vec<L>& v, I index, float bound, float c) {
-    const typename Vec<L>::Max most = v.max();
-    a.top = Vec<L>::larger(a.top, most);
-    if (Vec<L>::reaches(most, a.limit)) {
+    const typename Vec<L>::Max reach = v.max();
+    if (Vec<L>::reaches(reach, a.limit)) {
+        const float most = Vec<L>::value(reach);
+        a.top = fmaxf(a.top, fminf(most == most ? most : kNone, FLT_MAX));
         if (kTop) put_on_list(sm, v, index(), bound);
-        if (a.plain || Vec<L>::value(most) > a.far) {
+        if (a.plain || most > a.far) {
             a = add_far(a, v, bound, c);
             return;
         }
@@ -265,12 +266,12 @@ template <typename L>
 struct Part {
     const L* row;
     int head, lo, steps, more, V, rest;
-    __device__ __forceinline__ Part(const L* r, int V_, int rank, int ctas) : row(r), V(V_) {
+    __device__ __forceinline__ Part(const L* r, int V_, int rank, int shift) : row(r), V(V_) {       // of 1 << shift CTAs
         constexpr int kN = Vec<L>::kN;
         head = min((int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(L), V);
         const int n = (V - head) / kN;
-        lo = (int)((long long)n * rank / ctas);
-        const int own = (int)((long long)n * (rank + 1) / ctas) - lo;
+        lo = (int)((long long)n * rank >> shift);
+        const int own = (int)((long long)n * (rank + 1) >> shift) - lo;
         steps = own / kLogThreads;
         more = own % kLogThreads;
         rest = rank == 0 ? V - n * kN : 0;
@@ -302,9 +303,8 @@ struct Part {
     }
 };
 
-// A thread's vectors on their way through its own slots of shared memory, kRounds rounds of kStreams.  Round i < full has
-// the i-th vector of each of kStreams stretches of the part, so the first round is a sample of all of it; one more
-// round has what is left.  Nobody else reads a thread's slots, so its own wait for its copies is all there is to wait for.
+// A thread's vectors on their way through its own slots of shared memory, kRounds rounds of kVectors; the last round may
+// have fewer.  Nobody else reads a thread's slots, so its own wait for its copies is all there is to wait for.
 template <typename L>
 struct Ring {
     const Part<L>& p;
@@ -312,21 +312,19 @@ struct Ring {
     int full, rounds;
     __device__ __forceinline__ Ring(const Part<L>& part, const void* smem) : p(part) {
         slots = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
-        full = p.steps / kStreams;
-        rounds = full + (p.steps % kStreams || p.more ? 1 : 0);
+        full = p.steps / kVectors;
+        rounds = full + (p.steps % kVectors || p.more ? 1 : 0);
     }
-    __device__ __forceinline__ int step(int round, int j) const { return round < full ? j * full + round : kStreams * full + j; }
     __device__ __forceinline__ void issue(int round, uint32_t at) const {
         if (round < full) {
-            const L* from = p.row + p.index(round);
-            const size_t stretch = (size_t)full * kLogThreads * Vec<L>::kN;
+            const L* from = p.row + p.index(round * kVectors);
 #pragma unroll
-            for (int j = 0; j < kStreams; ++j)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slots + at + j * kSlot), "l"(from + j * stretch) : "memory");
+            for (int j = 0; j < kVectors; ++j)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slots + at + j * kSlot), "l"(from + j * kLogThreads * Vec<L>::kN) : "memory");
         } else if (round < rounds) {
 #pragma unroll
-            for (int j = 0; j < kStreams; ++j) {
-                const int it = kStreams * full + j;
+            for (int j = 0; j < kVectors; ++j) {
+                const int it = round * kVectors + j;
                 if (it < p.steps || (it == p.steps && (int)threadIdx.x < p.more)) {
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slots + at + j * kSlot), "l"(p.row + p.index(it)) : "memory");
                 } else {
@@ -337,6 +335,10 @@ struct Ring {
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void start() const {
+#pragma unroll
+        for (int i = 0; i < kRounds; ++i) issue(i, i * kVectors * kSlot);
     }
     // Round i's copies are there once only those of the kRounds - 1 issued behind it are not.
     __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" :: "n"(kRounds - 1) : "memory"); }
@@ -407,41 +409,34 @@ __device__ void search(LogShared& sm, const Part<L>& p, int k, Best* out) {
 }
 
 template <typename L, bool kTop>
-__global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const ft_logprob c, int ctas) {
+__global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const ft_logprob c, int shift) {
     __shared__ LogShared sm;
-    pdl_wait_and_release();
-    if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");      // waited for before the first remote store
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long r = blockIdx.x / ctas;
-    const int rank = blockIdx.x % ctas;
-    const L* row = static_cast<const L*>(c.logits) + r * c.stride;
-    const Part<L> p(row, c.V, rank, ctas);
-    const float c2 = fminf(c.scale * 1.4426950408889634f, FLT_MAX);
-
     extern __shared__ __align__(16) uint8_t log_ring[];
+    pdl_wait_and_release();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ctas = 1 << shift, rank = blockIdx.x & (ctas - 1);
+    if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");      // waited for before the first remote store
+    const float c2 = fminf(c.scale * 1.4426950408889634f, FLT_MAX);
+    const long long r = blockIdx.x >> shift;
+    const Part<L> p(static_cast<const L*>(c.logits) + r * c.stride, c.V, rank, shift);
     const Ring<L> ring(p, log_ring);
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) ring.issue(i, i * kStreams * kSlot);
+    ring.start();
     Vec<L> rest;
     p.load_rest(rest);
-    float asked = kNone;                                         // the given token's logit
+    float asked = kNone;                                     // the given token's logit
     if (rank == 0 && threadIdx.x == 0 && c.logp) {
-        const int t = c.tokens[r];
-        if (t >= 0 && t < c.V) {
-            asked = (float)row[t];
-            asked = asked == asked ? fminf(asked, FLT_MAX) : kNone;
-        }
+        const int token = c.tokens[r];
+        if (token >= 0 && token < c.V) asked = (float)p.row[token];
     }
-    // the sample
+
+    // the sample: its largest, and the warps' four largest
     ring.wait();
     typename Vec<L>::Max largest = Vec<L>::limit(kNone);
     if (ring.rounds) {
 #pragma unroll
-        for (int j = 0; j < kStreams; ++j) largest = Vec<L>::larger(largest, ring.get(0, j).max());
+        for (int j = 0; j < kVectors; ++j) largest = Vec<L>::larger(largest, ring.get(0, j).max());
     }
     float most = Vec<L>::value(largest);
     most = most == most ? fminf(most, FLT_MAX) : kNone;
-    // the warp's four largest
     unsigned key = ordered(most);
 #pragma unroll
     for (int i = 0; i < (kTop ? 4 : 1); ++i) {
@@ -468,29 +463,25 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
     } else if (threadIdx.x == 0) {
         float m = sm.few[0];
         for (int w = 1; w < kLogWarps; ++w) m = fmaxf(m, sm.few[4 * w]);
-        sm.ref = m;
+        sm.bound = sm.ref = m;
     }
     __syncthreads();
-
-    const float bound = kTop ? sm.bound : INFINITY;
+    const float bound = sm.bound;
     Sums<L> a;
     a.s = a.d = 0;
-    a.top = Vec<L>::limit(kNone);
+    a.top = sm.ref;
     a.against(sm.ref, bound, c2);
     if (p.rest) take<L, kTop>(sm, a, rest, [&] { return p.rest_index(); }, bound, c2);
     uint32_t slot = 0;
     for (int i = 0; i < ring.rounds; ++i) {
         ring.wait();
 #pragma unroll
-        for (int j = 0; j < kStreams; ++j) take<L, kTop>(sm, a, ring.get(slot, j), [&] { return p.index(ring.step(i, j)); }, bound, c2);
+        for (int j = 0; j < kVectors; ++j) take<L, kTop>(sm, a, ring.get(slot, j), [&] { return p.index(i * kVectors + j); }, bound, c2);
         ring.issue(i + kRounds, slot);
-        slot = slot == kRing - kStreams * kSlot ? 0 : slot + kStreams * kSlot;
+        slot = slot == kRing - kVectors * kSlot ? 0 : slot + kVectors * kSlot;
     }
-    float m = Vec<L>::value(a.top);
-    m = m == m ? fminf(m, FLT_MAX) : kNone;
-
     // the CTA's sums against its largest
-    m = unordered(__reduce_max_sync(0xffffffffu, ordered(m)));
+    float m = unordered(__reduce_max_sync(0xffffffffu, ordered(a.top)));
     if (lane == 0) sm.red[0][warp] = m;
     __syncthreads();
     m = sm.red[0][0];
@@ -503,24 +494,15 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
         sums.y += __shfl_xor_sync(0xffffffffu, sums.y, o);
     }
     if (lane == 0) sm.red[1][warp] = sums.x, sm.red[2][warp] = sums.y;
-    __syncthreads();
-    if (warp == 0) {
-        float x = lane < kLogWarps ? sm.red[1][lane] : 0.f, y = lane < kLogWarps ? sm.red[2][lane] : 0.f;
-#pragma unroll
-        for (int o = kLogWarps / 2; o > 0; o >>= 1) {
-            x += __shfl_xor_sync(0xffffffffu, x, o);
-            y += __shfl_xor_sync(0xffffffffu, y, o);
-        }
-        sums = make_float2(x, y);
-    }
     if (kTop) {
-        int n = sm.count;
+        int n = sm.count;                                    // complete since the barrier above
         while (n > kListed) {
             // the list's k-th largest bounds the row's; if it is no better than the last one, the searches
+            __syncthreads();
             rank_list(sm.list, kListed, c.k, sm.top);
             __syncthreads();
-            const float next = sm.top[c.k - 1].x;
-            if (!(next > sm.bound)) break;
+            const float next = sm.top[c.k - 1].x, last = sm.bound;
+            if (!(next > last)) break;
             __syncthreads();
             if (threadIdx.x == 0) sm.bound = next, sm.count = 0;
             __syncthreads();
@@ -531,8 +513,16 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
         if (n > kListed) search(sm, p, c.k, sm.top);
         else rank_list(sm.list, n, c.k, sm.top);
     }
-
     __syncthreads();
+    if (warp == 0) {
+        float x = lane < kLogWarps ? sm.red[1][lane] : 0.f, y = lane < kLogWarps ? sm.red[2][lane] : 0.f;
+#pragma unroll
+        for (int o = kLogWarps / 2; o > 0; o >>= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, o);
+            y += __shfl_xor_sync(0xffffffffu, y, o);
+        }
+        sums = make_float2(x, y);
+    }
     if (ctas > 1) {
         // what each CTA found, to the first one
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
@@ -568,25 +558,27 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
             }
         }
     }
-    if (warp) return;                                            // k is at most a warp's threads
-    sums.x = __shfl_sync(0xffffffffu, sums.x, 0);
-    const bool none = m == kNone;
-    const float log_sum = none ? 0.f : logf(sums.x);
-    if (threadIdx.x == 0) {
-        if (c.logp) c.logp[r] = asked == kNone ? kNone : (asked - m) * c.scale - log_sum;
-        if (c.entropy) c.entropy[r] = none ? 0.f : fmaxf(log_sum - sums.y / sums.x * 0.6931471805599453f, 0.f);
-    }
-    if (kTop && (int)threadIdx.x < c.k) {
-        const Best b = sm.top[threadIdx.x];
-        c.top_ids[r * c.k + threadIdx.x] = b.x > kNone ? b.i : -1;
-        c.top_logp[r * c.k + threadIdx.x] = b.x > kNone ? (b.x - m) * c.scale - log_sum : kNone;
+    if (warp == 0) {                                         // k is at most a warp's threads
+        sums.x = __shfl_sync(0xffffffffu, sums.x, 0);
+        const bool none = m == kNone;
+        const float log_sum = none ? 0.f : logf(sums.x);
+        if (lane == 0) {
+            const float x = asked == asked ? fminf(asked, FLT_MAX) : kNone;
+            if (c.logp) c.logp[r] = x == kNone ? kNone : (x - m) * c.scale - log_sum;
+            if (c.entropy) c.entropy[r] = none ? 0.f : fmaxf(log_sum - sums.y / sums.x * 0.6931471805599453f, 0.f);
+        }
+        if (kTop && lane < c.k) {
+            const Best b = sm.top[lane];
+            c.top_ids[r * c.k + lane] = b.x > kNone ? b.i : -1;
+            c.top_logp[r * c.k + lane] = b.x > kNone ? (b.x - m) * c.scale - log_sum : kNone;
+        }
     }
 }
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
 template <typename L, bool kTop>
-cudaError_t launch(const ft_logprob& c, int ctas, cudaStream_t s) {
+cudaError_t launch(const ft_logprob& c, int shift, cudaStream_t s) {
     static std::atomic<bool> done[kMaxDevices];                  // the kernel's attribute is set on this device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -597,7 +589,7 @@ cudaError_t launch(const ft_logprob& c, int ctas, cudaStream_t s) {
         if (dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)c.n * ctas);
+    cfg.gridDim = dim3((unsigned)c.n << shift);
     cfg.blockDim = dim3(kLogThreads);
     cfg.dynamicSmemBytes = kRing;
     cfg.stream = s;
@@ -605,11 +597,11 @@ cudaError_t launch(const ft_logprob& c, int ctas, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.x = 1 << shift;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<L, kTop>, c, ctas);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<L, kTop>, c, shift);
 }
 
 }  // namespace
@@ -629,11 +621,11 @@ extern "C" ft_status ft_logprobs(const ft_logprob* call, void* stream) {
     if (!aligned(c.tokens, 4) || !aligned(c.logp, 4) || !aligned(c.entropy, 4) || !aligned(c.top_ids, 4) || !aligned(c.top_logp, 4)) return FT_ERR_ARG;
     NvtxRange r("ft_logprobs");
     // CTAs of a row: as many as there is room for, each with a vector or more per thread
-    int ctas = 1;
+    int shift = 0;
     const long long vectors = (long long)c.V / (c.dtype == FT_DTYPE_BF16 ? 8 : 4);
-    while (ctas < kMaxCtas && 2LL * ctas * c.n <= (long long)kLogPerSm * sm_count() && vectors > (long long)ctas * kLogThreads) ctas *= 2;
+    while (1 << shift < kMaxCtas && (2LL << shift) * c.n <= (long long)kLogPerSm * sm_count() && vectors > (long long)kLogThreads << shift) ++shift;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = c.dtype == FT_DTYPE_BF16 ? (c.k ? launch<__nv_bfloat16, true>(c, ctas, s) : launch<__nv_bfloat16, false>(c, ctas, s))
-                                                   : (c.k ? launch<float, true>(c, ctas, s) : launch<float, false>(c, ctas, s));
+    const cudaError_t e = c.dtype == FT_DTYPE_BF16 ? (c.k ? launch<__nv_bfloat16, true>(c, shift, s) : launch<__nv_bfloat16, false>(c, shift, s))
+                                                   : (c.k ? launch<float, true>(c, shift, s) : launch<float, false>(c, shift, s));
     return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }
