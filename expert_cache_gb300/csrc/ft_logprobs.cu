@@ -23,6 +23,7 @@ constexpr int kVectors = 4;            // vectors of a thread in a round
 constexpr int kRounds = 2;             // rounds under way
 constexpr int kSlot = kLogThreads * 16, kRing = kRounds * kVectors * kSlot;
 constexpr int kListed = 1024;          // entries of a CTA's list
+constexpr int kHits = 64;              // vectors that a warp keeps for the list
 constexpr int kMaxCtas = 8;            // of a row
 constexpr float kNone = -INFINITY;
 
@@ -144,8 +145,10 @@ struct LogShared {
     alignas(16) Best list[kListed];
     alignas(16) Best top[kMaxK];                  // this CTA's k best
     alignas(16) Best tops[kMaxCtas * kMaxK];      // the row's CTAs' (in its first one)
-    alignas(16) float few[kLogWarps * 4];         // the sample's largest
-    float red[3][kLogWarps];
+    alignas(16) uint4 hit[kLogWarps][kHits];      // the warps' vectors that reach the bound, and where they stand
+    int hit_at[kLogWarps][kHits];
+    float few[kLogWarps * 4];                     // the sample's largest
+    float red[3][kLogWarps];                      // the warps' largest, S and D
     float sums[kMaxCtas][4];                      // the row's CTAs' largest, S and D (in its first one)
     Best one;
     int count;
@@ -245,13 +248,26 @@ __device__ __forceinline__ void put_on_list(LogShared& sm, const Vec<L>& v, int 
     }
 }
 
-template <typename L, bool kTop, typename I>
-__device__ __forceinline__ void take(LogShared& sm, Sums<L>& a, const Vec<L>& v, I index, float bound, float c) {
+// Adds a vector to a thread's sums; a whole warp calls it.  Vectors for the list are kept (hits of them so far) and looked
+// at when the warp is through: the atomic operations of the list at once cost a row of 131,072 logits a microsecond more.
+template <typename L, bool kTop>
+__device__ __forceinline__ void take(LogShared& sm, Sums<L>& a, int& hits, const Vec<L>& v, int index, float bound, float c) {
     const typename Vec<L>::Max reach = v.max();
-    if (Vec<L>::reaches(reach, a.limit)) {
-        const float most = Vec<L>::value(reach);
-        a.top = fmaxf(a.top, fminf(most == most ? most : kNone, FLT_MAX));
-        if (kTop) put_on_list(sm, v, index(), bound);
+    const bool hit = Vec<L>::reaches(reach, a.limit);
+    if (__any_sync(0xffffffffu, hit)) {
+        float most = Vec<L>::value(reach);
+        most = most == most ? most : kNone;
+        a.top = fmaxf(a.top, fminf(most, FLT_MAX));
+        if (kTop) {
+            const bool keep = most >= bound && most > kNone;
+            const unsigned kept = __ballot_sync(0xffffffffu, keep);
+            const int at = hits + __popc(kept & ((1u << (threadIdx.x & 31)) - 1));
+            if (keep && at < kHits) {
+                v.to_shared((uint32_t)__cvta_generic_to_shared(&sm.hit[threadIdx.x >> 5][at]));
+                sm.hit_at[threadIdx.x >> 5][at] = index;
+            }
+            hits += __popc(kept);
+        }
         if (a.plain || most > a.far) {
             a = add_far(a, v, bound, c);
             return;
@@ -356,21 +372,29 @@ __device__ void collect(LogShared& sm, const Part<L>& p) {
     p.each([&](const Vec<L>& v, int index) { put_on_list(sm, v, index, bound); });
 }
 
-// The k best of the list's n entries, in order, to out (entries without one: -inf).
+// How many of n things come before the one that is this thread's: `parts` neighbouring threads share one.
+template <typename F>
+__device__ __forceinline__ int count_before(int n, int parts, F before) {
+    int count = 0;
+    for (int i = threadIdx.x & (parts - 1); i < n; i += parts) count += before(i);
+    for (int o = parts >> 1; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
+    return count;
+}
+
+// The k best of the list's n entries, in order, to out (entries without one: -inf); several entries may be none.
 __device__ __forceinline__ void rank_list(const Best* list, int n, int k, Best* out) {
-    for (int j = threadIdx.x; j < k; j += kLogThreads)
-        if (j >= n) out[j] = Best{kNone, -1};
-    for (int e = threadIdx.x; e < n; e += kLogThreads) {
-        const Best mine = list[e];
-        int before = 0;
-#pragma unroll 4
-        for (int i = 0; i < n; i += 2) {                           // pairs of entries; several may be none
-            const float4 q = *reinterpret_cast<const float4*>(list + i);
-            const Best a{q.x, __float_as_int(q.y)}, b{q.z, __float_as_int(q.w)};
-            before += better(a, mine) || (a.x == mine.x && a.i == mine.i && i < e);
-            before += i + 1 < n && (better(b, mine) || (b.x == mine.x && b.i == mine.i && i + 1 < e));
-        }
-        if (before < k) out[before] = mine;
+    for (int j = n + threadIdx.x; j < k; j += kLogThreads) out[j] = Best{kNone, -1};
+    int shift = 0;                                                 // 1 << shift threads for an entry
+    while (shift < 5 && n << (shift + 1) <= kLogThreads) ++shift;
+    const int parts = 1 << shift;
+    for (int first = 0; first < n; first += kLogThreads >> shift) {
+        const int e = first + ((int)threadIdx.x >> shift);
+        const Best mine = e < n ? list[e] : Best{kNone, -1};
+        const int before = count_before(n, parts, [&](int i) {
+            const Best x = list[i];
+            return better(x, mine) || (x.x == mine.x && x.i == mine.i && i < e);
+        });
+        if (e < n && before < k && (threadIdx.x & (parts - 1)) == 0) out[before] = mine;
     }
 }
 
@@ -408,6 +432,22 @@ __device__ void search(LogShared& sm, const Part<L>& p, int k, Best* out) {
     }
 }
 
+// The sums of a warp's lanes, each against its own largest, against the largest of all; returns that.
+__device__ __forceinline__ float join(float own, float2 part, float c, float2& all) {
+    const float m = unordered(__reduce_max_sync(0xffffffffu, ordered(own)));
+    if (part.x > 0.f) {
+        const float y = fmaxf((own - m) * c, -1e30f), f = exp2_fast(y);
+        part = make_float2(f * part.x, f > 0.f ? f * fmaf(y, part.x, part.y) : 0.f);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        part.x += __shfl_xor_sync(0xffffffffu, part.x, o);
+        part.y += __shfl_xor_sync(0xffffffffu, part.y, o);
+    }
+    all = part;
+    return m;
+}
+
 template <typename L, bool kTop>
 __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const ft_logprob c, int shift) {
     __shared__ LogShared sm;
@@ -438,32 +478,20 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
     float most = Vec<L>::value(largest);
     most = most == most ? fminf(most, FLT_MAX) : kNone;
     unsigned key = ordered(most);
-#pragma unroll
-    for (int i = 0; i < (kTop ? 4 : 1); ++i) {
+    const int each = !kTop ? 1 : c.k <= 16 ? 2 : 4;              // of a warp: kLogWarps of them hold k
+    for (int i = 0; i < each; ++i) {
         const unsigned u = __reduce_max_sync(0xffffffffu, key);
-        if (lane == 0) sm.few[warp * 4 + i] = unordered(u);
+        if (lane == 0) sm.few[warp * each + i] = unordered(u);
         if (kTop && lane == __ffs(__ballot_sync(0xffffffffu, key == u)) - 1) key = ordered(kNone);
     }
     if (threadIdx.x == 0) sm.count = 0;
     __syncthreads();
-    if (kTop) {
-        if (threadIdx.x < kLogWarps * 4) {
-            const float mine = sm.few[threadIdx.x];
-            int before = 0;
-#pragma unroll
-            for (int i = 0; i < kLogWarps * 4; i += 4) {
-                const float4 x = *reinterpret_cast<const float4*>(sm.few + i);
-                const int t = threadIdx.x;
-                before += (x.x > mine || (x.x == mine && i < t)) + (x.y > mine || (x.y == mine && i + 1 < t)) +
-                          (x.z > mine || (x.z == mine && i + 2 < t)) + (x.w > mine || (x.w == mine && i + 3 < t));
-            }
-            if (before == c.k - 1) sm.bound = mine;
-            if (before == 0) sm.ref = mine;
-        }
-    } else if (threadIdx.x == 0) {
-        float m = sm.few[0];
-        for (int w = 1; w < kLogWarps; ++w) m = fmaxf(m, sm.few[4 * w]);
-        sm.bound = sm.ref = m;
+    {
+        const int n = kLogWarps * each, parts = min(kLogThreads / n, 32), mine_at = threadIdx.x / parts;
+        const float mine = mine_at < n ? sm.few[mine_at] : kNone;
+        const int before = count_before(n, parts, [&](int i) { return sm.few[i] > mine || (sm.few[i] == mine && i < mine_at); });
+        if (mine_at < n && before == 0) sm.ref = mine;
+        if (mine_at < n && before == (kTop ? c.k - 1 : 0)) sm.bound = mine;
     }
     __syncthreads();
     const float bound = sm.bound;
@@ -471,107 +499,106 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
     a.s = a.d = 0;
     a.top = sm.ref;
     a.against(sm.ref, bound, c2);
-    if (p.rest) take<L, kTop>(sm, a, rest, [&] { return p.rest_index(); }, bound, c2);
+    int hits = 0;
+    if (p.rest) take<L, kTop>(sm, a, hits, rest, p.rest_index(), bound, c2);
     uint32_t slot = 0;
     for (int i = 0; i < ring.rounds; ++i) {
         ring.wait();
 #pragma unroll
-        for (int j = 0; j < kVectors; ++j) take<L, kTop>(sm, a, ring.get(slot, j), [&] { return p.index(i * kVectors + j); }, bound, c2);
+        for (int j = 0; j < kVectors; ++j) take<L, kTop>(sm, a, hits, ring.get(slot, j), p.index(i * kVectors + j), bound, c2);
         ring.issue(i + kRounds, slot);
         slot = slot == kRing - kVectors * kSlot ? 0 : slot + kVectors * kSlot;
     }
-    // the CTA's sums against its largest
+    if (kTop) {
+        __syncwarp();
+        for (int e = lane; e < min(hits, kHits); e += 32) {
+            Vec<L> v;
+            v.from_shared((uint32_t)__cvta_generic_to_shared(&sm.hit[warp][e]));
+            put_on_list(sm, v, sm.hit_at[warp][e], bound);
+        }
+        if (lane == 0 && hits > kHits) atomicAdd(&sm.count, kListed + 1);        // not all of them: the part is read again
+    }
+
+    // the warp's sums against its largest
     float m = unordered(__reduce_max_sync(0xffffffffu, ordered(a.top)));
-    if (lane == 0) sm.red[0][warp] = m;
-    __syncthreads();
-    m = sm.red[0][0];
-#pragma unroll
-    for (int w = 1; w < kLogWarps; ++w) m = fmaxf(m, sm.red[0][w]);
     float2 sums = a.moved(m, c2);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         sums.x += __shfl_xor_sync(0xffffffffu, sums.x, o);
         sums.y += __shfl_xor_sync(0xffffffffu, sums.y, o);
     }
-    if (lane == 0) sm.red[1][warp] = sums.x, sm.red[2][warp] = sums.y;
+    if (lane == 0) sm.red[0][warp] = m, sm.red[1][warp] = sums.x, sm.red[2][warp] = sums.y;
+    __syncthreads();
     if (kTop) {
-        int n = sm.count;                                    // complete since the barrier above
-        while (n > kListed) {
-            // the list's k-th largest bounds the row's; if it is no better than the last one, the searches
+        int n = sm.count;
+        if (n > kListed) {
+            bool again = true;
+            while (again) {
+                __syncthreads();
+                if (threadIdx.x == 0) sm.count = 0;
+                __syncthreads();
+                collect(sm, p);
+                __syncthreads();
+                n = sm.count;
+                if (n <= kListed) break;
+                // the list's k-th largest bounds the row's; if it is no better than the last one, the searches
+                rank_list(sm.list, kListed, c.k, sm.top);
+                __syncthreads();
+                const float next = sm.top[c.k - 1].x;
+                again = next > sm.bound;
+                __syncthreads();
+                if (threadIdx.x == 0) sm.bound = next;
+            }
             __syncthreads();
-            rank_list(sm.list, kListed, c.k, sm.top);
-            __syncthreads();
-            const float next = sm.top[c.k - 1].x, last = sm.bound;
-            if (!(next > last)) break;
-            __syncthreads();
-            if (threadIdx.x == 0) sm.bound = next, sm.count = 0;
-            __syncthreads();
-            collect(sm, p);
-            __syncthreads();
-            n = sm.count;
         }
         if (n > kListed) search(sm, p, c.k, sm.top);
         else rank_list(sm.list, n, c.k, sm.top);
+        __syncthreads();
     }
-    __syncthreads();
     if (warp == 0) {
-        float x = lane < kLogWarps ? sm.red[1][lane] : 0.f, y = lane < kLogWarps ? sm.red[2][lane] : 0.f;
-#pragma unroll
-        for (int o = kLogWarps / 2; o > 0; o >>= 1) {
-            x += __shfl_xor_sync(0xffffffffu, x, o);
-            y += __shfl_xor_sync(0xffffffffu, y, o);
+        m = join(lane < kLogWarps ? sm.red[0][lane] : kNone, lane < kLogWarps ? make_float2(sm.red[1][lane], sm.red[2][lane]) : make_float2(0.f, 0.f),
+                 c2, sums);
+        if (ctas > 1) {
+            // what each CTA found, to the first one
+            asm volatile("barrier.cluster.wait;" ::: "memory");
+            if (kTop && lane < c.k) {
+                const Best b = sm.top[lane];
+                store_first(&sm.tops[rank * c.k + lane].x, __float_as_uint(b.x));
+                store_first(&sm.tops[rank * c.k + lane].i, (uint32_t)b.i);
+            }
+            if (lane == 0) {
+                store_first(&sm.sums[rank][0], __float_as_uint(m));
+                store_first(&sm.sums[rank][1], __float_as_uint(sums.x));
+                store_first(&sm.sums[rank][2], __float_as_uint(sums.y));
+            }
         }
-        sums = make_float2(x, y);
+    } else if (ctas > 1) {
+        asm volatile("barrier.cluster.wait;" ::: "memory");
     }
     if (ctas > 1) {
-        // what each CTA found, to the first one
-        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-        if (kTop && (int)threadIdx.x < c.k) {
-            const Best b = sm.top[threadIdx.x];
-            store_first(&sm.tops[rank * c.k + threadIdx.x].x, __float_as_uint(b.x));
-            store_first(&sm.tops[rank * c.k + threadIdx.x].i, (uint32_t)b.i);
-        }
-        if (threadIdx.x == 0) {
-            store_first(&sm.sums[rank][0], __float_as_uint(m));
-            store_first(&sm.sums[rank][1], __float_as_uint(sums.x));
-            store_first(&sm.sums[rank][2], __float_as_uint(sums.y));
-        }
-        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
         if (rank) return;
         if (kTop) {
             rank_list(sm.tops, ctas * c.k, c.k, sm.top);
             __syncthreads();
         }
-        if (warp == 0) {
-            const float own = lane < ctas ? sm.sums[lane][0] : kNone;
-            sums = lane < ctas ? make_float2(sm.sums[lane][1], sm.sums[lane][2]) : make_float2(0.f, 0.f);
-            m = unordered(__reduce_max_sync(0xffffffffu, ordered(own)));
-            if (sums.x > 0.f) {
-                const float y = fmaxf((own - m) * c2, -1e30f), f = exp2_fast(y);
-                sums = make_float2(f * sums.x, f > 0.f ? f * fmaf(y, sums.x, sums.y) : 0.f);
-            }
-#pragma unroll
-            for (int o = kMaxCtas / 2; o > 0; o >>= 1) {
-                sums.x += __shfl_xor_sync(0xffffffffu, sums.x, o);
-                sums.y += __shfl_xor_sync(0xffffffffu, sums.y, o);
-            }
-        }
+        if (warp == 0)
+            m = join(lane < ctas ? sm.sums[lane][0] : kNone, lane < ctas ? make_float2(sm.sums[lane][1], sm.sums[lane][2]) : make_float2(0.f, 0.f),
+                     c2, sums);
     }
-    if (warp == 0) {                                         // k is at most a warp's threads
-        sums.x = __shfl_sync(0xffffffffu, sums.x, 0);
-        const bool none = m == kNone;
-        const float log_sum = none ? 0.f : logf(sums.x);
-        if (lane == 0) {
-            const float x = asked == asked ? fminf(asked, FLT_MAX) : kNone;
-            if (c.logp) c.logp[r] = x == kNone ? kNone : (x - m) * c.scale - log_sum;
-            if (c.entropy) c.entropy[r] = none ? 0.f : fmaxf(log_sum - sums.y / sums.x * 0.6931471805599453f, 0.f);
-        }
-        if (kTop && lane < c.k) {
-            const Best b = sm.top[lane];
-            c.top_ids[r * c.k + lane] = b.x > kNone ? b.i : -1;
-            c.top_logp[r * c.k + lane] = b.x > kNone ? (b.x - m) * c.scale - log_sum : kNone;
-        }
+    if (warp) return;                                            // k is at most a warp's threads
+    const bool none = m == kNone;
+    const float log_sum = none ? 0.f : logf(sums.x);
+    if (lane == 0) {
+        const float x = asked == asked ? fminf(asked, FLT_MAX) : kNone;
+        if (c.logp) c.logp[r] = x == kNone ? kNone : (x - m) * c.scale - log_sum;
+        if (c.entropy) c.entropy[r] = none ? 0.f : fmaxf(log_sum - sums.y / sums.x * 0.6931471805599453f, 0.f);
+    }
+    if (kTop && lane < c.k) {
+        const Best b = sm.top[lane];
+        c.top_ids[r * c.k + lane] = b.x > kNone ? b.i : -1;
+        c.top_logp[r * c.k + lane] = b.x > kNone ? (b.x - m) * c.scale - log_sum : kNone;
     }
 }
 
