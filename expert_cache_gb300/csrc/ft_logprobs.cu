@@ -27,12 +27,6 @@ constexpr int kHits = 64;              // vectors that a warp keeps for the list
 constexpr int kMaxCtas = 8;            // of a row
 constexpr float kNone = -INFINITY;
 
-struct alignas(8) Best {
-    float x;
-    int i;
-};
-__device__ __forceinline__ bool better(Best a, Best b) { return a.x > b.x || (a.x == b.x && a.i < b.i); }
-
 // Pairs of fp32 (one instruction for both).
 typedef unsigned long long Pair;
 __device__ __forceinline__ Pair pair(float lo, float hi) {
@@ -141,16 +135,23 @@ __device__ __forceinline__ unsigned ordered(float x) {
 }
 __device__ __forceinline__ float unordered(unsigned u) { return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
 
+// A logit and its index as a number whose order is theirs: the larger logit first (NaN aside, +inf as the largest number, both
+// zeros equal), then the lower index.  Numbers below 2^32 stand for none.
+typedef unsigned long long Key;
+__device__ __forceinline__ Key key_of(float x, int i) { return (Key)ordered(fminf(x, FLT_MAX) + 0.f) << 32 | ~(unsigned)i; }
+__device__ __forceinline__ float key_logit(Key k) { return k >> 32 ? unordered((unsigned)(k >> 32)) : kNone; }
+__device__ __forceinline__ int key_index(Key k) { return k >> 32 ? (int)~(unsigned)k : -1; }
+
 struct LogShared {
-    alignas(16) Best list[kListed];
-    alignas(16) Best top[kMaxK];                  // this CTA's k best
-    alignas(16) Best tops[kMaxCtas * kMaxK];      // the row's CTAs' (in its first one)
+    alignas(16) Key list[kListed];
+    alignas(16) Key top[kMaxK];                   // this CTA's k best
+    alignas(16) Key tops[kMaxCtas * kMaxK];       // the row's CTAs' (in its first one)
     alignas(16) uint4 hit[kLogWarps][kHits];      // the warps' vectors that reach the bound, and where they stand
     int hit_at[kLogWarps][kHits];
     float few[kLogWarps * 4];                     // the sample's largest
     float red[3][kLogWarps];                      // the warps' largest, S and D
     float sums[kMaxCtas][4];                      // the row's CTAs' largest, S and D (in its first one)
-    Best one;
+    Key one;
     int count;
     float bound, ref;
 };
@@ -243,37 +244,45 @@ __device__ __forceinline__ void put_on_list(LogShared& sm, const Vec<L>& v, int 
     for (int j = 0; j < Vec<L>::kN; ++j) {
         if (x[j] >= bound && x[j] > kNone) {
             const int at = atomicAdd(&sm.count, 1);
-            if (at < kListed) sm.list[at] = Best{fminf(x[j], FLT_MAX), index + j};
+            if (at < kListed) sm.list[at] = key_of(x[j], index + j);
         }
     }
 }
 
-// Adds a vector to a thread's sums; a whole warp calls it.  Vectors for the list are kept (hits of them so far) and looked
+// Adds N vectors to a thread's sums; a whole warp calls it.  Vectors for the list are kept (hits of them so far) and looked
 // at when the warp is through: the atomic operations of the list at once cost a row of 131,072 logits a microsecond more.
-template <typename L, bool kTop>
-__device__ __forceinline__ void take(LogShared& sm, Sums<L>& a, int& hits, const Vec<L>& v, int index, float bound, float c) {
-    const typename Vec<L>::Max reach = v.max();
-    const bool hit = Vec<L>::reaches(reach, a.limit);
-    if (__any_sync(0xffffffffu, hit)) {
-        float most = Vec<L>::value(reach);
-        most = most == most ? most : kNone;
-        a.top = fmaxf(a.top, fminf(most, FLT_MAX));
+// index(j): where vector j stands.
+template <typename L, bool kTop, int N, typename I>
+__device__ __forceinline__ void take(LogShared& sm, Sums<L>& a, int& hits, const Vec<L> (&v)[N], I index, float bound, float c) {
+    typename Vec<L>::Max reach = v[0].max();
+#pragma unroll
+    for (int j = 1; j < N; ++j) reach = Vec<L>::larger(reach, v[j].max());
+    if (__any_sync(0xffffffffu, Vec<L>::reaches(reach, a.limit))) {
+        float top = Vec<L>::value(reach);
+        top = top == top ? fminf(top, FLT_MAX) : kNone;
+        a.top = fmaxf(a.top, top);
         if (kTop) {
-            const bool keep = most >= bound && most > kNone;
-            const unsigned kept = __ballot_sync(0xffffffffu, keep);
-            const int at = hits + __popc(kept & ((1u << (threadIdx.x & 31)) - 1));
-            if (keep && at < kHits) {
-                v.to_shared((uint32_t)__cvta_generic_to_shared(&sm.hit[threadIdx.x >> 5][at]));
-                sm.hit_at[threadIdx.x >> 5][at] = index;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float most = Vec<L>::value(v[j].max());
+                const bool keep = most >= bound && most > kNone;
+                const unsigned kept = __ballot_sync(0xffffffffu, keep);
+                const int at = hits + __popc(kept & ((1u << (threadIdx.x & 31)) - 1));
+                if (keep && at < kHits) {
+                    v[j].to_shared((uint32_t)__cvta_generic_to_shared(&sm.hit[threadIdx.x >> 5][at]));
+                    sm.hit_at[threadIdx.x >> 5][at] = index(j);
+                }
+                hits += __popc(kept);
             }
-            hits += __popc(kept);
         }
-        if (a.plain || most > a.far) {
-            a = add_far(a, v, bound, c);
+        if (a.plain || top > a.far) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) a = add_far(a, v[j], bound, c);
             return;
         }
     }
-    a.add(v, c);
+#pragma unroll
+    for (int j = 0; j < N; ++j) a.add(v[j], c);
 }
 
 // A CTA's part of a row: the row's vectors from lo on, `steps` for every thread and one more for the first `more`; for the
@@ -376,56 +385,50 @@ __device__ void collect(LogShared& sm, const Part<L>& p) {
 template <typename F>
 __device__ __forceinline__ int count_before(int n, int parts, F before) {
     int count = 0;
+#pragma unroll 4
     for (int i = threadIdx.x & (parts - 1); i < n; i += parts) count += before(i);
     for (int o = parts >> 1; o > 0; o >>= 1) count += __shfl_xor_sync(0xffffffffu, count, o);
     return count;
 }
 
-// The k best of the list's n entries, in order, to out (entries without one: -inf); several entries may be none.
-__device__ __forceinline__ void rank_list(const Best* list, int n, int k, Best* out) {
-    for (int j = n + threadIdx.x; j < k; j += kLogThreads) out[j] = Best{kNone, -1};
+// The k largest of n different keys, in order, to out; where there are fewer, numbers for none that no other CTA of the row has.
+__device__ __forceinline__ void rank_list(const Key* list, int n, int k, int rank, Key* out) {
+    for (int j = n + threadIdx.x; j < k; j += kLogThreads) out[j] = 1 + rank * kMaxK + j;
     int shift = 0;                                                 // 1 << shift threads for an entry
     while (shift < 5 && n << (shift + 1) <= kLogThreads) ++shift;
     const int parts = 1 << shift;
     for (int first = 0; first < n; first += kLogThreads >> shift) {
         const int e = first + ((int)threadIdx.x >> shift);
-        const Best mine = e < n ? list[e] : Best{kNone, -1};
-        const int before = count_before(n, parts, [&](int i) {
-            const Best x = list[i];
-            return better(x, mine) || (x.x == mine.x && x.i == mine.i && i < e);
-        });
+        const Key mine = e < n ? list[e] : 0;
+        const int before = count_before(n, parts, [&](int i) { return list[i] > mine; });
         if (e < n && before < k && (threadIdx.x & (parts - 1)) == 0) out[before] = mine;
     }
 }
 
-// The k best by k searches.
+// The k largest by k searches.
 template <typename L>
-__device__ void search(LogShared& sm, const Part<L>& p, int k, Best* out) {
-    Best last{INFINITY, -1};
+__device__ void search(LogShared& sm, const Part<L>& p, int k, int rank, Key* out) {
+    Key last = ~0ULL;
     for (int j = 0; j < k; ++j) {
-        Best b{kNone, 0x7FFFFFFF};
+        Key b = 0;
         p.each([&](const Vec<L>& v, int index) {
             float x[Vec<L>::kN];
             v.get(x);
 #pragma unroll
             for (int i = 0; i < Vec<L>::kN; ++i) {
-                const Best e{fminf(x[i], FLT_MAX), index + i};
-                if (x[i] > kNone && better(last, e) && better(e, b)) b = e;
+                const Key e = x[i] > kNone ? key_of(x[i], index + i) : 0;
+                if (e < last && e > b) b = e;
             }
         });
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const Best e{__shfl_xor_sync(0xffffffffu, b.x, o), __shfl_xor_sync(0xffffffffu, b.i, o)};
-            if (better(e, b)) b = e;
-        }
+        for (int o = 16; o > 0; o >>= 1) b = max(b, __shfl_xor_sync(0xffffffffu, b, o));
         __syncthreads();
         if ((threadIdx.x & 31) == 0) sm.list[threadIdx.x >> 5] = b;
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int w = 1; w < kLogWarps; ++w)
-                if (better(sm.list[w], b)) b = sm.list[w];
-            sm.one = b.x > kNone ? b : Best{kNone, 0x7FFFFFFF};
-            out[j] = b.x > kNone ? b : Best{kNone, -1};
+            for (int w = 1; w < kLogWarps; ++w) b = max(b, sm.list[w]);
+            sm.one = b;
+            out[j] = b ? b : 1 + rank * kMaxK + j;
         }
         __syncthreads();
         last = sm.one;
@@ -460,8 +463,8 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
     const Part<L> p(static_cast<const L*>(c.logits) + r * c.stride, c.V, rank, shift);
     const Ring<L> ring(p, log_ring);
     ring.start();
-    Vec<L> rest;
-    p.load_rest(rest);
+    Vec<L> rest[1];
+    p.load_rest(rest[0]);
     float asked = kNone;                                     // the given token's logit
     if (rank == 0 && threadIdx.x == 0 && c.logp) {
         const int token = c.tokens[r];
@@ -500,12 +503,14 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
     a.top = sm.ref;
     a.against(sm.ref, bound, c2);
     int hits = 0;
-    if (p.rest) take<L, kTop>(sm, a, hits, rest, p.rest_index(), bound, c2);
+    if (p.rest) take<L, kTop, 1>(sm, a, hits, rest, [&](int) { return p.rest_index(); }, bound, c2);
     uint32_t slot = 0;
     for (int i = 0; i < ring.rounds; ++i) {
         ring.wait();
+        Vec<L> v[kVectors];
 #pragma unroll
-        for (int j = 0; j < kVectors; ++j) take<L, kTop>(sm, a, hits, ring.get(slot, j), p.index(i * kVectors + j), bound, c2);
+        for (int j = 0; j < kVectors; ++j) v[j] = ring.get(slot, j);
+        take<L, kTop, kVectors>(sm, a, hits, v, [&](int j) { return p.index(i * kVectors + j); }, bound, c2);
         ring.issue(i + kRounds, slot);
         slot = slot == kRing - kVectors * kSlot ? 0 : slot + kVectors * kSlot;
     }
@@ -542,17 +547,17 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
                 n = sm.count;
                 if (n <= kListed) break;
                 // the list's k-th largest bounds the row's; if it is no better than the last one, the searches
-                rank_list(sm.list, kListed, c.k, sm.top);
+                rank_list(sm.list, kListed, c.k, rank, sm.top);
                 __syncthreads();
-                const float next = sm.top[c.k - 1].x;
+                const float next = key_logit(sm.top[c.k - 1]);
                 again = next > sm.bound;
                 __syncthreads();
                 if (threadIdx.x == 0) sm.bound = next;
             }
             __syncthreads();
         }
-        if (n > kListed) search(sm, p, c.k, sm.top);
-        else rank_list(sm.list, n, c.k, sm.top);
+        if (n > kListed) search(sm, p, c.k, rank, sm.top);
+        else rank_list(sm.list, n, c.k, rank, sm.top);
         __syncthreads();
     }
     if (warp == 0) {
@@ -562,9 +567,10 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
             // what each CTA found, to the first one
             asm volatile("barrier.cluster.wait;" ::: "memory");
             if (kTop && lane < c.k) {
-                const Best b = sm.top[lane];
-                store_first(&sm.tops[rank * c.k + lane].x, __float_as_uint(b.x));
-                store_first(&sm.tops[rank * c.k + lane].i, (uint32_t)b.i);
+                const Key b = sm.top[lane];
+                const uint32_t* to = reinterpret_cast<const uint32_t*>(&sm.tops[rank * c.k + lane]);
+                store_first(to, (uint32_t)b);
+                store_first(to + 1, (uint32_t)(b >> 32));
             }
             if (lane == 0) {
                 store_first(&sm.sums[rank][0], __float_as_uint(m));
@@ -580,7 +586,7 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
         asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
         if (rank) return;
         if (kTop) {
-            rank_list(sm.tops, ctas * c.k, c.k, sm.top);
+            rank_list(sm.tops, ctas * c.k, c.k, 0, sm.top);
             __syncthreads();
         }
         if (warp == 0)
@@ -596,9 +602,9 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
         if (c.entropy) c.entropy[r] = none ? 0.f : fmaxf(log_sum - sums.y / sums.x * 0.6931471805599453f, 0.f);
     }
     if (kTop && lane < c.k) {
-        const Best b = sm.top[lane];
-        c.top_ids[r * c.k + lane] = b.x > kNone ? b.i : -1;
-        c.top_logp[r * c.k + lane] = b.x > kNone ? (b.x - m) * c.scale - log_sum : kNone;
+        const float x = key_logit(sm.top[lane]);
+        c.top_ids[r * c.k + lane] = key_index(sm.top[lane]);
+        c.top_logp[r * c.k + lane] = x > kNone ? (x - m) * c.scale - log_sum : kNone;
     }
 }
 
