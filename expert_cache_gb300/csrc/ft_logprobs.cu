@@ -4,10 +4,11 @@
 // give log sum = log S and entropy = log S - D / S.  A thread's ref is a maximum of a sample of the row, so that no
 // sum has to be rescaled unless a logit lies e^69 above it; the row's own maximum is taken at the end.
 //
-// The k largest come out of the same pass.  From the sample (the first 4 vectors of every thread) the k-th largest of some 64 logits is a lower bound of the row's k-th; only what reaches it is
-// put on a list in shared memory (some dozens of 100,000), and the list is ranked at the end.  Where more reach it than
-// the list holds, its own k-th largest is the next bound and the part is read again; where that does not help (equal
-// logits by the thousand), k searches find them.  Which ones these are does not depend on any order: value, then index.
+// The k largest come out of the same pass.  From the sample (the first 8 vectors of every thread) the k-th largest of 16 to
+// 64 logits is a lower bound of the row's k-th; only what reaches it is kept and put on a list in shared memory (4 to 8 k of
+// 100,000), which is ranked at the end.  Where more reach it than the list holds, its own k-th largest is the next bound and
+// the part is read again; where that does not help (equal logits by the thousand), k searches find them.  Which ones
+// these are does not depend on any order: value, then index.
 #include <atomic>
 #include <cfloat>
 #include <cmath>
@@ -471,21 +472,25 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
         if (token >= 0 && token < c.V) asked = (float)p.row[token];
     }
 
-    // the sample: its largest, and the warps' four largest
-    ring.wait();
+    // the sample, all that is under way: its largest, and the warps' few largest
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     typename Vec<L>::Max largest = Vec<L>::limit(kNone);
-    if (ring.rounds) {
 #pragma unroll
-        for (int j = 0; j < kVectors; ++j) largest = Vec<L>::larger(largest, ring.get(0, j).max());
+    for (int i = 0; i < kRounds; ++i) {
+        if (i < ring.rounds) {
+#pragma unroll
+            for (int j = 0; j < kVectors; ++j) largest = Vec<L>::larger(largest, ring.get(i * kVectors * kSlot, j).max());
+        }
     }
     float most = Vec<L>::value(largest);
     most = most == most ? fminf(most, FLT_MAX) : kNone;
     unsigned key = ordered(most);
-    const int each = !kTop ? 1 : c.k <= 16 ? 2 : 4;              // of a warp: kLogWarps of them hold k
-    for (int i = 0; i < each; ++i) {
+    const int each = !kTop || c.k <= 8 ? 1 : c.k <= 16 ? 2 : 4;  // of a warp: kLogWarps of them hold k, and about the sample's k largest
+    for (int i = 0;;) {
         const unsigned u = __reduce_max_sync(0xffffffffu, key);
         if (lane == 0) sm.few[warp * each + i] = unordered(u);
-        if (kTop && lane == __ffs(__ballot_sync(0xffffffffu, key == u)) - 1) key = ordered(kNone);
+        if (++i == each) break;
+        if (lane == __ffs(__ballot_sync(0xffffffffu, key == u)) - 1) key = ordered(kNone);
     }
     if (threadIdx.x == 0) sm.count = 0;
     __syncthreads();
