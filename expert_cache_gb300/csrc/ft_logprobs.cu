@@ -14,6 +14,7 @@
 #include <cmath>
 
 #include "ft_internal.cuh"
+#include "ft_pair.cuh"
 
 namespace ft {
 
@@ -27,29 +28,6 @@ constexpr int kListed = 1024;          // entries of a CTA's list
 constexpr int kHits = 64;              // vectors that a warp keeps for the list
 constexpr int kMaxCtas = 8;            // of a row
 constexpr float kNone = -INFINITY;
-
-// Pairs of fp32 (one instruction for both).
-typedef unsigned long long Pair;
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-    Pair p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
-    return p;
-}
-__device__ __forceinline__ float2 halves(Pair p) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
-    return f;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-    Pair d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 
 // 16 bytes of logits.  Max: the largest so far, NaN aside, in the form that costs least; Floor: where logits are cut off.
 template <typename L>

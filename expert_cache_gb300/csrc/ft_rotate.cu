@@ -1,16 +1,17 @@
 // New queries, keys and values on their way to attention: the norm of each head, the rotation by position, queries rounded
 // to bf16, keys and values quantised into the cache.
 //
-// A lane has 16 dims of a head (a scale block of the cache), a warp whole heads of neighbouring tokens, so that the
-// mean of the squares takes two to four shuffles and the other half of a pair comes from a lane of the same warp.
-// For a query the norm's weights and the angles fold into two factors per dim, which serve all heads of a run:
-//   out[d] = r (x[d] A[d] + x[pair of d] B[d]),  A = w[d] c, B = -+ w[pair] s,  r = (mean x^2 + eps)^-1/2.
+// A warp has whole heads of neighbouring tokens, a lane 16 dims of a head as 8 pairs: 8 dims of the first half of what turns and
+// their 8 partners, or 16 neighbours.  So a rotation needs nothing from another lane, and the mean of the squares takes two
+// to four shuffles.  For a query the norm's weights and the angles fold into two factors per dim, which serve all heads of a run:
+//   out[d] = r (x[d] A[d] + x[partner of d] B[d]),  A = w[d] c, B = -+ w[partner] s,  r = (mean x^2 + eps)^-1/2.
 // A key is rounded to a few bits, and a last bit that differs can move its code by a whole step, so its values are carried as
 // unevaluated sums of two fp32 (products split by a fused multiply-add, sums by Knuth's two-sum) down to the rounding.
 #include <cmath>
 
 #include "ft_kv_host.cuh"
 #include "ft_kv_quant.cuh"
+#include "ft_pair.cuh"
 
 namespace ft {
 
@@ -30,6 +31,140 @@ struct RotateArgs {
     float eps;
 };
 
+// The bf16 words of a lane: word j holds the dims lo + 2 j and on (j < 4) or hi + 2 (j - 4).  Partners: of word j word j ^ 4, or
+// (kInter) the two dims of a word.
+template <int D, bool kInter>
+struct Lane {
+    static constexpr int kLanes = D / 16;
+    int b;               // of the head's lanes
+    int lo, hi;
+    bool turns;
+    __device__ __forceinline__ Lane(int rope_dim) {
+        b = (threadIdx.x & 31) % kLanes;
+        turns = 16 * b < rope_dim;
+        lo = !kInter && turns ? 8 * b : 16 * b;
+        hi = !kInter && turns ? rope_dim / 2 + lo : lo + 8;
+    }
+    __device__ __forceinline__ void load(uint32_t (&x)[8], const __nv_bfloat16* head) const {
+        const uint4 l = *reinterpret_cast<const uint4*>(head + lo), h = *reinterpret_cast<const uint4*>(head + hi);
+        x[0] = l.x; x[1] = l.y; x[2] = l.z; x[3] = l.w;
+        x[4] = h.x; x[5] = h.y; x[6] = h.z; x[7] = h.w;
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16* head, const uint32_t (&x)[8]) const {
+        *reinterpret_cast<uint4*>(head + lo) = make_uint4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<uint4*>(head + hi) = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+    // The norm's weights of the lane's dims (none: 1).
+    __device__ __forceinline__ void norms(Pair (&w)[8], const float* norm) const {
+        if (!norm) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = pair(1.f, 1.f);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 v = reinterpret_cast<const float4*>(norm + (j < 2 ? lo : hi - 8))[j];
+            w[2 * j] = pair(v.x, v.y);
+            w[2 * j + 1] = pair(v.z, v.w);
+        }
+    }
+    // Cosines and signed sines of the lane's dims at a position (none: 1 and 0).
+    __device__ __forceinline__ void angles(Pair (&c)[8], Pair (&s)[8], const float* table, int rope_dim, int pos) const {
+        if (!turns || pos < 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) c[j] = pair(1.f, 1.f), s[j] = pair(0.f, 0.f);
+            return;
+        }
+        const float4* row = reinterpret_cast<const float4*>(table + (size_t)pos * rope_dim + 8 * b);
+        const float4* sines = row + rope_dim / 8;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float4 cv = row[j], sv = sines[j];
+            if constexpr (kInter) {
+                c[4 * j] = pair(cv.x, cv.x); c[4 * j + 1] = pair(cv.y, cv.y); c[4 * j + 2] = pair(cv.z, cv.z); c[4 * j + 3] = pair(cv.w, cv.w);
+                s[4 * j] = pair(-sv.x, sv.x); s[4 * j + 1] = pair(-sv.y, sv.y); s[4 * j + 2] = pair(-sv.z, sv.z); s[4 * j + 3] = pair(-sv.w, sv.w);
+            } else {
+                c[2 * j] = c[2 * j + 4] = pair(cv.x, cv.y);
+                c[2 * j + 1] = c[2 * j + 5] = pair(cv.z, cv.w);
+                s[2 * j] = pair(-sv.x, -sv.y); s[2 * j + 4] = pair(sv.x, sv.y);
+                s[2 * j + 1] = pair(-sv.z, -sv.w); s[2 * j + 5] = pair(sv.z, sv.w);
+            }
+        }
+    }
+    // What stands at the partners of word j.
+    static __device__ __forceinline__ Pair partner(const Pair (&x)[8], int j) { return kInter ? swap2(x[j]) : x[j ^ 4]; }
+};
+
+__device__ __forceinline__ Pair unpack(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+__device__ __forceinline__ uint32_t pack_bf16(Pair p) {
+    const float2 f = halves(p);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void zero(uint32_t (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = 0;
+}
+// An infinite norm: numbers become 0 before a weight can make them infinite, infinities and NaN become NaN.
+__device__ __forceinline__ void times_zero(uint32_t (&x)[8]) {
+    const __nv_bfloat162 none = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const __nv_bfloat162 a = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x[j]), none);
+        x[j] = *reinterpret_cast<const uint32_t*>(&a);
+    }
+}
+
+// One head in fp32 by the folded factors.
+template <int D, bool kInter>
+__device__ __forceinline__ void turn_plainly(const Lane<D, kInter>& p, uint32_t (&w)[8], const Pair (&A)[8], const Pair (&B)[8], float r, bool part) {
+    Pair x[8];
+    const Pair rr = pair(r, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = mul2(unpack(w[j]), rr);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        Pair y = Lane<D, kInter>::partner(x, j);
+        if (part && !p.turns) y = 0;                               // 0 times an infinity is none
+        w[j] = pack_bf16(fma2(x[j], A[j], mul2(y, B[j])));
+    }
+}
+
+// A run of a token's query heads.
+template <int D, bool kInter>
+__device__ __forceinline__ void turn_queries(const RotateArgs& a, const Lane<D, kInter>& p, int tok, int pos, bool live, int head, int end) {
+    const __nv_bfloat16* from = a.q + (size_t)tok * a.q_stride;
+    uint32_t next[8];
+    p.load(next, from + head * D);
+    Pair A[8], B[8], w[8];
+    p.angles(A, B, a.rope, a.rope_dim, pos);
+    p.norms(w, a.q_norm);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) A[j] = mul2(A[j], w[j]), B[j] = mul2(B[j], Lane<D, kInter>::partner(w, j));
+    for (; head < end; ++head) {
+        uint32_t x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = next[j];
+        if (head + 1 < end) p.load(next, from + (head + 1) * D);
+        float r = 1.f;
+        if (a.q_norm) {
+            Pair two = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const Pair u = unpack(x[j]);
+                two = fma2(u, u, two);
+            }
+            float sum = halves(two).x + halves(two).y;
+#pragma unroll
+            for (int o = 1; o < D / 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            r = rsqrtf(sum * (1.f / D) + a.eps);
+            if (r == 0.f) times_zero(x);
+        }
+        turn_plainly(p, x, A, B, r, a.rope_dim < D);
+        if (live) p.store(a.q_out + (size_t)tok * a.q_out_stride + head * D, x);
+    }
+}
+
 struct Two {
     float h, l;          // the value is h + l
 };
@@ -37,219 +172,122 @@ __device__ __forceinline__ Two two_sum(float a, float b) {
     const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
     return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z))};
 }
-__device__ __forceinline__ Two two_mul(float a, float b) {
-    const float p = __fmul_rn(a, b);
-    return {p, __fmaf_rn(a, b, -p)};
-}
-
-// A lane's place: token, block of 16 dims, and where its pairs are.
-template <int D, bool kInter>
-struct Lane {
-    static constexpr int kLanes = D / 16;
-    int b, src;          // block of the head; lane that has the pairs' other dims (its own: within the block, or none)
-    int at, angle;       // first dim of that; first pair's index
-    bool turns, low;     // is rotated; its dims are the pairs' first ones
-    __device__ __forceinline__ Lane(int rope_dim) {
-        const int lane = threadIdx.x & 31;
-        b = lane % kLanes;
-        turns = 16 * b < rope_dim;
-        low = 32 * b < rope_dim;
-        int other = b;
-        if (!kInter && turns) other = low ? b + rope_dim / 32 : b - rope_dim / 32;
-        src = lane - b + other;
-        at = 16 * other;
-        angle = kInter ? 8 * b : 16 * (low ? b : other);
-    }
-};
-
-__device__ __forceinline__ void load16(float (&f)[16], const float* p) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float4 v = reinterpret_cast<const float4*>(p)[j];
-        f[4 * j] = v.x; f[4 * j + 1] = v.y; f[4 * j + 2] = v.z; f[4 * j + 3] = v.w;
-    }
-}
-
-// Cosine and signed sine of each of a lane's dims.
-template <bool kInter, int D>
-__device__ __forceinline__ void load_angles(const RotateArgs& a, const Lane<D, kInter>& p, int pos, float (&c)[16], float (&s)[16]) {
-    if (!p.turns || pos < 0) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) c[j] = 1.f, s[j] = 0.f;
-        return;
-    }
-    const float* row = a.rope + (size_t)pos * a.rope_dim + p.angle;
-    if constexpr (kInter) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float4 cc = reinterpret_cast<const float4*>(row)[j];
-            const float4 ss = reinterpret_cast<const float4*>(row + a.rope_dim / 2)[j];
-            const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c[8 * j + 2 * i] = c[8 * j + 2 * i + 1] = cv[i];
-                s[8 * j + 2 * i] = -sv[i];
-                s[8 * j + 2 * i + 1] = sv[i];
-            }
-        }
-    } else {
-        load16(c, row);
-        load16(s, row + a.rope_dim / 2);
-        if (p.low)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) s[j] = -s[j];
-    }
-}
-
-// The other dims of the lane's pairs (zeros where there are none).
-template <bool kInter, int D>
-__device__ __forceinline__ void pairs_of(const Lane<D, kInter>& p, const uint32_t (&x)[8], uint32_t (&y)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        y[j] = kInter ? __byte_perm(x[j], 0, 0x1032) : __shfl_sync(0xffffffffu, x[j], p.src);
-        if (!p.turns) y[j] = 0;
-    }
-}
-template <bool kInter, int D>
-__device__ __forceinline__ void load_norms(const Lane<D, kInter>& p, const float* norm, float (&w)[16], float (&wp)[16]) {
-    load16(w, norm + 16 * p.b);
-    if constexpr (kInter) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) wp[j] = w[j ^ 1];
-    } else {
-        load16(wp, norm + p.at);
-    }
-}
-
-__device__ __forceinline__ void zero(uint32_t (&x)[8]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = 0;
-}
-// An infinite norm: numbers become 0 before a weight can make them infinite, infinities and NaN become NaN.
-__device__ __forceinline__ void times_zero(uint32_t (&x)[8], uint32_t (&y)[8]) {
-    const __nv_bfloat162 none = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        __nv_bfloat162 a = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x[j]), none), b = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&y[j]), none);
-        x[j] = *reinterpret_cast<uint32_t*>(&a);
-        y[j] = *reinterpret_cast<uint32_t*>(&b);
-    }
-}
-__device__ __forceinline__ void store_block(__nv_bfloat16* dst, const uint32_t (&x)[8]) {
-    reinterpret_cast<uint4*>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<uint4*>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&p);
-}
-
-// A run of a token's query heads.
-template <int D, bool kInter>
-__device__ __forceinline__ void turn_queries(const RotateArgs& a, const Lane<D, kInter>& p, int tok, int pos, bool live, int head, int end) {
-    float A[16], B[16];
-    load_angles(a, p, pos, A, B);
-    if (a.q_norm) {
-        float w[16], wp[16];
-        load_norms(p, a.q_norm, w, wp);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) A[j] *= w[j], B[j] *= wp[j];
-    }
-    for (; head < end; ++head) {
-        uint32_t x[8], y[8];
-        if (live) load_block(x, a.q + (size_t)tok * a.q_stride + head * D + 16 * p.b);
-        else zero(x);
-        pairs_of(p, x, y);
-        float r = 1.f;
-        if (a.q_norm) {
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sum = fmaf(bf16_at(x, j), bf16_at(x, j), sum);
-#pragma unroll
-            for (int o = 1; o < D / 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            r = rsqrtf(sum * (1.f / D) + a.eps);
-            if (r == 0.f) times_zero(x, y);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float lo = r * fmaf(bf16_at(x, 2 * j), A[2 * j], bf16_at(y, 2 * j) * B[2 * j]);
-            const float hi = r * fmaf(bf16_at(x, 2 * j + 1), A[2 * j + 1], bf16_at(y, 2 * j + 1) * B[2 * j + 1]);
-            x[j] = pack_bf16(lo, hi);
-        }
-        if (live) store_block(a.q_out + (size_t)tok * a.q_out_stride + head * D + 16 * p.b, x);
-    }
+__device__ __forceinline__ void two_sum2(Pair a, Pair b, Pair& h, Pair& l) {
+    h = add2(a, b);
+    const Pair z = from2(a, h);
+    l = add2(from2(from2(z, h), a), from2(z, b));
 }
 
 // (mean x^2 + eps)^-1/2 of a head; squares of bf16 are exact in fp32.
 template <int D>
-__device__ __forceinline__ Two inverse_norm(const uint32_t (&x)[8], float eps) {
-    Two sum = {0.f, 0.f};
+__device__ __forceinline__ Two inverse_norm(const Pair (&x)[8], float eps) {
+    Pair h = mul2(x[0], x[0]), l = 0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const Two t = two_sum(sum.h, __fmul_rn(bf16_at(x, j), bf16_at(x, j)));
-        sum = {t.h, __fadd_rn(sum.l, t.l)};
+    for (int j = 1; j < 8; ++j) {
+        Pair e;
+        two_sum2(h, mul2(x[j], x[j]), h, e);
+        l = add2(l, e);
     }
+    const float2 hh = halves(h), ll = halves(l);
+    Two sum = two_sum(hh.x, hh.y);
+    sum.l = __fadd_rn(sum.l, __fadd_rn(ll.x, ll.y));
 #pragma unroll
     for (int o = 1; o < D / 16; o <<= 1) {
-        const float h = __shfl_xor_sync(0xffffffffu, sum.h, o), l = __shfl_xor_sync(0xffffffffu, sum.l, o);
-        const Two t = two_sum(sum.h, h);
-        sum = {t.h, __fadd_rn(__fadd_rn(sum.l, l), t.l)};
+        const float oh = __shfl_xor_sync(0xffffffffu, sum.h, o), ol = __shfl_xor_sync(0xffffffffu, sum.l, o);
+        const Two t = two_sum(sum.h, oh);
+        sum = {t.h, __fadd_rn(__fadd_rn(sum.l, ol), t.l)};
     }
     Two m = two_sum(__fmul_rn(sum.h, 1.f / D), eps);
     m.l = __fmaf_rn(sum.l, 1.f / D, m.l);
     // one step of Newton's on the fp32 root, its residual 1 - m r^2 in two parts
-    const float r = rsqrtf(m.h);
-    const Two r2 = two_mul(r, r);
-    float e = __fmaf_rn(-m.h, r2.h, 1.f);
-    e = __fmaf_rn(-m.h, r2.l, e);
-    e = __fmaf_rn(-m.l, r2.h, e);
+    const float r = rsqrtf(m.h), r2 = __fmul_rn(r, r), r2l = __fmaf_rn(r, r, -r2);
+    float e = __fmaf_rn(-m.h, r2, 1.f);
+    e = __fmaf_rn(-m.h, r2l, e);
+    e = __fmaf_rn(-m.l, r2, e);
     return {r, isinf(m.h) ? 0.f : __fmul_rn(__fmul_rn(0.5f, r), e)};
 }
 
-// r (x w c + y v s), rounded to fp32 once.
-__device__ __forceinline__ float turned(float x, float w, float c, float y, float v, float s, Two r) {
-    const Two xw = two_mul(x, w), yv = two_mul(y, v);
-    const Two p = two_mul(xw.h, c), q = two_mul(yv.h, s), t = two_sum(p.h, q.h);
-    float l = __fadd_rn(__fmaf_rn(xw.l, c, p.l), __fmaf_rn(yv.l, s, q.l));
-    l = __fadd_rn(l, t.l);
-    const Two o = two_mul(t.h, r.h);
-    l = __fmaf_rn(t.h, r.l, __fmaf_rn(l, r.h, o.l));
-    return isfinite(o.h) ? __fadd_rn(o.h, l) : o.h;
-}
-
+// A run of a token's key heads.
 template <int D, int kFormat, bool kInter>
 __device__ __forceinline__ void turn_keys(const RotateArgs& a, const Lane<D, kInter>& p, int tok, int pos, int slot, int head, int end,
                                           float inv_k) {
-    float c[16], s[16];
-    load_angles(a, p, pos, c, s);
+    typedef Lane<D, kInter> L;
+    uint32_t k[8];
+    p.load(k, a.k + (size_t)tok * a.k_stride + head * D);
+    Pair c[8], s[8];
+    p.angles(c, s, a.rope, a.rope_dim, pos);
     for (; head < end; ++head) {
-        uint32_t x[8], y[8];
-        if (slot >= 0) load_block(x, a.k + (size_t)tok * a.k_stride + head * D + 16 * p.b);
-        else zero(x);
-        pairs_of(p, x, y);
+        // an infinity or a NaN has no second part
+        __nv_bfloat162 most = __habs2(*reinterpret_cast<__nv_bfloat162*>(&k[0]));
+#pragma unroll
+        for (int j = 1; j < 8; ++j) most = __hmax2_nan(most, __habs2(*reinterpret_cast<__nv_bfloat162*>(&k[j])));
+        const float2 mm = __bfloat1622float2(most);
+        const bool numbers = mm.x < INFINITY && mm.y < INFINITY;
+        Pair x[8], n[8];                                           // value: x, then x - n
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = unpack(k[j]);
         Two r = {1.f, 0.f};
-        float w[16], wp[16];
         if (a.k_norm) {
             r = inverse_norm<D>(x, a.eps);
-            if (r.h == 0.f) times_zero(x, y);
-            load_norms(p, a.k_norm, w, wp);
+            if (r.h == 0.f) {
+                times_zero(k);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = unpack(k[j]);
+            }
+            Pair w[8];
+            p.norms(w, a.k_norm);
+            if (numbers) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const Pair u = x[j];
+                    x[j] = mul2(u, w[j]);
+                    n[j] = fma2(neg2(u), w[j], x[j]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = mul2(x[j], w[j]);
+            }
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = wp[j] = 1.f;
+            for (int j = 0; j < 8; ++j) n[j] = 0;
         }
+        if (numbers) {
+            const Pair rh = pair(r.h, r.h), rl = pair(r.l, r.l);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float f[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int d = 2 * j + i;
-                f[i] = turned(bf16_at(x, d), w[d], c[d], bf16_at(y, d), wp[d], s[d], r);
+            for (int j = 0; j < 8; ++j) {
+                const Pair y = L::partner(x, j), m = L::partner(n, j);
+                const Pair u = mul2(x[j], c[j]), ul = fma2(neg2(x[j]), c[j], u), v = mul2(y, s[j]), vl = fma2(neg2(y), s[j], v);
+                Pair h, l;
+                two_sum2(u, v, h, l);
+                l = from2(add2(fma2(n[j], c[j], ul), fma2(m, s[j], vl)), l);
+                const Pair o = mul2(h, rh), ol = fma2(neg2(h), rh, o);
+                k[j] = pack_bf16(add2(o, from2(ol, fma2(h, rl, mul2(l, rh)))));
             }
-            x[j] = pack_bf16(f[0], f[1]);
+        } else {
+            const Pair rh = pair(r.h, r.h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const Pair y = p.turns ? L::partner(x, j) : 0;
+                k[j] = pack_bf16(mul2(fma2(x[j], c[j], mul2(y, s[j])), rh));
+            }
         }
-        if (slot < 0) continue;
-        if (a.k_out) store_block(a.k_out + (size_t)tok * a.k_out_stride + head * D + 16 * p.b, x);
-        append_block<D, kFormat, false>(kv_tile_ptr(a.kv, slot, head, kv_tile(D, kFormat).bytes), slot & 15, p.b, x, a.kv.k_scale, inv_k);
+        if (slot >= 0 && a.k_out) p.store(a.k_out + (size_t)tok * a.k_out_stride + head * D, k);
+        int block = p.b;
+        if constexpr (!kInter) {
+            // of two neighbouring lanes' first and second halves, one lane gets the first block of 16 dims and one the second
+            const bool odd = p.b & 1;
+            uint32_t other[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) other[j] = __shfl_xor_sync(0xffffffffu, odd ? k[j] : k[j + 4], 1);
+            if (p.turns) {
+                block = p.b / 2 + (odd ? a.rope_dim / 32 : 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) (odd ? k[j] : k[j + 4]) = other[j];
+            }
+        }
+        if (slot >= 0)
+            append_block<D, kFormat, false>(kv_tile_ptr(a.kv, slot, head, kv_tile(D, kFormat).bytes), slot & 15, block, k, a.kv.k_scale, inv_k);
+        if (head + 1 < end) p.load(k, a.k + (size_t)tok * a.k_stride + (head + 1) * D);
     }
 }
 

@@ -584,7 +584,7 @@ ft_status ft_rope_table(const double* inv_freq, int32_t rope_dim, int32_t n_posi
  * gets it too); v is stored as it is.  q's values are in fp32; k's are good to some 2^-40 of the larger of their pair
  * before they are rounded, so what is stored is what the formula gives in 64 bits.  Where a head's squares pass fp32's range
  * its finite dims come out as 0.
- * Tokens whose slot is -1 are padding: nothing of them is read or written.  Another slot outside the cache, or a position
+ * Tokens whose slot is -1 are padding: nothing of them is written, and nothing depends on what they hold.  Another slot outside the cache, or a position
  * outside [0, n_positions), sets FT_DEV_BAD_ID and is treated the same way.  Slots differ from each other.
  * q_out may be q, k_out may be k (of the same stride); no other arrays overlap.
  * Errors (nothing launched): FT_ERR_ARG for layer outside [0, L), n < 0, NULL or misaligned q, k, v, q_out (16 bytes; k_out
