@@ -17,7 +17,8 @@ namespace ft {
 
 namespace {
 
-constexpr int kRotThreads = 128;
+constexpr int kRotThreads = 128, kRotPerSm = 5;
+constexpr int kAhead = 4;              // heads that a lane has under way
 
 struct RotateArgs {
     KvView kv;
@@ -27,7 +28,7 @@ struct RotateArgs {
     const float *q_norm, *k_norm, *rope;
     const int32_t *positions, *slots;
     int n, hq, rope_dim, n_positions;
-    int run, q_runs, k_runs, units;      // heads of a warp; runs of q's heads, of k's (and as many of v's), of all
+    int run, units;      // heads of a warp, and how many such runs the k, v and q heads (in this order) make
     float eps;
 };
 
@@ -44,11 +45,6 @@ struct Lane {
         turns = 16 * b < rope_dim;
         lo = !kInter && turns ? 8 * b : 16 * b;
         hi = !kInter && turns ? rope_dim / 2 + lo : lo + 8;
-    }
-    __device__ __forceinline__ void load(uint32_t (&x)[8], const __nv_bfloat16* head) const {
-        const uint4 l = *reinterpret_cast<const uint4*>(head + lo), h = *reinterpret_cast<const uint4*>(head + hi);
-        x[0] = l.x; x[1] = l.y; x[2] = l.z; x[3] = l.w;
-        x[4] = h.x; x[5] = h.y; x[6] = h.z; x[7] = h.w;
     }
     __device__ __forceinline__ void store(__nv_bfloat16* head, const uint32_t (&x)[8]) const {
         *reinterpret_cast<uint4*>(head + lo) = make_uint4(x[0], x[1], x[2], x[3]);
@@ -68,9 +64,14 @@ struct Lane {
             w[2 * j + 1] = pair(v.z, v.w);
         }
     }
+    // Those of word j.
+    __device__ __forceinline__ Pair norm(const float* norm, int j) const {
+        const float2 v = *reinterpret_cast<const float2*>(norm + (j < 4 ? lo + 2 * j : hi + 2 * (j - 4)));
+        return pair(v.x, v.y);
+    }
     // Cosines and signed sines of the lane's dims at a position (none: 1 and 0).
     __device__ __forceinline__ void angles(Pair (&c)[8], Pair (&s)[8], const float* table, int rope_dim, int pos) const {
-        if (!turns || pos < 0) {
+        if (!turns) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) c[j] = pair(1.f, 1.f), s[j] = pair(0.f, 0.f);
             return;
@@ -130,22 +131,47 @@ __device__ __forceinline__ void turn_plainly(const Lane<D, kInter>& p, uint32_t 
     }
 }
 
-// A run of a token's query heads.
+// A lane's bytes of a run of heads on their way through its own slots of shared memory, kAhead heads of them.  Nobody else
+// reads them, so its own wait for its copies is all there is to wait for.
+struct Heads {
+    const __nv_bfloat16 *k, *v, *q;    // the token's
+    int hkv, at, end, D;               // next head to ask for, in the order k, v, q; end of the run
+    uint32_t slots, ask, take;         // this thread's shared memory, where the next head goes, where the first one is
+
+    template <typename L>
+    __device__ __forceinline__ void issue(const L& p) {
+        if (at < end) {
+            const bool is_v = at >= hkv && at < 2 * hkv;
+            const __nv_bfloat16* head = at < hkv ? k + at * D : is_v ? v + (at - hkv) * D : q + (at - 2 * hkv) * D;
+            const __nv_bfloat16 *lo = head + (is_v ? 16 * p.b : p.lo), *hi = head + (is_v ? 16 * p.b + 8 : p.hi);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slots + ask), "l"(lo) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slots + ask + kRotThreads * 16), "l"(hi) : "memory");
+            ++at;
+        }
+        ask = (ask + 2 * kRotThreads * 16) & (2 * kAhead * kRotThreads * 16 - 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    template <typename L>
+    __device__ __forceinline__ void next(const L& p, uint32_t (&x)[8]) {
+        asm volatile("cp.async.wait_group %0;" :: "n"(kAhead - 1) : "memory");
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(slots + take));
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]) : "r"(slots + take + kRotThreads * 16));
+        issue(p);                      // into the slots of the head before
+        take = (take + 2 * kRotThreads * 16) & (2 * kAhead * kRotThreads * 16 - 1);
+    }
+};
+
+// Query heads head .. end - 1 of a token.
 template <int D, bool kInter>
-__device__ __forceinline__ void turn_queries(const RotateArgs& a, const Lane<D, kInter>& p, int tok, int pos, bool live, int head, int end) {
-    const __nv_bfloat16* from = a.q + (size_t)tok * a.q_stride;
-    uint32_t next[8];
-    p.load(next, from + head * D);
+__device__ __forceinline__ void turn_queries(const RotateArgs& a, const Lane<D, kInter>& p, Heads& heads, const Pair (&c)[8], const Pair (&s)[8],
+                                             int tok, bool live, int head, int end) {
     Pair A[8], B[8], w[8];
-    p.angles(A, B, a.rope, a.rope_dim, pos);
     p.norms(w, a.q_norm);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) A[j] = mul2(A[j], w[j]), B[j] = mul2(B[j], Lane<D, kInter>::partner(w, j));
+    for (int j = 0; j < 8; ++j) A[j] = mul2(c[j], w[j]), B[j] = mul2(s[j], Lane<D, kInter>::partner(w, j));
     for (; head < end; ++head) {
         uint32_t x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = next[j];
-        if (head + 1 < end) p.load(next, from + (head + 1) * D);
+        heads.next(p, x);
         float r = 1.f;
         if (a.q_norm) {
             Pair two = 0;
@@ -180,12 +206,14 @@ __device__ __forceinline__ void two_sum2(Pair a, Pair b, Pair& h, Pair& l) {
 
 // (mean x^2 + eps)^-1/2 of a head; squares of bf16 are exact in fp32.
 template <int D>
-__device__ __forceinline__ Two inverse_norm(const Pair (&x)[8], float eps) {
-    Pair h = mul2(x[0], x[0]), l = 0;
+__device__ __forceinline__ Two inverse_norm(const uint32_t (&x)[8], float eps) {
+    Pair h = unpack(x[0]), l = 0;
+    h = mul2(h, h);
 #pragma unroll
     for (int j = 1; j < 8; ++j) {
+        const Pair u = unpack(x[j]);
         Pair e;
-        two_sum2(h, mul2(x[j], x[j]), h, e);
+        two_sum2(h, mul2(u, u), h, e);
         l = add2(l, e);
     }
     const float2 hh = halves(h), ll = halves(l);
@@ -207,68 +235,57 @@ __device__ __forceinline__ Two inverse_norm(const Pair (&x)[8], float eps) {
     return {r, isinf(m.h) ? 0.f : __fmul_rn(__fmul_rn(0.5f, r), e)};
 }
 
-// A run of a token's key heads.
+// (x - n) c + (y - m) s times rh + rl, rounded to fp32 and to bf16: x - n and y - m stand for a pair's dims times their weights.
+__device__ __forceinline__ uint32_t turned(Pair x, Pair n, Pair y, Pair m, Pair c, Pair s, Pair rh, Pair rl) {
+    const Pair u = mul2(x, c), ul = fma2(neg2(x), c, u), v = mul2(y, s), vl = fma2(neg2(y), s, v);
+    Pair h, l;
+    two_sum2(u, v, h, l);
+    l = from2(add2(fma2(n, c, ul), fma2(m, s, vl)), l);
+    const Pair o = mul2(h, rh), ol = fma2(neg2(h), rh, o);
+    return pack_bf16(add2(o, from2(ol, fma2(h, rl, mul2(l, rh)))));
+}
+
+// Key heads head .. end - 1 of a token.
 template <int D, int kFormat, bool kInter>
-__device__ __forceinline__ void turn_keys(const RotateArgs& a, const Lane<D, kInter>& p, int tok, int pos, int slot, int head, int end,
-                                          float inv_k) {
-    typedef Lane<D, kInter> L;
-    uint32_t k[8];
-    p.load(k, a.k + (size_t)tok * a.k_stride + head * D);
-    Pair c[8], s[8];
-    p.angles(c, s, a.rope, a.rope_dim, pos);
+__device__ __forceinline__ void turn_keys(const RotateArgs& a, const Lane<D, kInter>& p, Heads& heads, const Pair (&c)[8], const Pair (&s)[8],
+                                          int tok, int slot, int head, int end, float inv_k) {
     for (; head < end; ++head) {
+        uint32_t k[8];
+        heads.next(p, k);
         // an infinity or a NaN has no second part
         __nv_bfloat162 most = __habs2(*reinterpret_cast<__nv_bfloat162*>(&k[0]));
 #pragma unroll
         for (int j = 1; j < 8; ++j) most = __hmax2_nan(most, __habs2(*reinterpret_cast<__nv_bfloat162*>(&k[j])));
         const float2 mm = __bfloat1622float2(most);
-        const bool numbers = mm.x < INFINITY && mm.y < INFINITY;
-        Pair x[8], n[8];                                           // value: x, then x - n
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = unpack(k[j]);
         Two r = {1.f, 0.f};
         if (a.k_norm) {
-            r = inverse_norm<D>(x, a.eps);
-            if (r.h == 0.f) {
-                times_zero(k);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = unpack(k[j]);
-            }
-            Pair w[8];
-            p.norms(w, a.k_norm);
-            if (numbers) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const Pair u = x[j];
-                    x[j] = mul2(u, w[j]);
-                    n[j] = fma2(neg2(u), w[j], x[j]);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = mul2(x[j], w[j]);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) n[j] = 0;
+            r = inverse_norm<D>(k, a.eps);
+            if (r.h == 0.f) times_zero(k);
         }
-        if (numbers) {
-            const Pair rh = pair(r.h, r.h), rl = pair(r.l, r.l);
+        const Pair rh = pair(r.h, r.h), rl = pair(r.l, r.l);
+        const bool numbers = mm.x < INFINITY && mm.y < INFINITY;
+        // word j and, unless its two dims are partners, word j + 4
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const Pair y = L::partner(x, j), m = L::partner(n, j);
-                const Pair u = mul2(x[j], c[j]), ul = fma2(neg2(x[j]), c[j], u), v = mul2(y, s[j]), vl = fma2(neg2(y), s[j], v);
-                Pair h, l;
-                two_sum2(u, v, h, l);
-                l = from2(add2(fma2(n[j], c[j], ul), fma2(m, s[j], vl)), l);
-                const Pair o = mul2(h, rh), ol = fma2(neg2(h), rh, o);
-                k[j] = pack_bf16(add2(o, from2(ol, fma2(h, rl, mul2(l, rh)))));
+        for (int j = 0; j < (kInter ? 8 : 4); ++j) {
+            Pair x = unpack(k[j]), n = 0, y = kInter ? 0 : unpack(k[j ^ 4]), m = 0;
+            if (a.k_norm) {
+                const Pair w = p.norm(a.k_norm, j), u = x;
+                x = mul2(u, w);
+                n = fma2(neg2(u), w, x);
+                if (!kInter) {
+                    const Pair z = p.norm(a.k_norm, j ^ 4), v = y;
+                    y = mul2(v, z);
+                    m = fma2(neg2(v), z, y);
+                }
             }
-        } else {
-            const Pair rh = pair(r.h, r.h);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const Pair y = p.turns ? L::partner(x, j) : 0;
-                k[j] = pack_bf16(mul2(fma2(x[j], c[j], mul2(y, s[j])), rh));
+            if (kInter) y = swap2(x), m = swap2(n);
+            if (numbers) {
+                k[j] = turned(x, n, y, m, c[j], s[j], rh, rl);
+                if (!kInter) k[j ^ 4] = turned(y, m, x, n, c[j], neg2(s[j]), rh, rl);
+            } else {
+                const Pair none = 0;
+                k[j] = pack_bf16(mul2(fma2(x, c[j], mul2(p.turns ? y : none, s[j])), rh));
+                if (!kInter) k[j ^ 4] = pack_bf16(mul2(fma2(y, c[j], mul2(p.turns ? x : none, neg2(s[j]))), rh));
             }
         }
         if (slot >= 0 && a.k_out) p.store(a.k_out + (size_t)tok * a.k_out_stride + head * D, k);
@@ -287,49 +304,44 @@ __device__ __forceinline__ void turn_keys(const RotateArgs& a, const Lane<D, kIn
         }
         if (slot >= 0)
             append_block<D, kFormat, false>(kv_tile_ptr(a.kv, slot, head, kv_tile(D, kFormat).bytes), slot & 15, block, k, a.kv.k_scale, inv_k);
-        if (head + 1 < end) p.load(k, a.k + (size_t)tok * a.k_stride + (head + 1) * D);
     }
 }
 
 template <int D, int kFormat, bool kInter>
-__global__ void __launch_bounds__(kRotThreads) kv_rotate_kernel(const RotateArgs a) {
+__global__ void __launch_bounds__(kRotThreads, kRotPerSm) kv_rotate_kernel(const RotateArgs a) {
+    __shared__ __align__(16) uint8_t ring[2 * kAhead * kRotThreads * 16];
     pdl_wait_and_release();
     constexpr int kTokens = 32 / (D / 16);
     const Lane<D, kInter> p(a.rope_dim);
     const long long warps = (long long)gridDim.x * (kRotThreads / 32), groups = ((long long)a.n + kTokens - 1) / kTokens;
     const long long all = groups * a.units;
-    const float inv_k = __frcp_rn(a.kv.k_scale), inv_v = __frcp_rn(a.kv.v_scale);
+    const int hkv = a.kv.hkv;
+    // runs of k's heads, which take longest, first
     for (long long u = (long long)blockIdx.x * (kRotThreads / 32) + (threadIdx.x >> 5); u < all; u += warps) {
-        const int unit = (int)(u % a.units);
-        const long long token = u / a.units * kTokens + (threadIdx.x & 31) / Lane<D, kInter>::kLanes;
+        const int first = (int)(u / groups) * a.run, end = min(first + a.run, a.hq + 2 * hkv);
+        const long long token = u % groups * kTokens + (threadIdx.x & 31) / Lane<D, kInter>::kLanes;
         const int tok = (int)min(token, (long long)a.n - 1);
-        int slot = token < a.n ? a.slots[tok] : -1, pos = -1;
-        if (slot != -1) {
-            bool bad = slot < 0 || (slot >> a.kv.page_shift) >= a.kv.n_pages;
-            if (a.rope_dim) {
-                pos = a.positions[tok];
-                bad = bad || pos < 0 || pos >= a.n_positions;
-            }
-            if (bad) {
-                if (unit == 0 && p.b == 0) atomicOr(a.kv.status, FT_DEV_BAD_ID);
-                slot = pos = -1;
-            }
+        Heads heads{a.k + (size_t)tok * a.k_stride, a.v + (size_t)tok * a.v_stride, a.q + (size_t)tok * a.q_stride, hkv, first, end, D,
+                    (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) heads.issue(p);
+        int slot = token < a.n ? a.slots[tok] : -1, pos = a.rope_dim ? a.positions[tok] : 0;
+        if (slot < 0 || (slot >> a.kv.page_shift) >= a.kv.n_pages || (a.rope_dim && (pos < 0 || pos >= a.n_positions))) {
+            if (slot != -1 && first == 0 && p.b == 0) atomicOr(a.kv.status, FT_DEV_BAD_ID);
+            slot = -1;
+            pos = 0;                                               // there is a row
         }
-        if (unit < a.q_runs) {
-            const int head = unit * a.run;
-            turn_queries(a, p, tok, pos, slot >= 0, head, min(head + a.run, a.hq));
-        } else if (unit < a.q_runs + a.k_runs) {
-            const int head = (unit - a.q_runs) * a.run;
-            turn_keys<D, kFormat, kInter>(a, p, tok, pos, slot, head, min(head + a.run, a.kv.hkv), inv_k);
-        } else {
-            int head = (unit - a.q_runs - a.k_runs) * a.run;
-            const int end = min(head + a.run, a.kv.hkv);
-            for (; head < end && slot >= 0; ++head) {
-                uint32_t x[8];
-                load_block(x, a.v + (size_t)tok * a.v_stride + head * D + 16 * p.b);
-                append_block<D, kFormat, true>(kv_tile_ptr(a.kv, slot, head, kv_tile(D, kFormat).bytes), slot & 15, p.b, x, a.kv.v_scale, inv_v);
-            }
+        Pair c[8], s[8];
+        p.angles(c, s, a.rope, a.rope_dim, pos);
+        if (first < hkv) turn_keys<D, kFormat, kInter>(a, p, heads, c, s, tok, slot, first, min(end, hkv), __frcp_rn(a.kv.k_scale));
+        for (int head = max(first, hkv); head < min(end, 2 * hkv); ++head) {
+            uint32_t x[8];
+            heads.next(p, x);
+            if (slot >= 0)
+                append_block<D, kFormat, true>(kv_tile_ptr(a.kv, slot, head - hkv, kv_tile(D, kFormat).bytes), slot & 15, p.b, x, a.kv.v_scale,
+                                               __frcp_rn(a.kv.v_scale));
         }
+        if (end > 2 * hkv) turn_queries(a, p, heads, c, s, tok, slot >= 0, max(first - 2 * hkv, 0), end - 2 * hkv);
     }
 }
 
@@ -339,10 +351,13 @@ struct Rotate {
         const cudaError_t e = inter ? prepare<kv_rotate_kernel<D, kFormat, true>>() : prepare<kv_rotate_kernel<D, kFormat, false>>();
         if (e != cudaSuccess) return e;
         const long long groups = ((long long)a.n + 32 / (D / 16) - 1) / (32 / (D / 16));
-        a.run = groups * (a.hq + 2 * a.kv.hkv) >= 32LL * sm_count() ? 4 : 1;
-        a.q_runs = (a.hq + a.run - 1) / a.run;
-        a.k_runs = (a.kv.hkv + a.run - 1) / a.run;
-        a.units = a.q_runs + 2 * a.k_runs;
+        const int heads = a.hq + 2 * a.kv.hkv;
+        // heads of a warp: its start (slot, position, angles, weights) is shared by them (8192 tokens of 32 + 8 + 8 heads of 128:
+        // 1 head 78 us, 4 53 us, 16 41 us), but there are to be 32 runs per SM (3001 tokens of 20 + 4 + 4 heads of 64: 1
+        // head 13.5 us, 2 10.5 us, 4 10.9 us)
+        const long long want = groups * heads / (32LL * sm_count());
+        a.run = want < 1 ? 1 : want > 16 ? 16 : (int)want;
+        a.units = (heads + a.run - 1) / a.run;
         const long long ctas = (groups * a.units + kRotThreads / 32 - 1) / (kRotThreads / 32);
         return launch_pdl(inter ? kv_rotate_kernel<D, kFormat, true> : kv_rotate_kernel<D, kFormat, false>,
                           dim3((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20)), dim3(kRotThreads), 0, s, a);
