@@ -1,4 +1,7 @@
-// Router: logits to the k experts of each token and their weights.  A warp per token; its choices stand in shared memory.
+// Router: logits to the k experts of each token and their weights.  A warp per token.
+//
+// Up to 512 experts the choices stay in registers.  The (k + 1)-th largest of the lanes' maxima bounds the (k + 1)-th largest choice
+// from below; what reaches it, k to some 1.3 k of 256, goes through shared memory and is ranked, each lane one.
 //
 // Choices are computed in fp32 with a bound on their error.  Where two neighbours of the sorted first k + 1 (or the last
 // group that stays and the first that does not) lie within their bounds, and do not come from the same logit and bias, the row is
@@ -6,6 +9,7 @@
 // is the logits' own and needs no rounding at all.
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "ft_internal.cuh"
 
@@ -23,6 +27,8 @@ struct RouteArgs {
     float* w;
     long long stride;
     int T, E, k, n_group, topk_group, group_best, size;     // size: experts of a group
+    int group_shift;       // 1 << group_shift lanes look at a group
+    unsigned group_mul;    // expert e < 512 is of group e * group_mul >> 20
     bool sigmoid, renormalise, by_logit;
     float scale;
 };
@@ -70,13 +76,16 @@ __device__ __forceinline__ Scores<V> scores_of(const RouteArgs& a, const float* 
     return s;
 }
 
-// A bound on the error of an fp32 choice: the roundings of the exponentials, of their arguments (at most -log of the score in
-// magnitude) and of the sum (E / 32 + 5 additions), what underflows, and the bias' addition.
-__device__ __forceinline__ float choice_error(const RouteArgs& a, float choice, float bias) {
-    const float score = fabsf(choice - bias);
-    return 0x1p-23f * (((float)(a.E / 32 + 16) - __log2f(fmaxf(score, 0x1p-120f))) * score + 2.f * fabsf(choice) + 0x1p-100f);
+// A bound on the error of an fp32 score: the roundings of the exponential (2^-22) and of its argument (at most -log2 of the
+// score in magnitude), those of the sum's terms and its E / 32 + 5 additions, two more operations, what underflows.  It rises with the score.
+__device__ __forceinline__ float score_error(const RouteArgs& a, float score) {
+    return 0x1p-24f * ((float)(a.E / 32 + 16) - 2.f * __log2f(fmaxf(score, 0x1p-120f))) * score + 0x1p-123f;
 }
-__device__ __forceinline__ double choice_error(const RouteArgs&, double, float) { return -1.0; }
+// Whether two neighbours among the sorted choices may stand the other way round, or one that is sorted further down belong between them:
+// any choice may be off by what the row's largest score may (most), and by the bias' addition.
+__device__ __forceinline__ bool too_near(const RouteArgs& a, float first, float second, float most) {
+    return first - second <= 2.f * score_error(a, most) + 0x1p-22f * (fabsf(first) + fabsf(second));
+}
 
 // The choices of a row in type V, the groups that stay, and the k first experts: lane j < k gets the j-th (-1: none).
 // Returns false if fp32 does not tell.
@@ -84,10 +93,12 @@ template <typename V>
 __device__ bool decide(const RouteArgs& a, const float* x, V* key, int& id) {
     const int lane = threadIdx.x & 31;
     bool sure = true;
+    float largest = 1.f;                                         // no score is above it
     if (a.by_logit) {
         for (int e = lane; e < a.E; e += 32) key[e] = x[e];
     } else {
         const Scores<V> s = scores_of<V>(a, x);
+        if (!a.sigmoid) largest = 1.f / (float)s.sum;
         for (int e = lane; e < a.E; e += 32) {
             V c = s.of(x[e]) + (a.bias ? V(a.bias[e]) : V(0));
             if (x[e] == kNone || !(c == c)) c = kNone;
@@ -108,8 +119,8 @@ __device__ bool decide(const RouteArgs& a, const float* x, V* key, int& id) {
         const V worth = a.group_best == 2 && two > V(kNone) ? one + two : one;
         float err = 0.f;
         if (!a.by_logit && sizeof(V) == 4 && one > V(kNone)) {
-            // the scores of a sum's terms are at most 1, and their magnitudes bound its own rounding
-            err = 0x1p-23f * (float)((a.E / 32 + 16) * a.group_best) + 0x1p-22f * (fabsf((float)one) + (two > V(kNone) ? fabsf((float)two) : 0.f));
+            // the magnitudes of a sum's terms bound its own rounding
+            err = score_error(a, largest) * a.group_best + 0x1p-22f * (fabsf((float)one) + (two > V(kNone) ? fabsf((float)two) : 0.f));
         }
         int before = 0;
         V least = INFINITY, most = kNone;
@@ -149,7 +160,7 @@ __device__ bool decide(const RouteArgs& a, const float* x, V* key, int& id) {
         if (best == V(kNone)) break;
         if (sizeof(V) == 4 && !a.by_logit && j) {
             const float b0 = a.bias ? a.bias[last_id] : 0.f, b1 = a.bias ? a.bias[at] : 0.f;
-            if (!(x[last_id] == x[at] && b0 == b1) && last - best <= choice_error(a, last, b0) + choice_error(a, best, b1)) sure = false;
+            if (!(x[last_id] == x[at] && b0 == b1) && too_near(a, last, best, largest)) sure = false;
         }
         if (lane == j && j < a.k) id = at;
         last = best;
@@ -160,45 +171,327 @@ __device__ bool decide(const RouteArgs& a, const float* x, V* key, int& id) {
     return sure;
 }
 
-template <typename L>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
-    extern __shared__ double route_smem[];
-    pdl_wait_and_release();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long t = (long long)blockIdx.x * (blockDim.x >> 5) + warp;
-    if (t >= a.T) return;
-    double* key = route_smem + (size_t)warp * a.E;
-    float* x = reinterpret_cast<float*>(route_smem + (size_t)(blockDim.x >> 5) * a.E) + (size_t)warp * a.E;
-    const L* row = static_cast<const L*>(a.logits) + t * a.stride;
-    for (int e = lane; e < a.E; e += 32) x[e] = load_logit(row + e);
-    __syncwarp();
-    int id;
-    if (!decide(a, x, reinterpret_cast<float*>(key), id)) {
-        __syncwarp();
-        decide(a, x, key, id);
-    }
-    // weights: against the largest of the selected, so that they do not underflow together
-    const float mine = id >= 0 ? x[id] : kNone;
+// The weights of a row's experts: lane j has the j-th, its logit `mine` (-inf: none).  Renormalised ones against the largest
+// selected, so that they do not underflow together.
+__device__ __forceinline__ float weight(const RouteArgs& a, float mine, const Scores<float>& s) {
+    const bool some = mine > kNone;
     float w = 0.f;
     if (a.renormalise) {
         float top = warp_max(mine);
         if (a.sigmoid) {
             // sigmoid(x) = e^min(x,0) / (1 + e^-|x|)
             top = fminf(top, 0.f);
-            if (id >= 0) w = expf(fminf(mine, 0.f) - top) / (1.f + expf(-fabsf(mine)));
-        } else if (id >= 0) {
+            if (some) w = expf(fminf(mine, 0.f) - top) / (1.f + expf(-fabsf(mine)));
+        } else if (some) {
             w = expf(mine - top);
         }
         const float sum = warp_sum(w);
-        if (id >= 0) w = w / sum;
-    } else {
-        const Scores<float> s = scores_of<float>(a, x);
-        if (id >= 0) w = s.of(mine);
+        if (some) w = w / sum;
+    } else if (some) {
+        w = s.of(mine);
     }
+    return w * a.scale;
+}
+
+// A row whose logits stand in shared memory (x, E values; key, E values of 64 bits).
+__device__ __noinline__ void route_row(const RouteArgs& a, float* x, double* key, long long t) {
+    const int lane = threadIdx.x & 31;
+    int id;
+    if (!decide(a, x, reinterpret_cast<float*>(key), id)) {
+        __syncwarp();
+        decide(a, x, key, id);
+    }
+    const float mine = id >= 0 ? x[id] : kNone;
+    const float w = weight(a, mine, a.renormalise ? Scores<float>{} : scores_of<float>(a, x));
     if (lane < a.k) {
         a.ids[t * a.k + lane] = id;
-        a.w[t * a.k + lane] = w * a.scale;
+        a.w[t * a.k + lane] = w;
     }
+}
+
+// More than 512 experts.
+template <typename L>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_wide_kernel(const RouteArgs a) {
+    extern __shared__ double route_smem[];
+    pdl_wait_and_release();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long t = (long long)blockIdx.x * (blockDim.x >> 5) + warp;
+    if (t >= a.T) return;
+    float* x = reinterpret_cast<float*>(route_smem + (size_t)(blockDim.x >> 5) * a.E) + (size_t)warp * a.E;
+    const L* row = static_cast<const L*>(a.logits) + t * a.stride;
+    for (int e = lane; e < a.E; e += 32) x[e] = load_logit(row + e);
+    __syncwarp();
+    route_row(a, x, route_smem + (size_t)warp * a.E, t);
+}
+
+__device__ __forceinline__ unsigned ordered(float x) {
+    const unsigned u = __float_as_uint(x);
+    return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(unsigned u) { return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xFFFFFFFFu)); }
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// kEach logits of a lane, in runs of kRun neighbours; element i of a lane is expert index(i).
+template <int kEach>
+struct Held {
+    static constexpr int kRun = kEach < 8 ? kEach : 8;
+    static __device__ __forceinline__ int index(int i) { return (i / kRun * 32 + (int)(threadIdx.x & 31)) * kRun + i % kRun; }
+};
+
+// A warp's logits (-inf past the last expert).  Runs are loaded at once where they are aligned.
+template <typename L, int kEach>
+__device__ __forceinline__ void load_row(float (&x)[kEach], const L* row, int E) {
+    constexpr int kRun = Held<kEach>::kRun, kBytes = kRun * (int)sizeof(L);
+    typedef typename std::conditional<kBytes >= 16, uint4, typename std::conditional<kBytes == 8, uint2, typename std::conditional<kBytes == 4, uint32_t,
+        uint16_t>::type>::type>::type Word;
+    constexpr int kWords = kBytes / (int)sizeof(Word), kIn = kRun / kWords;        // logits in a word
+    const bool whole = ((uintptr_t)row & (sizeof(Word) - 1)) == 0 && E % kRun == 0;
+#pragma unroll
+    for (int r = 0; r < kEach / kRun; ++r) {
+        const int first = Held<kEach>::index(r * kRun);
+        if (whole) {
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                Word v;
+                if (first < E) v = *reinterpret_cast<const Word*>(row + first + w * kIn);
+                const L* in = reinterpret_cast<const L*>(&v);
+#pragma unroll
+                for (int j = 0; j < kIn; ++j) x[r * kRun + w * kIn + j] = first < E ? load_logit(in + j) : kNone;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kRun; ++j) x[r * kRun + j] = first + j < E ? load_logit(row + first + j) : kNone;
+        }
+    }
+}
+
+// What a warp keeps in shared memory for a row: the choices of one with groups, or the logits and 64-bit choices of one that
+// is decided by searches; the logits of one that is decided again; what is ranked.
+template <typename V>
+struct Ranked {
+    V key;
+    float x;
+    int e;
+};
+__host__ __device__ inline size_t route_bytes(int E) { return (((size_t)E * 12 + 15) & ~(size_t)15) + 2 * 32 * sizeof(Ranked<double>); }
+
+__device__ __forceinline__ float score_exp(float x) { return exp2_fast(x * 1.4426950408889634f); }
+__device__ __forceinline__ double score_exp(double x) { return exp(x); }
+__device__ __forceinline__ float inverse(float x) { return __frcp_rn(x); }
+__device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
+
+enum Decided { kSure, kUnsure, kMany };
+
+// A row's k experts by choices of type V; lane j gets the j-th (e -1: none).
+template <typename V, int kEach, bool kByLogit>
+__device__ __forceinline__ Decided pick(const RouteArgs& a, const float (&x)[kEach], uint8_t* mem, Scores<float>& s, Ranked<V>& mine) {
+    constexpr bool k32 = sizeof(V) == 4;
+    const int lane = threadIdx.x & 31;
+    Ranked<V>* ranked = reinterpret_cast<Ranked<V>*>(mem + route_bytes(a.E) - 2 * 32 * sizeof(Ranked<double>));
+    V key[kEach];
+
+    // the choices
+    bool sure = true;
+    V inv = 1;
+    if (kByLogit ? !a.renormalise && !a.sigmoid : !a.sigmoid) {
+        float top = x[0];
+        V sum = 0;
+#pragma unroll
+        for (int i = 1; i < kEach; ++i) top = fmaxf(top, x[i]);
+        top = warp_max(top);
+        if (top == kNone) top = 0.f;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            key[i] = score_exp(V(x[i]) - V(top));
+            sum += key[i];
+        }
+        sum = warp_sum(sum);
+        inv = inverse(sum);
+        s.top = top;
+        s.sum = (float)sum;
+    }
+    if (kByLogit) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) key[i] = x[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int e = Held<kEach>::index(i);
+            const V score = a.sigmoid ? inverse(V(1) + score_exp(-V(x[i]))) : key[i] * inv;
+            const V c = score + (a.bias && e < a.E ? V(a.bias[e]) : V(0));
+            key[i] = x[i] > kNone && c == c ? c : V(kNone);
+        }
+    }
+
+    const float largest = a.sigmoid ? 1.f : (float)inv;            // no score is above it
+    // the groups that stay: some lanes for each group, their two largest choices
+    if (a.n_group > 1) {
+        V* flat = reinterpret_cast<V*>(mem);
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            if (Held<kEach>::index(i) < a.E) flat[Held<kEach>::index(i)] = key[i];
+        __syncwarp();
+        const int g = lane >> a.group_shift, parts = 1 << a.group_shift;
+        V one = kNone, two = kNone;
+        if (g < a.n_group) {
+            for (int i = lane & (parts - 1); i < a.size; i += parts) {
+                const V c = flat[g * a.size + i];
+                two = fmax(two, fmin(one, c));
+                one = fmax(one, c);
+            }
+        }
+        for (int o = 1; o < parts; o <<= 1) {
+            const V c = __shfl_xor_sync(0xffffffffu, one, o), d = __shfl_xor_sync(0xffffffffu, two, o);
+            two = fmax(fmax(two, d), fmin(one, c));
+            one = fmax(one, c);
+        }
+        const V worth = a.group_best == 2 && two > V(kNone) ? one + two : one;
+        int before = 0;
+        for (int i = 0; i < a.n_group; ++i) {
+            const V other = __shfl_sync(0xffffffffu, worth, i << a.group_shift);
+            before += other > worth || (other == worth && i < g);
+        }
+        const bool stays = g < a.n_group && before < a.topk_group;
+        const unsigned kept = __ballot_sync(0xffffffffu, stays);
+        if (!kByLogit && k32) {
+            // the magnitudes of a sum's terms bound its own rounding
+            const float err = score_error(a, largest) * a.group_best +
+                              0x1p-22f * ((one > V(kNone) ? fabsf((float)one) : 0.f) + (two > V(kNone) ? fabsf((float)two) : 0.f));
+            const float least = -warp_max(stays && worth > V(kNone) ? err - (float)worth : kNone);
+            const float most = warp_max(!stays && g < a.n_group && worth > V(kNone) ? (float)worth + err : kNone);
+            sure = least > most || most == kNone;
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int of = (int)(((unsigned)Held<kEach>::index(i) * a.group_mul) >> 20);
+            if (of >= a.n_group || !(kept >> (of << a.group_shift) & 1)) key[i] = kNone;
+        }
+        __syncwarp();
+    }
+    if (!sure) return kUnsure;
+
+    // the bound: of the lanes' maxima (as fp32, whose order is theirs), largest first, the (k + 1)-th; by logits the k-th is enough
+    V most = key[0];
+#pragma unroll
+    for (int i = 1; i < kEach; ++i) most = fmax(most, key[i]);
+    unsigned left = ordered((float)most), bound = ordered(kNone);
+    for (int n = 0; n < a.k + (kByLogit ? 0 : 1);) {
+        bound = __reduce_max_sync(0xffffffffu, left);
+        if (bound <= ordered(kNone)) break;
+        const bool is = left == bound;
+        n += __popc(__ballot_sync(0xffffffffu, is));
+        if (is) left = 0;
+    }
+    const float least = bound <= ordered(kNone) ? kNone : unordered(bound);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const bool in = (float)key[i] >= least && key[i] > V(kNone);
+        const unsigned who = __ballot_sync(0xffffffffu, in);
+        const int at = n + __popc(who & ((1u << lane) - 1));
+        if (in && at < 32) ranked[at] = Ranked<V>{key[i], x[i], Held<kEach>::index(i)};
+        n += __popc(who);
+    }
+    if (n > 32) return kMany;           // too few maxima to bound the (k + 1)-th choice, or many equal ones
+    __syncwarp();
+    mine = Ranked<V>{V(kNone), kNone, -1};
+    int rank = lane;
+    if (lane < n) {
+        mine = ranked[lane];
+        rank = 0;
+        for (int i = 0; i < n; ++i) rank += ranked[i].key > mine.key || (ranked[i].key == mine.key && ranked[i].e < mine.e);
+    }
+    ranked[32 + rank] = mine;                                      // those without one behind
+    __syncwarp();
+    mine = ranked[32 + lane];
+    if (!kByLogit && k32) {
+        const float key0 = (float)__shfl_up_sync(0xffffffffu, mine.key, 1), x0 = __shfl_up_sync(0xffffffffu, mine.x, 1);
+        const int e0 = __shfl_up_sync(0xffffffffu, mine.e, 1);
+        bool near = false;
+        if (lane > 0 && lane <= a.k && mine.e >= 0) {
+            const float key1 = (float)mine.key, b0 = a.bias ? a.bias[e0] : 0.f, b1 = a.bias ? a.bias[mine.e] : 0.f;
+            near = !(x0 == mine.x && b0 == b1) && too_near(a, key0, key1, largest);
+        }
+        if (__any_sync(0xffffffffu, near)) return kUnsure;
+    }
+    return kSure;
+}
+
+// The same in 64 bits, by searches where a lane each is not enough for what is ranked.
+template <int kEach>
+__device__ __noinline__ void pick_again(const RouteArgs& a, uint8_t* mem, Scores<float> s, bool many, long long t) {
+    const int lane = threadIdx.x & 31;
+    float* again = reinterpret_cast<float*>(mem + (size_t)a.E * 8);
+    if (!many) {
+        float x[kEach];
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) x[i] = Held<kEach>::index(i) < a.E ? again[Held<kEach>::index(i)] : kNone;
+        Ranked<double> mine;
+        if (pick<double, kEach, false>(a, x, mem, s, mine) == kSure) {
+            const bool some = lane < a.k && mine.e >= 0;
+            const float w = weight(a, some ? mine.x : kNone, s);
+            if (lane < a.k) {
+                a.ids[t * a.k + lane] = some ? mine.e : -1;
+                a.w[t * a.k + lane] = w;
+            }
+            return;
+        }
+        __syncwarp();
+    }
+    route_row(a, again, reinterpret_cast<double*>(mem), t);
+}
+
+template <typename L, int kEach, bool kByLogit>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs a) {
+    extern __shared__ __align__(16) uint8_t route_mem[];
+    pdl_wait_and_release();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long t = (long long)blockIdx.x * kRouteWarps + warp;
+    if (t >= a.T) return;
+    uint8_t* mem = route_mem + warp * route_bytes(a.E);
+    float x[kEach];
+    load_row<L, kEach>(x, static_cast<const L*>(a.logits) + t * a.stride, a.E);
+    Scores<float> s{0.f, 1.f, a.sigmoid};
+    Ranked<float> mine;
+    const Decided d = pick<float, kEach, kByLogit>(a, x, mem, s, mine);
+    if (d == kSure) {
+        const bool some = lane < a.k && mine.e >= 0;
+        const float w = weight(a, some ? mine.x : kNone, s);
+        if (lane < a.k) {
+            a.ids[t * a.k + lane] = some ? mine.e : -1;
+            a.w[t * a.k + lane] = w;
+        }
+        return;
+    }
+    float* again = reinterpret_cast<float*>(mem + (size_t)a.E * 8);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+        if (Held<kEach>::index(i) < a.E) again[Held<kEach>::index(i)] = x[i];
+    __syncwarp();
+    pick_again<kEach>(a, mem, s, kByLogit || d == kMany, t);
+}
+
+template <typename L, int kEach, bool kByLogit>
+cudaError_t launch(const RouteArgs& a, cudaStream_t s) {
+    return launch_pdl(route_kernel<L, kEach, kByLogit>, dim3((unsigned)((a.T + (long long)kRouteWarps - 1) / kRouteWarps)), dim3(kRouteWarps * 32),
+                      kRouteWarps * route_bytes(a.E), s, a);
+}
+
+// Lanes hold as few logits as E takes.
+template <typename L, bool kByLogit>
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
+    if (a.E <= 32) return launch<L, 1, kByLogit>(a, s);
+    if (a.E <= 64) return launch<L, 2, kByLogit>(a, s);
+    if (a.E <= 128) return launch<L, 4, kByLogit>(a, s);
+    if (a.E <= 256) return launch<L, 8, kByLogit>(a, s);
+    if (a.E <= 512) return launch<L, 16, kByLogit>(a, s);
+    const int warps = a.E > 1024 ? 1 : kRouteWarps;
+    return launch_pdl(route_wide_kernel<L>, dim3((unsigned)((a.T + (long long)warps - 1) / warps)), dim3(warps * 32), (size_t)warps * a.E * 12, s, a);
 }
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
@@ -239,10 +532,11 @@ extern "C" ft_status ft_moe_route(const ft_route* call, void* stream) {
     a.renormalise = c.renormalise != 0;
     a.by_logit = !c.bias && (c.n_group == 1 || c.group_best == 1);
     a.scale = c.scale;
-    const int warps = c.E > 1024 ? 1 : kRouteWarps;
-    const size_t smem = (size_t)warps * c.E * 12;                // at most 48 KB
-    const unsigned ctas = (unsigned)((c.T + (long long)warps - 1) / warps);
-    const cudaError_t e = launch_pdl(c.dtype == FT_DTYPE_BF16 ? route_kernel<__nv_bfloat16> : route_kernel<float>, dim3(ctas),
-                                     dim3(warps * 32), smem, static_cast<cudaStream_t>(stream), a);
+    a.group_shift = 0;
+    while (c.n_group << (a.group_shift + 1) <= 32) ++a.group_shift;
+    a.group_mul = ((1u << 20) + a.size - 1) / a.size;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = c.dtype == FT_DTYPE_BF16 ? (a.by_logit ? launch_route<__nv_bfloat16, true>(a, s) : launch_route<__nv_bfloat16, false>(a, s))
+                                                   : (a.by_logit ? launch_route<float, true>(a, s) : launch_route<float, false>(a, s));
     return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }

@@ -105,6 +105,25 @@ def test_choices_closer_than_fp32_tells(ft, score):
         check(t, *run(ft, t, 6, **kw), 6, **kw)
 
 
+@pytest.mark.parametrize("E", [64, 600])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_large_score_passes_between_two_small_ones(ft, score, E):
+    """A large score with a bias far below it, and so a larger error, rises past the last that is chosen and the first that is
+    not, which lie further apart than their own errors."""
+    T = 2000
+    x = np.full((T, E), -4.0, np.float32)
+    x[:, 1], x[:, 2], x[:, 3] = 0.0, -1.0, -2.0
+    x[:, 0] = 2.2 + (np.arange(T) - T / 2) * 2.0 ** -21
+    p = np.exp(x[T // 2].astype(np.float64))
+    sc = p / p.sum() if score == "softmax" else p / (1 + p)
+    bias = np.full(E, -1.0, np.float32)
+    bias[1], bias[2], bias[3] = 0.5 - sc[1], 0.3 - sc[2], 0.3 - 5e-7 - sc[3]
+    bias[0] = 0.3 - 2.5e-7 - sc[0]
+    t = torch.from_numpy(x).cuda()
+    kw = dict(score=score, bias=bias)
+    check(t, *run(ft, t, 2, **kw), 2, rows=range(T // 2 - 150, T // 2 + 150), **kw)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_what_is_masked(ft, score, dtype):
