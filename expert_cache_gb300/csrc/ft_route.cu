@@ -284,6 +284,40 @@ __device__ __forceinline__ double score_exp(double x) { return exp(x); }
 __device__ __forceinline__ float inverse(float x) { return __frcp_rn(x); }
 __device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
 
+// Ranks the n choices of the lanes (logit mine, expert e) in 64 bits; returns the lane's logit and expert (as its bits).
+template <int kEach>
+__device__ __noinline__ float2 rank_again(const RouteArgs& a, const float* x, float top, float mine, int e, int n) {
+    const int lane = threadIdx.x & 31;
+    double choice = kNone;
+    if (a.sigmoid) {
+        if (lane < n) choice = 1.0 / (1.0 + exp(-(double)mine));
+    } else {
+        double p[kEach], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) p[i] = Held<kEach>::index(i) < a.E ? exp((double)x[Held<kEach>::index(i)] - top) : 0.0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) sum += p[i];
+        sum = warp_sum(sum);
+        if (lane < n) choice = exp((double)mine - top) / sum;
+    }
+    if (a.bias && lane < n) choice += (double)a.bias[e];
+    int rank = lane < n ? 0 : lane;
+    for (int i = 0; i < n; ++i) {
+        const double c = __shfl_sync(0xffffffffu, choice, i);
+        const int of = __shfl_sync(0xffffffffu, e, i);
+        if (lane < n) rank += c > choice || (c == choice && of < e);
+    }
+    // to the lane of its rank
+    float2 out = make_float2(kNone, __int_as_float(-1));
+    for (int i = 0; i < n; ++i) {
+        const int to = __shfl_sync(0xffffffffu, rank, i);
+        const float y = __shfl_sync(0xffffffffu, mine, i);
+        const int of = __shfl_sync(0xffffffffu, e, i);
+        if (lane == to) out = make_float2(y, __int_as_float(of));
+    }
+    return out;
+}
+
 enum Decided { kSure, kUnsure, kMany };
 
 // A row's k experts by choices of type V; lane j gets the j-th (e -1: none).
@@ -386,7 +420,8 @@ __device__ __forceinline__ Decided pick(const RouteArgs& a, const float (&x)[kEa
         n += __popc(__ballot_sync(0xffffffffu, is));
         if (is) left = 0;
     }
-    const float least = bound <= ordered(kNone) ? kNone : unordered(bound);
+    float least = bound <= ordered(kNone) ? kNone : unordered(bound);
+    if (!kByLogit && k32) least -= 2.f * (2.f * score_error(a, largest) + 0x1p-21f * fabsf(least));        // nothing that may be a (k + 1)-th is left out
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -416,7 +451,17 @@ __device__ __forceinline__ Decided pick(const RouteArgs& a, const float (&x)[kEa
             const float key1 = (float)mine.key, b0 = a.bias ? a.bias[e0] : 0.f, b1 = a.bias ? a.bias[mine.e] : 0.f;
             near = !(x0 == mine.x && b0 == b1) && too_near(a, key0, key1, largest);
         }
-        if (__any_sync(0xffffffffu, near)) return kUnsure;
+        if (__any_sync(0xffffffffu, near)) {
+            // the row's logits, for the sum in 64 bits
+            float* again = reinterpret_cast<float*>(mem + (size_t)a.E * 8);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (Held<kEach>::index(i) < a.E) again[Held<kEach>::index(i)] = x[i];
+            __syncwarp();
+            const float2 m = rank_again<kEach>(a, again, s.top, mine.x, mine.e, n);
+            mine.x = m.x;
+            mine.e = __float_as_int(m.y);
+        }
     }
     return kSure;
 }
