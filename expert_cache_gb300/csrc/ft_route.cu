@@ -235,10 +235,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// kEach logits of a lane, in runs of kRun neighbours; element i of a lane is expert index(i).
+// kEach logits of a lane, in runs of kRun neighbours; element i of a lane is expert index(i).  Runs of two: of the experts of a group,
+// or of neighbours that come out on top together, hardly two are a lane's, and its maximum bounds little else (runs of eight, one
+// load each: 3 of 8 groups left 8 lanes and often more than 32 experts to rank, 16 us instead of 9 us for 5003 tokens of 160).
 template <int kEach>
 struct Held {
-    static constexpr int kRun = kEach < 8 ? kEach : 8;
+    static constexpr int kRun = kEach < 2 ? kEach : 2;
     static __device__ __forceinline__ int index(int i) { return (i / kRun * 32 + (int)(threadIdx.x & 31)) * kRun + i % kRun; }
 };
 
@@ -246,26 +248,21 @@ struct Held {
 template <typename L, int kEach>
 __device__ __forceinline__ void load_row(float (&x)[kEach], const L* row, int E) {
     constexpr int kRun = Held<kEach>::kRun, kBytes = kRun * (int)sizeof(L);
-    typedef typename std::conditional<kBytes >= 16, uint4, typename std::conditional<kBytes == 8, uint2, typename std::conditional<kBytes == 4, uint32_t,
-        uint16_t>::type>::type>::type Word;
-    constexpr int kWords = kBytes / (int)sizeof(Word), kIn = kRun / kWords;        // logits in a word
+    typedef typename std::conditional<kBytes == 8, uint2, typename std::conditional<kBytes == 4, uint32_t, uint16_t>::type>::type Word;
     const bool whole = ((uintptr_t)row & (sizeof(Word) - 1)) == 0 && E % kRun == 0;
+    if (whole) {
+        Word v[kEach / kRun];                                      // all of them under way at once
 #pragma unroll
-    for (int r = 0; r < kEach / kRun; ++r) {
-        const int first = Held<kEach>::index(r * kRun);
-        if (whole) {
+        for (int r = 0; r < kEach / kRun; ++r) v[r] = *reinterpret_cast<const Word*>(row + min(Held<kEach>::index(r * kRun), E - kRun));
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                Word v;
-                if (first < E) v = *reinterpret_cast<const Word*>(row + first + w * kIn);
-                const L* in = reinterpret_cast<const L*>(&v);
+        for (int i = 0; i < kEach; ++i)
+            x[i] = Held<kEach>::index(i) < E ? load_logit(reinterpret_cast<const L*>(&v[i / kRun]) + i % kRun) : kNone;
+    } else {
+        L v[kEach];
 #pragma unroll
-                for (int j = 0; j < kIn; ++j) x[r * kRun + w * kIn + j] = first < E ? load_logit(in + j) : kNone;
-            }
-        } else {
+        for (int i = 0; i < kEach; ++i) v[i] = row[min(Held<kEach>::index(i), E - 1)];
 #pragma unroll
-            for (int j = 0; j < kRun; ++j) x[r * kRun + j] = first + j < E ? load_logit(row + first + j) : kNone;
-        }
+        for (int i = 0; i < kEach; ++i) x[i] = Held<kEach>::index(i) < E ? load_logit(&v[i]) : kNone;
     }
 }
 
@@ -284,24 +281,45 @@ __device__ __forceinline__ double score_exp(double x) { return exp(x); }
 __device__ __forceinline__ float inverse(float x) { return __frcp_rn(x); }
 __device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
 
-// Ranks the n choices of the lanes (logit mine, expert e) in 64 bits; returns the lane's logit and expert (as its bits).
-template <int kEach>
+// e^y for y <= 0 (below -700: e^-700) to some 2^-51: y = n ln 2 + r with ln 2 in two parts (Cody and Waite 1980), the first of 41 bits, so
+// that n times it is exact; Taylor's series to r^13 / 13!, whose rest is below 2^-57 for |r| <= ln 2 / 2.
+__device__ __forceinline__ double exp_negative(double y) {
+    y = fmax(y, -700.0);
+    const double n = rint(y * 1.4426950408889634);
+    const double r = fma(n, -0x1.3de6af278ece6p-42, fma(n, -0x1.62e42fefa3000p-1, y));
+    double p = 1.0 / 6227020800.0;
+    constexpr double c[] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320, 1.0 / 362880, 1.0 / 3628800,
+                            1.0 / 39916800, 1.0 / 479001600};
+#pragma unroll
+    for (int i = 12; i >= 0; --i) p = fma(p, r, c[i]);
+    return __longlong_as_double(__double_as_longlong(p) + ((long long)(int)n << 52));
+}
+
+// 1 / x to some 2^-52 for a normal fp32 range of x: two steps of Newton's from the fp32 reciprocal.
+__device__ __forceinline__ double inverse_double(double x) {
+    double r = 1.0f / (float)x;
+    r = fma(r, fma(-x, r, 1.0), r);
+    return fma(r, fma(-x, r, 1.0), r);
+}
+
+// Ranks the n choices of the lanes (logit mine, expert e) in 64 bits; returns the lane's logit and expert (as its bits).  Little
+// code, rolled: it is fetched while the row's warp waits (a few KB of it took 6 us).
 __device__ __noinline__ float2 rank_again(const RouteArgs& a, const float* x, float top, float mine, int e, int n) {
     const int lane = threadIdx.x & 31;
-    double choice = kNone;
-    if (a.sigmoid) {
-        if (lane < n) choice = 1.0 / (1.0 + exp(-(double)mine));
-    } else {
-        double p[kEach], sum = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) p[i] = Held<kEach>::index(i) < a.E ? exp((double)x[Held<kEach>::index(i)] - top) : 0.0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) sum += p[i];
+    double sum = 0;
+    if (!a.sigmoid) {
+#pragma unroll 1
+        for (int i = lane; i < a.E; i += 32) sum += exp_negative((double)x[i] - top);
         sum = warp_sum(sum);
-        if (lane < n) choice = exp((double)mine - top) / sum;
     }
-    if (a.bias && lane < n) choice += (double)a.bias[e];
+    double choice = kNone;
+    if (lane < n) {
+        const double p = exp_negative(a.sigmoid ? -fabs((double)mine) : (double)mine - top);
+        choice = (a.sigmoid && mine >= 0.f ? 1.0 : p) * inverse_double(a.sigmoid ? 1.0 + p : sum);
+        if (a.bias) choice += (double)a.bias[e];
+    }
     int rank = lane < n ? 0 : lane;
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
         const double c = __shfl_sync(0xffffffffu, choice, i);
         const int of = __shfl_sync(0xffffffffu, e, i);
@@ -309,6 +327,7 @@ __device__ __noinline__ float2 rank_again(const RouteArgs& a, const float* x, fl
     }
     // to the lane of its rank
     float2 out = make_float2(kNone, __int_as_float(-1));
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
         const int to = __shfl_sync(0xffffffffu, rank, i);
         const float y = __shfl_sync(0xffffffffu, mine, i);
@@ -353,12 +372,16 @@ __device__ __forceinline__ Decided pick(const RouteArgs& a, const float (&x)[kEa
         for (int i = 0; i < kEach; ++i) key[i] = x[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const int e = Held<kEach>::index(i);
-            const V score = a.sigmoid ? inverse(V(1) + score_exp(-V(x[i]))) : key[i] * inv;
-            const V c = score + (a.bias && e < a.E ? V(a.bias[e]) : V(0));
-            key[i] = x[i] > kNone && c == c ? c : V(kNone);
+        for (int i = 0; i < kEach; ++i) key[i] = a.sigmoid ? inverse(V(1) + score_exp(-V(x[i]))) : key[i] * inv;
+        if (a.bias) {
+            float bias[kEach];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) bias[i] = a.bias[min(Held<kEach>::index(i), a.E - 1)];
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) key[i] += V(bias[i]);
         }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) key[i] = x[i] > kNone && key[i] == key[i] ? key[i] : V(kNone);
     }
 
     const float largest = a.sigmoid ? 1.f : (float)inv;            // no score is above it
@@ -458,7 +481,7 @@ __device__ __forceinline__ Decided pick(const RouteArgs& a, const float (&x)[kEa
             for (int i = 0; i < kEach; ++i)
                 if (Held<kEach>::index(i) < a.E) again[Held<kEach>::index(i)] = x[i];
             __syncwarp();
-            const float2 m = rank_again<kEach>(a, again, s.top, mine.x, mine.e, n);
+            const float2 m = rank_again(a, again, s.top, mine.x, mine.e, n);
             mine.x = m.x;
             mine.e = __float_as_int(m.y);
         }
