@@ -426,6 +426,7 @@ def ft_kv_destroy(handle):
 
 
 _bf16 = _i32 = _f32 = _f64 = _i64 = _u64 = None             # torch's types, known from the first handle on
+_DTYPES = {}                                                # types of logits
 
 
 def _load_types():
@@ -435,6 +436,7 @@ def _load_types():
     except ImportError:                                     # raw addresses only
         return
     _bf16, _i32, _f32, _f64, _i64, _u64 = torch.bfloat16, torch.int32, torch.float32, torch.float64, torch.int64, torch.uint64
+    _DTYPES.update({_bf16: FT_DTYPE_BF16, _f32: FT_DTYPE_F32})
 
 
 def _refuse(t, what, needs):
@@ -562,26 +564,30 @@ _kv_plan, _kv_append_rotated, _moe_route, _logprobs = (
 
 def ft_kv_plan(handle, n_new, len, held, block_table, table_stride, free_pages, n_free, n_seqs, n_tokens, q_start, kv_len, slots,
                len_out, held_out, n_free_out, positions=None, tree_mask=None, stream=None):
-    ints = (n_new, len, held, n_free, free_pages, q_start, kv_len, slots, len_out, held_out, n_free_out)
+    i32 = _i32
+    pp = pm = 0
     try:
-        p = [t.data_ptr() for t in ints]
-        plain = True
-        for t in ints:
-            if t.dtype is not _i32 or not t.is_contiguous():
-                plain = False
-        pt, pp, pm = block_table.data_ptr(), 0, 0
-        plain = plain and block_table.dtype is _i32 and block_table.is_contiguous()
+        p = (n_new.data_ptr(), len.data_ptr(), held.data_ptr(), n_free.data_ptr(), free_pages.data_ptr(), q_start.data_ptr(),
+             kv_len.data_ptr(), slots.data_ptr(), len_out.data_ptr(), held_out.data_ptr(), n_free_out.data_ptr())
+        pt = block_table.data_ptr()
+        plain = (n_new.dtype is i32 and len.dtype is i32 and held.dtype is i32 and n_free.dtype is i32 and free_pages.dtype is i32
+                 and q_start.dtype is i32 and kv_len.dtype is i32 and slots.dtype is i32 and len_out.dtype is i32
+                 and held_out.dtype is i32 and n_free_out.dtype is i32 and block_table.dtype is i32
+                 and n_new.is_contiguous() and len.is_contiguous() and held.is_contiguous() and n_free.is_contiguous()
+                 and free_pages.is_contiguous() and q_start.is_contiguous() and kv_len.is_contiguous() and slots.is_contiguous()
+                 and len_out.is_contiguous() and held_out.is_contiguous() and n_free_out.is_contiguous() and block_table.is_contiguous())
         if positions is not None:
             pp = positions.data_ptr()
-            plain = plain and positions.dtype is _i32 and positions.is_contiguous()
+            plain = plain and positions.dtype is i32 and positions.is_contiguous()
         if tree_mask is not None:
             pm = tree_mask.data_ptr()
             plain = plain and tree_mask.dtype is _i64 and tree_mask.is_contiguous()
     except AttributeError:
         plain = False
     if not plain:
-        names = ("n_new", "len", "held", "n_free", "free_pages", "q_start", "kv_len", "slots", "len_out", "held_out", "n_free_out")
-        p = [_address(t, _i32, f"plan: {name}") for t, name in zip(ints, names)]
+        p = [_address(t, _i32, f"plan: {name}") for t, name in (
+            (n_new, "n_new"), (len, "len"), (held, "held"), (n_free, "n_free"), (free_pages, "free_pages"), (q_start, "q_start"),
+            (kv_len, "kv_len"), (slots, "slots"), (len_out, "len_out"), (held_out, "held_out"), (n_free_out, "n_free_out"))]
         pt = _address(block_table, _i32, "plan: block_table", False)             # its rows may be parts of longer ones
         if pt and not isinstance(block_table, int) and not (block_table.is_contiguous() or block_table.stride(-1) == 1):
             _refuse(block_table, "plan: block_table", "dense rows")
@@ -666,9 +672,23 @@ def _logits(t, width, what, stride, dtype):
 def ft_moe_route(logits, T, E, k, topk_ids, topk_w, score="softmax", bias=None, n_group=1, topk_group=1, group_best=1, renormalise=True,
                  scale=1.0, stride=None, dtype="bf16", stream=None):
     """dtype ("bf16" or "fp32") names the type of logits that are given as a raw address."""
-    pl, dt, stride = _logits(logits, E, "route: logits", stride, dtype)
-    pi, pw, pb = _address(topk_ids, _i32, "route: topk_ids"), _address(topk_w, _f32, "route: topk_w"), _address(bias, _f32, "route: bias")
-    status = _moe_route(_ROUTE.pack(pl, pb, pi, pw, stride, T, E, k, dt, ROUTE_SCORES[score], n_group, topk_group, group_best,
+    pb = 0
+    try:
+        pl, pi, pw, dt = logits.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(), _DTYPES.get(logits.dtype)
+        plain = dt is not None and topk_ids.dtype is _i32 and topk_w.dtype is _f32 and topk_ids.is_contiguous() and topk_w.is_contiguous()
+        if bias is not None:
+            pb = bias.data_ptr()
+            plain = plain and bias.dtype is _f32 and bias.is_contiguous()
+        step = stride
+        if step is None:
+            step = logits.stride(0)
+            plain = plain and logits.is_contiguous() and step >= E and logits.dim() == 2
+    except (AttributeError, IndexError):
+        plain = False
+    if not plain:
+        pl, dt, step = _logits(logits, E, "route: logits", stride, dtype)
+        pi, pw, pb = _address(topk_ids, _i32, "route: topk_ids"), _address(topk_w, _f32, "route: topk_w"), _address(bias, _f32, "route: bias")
+    status = _moe_route(_ROUTE.pack(pl, pb, pi, pw, step, T, E, k, dt, ROUTE_SCORES[score], n_group, topk_group, group_best,
                                     bool(renormalise), scale), _stream(stream))
     if status:
         _check(status)
@@ -677,11 +697,31 @@ def ft_moe_route(logits, T, E, k, topk_ids, topk_w, score="softmax", bias=None, 
 def ft_logprobs(logits, n, V, tokens=None, logp=None, entropy=None, top_ids=None, top_logp=None, k=0, scale=1.0, stride=None, dtype="bf16",
                 stream=None):
     """dtype ("bf16" or "fp32") names the type of logits that are given as a raw address."""
-    pl, dt, stride = _logits(logits, V, "logprobs: logits", stride, dtype)
-    pt, pi = _address(tokens, _i32, "logprobs: tokens"), _address(top_ids, _i32, "logprobs: top_ids")
-    pp, pe, px = (_address(t, _f32, what) for t, what in (
-        (logp, "logprobs: logp"), (entropy, "logprobs: entropy"), (top_logp, "logprobs: top_logp")))
-    status = _logprobs(_LOGPROB.pack(pl, pt, pp, pe, pi, px, stride, n, V, k, dt, scale), _stream(stream))
+    pt = pp = pe = pi = px = 0
+    try:
+        pl, dt = logits.data_ptr(), _DTYPES.get(logits.dtype)
+        plain = dt is not None
+        if logp is not None:
+            pt, pp = tokens.data_ptr(), logp.data_ptr()
+            plain = plain and tokens.dtype is _i32 and logp.dtype is _f32 and tokens.is_contiguous() and logp.is_contiguous()
+        if entropy is not None:
+            pe = entropy.data_ptr()
+            plain = plain and entropy.dtype is _f32 and entropy.is_contiguous()
+        if top_ids is not None:
+            pi, px = top_ids.data_ptr(), top_logp.data_ptr()
+            plain = plain and top_ids.dtype is _i32 and top_logp.dtype is _f32 and top_ids.is_contiguous() and top_logp.is_contiguous()
+        step = stride
+        if step is None:
+            step = logits.stride(0)
+            plain = plain and logits.is_contiguous() and step >= V and logits.dim() == 2
+    except (AttributeError, IndexError):
+        plain = False
+    if not plain:
+        pl, dt, step = _logits(logits, V, "logprobs: logits", stride, dtype)
+        pt, pi = _address(tokens, _i32, "logprobs: tokens"), _address(top_ids, _i32, "logprobs: top_ids")
+        pp, pe, px = (_address(t, _f32, what) for t, what in (
+            (logp, "logprobs: logp"), (entropy, "logprobs: entropy"), (top_logp, "logprobs: top_logp")))
+    status = _logprobs(_LOGPROB.pack(pl, pt, pp, pe, pi, px, step, n, V, k, dt, scale), _stream(stream))
     if status:
         _check(status)
 

@@ -33,14 +33,14 @@ __device__ __forceinline__ void block_sums(const long long (&v)[N], long long (&
         if (lane == 31) buf[i][warp] = incl[i];
     }
     __syncthreads();
-    if (warp < N) {
-        long long w = lane < warps ? buf[warp][lane] : 0;
+    for (int i = warp; i < N; i += warps) {
+        long long w = lane < warps ? buf[i][lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long t = __shfl_up_sync(0xffffffffu, w, o);
             if (lane >= o) w += t;
         }
-        buf[warp][lane] = w;
+        buf[i][lane] = w;
     }
     __syncthreads();
 #pragma unroll
@@ -68,7 +68,7 @@ __device__ __forceinline__ int count_up_to(const T* at, int n, T x) {
 __global__ void __launch_bounds__(kMaxSeqs) kv_plan_kernel(const PlanArgs a) {
     __shared__ int end[kMaxSeqs], len[kMaxSeqs], held[kMaxSeqs], want[kMaxSeqs];       // end: row after a sequence's last
     __shared__ long long taken[kMaxSeqs], given_end[kMaxSeqs];                          // taken: before it, -1 if it is refused
-    __shared__ long long buf[2][33];
+    __shared__ long long buf[3][33];
     pdl_wait_and_release();
     const ft_kv_step& c = a.c;
     const int s = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
@@ -95,27 +95,28 @@ __global__ void __launch_bounds__(kMaxSeqs) kv_plan_kernel(const PlanArgs a) {
     if (!ends)
         fine = fine && l >= 0 && (((long long)l + page - 1) >> a.page_shift) <= h && wants <= c.table_stride && after <= 0x7FFFFFFFLL &&
                (!c.tree_mask || rows <= kTreeMax);
-    const long long r[1] = {rows};
-    long long first[1], all_rows[1];
-    block_sums<1>(r, first, all_rows, buf);
-    fine = fine && (rows == 0 || first[0] + rows <= c.n_tokens);
+    long long v[3] = {rows, fine ? max(wants - h, 0LL) : 0, fine ? max(h - wants, 0LL) : 0}, before[3], total[3];
+    block_sums<3>(v, before, total, buf);
+    const long long first = before[0], all_rows = total[0];
+    if (all_rows > c.n_tokens) {                                 // those whose rows do not all fit take and give nothing
+        fine = fine && (rows == 0 || first + rows <= c.n_tokens);
+        if (!fine) v[1] = v[2] = 0;
+        block_sums<3>(v, before, total, buf);
+    }
     if (!fine) bits |= FT_DEV_BAD_ID;
-    const long long v[2] = {fine ? max(wants - h, 0LL) : 0, fine ? max(h - wants, 0LL) : 0};
-    long long before[2], total[2];
-    block_sums<2>(v, before, total, buf);
-    const long long avail = n_free + total[1];
-    const bool served = fine && (v[0] == 0 || before[0] + v[0] <= avail);
+    const long long avail = n_free + total[2];
+    const bool served = fine && (v[1] == 0 || before[1] + v[1] <= avail);
     if (fine && !served) bits |= FT_DEV_NO_PAGES;
     if (s < c.n_seqs) {
-        end[s] = (int)min(first[0] + rows, (long long)c.n_tokens);
+        end[s] = (int)min(first + rows, (long long)c.n_tokens);
         len[s] = l;
         held[s] = h;
         want[s] = (int)wants;
-        taken[s] = served ? before[0] : -1;
-        given_end[s] = before[1] + v[1];
+        taken[s] = served ? before[1] : -1;
+        given_end[s] = before[2] + v[2];
     }
     // the pages that leave the stack: those of the last sequence that is served with any
-    long long all_taken = served && v[0] ? before[0] + v[0] : 0;
+    long long all_taken = served && v[1] ? before[1] + v[1] : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) all_taken = max(all_taken, __shfl_xor_sync(0xffffffffu, all_taken, o));
     if ((s & 31) == 0) buf[0][s >> 5] = all_taken;
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kMaxSeqs) kv_plan_kernel(const PlanArgs a) {
         return c.block_table[(size_t)q * c.table_stride + want[q] + (g - (q ? given_end[q - 1] : 0))];
     };
     const int at = rank * blockDim.x + threadIdx.x, step = ctas * blockDim.x;
-    const int live = (int)min(all_rows[0], (long long)c.n_tokens);
+    const int live = (int)min(all_rows, (long long)c.n_tokens);
     for (int t = at; t < c.n_tokens; t += step) {
         int slot = -1, pos = 0;
         if (t < live) {

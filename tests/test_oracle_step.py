@@ -310,7 +310,12 @@ def test_route_and_logprobs_look_at_their_arrays(ft, calls):
     ft.ft_moe_route(**(good | dict(logits=bf16(1, 64), T=1, score="sigmoid", bias=None, renormalise=False)))
     got = ft._ROUTE.unpack(calls.pop("moe_route")[0])
     assert got[1] == 0 and got[4:15] == (64, 1, 64, 4, ft.FT_DTYPE_BF16, ft.FT_ROUTE_SIGMOID, 1, 1, 1, 0, 1.0)
-    for n, ts in dict(logits=[wide.half(), wide.double(), torch.zeros(64, 6).t(), torch.zeros(6, 128)[:, ::2]], topk_ids=[i32(6, 8)[:, ::2], i32(6, 4).long()],
+    one = torch.zeros(8, 64)[:1].as_strided((1, 64), (0, 1))                     # the stride of a single row says nothing
+    ft.ft_moe_route(**(good | dict(logits=one, T=1)))
+    assert ft._ROUTE.unpack(calls.pop("moe_route")[0])[4] == 64
+    ft.ft_moe_route(**(good | dict(logits=torch.zeros(6, 100))))                 # more columns than experts
+    assert ft._ROUTE.unpack(calls.pop("moe_route")[0])[4] == 100
+    for n, ts in dict(logits=[torch.zeros(3, 2, 64), torch.zeros(64), torch.zeros(()), wide.half(), wide.double(), torch.zeros(64, 6).t(), torch.zeros(6, 128)[:, ::2]], topk_ids=[i32(6, 8)[:, ::2], i32(6, 4).long()],
                       topk_w=[bf16(6, 4), torch.zeros(4, 6).t()], bias=[bf16(64), torch.zeros(128)[::2]]).items():
         for t in ts:
             misread(ft, f"route: {n}", lambda: ft.ft_moe_route(**(good | {n: t})))
@@ -319,7 +324,7 @@ def test_route_and_logprobs_look_at_their_arrays(ft, calls):
     ft.ft_logprobs(**good)
     got = ft._LOGPROB.unpack(calls.pop("logprobs")[0])
     assert got == (*(good[n].data_ptr() for n in ("logits", "tokens", "logp", "entropy", "top_ids", "top_logp")), 70, 6, 64, 4, ft.FT_DTYPE_BF16, 0.5)
-    for n, ts in dict(logits=[wide.half(), torch.zeros(64, 6).t()], tokens=[i32(12)[::2], i32(6).long()], logp=[bf16(6)], entropy=[torch.zeros(12)[::2]],
+    for n, ts in dict(logits=[torch.zeros(3, 2, 64), torch.zeros(64), torch.zeros(()), wide.half(), torch.zeros(64, 6).t()], tokens=[i32(12)[::2], i32(6).long()], logp=[bf16(6)], entropy=[torch.zeros(12)[::2]],
                       top_ids=[i32(6, 4).long()], top_logp=[torch.zeros(4, 6).t()]).items():
         for t in ts:
             misread(ft, f"logprobs: {n}", lambda: ft.ft_logprobs(**(good | {n: t})))
