@@ -2,12 +2,16 @@
 expert cache, run three ways over the same text: one token per step, the prompt in chunks, and trees
 of drafted tokens verified in one step.
 
-    python examples/tree_decode.py [--fmt nvfp4|fp8] [--tokens N]
+    python examples/tree_decode.py [--fmt nvfp4|fp8] [--tokens N] [--served]
 
 Every layer call is the order a serving loop has: ft_kv_append stores the step's new tokens,
 ft_kv_attention reads the cache (the odd layers through a sliding window with two sink tokens),
 ft_moe_decode adds the routed experts.  Weights are random; a drafter is stood in for by the tokens
 of a first run among wrong ones.
+
+With --served everything around these is the library's too: ft_kv_plan makes the step's rows, slots and positions and
+hands out pages, ft_kv_append_rotated normalises and turns queries and keys on their way into the cache (in place of
+the embedding of places), ft_moe_route picks the experts and ft_logprobs the tokens.
 """
 from __future__ import annotations
 
@@ -99,6 +103,10 @@ class Decoder:
             ft.ft_kv_append(self.kv.handle, l, k[pick], v[pick], slots, len(path))
         self.len = base + len(path)
 
+    def best(self, logits):
+        """The most likely token after each row."""
+        return logits.argmax(-1).tolist()
+
     def verify(self, last, drafts):
         """One step over a tree: the last token and drafted ones, (token, parent's index; 0 is the last
         token).  Returns the tokens that greedy decoding would emit, and the logits along its path."""
@@ -108,7 +116,7 @@ class Decoder:
             masks.append(masks[parent] | 1 << j)
             places.append(places[parent] + 1)
         logits, kept = self.step(tokens, places, masks)
-        best = logits.argmax(-1).tolist()
+        best = self.best(logits)
         path = [0]
         while True:
             follow = [j for j, (token, parent) in enumerate(drafts, 1) if parent == path[-1] and token == best[path[-1]]]
@@ -126,25 +134,84 @@ class Decoder:
         self.experts.close()
 
 
-def plain(prompt, n, **kw):
+class Served(Decoder):
+    """The same with the pages, the rotation, the router and the choice of tokens on the GPU."""
+
+    def __init__(self, most=1024, seed=0, **kw):
+        super().__init__(most=most, seed=seed, **kw)
+        s, d = self.shape, self.head_dim
+        g = torch.Generator().manual_seed(seed + 1)
+        for w in self.layers:
+            w["qn"], w["kn"] = ((1 + 0.1 * torch.randn(d, generator=g)).cuda() for _ in range(2))
+            w["b"] = (0.01 * torch.randn(s.E, generator=g)).cuda()             # the router's bias
+        self.places, self.rope_dim = most, d // 2
+        self.rope = torch.empty(most, self.rope_dim, device="cuda")
+        freq = 1e4 ** (-torch.arange(self.rope_dim // 2, dtype=torch.float64) / (self.rope_dim // 2))
+        ft.ft_rope_table(freq.cuda(), self.rope_dim, most, self.rope)
+        # no page is the sequence's yet; the free ones lie on a stack
+        pages = most // PAGE
+        self.free, self.table = self.table[0].clone(), torch.zeros(1, pages, dtype=torch.int32, device="cuda")
+        self.n_free = torch.tensor([pages], dtype=torch.int32, device="cuda")
+        self.cached, self.held = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+
+    def step(self, tokens, places, masks=None):
+        s, n, i32 = self.shape, len(tokens), dict(dtype=torch.int32, device="cuda")
+        start, length, at, slots = torch.empty(2, **i32), torch.empty(1, **i32), torch.empty(n, **i32), torch.empty(n, **i32)
+        tree = None if masks is None else torch.from_numpy(np.array(masks, np.uint64).view(np.int64)).cuda()
+        ft.ft_kv_plan(self.kv.handle, torch.tensor([n], **i32), self.cached, self.held, self.table, self.table.stride(0), self.free, self.n_free, 1, n,
+                      start, length, slots, self.cached, self.held, self.n_free, positions=at, tree_mask=tree)
+        x = self.embed[tokens].float()
+        y = torch.empty(n, s.H, device="cuda")
+        ids, gate, deferred = torch.empty(n, s.k, **i32), torch.empty(n, s.k, device="cuda"), torch.empty(n, s.k, **i32)
+        kept = []
+        for l, w in enumerate(self.layers):
+            h = torch.nn.functional.normalize(x, dim=-1).mul(s.H ** 0.5).to(torch.bfloat16)
+            q, k, v = (h @ w["q"]).view(n, self.n_q, self.head_dim), *((h @ w[i]).view(n, self.n_kv, self.head_dim) for i in "kv")
+            ft.ft_kv_append_rotated(self.kv.handle, l, q, k, v, slots, n, q, at, self.rope, self.rope_dim, self.places, k_out=k, q_norm=w["qn"],
+                                    k_norm=w["kn"])
+            o = torch.empty_like(q)
+            ft.ft_kv_attention(self.kv.handle, l, q, start, length, self.table, self.table.stride(0), 1, n, n, o,
+                               tree_mask=tree, window=WINDOW if l % 2 else 0, n_sink=SINKS if l % 2 else 0,
+                               sm_scale=self.head_dim ** -0.5)
+            x = x + (o.view(n, -1) @ w["o"]).float()
+            h = torch.nn.functional.normalize(x, dim=-1).mul(s.H ** 0.5).to(torch.bfloat16)
+            ft.ft_moe_route(h @ w["r"], n, s.E, s.k, ids, gate, score="sigmoid", bias=w["b"], n_group=4, topk_group=2, group_best=2)
+            ft.ft_moe_decode(self.experts.handle, l, h, ids, gate, n, s.k, y, deferred)
+            x = x + y
+            kept.append((k, v))                                  # turned already: they may be appended elsewhere
+        self.len += n
+        return (torch.nn.functional.normalize(x, dim=-1).mul(s.H ** 0.5).to(torch.bfloat16) @ self.head).float(), kept
+
+    def keep(self, n_new, path, kept):
+        super().keep(n_new, path, kept)
+        self.cached.fill_(self.len)                              # the next step's plan gives the pages back that this leaves over
+
+    def best(self, logits):
+        n = len(logits)
+        ids, logp = torch.empty(n, 1, dtype=torch.int32, device="cuda"), torch.empty(n, 1, device="cuda")
+        ft.ft_logprobs(logits, n, VOCAB, top_ids=ids, top_logp=logp, k=1)
+        return ids[:, 0].tolist()
+
+
+def plain(prompt, n, cls=Decoder, **kw):
     """n tokens after the prompt, one per step, and the logits that gave them."""
-    d = Decoder(**kw)
+    d = cls(**kw)
     out = [d.chunk([t]) for t in prompt][-1:]
-    tokens = [int(out[0][-1].argmax())]
+    tokens = d.best(out[0][-1:])
     while len(tokens) < n:
         out.append(d.chunk([tokens[-1]]))
-        tokens.append(int(out[-1][-1].argmax()))
+        tokens += d.best(out[-1][-1:])
     d.close()
     return tokens, torch.cat(out)
 
 
-def by_trees(prompt, n, guess, rng, depth=6, **kw):
+def by_trees(prompt, n, guess, rng, depth=6, cls=Decoder, **kw):
     """The same by chunks and trees: a branch of the guess's next tokens, wrong ones hanging from it.
     Returns the tokens, their logits and the number of verifying steps."""
-    d = Decoder(**kw)
+    d = cls(**kw)
     for at in range(0, len(prompt), BATCH):
         logits = d.chunk(prompt[at:at + BATCH])
-    tokens, out, steps = [int(logits[-1].argmax())], [logits[-1:]], 0
+    tokens, out, steps = d.best(logits[-1:]), [logits[-1:]], 0
     while len(tokens) < n:
         drafts, parent = [], 0
         for t in guess[len(tokens):len(tokens) + depth]:
@@ -164,11 +231,13 @@ def main():
     p = argparse.ArgumentParser()
     p.add_argument("--fmt", default="nvfp4", choices=["nvfp4", "fp8"])
     p.add_argument("--tokens", type=int, default=96)
+    p.add_argument("--served", action="store_true")
     args = p.parse_args()
+    cls = Served if args.served else Decoder
     rng = np.random.default_rng(0)
     prompt = rng.integers(0, VOCAB, 50).tolist()
-    a, la = plain(prompt, args.tokens, fmt=args.fmt)
-    b, lb, steps = by_trees(prompt, args.tokens, a, rng, fmt=args.fmt)
+    a, la = plain(prompt, args.tokens, cls, fmt=args.fmt)
+    b, lb, steps = by_trees(prompt, args.tokens, a, rng, cls=cls, fmt=args.fmt)
     same = next((i for i in range(len(a)) if a[i] != b[i]), len(a))
     print(f"{args.tokens} tokens: {args.tokens} steps one by one, {steps} steps by trees; the same up to token {same}; "
           f"logits differ by {((la - lb)[:same].norm() / la[:same].norm()).item():.1e} of their norm")
