@@ -556,6 +556,7 @@ def ft_kv_attention(handle, layer, q, q_start, kv_len, block_table, table_stride
 # ft_kv_step, ft_kv_qkv, ft_route and ft_logprob, packed at once
 _KV_STEP = struct.Struct("@14P3i4x")
 _KV_QKV = struct.Struct("@5P5q5P5if")
+_ONE = 1 << 40                                              # token stride of a single token, which means nothing
 _ROUTE = struct.Struct("@4Pq9if")
 _LOGPROB = struct.Struct("@6Pq4if4x")
 _kv_plan, _kv_append_rotated, _moe_route, _logprobs = (
@@ -633,16 +634,20 @@ def ft_kv_append_rotated(handle, layer, q, k, v, slots, n, q_out, positions, rop
                                for t, name in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out"), (k_out, "k_out")))
         ps, pp = _address(slots, _i32, "append_rotated: slots"), _address(positions, _i32, "append_rotated: positions")
         pr, pqn, pkn = (_address(t, _f32, f"append_rotated: {name}") for t, name in ((rope, "rope"), (q_norm, "q_norm"), (k_norm, "k_norm")))
-    if q_stride is None:
-        q_stride = _token_stride(q, "append_rotated: q")
-    if k_stride is None:
-        k_stride = _token_stride(k, "append_rotated: k")
-    if v_stride is None:
-        v_stride = _token_stride(v, "append_rotated: v")
-    if q_out_stride is None:
-        q_out_stride = _token_stride(q_out, "append_rotated: q_out")
-    if k_out_stride is None:
-        k_out_stride = _token_stride(k_out, "append_rotated: k_out") if pko else 0
+    try:
+        if q_stride is None:
+            q_stride = (q.stride(0) if n != 1 else _ONE) if q.is_contiguous() else _token_stride(q, "append_rotated: q")
+        if k_stride is None:
+            k_stride = (k.stride(0) if n != 1 else _ONE) if k.is_contiguous() else _token_stride(k, "append_rotated: k")
+        if v_stride is None:
+            v_stride = (v.stride(0) if n != 1 else _ONE) if v.is_contiguous() else _token_stride(v, "append_rotated: v")
+        if q_out_stride is None:
+            q_out_stride = (q_out.stride(0) if n != 1 else _ONE) if q_out.is_contiguous() else _token_stride(q_out, "append_rotated: q_out")
+        if k_out_stride is None:
+            k_out_stride = 0 if not pko else (k_out.stride(0) if n != 1 else _ONE) if k_out.is_contiguous() else _token_stride(
+                k_out, "append_rotated: k_out")
+    except AttributeError:
+        raise TypeError("append_rotated: a raw address needs its token stride") from None
     status = _kv_append_rotated(handle, _KV_QKV.pack(pq, pk, pv, po, pko, q_stride, k_stride, v_stride, q_out_stride, k_out_stride,
                                                      pqn, pkn, pr, pp, ps, layer, n, rope_dim, n_positions, interleaved, eps), _stream(stream))
     if status:

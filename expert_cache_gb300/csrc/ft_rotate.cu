@@ -135,18 +135,27 @@ __device__ __forceinline__ void turn_plainly(const Lane<D, kInter>& p, uint32_t 
 // reads them, so its own wait for its copies is all there is to wait for.
 struct Heads {
     const __nv_bfloat16 *k, *v, *q;    // the token's
-    int hkv, at, end, D;               // next head to ask for, in the order k, v, q; end of the run
+    const __nv_bfloat16 *lo, *hi;      // the lane's dims of the next head to ask for
+    int hkv, at, end, D;               // that head, in the order k, v, q; end of the run
+    int turn;                          // where lo and hi pass on to the next of the three
     uint32_t slots, ask, take;         // this thread's shared memory, where the next head goes, where the first one is
 
     template <typename L>
+    __device__ __forceinline__ void point(const L& p) {
+        const bool is_v = at >= hkv && at < 2 * hkv;
+        const __nv_bfloat16* head = at < hkv ? k + at * D : is_v ? v + (at - hkv) * D : q + (at - 2 * hkv) * D;
+        lo = head + (is_v ? 16 * p.b : p.lo);
+        hi = head + (is_v ? 16 * p.b + 8 : p.hi);
+        turn = at < hkv ? hkv : is_v ? 2 * hkv : end;
+    }
+    template <typename L>
     __device__ __forceinline__ void issue(const L& p) {
         if (at < end) {
-            const bool is_v = at >= hkv && at < 2 * hkv;
-            const __nv_bfloat16* head = at < hkv ? k + at * D : is_v ? v + (at - hkv) * D : q + (at - 2 * hkv) * D;
-            const __nv_bfloat16 *lo = head + (is_v ? 16 * p.b : p.lo), *hi = head + (is_v ? 16 * p.b + 8 : p.hi);
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slots + ask), "l"(lo) : "memory");
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slots + ask + kRotThreads * 16), "l"(hi) : "memory");
-            ++at;
+            lo += D;
+            hi += D;
+            if (++at == turn) point(p);
         }
         ask = (ask + 2 * kRotThreads * 16) & (2 * kAhead * kRotThreads * 16 - 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -236,8 +245,8 @@ __device__ __forceinline__ Two inverse_norm(const uint32_t (&x)[8], float eps) {
 }
 
 // (x - n) c + (y - m) s times rh + rl, rounded to fp32 and to bf16: x - n and y - m stand for a pair's dims times their weights.
-__device__ __forceinline__ uint32_t turned(Pair x, Pair n, Pair y, Pair m, Pair c, Pair s, Pair rh, Pair rl) {
-    const Pair u = mul2(x, c), ul = fma2(neg2(x), c, u), v = mul2(y, s), vl = fma2(neg2(y), s, v);
+__device__ __forceinline__ uint32_t turned(Pair x, Pair n, Pair y, Pair m, Pair c, Pair s, Pair nc, Pair ns, Pair rh, Pair rl) {
+    const Pair u = mul2(x, c), ul = fma2(x, nc, u), v = mul2(y, s), vl = fma2(y, ns, v);
     Pair h, l;
     two_sum2(u, v, h, l);
     l = from2(add2(fma2(n, c, ul), fma2(m, s, vl)), l);
@@ -249,6 +258,9 @@ __device__ __forceinline__ uint32_t turned(Pair x, Pair n, Pair y, Pair m, Pair 
 template <int D, int kFormat, bool kInter>
 __device__ __forceinline__ void turn_keys(const RotateArgs& a, const Lane<D, kInter>& p, Heads& heads, const Pair (&c)[8], const Pair (&s)[8],
                                           int tok, int slot, int head, int end, float inv_k) {
+    Pair nc[8], ns[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) nc[j] = neg2(c[j]), ns[j] = neg2(s[j]);
     for (; head < end; ++head) {
         uint32_t k[8];
         heads.next(p, k);
@@ -280,8 +292,8 @@ __device__ __forceinline__ void turn_keys(const RotateArgs& a, const Lane<D, kIn
             }
             if (kInter) y = swap2(x), m = swap2(n);
             if (numbers) {
-                k[j] = turned(x, n, y, m, c[j], s[j], rh, rl);
-                if (!kInter) k[j ^ 4] = turned(y, m, x, n, c[j], neg2(s[j]), rh, rl);
+                k[j] = turned(x, n, y, m, c[j], s[j], nc[j], ns[j], rh, rl);
+                if (!kInter) k[j ^ 4] = turned(y, m, x, n, c[j], ns[j], nc[j], s[j], rh, rl);
             } else {
                 const Pair none = 0;
                 k[j] = pack_bf16(mul2(fma2(x, c[j], mul2(p.turns ? y : none, s[j])), rh));
@@ -321,8 +333,9 @@ __global__ void __launch_bounds__(kRotThreads, kRotPerSm) kv_rotate_kernel(const
         const int first = (int)(u / groups) * a.run, end = min(first + a.run, a.hq + 2 * hkv);
         const long long token = u % groups * kTokens + (threadIdx.x & 31) / Lane<D, kInter>::kLanes;
         const int tok = (int)min(token, (long long)a.n - 1);
-        Heads heads{a.k + (size_t)tok * a.k_stride, a.v + (size_t)tok * a.v_stride, a.q + (size_t)tok * a.q_stride, hkv, first, end, D,
-                    (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16, 0, 0};
+        Heads heads{a.k + (size_t)tok * a.k_stride, a.v + (size_t)tok * a.v_stride, a.q + (size_t)tok * a.q_stride, nullptr, nullptr, hkv, first, end, D,
+                    0, (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16, 0, 0};
+        heads.point(p);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) heads.issue(p);
         int slot = token < a.n ? a.slots[tok] : -1, pos = a.rope_dim ? a.positions[tok] : 0;

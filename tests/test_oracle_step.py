@@ -290,10 +290,16 @@ def test_append_rotated_looks_at_its_arrays(ft, calls):
     ft.ft_kv_append_rotated(7, **(good | dict(k_out=None, q_norm=None, k_norm=None, rope=None, positions=None, rope_dim=0, interleaved=True)))
     got = ft._KV_QKV.unpack(calls["kv_append_rotated"][1])
     assert got[4] == got[9] == got[10] == got[11] == got[12] == got[13] == 0 and got[17] == 0 and got[19] == 1
+    one = {x: good[x][:1] for x in ("q", "k", "v", "q_out", "k_out", "slots", "positions")}
+    ft.ft_kv_append_rotated(7, **(good | one | dict(n=1, q_out=bf16(64, 4).t().reshape(1, 64, 4).transpose(1, 2).contiguous())))
+    assert all(x % 8 == 0 and x >= 256 for x in ft._KV_QKV.unpack(calls["kv_append_rotated"][1])[5:10])
+    with pytest.raises(TypeError, match="stride"):
+        ft.ft_kv_append_rotated(7, **(good | dict(q=good["q"].data_ptr())))
     calls.clear()
     for n in ("q", "k", "v", "q_out", "k_out"):
         for t in (good[n].float(), bf16(5, 4, 2, 64)[:, :, 0], bf16(5, 64, 2).transpose(1, 2)):
             misread(ft, f"append_rotated: {n}", lambda: ft.ft_kv_append_rotated(7, **(good | {n: t})))
+        misread(ft, f"append_rotated: {n}", lambda: ft.ft_kv_append_rotated(7, **(good | one | dict(n=1) | {n: bf16(1, 4, 2, 64)[:, :, 0]})))
     for n in ("slots", "positions", "rope", "q_norm", "k_norm"):
         for t in (good[n].double(), good[n].repeat(2, *[1] * (good[n].dim() - 1))[::2]):
             misread(ft, f"append_rotated: {n}", lambda: ft.ft_kv_append_rotated(7, **(good | {n: t})))
