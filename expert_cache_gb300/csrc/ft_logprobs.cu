@@ -7,7 +7,7 @@
 // The k largest come out of the same pass.  From the sample (the first 8 vectors of every thread) the k-th largest of 16 to
 // 64 logits is a lower bound of the row's k-th; only what reaches it is kept and put on a list in shared memory (4 to 8 k of
 // 100,000), which is ranked at the end.  Where more reach it than the list holds, its own k-th largest is the next bound and
-// the part is read again; where that does not help (equal logits by the thousand), k searches find them.  Which ones
+// the part is read again; where that does not help (equal logits by the thousand, rising ones), k searches find them.  Which ones
 // these are does not depend on any order: value, then index.
 #include <atomic>
 #include <cfloat>
@@ -355,8 +355,7 @@ struct Ring {
 
 // Puts everything that reaches the bound on the list.
 template <typename L>
-__device__ void collect(LogShared& sm, const Part<L>& p) {
-    const float bound = sm.bound;
+__device__ void collect(LogShared& sm, const Part<L>& p, float bound) {
     p.each([&](const Vec<L>& v, int index) { put_on_list(sm, v, index, bound); });
 }
 
@@ -520,22 +519,20 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
     if (kTop) {
         int n = sm.count;
         if (n > kListed) {
-            bool again = true;
-            while (again) {
+            // at most twice (rising logits let a list's worth through each time)
+            float next = bound;
+            for (int i = 0; i < 2; ++i) {
                 __syncthreads();
                 if (threadIdx.x == 0) sm.count = 0;
                 __syncthreads();
-                collect(sm, p);
+                collect(sm, p, next);
                 __syncthreads();
                 n = sm.count;
                 if (n <= kListed) break;
-                // the list's k-th largest bounds the row's; if it is no better than the last one, the searches
+                // the list's k-th largest bounds the row's
                 rank_list(sm.list, kListed, c.k, rank, sm.top);
                 __syncthreads();
-                const float next = key_logit(sm.top[c.k - 1]);
-                again = next > sm.bound;
-                __syncthreads();
-                if (threadIdx.x == 0) sm.bound = next;
+                next = key_logit(sm.top[c.k - 1]);
             }
             __syncthreads();
         }
@@ -636,10 +633,11 @@ extern "C" ft_status ft_logprobs(const ft_logprob* call, void* stream) {
         return FT_ERR_ARG;
     if (!aligned(c.tokens, 4) || !aligned(c.logp, 4) || !aligned(c.entropy, 4) || !aligned(c.top_ids, 4) || !aligned(c.top_logp, 4)) return FT_ERR_ARG;
     NvtxRange r("ft_logprobs");
-    // CTAs of a row: as many as there is room for, each with a vector or more per thread
+    // CTAs of a row: as many as leave no SM with two, each with a vector or more per thread (48 rows of 100,003 fp32, k = 20: 2 CTAs
+    // 11.2 us, 4, of which some share an SM, 12.3 us, 8 19.1 us; 24 rows of 131,072 bf16: 4 7.2 us, 8 7.4 us)
     int shift = 0;
     const long long vectors = (long long)c.V / (c.dtype == FT_DTYPE_BF16 ? 8 : 4);
-    while (1 << shift < kMaxCtas && (2LL << shift) * c.n <= (long long)kLogPerSm * sm_count() && vectors > (long long)kLogThreads << shift) ++shift;
+    while (1 << shift < kMaxCtas && (2LL << shift) * c.n <= sm_count() && vectors > (long long)kLogThreads << shift) ++shift;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = c.dtype == FT_DTYPE_BF16 ? (c.k ? launch<__nv_bfloat16, true>(c, shift, s) : launch<__nv_bfloat16, false>(c, shift, s))
                                                    : (c.k ? launch<float, true>(c, shift, s) : launch<float, false>(c, shift, s));

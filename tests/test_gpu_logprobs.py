@@ -153,6 +153,16 @@ def test_what_is_masked(ft, V, dtype):
         check(x, t, got, k, scale)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_long_rising_rows(ft, dtype):
+    """Rows whose every part is larger than the one before, in steps that the type tells apart: a bound from the front says nothing."""
+    n, V = 3, 400000
+    x = torch.arange(V, device="cuda", dtype=torch.float32)[None].repeat(n, 1) * torch.tensor([1e-4, 1e-3, 0.1], device="cuda")[:, None]
+    x, t = x.to(dtype), tokens_of(3, n, V)
+    for k in (1, 32):
+        check(x, t, run(ft, x, t, k), k)
+
+
 def test_temperatures_and_tokens(ft):
     x = logits(3, 6, 40000)
     t = tokens_of(0, 6, 40000)
