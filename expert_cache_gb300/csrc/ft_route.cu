@@ -34,7 +34,7 @@ struct RouteArgs {
 };
 
 // A logit as the formula takes it: NaN is -inf, +inf the largest number.
-__device__ __forceinline__ float route_logit(float x) { return x == x ? fminf(x, FLT_MAX) : kNone; }
+__device__ __forceinline__ float route_logit(float x) { return fminf(fmaxf(x, kNone), FLT_MAX); }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) { return route_logit(__bfloat162float(*p)); }
 __device__ __forceinline__ float load_logit(const float* p) { return route_logit(*p); }
 
@@ -51,30 +51,43 @@ __device__ __forceinline__ V warp_sum(V v) {
     return v;
 }
 
-// The scores of a row in type V: softmax's as exp(x - top) / sum.
-template <typename V>
-struct Scores {
-    V top, sum;
-    bool sigmoid;
-    __device__ __forceinline__ V of(float x) const {
-        if (sigmoid) return V(1) / (V(1) + exp(-V(x)));
-        return exp(V(x) - top) / sum;
-    }
-};
-template <typename V>
-__device__ __forceinline__ Scores<V> scores_of(const RouteArgs& a, const float* x) {
-    const int lane = threadIdx.x & 31;
-    Scores<V> s{V(0), V(1), a.sigmoid};
-    if (a.sigmoid) return s;
-    V top = kNone, sum = 0;
-    for (int e = lane; e < a.E; e += 32) top = fmax(top, V(x[e]));
-    top = warp_max(top);
-    if (top == V(kNone)) top = 0;
-    for (int e = lane; e < a.E; e += 32) sum += exp(V(x[e]) - top);
-    s.top = top;
-    s.sum = warp_sum(sum);
-    return s;
+// e^y for y <= 0 (below -700: e^-700) to some 2^-51: y = n ln 2 + r with ln 2 in two parts (Cody and Waite 1980), the first of 41 bits, so
+// that n times it is exact; Taylor's series to r^13 / 13!, whose rest is below 2^-57 for |r| <= ln 2 / 2.
+__device__ __forceinline__ double exp_negative(double y) {
+    y = fmax(y, -700.0);
+    const double n = rint(y * 1.4426950408889634);
+    const double r = fma(n, -0x1.3de6af278ece6p-42, fma(n, -0x1.62e42fefa3000p-1, y));
+    double p = 1.0 / 6227020800.0;
+    constexpr double c[] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320, 1.0 / 362880, 1.0 / 3628800,
+                            1.0 / 39916800, 1.0 / 479001600};
+#pragma unroll
+    for (int i = 12; i >= 0; --i) p = fma(p, r, c[i]);
+    return __longlong_as_double(__double_as_longlong(p) + ((long long)(int)n << 52));
 }
+
+// 1 / x to some 2^-52 for a normal fp32 range of x: two steps of Newton's from the fp32 reciprocal.
+__device__ __forceinline__ double inverse_double(double x) {
+    double r = 1.0f / (float)x;
+    r = fma(r, fma(-x, r, 1.0), r);
+    return fma(r, fma(-x, r, 1.0), r);
+}
+
+__device__ __forceinline__ float exp_of(float y) { return expf(y); }
+__device__ __forceinline__ double exp_of(double y) { return exp_negative(y); }
+__device__ __forceinline__ float inverse(float x) { return __frcp_rn(x); }
+__device__ __forceinline__ double inverse(double x) { return inverse_double(x); }
+
+// sigmoid(x), by an exponential that does not grow.
+template <typename V>
+__device__ __forceinline__ V sigmoid(float x) {
+    const V p = exp_of(-V(fabsf(x)));
+    return (x >= 0.f ? V(1) : p) * inverse(V(1) + p);
+}
+
+// What softmax's scores e^(x - top) / sum are made of.
+struct Scores {
+    float top, sum;
+};
 
 // A bound on the error of an fp32 score: the roundings of the exponential (2^-22) and of its argument (at most -log2 of the
 // score in magnitude), those of the sum's terms and its E / 32 + 5 additions, two more operations, what underflows.  It rises with the score.
@@ -90,31 +103,53 @@ __device__ __forceinline__ bool too_near(const RouteArgs& a, float first, float 
 // The choices of a row in type V, the groups that stay, and the k first experts: lane j < k gets the j-th (-1: none).
 // Returns false if fp32 does not tell.
 template <typename V>
-__device__ bool decide(const RouteArgs& a, const float* x, V* key, int& id) {
+__device__ __forceinline__ bool decide(const RouteArgs& a, const float* x, V* key, Scores& s, int& id) {
     const int lane = threadIdx.x & 31;
     bool sure = true;
     float largest = 1.f;                                         // no score is above it
-    if (a.by_logit) {
-        for (int e = lane; e < a.E; e += 32) key[e] = x[e];
-    } else {
-        const Scores<V> s = scores_of<V>(a, x);
-        if (!a.sigmoid) largest = 1.f / (float)s.sum;
+    if (!a.sigmoid && !(a.by_logit && a.renormalise)) {
+        float top = kNone;
+        V sum = 0;
+        for (int e = lane; e < a.E; e += 32) top = fmaxf(top, x[e]);
+        top = warp_max(top);
+        if (top == kNone) top = 0.f;
+#pragma unroll 1
         for (int e = lane; e < a.E; e += 32) {
-            V c = s.of(x[e]) + (a.bias ? V(a.bias[e]) : V(0));
-            if (x[e] == kNone || !(c == c)) c = kNone;
-            key[e] = c;
+            const V p = exp_of(V(x[e]) - V(top));
+            sum += p;
+            key[e] = p;
         }
+        sum = warp_sum(sum);
+        s.top = top;
+        s.sum = (float)sum;
+        const V inv = inverse(sum);
+        largest = (float)inv;
+        for (int e = lane; e < a.E; e += 32) key[e] *= inv;
+    } else if (!a.by_logit) {
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32) key[e] = sigmoid<V>(x[e]);
+    }
+    for (int e = lane; e < a.E; e += 32) {
+        V c = a.by_logit ? V(x[e]) : a.bias ? key[e] + V(a.bias[e]) : key[e];
+        if (x[e] == kNone || !(c == c)) c = kNone;
+        key[e] = c;
     }
     __syncwarp();
     if (a.n_group > 1) {
-        // lane g has the two largest of group g
+        // some lanes for each group: their two largest
+        const int g = lane >> a.group_shift, parts = 1 << a.group_shift;
         V one = kNone, two = kNone;
-        if (lane < a.n_group) {
-            for (int i = 0; i < a.size; ++i) {
-                const V c = key[lane * a.size + i];
+        if (g < a.n_group) {
+            for (int i = lane & (parts - 1); i < a.size; i += parts) {
+                const V c = key[g * a.size + i];
                 two = fmax(two, fmin(one, c));
                 one = fmax(one, c);
             }
+        }
+        for (int o = 1; o < parts; o <<= 1) {
+            const V c = __shfl_xor_sync(0xffffffffu, one, o), d = __shfl_xor_sync(0xffffffffu, two, o);
+            two = fmax(fmax(two, d), fmin(one, c));
+            one = fmax(one, c);
         }
         const V worth = a.group_best == 2 && two > V(kNone) ? one + two : one;
         float err = 0.f;
@@ -123,30 +158,25 @@ __device__ bool decide(const RouteArgs& a, const float* x, V* key, int& id) {
             err = score_error(a, largest) * a.group_best + 0x1p-22f * (fabsf((float)one) + (two > V(kNone) ? fabsf((float)two) : 0.f));
         }
         int before = 0;
-        V least = INFINITY, most = kNone;
-        for (int g = 0; g < a.n_group; ++g) {
-            const V other = __shfl_sync(0xffffffffu, worth, g);
-            before += other > worth || (other == worth && g < lane);
+        for (int i = 0; i < a.n_group; ++i) {
+            const V other = __shfl_sync(0xffffffffu, worth, i << a.group_shift);
+            before += other > worth || (other == worth && i < g);
         }
-        const bool stays = lane < a.n_group && before < a.topk_group;
+        const bool stays = g < a.n_group && before < a.topk_group;
         if (sizeof(V) == 4 && !a.by_logit) {
             // worth - err of those that stay against worth + err of those that do not
-            if (lane < a.n_group) {
-                if (stays) least = worth - V(err);
-                else most = worth + V(err);
-            }
-            least = -warp_max(-least);
-            most = warp_max(most);
-            if (!(least > most) && most > V(kNone)) sure = false;
+            const float least = -warp_max(stays && worth > V(kNone) ? err - (float)worth : kNone);
+            const float most = warp_max(!stays && g < a.n_group && worth > V(kNone) ? (float)worth + err : kNone);
+            if (!(least > most) && most > kNone) sure = false;
         }
-        if (lane < a.n_group && !stays)
-            for (int i = 0; i < a.size; ++i) key[lane * a.size + i] = kNone;
+        if (g < a.n_group && !stays)
+            for (int i = lane & (parts - 1); i < a.size; i += parts) key[g * a.size + i] = kNone;
         __syncwarp();
     }
     id = -1;
     V last = 0;
     int last_id = -1;
-    for (int j = 0; j <= a.k; ++j) {
+    for (int j = 0; j < a.k + (sizeof(V) == 4); ++j) {
         V best = kNone;
         int at = 0x7FFFFFFF;
         for (int e = lane; e < a.E; e += 32)
@@ -173,7 +203,7 @@ __device__ bool decide(const RouteArgs& a, const float* x, V* key, int& id) {
 
 // The weights of a row's experts: lane j has the j-th, its logit `mine` (-inf: none).  Renormalised ones against the largest
 // selected, so that they do not underflow together.
-__device__ __forceinline__ float weight(const RouteArgs& a, float mine, const Scores<float>& s) {
+__device__ __forceinline__ float weight(const RouteArgs& a, float mine, const Scores& s) {
     const bool some = mine > kNone;
     float w = 0.f;
     if (a.renormalise) {
@@ -181,28 +211,28 @@ __device__ __forceinline__ float weight(const RouteArgs& a, float mine, const Sc
         if (a.sigmoid) {
             // sigmoid(x) = e^min(x,0) / (1 + e^-|x|)
             top = fminf(top, 0.f);
-            if (some) w = expf(fminf(mine, 0.f) - top) / (1.f + expf(-fabsf(mine)));
+            if (some) w = expf(fminf(mine, 0.f) - top) * __frcp_rn(1.f + expf(-fabsf(mine)));
         } else if (some) {
             w = expf(mine - top);
         }
         const float sum = warp_sum(w);
-        if (some) w = w / sum;
+        if (some) w *= __frcp_rn(sum);
     } else if (some) {
-        w = s.of(mine);
+        w = a.sigmoid ? sigmoid<float>(mine) : expf(mine - s.top) * __frcp_rn(s.sum);
     }
     return w * a.scale;
 }
 
-// A row whose logits stand in shared memory (x, E values; key, E values of 64 bits).
-__device__ __noinline__ void route_row(const RouteArgs& a, float* x, double* key, long long t) {
+// A row whose logits stand in shared memory (x, E values; key, E values of 64 bits).  sure: whether fp32 may still tell.
+__device__ __noinline__ void route_row(const RouteArgs& a, float* x, double* key, bool sure, long long t) {
     const int lane = threadIdx.x & 31;
+    Scores s{0.f, 1.f};
     int id;
-    if (!decide(a, x, reinterpret_cast<float*>(key), id)) {
+    if (!sure || !decide(a, x, reinterpret_cast<float*>(key), s, id)) {
         __syncwarp();
-        decide(a, x, key, id);
+        decide(a, x, key, s, id);
     }
-    const float mine = id >= 0 ? x[id] : kNone;
-    const float w = weight(a, mine, a.renormalise ? Scores<float>{} : scores_of<float>(a, x));
+    const float w = weight(a, id >= 0 ? x[id] : kNone, s);
     if (lane < a.k) {
         a.ids[t * a.k + lane] = id;
         a.w[t * a.k + lane] = w;
@@ -221,7 +251,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_wide_kernel(const Rout
     const L* row = static_cast<const L*>(a.logits) + t * a.stride;
     for (int e = lane; e < a.E; e += 32) x[e] = load_logit(row + e);
     __syncwarp();
-    route_row(a, x, route_smem + (size_t)warp * a.E, t);
+    route_row(a, x, route_smem + (size_t)warp * a.E, true, t);
 }
 
 __device__ __forceinline__ unsigned ordered(float x) {
@@ -266,41 +296,19 @@ __device__ __forceinline__ void load_row(float (&x)[kEach], const L* row, int E)
     }
 }
 
+// A choice and its expert as a number whose order is theirs: the larger choice first, then the lower index.  0 stands for none.
+typedef unsigned long long Key;
+__device__ __forceinline__ Key key_of(float choice, int e) { return (Key)ordered(choice + 0.f) << 32 | ~(unsigned)e; }
+__device__ __forceinline__ float key_choice(Key k) { return k ? unordered((unsigned)(k >> 32)) : kNone; }
+__device__ __forceinline__ int key_expert(Key k) { return k ? (int)~(unsigned)k : -1; }
+
 // What a warp keeps in shared memory for a row: the choices of one with groups, or the logits and 64-bit choices of one that
-// is decided by searches; the logits of one that is decided again; what is ranked.
-template <typename V>
+// is decided again; what is ranked, unsorted and sorted.
 struct Ranked {
-    V key;
-    float x;
-    int e;
+    Key key[64];
+    float x[64];
 };
-__host__ __device__ inline size_t route_bytes(int E) { return (((size_t)E * 12 + 15) & ~(size_t)15) + 2 * 32 * sizeof(Ranked<double>); }
-
-__device__ __forceinline__ float score_exp(float x) { return exp2_fast(x * 1.4426950408889634f); }
-__device__ __forceinline__ double score_exp(double x) { return exp(x); }
-__device__ __forceinline__ float inverse(float x) { return __frcp_rn(x); }
-__device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
-
-// e^y for y <= 0 (below -700: e^-700) to some 2^-51: y = n ln 2 + r with ln 2 in two parts (Cody and Waite 1980), the first of 41 bits, so
-// that n times it is exact; Taylor's series to r^13 / 13!, whose rest is below 2^-57 for |r| <= ln 2 / 2.
-__device__ __forceinline__ double exp_negative(double y) {
-    y = fmax(y, -700.0);
-    const double n = rint(y * 1.4426950408889634);
-    const double r = fma(n, -0x1.3de6af278ece6p-42, fma(n, -0x1.62e42fefa3000p-1, y));
-    double p = 1.0 / 6227020800.0;
-    constexpr double c[] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320, 1.0 / 362880, 1.0 / 3628800,
-                            1.0 / 39916800, 1.0 / 479001600};
-#pragma unroll
-    for (int i = 12; i >= 0; --i) p = fma(p, r, c[i]);
-    return __longlong_as_double(__double_as_longlong(p) + ((long long)(int)n << 52));
-}
-
-// 1 / x to some 2^-52 for a normal fp32 range of x: two steps of Newton's from the fp32 reciprocal.
-__device__ __forceinline__ double inverse_double(double x) {
-    double r = 1.0f / (float)x;
-    r = fma(r, fma(-x, r, 1.0), r);
-    return fma(r, fma(-x, r, 1.0), r);
-}
+__host__ __device__ inline size_t route_bytes(int E) { return (((size_t)E * 12 + 15) & ~(size_t)15) + sizeof(Ranked); }
 
 // Ranks the n choices of the lanes (logit mine, expert e) in 64 bits; returns the lane's logit and expert (as its bits).  Little
 // code, rolled: it is fetched while the row's warp waits (a few KB of it took 6 us).
@@ -337,90 +345,84 @@ __device__ __noinline__ float2 rank_again(const RouteArgs& a, const float* x, fl
     return out;
 }
 
-enum Decided { kSure, kUnsure, kMany };
-
-// A row's k experts by choices of type V; lane j gets the j-th (e -1: none).
-template <typename V, int kEach, bool kByLogit>
-__device__ __forceinline__ Decided pick(const RouteArgs& a, const float (&x)[kEach], uint8_t* mem, Scores<float>& s, Ranked<V>& mine) {
-    constexpr bool k32 = sizeof(V) == 4;
+// A row's k experts and their logits; lane j gets the j-th (expert -1: none).
+enum Picked { kDone, kUnsure, kMany };       // kUnsure: fp32 does not tell the groups; kMany: a lane each is not enough for the ranking
+template <int kEach, bool kByLogit>
+__device__ __forceinline__ Picked pick(const RouteArgs& a, const float (&x)[kEach], uint8_t* mem, Scores& s, float& logit, int& expert) {
     const int lane = threadIdx.x & 31;
-    Ranked<V>* ranked = reinterpret_cast<Ranked<V>*>(mem + route_bytes(a.E) - 2 * 32 * sizeof(Ranked<double>));
-    V key[kEach];
+    Ranked& ranked = *reinterpret_cast<Ranked*>(mem + route_bytes(a.E) - sizeof(Ranked));
+    float key[kEach];
 
     // the choices
-    bool sure = true;
-    V inv = 1;
+    float inv = 1.f;
     if (kByLogit ? !a.renormalise && !a.sigmoid : !a.sigmoid) {
-        float top = x[0];
-        V sum = 0;
+        float top = x[0], sum = 0.f;
 #pragma unroll
         for (int i = 1; i < kEach; ++i) top = fmaxf(top, x[i]);
         top = warp_max(top);
         if (top == kNone) top = 0.f;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            key[i] = score_exp(V(x[i]) - V(top));
+            key[i] = exp2_fast((x[i] - top) * 1.4426950408889634f);
             sum += key[i];
         }
-        sum = warp_sum(sum);
-        inv = inverse(sum);
         s.top = top;
-        s.sum = (float)sum;
+        s.sum = warp_sum(sum);
+        inv = __frcp_rn(s.sum);
     }
     if (kByLogit) {
 #pragma unroll
         for (int i = 0; i < kEach; ++i) key[i] = x[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) key[i] = a.sigmoid ? inverse(V(1) + score_exp(-V(x[i]))) : key[i] * inv;
+        for (int i = 0; i < kEach; ++i) key[i] = a.sigmoid ? __frcp_rn(1.f + exp2_fast(x[i] * -1.4426950408889634f)) : key[i] * inv;
         if (a.bias) {
             float bias[kEach];
 #pragma unroll
             for (int i = 0; i < kEach; ++i) bias[i] = a.bias[min(Held<kEach>::index(i), a.E - 1)];
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) key[i] += V(bias[i]);
+            for (int i = 0; i < kEach; ++i) key[i] += bias[i];
         }
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) key[i] = x[i] > kNone && key[i] == key[i] ? key[i] : V(kNone);
+        for (int i = 0; i < kEach; ++i) key[i] = x[i] > kNone && key[i] == key[i] ? key[i] : kNone;
     }
 
-    const float largest = a.sigmoid ? 1.f : (float)inv;            // no score is above it
+    const float largest = a.sigmoid ? 1.f : inv;                   // no score is above it
     // the groups that stay: some lanes for each group, their two largest choices
     if (a.n_group > 1) {
-        V* flat = reinterpret_cast<V*>(mem);
+        float* flat = reinterpret_cast<float*>(mem);
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
             if (Held<kEach>::index(i) < a.E) flat[Held<kEach>::index(i)] = key[i];
         __syncwarp();
         const int g = lane >> a.group_shift, parts = 1 << a.group_shift;
-        V one = kNone, two = kNone;
+        float one = kNone, two = kNone;
         if (g < a.n_group) {
             for (int i = lane & (parts - 1); i < a.size; i += parts) {
-                const V c = flat[g * a.size + i];
-                two = fmax(two, fmin(one, c));
-                one = fmax(one, c);
+                const float c = flat[g * a.size + i];
+                two = fmaxf(two, fminf(one, c));
+                one = fmaxf(one, c);
             }
         }
         for (int o = 1; o < parts; o <<= 1) {
-            const V c = __shfl_xor_sync(0xffffffffu, one, o), d = __shfl_xor_sync(0xffffffffu, two, o);
-            two = fmax(fmax(two, d), fmin(one, c));
-            one = fmax(one, c);
+            const float c = __shfl_xor_sync(0xffffffffu, one, o), d = __shfl_xor_sync(0xffffffffu, two, o);
+            two = fmaxf(fmaxf(two, d), fminf(one, c));
+            one = fmaxf(one, c);
         }
-        const V worth = a.group_best == 2 && two > V(kNone) ? one + two : one;
+        const float worth = a.group_best == 2 && two > kNone ? one + two : one;
         int before = 0;
         for (int i = 0; i < a.n_group; ++i) {
-            const V other = __shfl_sync(0xffffffffu, worth, i << a.group_shift);
+            const float other = __shfl_sync(0xffffffffu, worth, i << a.group_shift);
             before += other > worth || (other == worth && i < g);
         }
         const bool stays = g < a.n_group && before < a.topk_group;
         const unsigned kept = __ballot_sync(0xffffffffu, stays);
-        if (!kByLogit && k32) {
+        if (!kByLogit) {
             // the magnitudes of a sum's terms bound its own rounding
-            const float err = score_error(a, largest) * a.group_best +
-                              0x1p-22f * ((one > V(kNone) ? fabsf((float)one) : 0.f) + (two > V(kNone) ? fabsf((float)two) : 0.f));
-            const float least = -warp_max(stays && worth > V(kNone) ? err - (float)worth : kNone);
-            const float most = warp_max(!stays && g < a.n_group && worth > V(kNone) ? (float)worth + err : kNone);
-            sure = least > most || most == kNone;
+            const float err = score_error(a, largest) * a.group_best + 0x1p-22f * ((one > kNone ? fabsf(one) : 0.f) + (two > kNone ? fabsf(two) : 0.f));
+            const float least = -warp_max(stays && worth > kNone ? err - worth : kNone);
+            const float most = warp_max(!stays && g < a.n_group && worth > kNone ? worth + err : kNone);
+            if (!(least > most) && most > kNone) return kUnsure;
         }
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
@@ -429,13 +431,12 @@ __device__ __forceinline__ Decided pick(const RouteArgs& a, const float (&x)[kEa
         }
         __syncwarp();
     }
-    if (!sure) return kUnsure;
 
-    // the bound: of the lanes' maxima (as fp32, whose order is theirs), largest first, the (k + 1)-th; by logits the k-th is enough
-    V most = key[0];
+    // the bound: of the lanes' maxima, largest first, the (k + 1)-th; by logits the k-th is enough
+    float most = key[0];
 #pragma unroll
-    for (int i = 1; i < kEach; ++i) most = fmax(most, key[i]);
-    unsigned left = ordered((float)most), bound = ordered(kNone);
+    for (int i = 1; i < kEach; ++i) most = fmaxf(most, key[i]);
+    unsigned left = ordered(most), bound = ordered(kNone);
     for (int n = 0; n < a.k + (kByLogit ? 0 : 1);) {
         bound = __reduce_max_sync(0xffffffffu, left);
         if (bound <= ordered(kNone)) break;
@@ -443,36 +444,42 @@ __device__ __forceinline__ Decided pick(const RouteArgs& a, const float (&x)[kEa
         n += __popc(__ballot_sync(0xffffffffu, is));
         if (is) left = 0;
     }
-    float least = bound <= ordered(kNone) ? kNone : unordered(bound);
-    if (!kByLogit && k32) least -= 2.f * (2.f * score_error(a, largest) + 0x1p-21f * fabsf(least));        // nothing that may be a (k + 1)-th is left out
+    float least = bound <= ordered(kNone) ? -FLT_MAX : unordered(bound);
+    if (!kByLogit) least = fmaxf(least - 2.f * (2.f * score_error(a, largest) + 0x1p-21f * fabsf(least)), -FLT_MAX);      // nothing that may be a (k + 1)-th is left out
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        const bool in = (float)key[i] >= least && key[i] > V(kNone);
+        const bool in = key[i] >= least;
         const unsigned who = __ballot_sync(0xffffffffu, in);
         const int at = n + __popc(who & ((1u << lane) - 1));
-        if (in && at < 32) ranked[at] = Ranked<V>{key[i], x[i], Held<kEach>::index(i)};
+        if (in && at < 32) {
+            ranked.key[at] = key_of(key[i], Held<kEach>::index(i));
+            if (!kByLogit) ranked.x[at] = x[i];
+        }
         n += __popc(who);
     }
     if (n > 32) return kMany;           // too few maxima to bound the (k + 1)-th choice, or many equal ones
     __syncwarp();
-    mine = Ranked<V>{V(kNone), kNone, -1};
+    Key mine = 0;
     int rank = lane;
     if (lane < n) {
-        mine = ranked[lane];
+        mine = ranked.key[lane];
         rank = 0;
-        for (int i = 0; i < n; ++i) rank += ranked[i].key > mine.key || (ranked[i].key == mine.key && ranked[i].e < mine.e);
+        for (int i = 0; i < n; ++i) rank += ranked.key[i] > mine;
     }
-    ranked[32 + rank] = mine;                                      // those without one behind
+    ranked.key[32 + rank] = mine;                                  // those without one behind
+    if (!kByLogit) ranked.x[32 + rank] = lane < n ? ranked.x[lane] : kNone;
     __syncwarp();
-    mine = ranked[32 + lane];
-    if (!kByLogit && k32) {
-        const float key0 = (float)__shfl_up_sync(0xffffffffu, mine.key, 1), x0 = __shfl_up_sync(0xffffffffu, mine.x, 1);
-        const int e0 = __shfl_up_sync(0xffffffffu, mine.e, 1);
+    mine = ranked.key[32 + lane];
+    expert = key_expert(mine);
+    logit = kByLogit ? key_choice(mine) : ranked.x[32 + lane];
+    if (!kByLogit) {
+        const float key1 = key_choice(mine), key0 = __shfl_up_sync(0xffffffffu, key1, 1), x0 = __shfl_up_sync(0xffffffffu, logit, 1);
+        const int e0 = __shfl_up_sync(0xffffffffu, expert, 1);
         bool near = false;
-        if (lane > 0 && lane <= a.k && mine.e >= 0) {
-            const float key1 = (float)mine.key, b0 = a.bias ? a.bias[e0] : 0.f, b1 = a.bias ? a.bias[mine.e] : 0.f;
-            near = !(x0 == mine.x && b0 == b1) && too_near(a, key0, key1, largest);
+        if (lane > 0 && lane <= a.k && expert >= 0) {
+            const float b0 = a.bias ? a.bias[e0] : 0.f, b1 = a.bias ? a.bias[expert] : 0.f;
+            near = !(x0 == logit && b0 == b1) && too_near(a, key0, key1, largest);
         }
         if (__any_sync(0xffffffffu, near)) {
             // the row's logits, for the sum in 64 bits
@@ -481,36 +488,12 @@ __device__ __forceinline__ Decided pick(const RouteArgs& a, const float (&x)[kEa
             for (int i = 0; i < kEach; ++i)
                 if (Held<kEach>::index(i) < a.E) again[Held<kEach>::index(i)] = x[i];
             __syncwarp();
-            const float2 m = rank_again(a, again, s.top, mine.x, mine.e, n);
-            mine.x = m.x;
-            mine.e = __float_as_int(m.y);
+            const float2 m = rank_again(a, again, s.top, logit, expert, n);
+            logit = m.x;
+            expert = __float_as_int(m.y);
         }
     }
-    return kSure;
-}
-
-// The same in 64 bits, by searches where a lane each is not enough for what is ranked.
-template <int kEach>
-__device__ __noinline__ void pick_again(const RouteArgs& a, uint8_t* mem, Scores<float> s, bool many, long long t) {
-    const int lane = threadIdx.x & 31;
-    float* again = reinterpret_cast<float*>(mem + (size_t)a.E * 8);
-    if (!many) {
-        float x[kEach];
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) x[i] = Held<kEach>::index(i) < a.E ? again[Held<kEach>::index(i)] : kNone;
-        Ranked<double> mine;
-        if (pick<double, kEach, false>(a, x, mem, s, mine) == kSure) {
-            const bool some = lane < a.k && mine.e >= 0;
-            const float w = weight(a, some ? mine.x : kNone, s);
-            if (lane < a.k) {
-                a.ids[t * a.k + lane] = some ? mine.e : -1;
-                a.w[t * a.k + lane] = w;
-            }
-            return;
-        }
-        __syncwarp();
-    }
-    route_row(a, again, reinterpret_cast<double*>(mem), t);
+    return kDone;
 }
 
 template <typename L, int kEach, bool kByLogit>
@@ -523,14 +506,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
     uint8_t* mem = route_mem + warp * route_bytes(a.E);
     float x[kEach];
     load_row<L, kEach>(x, static_cast<const L*>(a.logits) + t * a.stride, a.E);
-    Scores<float> s{0.f, 1.f, a.sigmoid};
-    Ranked<float> mine;
-    const Decided d = pick<float, kEach, kByLogit>(a, x, mem, s, mine);
-    if (d == kSure) {
-        const bool some = lane < a.k && mine.e >= 0;
-        const float w = weight(a, some ? mine.x : kNone, s);
+    Scores s{0.f, 1.f};
+    float logit;
+    int expert;
+    const Picked p = pick<kEach, kByLogit>(a, x, mem, s, logit, expert);
+    if (p == kDone) {
+        const bool some = lane < a.k && expert >= 0;
+        const float w = weight(a, some ? logit : kNone, s);
         if (lane < a.k) {
-            a.ids[t * a.k + lane] = some ? mine.e : -1;
+            a.ids[t * a.k + lane] = some ? expert : -1;
             a.w[t * a.k + lane] = w;
         }
         return;
@@ -541,7 +525,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(const RouteArgs
     for (int i = 0; i < kEach; ++i)
         if (Held<kEach>::index(i) < a.E) again[Held<kEach>::index(i)] = x[i];
     __syncwarp();
-    pick_again<kEach>(a, mem, s, kByLogit || d == kMany, t);
+    route_row(a, again, reinterpret_cast<double*>(mem), p == kMany, t);
 }
 
 template <typename L, int kEach, bool kByLogit>
