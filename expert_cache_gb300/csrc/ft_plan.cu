@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(kMaxSeqs) kv_plan_kernel(const PlanArgs a) {
     };
     const int at = rank * blockDim.x + threadIdx.x, step = ctas * blockDim.x;
     const int live = (int)min(all_rows, (long long)c.n_tokens);
-    for (int t = at; t < c.n_tokens; t += step) {
+    for (unsigned i = at; i < (unsigned)c.n_tokens; i += step) {
+        const int t = (int)i;
         int slot = -1, pos = 0;
         if (t < live) {
             const int q = count_up_to(end, c.n_seqs, t), row = t - (q ? end[q - 1] : 0);

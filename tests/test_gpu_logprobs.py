@@ -74,7 +74,7 @@ def tokens_of(seed, n, V):
 
 
 @pytest.mark.parametrize("n,V", [(1, 1), (3, 2), (2, 7), (5, 31), (4, 64), (3, 257), (9, 1000), (2, 4095), (3, 8200), (2, 30011), (1, 65536), (3, 100003), (1, 131072),
-                                 (2, 200000), (1, 262147), (700, 500), (160, 5000), (330, 33000)])
+                                 (2, 200000), (1, 262147), (700, 500), (160, 5000), (330, 33000), (70000, 3)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("k", [0, 1, 5, 20, 32])
 def test_sizes(ft, n, V, dtype, k):
@@ -179,6 +179,18 @@ def test_temperatures_and_tokens(ft):
                        top_ids=out[2] if 2 in keep else None, top_logp=out[3] if 3 in keep else None, k=5 if 2 in keep else 0)
         for i, (a, b) in enumerate(zip(out, full)):
             assert torch.equal(a, b if i in keep else torch.full_like(b, -3))
+
+
+def test_two_calls_at_once(ft):
+    xs, t = [logits(i, 300, 50000, torch.bfloat16) for i in range(2)], tokens_of(0, 300, 50000)
+    alone = [run(ft, x, t, 7) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [run(ft, x, t, 7, stream=s) for x, s in zip(xs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(alone, outs):
+            assert all(torch.equal(p, q) for p, q in zip(a, b))
 
 
 def test_far_rows_streams_and_graphs(ft):

@@ -69,6 +69,29 @@ def test_shapes(ft, T, E, k, groups, score, bias, dtype):
             check(x, *run(ft, x, k, **kw), k, **kw)                # may leave fewer than k experts
 
 
+@pytest.mark.parametrize("E", [31, 32, 33, 63, 65, 127, 129, 255, 257, 511, 512, 513, 1023, 1025])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sizes_around_the_variants(ft, E, dtype):
+    """Numbers of experts at which another variant takes over, with one expert chosen and with as many as there may be."""
+    x = logits(E, 5, E, dtype, pad=E % 2)
+    b = np.random.default_rng(E).standard_normal(E).astype(np.float32) * 0.1
+    for k in (1, 31, min(E, 32)):
+        for bias in (None, b):
+            kw = dict(score="sigmoid" if E % 2 else "softmax", bias=bias)
+            check(x, *run(ft, x, k, **kw), k, **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_experts_that_come_out_on_top_together(ft, dtype):
+    """The chosen ones are neighbours: rising and falling rows and biases."""
+    for E in (40, 160, 256, 500):
+        x = torch.stack([torch.arange(E) * 0.5, -torch.arange(E) * 0.5, torch.zeros(E), (torch.arange(E) // 8) * 1.0]).to(dtype).cuda()
+        for bias in (None, np.arange(E, dtype=np.float32) * 10, -np.arange(E, dtype=np.float32)):
+            for groups in (1, 4):
+                kw = dict(score="softmax", bias=bias, n_group=groups, topk_group=2 if groups > 1 else 1, group_best=2)
+                check(x, *run(ft, x, 9, **kw), 9, **kw)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E", [8, 100, 256, 2048])
 def test_ties_take_the_lower_index(ft, score, E):
