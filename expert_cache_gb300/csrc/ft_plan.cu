@@ -5,6 +5,11 @@
 // for another: the r-th page that is taken is the r-th from the top of the stack once everything given lies on it, so a
 // token finds its page from its sequence's sums alone, in the table (held before), on the old stack, or among the given ones (their
 // owners' table entries, which nobody changes).
+//
+// Bound by latency throughout (32 bytes a sequence, 8 a token): the launch, one round of loads, the sums' barriers, a search and a
+// load per token.  16 sequences of a token each: 2.4 us in a graph, 6.2 us by calls (their host time); 200 sequences over 60,000
+// places for tokens, of which 12,000 are filled, 20 ending: 8.0 us.  Sums in one pass instead of two save 0.2 to 0.5 us; four tokens
+// per thread at a time, and more threads than tokens for the pages given back, were slower (8.5 and 5.9 against 8.2 and 5.0 us).
 #include "ft_kv_host.cuh"
 
 namespace ft {

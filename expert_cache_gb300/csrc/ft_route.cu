@@ -7,6 +7,11 @@
 // group that stays and the first that does not) lie within their bounds, and do not come from the same logit and bias, the row is
 // decided again in 64 bits; so the ids are the formula's.  Without a bias, and without sums of a group's choices, the scores' order
 // is the logits' own and needs no rounding at all.
+//
+// Bound by latency and, for many tokens, by instructions (570 a row of 256), not by the 4.7 MB of 8192 tokens of 256 experts
+// (0.7 us): those take 6.6 us, one token 2.0 us, 16 with groups and a bias 3.8 us, 5003 of 160 experts with a bias 6.4 us, and 12
+// to 14 us where a row among them goes to 64 bits, whose latency stands alone at the end.  k searches of a warp through shared
+// memory, the form above 512 experts, take 14.2, 4.3, 7.3 and 31 us.
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
