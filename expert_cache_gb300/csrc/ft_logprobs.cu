@@ -115,6 +115,11 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float inverse_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // Unsigned words in the order of the floats.
 __device__ __forceinline__ unsigned ordered(float x) {
     const unsigned u = __float_as_uint(x);
@@ -161,12 +166,13 @@ struct Sums {
     float top;                         // the largest seen: the sample's, or one that reached the limit
     Pair s, d;
 
-    __device__ __forceinline__ void against(float to, float bound, float c) {
+    // span: some 100 / c, 0 or infinite where that is no normal number.
+    __device__ __forceinline__ void against(float to, float bound, float c, float span) {
         ref = to;
-        far = to == kNone ? kNone : to + 100.f / c;
-        plain = !(fabsf(to) * c < 0x1p60f && to - 200.f / c > -1e38f);
+        far = to == kNone ? kNone : to + span;
+        plain = !(fabsf(to) * c < 0x1p60f && span > 0.f && to - 2.f * span > -1e38f);
         rc = plain ? 0.f : to * c;
-        floor = Vec<L>::limit(to - 200.f / c);
+        floor = Vec<L>::limit(to - 2.f * span);
         limit = Vec<L>::limit(plain ? kNone : fminf(bound, far));
     }
     __device__ __forceinline__ void add(const Vec<L>& v, float c) {
@@ -199,7 +205,7 @@ __device__ __noinline__ Sums<L> add_far(Sums<L> a, Vec<L> v, float bound, float 
     most = most == most ? fminf(most, FLT_MAX) : kNone;
     if (most > a.far) {
         const float2 m = a.moved(most, c);
-        a.against(most, bound, c);
+        a.against(most, bound, c, 100.f * inverse_fast(c));
         const float off = a.plain ? 0.f : fmaf(a.ref, c, -a.rc), f = exp2_fast(off);
         a.s = pair(f * m.x, 0.f);
         a.d = pair(f * fmaf(off, m.x, m.y), 0.f);
@@ -282,8 +288,8 @@ struct Part {
         constexpr int kN = Vec<L>::kN;
         head = min((int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(L), V);
         const int n = (V - head) / kN;
-        lo = (int)((long long)n * rank >> shift);
-        const int own = (int)((long long)n * (rank + 1) >> shift) - lo;
+        lo = (int)((unsigned)n * rank >> shift);                    // n is at most 2^28
+        const int own = (int)((unsigned)n * (rank + 1) >> shift) - lo;
         steps = own / kLogThreads;
         more = own % kLogThreads;
         rest = rank == 0 ? V - n * kN : 0;
@@ -378,16 +384,15 @@ __device__ __forceinline__ int count_before(int n, int parts, F before) {
 }
 
 // The k largest of n different keys, in order, to out; where there are fewer, numbers for none that no other CTA of the row has.
+// Few keys by few warps: the others have nothing to wait for but a barrier.
 __device__ __forceinline__ void rank_list(const Key* list, int n, int k, int rank, Key* out) {
     for (int j = n + threadIdx.x; j < k; j += kLogThreads) out[j] = 1 + rank * kMaxK + j;
-    int shift = 0;                                                 // 1 << shift threads for an entry
-    while (shift < 5 && n << (shift + 1) <= kLogThreads) ++shift;
-    const int parts = 1 << shift;
-    for (int first = 0; first < n; first += kLogThreads >> shift) {
-        const int e = first + ((int)threadIdx.x >> shift);
+    const int shift = n <= 32 ? 2 : n <= 128 ? 1 : 0;              // 1 << shift threads for an entry
+    for (int first = threadIdx.x & ~31; first < n << shift; first += kLogThreads) {
+        const int e = (first + (int)(threadIdx.x & 31)) >> shift;
         const Key mine = e < n ? list[e] : 0;
-        const int before = count_before(n, parts, [&](int i) { return list[i] > mine; });
-        if (e < n && before < k && (threadIdx.x & (parts - 1)) == 0) out[before] = mine;
+        const int before = count_before(n, 1 << shift, [&](int i) { return list[i] > mine; });
+        if (e < n && before < k && (threadIdx.x & ((1 << shift) - 1)) == 0) out[before] = mine;
     }
 }
 
@@ -479,19 +484,19 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
     }
     if (threadIdx.x == 0) sm.count = 0;
     __syncthreads();
-    {
-        const int n = kLogWarps * each, parts = min(kLogThreads / n, 32), mine_at = threadIdx.x / parts;
-        const float mine = mine_at < n ? sm.few[mine_at] : kNone;
-        const int before = count_before(n, parts, [&](int i) { return sm.few[i] > mine || (sm.few[i] == mine && i < mine_at); });
-        if (mine_at < n && before == 0) sm.ref = mine;
-        if (mine_at < n && before == (kTop ? c.k - 1 : 0)) sm.bound = mine;
+    if ((int)(threadIdx.x & ~31) < 4 * kLogWarps * each) {        // four threads for each of them
+        const int n = kLogWarps * each, mine_at = threadIdx.x >> 2;
+        const float mine = sm.few[mine_at];
+        const int before = count_before(n, 4, [&](int i) { return sm.few[i] > mine || (sm.few[i] == mine && i < mine_at); });
+        if (before == 0) sm.ref = mine;
+        if (before == (kTop ? c.k - 1 : 0)) sm.bound = mine;
     }
     __syncthreads();
     const float bound = sm.bound;
     Sums<L> a;
     a.s = a.d = 0;
     a.top = sm.ref;
-    a.against(sm.ref, bound, c2);
+    a.against(sm.ref, bound, c2, 100.f * inverse_fast(c2));
     int hits = 0;
     if (p.rest) take<L, kTop, 1>(sm, a, hits, rest, [&](int) { return p.rest_index(); }, bound, c2);
     uint32_t slot = 0;
