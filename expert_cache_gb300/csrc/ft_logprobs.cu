@@ -260,6 +260,7 @@ __device__ __forceinline__ void take(LogShared& sm, Sums<L>& a, int& hits, const
                 const float most = Vec<L>::value(v[j].max());
                 const bool keep = most >= bound && most > kNone;
                 const unsigned kept = __ballot_sync(0xffffffffu, keep);
+                if (!kept) continue;
                 const int at = hits + __popc(kept & ((1u << (threadIdx.x & 31)) - 1));
                 if (keep && at < kHits) {
                     v[j].to_shared((uint32_t)__cvta_generic_to_shared(&sm.hit[threadIdx.x >> 5][at]));
@@ -387,7 +388,7 @@ __device__ __forceinline__ int count_before(int n, int parts, F before) {
 // Few keys by few warps: the others have nothing to wait for but a barrier.
 __device__ __forceinline__ void rank_list(const Key* list, int n, int k, int rank, Key* out) {
     for (int j = n + threadIdx.x; j < k; j += kLogThreads) out[j] = 1 + rank * kMaxK + j;
-    const int shift = n <= 32 ? 2 : n <= 128 ? 1 : 0;              // 1 << shift threads for an entry
+    const int shift = n <= 64 ? 3 : n <= 128 ? 2 : n <= 256 ? 1 : 0;              // 1 << shift threads for an entry
     for (int first = threadIdx.x & ~31; first < n << shift; first += kLogThreads) {
         const int e = (first + (int)(threadIdx.x & 31)) >> shift;
         const Key mine = e < n ? list[e] : 0;
@@ -646,8 +647,8 @@ extern "C" ft_status ft_logprobs(const ft_logprob* call, void* stream) {
         return FT_ERR_ARG;
     if (!aligned(c.tokens, 4) || !aligned(c.logp, 4) || !aligned(c.entropy, 4) || !aligned(c.top_ids, 4) || !aligned(c.top_logp, 4)) return FT_ERR_ARG;
     NvtxRange r("ft_logprobs");
-    // CTAs of a row: as many as leave no SM with two, each with a vector or more per thread (48 rows of 100,003 fp32, k = 20: 2 CTAs
-    // 11.2 us, 4, of which some share an SM, 12.3 us, 8 19.1 us; 24 rows of 131,072 bf16: 4 7.2 us, 8 7.4 us)
+    // CTAs of a row, a power of two: as many as leave no SM with two, each with a vector or more per thread (48 rows of 100,003 fp32, k =
+    // 20: 2 CTAs 11.0 us, 3 12.2 us, 4, of which some share an SM, 12.3 us; 24 rows: 4 8.5 us, 6 10.5 us)
     int shift = 0;
     const long long vectors = (long long)c.V / (c.dtype == FT_DTYPE_BF16 ? 8 : 4);
     while (1 << shift < kMaxCtas && (2LL << shift) * c.n <= sm_count() && vectors > (long long)kLogThreads << shift) ++shift;
