@@ -10,11 +10,11 @@
 // the part is read again; where that does not help (equal logits by the thousand, rising ones), k searches find them.  Which ones
 // these are does not depend on any order: value, then index.
 //
-// 2048 rows of 131,072 bf16: 101 us, 5.3 TB/s, 0.80 of the copy rate; without the k largest 81 to 84 us, the copy rate.  The k
-// largest cost the barriers of the sample and of the list, during which a CTA's SM has only the other one's loads under way (2.7
-// us a row of 15).  One row: 5.5 us in 8 CTAs, launch and barriers.  On the way: vectors through registers, 4 or 8 under way,
+// 2048 rows of 131,072 bf16: 95 us, 5.6 TB/s, 0.84 of the copy rate; without the k largest 81 to 84 us, the copy rate.  The k
+// largest cost the barriers of the sample and of the list, during which a CTA's SM has only the other one's loads under way (2
+// us a row of 14).  One row: 5.1 us in 8 CTAs, launch and barriers.  On the way: vectors through registers, 4 or 8 under way,
 // 151 to 193 us; through thread-owned shared memory 114 us; neighbouring vectors instead of four stretches of the row 103 us; the
-// list by warps instead of at once 101 us, and ranks by several threads per entry (one row 7.3 -> 5.5 us).  CTAs of 256 threads
+// list by warps instead of at once 101 us, and ranks by several threads per entry (one row 7.3 -> 5.5 us), of few warps 95 us.  CTAs of 256 threads
 // (107 us) or 1024 (151 us), rows in a loop with the next one's first vectors loaded ahead (127 us), and the bound worked out by every
 // warp for itself (107 us) were slower.
 #include <atomic>

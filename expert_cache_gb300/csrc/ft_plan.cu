@@ -7,9 +7,9 @@
 // owners' table entries, which nobody changes).
 //
 // Bound by latency throughout (32 bytes a sequence, 8 a token): the launch, one round of loads, the sums' barriers, a search and a
-// load per token.  16 sequences of a token each: 2.4 us in a graph, 6.2 us by calls (their host time); 200 sequences over 60,000
-// places for tokens, of which 12,000 are filled, 20 ending: 8.0 us.  Sums in one pass instead of two save 0.2 to 0.5 us; four tokens
-// per thread at a time, and more threads than tokens for the pages given back, were slower (8.5 and 5.9 against 8.2 and 5.0 us).
+// load per token.  16 sequences of a token each: 2.2 us in a graph, 6.2 us by calls (their host time); 200 sequences over 60,000
+// places for tokens, of which 12,000 are filled, 20 ending: 6.3 us.  With sums of 64 bits it was 8.0 us (every CTA executes them, and
+// a CTA's instructions are its SM's); four tokens or four given pages per thread at a time were slower (8.5 and 8.2 us).
 #include "ft_kv_host.cuh"
 
 namespace ft {
@@ -22,43 +22,45 @@ struct PlanArgs {
     int* status;
 };
 
-// Exclusive prefix sums of each thread's values over the block; every thread calls it.
+// Sums stop at kMost, which no number of rows or pages that is served reaches.
+constexpr unsigned kMost = 1u << 30;
+__device__ __forceinline__ unsigned sum_up_to(unsigned a, unsigned b) { return min(a + b, kMost); }
+
+// Prefix sums (with the thread's own value) of each thread's values over the block; every thread calls it.
 template <int N>
-__device__ __forceinline__ void block_sums(const long long (&v)[N], long long (&before)[N], long long (&total)[N], long long (*buf)[33]) {
+__device__ __forceinline__ void block_sums(const unsigned (&v)[N], unsigned (&incl)[N], unsigned (&total)[N], unsigned (*buf)[32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    long long incl[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         incl[i] = v[i];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, incl[i], o);
-            if (lane >= o) incl[i] += t;
+            const unsigned t = __shfl_up_sync(0xffffffffu, incl[i], o);
+            if (lane >= o) incl[i] = sum_up_to(incl[i], t);
         }
         if (lane == 31) buf[i][warp] = incl[i];
     }
     __syncthreads();
     for (int i = warp; i < N; i += warps) {
-        long long w = lane < warps ? buf[i][lane] : 0;
+        unsigned w = lane < warps ? buf[i][lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += t;
+            const unsigned t = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w = sum_up_to(w, t);
         }
         buf[i][lane] = w;
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        before[i] = (warp ? buf[i][warp - 1] : 0) + incl[i] - v[i];
+        if (warp) incl[i] = sum_up_to(incl[i], buf[i][warp - 1]);
         total[i] = buf[i][warps - 1];
     }
     __syncthreads();
 }
 
 // How many of the ascending values at[0 .. n) are at most x.
-template <typename T>
-__device__ __forceinline__ int count_up_to(const T* at, int n, T x) {
+__device__ __forceinline__ int count_up_to(const int* at, int n, int x) {
     int lo = 0, hi = n;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -72,8 +74,10 @@ __device__ __forceinline__ int count_up_to(const T* at, int n, T x) {
 // the sums out for itself, and the state, which may be updated in place, is written once all have read it.
 __global__ void __launch_bounds__(kMaxSeqs) kv_plan_kernel(const PlanArgs a) {
     __shared__ int end[kMaxSeqs], len[kMaxSeqs], held[kMaxSeqs], want[kMaxSeqs];       // end: row after a sequence's last
-    __shared__ long long taken[kMaxSeqs], given_end[kMaxSeqs];                          // taken: before it, -1 if it is refused
-    __shared__ long long buf[3][33];
+    __shared__ int taken[kMaxSeqs], given_end[kMaxSeqs];                                // taken: before it, -1 if it is refused
+    __shared__ unsigned buf[3][32];
+    __shared__ int last_taken;
+    if (threadIdx.x == 0) last_taken = 0;
     pdl_wait_and_release();
     const ft_kv_step& c = a.c;
     const int s = threadIdx.x, rank = blockIdx.x, ctas = gridDim.x;
@@ -100,42 +104,40 @@ __global__ void __launch_bounds__(kMaxSeqs) kv_plan_kernel(const PlanArgs a) {
     if (!ends)
         fine = fine && l >= 0 && (((long long)l + page - 1) >> a.page_shift) <= h && wants <= c.table_stride && after <= 0x7FFFFFFFLL &&
                (!c.tree_mask || rows <= kTreeMax);
-    long long v[3] = {rows, fine ? max(wants - h, 0LL) : 0, fine ? max(h - wants, 0LL) : 0}, before[3], total[3];
-    block_sums<3>(v, before, total, buf);
-    const long long first = before[0], all_rows = total[0];
-    if (all_rows > c.n_tokens) {                                 // those whose rows do not all fit take and give nothing
-        fine = fine && (rows == 0 || first + rows <= c.n_tokens);
+    const unsigned lacks = wants > h ? (unsigned)min(wants - h, (long long)kMost) : 0;
+    unsigned v[3] = {min((unsigned)rows, kMost), fine ? lacks : 0, fine && wants < h ? (unsigned)(h - wants) : 0}, upto[3], total[3];
+    block_sums<3>(v, upto, total, buf);
+    const unsigned last = upto[0], all_rows = total[0];          // of this sequence, of all
+    if (all_rows > (unsigned)c.n_tokens) {                       // those whose rows do not all fit take and give nothing
+        fine = fine && (rows == 0 || last <= (unsigned)c.n_tokens);
         if (!fine) v[1] = v[2] = 0;
-        block_sums<3>(v, before, total, buf);
+        block_sums<3>(v, upto, total, buf);
     }
     if (!fine) bits |= FT_DEV_BAD_ID;
-    const long long avail = n_free + total[2];
-    const bool served = fine && (v[1] == 0 || before[1] + v[1] <= avail);
+    const int avail = n_free + (int)total[2];
+    const bool served = fine && (v[1] == 0 || upto[1] <= min((unsigned)avail, kMost - 1));
     if (fine && !served) bits |= FT_DEV_NO_PAGES;
     if (s < c.n_seqs) {
-        end[s] = (int)min(first + rows, (long long)c.n_tokens);
+        end[s] = (int)min(last, (unsigned)c.n_tokens);
         len[s] = l;
         held[s] = h;
         want[s] = (int)wants;
-        taken[s] = served ? before[1] : -1;
-        given_end[s] = before[2] + v[2];
+        taken[s] = served ? (int)(upto[1] - v[1]) : -1;
+        given_end[s] = (int)upto[2];
     }
-    // the pages that leave the stack: those of the last sequence that is served with any
-    long long all_taken = served && v[1] ? before[1] + v[1] : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all_taken = max(all_taken, __shfl_xor_sync(0xffffffffu, all_taken, o));
-    if ((s & 31) == 0) buf[0][s >> 5] = all_taken;
+    // the pages that leave the stack: up to those of the last sequence that is served with any
+    const unsigned most = __reduce_max_sync(0xffffffffu, served && v[1] ? upto[1] : 0);
+    if ((s & 31) == 0) atomicMax(&last_taken, (int)most);
     __syncthreads();
-    for (int w = 0; w < (int)blockDim.x >> 5; ++w) all_taken = max(all_taken, buf[0][w]);
-    const long long left = avail - all_taken;
+    const int left = avail - last_taken;
 
     // The g-th page given back.
-    auto given = [&](long long g) {
+    auto given = [&](int g) {
         const int q = count_up_to(given_end, c.n_seqs, g);
         return c.block_table[(size_t)q * c.table_stride + want[q] + (g - (q ? given_end[q - 1] : 0))];
     };
     const int at = rank * blockDim.x + threadIdx.x, step = ctas * blockDim.x;
-    const int live = (int)min(all_rows, (long long)c.n_tokens);
+    const int live = (int)min(all_rows, (unsigned)c.n_tokens);
     for (unsigned i = at; i < (unsigned)c.n_tokens; i += step) {
         const int t = (int)i;
         int slot = -1, pos = 0;
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kMaxSeqs) kv_plan_kernel(const PlanArgs a) {
                 if (j < held[q]) {
                     pg = *entry;
                 } else {
-                    const long long from = avail - 1 - (taken[q] + j - held[q]);
+                    const int from = avail - 1 - (taken[q] + j - held[q]);
                     pg = from >= n_free ? given(from - n_free) : c.free_pages[from];
                     if ((p & (int)(page - 1)) == 0) *entry = pg;       // a page that is taken starts with a new token
                 }
@@ -161,9 +163,9 @@ __global__ void __launch_bounds__(kMaxSeqs) kv_plan_kernel(const PlanArgs a) {
         if (c.positions) c.positions[t] = pos;
     }
     // what is given and not taken at once
-    const long long pushed = min(left, (long long)a.n_pages) - n_free;
+    const int pushed = min(left, a.n_pages) - n_free;
     if (left > a.n_pages) bits |= FT_DEV_BAD_ID;
-    for (long long g = at; g < pushed; g += step) c.free_pages[n_free + g] = given(g);
+    for (int g = at; g < pushed; g += step) c.free_pages[n_free + g] = given(g);
 
     if (ctas > 1) {
         asm volatile("barrier.cluster.arrive.release;" ::: "memory");
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(kMaxSeqs) kv_plan_kernel(const PlanArgs a) {
         }
         if (s == 0) {
             c.q_start[0] = 0;
-            *c.n_free_out = (int)min(left, (long long)a.n_pages);
+            *c.n_free_out = min(left, a.n_pages);
         }
     }
     if (bits) atomicOr(a.status, bits);
@@ -196,7 +198,7 @@ extern "C" ft_status ft_kv_plan(ft_kv* kv, const ft_kv_step* call, void* stream)
     if (!kv) return FT_ERR_ARG;
     if (!call) return fail(kv, FT_ERR_ARG, "plan: NULL call");
     const ft_kv_step& c = *call;
-    if (c.n_seqs < 0 || c.n_seqs > kv->d.max_seqs || c.n_tokens < 0 || c.table_stride < 1)
+    if (c.n_seqs < 0 || c.n_seqs > kv->d.max_seqs || c.n_tokens < 0 || c.n_tokens >= (int)kMost || c.table_stride < 1)
         return fail(kv, FT_ERR_ARG, "plan: n_seqs, n_tokens or table_stride out of range");
     if (!c.n_free || !c.free_pages || !c.q_start || !c.n_free_out || (c.n_tokens && !c.slots) ||
         (c.n_seqs && (!c.n_new || !c.len || !c.held || !c.block_table || !c.kv_len || !c.len_out || !c.held_out)))

@@ -549,8 +549,8 @@ ft_status ft_kv_attention(ft_kv* kv, const ft_kv_attn* call, void* stream);
  * Entries of the table past held_out and of the stack from n_free_out on are left as they were (surplus pages' entries keep
  * their old value).  A page outside [0, n_pages) in the table or on the stack gives its tokens the slot -1 and sets
  * FT_DEV_BAD_ID, as does n_free outside [0, n_pages] (it is cut to that) or pages pushed past n_pages (dropped).
- * Errors (nothing launched): FT_ERR_ARG for n_seqs outside [0, max_seqs], n_tokens < 0, table_stride < 1, NULL pointers
- * (arrays of no elements may be NULL). */
+ * Errors (nothing launched): FT_ERR_ARG for n_seqs outside [0, max_seqs], n_tokens outside [0, 2^30), table_stride < 1, NULL
+ * pointers (arrays of no elements may be NULL). */
 typedef struct {
     const int32_t* n_new;       /* device [n_seqs] */
     const int32_t* len;         /* device [n_seqs] */

@@ -137,6 +137,22 @@ def test_bad_descriptions(ft):
         assert c.step([-1, 9], 64)[1] & S.BAD_ID
 
 
+def test_states_of_more_pages_than_there_are(ft):
+    """Every sequence claims all pages, or wants more than any table may have: sums that 32 bits do not hold are cut, nothing is read
+    outside its row."""
+    c = State(ft, [0] * 1000, n_pages=5000, stride=5000, held=[0] * 1000)
+    c.held[:] = 5000
+    c.table[:] = np.arange(5000)
+    want, status = c.step([1] + [-1] * 999, 4)
+    assert status == S.BAD_ID and want["n_free_out"] == 5000
+    c = State(ft, [0] * 1000, n_pages=200, stride=1 << 16, page=256, held=[0] * 1000)
+    want, status = c.step([1 << 23] * 1000, 1 << 10)
+    assert status == S.BAD_ID and not want["kv_len"].any()
+    c = State(ft, [0] * 3, n_pages=200, stride=1 << 16, page=16, held=[0] * 3)
+    want, status = c.step([5, 1 << 20, 5], (1 << 20) + 10)
+    assert status == S.NO_PAGES and want["kv_len"].tolist() == [5, 0, 0]
+
+
 def test_rows_past_the_tokens(ft):
     c = State(ft, [16, 16, 16, 16])
     want, status = c.step([5, 6, 0, -1], 8)                       # the second's rows do not all fit
@@ -157,7 +173,7 @@ def test_refusals(ft):
     t = dict(n_new=dev([1, 1]), len=dev([4, 5]), held=dev([1, 1]), block_table=dev(c.table), table_stride=c.stride, free_pages=dev(c.free), n_free=dev([3]),
              n_seqs=2, n_tokens=4, q_start=dev([0, 0, 0]), kv_len=dev([0, 0]), slots=dev([0] * 4), len_out=dev([0, 0]), held_out=dev([0, 0]),
              n_free_out=dev([0]))
-    for bad in (dict(n_seqs=-1), dict(n_seqs=3), dict(n_tokens=-1), dict(table_stride=0), *({k: None} for k in (
+    for bad in (dict(n_seqs=-1), dict(n_seqs=3), dict(n_tokens=-1), dict(n_tokens=1 << 30), dict(table_stride=0), *({k: None} for k in (
             "n_new", "len", "held", "block_table", "free_pages", "n_free", "q_start", "kv_len", "slots", "len_out", "held_out", "n_free_out"))):
         with pytest.raises(ft.FtError, match="plan") as ei:
             ft.ft_kv_plan(c.kv.handle, **(t | bad))
