@@ -534,12 +534,12 @@ ft_status ft_kv_attention(ft_kv* kv, const ft_kv_attn* call, void* stream);
  * want = ceil(after / page_size) pages afterwards:
  *   - surplus pages (j >= want) of all sequences are pushed on the stack of free pages, in ascending (s, j);
  *   - then missing ones are popped from it, in ascending (s, j), and entered in the table.
- * A sequence is refused if pages run out (if it takes any, and those that the sequences up to it take are more than are
- * free; FT_DEV_NO_PAGES), or if its description does not hold (FT_DEV_BAD_ID): held outside [0, table_stride] or
+ * A sequence is refused if pages run out (if it takes any, and those that the sequences up to it ask for, this one and others refused
+ * for want of pages too, are more than are free; FT_DEV_NO_PAGES), or if its description does not hold (FT_DEV_BAD_ID): held outside [0, table_stride] or
  * above n_pages; for one that goes on also len < 0, held less than its len needs, rows past n_tokens, more than
  * table_stride pages or 2^31 - 1 tokens, and, with tree_mask, more than 64 new tokens.  A refused sequence keeps its len
  * and its pages; its rows stay in q_start, get the slot -1 (which ft_kv_append skips) and kv_len 0 (under which
- * ft_kv_attention gives o = 0), and the sequences that it leaves room for are served.
+ * ft_kv_attention gives o = 0), and others are served as if it asked for nothing, but for the pages that it was refused.
  *   q_start   [n_seqs + 1]  first row of each sequence, at most n_tokens
  *   kv_len    [n_seqs]      the length that attention is to use (after, or 0 for a refused sequence)
  *   slots, positions [n_tokens]  of each row; a drafted row's position is len + the number of set bits of its mask other than
