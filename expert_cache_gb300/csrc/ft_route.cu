@@ -3,9 +3,9 @@
 // Up to 512 experts the choices stay in registers.  The (k + 1)-th largest of the lanes' maxima bounds the (k + 1)-th largest choice
 // from below; what reaches it, k to some 1.3 k of 256, goes through shared memory and is ranked, each lane one.
 //
-// Choices are computed in fp32 with a bound on their error.  Where two neighbours of the sorted first k + 1 (or the last
-// group that stays and the first that does not) lie within their bounds, and do not come from the same logit and bias, the row is
-// decided again in 64 bits; so the ids are the formula's.  Without a bias, and without sums of a group's choices, the scores' order
+// Choices are computed in fp32 with a bound on their error.  Where two neighbours of the sorted first k, the k-th and one behind it
+// or the last group that stays and the first that does not lie within their bounds, and do not come from the same logit and bias, the
+// row is decided again in 64 bits; so the ids are the formula's.  Without a bias, and without sums of a group's choices, the scores' order
 // is the logits' own and needs no rounding at all.
 //
 // Bound by latency and, for many tokens, by instructions (570 a row of 256), not by the 4.7 MB of 8192 tokens of 256 experts
@@ -56,10 +56,10 @@ __device__ __forceinline__ V warp_sum(V v) {
     return v;
 }
 
-// e^y for y <= 0 (below -700: e^-700) to some 2^-51: y = n ln 2 + r with ln 2 in two parts (Cody and Waite 1980), the first of 41 bits, so
+// e^y for y <= 0 to some 2^-51, or half of 2^-1074: y = n ln 2 + r with ln 2 in two parts (Cody and Waite 1980), the first of 41 bits, so
 // that n times it is exact; Taylor's series to r^13 / 13!, whose rest is below 2^-57 for |r| <= ln 2 / 2.
 __device__ __forceinline__ double exp_negative(double y) {
-    y = fmax(y, -700.0);
+    y = fmax(y, -750.0);                                         // 0, as all below -745.2
     const double n = rint(y * 1.4426950408889634);
     const double r = fma(n, -0x1.3de6af278ece6p-42, fma(n, -0x1.62e42fefa3000p-1, y));
     double p = 1.0 / 6227020800.0;
@@ -67,7 +67,8 @@ __device__ __forceinline__ double exp_negative(double y) {
                             1.0 / 39916800, 1.0 / 479001600};
 #pragma unroll
     for (int i = 12; i >= 0; --i) p = fma(p, r, c[i]);
-    return __longlong_as_double(__double_as_longlong(p) + ((long long)(int)n << 52));
+    const int m = (int)n, h = m / 2;                             // 2^m in two factors: below 2^-1022 there is only the second rounding
+    return p * __longlong_as_double((long long)(1023 + h) << 52) * __longlong_as_double((long long)(1023 + m - h) << 52);
 }
 
 // 1 / x to some 2^-52 for a normal fp32 range of x: two steps of Newton's from the fp32 reciprocal.
@@ -169,10 +170,10 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, const float* x, V* ke
         }
         const bool stays = g < a.n_group && before < a.topk_group;
         if (sizeof(V) == 4 && !a.by_logit) {
-            // worth - err of those that stay against worth + err of those that do not
+            // worth - err of those that stay against worth + err of those that do not; sums past fp32's range have no order
             const float least = -warp_max(stays && worth > V(kNone) ? err - (float)worth : kNone);
             const float most = warp_max(!stays && g < a.n_group && worth > V(kNone) ? (float)worth + err : kNone);
-            if (!(least > most) && most > kNone) sure = false;
+            if ((!(least > most) && most > kNone) || __any_sync(0xffffffffu, one > V(kNone) && isinf((float)worth))) sure = false;
         }
         if (g < a.n_group && !stays)
             for (int i = lane & (parts - 1); i < a.size; i += parts) key[g * a.size + i] = kNone;
@@ -181,7 +182,7 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, const float* x, V* ke
     id = -1;
     V last = 0;
     int last_id = -1;
-    for (int j = 0; j < a.k + (sizeof(V) == 4); ++j) {
+    for (int j = 0; j < a.k; ++j) {
         V best = kNone;
         int at = 0x7FFFFFFF;
         for (int e = lane; e < a.E; e += 32)
@@ -197,11 +198,19 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, const float* x, V* ke
             const float b0 = a.bias ? a.bias[last_id] : 0.f, b1 = a.bias ? a.bias[at] : 0.f;
             if (!(x[last_id] == x[at] && b0 == b1) && too_near(a, last, best, largest)) sure = false;
         }
-        if (lane == j && j < a.k) id = at;
+        if (lane == j) id = at;
         last = best;
         last_id = at;
         if (lane == (at & 31)) key[at] = kNone;
         __syncwarp();
+    }
+    if (sizeof(V) == 4 && !a.by_logit && last_id >= 0) {
+        // none of the others may belong before the last: not the next one alone, which may be equal to it
+        const float x0 = x[last_id], b0 = a.bias ? a.bias[last_id] : 0.f;
+        bool near = false;
+        for (int e = lane; e < a.E; e += 32)
+            near |= key[e] > V(kNone) && !(x[e] == x0 && (a.bias ? a.bias[e] : 0.f) == b0) && too_near(a, last, key[e], largest);
+        if (__any_sync(0xffffffffu, near)) sure = false;
     }
     return sure;
 }
@@ -423,11 +432,11 @@ __device__ __forceinline__ Picked pick(const RouteArgs& a, const float (&x)[kEac
         const bool stays = g < a.n_group && before < a.topk_group;
         const unsigned kept = __ballot_sync(0xffffffffu, stays);
         if (!kByLogit) {
-            // the magnitudes of a sum's terms bound its own rounding
+            // the magnitudes of a sum's terms bound its own rounding; past fp32's range they have no order
             const float err = score_error(a, largest) * a.group_best + 0x1p-22f * ((one > kNone ? fabsf(one) : 0.f) + (two > kNone ? fabsf(two) : 0.f));
             const float least = -warp_max(stays && worth > kNone ? err - worth : kNone);
             const float most = warp_max(!stays && g < a.n_group && worth > kNone ? worth + err : kNone);
-            if (!(least > most) && most > kNone) return kUnsure;
+            if ((!(least > most) && most > kNone) || __any_sync(0xffffffffu, one > kNone && isinf(worth))) return kUnsure;
         }
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
@@ -479,10 +488,12 @@ __device__ __forceinline__ Picked pick(const RouteArgs& a, const float (&x)[kEac
     expert = key_expert(mine);
     logit = kByLogit ? key_choice(mine) : ranked.x[32 + lane];
     if (!kByLogit) {
-        const float key1 = key_choice(mine), key0 = __shfl_up_sync(0xffffffffu, key1, 1), x0 = __shfl_up_sync(0xffffffffu, logit, 1);
-        const int e0 = __shfl_up_sync(0xffffffffu, expert, 1);
+        // each of the first k against the one before it, the others against the k-th (the next one may be equal to it)
+        const int before = lane < a.k ? max(lane - 1, 0) : a.k - 1;
+        const float key1 = key_choice(mine), key0 = __shfl_sync(0xffffffffu, key1, before), x0 = __shfl_sync(0xffffffffu, logit, before);
+        const int e0 = __shfl_sync(0xffffffffu, expert, before);
         bool near = false;
-        if (lane > 0 && lane <= a.k && expert >= 0) {
+        if (lane > 0 && expert >= 0) {
             const float b0 = a.bias ? a.bias[e0] : 0.f, b1 = a.bias ? a.bias[expert] : 0.f;
             near = !(x0 == logit && b0 == b1) && too_near(a, key0, key1, largest);
         }

@@ -148,6 +148,66 @@ def test_a_large_score_passes_between_two_small_ones(ft, score, E):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [64, 544])
+def test_groups_worth_more_than_fp32_holds(ft, score, E):
+    """Biases of the type's lowest value (a mask), two of which have a sum in 64 bits only: such a group comes before one without
+    experts, and one of two lesser values before it."""
+    groups = 4 if E == 64 else 32
+    size = E // groups
+    rng = np.random.default_rng(E)
+    x = rng.standard_normal((6, E)).astype(np.float32)
+    x[:, 4 * size:] = np.nan                                       # only the first four groups have experts
+    x[:3, :size] = np.nan                                          # in these rows without the first
+    bias = rng.standard_normal(E).astype(np.float32)
+    bias[size:2 * size] = np.finfo(np.float32).min
+    bias[2 * size:3 * size] = -3e38
+    t = torch.from_numpy(x).cuda()
+    for topk_group in (1, 2, 3, 4):
+        kw = dict(score=score, bias=bias, n_group=groups, topk_group=topk_group, group_best=2, renormalise=False)
+        check(t, *run(ft, t, 32, **kw), 32, **kw)
+    most = np.finfo(np.float32).max
+    bias[size:2 * size], bias[2 * size:3 * size] = most, 3e38
+    for topk_group in (1, 2):
+        kw = dict(score=score, bias=bias, n_group=groups, topk_group=topk_group, group_best=2, renormalise=False)
+        check(t, *run(ft, t, 32, **kw), 32, **kw)
+
+
+@pytest.mark.parametrize("E", [40, 256, 640])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_equal_logits_around_the_last_place(ft, E, dtype):
+    """The k-th, the next and more are equal, and behind them stand larger ones that fp32 does not tell from them."""
+    x = torch.linspace(-3, 1, E, dtype=torch.float32).repeat(2, 1)
+    x[0, :10], x[0, E - 1], x[0, E - 5] = 20.0, 25.0, 22.0        # a sigmoid of 1 in fp32
+    x[1, E - 20:E - 5], x[1, E - 1], x[1, E - 3] = 18.0, 18.5, 19.0
+    t = x.to(dtype).cuda()
+    kw = dict(score="sigmoid", bias=np.zeros(E, np.float32))
+    for k in (1, 3, 4, 8):
+        check(t, *run(ft, t, k, **kw), k, **kw)
+    kw = dict(score="softmax", bias=np.full(E, 1e7, np.float32))  # any score is lost in the sum
+    for k in (1, 3, 4, 8):
+        check(t, *run(ft, t, k, **kw), k, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [96, 640])
+def test_scores_at_the_end_of_64_bits(ft, score, E):
+    """Scores of e^-690 to e^-709 (and, softmax, to e^-740, which numbers of 64 bits below the normal ones hold) are in order; below
+    e^-746 they are all 0 and the lower index comes first."""
+    rng = np.random.default_rng(E)
+    last = -740.0 if score == "softmax" else -709.0
+    x = np.full((4, E), -800.0, np.float32)
+    for row in x:
+        at = rng.permutation(E - 1)[:9]
+        row[at] = np.linspace(-690.0, last, 9)
+    x[:, E - 1] = 0.0                                              # the largest
+    x[3, :] = np.where(np.arange(E) < E - 1, -760.0 - rng.permutation(E), 0.0)
+    bias = np.zeros(E, np.float32)
+    t = torch.from_numpy(x).cuda()
+    kw = dict(score=score, bias=bias, renormalise=False)
+    check(t, *run(ft, t, 12, **kw), 12, **kw)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_what_is_masked(ft, score, dtype):
     inf, nan, low = float("inf"), float("nan"), torch.finfo(dtype).min
