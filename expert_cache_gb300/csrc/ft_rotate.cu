@@ -261,6 +261,12 @@ __device__ __forceinline__ uint32_t turned(Pair x, Pair n, Pair y, Pair m, Pair 
     return pack_bf16(add2(o, from2(ol, fma2(h, rl, mul2(l, rh)))));
 }
 
+// x c + y s in 64 bits, for a head of which a norm leaves nothing but 0, infinities and NaN (turns: 0 times an infinity is none).
+__device__ __forceinline__ uint32_t turned_plainly(Pair x, Pair y, Pair c, Pair s, bool turns) {
+    const float2 xx = halves(x), yy = turns ? halves(y) : make_float2(0.f, 0.f), cc = halves(c), ss = halves(s);
+    return pack_bf16(pair((float)((double)xx.x * cc.x + (double)yy.x * ss.x), (float)((double)xx.y * cc.y + (double)yy.y * ss.y)));
+}
+
 // Key heads head .. end - 1 of a token.
 template <int D, int kFormat, bool kInter>
 __device__ __forceinline__ void turn_keys(const RotateArgs& a, const Lane<D, kInter>& p, Heads& heads, const Pair (&c)[8], const Pair (&s)[8],
@@ -271,7 +277,7 @@ __device__ __forceinline__ void turn_keys(const RotateArgs& a, const Lane<D, kIn
     for (; head < end; ++head) {
         uint32_t k[8];
         heads.next(p, k);
-        // an infinity or a NaN has no second part
+        // an infinity or a NaN has no second part, nor has what a turn takes past fp32's range
         __nv_bfloat162 most = __habs2(*reinterpret_cast<__nv_bfloat162*>(&k[0]));
 #pragma unroll
         for (int j = 1; j < 8; ++j) most = __hmax2_nan(most, __habs2(*reinterpret_cast<__nv_bfloat162*>(&k[j])));
@@ -282,7 +288,7 @@ __device__ __forceinline__ void turn_keys(const RotateArgs& a, const Lane<D, kIn
             if (r.h == 0.f) times_zero(k);
         }
         const Pair rh = pair(r.h, r.h), rl = pair(r.l, r.l);
-        const bool numbers = mm.x < INFINITY && mm.y < INFINITY;
+        const bool numbers = mm.x < 0x1p120f && mm.y < 0x1p120f;
         // word j and, unless its two dims are partners, word j + 4
 #pragma unroll
         for (int j = 0; j < (kInter ? 8 : 4); ++j) {
@@ -302,9 +308,8 @@ __device__ __forceinline__ void turn_keys(const RotateArgs& a, const Lane<D, kIn
                 k[j] = turned(x, n, y, m, c[j], s[j], nc[j], ns[j], rh, rl);
                 if (!kInter) k[j ^ 4] = turned(y, m, x, n, c[j], ns[j], nc[j], s[j], rh, rl);
             } else {
-                const Pair none = 0;
-                k[j] = pack_bf16(mul2(fma2(x, c[j], mul2(p.turns ? y : none, s[j])), rh));
-                if (!kInter) k[j ^ 4] = pack_bf16(mul2(fma2(y, c[j], mul2(p.turns ? x : none, neg2(s[j]))), rh));
+                k[j] = turned_plainly(x, y, c[j], s[j], p.turns);
+                if (!kInter) k[j ^ 4] = turned_plainly(y, x, c[j], neg2(s[j]), p.turns);
             }
         }
         if (slot >= 0 && a.k_out) p.store(a.k_out + (size_t)tok * a.k_out_stride + head * D, k);

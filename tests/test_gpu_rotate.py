@@ -204,6 +204,23 @@ def test_values_that_are_hard(ft, D, fmt):
         assert torch.isfinite(q[0, 1]).sum() == D - 1 and torch.isfinite(k[0, 1]).sum() == D - 1
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,rope,fmt", [(64, 64, "fp8"), (128, 128, "nvfp4"), (256, 128, "nvfp4")])
+def test_keys_at_the_end_of_the_range(ft, D, rope, fmt, inter):
+    """Keys without a norm whose turn may leave fp32's range: an infinity then, stored as the largest value, not a NaN, and numbers
+    where the formula gives one although its terms are larger."""
+    c = Case(ft, fmt, D, 3, 3, 40, rope, norm=False, inter=inter)
+    c.table *= 1.375                                               # as a mscale does, in numbers that fp32 holds
+    rng = np.random.default_rng(D)
+    x = rng.choice([-1.0, 1.0], (40, 3, D)) * np.exp2(rng.uniform(110, 127.99, (40, 3, D)))
+    x[:10, 1] *= 2.0 ** -8                                         # these do not leave it
+    x[10:20, 2] = np.where(rng.random((10, D)) < 0.9, 3.3e38, x[10:20, 2])
+    c.k.copy_(torch.from_numpy(x.reshape(40, 3 * D).astype(np.float32)).to(torch.bfloat16))
+    ok = c.want()[2]
+    assert torch.isinf(ok).any() and not torch.isnan(ok).any()
+    c.check(*c.run())
+
+
 def test_places_that_are_none(ft):
     """Slots outside the cache, positions outside the table: skipped, reported, the rest served."""
     c = Case(ft, "nvfp4", 128, 4, 2, 12, 64)
