@@ -4,19 +4,19 @@
 // give log sum = log S and entropy = log S - D / S.  A thread's ref is a maximum of a sample of the row, so that no
 // sum has to be rescaled unless a logit lies e^69 above it; the row's own maximum is taken at the end.
 //
-// The k largest come out of the same pass.  From the sample (the first 8 vectors of every thread) the k-th largest of 16 to
-// 64 logits is a lower bound of the row's k-th; only what reaches it is kept and put on a list in shared memory (4 to 8 k of
+// The k largest come out of the same pass.  From the sample (the first 8 vectors of every thread) the k-th largest of some 2 k
+// logits is a lower bound of the row's k-th; only what reaches it is kept and put on a list in shared memory (4 to 8 k of
 // 100,000), which is ranked at the end.  Where more reach it than the list holds, its own k-th largest is the next bound and
 // the part is read again; where that does not help (equal logits by the thousand, rising ones), k searches find them.  Which ones
 // these are does not depend on any order: value, then index.
 //
-// 2048 rows of 131,072 bf16: 95 us, 5.6 TB/s, 0.84 of the copy rate; without the k largest 81 to 84 us, the copy rate.  The k
-// largest cost the barriers of the sample and of the list, during which a CTA's SM has only the other one's loads under way (2
-// us a row of 14).  One row: 5.1 us in 8 CTAs, launch and barriers.  On the way: vectors through registers, 4 or 8 under way,
-// 151 to 193 us; through thread-owned shared memory 114 us; neighbouring vectors instead of four stretches of the row 103 us; the
-// list by warps instead of at once 101 us, and ranks by several threads per entry (one row 7.3 -> 5.5 us), of few warps 95 us.  CTAs of 256 threads
-// (107 us) or 1024 (151 us), rows in a loop with the next one's first vectors loaded ahead (127 us), and the bound worked out by every
-// warp for itself (107 us) were slower.
+// 2048 rows of 131,072 bf16: 88.7 us, 6.05 TB/s, 0.91 of the copy rate; without the k largest 80 us, the copy rate.  The k
+// largest cost the barriers of the sample and of the list, during which an SM has only its other CTAs' loads under way.  One
+// row: 5.1 us in 8 CTAs, launch and barriers.  On the way: vectors through registers, 4 or 8 under way, 151 to 193 us; through
+// thread-owned shared memory 114 us; neighbouring vectors instead of four stretches of the row 103 us; the list by warps instead of at
+// once 101 us; ranks by several threads per entry (one row 7.3 -> 5.5 us), of few warps 95 us; three CTAs of 384 threads an SM
+// instead of two of 512 (see launch) 88.7 us.  Rows in a loop with the next one's first vectors loaded ahead (127 us instead of 101),
+// and the bound worked out by every warp for itself (107 us) were slower.
 #include <atomic>
 #include <cfloat>
 #include <cmath>
@@ -28,14 +28,19 @@ namespace ft {
 
 namespace {
 
-constexpr int kLogThreads = 512, kLogWarps = kLogThreads / 32, kLogPerSm = 2;
 constexpr int kVectors = 4;            // vectors of a thread in a round
 constexpr int kRounds = 2;             // rounds under way
-constexpr int kSlot = kLogThreads * 16, kRing = kRounds * kVectors * kSlot;
 constexpr int kListed = 1024;          // entries of a CTA's list
-constexpr int kHits = 64;              // vectors that a warp keeps for the list
 constexpr int kMaxCtas = 8;            // of a row
 constexpr float kNone = -INFINITY;
+
+// What follows from the number of a CTA's threads.
+template <int T>
+struct Cta {
+    static constexpr int kWarps = T / 32, kPerSm = 1152 / T;
+    static constexpr int kSlot = T * 16, kRing = kRounds * kVectors * kSlot;
+    static constexpr int kHits = T == 384 ? 48 : 64;           // vectors that a warp keeps for the list
+};
 
 // 16 bytes of logits.  Max: the largest so far, NaN aside, in the form that costs least; Floor: where logits are cut off.
 template <typename L>
@@ -134,14 +139,16 @@ __device__ __forceinline__ Key key_of(float x, int i) { return (Key)ordered(fmin
 __device__ __forceinline__ float key_logit(Key k) { return k >> 32 ? unordered((unsigned)(k >> 32)) : kNone; }
 __device__ __forceinline__ int key_index(Key k) { return k >> 32 ? (int)~(unsigned)k : -1; }
 
+template <int T>
 struct LogShared {
+    static constexpr int kWarps = Cta<T>::kWarps, kHits = Cta<T>::kHits;
     alignas(16) Key list[kListed];
     alignas(16) Key top[kMaxK];                   // this CTA's k best
     alignas(16) Key tops[kMaxCtas * kMaxK];       // the row's CTAs' (in its first one)
-    alignas(16) uint4 hit[kLogWarps][kHits];      // the warps' vectors that reach the bound, and where they stand
-    int hit_at[kLogWarps][kHits];
-    float few[kLogWarps * 4];                     // the sample's largest
-    float red[3][kLogWarps];                      // the warps' largest, S and D
+    alignas(16) uint4 hit[kWarps][kHits];      // the warps' vectors that reach the bound, and where they stand
+    int hit_at[kWarps][kHits];
+    float few[2 * kMaxK + kWarps];                // the sample's largest
+    float red[3][kWarps];                         // the warps' largest, S and D
     float sums[kMaxCtas][4];                      // the row's CTAs' largest, S and D (in its first one)
     Key one;
     int count;
@@ -229,8 +236,8 @@ __device__ __noinline__ Sums<L> add_far(Sums<L> a, Vec<L> v, float bound, float 
 }
 
 // Puts what reaches the bound on the list.
-template <typename L>
-__device__ __forceinline__ void put_on_list(LogShared& sm, const Vec<L>& v, int index, float bound) {
+template <typename L, int T>
+__device__ __forceinline__ void put_on_list(LogShared<T>& sm, const Vec<L>& v, int index, float bound) {
     float x[Vec<L>::kN];
     v.get(x);
 #pragma unroll
@@ -245,8 +252,8 @@ __device__ __forceinline__ void put_on_list(LogShared& sm, const Vec<L>& v, int 
 // Adds N vectors to a thread's sums; a whole warp calls it.  Vectors for the list are kept (hits of them so far) and looked
 // at when the warp is through: the atomic operations of the list at once cost a row of 131,072 logits a microsecond more.
 // index(j): where vector j stands.
-template <typename L, bool kTop, int N, typename I>
-__device__ __forceinline__ void take(LogShared& sm, Sums<L>& a, int& hits, const Vec<L> (&v)[N], I index, float bound, float c) {
+template <typename L, bool kTop, int T, int N, typename I>
+__device__ __forceinline__ void take(LogShared<T>& sm, Sums<L>& a, int& hits, const Vec<L> (&v)[N], I index, float bound, float c) {
     typename Vec<L>::Max reach = v[0].max();
 #pragma unroll
     for (int j = 1; j < N; ++j) reach = Vec<L>::larger(reach, v[j].max());
@@ -262,7 +269,7 @@ __device__ __forceinline__ void take(LogShared& sm, Sums<L>& a, int& hits, const
                 const unsigned kept = __ballot_sync(0xffffffffu, keep);
                 if (!kept) continue;
                 const int at = hits + __popc(kept & ((1u << (threadIdx.x & 31)) - 1));
-                if (keep && at < kHits) {
+                if (keep && at < Cta<T>::kHits) {
                     v[j].to_shared((uint32_t)__cvta_generic_to_shared(&sm.hit[threadIdx.x >> 5][at]));
                     sm.hit_at[threadIdx.x >> 5][at] = index(j);
                 }
@@ -281,7 +288,7 @@ __device__ __forceinline__ void take(LogShared& sm, Sums<L>& a, int& hits, const
 
 // A CTA's part of a row: the row's vectors from lo on, `steps` for every thread and one more for the first `more`; for the
 // row's first CTA also the elements before and behind its vectors.
-template <typename L>
+template <typename L, int T>
 struct Part {
     const L* row;
     int head, lo, steps, more, V, rest;
@@ -291,11 +298,11 @@ struct Part {
         const int n = (V - head) / kN;
         lo = (int)((unsigned)n * rank >> shift);                    // n is at most 2^28
         const int own = (int)((unsigned)n * (rank + 1) >> shift) - lo;
-        steps = own / kLogThreads;
-        more = own % kLogThreads;
+        steps = own / T;
+        more = own % T;
         rest = rank == 0 ? V - n * kN : 0;
     }
-    __device__ __forceinline__ int index(int it) const { return head + (lo + it * kLogThreads + (int)threadIdx.x) * Vec<L>::kN; }
+    __device__ __forceinline__ int index(int it) const { return head + (lo + it * T + (int)threadIdx.x) * Vec<L>::kN; }
     __device__ __forceinline__ void load(Vec<L>& v, int it) const { v.load(row + index(it)); }
     // Those that not every thread has (no logits for the others).
     __device__ __forceinline__ void load_more(Vec<L>& v) const {
@@ -324,12 +331,13 @@ struct Part {
 
 // A thread's vectors on their way through its own slots of shared memory, kRounds rounds of kVectors; the last round may
 // have fewer.  Nobody else reads a thread's slots, so its own wait for its copies is all there is to wait for.
-template <typename L>
+template <typename L, int T>
 struct Ring {
-    const Part<L>& p;
+    static constexpr int kSlot = Cta<T>::kSlot;
+    const Part<L, T>& p;
     uint32_t slots;
     int full, rounds;
-    __device__ __forceinline__ Ring(const Part<L>& part, const void* smem) : p(part) {
+    __device__ __forceinline__ Ring(const Part<L, T>& part, const void* smem) : p(part) {
         slots = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
         full = p.steps / kVectors;
         rounds = full + (p.steps % kVectors || p.more ? 1 : 0);
@@ -339,7 +347,7 @@ struct Ring {
             const L* from = p.row + p.index(round * kVectors);
 #pragma unroll
             for (int j = 0; j < kVectors; ++j)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slots + at + j * kSlot), "l"(from + j * kLogThreads * Vec<L>::kN) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(slots + at + j * kSlot), "l"(from + j * T * Vec<L>::kN) : "memory");
         } else if (round < rounds) {
 #pragma unroll
             for (int j = 0; j < kVectors; ++j) {
@@ -369,8 +377,8 @@ struct Ring {
 };
 
 // Puts everything that reaches the bound on the list.
-template <typename L>
-__device__ void collect(LogShared& sm, const Part<L>& p, float bound) {
+template <typename L, int T>
+__device__ void collect(LogShared<T>& sm, const Part<L, T>& p, float bound) {
     p.each([&](const Vec<L>& v, int index) { put_on_list(sm, v, index, bound); });
 }
 
@@ -386,10 +394,11 @@ __device__ __forceinline__ int count_before(int n, int parts, F before) {
 
 // The k largest of n different keys, in order, to out; where there are fewer, numbers for none that no other CTA of the row has.
 // Few keys by few warps: the others have nothing to wait for but a barrier.
+template <int T>
 __device__ __forceinline__ void rank_list(const Key* list, int n, int k, int rank, Key* out) {
-    for (int j = n + threadIdx.x; j < k; j += kLogThreads) out[j] = 1 + rank * kMaxK + j;
+    for (int j = n + threadIdx.x; j < k; j += T) out[j] = 1 + rank * kMaxK + j;
     const int shift = n <= 64 ? 3 : n <= 128 ? 2 : n <= 256 ? 1 : 0;              // 1 << shift threads for an entry
-    for (int first = threadIdx.x & ~31; first < n << shift; first += kLogThreads) {
+    for (int first = threadIdx.x & ~31; first < n << shift; first += T) {
         const int e = (first + (int)(threadIdx.x & 31)) >> shift;
         const Key mine = e < n ? list[e] : 0;
         const int before = count_before(n, 1 << shift, [&](int i) { return list[i] > mine; });
@@ -398,8 +407,8 @@ __device__ __forceinline__ void rank_list(const Key* list, int n, int k, int ran
 }
 
 // The k largest by k searches.
-template <typename L>
-__device__ void search(LogShared& sm, const Part<L>& p, int k, int rank, Key* out) {
+template <typename L, int T>
+__device__ void search(LogShared<T>& sm, const Part<L, T>& p, int k, int rank, Key* out) {
     Key last = ~0ULL;
     for (int j = 0; j < k; ++j) {
         Key b = 0;
@@ -418,7 +427,7 @@ __device__ void search(LogShared& sm, const Part<L>& p, int k, int rank, Key* ou
         if ((threadIdx.x & 31) == 0) sm.list[threadIdx.x >> 5] = b;
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int w = 1; w < kLogWarps; ++w) b = max(b, sm.list[w]);
+            for (int w = 1; w < Cta<T>::kWarps; ++w) b = max(b, sm.list[w]);
             sm.one = b;
             out[j] = b ? b : 1 + rank * kMaxK + j;
         }
@@ -443,17 +452,18 @@ __device__ __forceinline__ float join(float own, float2 part, float c, float2& a
     return m;
 }
 
-template <typename L, bool kTop>
-__global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const ft_logprob c, int shift) {
-    __shared__ LogShared sm;
+template <typename L, bool kTop, int T>
+__global__ void __launch_bounds__(T, Cta<T>::kPerSm) logprobs_kernel(const ft_logprob c, int shift) {
+    constexpr int kWarps = Cta<T>::kWarps, kSlot = Cta<T>::kSlot, kHits = Cta<T>::kHits;
+    __shared__ LogShared<T> sm;
     extern __shared__ __align__(16) uint8_t log_ring[];
     pdl_wait_and_release();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ctas = 1 << shift, rank = blockIdx.x & (ctas - 1);
     if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");      // waited for before the first remote store
     const float c2 = fminf(c.scale * 1.4426950408889634f, FLT_MAX);
     const long long r = blockIdx.x >> shift;
-    const Part<L> p(static_cast<const L*>(c.logits) + r * c.stride, c.V, rank, shift);
-    const Ring<L> ring(p, log_ring);
+    const Part<L, T> p(static_cast<const L*>(c.logits) + r * c.stride, c.V, rank, shift);
+    const Ring<L, T> ring(p, log_ring);
     ring.start();
     Vec<L> rest[1];
     p.load_rest(rest[0]);
@@ -476,7 +486,7 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
     float most = Vec<L>::value(largest);
     most = most == most ? fminf(most, FLT_MAX) : kNone;
     unsigned key = ordered(most);
-    const int each = !kTop || c.k <= 8 ? 1 : c.k <= 16 ? 2 : 4;  // of a warp: kLogWarps of them hold k, and about the sample's k largest
+    const int each = kTop ? (2 * c.k + kWarps - 1) / kWarps : 1;  // of a warp: together at least 2 k, which hold about the sample's k largest
     for (int i = 0;;) {
         const unsigned u = __reduce_max_sync(0xffffffffu, key);
         if (lane == 0) sm.few[warp * each + i] = unordered(u);
@@ -485,12 +495,12 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
     }
     if (threadIdx.x == 0) sm.count = 0;
     __syncthreads();
-    if ((int)(threadIdx.x & ~31) < 4 * kLogWarps * each) {        // four threads for each of them
-        const int n = kLogWarps * each, mine_at = threadIdx.x >> 2;
-        const float mine = sm.few[mine_at];
+    if ((int)(threadIdx.x & ~31) < 4 * kWarps * each) {           // four threads for each of them
+        const int n = kWarps * each, mine_at = threadIdx.x >> 2;
+        const float mine = mine_at < n ? sm.few[mine_at] : kNone;
         const int before = count_before(n, 4, [&](int i) { return sm.few[i] > mine || (sm.few[i] == mine && i < mine_at); });
-        if (before == 0) sm.ref = mine;
-        if (before == (kTop ? c.k - 1 : 0)) sm.bound = mine;
+        if (mine_at < n && before == 0) sm.ref = mine;
+        if (mine_at < n && before == (kTop ? c.k - 1 : 0)) sm.bound = mine;
     }
     __syncthreads();
     const float bound = sm.bound;
@@ -499,16 +509,16 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
     a.top = sm.ref;
     a.against(sm.ref, bound, c2, 100.f * inverse_fast(c2));
     int hits = 0;
-    if (p.rest) take<L, kTop, 1>(sm, a, hits, rest, [&](int) { return p.rest_index(); }, bound, c2);
+    if (p.rest) take<L, kTop, T, 1>(sm, a, hits, rest, [&](int) { return p.rest_index(); }, bound, c2);
     uint32_t slot = 0;
     for (int i = 0; i < ring.rounds; ++i) {
         ring.wait();
         Vec<L> v[kVectors];
 #pragma unroll
         for (int j = 0; j < kVectors; ++j) v[j] = ring.get(slot, j);
-        take<L, kTop, kVectors>(sm, a, hits, v, [&](int j) { return p.index(i * kVectors + j); }, bound, c2);
+        take<L, kTop, T, kVectors>(sm, a, hits, v, [&](int j) { return p.index(i * kVectors + j); }, bound, c2);
         ring.issue(i + kRounds, slot);
-        slot = slot == kRing - kVectors * kSlot ? 0 : slot + kVectors * kSlot;
+        slot = slot == Cta<T>::kRing - kVectors * kSlot ? 0 : slot + kVectors * kSlot;
     }
     if (kTop) {
         __syncwarp();
@@ -544,18 +554,18 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
                 n = sm.count;
                 if (n <= kListed) break;
                 // the list's k-th largest bounds the row's
-                rank_list(sm.list, kListed, c.k, rank, sm.top);
+                rank_list<T>(sm.list, kListed, c.k, rank, sm.top);
                 __syncthreads();
                 next = key_logit(sm.top[c.k - 1]);
             }
             __syncthreads();
         }
         if (n > kListed) search(sm, p, c.k, rank, sm.top);
-        else rank_list(sm.list, n, c.k, rank, sm.top);
+        else rank_list<T>(sm.list, n, c.k, rank, sm.top);
         __syncthreads();
     }
     if (warp == 0) {
-        m = join(lane < kLogWarps ? sm.red[0][lane] : kNone, lane < kLogWarps ? make_float2(sm.red[1][lane], sm.red[2][lane]) : make_float2(0.f, 0.f),
+        m = join(lane < kWarps ? sm.red[0][lane] : kNone, lane < kWarps ? make_float2(sm.red[1][lane], sm.red[2][lane]) : make_float2(0.f, 0.f),
                  c2, sums);
         if (ctas > 1) {
             // what each CTA found, to the first one
@@ -580,7 +590,7 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
         asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
         if (rank) return;
         if (kTop) {
-            rank_list(sm.tops, ctas * c.k, c.k, 0, sm.top);
+            rank_list<T>(sm.tops, ctas * c.k, c.k, 0, sm.top);
             __syncthreads();
         }
         if (warp == 0)
@@ -604,21 +614,21 @@ __global__ void __launch_bounds__(kLogThreads, kLogPerSm) logprobs_kernel(const 
 
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
-template <typename L, bool kTop>
+template <typename L, bool kTop, int T>
 cudaError_t launch(const ft_logprob& c, int shift, cudaStream_t s) {
     static std::atomic<bool> done[kMaxDevices];                  // the kernel's attribute is set on this device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices || !done[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(logprobs_kernel<L, kTop>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+        e = cudaFuncSetAttribute(logprobs_kernel<L, kTop, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cta<T>::kRing);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDevices) done[dev].store(true, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)c.n << shift);
-    cfg.blockDim = dim3(kLogThreads);
-    cfg.dynamicSmemBytes = kRing;
+    cfg.blockDim = dim3(T);
+    cfg.dynamicSmemBytes = Cta<T>::kRing;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -628,7 +638,24 @@ cudaError_t launch(const ft_logprob& c, int shift, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<L, kTop>, c, shift);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<L, kTop, T>, c, shift);
+}
+
+// Threads of a CTA: 512 (2 CTAs per SM), 384 (3) or 256 (4).  More CTAs overlap more of the rows' barriers, but their samples are
+// smaller and let more logits, k V / sample, through to be ranked; and few rows leave few CTAs.  us with 512, 384, 256 threads, bf16:
+//   2048 rows of 131,072: k = 1 91 83.5 85, k = 5 95.5 89 89, k = 20 110 106 114, k = 32 121 125 168
+//   2048 rows of 50,304: k = 5 60.5 50 45, k = 32 75 67 65;  of 8192: k = 5 35 25.5 20
+//   304 rows of 131,072: 17.1 22.8 19.4;  456: 25.5 24.4 28.8
+template <typename L, bool kTop>
+cudaError_t launch(const ft_logprob& c, int shift, cudaStream_t s) {
+    const long long vectors = c.V / Vec<L>::kN, listed = vectors * c.k;
+    if (c.n <= 2 * sm_count() || listed > 450000) return launch<L, kTop, 512>(c, shift, s);
+    if (vectors > 14000 || listed > 200000) return launch<L, kTop, 384>(c, shift, s);
+    return launch<L, kTop, 256>(c, shift, s);
+}
+template <typename L>
+cudaError_t launch(const ft_logprob& c, int shift, cudaStream_t s) {
+    return c.k ? launch<L, true>(c, shift, s) : launch<L, false>(c, shift, s);
 }
 
 }  // namespace
@@ -651,9 +678,8 @@ extern "C" ft_status ft_logprobs(const ft_logprob* call, void* stream) {
     // 20: 2 CTAs 11.0 us, 3 12.2 us, 4, of which some share an SM, 12.3 us; 24 rows: 4 8.5 us, 6 10.5 us)
     int shift = 0;
     const long long vectors = (long long)c.V / (c.dtype == FT_DTYPE_BF16 ? 8 : 4);
-    while (1 << shift < kMaxCtas && (2LL << shift) * c.n <= sm_count() && vectors > (long long)kLogThreads << shift) ++shift;
+    while (1 << shift < kMaxCtas && (2LL << shift) * c.n <= sm_count() && vectors > 512LL << shift) ++shift;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = c.dtype == FT_DTYPE_BF16 ? (c.k ? launch<__nv_bfloat16, true>(c, shift, s) : launch<__nv_bfloat16, false>(c, shift, s))
-                                                   : (c.k ? launch<float, true>(c, shift, s) : launch<float, false>(c, shift, s));
+    const cudaError_t e = c.dtype == FT_DTYPE_BF16 ? launch<__nv_bfloat16>(c, shift, s) : launch<float>(c, shift, s);
     return e == cudaSuccess ? FT_OK : FT_ERR_CUDA;
 }

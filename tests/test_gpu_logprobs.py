@@ -163,6 +163,22 @@ def test_long_rising_rows(ft, dtype):
         check(x, t, run(ft, x, t, k), k)
 
 
+@pytest.mark.parametrize("V,dtype", [(33, torch.bfloat16), (4099, torch.float32), (20000, torch.bfloat16), (50305, torch.float32), (57001, torch.float32),
+                                     (112503, torch.bfloat16)])
+def test_more_rows_than_the_gpu_holds(ft, V, dtype):
+    """Hard rows among many others, k on both sides of what decides how many threads a row gets."""
+    n = 2 * torch.cuda.get_device_properties(0).multi_processor_count + 17
+    x = logits(V, n, V, dtype, pad=3)
+    i = torch.arange(V, device="cuda", dtype=torch.float32)
+    x[0], x[1], x[2] = 1.5, (i / V * 40).to(dtype), (-i / V * 40).to(dtype)
+    x[3], x[4] = torch.where(i < V - 40, 0.0, 5.0).to(dtype), float("nan")
+    x[5, 1:], x[6, ::2], x[7] = float("-inf"), float("nan"), torch.finfo(dtype).min
+    x[8, V // 2], x[n - 1, V - 1] = float("inf"), 50.0
+    t = tokens_of(2, n, V)
+    for k in (0, 1, 4, 16, 32):
+        check(x, t, run(ft, x, t, k), k, rows=[0, 1, 2, 3, 4, 5, 6, 7, 8, 9, n // 2, n - 2, n - 1])
+
+
 def test_temperatures_and_tokens(ft):
     x = logits(3, 6, 40000)
     t = tokens_of(0, 6, 40000)
