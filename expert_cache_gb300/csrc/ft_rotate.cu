@@ -9,11 +9,12 @@
 // unevaluated sums of two fp32 (products split by a fused multiply-add, sums by Knuth's two-sum) down to the rounding.
 //
 // 8192 tokens of 32 query and 8 + 8 key and value heads of 128, NVFP4, all normalised and turned: 41 us for 194 MB, 0.7 of the copy
-// rate (reading them back takes another 10 us).  Bound by instructions, issued 63 % of the time by 20 warps per SM: some 190 for
+// rate (reading them back takes another 10 us).  Bound by instructions, issued 60 % of the time by up to 20 warps per SM: some 190 for
 // a query's 16 dims of 32 lanes, 1000 for a key's and a value's together (of which the two parts take 400, quantising 260).  A token
-// alone: 4.2 us with reading back, two launches.  On the way: a lane per scale block with its partners in another lane, 16 shuffles
+// alone: 4.1 us with reading back, two launches.  On the way: a lane per scale block with its partners in another lane, 16 shuffles
 // a head, 94 us with reading back; partners in the same lane and packed arithmetic 82 us; heads asked for four ahead through
-// shared memory instead of one through registers 56 us; words taken one by one, so that 96 registers are enough for five CTAs 52 us.
+// shared memory instead of one through registers 56 us; words taken one by one, so that 96 registers are enough for 20 warps per SM 52 us; CTAs of one warp, whose
+// place is free as soon as it is through, 50.4 us (of four 50.7; 3001 tokens of 20 + 4 + 4 heads of 64 11.8 us, of four 13.1).
 #include <cmath>
 
 #include "ft_kv_host.cuh"
@@ -24,7 +25,7 @@ namespace ft {
 
 namespace {
 
-constexpr int kRotThreads = 128, kRotPerSm = 5;
+constexpr int kRotThreads = 32, kRotPerSm = 20;
 constexpr int kAhead = 4;              // heads that a lane has under way
 
 struct RotateArgs {
@@ -378,8 +379,8 @@ struct Rotate {
         const long long groups = ((long long)a.n + 32 / (D / 16) - 1) / (32 / (D / 16));
         const int heads = a.hq + 2 * a.kv.hkv;
         // heads of a warp: its start (slot, position, angles, weights) is shared by them (8192 tokens of 32 + 8 + 8 heads of 128, with
-        // reading back: 1 head 95 us, 2 70, 4 61, 8 54, 16 51), but there are to be 32 runs per SM (3001 tokens of 20 + 4 + 4 heads
-        // of 64: 1 head 15.3 us, 2 13.1, 4 13.8, 8 13.9, 16 15.1)
+        // reading back: 1 head 113 us, 2 70, 4 58, 8 53, 16 50), but there are to be 32 runs per SM (3001 tokens of 20 + 4 + 4 heads
+        // of 64: 1 head 15.1 us, 2 11.8, 4 13.6, 8 12.8, 16 13.4)
         const long long want = groups * heads / (32LL * sm_count());
         a.run = want < 1 ? 1 : want > 16 ? 16 : (int)want;
         a.units = (heads + a.run - 1) / a.run;
