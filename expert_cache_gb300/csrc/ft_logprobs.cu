@@ -161,9 +161,10 @@ __device__ __forceinline__ void store_first(const void* p, uint32_t v) {
     asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\tst.shared::cluster.b32 [r], %1;\n\t}" :: "r"(a), "r"(v) : "memory");
 }
 
-// A thread's sums against its ref, in units of log 2: with y = c x - rc, rc = RN(c ref), S = sum 2^y and D = sum 2^y y.  (What
-// rc's rounding moves them by is taken back at the end.)  Logits below floor, whose 2^y is 0, are raised to it, so that y is a
-// number; those from limit on go out of line, as do all where c ref or the floor would be too large (plain).
+// A thread's sums against its ref, in units of log 2: with y = c x - rc, rc = RN(c ref), S = sum 2^y and D = sum 2^y y.  What
+// rc's rounding moves them by is taken back at the end: below 2^26 it is at most 2, so that S keeps its bits and D two fewer (from 2^31 on
+// 2^y could be infinite, or 0 for every logit).  Logits below floor, whose 2^y is 0, are raised to it, so that y is a
+// number; those from limit on go out of line, as do all where c ref or the floor would be too large (plain: x - ref first, then c).
 template <typename L>
 struct Sums {
     typedef typename Vec<L>::Max Max;
@@ -176,8 +177,8 @@ struct Sums {
     // span: some 100 / c, 0 or infinite where that is no normal number.
     __device__ __forceinline__ void against(float to, float bound, float c, float span) {
         ref = to;
-        far = to == kNone ? kNone : to + span;
-        plain = !(fabsf(to) * c < 0x1p60f && span > 0.f && to - 2.f * span > -1e38f);
+        far = to == kNone ? kNone : __fadd_rd(to, span);         // not above it: next to a large ref one step may be worth more than the span
+        plain = !(fabsf(to) * c < 0x1p26f && span > 0.f && to - 2.f * span > -1e38f);
         rc = plain ? 0.f : to * c;
         floor = Vec<L>::limit(to - 2.f * span);
         limit = Vec<L>::limit(plain ? kNone : fminf(bound, far));

@@ -240,3 +240,34 @@ def test_results_do_not_depend_on_the_run_or_the_other_rows(ft):
     a = run(ft, x, t, 9)
     for _ in range(3):
         assert all(torch.equal(p, q) for p, q in zip(a, run(ft, x, t, 9)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,V", [(2, 131072), (200, 20000), (330, 60001)])
+def test_scales_by_decades(ft, n, V, dtype):
+    """Temperatures down to 1e-20: scale times the largest logit through every power of two from 2^16 to 2^70.  (Where it is kept as a
+    rounded product, an offset of at most 2 in the base-2 exponents costs the entropy 2 log 2 of the n roundings of s that are not
+    made: V / 256 counts twice the additions of a term.)"""
+    x, t = logits(n + V, n, V, dtype), tokens_of(V, n, V)
+    t[0] = int(x[0].float().argmax())
+    for e in range(4, 21):
+        for k in (0, 5):
+            check(x, t, run(ft, x, t, k, 10.0 ** e), k, 10.0 ** e, rows=[0, n // 2, n - 1])
+
+
+@pytest.mark.parametrize("k", [0, 4])
+@pytest.mark.parametrize("n,V", [(2, 131072), (200, 60001)])
+def test_neighbours_far_from_zero(ft, n, V, k):
+    """Logits a few steps of fp32 apart around 2^10 to 2^100, a step worth 1/4 to 140: first the lower ones, so that the later ones lie above
+    every thread's reference.  The same bound as in test_scales_by_decades."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    step = torch.randint(0, 4, (n, V), generator=g, device="cuda")
+    step[:, V // 4 * 3:] += 1
+    step[n - 1, V - 1] += 2
+    t = tokens_of(k, n, V)
+    for e in (10, 26, 30, 31, 40, 60, 100):
+        x = (1 + step * 2.0 ** -23) * 2.0 ** e
+        for worth in (0.25, 1.0, 2.0, 5.0, 16.0, 70.0, 100.0, 140.0):
+            scale = worth * 2.0 ** (23 - e)
+            check(x, t, run(ft, x, t, k, scale), k, scale, rows=[0, n - 1])
+            check(-x, t, run(ft, -x, t, k, scale), k, scale, rows=[0, n - 1])
