@@ -164,7 +164,8 @@ __device__ __forceinline__ void store_first(const void* p, uint32_t v) {
 // A thread's sums against its ref, in units of log 2: with y = c x - rc, rc = RN(c ref), S = sum 2^y and D = sum 2^y y.  What
 // rc's rounding moves them by is taken back at the end: below 2^26 it is at most 2, so that S keeps its bits and D two fewer (from 2^31 on
 // 2^y could be infinite, or 0 for every logit).  Logits below floor, whose 2^y is 0, are raised to it, so that y is a
-// number; those from limit on go out of line, as do all where c ref or the floor would be too large (plain: x - ref first, then c).
+// number; those from limit on go out of line, as do all where c ref, the floor or far would be too large (plain: x is cut to the
+// largest number and x - ref comes first).  Since far is a smaller number than the largest elsewhere, an infinity always lies above it.
 template <typename L>
 struct Sums {
     typedef typename Vec<L>::Max Max;
@@ -178,7 +179,7 @@ struct Sums {
     __device__ __forceinline__ void against(float to, float bound, float c, float span) {
         ref = to;
         far = to == kNone ? kNone : __fadd_rd(to, span);         // not above it: next to a large ref one step may be worth more than the span
-        plain = !(fabsf(to) * c < 0x1p26f && span > 0.f && to - 2.f * span > -1e38f);
+        plain = !(fabsf(to) * c < 0x1p26f && span > 0.f && to - 2.f * span > -1e38f && far < FLT_MAX);
         rc = plain ? 0.f : to * c;
         floor = Vec<L>::limit(to - 2.f * span);
         limit = Vec<L>::limit(plain ? kNone : fminf(bound, far));

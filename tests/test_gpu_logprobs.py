@@ -271,3 +271,23 @@ def test_neighbours_far_from_zero(ft, n, V, k):
             scale = worth * 2.0 ** (23 - e)
             check(x, t, run(ft, x, t, k, scale), k, scale, rows=[0, n - 1])
             check(-x, t, run(ft, -x, t, k, scale), k, scale, rows=[0, n - 1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,V", [(9, 131072), (200, 20000), (330, 60001)])
+def test_infinities_at_every_scale(ft, n, V, dtype):
+    """+inf counts as the largest fp32 value, first, last, alone, beside numbers that lie within the exponentials' range of it, and everywhere."""
+    inf, x, t = float("inf"), logits(n + V, n, V, dtype), tokens_of(V, n, V)
+    x[0, 3] = inf
+    x[1, V - 1] = inf
+    x[2, 9], x[2, V - 1] = 2.5e38, inf                            # the span may pass the largest number
+    x[3, 9], x[3, V // 2] = 3.3e38, inf
+    x[4, ::5] = inf
+    x[5] = inf
+    x[6, V // 2:] = inf
+    x[7] = -inf
+    x[7, V - 2] = inf
+    t[0], t[1], t[2], t[3] = 3, V - 1, 9, 9
+    for scale in (1e-36, 6e-37, 5.5e-37, 4e-37, 3e-36, 1e-33, 1e-30, 1e-25, 1e-22, 2e-21, 1e-20, 1e-15, 1e-10, 1e-5, 1.0, 1e5, 1e15, 1e25):
+        for k in (0, 3):
+            check(x, t, run(ft, x, t, k, scale), k, scale, rows=range(9))
