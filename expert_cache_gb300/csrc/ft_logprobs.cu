@@ -155,6 +155,12 @@ struct LogShared {
     float bound, ref;
 };
 
+// (a - b) c + d, for c > 0.  The difference may pass fp32's range where its product does not.
+__device__ __forceinline__ float apart(float a, float b, float c, float d) {
+    const float x = a - b;
+    return fabsf(x) <= FLT_MAX ? fmaf(x, c, d) : fmaf(0.5f * a - 0.5f * b, 2.f * c, d);
+}
+
 // A word to the same place in the shared memory of the cluster's first CTA.
 __device__ __forceinline__ void store_first(const void* p, uint32_t v) {
     const uint32_t a = (uint32_t)__cvta_generic_to_shared(p);
@@ -201,7 +207,7 @@ struct Sums {
         const float sum = a.x + a.y, dot = b.x + b.y;
         if (!(sum > 0.f)) return make_float2(0.f, 0.f);
         const float off = plain ? 0.f : fmaf(ref, c, -rc);                       // y is too large by this much
-        const float y = fmaxf((ref - to) * c, -1e30f) - off, f = exp2_fast(y);
+        const float y = fmaxf(apart(ref, to, c, 0.f), -1e30f) - off, f = exp2_fast(y);
         return make_float2(f * sum, f > 0.f ? f * fmaf(y, sum, dot) : 0.f);
     }
 };
@@ -212,7 +218,7 @@ template <typename L>
 __device__ __noinline__ Sums<L> add_far(Sums<L> a, Vec<L> v, float bound, float c) {
     float most = Vec<L>::value(v.max());
     most = most == most ? fminf(most, FLT_MAX) : kNone;
-    if (most > a.far) {
+    if (most > a.far || apart(most, a.ref, c, 0.f) > 100.f) {          // far is no bound where it is infinite
         const float2 m = a.moved(most, c);
         a.against(most, bound, c, 100.f * inverse_fast(c));
         const float off = a.plain ? 0.f : fmaf(a.ref, c, -a.rc), f = exp2_fast(off);
@@ -228,7 +234,7 @@ __device__ __noinline__ Sums<L> add_far(Sums<L> a, Vec<L> v, float bound, float 
     float2 s = halves(a.s), d = halves(a.d);
 #pragma unroll
     for (int j = 0; j < Vec<L>::kN; ++j) {
-        const float y = fmaxf((fminf(x[j], FLT_MAX) - a.ref) * c, -200.f), e = exp2_fast(x[j] == x[j] ? y : -200.f);
+        const float y = fmaxf(apart(fminf(x[j], FLT_MAX), a.ref, c, 0.f), -200.f), e = exp2_fast(x[j] == x[j] ? y : -200.f);
         s.x += e;
         d.x = fmaf(e, y, d.x);
     }
@@ -442,7 +448,7 @@ __device__ void search(LogShared<T>& sm, const Part<L, T>& p, int k, int rank, K
 __device__ __forceinline__ float join(float own, float2 part, float c, float2& all) {
     const float m = unordered(__reduce_max_sync(0xffffffffu, ordered(own)));
     if (part.x > 0.f) {
-        const float y = fmaxf((own - m) * c, -1e30f), f = exp2_fast(y);
+        const float y = fmaxf(apart(own, m, c, 0.f), -1e30f), f = exp2_fast(y);
         part = make_float2(f * part.x, f > 0.f ? f * fmaf(y, part.x, part.y) : 0.f);
     }
 #pragma unroll
@@ -604,13 +610,13 @@ __global__ void __launch_bounds__(T, Cta<T>::kPerSm) logprobs_kernel(const ft_lo
     const float log_sum = none ? 0.f : logf(sums.x);
     if (lane == 0) {
         const float x = asked == asked ? fminf(asked, FLT_MAX) : kNone;
-        if (c.logp) c.logp[r] = x == kNone ? kNone : (x - m) * c.scale - log_sum;
+        if (c.logp) c.logp[r] = x == kNone ? kNone : apart(x, m, c.scale, -log_sum);
         if (c.entropy) c.entropy[r] = none ? 0.f : fmaxf(log_sum - sums.y / sums.x * 0.6931471805599453f, 0.f);
     }
     if (kTop && lane < c.k) {
         const float x = key_logit(sm.top[lane]);
         c.top_ids[r * c.k + lane] = key_index(sm.top[lane]);
-        c.top_logp[r * c.k + lane] = x > kNone ? (x - m) * c.scale - log_sum : kNone;
+        c.top_logp[r * c.k + lane] = x > kNone ? apart(x, m, c.scale, -log_sum) : kNone;
     }
 }
 

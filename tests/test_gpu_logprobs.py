@@ -291,3 +291,26 @@ def test_infinities_at_every_scale(ft, n, V, dtype):
     for scale in (1e-36, 6e-37, 5.5e-37, 4e-37, 3e-36, 1e-33, 1e-30, 1e-25, 1e-22, 2e-21, 1e-20, 1e-15, 1e-10, 1e-5, 1.0, 1e5, 1e15, 1e25):
         for k in (0, 3):
             check(x, t, run(ft, x, t, k, scale), k, scale, rows=range(9))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,V", [(9, 131072), (200, 20000), (330, 60001)])
+def test_differences_past_the_range(ft, n, V, dtype):
+    """Rows over the whole range of the type at scales that leave their exponentials numbers.  (Below 1.2e-38 the scale in base 2 is
+    rounded to a step of 2^-149, which moves an exponent by at most 2^-150 times 2^129, half of the 70 roundings of s that no row makes.)"""
+    x, t = torch.empty(n, V, dtype=dtype, device="cuda"), tokens_of(V, n, V)
+    most, low = torch.finfo(dtype).max, torch.finfo(dtype).min
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x.copy_((torch.rand(n, V, generator=g, device="cuda") * 2 - 1) * 3.38e38)
+    x[0, :V // 2], x[0, V // 2:] = low, most                      # every thread's reference is the lowest value at first
+    x[1, :V // 2], x[1, V // 2:] = most, low
+    x[2] = low
+    x[2, V - 1] = float("inf")
+    x[3] = low
+    x[3, 0] = float("inf")
+    x[4, V // 4 * 3:] = most
+    x[5, ::2] = float("-inf")
+    t[0], t[1], t[2], t[3] = 0, V - 1, 0, V - 1
+    for scale in (1e-42, 1e-40, 4e-39, 1e-38, 5e-38, 1e-37, 1.9e-37, 2.5e-37, 3e-37, 1e-36, 1e-35):
+        for k in (0, 3):
+            check(x, t, run(ft, x, t, k, scale), k, scale, rows=range(9))
