@@ -463,15 +463,18 @@ def _inner_dense(t, s):
     return True
 
 
-def _token_stride(t, what):
-    """Token stride in elements of a tensor whose tokens are dense.  That of a single token means nothing: its
-    elements, rounded to what the calls ask for."""
+def _token_stride(t, what, n):
+    """Token stride in elements of a tensor of n or more tokens, one per row, that are dense.  That of a single token means
+    nothing: its elements, rounded to what the calls ask for.  (Fewer rows are not tokens: n tokens at the stride of a
+    batch of them would lie behind the tensor.)"""
     try:
         s = t.stride()
     except AttributeError:
         raise TypeError(f"{what}: a raw address needs its token stride") from None
     if not ((len(s) == 2 and s[1] == 1) or t.is_contiguous() or _inner_dense(t, s)):
         _refuse(t, what, "dense rows, or a token stride")
+    if not s or t.shape[0] < n:
+        _refuse(t, what, f"a row for each of {n} tokens, or a token stride")
     return s[0] if t.shape[0] != 1 else t.numel() + 7 & ~7
 
 
@@ -491,9 +494,9 @@ def ft_kv_append(handle, layer, k, v, slots, n, k_stride=None, v_stride=None, st
         pk, pv = _address(k, _bf16, "append: k", False), _address(v, _bf16, "append: v", False)
         ps = _address(slots, _i32, "append: slots")
     if k_stride is None:
-        k_stride = _token_stride(k, "append: k")
+        k_stride = _token_stride(k, "append: k", n)
     if v_stride is None:
-        v_stride = _token_stride(v, "append: v")
+        v_stride = _token_stride(v, "append: v", n)
     status = _kv_append(handle, layer, pk, pv, k_stride, v_stride, ps, n, _stream(stream))
     if status:
         _check_kv(status, handle)
@@ -545,9 +548,9 @@ def ft_kv_attention(handle, layer, q, q_start, kv_len, block_table, table_stride
         pe = _address(lse, _f32, "attention: lse")
         pm = _address(tree_mask, _u64 if getattr(tree_mask, "dtype", None) is _u64 else _i64, "attention: tree_mask")
     if q_stride is None:
-        q_stride = _token_stride(q, "attention: q")
+        q_stride = _token_stride(q, "attention: q", n_tokens)
     if o_stride is None:
-        o_stride = _token_stride(o, "attention: o")
+        o_stride = _token_stride(o, "attention: o", n_tokens)
     status = _kv_attention(handle, _KV_ATTN.pack(pq, po, pe, q_stride, o_stride, ps, pl, pt, pm, layer, table_stride,
                                                  n_seqs, n_tokens, max_q, window, n_sink, sm_scale), _stream(stream))
     if status:
@@ -636,16 +639,20 @@ def ft_kv_append_rotated(handle, layer, q, k, v, slots, n, q_out, positions, rop
         pr, pqn, pkn = (_address(t, _f32, f"append_rotated: {name}") for t, name in ((rope, "rope"), (q_norm, "q_norm"), (k_norm, "k_norm")))
     try:
         if q_stride is None:
-            q_stride = (q.stride(0) if n != 1 else _ONE) if q.is_contiguous() else _token_stride(q, "append_rotated: q")
+            q_stride = (q.stride(0) if n != 1 else _ONE) if q.is_contiguous() and q.size(0) >= n else _token_stride(
+                q, "append_rotated: q", n)
         if k_stride is None:
-            k_stride = (k.stride(0) if n != 1 else _ONE) if k.is_contiguous() else _token_stride(k, "append_rotated: k")
+            k_stride = (k.stride(0) if n != 1 else _ONE) if k.is_contiguous() and k.size(0) >= n else _token_stride(
+                k, "append_rotated: k", n)
         if v_stride is None:
-            v_stride = (v.stride(0) if n != 1 else _ONE) if v.is_contiguous() else _token_stride(v, "append_rotated: v")
+            v_stride = (v.stride(0) if n != 1 else _ONE) if v.is_contiguous() and v.size(0) >= n else _token_stride(
+                v, "append_rotated: v", n)
         if q_out_stride is None:
-            q_out_stride = (q_out.stride(0) if n != 1 else _ONE) if q_out.is_contiguous() else _token_stride(q_out, "append_rotated: q_out")
+            q_out_stride = (q_out.stride(0) if n != 1 else _ONE) if q_out.is_contiguous() and q_out.size(0) >= n else _token_stride(
+                q_out, "append_rotated: q_out", n)
         if k_out_stride is None:
-            k_out_stride = 0 if not pko else (k_out.stride(0) if n != 1 else _ONE) if k_out.is_contiguous() else _token_stride(
-                k_out, "append_rotated: k_out")
+            k_out_stride = 0 if not pko else (k_out.stride(0) if n != 1 else _ONE) if k_out.is_contiguous() and k_out.size(
+                0) >= n else _token_stride(k_out, "append_rotated: k_out", n)
     except AttributeError:
         raise TypeError("append_rotated: a raw address needs its token stride") from None
     status = _kv_append_rotated(handle, _KV_QKV.pack(pq, pk, pv, po, pko, q_stride, k_stride, v_stride, q_out_stride, k_out_stride,

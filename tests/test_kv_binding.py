@@ -102,3 +102,45 @@ def test_attention_refuses_what_it_would_misread(ft, calls):
     assert not calls
     with pytest.raises(TypeError, match="stride"):
         ft.ft_kv_attention(7, **{**good, "q": good["q"].data_ptr()})
+
+
+@pytest.fixture
+def rotated(ft, monkeypatch):
+    got = []
+    monkeypatch.setattr(ft, "_kv_append_rotated", lambda *args: got.append(args) or 0)
+    return got
+
+
+def test_rows_that_are_no_tokens(ft, calls, rotated):
+    """A batch of sequences is not taken for its tokens: their stride would be a sequence's, and most of them lie behind the tensor."""
+    n = 12
+    fine = dict(q=bf16(n, 4, 64), k=bf16(n, 2, 64), v=bf16(n, 2, 64), q_out=bf16(n, 4, 64), k_out=bf16(n, 2, 64), slots=i32(n))
+    attn = dict(layer=0, q=bf16(n, 4, 64), q_start=i32(3), kv_len=i32(2), block_table=i32(2, 5), table_stride=5, n_seqs=2, n_tokens=n, max_q=n,
+                o=bf16(n, 4, 64), stream=0)
+
+    def rotate(n=n, **kw):
+        ft.ft_kv_append_rotated(7, 0, n=n, positions=None, rope=None, rope_dim=0, n_positions=0, stream=0, **(fine | kw))
+
+    rotate()
+    for name, t in list(fine.items())[:5]:
+        h = t.shape[1]
+        for batch in (t[None], t.view(3, 4, h, 64), t.view(3, 4, h * 64), t.view(1, n * h * 64), bf16(3, 4, 2 * h, 64)[:, :, :h].contiguous(),
+                      bf16(3, 4, h * 64 + 8)[:, :, :h * 64], t[:n - 1]):
+            refused(ft, f"append_rotated: {name}", lambda: rotate(**{name: batch}))
+    assert len(rotated) == 1
+    for batch in (fine["k"][None], fine["k"].view(3, 4, 128), fine["k"][:5], fine["k"][:0], bf16(())):
+        refused(ft, "append: k", lambda: ft.ft_kv_append(7, 0, batch, fine["v"], fine["slots"], n, stream=0))
+        refused(ft, "append: v", lambda: ft.ft_kv_append(7, 0, fine["k"], batch, fine["slots"], n, stream=0))
+    for name in ("q", "o"):
+        for batch in (attn[name][None], attn[name].view(3, 4, 256), attn[name][:5]):
+            refused(ft, f"attention: {name}", lambda: ft.ft_kv_attention(7, **(attn | {name: batch})))
+    assert not calls
+    # more rows than tokens, one token in any shape, a stride that is given
+    rotate(n=5)
+    rotate(**{name: t[:1][None] for name, t in fine.items()}, n=1)
+    rotate(q=fine["q"][None], q_stride=256)
+    assert ft._KV_QKV.unpack(rotated[1][1])[5:10] == (256, 128, 128, 256, 128) == ft._KV_QKV.unpack(rotated[3][1])[5:10]
+    assert len(rotated) == 4 and all(x >= 256 and x % 8 == 0 for x in ft._KV_QKV.unpack(rotated[2][1])[5:10])
+    ft.ft_kv_append(7, 0, fine["k"], fine["v"], fine["slots"], 5, stream=0)
+    ft.ft_kv_attention(7, **(attn | dict(n_tokens=5)))
+    assert calls["append"][4:6] == (128, 128) and ft._KV_ATTN.unpack(calls["attention"][1])[3:5] == (256, 256)
