@@ -114,9 +114,10 @@ __device__ __forceinline__ void zero(uint32_t (&x)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = 0;
 }
-// An infinite norm: numbers become 0 before a weight can make them infinite, infinities and NaN become NaN.
-__device__ __forceinline__ void times_zero(uint32_t (&x)[8]) {
-    const __nv_bfloat162 none = __floats2bfloat162_rn(0.f, 0.f);
+// An inverse norm r that is no positive number.  0, of an infinite norm: numbers become 0 before a weight can make them infinite,
+// infinities and NaN become NaN.  NaN, of a head with a NaN: all dims do.
+__device__ __forceinline__ void times(uint32_t (&x)[8], float r) {
+    const __nv_bfloat162 none = __floats2bfloat162_rn(r, r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const __nv_bfloat162 a = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x[j]), none);
@@ -201,7 +202,7 @@ __device__ __forceinline__ void turn_queries(const RotateArgs& a, const Lane<D, 
 #pragma unroll
             for (int o = 1; o < D / 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             r = rsqrtf(sum * (1.f / D) + a.eps);
-            if (r == 0.f) times_zero(x);
+            if (r == 0.f) times(x, r);
         }
         turn_plainly(p, x, A, B, r, a.rope_dim < D);
         if (live) p.store(a.q_out + (size_t)tok * a.q_out_stride + head * D, x);
@@ -286,7 +287,7 @@ __device__ __forceinline__ void turn_keys(const RotateArgs& a, const Lane<D, kIn
         Two r = {1.f, 0.f};
         if (a.k_norm) {
             r = inverse_norm<D>(k, a.eps);
-            if (r.h == 0.f) times_zero(k);
+            if (!(r.h > 0.f)) times(k, r.h);
         }
         const Pair rh = pair(r.h, r.h), rl = pair(r.l, r.l);
         const bool numbers = mm.x < 0x1p120f && mm.y < 0x1p120f;

@@ -297,3 +297,31 @@ def test_refusals(ft):
         c.layer = layer
         with pytest.raises(ft.FtError):
             c.run()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,rope,fmt", [(64, 32, "fp8"), (64, 64, "nvfp4"), (128, 128, "nvfp4"), (128, 64, "fp8"), (256, 0, "nvfp4"), (256, 160, "fp8")])
+def test_a_norm_of_a_nan_or_an_infinity(ft, D, rope, fmt, inter):
+    """A NaN makes every dim of its head one; an infinity leaves zeros and, where it and its partner stand, NaN.  Both are stored as
+    such, in whichever lane they stand."""
+    c = Case(ft, fmt, D, 3, 3, 60, rope, inter=inter)
+    rng = np.random.default_rng(D + rope)
+    q, k = c.q.view(60, 3, D), c.k.view(60, 3, D)
+    for i in range(60):
+        d = i * D // 60 if i < 50 else int(rng.integers(0, D))
+        value = [float("nan"), float("inf"), float("-inf")][i % 3]
+        q[i, i % 2, d] = value
+        k[i, i % 2, d] = value
+    q_out, k_out = c.run()
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        oq, tol, ok, _ = c.want()
+    got = q_out.double().cpu().numpy()
+    none = np.isnan(oq)
+    assert np.array_equal(np.isnan(got), none) and np.all(np.abs(got - oq)[~none] <= tol[~none])
+    assert torch.equal(k_out.cpu().isnan(), ok.isnan()) and torch.equal(k_out.cpu().nan_to_num(), ok.nan_to_num())
+    assert ok[0, 0].isnan().all() and not ok[1, 1].isnan().all()
+    back = torch.empty(60, 3, D, dtype=torch.bfloat16, device="cuda")
+    ft.ft_kv_read(c.kv.handle, c.layer, c.slots, 60, back, torch.empty_like(back))
+    val = K.values(*K.quantise(ok.float().numpy(), fmt, c.scales[0]), fmt, c.scales[0])
+    assert torch.equal(back.cpu(), torch.from_numpy(val.astype(np.float32)).to(torch.bfloat16))
