@@ -245,11 +245,11 @@ __device__ __forceinline__ Two inverse_norm(const uint32_t (&x)[8], float eps) {
     }
     Two m = two_sum(__fmul_rn(sum.h, 1.f / D), eps);
     m.l = __fmaf_rn(sum.l, 1.f / D, m.l);
-    // one step of Newton's on the fp32 root, its residual 1 - m r^2 in two parts
-    const float r = rsqrtf(m.h), r2 = __fmul_rn(r, r), r2l = __fmaf_rn(r, r, -r2);
-    float e = __fmaf_rn(-m.h, r2, 1.f);
-    e = __fmaf_rn(-m.h, r2l, e);
-    e = __fmaf_rn(-m.l, r2, e);
+    // one step of Newton's on the fp32 root, its residual 1 - m r^2 by way of m r in two parts (r^2 would leave the range at both ends)
+    const float r = rsqrtf(m.h), t = __fmul_rn(m.h, r), tl = __fmaf_rn(m.h, r, -t);
+    float e = __fmaf_rn(-t, r, 1.f);
+    e = __fmaf_rn(-tl, r, e);
+    e = __fmaf_rn(-__fmul_rn(m.l, r), r, e);
     return {r, isinf(m.h) ? 0.f : __fmul_rn(__fmul_rn(0.5f, r), e)};
 }
 

@@ -581,9 +581,9 @@ ft_status ft_rope_table(const double* inv_freq, int32_t rope_dim, int32_t n_posi
  *   the pairs (a, b) of y become (a c - b s, b c + a s) with c and s of the token's row of the table; pair i is
  *   (y[i], y[i + rope_dim / 2]), or (y[2 i], y[2 i + 1]) if interleaved; dims from rope_dim on stay.
  * q_out gets q's result rounded to bf16.  k's result is rounded to fp32, then to bf16, and stored as ft_kv_append stores that (k_out
- * gets it too); v is stored as it is.  q's values are in fp32; k's are good to some 2^-40 of the larger of their pair (above 2^-100)
- * before they are rounded, so what is stored is what the formula gives in 64 bits.  Where a head's squares pass fp32's range
- * its finite dims come out as 0.
+ * gets it too); v is stored as it is.  q's values are in fp32; k's are good to some 2^-40 of the larger of their pair (above 2^-100;
+ * with a norm also eps, or the mean of the squares) before they are rounded, so what is stored is what the formula gives in 64 bits.  Where
+ * the sum of a head's squares, or their mean plus eps, passes fp32's range its finite dims come out as 0.
  * Tokens whose slot is -1 are padding: nothing of them is written, and nothing depends on what they hold.  Another slot outside the cache, or a position
  * outside [0, n_positions), sets FT_DEV_BAD_ID and is treated the same way.  Slots differ from each other.
  * q_out may be q, k_out may be k (of the same stride); no other arrays overlap.

@@ -325,3 +325,26 @@ def test_a_norm_of_a_nan_or_an_infinity(ft, D, rope, fmt, inter):
     ft.ft_kv_read(c.kv.handle, c.layer, c.slots, 60, back, torch.empty_like(back))
     val = K.values(*K.quantise(ok.float().numpy(), fmt, c.scales[0]), fmt, c.scales[0])
     assert torch.equal(back.cpu(), torch.from_numpy(val.astype(np.float32)).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("D,rope,fmt", [(64, 32, "fp8"), (128, 128, "nvfp4"), (256, 96, "nvfp4")])
+@pytest.mark.parametrize("eps", [1.5e-45, 1e-42, 3e-39, 1.2e-38, 1e-30, 1e-3, 1e30, 3.4e38])
+def test_norms_at_the_ends_of_the_range(ft, D, rope, fmt, eps):
+    """Any positive eps, with heads of zeros and of values up to 2^60: the norm stays good to 2^-40 as long as eps or the squares do not
+    lie below some 2^-100 (other heads are left out here where eps is)."""
+    c = Case(ft, fmt, D, 3, 3, 200, rope, eps=eps)
+    rng = np.random.default_rng(D)
+    for t in (c.q, c.k):
+        x = t.view(200, 3, D)
+        x[:150] *= torch.from_numpy(np.exp2(rng.uniform(-40 if eps < 1e-30 else -60, 58, (150, 3, 1))).astype(np.float32)).to(torch.bfloat16).cuda()
+        x[::7] = 0
+        x[1::7, 1] = 0
+        x[3, :, 1:] = 0                                            # one dim of a head
+    q_out, k_out = c.run()
+    # a number of bf16 below 2^-126 is a multiple of 2^-133, so its rounding may be off by 2^-134 (and the two products' and the sum's before
+    # it, below fp32's 2^-126, by 3 times 2^-150)
+    oq, tol, _, _ = c.want()
+    got = q_out.double().cpu().numpy()
+    assert np.all(np.abs(got - oq) <= tol + 2.0 ** -134 + 2.0 ** -148)
+    small = np.abs(oq) < 2.0 ** -125
+    c.check(torch.where(torch.from_numpy(small).cuda(), torch.from_numpy(oq).cuda(), q_out.double()), k_out)
