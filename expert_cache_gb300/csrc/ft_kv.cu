@@ -294,7 +294,7 @@ ft_status ft_kv_append(ft_kv* kv, int32_t layer, const void* k, const void* v, i
     if (!kv) return FT_ERR_ARG;
     if (layer < 0 || layer >= kv->d.L || n < 0) return fail(kv, FT_ERR_ARG, "append: layer or n out of range");
     if (n == 0) return FT_OK;
-    if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16))
+    if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16) || !words(slots))
         return fail(kv, FT_ERR_ARG, "append: NULL or misaligned k, v or slots");
     const int64_t row = (int64_t)kv->d.n_kv_heads * kv->d.head_dim;
     if (k_stride < row || v_stride < row || k_stride % 8 || v_stride % 8)
@@ -309,7 +309,7 @@ ft_status ft_kv_read(ft_kv* kv, int32_t layer, const int32_t* slots, int32_t n, 
     if (!kv) return FT_ERR_ARG;
     if (layer < 0 || layer >= kv->d.L || n < 0) return fail(kv, FT_ERR_ARG, "read: layer or n out of range");
     if (n == 0) return FT_OK;
-    if (!slots || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16))
+    if (!slots || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16) || !words(slots))
         return fail(kv, FT_ERR_ARG, "read: NULL or misaligned slots, k_out or v_out");
     NvtxRange r("ft_kv_read");
     const cudaError_t e = launch_kv_read(view(kv, layer), kv->d.head_dim, kv->d.format, slots, n, k_out, v_out,
@@ -332,7 +332,7 @@ ft_status ft_kv_attention(ft_kv* kv, const ft_kv_attn* call, void* stream) {
         return fail(kv, FT_ERR_ARG, "attention: window, n_sink or sm_scale");
     if (c.n_seqs == 0 || c.n_tokens == 0) return FT_OK;
     if (!c.q || !c.q_start || !c.kv_len || !c.block_table || !c.o || !aligned(c.q, 16) || !aligned(c.o, 16) ||
-        !aligned(c.tree_mask, 8))
+        !aligned(c.tree_mask, 8) || !words(c.q_start, c.kv_len, c.block_table, c.lse))
         return fail(kv, FT_ERR_ARG, "attention: NULL or misaligned pointer");
     const int64_t row = (int64_t)d.n_q_heads * d.head_dim;
     if (c.q_stride < row || c.o_stride < row || c.q_stride % 8 || c.o_stride % 8)

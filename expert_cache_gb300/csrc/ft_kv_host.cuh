@@ -46,6 +46,9 @@ inline ft_status cuda_fail(ft_kv* kv, cudaError_t e, const char* what) {
 }
 
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+// Arrays of 32-bit elements (or NULL).
+template <typename... P>
+bool words(const P*... p) { return (((uintptr_t)p | ...) & 3) == 0; }
 
 inline KvView view(const ft_kv* kv, int layer) {
     const ft_kv_desc& d = kv->d;

@@ -204,6 +204,9 @@ extern "C" ft_status ft_kv_plan(ft_kv* kv, const ft_kv_step* call, void* stream)
         (c.n_seqs && (!c.n_new || !c.len || !c.held || !c.block_table || !c.kv_len || !c.len_out || !c.held_out)))
         return fail(kv, FT_ERR_ARG, "plan: NULL pointer");
     if (!aligned(c.tree_mask, 8)) return fail(kv, FT_ERR_ARG, "plan: misaligned tree_mask");
+    if (!words(c.n_new, c.len, c.held, c.n_free, c.block_table, c.free_pages, c.q_start, c.kv_len, c.slots, c.positions, c.len_out, c.held_out,
+               c.n_free_out))
+        return fail(kv, FT_ERR_ARG, "plan: misaligned pointer");
     NvtxRange r("ft_kv_plan");
     cudaError_t e = prepare<kv_plan_kernel>();
     if (e != cudaSuccess) return cuda_fail(kv, e, "plan");

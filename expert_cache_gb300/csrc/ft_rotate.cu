@@ -433,7 +433,7 @@ ft_status ft_kv_append_rotated(ft_kv* kv, const ft_kv_qkv* call, void* stream) {
     if (!c.q || !c.k || !c.v || !c.q_out || !c.slots || (c.rope_dim && (!c.rope || !c.positions)))
         return fail(kv, FT_ERR_ARG, "append_rotated: NULL pointer");
     if (!aligned(c.q, 16) || !aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.q_out, 16) || !aligned(c.k_out, 16) ||
-        !aligned(c.q_norm, 16) || !aligned(c.k_norm, 16) || !aligned(c.rope, 16))
+        !aligned(c.q_norm, 16) || !aligned(c.k_norm, 16) || !aligned(c.rope, 16) || !words(c.slots, c.positions))
         return fail(kv, FT_ERR_ARG, "append_rotated: misaligned pointer");
     const int64_t q_row = (int64_t)d.n_q_heads * d.head_dim, k_row = (int64_t)d.n_kv_heads * d.head_dim;
     if (c.q_stride < q_row || c.q_out_stride < q_row || c.k_stride < k_row || c.v_stride < k_row || (c.k_out && c.k_out_stride < k_row) ||

@@ -455,7 +455,7 @@ void      ft_kv_destroy(ft_kv* kv);
  *             slot outside [0, n_pages * page_size) is skipped and sets FT_DEV_BAD_ID;
  *             the slots of one call differ from each other
  * Asynchronous on stream, capturable.  n = 0 does nothing.  Errors (nothing launched):
- * FT_ERR_ARG for layer outside [0, L), n < 0, NULL or misaligned k/v, bad strides. */
+ * FT_ERR_ARG for layer outside [0, L), n < 0, NULL or misaligned k, v (16 bytes) or slots (4), bad strides. */
 ft_status ft_kv_append(ft_kv* kv, int32_t layer, const void* k, const void* v, int64_t k_stride,
                        int64_t v_stride, const int32_t* slots, int32_t n, void* stream);
 
@@ -550,7 +550,7 @@ ft_status ft_kv_attention(ft_kv* kv, const ft_kv_attn* call, void* stream);
  * their old value).  A page outside [0, n_pages) in the table or on the stack gives its tokens the slot -1 and sets
  * FT_DEV_BAD_ID, as does n_free outside [0, n_pages] (it is cut to that) or pages pushed past n_pages (dropped).
  * Errors (nothing launched): FT_ERR_ARG for n_seqs outside [0, max_seqs], n_tokens outside [0, 2^30), table_stride < 1, NULL
- * pointers (arrays of no elements may be NULL). */
+ * pointers (arrays of no elements may be NULL) or misaligned ones (to an element). */
 typedef struct {
     const int32_t* n_new;       /* device [n_seqs] */
     const int32_t* len;         /* device [n_seqs] */
@@ -588,7 +588,7 @@ ft_status ft_rope_table(const double* inv_freq, int32_t rope_dim, int32_t n_posi
  * outside [0, n_positions), sets FT_DEV_BAD_ID and is treated the same way.  Slots differ from each other.
  * q_out may be q, k_out may be k (of the same stride); no other arrays overlap.
  * Errors (nothing launched): FT_ERR_ARG for layer outside [0, L), n < 0, NULL or misaligned q, k, v, q_out (16 bytes; k_out
- * too), norms or table (16 bytes), strides that are no multiples of 8 or less than a token, rope_dim no multiple of 32 or outside
+ * too), norms or table (16 bytes), slots or positions (4), strides that are no multiples of 8 or less than a token, rope_dim no multiple of 32 or outside
  * [0, head_dim], n_positions < 1 with rope_dim > 0, eps not finite or <= 0 with a norm. */
 typedef struct {
     const void* q;            /* device bf16 [n, n_q_heads, D] */

@@ -1,5 +1,7 @@
 """The key/value calls of the binding look at the types and strides of the tensors that they are given: what the kernels would
 misread is refused, and what they can read reaches them with the right strides.  No GPU: the C calls are caught."""
+import ctypes
+
 import pytest
 import torch
 
@@ -144,3 +146,35 @@ def test_rows_that_are_no_tokens(ft, calls, rotated):
     ft.ft_kv_append(7, 0, fine["k"], fine["v"], fine["slots"], 5, stream=0)
     ft.ft_kv_attention(7, **(attn | dict(n_tokens=5)))
     assert calls["append"][4:6] == (128, 128) and ft._KV_ATTN.unpack(calls["attention"][1])[3:5] == (256, 256)
+
+
+def test_arrays_at_odd_addresses(ft):
+    """Arrays of 32-bit elements that do not start at one are refused by the calls themselves, before anything is launched.  The handle's
+    fields stand in host memory here; a call that is not refused finds no GPU, or no work."""
+    class Handle(ctypes.Structure):
+        _fields_ = [("d", ft.FtKvDesc), ("layer_bytes", ctypes.c_size_t), ("page_shift", ctypes.c_int), ("err", ctypes.c_char * 256)]
+
+    h = Handle(ft.FtKvDesc(1, 8, 16, 2, 64, 4, 2, ft.FT_KV_FP8, 1.0, 1.0, None, None), 8 * 16 * 2 * 128, 4, b"")
+    handle, at = ctypes.addressof(h), 1 << 12
+
+    def misaligned(what, f):
+        with pytest.raises(ft.FtError, match=f"{what}: .*misaligned") as ei:
+            f()
+        assert ei.value.status == ft.FT_ERR_ARG
+
+    for odd in (1, 2, 3):
+        misaligned("append", lambda: ft.ft_kv_append(handle, 0, at, at, at + odd, 2, k_stride=128, v_stride=128, stream=0))
+        misaligned("read", lambda: ft.ft_kv_read(handle, 0, at + odd, 2, at, at, stream=0))
+        attn = dict(layer=0, q=at, q_start=at, kv_len=at, block_table=at, table_stride=4, n_seqs=1, n_tokens=2, max_q=2, o=at, lse=at, q_stride=256,
+                    o_stride=256, stream=0)
+        for name in ("q_start", "kv_len", "block_table", "lse"):
+            misaligned("attention", lambda: ft.ft_kv_attention(handle, **(attn | {name: at + odd})))
+        plan = dict(n_new=at, len=at, held=at, block_table=at, table_stride=4, free_pages=at, n_free=at, n_seqs=1, n_tokens=2, q_start=at, kv_len=at,
+                    slots=at, len_out=at, held_out=at, n_free_out=at, positions=at, stream=0)
+        for name in plan:
+            if plan[name] == at:
+                misaligned("plan", lambda: ft.ft_kv_plan(handle, **(plan | {name: at + odd})))
+        turn = dict(layer=0, q=at, k=at, v=at, slots=at, n=2, q_out=at, positions=at, rope=at, rope_dim=32, n_positions=9, q_stride=256, k_stride=128,
+                    v_stride=128, q_out_stride=256, stream=0)
+        for name in ("slots", "positions"):
+            misaligned("append_rotated", lambda: ft.ft_kv_append_rotated(handle, **(turn | {name: at + odd})))
