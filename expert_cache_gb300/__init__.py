@@ -473,9 +473,10 @@ def _token_stride(t, what, n):
         raise TypeError(f"{what}: a raw address needs its token stride") from None
     if not ((len(s) == 2 and s[1] == 1) or t.is_contiguous() or _inner_dense(t, s)):
         _refuse(t, what, "dense rows, or a token stride")
-    if not s or t.shape[0] < n:
+    rows = t.shape[0] if s else -1
+    if rows < n or rows < 0:
         _refuse(t, what, f"a row for each of {n} tokens, or a token stride")
-    return s[0] if t.shape[0] != 1 else t.numel() + 7 & ~7
+    return s[0] if rows != 1 else t.numel() + 7 & ~7
 
 
 # The calls below look at the tensors' types and strides themselves where that takes one test per tensor (a call's host
@@ -639,20 +640,20 @@ def ft_kv_append_rotated(handle, layer, q, k, v, slots, n, q_out, positions, rop
         pr, pqn, pkn = (_address(t, _f32, f"append_rotated: {name}") for t, name in ((rope, "rope"), (q_norm, "q_norm"), (k_norm, "k_norm")))
     try:
         if q_stride is None:
-            q_stride = (q.stride(0) if n != 1 else _ONE) if q.is_contiguous() and q.size(0) >= n else _token_stride(
-                q, "append_rotated: q", n)
+            q_stride = (_ONE if n == 1 else s if n * (s := q.stride()[0]) <= q.numel() else _token_stride(
+                q, "append_rotated: q", n)) if q.is_contiguous() else _token_stride(q, "append_rotated: q", n)
         if k_stride is None:
-            k_stride = (k.stride(0) if n != 1 else _ONE) if k.is_contiguous() and k.size(0) >= n else _token_stride(
-                k, "append_rotated: k", n)
+            k_stride = (_ONE if n == 1 else s if n * (s := k.stride()[0]) <= k.numel() else _token_stride(
+                k, "append_rotated: k", n)) if k.is_contiguous() else _token_stride(k, "append_rotated: k", n)
         if v_stride is None:
-            v_stride = (v.stride(0) if n != 1 else _ONE) if v.is_contiguous() and v.size(0) >= n else _token_stride(
-                v, "append_rotated: v", n)
+            v_stride = (_ONE if n == 1 else s if n * (s := v.stride()[0]) <= v.numel() else _token_stride(
+                v, "append_rotated: v", n)) if v.is_contiguous() else _token_stride(v, "append_rotated: v", n)
         if q_out_stride is None:
-            q_out_stride = (q_out.stride(0) if n != 1 else _ONE) if q_out.is_contiguous() and q_out.size(0) >= n else _token_stride(
-                q_out, "append_rotated: q_out", n)
+            q_out_stride = (_ONE if n == 1 else s if n * (s := q_out.stride()[0]) <= q_out.numel() else _token_stride(
+                q_out, "append_rotated: q_out", n)) if q_out.is_contiguous() else _token_stride(q_out, "append_rotated: q_out", n)
         if k_out_stride is None:
-            k_out_stride = 0 if not pko else (k_out.stride(0) if n != 1 else _ONE) if k_out.is_contiguous() and k_out.size(
-                0) >= n else _token_stride(k_out, "append_rotated: k_out", n)
+            k_out_stride = 0 if not pko else (_ONE if n == 1 else s if n * (s := k_out.stride()[0]) <= k_out.numel() else _token_stride(
+                k_out, "append_rotated: k_out", n)) if k_out.is_contiguous() else _token_stride(k_out, "append_rotated: k_out", n)
     except AttributeError:
         raise TypeError("append_rotated: a raw address needs its token stride") from None
     status = _kv_append_rotated(handle, _KV_QKV.pack(pq, pk, pv, po, pko, q_stride, k_stride, v_stride, q_out_stride, k_out_stride,
