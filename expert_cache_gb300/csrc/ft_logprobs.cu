@@ -157,8 +157,9 @@ struct LogShared {
 
 // (a - b) c + d, for c > 0.  The difference may pass fp32's range where its product does not.
 __device__ __forceinline__ float apart(float a, float b, float c, float d) {
-    const float x = a - b;
-    return fabsf(x) <= FLT_MAX ? fmaf(x, c, d) : fmaf(0.5f * a - 0.5f * b, 2.f * c, d);
+    float x = a - b;
+    if (!(fabsf(x) <= FLT_MAX)) x = 0.5f * a - 0.5f * b, c *= 2.f;
+    return fmaf(x, c, d);
 }
 
 // A word to the same place in the shared memory of the cluster's first CTA.
