@@ -235,7 +235,7 @@ __device__ __noinline__ Sums<L> add_far(Sums<L> a, Vec<L> v, float bound, float 
     float2 s = halves(a.s), d = halves(a.d);
 #pragma unroll
     for (int j = 0; j < Vec<L>::kN; ++j) {
-        const float y = fmaxf(apart(fminf(x[j], FLT_MAX), a.ref, c, 0.f), -200.f), e = exp2_fast(x[j] == x[j] ? y : -200.f);
+        const float y = x[j] == x[j] ? fmaxf(apart(fminf(x[j], FLT_MAX), a.ref, c, 0.f), -200.f) : -200.f, e = exp2_fast(y);
         s.x += e;
         d.x = fmaf(e, y, d.x);
     }

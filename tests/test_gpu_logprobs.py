@@ -314,3 +314,21 @@ def test_differences_past_the_range(ft, n, V, dtype):
     for scale in (1e-42, 1e-40, 4e-39, 1e-38, 5e-38, 1e-37, 1.9e-37, 2.5e-37, 3e-37, 1e-36, 1e-35):
         for k in (0, 3):
             check(x, t, run(ft, x, t, k, scale), k, scale, rows=range(9))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,V", [(6, 131072), (200, 20000), (330, 60001), (3, 29)])
+def test_nan_among_equal_logits(ft, n, V, dtype):
+    """NaN counts for nothing wherever the sums are taken apart: large scales, large logits, the ends of both; many logits share the
+    largest value, so that the entropy is no zero."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    hit = torch.rand(n, V, generator=g, device="cuda")
+    t = tokens_of(V, n, V)
+    for top in (3.0, 1e12, -1e12, 2e38, float("inf")):
+        x = torch.where(hit < 0.3, top, logits(V, n, V) - 20 if top == 3.0 else float("-inf")).to(dtype)
+        x[hit > 0.6] = float("nan")
+        x[0, 0], x[1, -1] = float("nan"), float("nan")
+        x[2, V // 2] = top
+        for scale in (1e-42, 1e-37, 1e-25, 1e-3, 1.0, 50.0, 1e8, 1e12, 1e19, 1e30, 3e38):
+            for k in (0, 3):
+                check(x, t, run(ft, x, t, k, scale), k, scale, rows=range(3))
