@@ -2,7 +2,7 @@
 //
 // One pass over a row, by a cluster of 1 to 8 CTAs: with y = scale (x - ref) per thread the sums S = sum e^y and D = sum e^y y
 // give log sum = log S and entropy = log S - D / S.  A thread's ref is a maximum of a sample of the row, so that no
-// sum has to be rescaled unless a logit lies e^69 above it; the row's own maximum is taken at the end.
+// sum has to be rescaled unless a logit lies e^44 above it; the row's own maximum is taken at the end.
 //
 // The k largest come out of the same pass.  From the sample (the first 8 vectors of every thread) the k-th largest of some 2 k
 // logits is a lower bound of the row's k-th; only what reaches it is kept and put on a list in shared memory (4 to 8 k of
@@ -33,6 +33,10 @@ constexpr int kRounds = 2;             // rounds under way
 constexpr int kListed = 1024;          // entries of a CTA's list
 constexpr int kMaxCtas = 8;            // of a row
 constexpr float kNone = -INFINITY;
+// How far, in powers of 2, a logit may lie above a thread's reference.  2^y loses 22 roundings of 2^-24 to y's own just below 64 (45 at
+// 100, where the sums would still be numbers, and 1 at 2; but every step up costs a call: 2048 rows of 131,072 at a scale of 20 take
+// 90.0, 91.6 and 94.2 us with 100, 64 and 40, rising ones 132, 167 and 230).
+constexpr float kFar = 64.f;
 
 // What follows from the number of a CTA's threads.
 template <int T>
@@ -155,10 +159,11 @@ struct LogShared {
     float bound, ref;
 };
 
-// (a - b) c + d, for c > 0.  The difference may pass fp32's range where its product does not.
-__device__ __forceinline__ float apart(float a, float b, float c, float d) {
+// (a - b) c + d, for c > 0.  Below `halved` the difference is taken in halves: it may pass fp32's range where its product does not
+// (or, at the default, where that is not so far out that its power of 2 is 0).
+__device__ __forceinline__ float apart(float a, float b, float c, float d, float halved = 1e-36f) {
     float x = a - b;
-    if (!(fabsf(x) <= FLT_MAX)) x = 0.5f * a - 0.5f * b, c *= 2.f;
+    if (c < halved) x = 0.5f * a - 0.5f * b, c *= 2.f;
     return fmaf(x, c, d);
 }
 
@@ -185,7 +190,8 @@ struct Sums {
     // span: some 100 / c, 0 or infinite where that is no normal number.
     __device__ __forceinline__ void against(float to, float bound, float c, float span) {
         ref = to;
-        far = to == kNone ? kNone : __fadd_rd(to, span);         // not above it: next to a large ref one step may be worth more than the span
+        // rounded down: next to a large ref one step may be worth more than the span
+        far = to == kNone ? kNone : __fadd_rd(to, kFar / 100.f * span);
         plain = !(fabsf(to) * c < 0x1p26f && span > 0.f && to - 2.f * span > -1e38f && far < FLT_MAX);
         rc = plain ? 0.f : to * c;
         floor = Vec<L>::limit(to - 2.f * span);
@@ -207,8 +213,8 @@ struct Sums {
         const float2 a = halves(s), b = halves(d);
         const float sum = a.x + a.y, dot = b.x + b.y;
         if (!(sum > 0.f)) return make_float2(0.f, 0.f);
-        const float off = plain ? 0.f : fmaf(ref, c, -rc);                       // y is too large by this much
-        const float y = fmaxf(apart(ref, to, c, 0.f), -1e30f) - off, f = exp2_fast(y);
+        // (otherwise the very number that y was for such a logit, so that its rounding cancels)
+        const float y = fmaxf(plain ? apart(ref, to, c, 0.f) : fmaf(-to, c, rc), -1e30f), f = exp2_fast(y);
         return make_float2(f * sum, f > 0.f ? f * fmaf(y, sum, dot) : 0.f);
     }
 };
@@ -219,7 +225,7 @@ template <typename L>
 __device__ __noinline__ Sums<L> add_far(Sums<L> a, Vec<L> v, float bound, float c) {
     float most = Vec<L>::value(v.max());
     most = most == most ? fminf(most, FLT_MAX) : kNone;
-    if (most > a.far || apart(most, a.ref, c, 0.f) > 100.f) {          // far is no bound where it is infinite
+    if (most > a.far || apart(most, a.ref, c, 0.f) > kFar) {          // far is no bound where it is infinite
         const float2 m = a.moved(most, c);
         a.against(most, bound, c, 100.f * inverse_fast(c));
         const float off = a.plain ? 0.f : fmaf(a.ref, c, -a.rc), f = exp2_fast(off);
@@ -611,13 +617,13 @@ __global__ void __launch_bounds__(T, Cta<T>::kPerSm) logprobs_kernel(const ft_lo
     const float log_sum = none ? 0.f : logf(sums.x);
     if (lane == 0) {
         const float x = asked == asked ? fminf(asked, FLT_MAX) : kNone;
-        if (c.logp) c.logp[r] = x == kNone ? kNone : apart(x, m, c.scale, -log_sum);
+        if (c.logp) c.logp[r] = x == kNone ? kNone : apart(x, m, c.scale, -log_sum, 2.f);
         if (c.entropy) c.entropy[r] = none ? 0.f : fmaxf(log_sum - sums.y / sums.x * 0.6931471805599453f, 0.f);
     }
     if (kTop && lane < c.k) {
         const float x = key_logit(sm.top[lane]);
         c.top_ids[r * c.k + lane] = key_index(sm.top[lane]);
-        c.top_logp[r * c.k + lane] = x > kNone ? apart(x, m, c.scale, -log_sum) : kNone;
+        c.top_logp[r * c.k + lane] = x > kNone ? apart(x, m, c.scale, -log_sum, 2.f) : kNone;
     }
 }
 

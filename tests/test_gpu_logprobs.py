@@ -332,3 +332,22 @@ def test_nan_among_equal_logits(ft, n, V, dtype):
         for scale in (1e-42, 1e-37, 1e-25, 1e-3, 1.0, 50.0, 1e8, 1e12, 1e19, 1e30, 3e38):
             for k in (0, 3):
                 check(x, t, run(ft, x, t, k, scale), k, scale, rows=range(3))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [12, 30, 318, 1003, 2041])
+def test_a_largest_logit_that_comes_late(ft, V, dtype):
+    """The largest stands behind what the references are taken from, 1 to 200 above the others.  (A thread's terms lie up to 2^64 above its
+    reference.  The exponent's rounding is then 22 of the 2^-24 of which s has 70 or more, that of the factor back to the largest another 22,
+    the exponentials 8; a term of these short rows passes fewer than 16 additions.)"""
+    gaps = [1, 3, 8, 11, 12, 13, 20, 33, 41, 55, 60, 66, 68, 70, 90, 120, 200]
+    n = 2 * len(gaps)
+    x = logits(V, n, V, dtype, spread=1.0)
+    for i, gap in enumerate(gaps):
+        x[2 * i, V - 1] = x[2 * i].float().max() + gap
+        x[2 * i + 1, V - 1] = x[2 * i + 1].float().max() + gap + 0.37
+        x[2 * i + 1, V - 2] = x[2 * i + 1, V - 1].float() - 1
+    t = torch.full((n,), V - 1, dtype=torch.int32, device="cuda")
+    for scale in (1.0, 0.9, 1.2587579488754272):
+        for k in (0, 2):
+            check(x, t, run(ft, x, t, k, scale), k, scale)
