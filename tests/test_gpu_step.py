@@ -190,3 +190,38 @@ def test_refused_sequences_are_harmless(ft):
     s.experts.close()
     s.kv.close()
     pool.free()
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "fp8"])
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_served_decoder_over_a_given_text(ft, example, fmt, seed):
+    """The same text by single tokens, by chunks and by trees whose branch it is, so that no tie of two tokens parts the ways: the
+    logits of every place, within the plain decoder's bound (test_layers_together)."""
+    ex, rng = example, np.random.default_rng(seed)
+    text = rng.integers(0, ex.VOCAB, 130).tolist()
+    d = ex.Served(fmt=fmt)
+    one = torch.cat([d.chunk([t]) for t in text])
+    d.close()
+    d, chunks, at = ex.Served(fmt=fmt), [], 0
+    while at < len(text):
+        n = int(rng.integers(1, ex.BATCH + 1))
+        chunks.append(d.chunk(text[at:at + n]))
+        at += n
+    d.close()
+    d, trees, at = ex.Served(fmt=fmt), [], 0
+    while at < len(text):
+        tokens, masks, path = [text[at]], [1], [0]
+        for t in text[at + 1:at + 1 + int(rng.integers(0, 7))]:
+            for wrong in range(int(rng.integers(0, 3))):           # siblings that are not the text's
+                masks.append(masks[path[-1]] | 1 << len(tokens))
+                tokens.append((t + 1 + wrong) % ex.VOCAB)
+            masks.append(masks[path[-1]] | 1 << len(tokens))
+            path.append(len(tokens))
+            tokens.append(t)
+        logits, kept = d.step(tokens, None, masks)
+        d.keep(len(tokens), path, kept)
+        trees.append(logits[path])
+        at += len(path)
+    d.close()
+    for other in (torch.cat(chunks), torch.cat(trees)):
+        assert other.shape == one.shape and ((other - one).norm() / one.norm()).item() < 2.0 ** -4
