@@ -10,12 +10,15 @@
 // the part is read again; where that does not help (equal logits by the thousand, rising ones), k searches find them.  Which ones
 // these are does not depend on any order: value, then index.
 //
-// 2048 rows of 131,072 bf16: 88.7 us, 6.05 TB/s, 0.91 of the copy rate; without the k largest 80 us, the copy rate.  The k
-// largest cost the barriers of the sample and of the list, during which an SM has only its other CTAs' loads under way.  One
-// row: 5.1 us in 8 CTAs, launch and barriers.  On the way: vectors through registers, 4 or 8 under way, 151 to 193 us; through
+// 2048 rows of 131,072 bf16: 89.1 us, 6.03 TB/s, 0.90 of the copy rate; without the k largest 80.5 us, the copy rate.  The k
+// largest cost the barriers of the sample and of the list, during which an SM has only its other CTAs' loads under way.  (fp32: 156 us,
+// of 65,536 82 us.)  Two kinds of rows are slow: where the scale times the logits passes 2^26 every vector goes out of line (see Sums), 575 us; and
+// where a CTA's part has fewer than k logits above thousands of equal ones it is read again and again: rows of the type's lowest value but
+// for their first 3 take 2.2 ms for k = 5 and 7.2 ms for k = 32, a row whose second half is masked so 88 and 165 us instead of 5.3.  One
+// row: 5.3 us in 8 CTAs, launch and barriers.  On the way: vectors through registers, 4 or 8 under way, 151 to 193 us; through
 // thread-owned shared memory 114 us; neighbouring vectors instead of four stretches of the row 103 us; the list by warps instead of at
 // once 101 us; ranks by several threads per entry (one row 7.3 -> 5.5 us), of few warps 95 us; three CTAs of 384 threads an SM
-// instead of two of 512 (see launch) 88.7 us.  Rows in a loop with the next one's first vectors loaded ahead (127 us instead of 101),
+// instead of two of 512 (see launch) 89 us.  Rows in a loop with the next one's first vectors loaded ahead (127 us instead of 101),
 // and the bound worked out by every warp for itself (107 us) were slower.
 #include <atomic>
 #include <cfloat>
@@ -658,6 +661,7 @@ cudaError_t launch(const ft_logprob& c, int shift, cudaStream_t s) {
 
 // Threads of a CTA: 512 (2 CTAs per SM), 384 (3) or 256 (4).  More CTAs overlap more of the rows' barriers, but their samples are
 // smaller and let more logits, k V / sample, through to be ranked; and few rows leave few CTAs.  us with 512, 384, 256 threads, bf16:
+// (fp32 rows go by the same rule, unmeasured with other widths)
 //   2048 rows of 131,072: k = 1 91 83.5 85, k = 5 95.5 89 89, k = 20 110 106 114, k = 32 121 125 168
 //   2048 rows of 50,304: k = 5 60.5 50 45, k = 32 75 67 65;  of 8192: k = 5 35 25.5 20
 //   304 rows of 131,072: 17.1 22.8 19.4;  456: 25.5 24.4 28.8

@@ -9,7 +9,8 @@
 // unevaluated sums of two fp32 (products split by a fused multiply-add, sums by Knuth's two-sum) down to the rounding.
 //
 // 8192 tokens of 32 query and 8 + 8 key and value heads of 128, NVFP4, all normalised and turned: 41 us for 194 MB, 0.7 of the copy
-// rate (reading them back takes another 10 us).  Bound by instructions, issued 60 % of the time by up to 20 warps per SM: some 190 for
+// rate (reading them back takes another 10 us).  Bound by no one thing: instructions are issued 60 % of the time by up to 20 warps per SM, which
+// wait for results, for loads and for their turn about equally; some 190 for
 // a query's 16 dims of 32 lanes, 1000 for a key's and a value's together (of which the two parts take 400, quantising 260).  A token
 // alone: 4.1 us with reading back, two launches.  On the way: a lane per scale block with its partners in another lane, 16 shuffles
 // a head, 94 us with reading back; partners in the same lane and packed arithmetic 82 us; heads asked for four ahead through
@@ -174,7 +175,7 @@ struct Heads {
         asm volatile("cp.async.wait_group %0;" :: "n"(kAhead - 1) : "memory");
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(slots + take));
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]) : "r"(slots + take + kRotThreads * 16));
-        issue(p);                      // into the slots of the head before
+        issue(p);                      // into the slots just read
         take = (take + 2 * kRotThreads * 16) & (2 * kAhead * kRotThreads * 16 - 1);
     }
 };

@@ -1,7 +1,11 @@
 // Router: logits to the k experts of each token and their weights.  A warp per token.
 //
 // Up to 512 experts the choices stay in registers.  The (k + 1)-th largest of the lanes' maxima bounds the (k + 1)-th largest choice
-// from below; what reaches it, k to some 1.3 k of 256, goes through shared memory and is ranked, each lane one.
+// from below; what reaches it, for small k k to some 1.3 k of 256, goes through shared memory and is ranked, each lane one.  With more
+// choices the lanes' maxima bound less and less: from some 14 (of scores with a bias) or 16 (of logits) on more than 32 experts reach the bound
+// in some rows, at k = 32 in all of them (of scores always: 33 maxima are asked for), and the row goes to the searches below.
+// 8192 tokens of 256 experts, by logits: k = 1 6.2 us, 8 6.8, 12 7.4, 16 13.8, 20 23, 24 40, 32 50; sigmoid with a bias: 4 10.5, 8 12.2, 12 13.8, 16 20, 18 48,
+// 24 93, 32 115.
 //
 // Choices are computed in fp32 with a bound on their error.  Where two neighbours of the sorted first k, the k-th and one behind it
 // or the last group that stays and the first that does not lie within their bounds, and do not come from the same logit and bias, the
@@ -9,9 +13,11 @@
 // is the logits' own and needs no rounding at all.
 //
 // Bound by latency and, for many tokens, by instructions (570 a row of 256), not by the 4.7 MB of 8192 tokens of 256 experts
-// (0.7 us): those take 6.6 us, one token 2.0 us, 16 with groups and a bias 3.8 us, 5003 of 160 experts with a bias 6.4 us, and 12
-// to 14 us where a row among them goes to 64 bits, whose latency stands alone at the end.  k searches of a warp through shared
-// memory, the form above 512 experts, take 14.2, 4.3, 7.3 and 31 us.
+// (0.7 us): those take 6.8 us, one token 2.0 us, 16 with groups and a bias 3.7 us, 5003 of 160 experts with groups and a bias 8.3 us, 12 to 15 us
+// where a row among them goes to 64 bits for its choices, and 20 us where one does for its groups: their latency stands alone at the end.
+// With that bias (0.05 beside scores of 160) the one is 2 rows in 10,000 and the other 1 in 20,000: of 60 such calls 17, 29 and 14.  k searches of
+// a warp through shared memory take 14.2, 4.3, 7.3 and 31 us for those; above 512 experts it is the only form (k = 8: 513 experts 6.1 us for a token and
+// 8.0 for 1024, 1024 experts 6.8 and 8.4, 4096 experts 16 and 34; k = 32 of 4096 82 us for 1024).
 #include <cfloat>
 #include <cmath>
 #include <type_traits>

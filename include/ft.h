@@ -535,7 +535,8 @@ ft_status ft_kv_attention(ft_kv* kv, const ft_kv_attn* call, void* stream);
  *   - surplus pages (j >= want) of all sequences are pushed on the stack of free pages, in ascending (s, j);
  *   - then missing ones are popped from it, in ascending (s, j), and entered in the table.
  * A sequence is refused if pages run out (if it takes any, and those that the sequences up to it ask for, this one and others refused
- * for want of pages too, are more than are free; FT_DEV_NO_PAGES), or if its description does not hold (FT_DEV_BAD_ID): held outside [0, table_stride] or
+ * for want of pages too, are more than are free; FT_DEV_NO_PAGES: from the first that does not fit on, every sequence that needs a page is
+ * refused, however few it needs, so long prompts belong last), or if its description does not hold (FT_DEV_BAD_ID): held outside [0, table_stride] or
  * above n_pages; for one that goes on also len < 0, held less than its len needs, rows past n_tokens, more than
  * table_stride pages or 2^31 - 1 tokens, and, with tree_mask, more than 64 new tokens.  A refused sequence keeps its len
  * and its pages; its rows stay in q_start, get the slot -1 (which ft_kv_append skips) and kv_len 0 (under which
